@@ -95,6 +95,8 @@ enum mnw_status {
 /* Bits of the device error word. */
 #define MNW_DEVERR_BAD_EXPERT_ID 0x1u  /* an id outside [0, E); that assignment was dropped */
 #define MNW_DEVERR_TIMEOUT 0x2u        /* a kernel-internal wait ran out; its output is invalid */
+#define MNW_DEVERR_BAD_LENGTH 0x4u     /* a cache length or token range that does not fit; what does not fit was left out */
+#define MNW_DEVERR_BAD_PAGE 0x8u       /* a page number outside [0, n_pages); not written, and read as zeros */
 
 enum mnw_wfmt { MNW_FMT_BF16 = 0, MNW_FMT_INT8_G128 = 1, MNW_FMT_INT4_G128 = 2, MNW_FMT_NVFP4_G16 = 3 };
 /* MNW_ACT_F16_ROWS is an operand form, not a layer mode: BF16 rows re-encoded
@@ -417,6 +419,95 @@ int mnw_moe_selftest_counter_timeout(uint32_t limit_us, const uint32_t* counter,
 size_t mnw_attn_workspace_size(int B, int T, int Hkv, int d);
 int mnw_attn_prefill(const void* q, const void* k, const void* v, int B, int T, int Hq, int Hkv, int d, int blk,
                      float scale, void* out, void* ws, size_t ws_bytes, uint32_t* err, mnw_stream stream);
+
+/* ---- the decode step around the layer: norm, paged cache, attention ----
+ * The pages' decode path refines 32-token blocks over cached keys and values
+ * and gives no formulas; these are the usual ones. */
+
+/* Root-mean-square norm of T rows of H values, with the residual's addition:
+ *   r' = bf16(x + residual)  (r' = x where residual is NULL)
+ *   y  = bf16(r' * (mean(r'^2) + eps)^-1/2 * w)
+ * x: device bf16, rows x_stride elements apart (>= H, a multiple of 8);
+ * residual, residual_out, y: device bf16 [T, H]; w: device bf16 [H].
+ * residual_out (nullable; only with a residual) receives r' and may be
+ * `residual` itself, or x where x_stride == H.  y may be NULL if codes is not.
+ * codes (int8 [T, H]) and scales (f32 [T, H/128]), both or neither, receive
+ * the INT8 form of y, the operand of the W8A8 / W4A8 GEMMs, bit for bit what
+ * mnw_moe_quantize_act(MNW_ACT_INT8_G128) gives for y.  The sum of squares is
+ * FP32 in a fixed order.  H % 8 == 0 (codes: H % 128 == 0), H <= 16384.
+ * T = 0 is a no-op. */
+int mnw_rmsnorm(const void* x, long long x_stride, const void* residual, const void* w, int T, int H, float eps,
+                void* residual_out, void* y, int8_t* codes, float* scales, mnw_stream stream);
+
+/* A paged key/value cache (of one layer): k_cache and v_cache
+ * [n_pages][Hkv][page_size][d], consecutive pages page_stride elements apart
+ * (>= Hkv * page_size * d; a multiple of 16 bytes), so that several layers, or
+ * keys and values, may share one allocation.  fmt MNW_KV_BF16: bf16.
+ * MNW_KV_INT8: int8 codes, with k_scale and v_scale f32
+ * [n_pages][Hkv][page_size], one scale per cached head row (max / 127, the
+ * rule of MNW_ACT_INT8_G128).  d is 64 or 128, page_size 1 .. 65536.
+ * block_table int32 [B, max_pages]: position p of sequence b lies in page
+ * block_table[b][p / page_size], slot p % page_size; entries past the length
+ * are not read.  cache_lens int32 [B]: cached positions of each sequence,
+ * its new tokens included: the n new tokens are the last n.  The new tokens of
+ * all sequences are T rows, one sequence after another: sequence b owns rows
+ * [q_start[b], q_start[b+1]) (int32 [B+1], ascending from 0 to T), or T / B
+ * each where q_start is NULL.  All of these are device memory.
+ * A length below zero, above max_pages * page_size or below the sequence's new
+ * tokens, or a q_start out of order, ORs MNW_DEVERR_BAD_LENGTH into *err (device, nullable);
+ * tokens without a position are left out.  A page outside [0, n_pages) ORs
+ * MNW_DEVERR_BAD_PAGE: nothing is written there, and it reads as zeros. */
+enum mnw_kvfmt { MNW_KV_BF16 = 0, MNW_KV_INT8 = 1 };
+enum mnw_rope { MNW_ROPE_HALF = 0, MNW_ROPE_INTERLEAVED = 1 };
+
+/* Writes the new tokens' keys and values to their slots, keys rotated by
+ * position, and rotates the queries.  Pair i of a head, at position p with
+ * a = p * inv_freq[i], becomes mscale * (u cos a - w sin a, w cos a + u sin a);
+ * (u, w) are elements (i, i + rot/2) (MNW_ROPE_HALF) or (2i, 2i + 1)
+ * (MNW_ROPE_INTERLEAVED); elements from rot on are copied.  inv_freq: device
+ * f32 [rot/2] (scaled as long contexts want: mnw_rope_frequencies); rot = 0
+ * rotates nothing.  The angle keeps its fraction of a turn to about 2^-24 at
+ * any 32-bit position.  q [T, Hq, d], k, v [T, Hkv, d] bf16, a token's heads
+ * contiguous, tokens *_stride elements apart (multiples of 8), so the
+ * slices of one fused projection can be passed.  q_out: bf16 [T, Hq, d] contiguous;
+ * may be q itself where q_stride == Hq * d.  q NULL: keys and values only.
+ * FP32 arithmetic, rounded to BF16 once; INT8 caches quantise the rounded
+ * rows.  rot % 16 == 0, rot <= d. */
+int mnw_kv_append(const void* q, long long q_stride, const void* k, long long k_stride, const void* v,
+                  long long v_stride, int B, int T, int Hq, int Hkv, int d, const float* inv_freq, int rot, int layout,
+                  float mscale, void* k_cache, void* v_cache, float* k_scale, float* v_scale, int fmt, int n_pages,
+                  int page_size, long long page_stride, const int32_t* block_table, int max_pages,
+                  const int32_t* cache_lens, const int32_t* q_start, void* q_out, uint32_t* err, mnw_stream stream);
+
+/* Attention of the new tokens over the cache (their own keys and values
+ * included: append first).  Token at position p sees positions j < min(len,
+ * (p / blk + 1) * blk): blk = 1 is causal, a block size lets a block see
+ * itself whole, blk >= len everything.  Query head h reads kv head
+ * h / (Hq / Hkv).  q as above (rotated); out: bf16 [T, Hq, d]; lse (f32
+ * [T, Hq], nullable): log of the row's sum of e^(scale * q . k).  A row that
+ * sees nothing gives zeros and lse = -inf; rows of no sequence are not
+ * written.  Slots past the length may hold anything, NaN included.  Scores, softmax and sums are
+ * FP32; results do not depend on timing.  ws: device, 256-byte aligned,
+ * >= mnw_attn_paged_workspace_size() bytes, any contents; calls that overlap
+ * need one each. */
+size_t mnw_attn_paged_workspace_size(int B, int T, int Hq, int Hkv, int d);
+int mnw_attn_paged(const void* q, long long q_stride, int B, int T, int Hq, int Hkv, int d, const void* k_cache,
+                   const void* v_cache, const float* k_scale, const float* v_scale, int fmt, int n_pages,
+                   int page_size, long long page_stride, const int32_t* block_table, int max_pages,
+                   const int32_t* cache_lens, const int32_t* q_start, int blk, float scale, void* out, float* lse,
+                   void* ws, size_t ws_bytes, uint32_t* err, mnw_stream stream);
+
+/* Rotation frequencies, on the host: inv_freq_host f32 [rot/2] receives
+ * base^(-2i/rot), scaled for contexts `factor` times the original_len that a
+ * model was trained on: MNW_ROPE_SCALE_NONE; _LINEAR divides all by factor;
+ * _NTK raises the base by factor^(rot/(rot-2)); _BY_PARTS keeps frequencies
+ * that turn at least beta_fast times within original_len, divides those that
+ * turn at most beta_slow times, and blends linearly (in the number of pair)
+ * between, with *mscale = 0.1 ln(factor) + 1 (1 for the others). */
+enum mnw_rope_scale { MNW_ROPE_SCALE_NONE = 0, MNW_ROPE_SCALE_LINEAR = 1, MNW_ROPE_SCALE_NTK = 2,
+                      MNW_ROPE_SCALE_BY_PARTS = 3 };
+int mnw_rope_frequencies(int rot, double base, int scale, double factor, double original_len, double beta_fast,
+                         double beta_slow, float* inv_freq_host, float* mscale);
 
 /* Synchronise `stream`, then copy the device error word to *out_host. */
 int mnw_moe_read_error(const uint32_t* err, uint32_t* out_host, mnw_stream stream);

@@ -21,11 +21,15 @@ MNW_OK = 0
 FMT_BF16, FMT_INT8_G128, FMT_INT4_G128, FMT_NVFP4_G16 = 0, 1, 2, 3
 ACT_BF16, ACT_INT8_G128, ACT_NVFP4_G16, ACT_F16_ROWS = 0, 1, 2, 3
 KIND_GATE_UP, KIND_DOWN, KIND_GATE, KIND_UP = 0, 1, 2, 3
-DEVERR_BAD_EXPERT_ID, DEVERR_TIMEOUT = 0x1, 0x2
+DEVERR_BAD_EXPERT_ID, DEVERR_TIMEOUT, DEVERR_BAD_LENGTH, DEVERR_BAD_PAGE = 0x1, 0x2, 0x4, 0x8
+KV_BF16, KV_INT8 = 0, 1
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+ROPE_SCALE_NONE, ROPE_SCALE_LINEAR, ROPE_SCALE_NTK, ROPE_SCALE_BY_PARTS = 0, 1, 2, 3
 PATH_AUTO, PATH_TCGEN05, PATH_WARP_MMA, PATH_ROWS = 0, 1, 2, 3
 
 # Symbols of include/mnw_moe.h, with their ctypes signatures.
 _P, _I, _SZ, _U32P = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p
+_LL = ctypes.c_longlong
 SIGNATURES = {
     "mnw_status_string": (ctypes.c_char_p, [_I]),
     "mnw_moe_layer_init": (_I, [_P, _P, _SZ, ctypes.POINTER(_P)]),
@@ -61,6 +65,14 @@ SIGNATURES = {
     "mnw_moe_forward_static": (_I, [_P, _I, _P, _P, _P, _I, _I, _P, _U32P, _P]),
     "mnw_moe_selftest_wait_timeout": (_I, [ctypes.c_uint32, _U32P, _U32P, _P]),
     "mnw_moe_selftest_counter_timeout": (_I, [ctypes.c_uint32, _U32P, ctypes.c_uint32, _U32P, _P]),
+    "mnw_rmsnorm": (_I, [_P, _LL, _P, _P, _I, _I, ctypes.c_float, _P, _P, _P, _P, _P]),
+    "mnw_kv_append": (_I, [_P, _LL, _P, _LL, _P, _LL, _I, _I, _I, _I, _I, _P, _I, _I, ctypes.c_float, _P, _P, _P, _P,
+                           _I, _I, _I, _LL, _P, _I, _P, _P, _P, _U32P, _P]),
+    "mnw_attn_paged_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
+    "mnw_attn_paged": (_I, [_P, _LL, _I, _I, _I, _I, _I, _P, _P, _P, _P, _I, _I, _I, _LL, _P, _I, _P, _P, _I,
+                            ctypes.c_float, _P, _P, _P, _SZ, _U32P, _P]),
+    "mnw_rope_frequencies": (_I, [_I, ctypes.c_double, _I, ctypes.c_double, ctypes.c_double, ctypes.c_double,
+                                  ctypes.c_double, _P, _P]),
     "mnw_attn_workspace_size": (_SZ, [_I, _I, _I, _I]),
     "mnw_attn_prefill": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I, ctypes.c_float, _P, _P, _SZ, _U32P, _P]),
 }
@@ -266,6 +278,202 @@ def mnw_attn_prefill(q, k, v, blk: int, scale: float, out=None, ws=None, err=Non
     _check(L.mnw_attn_prefill(_ptr(q), _ptr(k), _ptr(v), B, T, Hq, Hkv, d, int(blk), float(scale), _ptr(out),
                               _ptr(ws), ws.numel(), _ptr(err), _stream(stream)), "mnw_attn_prefill")
     return out
+
+
+# ---- the decode step around the layer: norm, paged cache, attention ----
+
+
+def _need(t, dtype, what, dim=None):
+    """Address of a CUDA tensor of the given type (and, with `dim`, that many dimensions, the last one contiguous)."""
+    if not t.is_cuda or t.dtype is not dtype:
+        raise MnwError(f"{what}: expected a CUDA tensor of {dtype}")
+    if dim is not None and (t.dim() != dim or (t.stride(-1) != 1 and t.shape[-1] > 1)):
+        raise MnwError(f"{what}: expected {dim} dimensions, the last one contiguous")
+    return t.data_ptr()
+
+
+def _whole(t, dtype, shape, what):
+    """Address of a contiguous CUDA tensor of the given type and shape."""
+    if not t.is_cuda or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise MnwError(f"{what}: expected a contiguous CUDA tensor of {dtype} and shape {tuple(shape)}")
+    return t.data_ptr()
+
+
+def _new(shape, dtype, device, stream):
+    """A device tensor for results written on `stream`: allocated under it, so its memory is reused in its order."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _stream_of(t, stream):
+    return (torch.cuda.current_stream(t.device) if stream is None else stream).cuda_stream
+
+
+def mnw_rmsnorm(x, weight, eps=1e-6, residual=None, residual_out=None, y=None, codes=None, scales=None, int8=False,
+                stream=None):
+    """Root-mean-square norm of bf16 x [T, H] with the residual's addition
+    (see include/mnw_moe.h).  Returns (y bf16 [T, H], residual_out bf16 [T, H]
+    or None, codes int8 [T, H] or None, scales f32 [T, H/128] or None); with
+    int8 the last two are the INT8 groups of y, as mnw_moe_quantize_act gives
+    them.  residual_out may be `residual` (in place)."""
+    xp = _need(x, torch.bfloat16, "x", 2)
+    T, H = x.shape
+    shape, dev = x.shape, x.device
+    wp = _whole(weight, torch.bfloat16, (H,), "weight")
+    rp = ro = None
+    if residual is not None:
+        rp = _whole(residual, torch.bfloat16, shape, "residual")
+        if residual_out is None:
+            residual_out = _new(shape, torch.bfloat16, dev, stream)
+        ro = _whole(residual_out, torch.bfloat16, shape, "residual_out")
+    elif residual_out is not None:
+        raise MnwError("residual_out needs a residual")
+    if y is None:
+        y = _new(shape, torch.bfloat16, dev, stream)
+    yp = _whole(y, torch.bfloat16, shape, "y")
+    cp = sp = None
+    if int8 or codes is not None or scales is not None:
+        if codes is None:
+            codes = _new(shape, torch.int8, dev, stream)
+        if scales is None:
+            scales = _new((T, H // 128), torch.float32, dev, stream)
+        cp = _whole(codes, torch.int8, shape, "codes")
+        sp = _whole(scales, torch.float32, (T, H // 128), "scales")
+    stride = x.stride(0) if T > 1 else max(H, x.stride(0))
+    rc = load().mnw_rmsnorm(xp, stride, rp, wp, T, H, eps, ro, yp, cp, sp, _stream_of(x, stream))
+    if rc:
+        _check(rc, "mnw_rmsnorm")
+    return y, residual_out, codes, scales
+
+
+def _token_rows(t, what, d=None):
+    """(address, tokens, heads, d, elements between tokens) of bf16 [T, heads, d], a token's heads contiguous."""
+    p = _need(t, torch.bfloat16, what, 3)
+    T, h, dd = t.shape
+    if (d is not None and dd != d) or (h > 1 and t.stride(1) != dd):
+        raise MnwError(f"{what}: expected [T, heads, {d or 'd'}] with a token's heads contiguous")
+    return p, T, h, dd, t.stride(0) if T > 1 else max(h * dd, t.stride(0) // 8 * 8)
+
+
+def _cache_args(k_cache, v_cache, k_scale, v_scale):
+    """The cache's part of the C arguments: k, v, k_scale, v_scale, fmt, n_pages, page_size, page_stride; Hkv and d."""
+    dtype = k_cache.dtype
+    if dtype is torch.bfloat16:
+        fmt = KV_BF16
+    elif dtype is torch.int8:
+        fmt = KV_INT8
+    else:
+        raise MnwError("the cache is bf16 or int8")
+    kp, vp = _need(k_cache, dtype, "k_cache", 4), _need(v_cache, dtype, "v_cache", 4)
+    n, h, page, d = k_cache.shape
+    st = k_cache.stride()
+    if v_cache.shape != k_cache.shape or v_cache.stride() != st:
+        raise MnwError("k_cache and v_cache differ in shape or strides")
+    if (page > 1 and st[2] != d) or (h > 1 and st[1] != page * d):
+        raise MnwError("a page of the cache [Hkv, page_size, d] has to be contiguous")
+    ks = vs = None
+    if fmt == KV_INT8:
+        if k_scale is None or v_scale is None:
+            raise MnwError("an int8 cache needs k_scale and v_scale")
+        ks = _whole(k_scale, torch.float32, (n, h, page), "k_scale")
+        vs = _whole(v_scale, torch.float32, (n, h, page), "v_scale")
+    elif k_scale is not None or v_scale is not None:
+        raise MnwError("a bf16 cache has no scales")
+    return kp, vp, ks, vs, fmt, n, page, (st[0] if n > 1 else h * page * d), h, d
+
+
+def _batch_args(block_table, cache_lens, q_start):
+    tp = _need(block_table, torch.int32, "block_table", 2)
+    B, most = block_table.shape
+    if not block_table.is_contiguous():
+        raise MnwError("block_table has to be contiguous")
+    lp = _whole(cache_lens, torch.int32, (B,), "cache_lens")
+    sp = None if q_start is None else _whole(q_start, torch.int32, (B + 1,), "q_start")
+    return B, most, tp, lp, sp
+
+
+def mnw_kv_append(q, k, v, k_cache, v_cache, block_table, cache_lens, inv_freq=None, layout=ROPE_HALF, mscale=1.0,
+                  k_scale=None, v_scale=None, q_start=None, q_out=None, err=None, stream=None):
+    """Writes new tokens' keys and values into a paged cache, keys rotated by
+    position; returns the rotated queries [T, Hq, d] (None where q is None).
+    q [T, Hq, d], k and v [T, Hkv, d] bf16, slices of one projection's output
+    at will; caches [n_pages, Hkv, page_size, d] bf16, or int8 with scales f32
+    [n_pages, Hkv, page_size]; block_table int32 [B, max_pages]; cache_lens
+    int32 [B], the new tokens included; q_start int32 [B + 1] or None (T / B
+    tokens each).  inv_freq f32 [rot / 2] (None: no rotation); see
+    mnw_rope_frequencies and include/mnw_moe.h."""
+    kc, vc, ks, vs, fmt, n_pages, page, page_stride, Hkv, d = _cache_args(k_cache, v_cache, k_scale, v_scale)
+    B, most, tp, lp, sp = _batch_args(block_table, cache_lens, q_start)
+    kp, T, hk, _, kst = _token_rows(k, "k", d)
+    vp, Tv, hv, _, vst = _token_rows(v, "v", d)
+    if hk != Hkv or hv != Hkv or Tv != T:
+        raise MnwError("k and v have to be [T, Hkv, d] with the cache's Hkv")
+    qp = qo = None
+    Hq = qst = 0
+    if q is not None:
+        qp, Tq, Hq, _, qst = _token_rows(q, "q", d)
+        if Tq != T:
+            raise MnwError("q has another number of tokens than k")
+        if q_out is None:
+            q_out = _new((T, Hq, d), torch.bfloat16, q.device, stream)
+        qo = _whole(q_out, torch.bfloat16, (T, Hq, d), "q_out")
+    elif q_out is not None:
+        raise MnwError("q_out needs q")
+    fp, rot = None, 0
+    if inv_freq is not None:
+        rot = 2 * inv_freq.numel()
+        fp = _whole(inv_freq, torch.float32, (rot // 2,), "inv_freq")
+    ep = None if err is None else _ptr(err)
+    rc = load().mnw_kv_append(qp, qst, kp, kst, vp, vst, B, T, Hq, Hkv, d, fp, rot, layout, mscale, kc, vc, ks, vs, fmt,
+                              n_pages, page, page_stride, tp, most, lp, sp, qo, ep, _stream_of(k, stream))
+    if rc:
+        _check(rc, "mnw_kv_append")
+    return q_out
+
+
+def mnw_attn_paged_workspace_size(B, T, Hq, Hkv, d) -> int:
+    return int(load().mnw_attn_paged_workspace_size(B, T, Hq, Hkv, d))
+
+
+def mnw_attn_paged(q, k_cache, v_cache, block_table, cache_lens, blk, scale, k_scale=None, v_scale=None, q_start=None,
+                   out=None, lse=None, want_lse=False, ws=None, err=None, stream=None):
+    """Attention of new tokens q [T, Hq, d] over a paged cache (arguments as
+    mnw_kv_append; append first).  A token at position p sees positions below
+    (p // blk + 1) * blk.  Returns out [T, Hq, d] bf16, with want_lse or lse
+    (out, lse f32 [T, Hq]).  ws: a uint8 device tensor of at least
+    mnw_attn_paged_workspace_size bytes, 256-byte aligned."""
+    kc, vc, ks, vs, fmt, n_pages, page, page_stride, Hkv, d = _cache_args(k_cache, v_cache, k_scale, v_scale)
+    B, most, tp, lp, sp = _batch_args(block_table, cache_lens, q_start)
+    qp, T, Hq, _, qst = _token_rows(q, "q", d)
+    dev = q.device
+    if out is None:
+        out = _new((T, Hq, d), torch.bfloat16, dev, stream)
+    op = _whole(out, torch.bfloat16, (T, Hq, d), "out")
+    if lse is None and want_lse:
+        lse = _new((T, Hq), torch.float32, dev, stream)
+    ep = None if err is None else _ptr(err)
+    lib = load()
+    if ws is None:
+        ws = _new((max(256, lib.mnw_attn_paged_workspace_size(B, T, Hq, Hkv, d)),), torch.uint8, dev, stream)
+    rc = lib.mnw_attn_paged(qp, qst, B, T, Hq, Hkv, d, kc, vc, ks, vs, fmt, n_pages, page, page_stride, tp, most, lp, sp,
+                            blk, scale, op, None if lse is None else _whole(lse, torch.float32, (T, Hq), "lse"),
+                            _need(ws, torch.uint8, "ws"), ws.numel(), ep, _stream_of(q, stream))
+    if rc:
+        _check(rc, "mnw_attn_paged")
+    return out if lse is None else (out, lse)
+
+
+def mnw_rope_frequencies(rot, base=10000.0, scale=ROPE_SCALE_NONE, factor=1.0, original_len=4096, beta_fast=32.0,
+                         beta_slow=1.0, device=None):
+    """(inv_freq f32 [rot / 2], mscale) for mnw_kv_append, scaled for contexts
+    `factor` times original_len (see include/mnw_moe.h)."""
+    f = torch.empty(max(rot, 0) // 2, dtype=torch.float32)
+    m = ctypes.c_float()
+    _check(load().mnw_rope_frequencies(rot, base, scale, factor, original_len, beta_fast, beta_slow,
+                                       ctypes.c_void_p(f.data_ptr()), ctypes.byref(m)), "mnw_rope_frequencies")
+    return (f if device is None else f.to(device)), m.value
 
 
 def _gemm_out(layer, kind, P, dev):

@@ -1,0 +1,857 @@
+// mnw_attn_paged.cu -- attention of new tokens (one each, a refinement block,
+// several) over a paged key/value cache, split over the cache's length.
+//
+// For new token i of sequence b (position p = len - n + i) and query head h
+// (kv head g = h / (Hq / Hkv)), over the allowed positions j < min(len,
+// (p / blk + 1) * blk):
+//   s_j = scale * q . k_j,   out = sum_j e^{s_j} v_j / sum_j e^{s_j},
+//   lse = log sum_j e^{s_j}
+// One pass with a running maximum and sum per row.
+//
+// Bound: every cached key and value is read once for all rows of its kv head
+// (n * Hq / Hkv query rows), so up to ~100 rows the reads of the cache are the
+// floor.
+//
+// Work split: the unit is one tile of kTK keys of one item (sequence, kv
+// head, tile of query rows).  All units in order are cut into equal runs, one
+// per CTA, so ragged lengths load the CTAs evenly and one long sequence
+// spreads over the whole GPU.  A run that covers an item whole writes its
+// output; otherwise it leaves (maximum, sum, unnormalised output) in the
+// workspace, and a second kernel joins an item's parts in run order (the
+// result does not depend on timing).
+//
+// A CTA is WR x WK warps: WR row blocks of 16 query rows, each tile's keys cut
+// over WK warps.  Tiles arrive by 16-byte cp.async through a ring of kStages
+// stages, one page lookup per row piece, so pages of any size may end inside
+// a tile; rows past the length are filled with zeros (a masked probability of
+// 0 then meets a finite value, whatever the page holds there).  Both products
+// are mma.sync m16n8k16 with FP32 accumulation.
+//
+// BF16 caches: probabilities enter the second product rounded to BF16 (2^-9
+// relative each, independent, so the sum's error stays near the output's own
+// rounding); the sum of probabilities is taken before that rounding.
+// INT8 caches: the first product runs on FP16 operands: codes are exact there,
+// and q is re-encoded per row as FP16 times a power of two (exact for values
+// within 2^28 of the row's largest); the keys' scales multiply the FP32 scores.
+// The second runs on TF32: codes are exact, and the probabilities times the
+// values' scales, rounded to 11 bits (2^-12), keep FP32's exponents, so value scales
+// of any spread keep the sum's accuracy (FP16 would lose weights 2^-24 below
+// the largest).
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <atomic>
+
+#include "mnw_convert.cuh"
+#include "mnw_internal.h"
+#include "mnw_paged.cuh"
+#include "mnw_ptx.cuh"
+
+namespace mnw {
+namespace pattn {
+
+using paged::Batch;
+using paged::FastDiv;
+using paged::Seq;
+
+constexpr int kTK = 64;        // keys per tile
+constexpr int kMinUnits = 2;   // tiles per CTA at least, where there are few
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct Args {
+  Batch bt;
+  const __nv_bfloat16* q;
+  long long q_stride;
+  const uint8_t *kc, *vc;
+  const float *ks, *vs;
+  long long page_bytes;  // bytes between pages of kc and vc
+  FastDiv page_div;
+  int n_pages, page_size, Hq, Hkv, G, blk;
+  float scale_log2;
+  __nv_bfloat16* out;
+  float* lse;
+  long long* starts;  // [B + 1] first unit of each sequence (workspace), [B + 1] = units per run
+  float* part_o;      // [2 * runs][RT][D]
+  float2* part_ml;    // [2 * runs][RT]
+  uint32_t* err;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+template <bool F16>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (F16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Four unsigned-biased codes (code + 128 per byte) -> FP16 pairs: byte b under
+// the exponent byte 0x64 is the FP16 value 1024 + b.
+__device__ __forceinline__ uint32_t codes_lo(uint32_t w) { return f16x2_sub(prmt(w, 0x64646464u, 0x4140), 0x64806480u); }
+__device__ __forceinline__ uint32_t codes_hi(uint32_t w) { return f16x2_sub(prmt(w, 0x64646464u, 0x4342), 0x64806480u); }
+// Code `B` of four biased ones as FP32: the byte under the exponent of 2^23 is
+// the value 2^23 + byte.
+template <int B>
+__device__ __forceinline__ uint32_t code_f32(uint32_t w) {
+  return __float_as_uint(__uint_as_float(prmt(w, 0x4B000000u, 0x7440 + B)) - 8388736.f);
+}
+__device__ __forceinline__ uint32_t tf32(float x) {
+  uint32_t y;
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void mma1688(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Units of a sequence.
+struct Shape {
+  long long units;
+  int rt, kt;  // row tiles, key tiles (one at least, so that empty caches still write their rows)
+};
+template <int RT>
+__device__ __forceinline__ Shape shape_of(const Seq& s, int G, int Hkv) {
+  Shape h;
+  h.rt = static_cast<int>((static_cast<long long>(s.n) * G + RT - 1) / RT);
+  h.kt = max(1, (s.len + kTK - 1) / kTK);
+  h.units = static_cast<long long>(Hkv) * h.rt * h.kt;
+  return h;
+}
+
+__host__ __device__ __forceinline__ long long run_length(long long units, long long runs) {
+  const long long per = (units + runs - 1) / runs;
+  return per < kMinUnits ? kMinUnits : per;
+}
+
+template <int D, bool INT8, int WR, int WK>
+struct Cfg {
+  static constexpr int kWarps = WR * WK, kThreads = kWarps * 32, kRT = WR * 16;
+  static constexpr int kRowBytes = INT8 ? D : 2 * D;
+  static constexpr int kTileBytes = kTK * kRowBytes;
+  static constexpr int kScaleBytes = INT8 ? 2 * kTK * 4 : 0;
+  static constexpr int kStageBytes = 2 * kTileBytes + kScaleBytes;
+  static constexpr int kStages = 3;
+  static constexpr int kMergeBytes = WK > 1 ? kWarps * 16 * (D + 2) * 4 : 0;
+  static constexpr int kRing = kStages * kStageBytes;
+  static constexpr int kSmem = kRing > kMergeBytes ? kRing : kMergeBytes;
+};
+
+// Byte offset of 16-byte chunk c of row r in a tile: chunks are exchanged by
+// the row so that the eight rows of a matrix load fall into different banks.
+template <int D, bool INT8>
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
+  if constexpr (!INT8) return static_cast<uint32_t>(r * D * 2 + ((c ^ (r & 7)) << 4));
+  else if constexpr (D == 128)  // key reads take rows 2h, 2h+1 x 4 chunks, value reads rows 0,2,4,6 x 2 chunks
+    return static_cast<uint32_t>(r * D + ((c ^ ((r & 6) ^ ((r & 1) << 2))) << 4));
+  else
+    return static_cast<uint32_t>(r * D + ((c ^ ((r >> 1) & 3)) << 4));
+}
+
+template <int D, bool INT8, int WR, int WK>
+__global__ void __launch_bounds__(WR* WK * 32) paged_attn_kernel(const Args a) {
+  using C = Cfg<D, INT8, WR, WK>;
+  constexpr int kRT = C::kRT, kThreads = C::kThreads, kStages = C::kStages;
+  constexpr int kKS = D / 16;        // k steps of the first product
+  constexpr int kNO = D / 8;         // output column tiles
+  constexpr int kKW = kTK / WK;      // keys of a tile per warp
+  constexpr int kNB = kKW / 16;      // 16-key blocks per warp
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ long long sh_scan[32];
+  __shared__ long long sh_first;  // first unit of sequence sh_b
+  __shared__ int sh_b;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int wr = warp / WK, wk = warp % WK;
+  const int g8 = lane >> 2, t4 = lane & 3;
+  const uint32_t sbase = smem_u32(smem);
+
+  pdl_launch_dependents();
+  pdl_wait();
+
+  // ---- where this run begins ----
+  const Batch& bt = a.bt;
+  long long total = 0;
+  for (int b = tid; b < bt.B; b += kThreads) {
+    bool bad;
+    const Seq s = paged::sequence(bt, b, a.page_size, &bad);
+    if (bad && blockIdx.x == 0 && a.err) atomicOr(a.err, MNW_DEVERR_BAD_LENGTH);
+    total += shape_of<kRT>(s, a.G, a.Hkv).units;
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
+  if (lane == 0) sh_scan[warp] = total;
+  __syncthreads();
+  total = 0;
+  for (int w = 0; w < C::kWarps; ++w) total += sh_scan[w];
+  const long long per = run_length(total, gridDim.x);
+  const long long u0 = blockIdx.x * per, u1 = min(total, u0 + per);
+  const bool scribe = blockIdx.x == 0;  // run 0 writes the sequences' first units for the joining kernel
+  if (scribe && tid == 0) a.starts[bt.B + 1] = per;
+  if (tid == 0) sh_b = -1;
+  if (u0 >= u1 && !scribe) return;
+  {
+    long long carry = 0;
+    for (int b0 = 0; b0 < bt.B; b0 += kThreads) {
+      const int b = b0 + tid;
+      long long mine = 0;
+      if (b < bt.B) {
+        bool bad;
+        mine = shape_of<kRT>(paged::sequence(bt, b, a.page_size, &bad), a.G, a.Hkv).units;
+      }
+      long long incl = mine;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += o;
+      }
+      __syncthreads();
+      if (lane == 31) sh_scan[warp] = incl;
+      __syncthreads();
+      long long before = carry;
+      for (int w = 0; w < warp; ++w) before += sh_scan[w];
+      const long long first = before + incl - mine;
+      if (b < bt.B) {
+        if (scribe) a.starts[b] = first;
+        if (mine > 0 && first <= u0 && u0 < first + mine) {
+          sh_b = b;
+          sh_first = first;
+        }
+      }
+      for (int w = 0; w < C::kWarps; ++w) carry += sh_scan[w];
+    }
+    __syncthreads();
+  }
+  if (u0 >= u1) return;
+
+  int b = sh_b;
+  if (b < 0) return;  // the lengths changed under the kernel
+  long long u = u0, seq_first = sh_first;
+  bool bad;
+  Seq s = paged::sequence(bt, b, a.page_size, &bad);
+  Shape sh = shape_of<kRT>(s, a.G, a.Hkv);
+
+  while (u < u1) {
+    while (u >= seq_first + sh.units) {
+      seq_first += sh.units;
+      if (++b >= bt.B) return;
+      s = paged::sequence(bt, b, a.page_size, &bad);
+      sh = shape_of<kRT>(s, a.G, a.Hkv);
+    }
+    const long long in_seq = u - seq_first;
+    const long long item = in_seq / sh.kt;
+    const int kt0 = static_cast<int>(in_seq - item * sh.kt);
+    const int kt1 = static_cast<int>(min(static_cast<long long>(sh.kt), kt0 + (u1 - u)));
+    const int g = static_cast<int>(item / sh.rt), rt = static_cast<int>(item - static_cast<long long>(g) * sh.rt);
+    const bool whole = kt0 == 0 && kt1 == sh.kt;
+    u += kt1 - kt0;
+
+    const int rows = min(kRT, s.n * a.G - rt * kRT);  // query rows of this tile (n * G < 2^31: checked by the host)
+    // limit of a query row r: its first forbidden position
+    auto limit = [&](int r) -> int {
+      const int i = (rt * kRT + r) / a.G;
+      const int p = s.len - s.n + i;
+      if (p < 0) return 0;
+      const long long e = (static_cast<long long>(p / a.blk) + 1) * a.blk;
+      return e < s.len ? static_cast<int>(e) : s.len;
+    };
+    const int lim_lo = limit(0), lim_hi = limit(rows - 1);
+    const int r0 = wr * 16 + g8, r1 = r0 + 8;
+    const int lim0 = r0 < rows ? limit(r0) : lim_hi, lim1 = r1 < rows ? limit(r1) : lim_hi;
+
+    // ---- query fragments ----
+    uint32_t qf[kKS][4];
+    float qfac0 = a.scale_log2, qfac1 = a.scale_log2;  // score factor of rows r0, r1
+    {
+      auto row_ptr = [&](int r) -> const __nv_bfloat16* {
+        const int ri = rt * kRT + r;
+        const int i = ri / a.G, hh = ri - i * a.G;
+        return a.q + static_cast<long long>(s.start + i) * a.q_stride + static_cast<long long>(g * a.G + hh) * D;
+      };
+      const bool ok0 = r0 < rows, ok1 = r1 < rows;
+      const __nv_bfloat16 *p0 = row_ptr(ok0 ? r0 : 0), *p1 = row_ptr(ok1 ? r1 : 0);
+      if constexpr (!INT8) {
+#pragma unroll
+        for (int ks = 0; ks < kKS; ++ks) {
+          qf[ks][0] = ok0 ? *reinterpret_cast<const uint32_t*>(p0 + 16 * ks + 2 * t4) : 0u;
+          qf[ks][1] = ok1 ? *reinterpret_cast<const uint32_t*>(p1 + 16 * ks + 2 * t4) : 0u;
+          qf[ks][2] = ok0 ? *reinterpret_cast<const uint32_t*>(p0 + 16 * ks + 2 * t4 + 8) : 0u;
+          qf[ks][3] = ok1 ? *reinterpret_cast<const uint32_t*>(p1 + 16 * ks + 2 * t4 + 8) : 0u;
+        }
+      } else {
+        // k step 4j + s4 of the products takes elements 16 (t4 + 4j) + 4 s4 .. + 3 of lane t4: the order in
+        // which a lane's 16-byte word of codes holds them
+        uint32_t m0 = 0, m1 = 0;  // magnitudes' largest bit patterns
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+          for (int s4 = 0; s4 < 4; ++s4) {
+            const int e = 16 * (t4 + 4 * j) + 4 * s4;
+            const uint2 x0 = ok0 ? *reinterpret_cast<const uint2*>(p0 + e) : make_uint2(0, 0);
+            const uint2 x1 = ok1 ? *reinterpret_cast<const uint2*>(p1 + e) : make_uint2(0, 0);
+            qf[4 * j + s4][0] = x0.x;
+            qf[4 * j + s4][2] = x0.y;
+            qf[4 * j + s4][1] = x1.x;
+            qf[4 * j + s4][3] = x1.y;
+            m0 = max(max(m0, x0.x & 0x7FFFu), max((x0.x >> 16) & 0x7FFFu, max(x0.y & 0x7FFFu, (x0.y >> 16) & 0x7FFFu)));
+            m1 = max(max(m1, x1.x & 0x7FFFu), max((x1.x >> 16) & 0x7FFFu, max(x1.y & 0x7FFFu, (x1.y >> 16) & 0x7FFFu)));
+          }
+#pragma unroll
+        for (int d = 1; d < 4; d <<= 1) {
+          m0 = max(m0, __shfl_xor_sync(0xffffffffu, m0, d));
+          m1 = max(m1, __shfl_xor_sync(0xffffffffu, m1, d));
+        }
+        // 2^e with the row's largest magnitude in [2^14, 2^15) after x * 2^-e
+        auto expo = [](uint32_t m) { return m == 0 ? 0 : max(-110, min(113, static_cast<int>(m >> 7) - 127 - 14)); };
+        const int e0 = expo(m0), e1 = expo(m1);
+        const float i0 = __uint_as_float(static_cast<uint32_t>(127 - e0) << 23);
+        const float i1 = __uint_as_float(static_cast<uint32_t>(127 - e1) << 23);
+        qfac0 = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e0) << 23);
+        qfac1 = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e1) << 23);
+#pragma unroll
+        for (int ks = 0; ks < kKS; ++ks)
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const float f = (w & 1) ? i1 : i0;
+            const uint32_t x = qf[ks][w];
+            const __half2 hv = __floats2half2_rn(__uint_as_float(x << 16) * f, __uint_as_float(x & 0xFFFF0000u) * f);
+            qf[ks][w] = *reinterpret_cast<const uint32_t*>(&hv);
+          }
+      }
+    }
+
+    // ---- tile loads ----
+    const int32_t* table = bt.block_table + static_cast<size_t>(b) * bt.max_pages;
+    auto load_tile = [&](int kt, int stage) {
+      const uint32_t st = sbase + stage * C::kStageBytes;
+      constexpr int kCh = C::kRowBytes / 16;        // chunks per row
+      constexpr int kRP = kThreads / kCh;           // rows per pass
+      const int c = tid % kCh;
+#pragma unroll
+      for (int i = 0; i < kTK / kRP; ++i) {
+        const int r = i * kRP + tid / kCh;
+        const int p = kt * kTK + r;
+        const uint8_t *ks = a.kc, *vs = a.vc;
+        uint32_t n = 0;
+        if (p < s.len) {
+          const int pi = static_cast<int>(paged::quotient(p, a.page_div));
+          const int page = __ldg(table + pi);
+          if (static_cast<unsigned>(page) < static_cast<unsigned>(a.n_pages)) {
+            const long long off = page * a.page_bytes +
+                                  (static_cast<long long>(g) * a.page_size + (p - pi * a.page_size)) * C::kRowBytes + c * 16;
+            ks += off;
+            vs += off;
+            n = 16;
+          } else if (a.err) {
+            atomicOr(a.err, MNW_DEVERR_BAD_PAGE);
+          }
+        }
+        const uint32_t at = chunk_at<D, INT8>(r, c);
+        cp_async16(st + at, ks, n);
+        cp_async16(st + C::kTileBytes + at, vs, n);
+      }
+      if constexpr (INT8) {
+        for (int r2 = tid; r2 < 2 * kTK; r2 += kThreads) {
+          const int r = r2 % kTK;
+          const int p = kt * kTK + r;
+          const float* src = r2 < kTK ? a.ks : a.vs;
+          uint32_t n = 0;
+          if (p < s.len) {
+            const int pi = static_cast<int>(paged::quotient(p, a.page_div));
+            const int page = __ldg(table + pi);
+            if (static_cast<unsigned>(page) < static_cast<unsigned>(a.n_pages)) {
+              src += (static_cast<long long>(page) * a.Hkv + g) * a.page_size + (p - pi * a.page_size);
+              n = 4;
+            }
+          }
+          cp_async4(st + 2 * C::kTileBytes + r2 * 4, src, n);
+        }
+      }
+    };
+
+    // ---- main loop ----
+    float o[kNO][4];
+#pragma unroll
+    for (int i = 0; i < kNO; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+
+    // tiles past every row's limit add nothing
+    const int kte = min(kt1, (lim_hi + kTK - 1) / kTK);
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) {
+      if (kt0 + i < kte) load_tile(kt0 + i, i);
+      cp_commit();
+    }
+    int slot = 0;
+    for (int kt = kt0; kt < kte; ++kt) {
+      cp_wait<kStages - 2>();
+      __syncthreads();
+      {
+        int ns = slot + kStages - 1;
+        if (ns >= kStages) ns -= kStages;
+        if (kt + kStages - 1 < kte) load_tile(kt + kStages - 1, ns);
+        cp_commit();
+      }
+      const uint32_t kst = sbase + slot * C::kStageBytes, vst = kst + C::kTileBytes;
+      const uint8_t* stage = smem + slot * C::kStageBytes;
+      if (++slot == kStages) slot = 0;
+
+      // scores of the warp's keys
+      float sc[2 * kNB][4];
+#pragma unroll
+      for (int i = 0; i < 2 * kNB; ++i) sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.f;
+#pragma unroll
+      for (int nb = 0; nb < kNB; ++nb) {
+        const int key0 = wk * kKW + nb * 16;
+        if constexpr (!INT8) {
+          const int row = key0 + (lane & 7) + ((lane >> 4) << 3);
+#pragma unroll
+          for (int ks = 0; ks < kKS; ++ks) {
+            uint32_t kf[4];
+            ldsm4(kst + chunk_at<D, INT8>(row, 2 * ks + ((lane >> 3) & 1)), kf);
+            mma16816<false>(sc[2 * nb], qf[ks], kf[0], kf[1]);
+            mma16816<false>(sc[2 * nb + 1], qf[ks], kf[2], kf[3]);
+          }
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < D / 64; ++j) {
+              const uint4 w = *reinterpret_cast<const uint4*>(stage + chunk_at<D, INT8>(key0 + 8 * h + g8, t4 + 4 * j));
+              const uint32_t ww[4] = {w.x ^ 0x80808080u, w.y ^ 0x80808080u, w.z ^ 0x80808080u, w.w ^ 0x80808080u};
+#pragma unroll
+              for (int s4 = 0; s4 < 4; ++s4)
+                mma16816<true>(sc[2 * nb + h], qf[4 * j + s4], codes_lo(ww[s4]), codes_hi(ww[s4]));
+            }
+        }
+      }
+      if constexpr (INT8) {
+        const float* ksc = reinterpret_cast<const float*>(stage + 2 * C::kTileBytes);
+#pragma unroll
+        for (int i = 0; i < 2 * kNB; ++i) {
+          const float2 f = *reinterpret_cast<const float2*>(ksc + wk * kKW + 8 * i + 2 * t4);
+          sc[i][0] *= f.x;
+          sc[i][1] *= f.y;
+          sc[i][2] *= f.x;
+          sc[i][3] *= f.y;
+        }
+      }
+      const int key_base = kt * kTK + wk * kKW + 2 * t4;
+      if ((kt + 1) * kTK > lim_lo) {  // some row's limit lies in this tile
+#pragma unroll
+        for (int i = 0; i < 2 * kNB; ++i) {
+          const int k = key_base + 8 * i;
+          if (k >= lim0) sc[i][0] = -INFINITY;
+          if (k + 1 >= lim0) sc[i][1] = -INFINITY;
+          if (k >= lim1) sc[i][2] = -INFINITY;
+          if (k + 1 >= lim1) sc[i][3] = -INFINITY;
+        }
+      }
+      float x0 = -INFINITY, x1 = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 2 * kNB; ++i) {
+        x0 = fmaxf(x0, fmaxf(sc[i][0], sc[i][1]));
+        x1 = fmaxf(x1, fmaxf(sc[i][2], sc[i][3]));
+      }
+#pragma unroll
+      for (int d = 1; d < 4; d <<= 1) {
+        x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, d));
+        x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, d));
+      }
+      const float n0 = fmaxf(m0, x0 * qfac0), n1 = fmaxf(m1, x1 * qfac1);
+      const float b0 = n0 == -INFINITY ? 0.f : n0, b1 = n1 == -INFINITY ? 0.f : n1;
+      float c0 = ex2(m0 - b0), c1 = ex2(m1 - b1);
+      m0 = n0;
+      m1 = n1;
+      l0 *= c0;
+      l1 *= c1;
+#pragma unroll
+      for (int i = 0; i < 2 * kNB; ++i) {
+        sc[i][0] = ex2(fmaf(sc[i][0], qfac0, -b0));
+        sc[i][1] = ex2(fmaf(sc[i][1], qfac0, -b0));
+        sc[i][2] = ex2(fmaf(sc[i][2], qfac1, -b1));
+        sc[i][3] = ex2(fmaf(sc[i][3], qfac1, -b1));
+        l0 += sc[i][0] + sc[i][1];
+        l1 += sc[i][2] + sc[i][3];
+      }
+      if constexpr (INT8) {
+        const float* vsc = reinterpret_cast<const float*>(stage + 2 * C::kTileBytes) + kTK;
+#pragma unroll
+        for (int i = 0; i < 2 * kNB; ++i) {
+          const float2 f = *reinterpret_cast<const float2*>(vsc + wk * kKW + 8 * i + 2 * t4);
+          sc[i][0] *= f.x;
+          sc[i][1] *= f.y;
+          sc[i][2] *= f.x;
+          sc[i][3] *= f.y;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kNO; ++i) {
+        o[i][0] *= c0;
+        o[i][1] *= c0;
+        o[i][2] *= c1;
+        o[i][3] *= c1;
+      }
+#pragma unroll
+      for (int nb = 0; nb < kNB; ++nb) {
+        const int key0 = wk * kKW + nb * 16;
+        if constexpr (!INT8) {
+          uint32_t pf[4];
+          pf[0] = pack_bf16x2(sc[2 * nb][0], sc[2 * nb][1]);
+          pf[1] = pack_bf16x2(sc[2 * nb][2], sc[2 * nb][3]);
+          pf[2] = pack_bf16x2(sc[2 * nb + 1][0], sc[2 * nb + 1][1]);
+          pf[3] = pack_bf16x2(sc[2 * nb + 1][2], sc[2 * nb + 1][3]);
+          const int row = key0 + (lane & 7) + (((lane >> 3) & 1) << 3);
+#pragma unroll
+          for (int db = 0; db < kNO / 2; ++db) {
+            uint32_t vf[4];
+            ldsm4t(vst + chunk_at<D, INT8>(row, 2 * db + (lane >> 4)), vf);
+            mma16816<false>(o[2 * db], pf, vf[0], vf[1]);
+            mma16816<false>(o[2 * db + 1], pf, vf[2], vf[3]);
+          }
+        } else {
+          // k slot t4 (t4 + 4) of an 8-key step is key 2 t4 (2 t4 + 1), as the scores lie; a lane holds elements
+          // kNO g8 .. kNO g8 + kNO - 1 of its two keys, output tile i takes element kNO g8 + i
+          constexpr int kWords = kNO / 4;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float(&p)[4] = sc[2 * nb + h];
+            const uint32_t pf[4] = {tf32(p[0]), tf32(p[2]), tf32(p[1]), tf32(p[3])};
+            uint32_t cw[2][kWords];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const int row = key0 + 8 * h + 2 * t4 + x;
+              const uint8_t* at = stage + C::kTileBytes + chunk_at<D, INT8>(row, D == 128 ? g8 : g8 >> 1);
+              if constexpr (D == 128) {
+                const uint4 w = *reinterpret_cast<const uint4*>(at);
+                cw[x][0] = w.x; cw[x][1] = w.y; cw[x][2] = w.z; cw[x][3] = w.w;
+              } else {
+                const uint2 w = *reinterpret_cast<const uint2*>(at + 8 * (g8 & 1));
+                cw[x][0] = w.x; cw[x][1] = w.y;
+              }
+#pragma unroll
+              for (int y = 0; y < kWords; ++y) cw[x][y] ^= 0x80808080u;
+            }
+#pragma unroll
+            for (int y = 0; y < kWords; ++y) {
+              mma1688(o[4 * y], pf, code_f32<0>(cw[0][y]), code_f32<0>(cw[1][y]));
+              mma1688(o[4 * y + 1], pf, code_f32<1>(cw[0][y]), code_f32<1>(cw[1][y]));
+              mma1688(o[4 * y + 2], pf, code_f32<2>(cw[0][y]), code_f32<2>(cw[1][y]));
+              mma1688(o[4 * y + 3], pf, code_f32<3>(cw[0][y]), code_f32<3>(cw[1][y]));
+            }
+          }
+        }
+      }
+    }
+    cp_wait<0>();
+#pragma unroll
+    for (int d = 1; d < 4; d <<= 1) {
+      l0 += __shfl_xor_sync(0xffffffffu, l0, d);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, d);
+    }
+    __syncthreads();  // the ring is free: every copy has landed and been read
+
+    // ---- join the warps' key slices ----
+    // element column of accumulator (i, j): j = 0, 1
+    auto col = [&](int i, int j) { return INT8 ? kNO * (2 * t4 + j) + i : 8 * i + 2 * t4 + j; };
+    if constexpr (WK > 1) {
+      float* mo = reinterpret_cast<float*>(smem);                       // [warp][16][D]
+      float2* ml = reinterpret_cast<float2*>(mo + C::kWarps * 16 * D);  // [warp][16]
+#pragma unroll
+      for (int i = 0; i < kNO; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          mo[(warp * 16 + g8) * D + col(i, j)] = o[i][j];
+          mo[(warp * 16 + g8 + 8) * D + col(i, j)] = o[i][2 + j];
+        }
+      if (t4 == 0) {
+        ml[warp * 16 + g8] = make_float2(m0, l0);
+        ml[warp * 16 + g8 + 8] = make_float2(m1, l1);
+      }
+      __syncthreads();
+    }
+    const long long run = blockIdx.x;
+    const long long pslot = 2 * run + (kt0 > 0 ? 0 : 1);
+    if constexpr (WK > 1) {
+      const float* mo = reinterpret_cast<const float*>(smem);
+      const float2* ml = reinterpret_cast<const float2*>(mo + C::kWarps * 16 * D);
+      for (int e = tid * 4; e < rows * D; e += kThreads * 4) {
+        const int r = e / D, c = e % D;
+        const int w0 = (r >> 4) * WK, rr = r & 15;
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < WK; ++w) M = fmaxf(M, ml[(w0 + w) * 16 + rr].x);
+        const float base = M == -INFINITY ? 0.f : M;
+        float L = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < WK; ++w) {
+          const float2 q = ml[(w0 + w) * 16 + rr];
+          const float f = ex2(q.x - base);
+          const float4 v = *reinterpret_cast<const float4*>(mo + ((w0 + w) * 16 + rr) * D + c);
+          L += f * q.y;
+          acc.x += f * v.x;
+          acc.y += f * v.y;
+          acc.z += f * v.z;
+          acc.w += f * v.w;
+        }
+        if (whole) {
+          const int ri = rt * kRT + r, i = ri / a.G, hh = ri - i * a.G;
+          const size_t row = static_cast<size_t>(s.start + i) * a.Hq + g * a.G + hh;
+          const float inv = L == 0.f ? 0.f : 1.f / L;
+          *reinterpret_cast<uint2*>(a.out + row * D + c) =
+              make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+          if (a.lse && c == 0) a.lse[row] = (M + log2f(L)) * kLn2;
+        } else {
+          *reinterpret_cast<float4*>(a.part_o + (pslot * kRT + r) * D + c) = acc;
+          if (c == 0) a.part_ml[pslot * kRT + r] = make_float2(M, L);
+        }
+      }
+      __syncthreads();  // the next item's tiles go where the parts lay
+    } else {
+#pragma unroll
+      for (int hrow = 0; hrow < 2; ++hrow) {
+        const int r = hrow ? r1 : r0;
+        const float M = hrow ? m1 : m0, L = hrow ? l1 : l0;
+        if (r < rows) {
+          if (whole) {
+            const int ri = rt * kRT + r, i = ri / a.G, hh = ri - i * a.G;
+            const size_t row = static_cast<size_t>(s.start + i) * a.Hq + g * a.G + hh;
+            const float inv = L == 0.f ? 0.f : 1.f / L;
+            if constexpr (!INT8) {
+#pragma unroll
+              for (int n = 0; n < kNO; ++n)
+                *reinterpret_cast<uint32_t*>(a.out + row * D + col(n, 0)) =
+                    pack_bf16x2(o[n][2 * hrow] * inv, o[n][2 * hrow + 1] * inv);
+            } else {
+#pragma unroll
+              for (int n = 0; n < kNO; n += 2)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                  *reinterpret_cast<uint32_t*>(a.out + row * D + col(n, j)) =
+                      pack_bf16x2(o[n][2 * hrow + j] * inv, o[n + 1][2 * hrow + j] * inv);
+            }
+            if (a.lse && t4 == 0) a.lse[row] = (M + log2f(L)) * kLn2;
+          } else {
+            float* dst = a.part_o + (pslot * kRT + r) * D;
+#pragma unroll
+            for (int n = 0; n < kNO; ++n) {
+              dst[col(n, 0)] = o[n][2 * hrow];
+              dst[col(n, 1)] = o[n][2 * hrow + 1];
+            }
+            if (t4 == 0) a.part_ml[pslot * kRT + r] = make_float2(M, L);
+          }
+        }
+      }
+    }
+  }
+}
+
+// Joins the parts of items that several runs share: one warp per (token, query
+// head) row; rows of items that one run covered are done already.
+template <int D, int RT>
+__global__ void __launch_bounds__(256) paged_join_kernel(const Args a) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const long long row = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (row >= static_cast<long long>(a.bt.T) * a.Hq) return;
+  const int t = static_cast<int>(row / a.Hq), h = static_cast<int>(row % a.Hq);
+  int b;
+  if (a.bt.q_start) {
+    int cnt = 0;
+    for (int j = lane; j < a.bt.B; j += 32) cnt += __ldg(a.bt.q_start + j + 1) <= t ? 1 : 0;
+    b = __reduce_add_sync(0xffffffffu, cnt);
+  } else {
+    b = t / a.bt.n_uniform;
+  }
+  if (b >= a.bt.B) return;
+  bool bad;
+  const Seq s = paged::sequence(a.bt, b, a.page_size, &bad);
+  if (t < s.start || t >= s.start + s.n) return;
+  const Shape sh = shape_of<RT>(s, a.G, a.Hkv);
+  const int g = h / a.G, ri = (t - s.start) * a.G + (h - g * a.G);
+  const int rt = ri / RT, r = ri % RT;
+  const long long per = a.starts[a.bt.B + 1];
+  const long long us = a.starts[b] + (static_cast<long long>(g) * sh.rt + rt) * sh.kt, ue = us + sh.kt;
+  const long long c0 = us / per, c1 = (ue - 1) / per;
+  if (c0 == c1) return;
+  auto slot_of = [&](long long c) { return 2 * c + (c * per > us ? 0 : 1); };
+  float M = -INFINITY;
+  for (long long c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, a.part_ml[slot_of(c) * RT + r].x);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+  const float base = M == -INFINITY ? 0.f : M;
+  constexpr int V = D / 32;
+  float acc[V], L = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) acc[i] = 0.f;
+#pragma unroll 4
+  for (long long c = c0; c <= c1; ++c) {
+    const long long p = slot_of(c) * RT + r;
+    const float2 ml = a.part_ml[p];
+    const float f = ex2(ml.x - base);
+    L += f * ml.y;
+    const float* src = a.part_o + p * D + lane * V;
+    if constexpr (V == 4) {
+      const float4 v = *reinterpret_cast<const float4*>(src);
+      acc[0] += f * v.x;
+      acc[1] += f * v.y;
+      acc[2] += f * v.z;
+      acc[3] += f * v.w;
+    } else {
+      const float2 v = *reinterpret_cast<const float2*>(src);
+      acc[0] += f * v.x;
+      acc[1] += f * v.y;
+    }
+  }
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  __nv_bfloat16* dst = a.out + row * D + lane * V;
+  if constexpr (V == 4)
+    *reinterpret_cast<uint2*>(dst) =
+        make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+  else
+    *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+  if (a.lse && lane == 0) a.lse[row] = (M + log2f(L)) * kLn2;
+}
+
+// ---- host ----
+
+// Row tile for `rows` query rows per (sequence, kv head) on average.
+inline int row_tile(long long rows) { return rows <= 16 ? 16 : (rows <= 32 ? 32 : 64); }
+constexpr int kRunsPerSm = 2;  // CTAs resident on an SM
+
+inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+inline size_t bytes_starts(int B) { return up256((static_cast<size_t>(B) + 2) * 8); }
+inline size_t bytes_ml(int rt) { return up256(static_cast<size_t>(2) * kRunsPerSm * current_sm_count() * rt * 8); }
+inline size_t bytes_o(int rt, int d) { return static_cast<size_t>(2) * kRunsPerSm * current_sm_count() * rt * d * 4; }
+
+template <int D, bool INT8, int WR, int WK>
+cudaError_t launch(Args& a, uint8_t* ws, cudaStream_t st) {
+  using C = Cfg<D, INT8, WR, WK>;
+  auto kern = paged_attn_kernel<D, INT8, WR, WK>;
+  static std::atomic<uint64_t> attr{0};
+  uint64_t bit;
+  if (attrs_needed(attr, &bit)) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    attrs_done(attr, bit);
+  }
+  a.starts = reinterpret_cast<long long*>(ws);
+  a.part_ml = reinterpret_cast<float2*>(ws + bytes_starts(a.bt.B));
+  a.part_o = reinterpret_cast<float*>(ws + bytes_starts(a.bt.B) + bytes_ml(C::kRT));
+  // most units that the batch can have: every row tile over a full block table
+  const long long kt = (static_cast<long long>(a.bt.max_pages) * a.page_size + kTK - 1) / kTK;
+  const long long tiles = (static_cast<long long>(a.bt.T) * a.G) / C::kRT + a.bt.B;
+  const long long units = tiles * a.Hkv * (kt < 1 ? 1 : kt);
+  long long runs = static_cast<long long>(kRunsPerSm) * current_sm_count();
+  const long long most = (units + kMinUnits - 1) / kMinUnits;
+  if (runs > most) runs = most;
+  cudaError_t e = launch_pdl(kern, dim3(static_cast<unsigned>(runs)), dim3(C::kThreads), C::kSmem, st, a);
+  if (e != cudaSuccess || kt <= 1) return e;  // items of one tile are never shared
+  const long long rows = static_cast<long long>(a.bt.T) * a.Hq;
+  return launch_pdl(paged_join_kernel<D, C::kRT>, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0, st, a);
+}
+
+template <int D, bool INT8>
+cudaError_t launch_rows(Args& a, uint8_t* ws, int rt, cudaStream_t st) {
+  if (rt == 16) return launch<D, INT8, 1, 4>(a, ws, st);
+  if (rt == 32) return launch<D, INT8, 2, 2>(a, ws, st);
+  return launch<D, INT8, 4, 2>(a, ws, st);
+}
+
+}  // namespace pattn
+}  // namespace mnw
+
+using namespace mnw;
+
+extern "C" {
+
+size_t mnw_attn_paged_workspace_size(int B, int T, int Hq, int Hkv, int d) {
+  if (B <= 0 || T <= 0 || Hq <= 0 || Hkv <= 0 || d <= 0 || Hq % Hkv) return 0;
+  const int rt = pattn::row_tile((static_cast<long long>(T) + B - 1) / B * (Hq / Hkv));
+  return pattn::up256(pattn::bytes_starts(B) + pattn::bytes_ml(rt) + pattn::bytes_o(rt, d));
+}
+
+int mnw_attn_paged(const void* q, long long q_stride, int B, int T, int Hq, int Hkv, int d, const void* k_cache,
+                   const void* v_cache, const float* k_scale, const float* v_scale, int fmt, int n_pages,
+                   int page_size, long long page_stride, const int32_t* block_table, int max_pages,
+                   const int32_t* cache_lens, const int32_t* q_start, int blk, float scale, void* out, float* lse,
+                   void* ws, size_t ws_bytes, uint32_t* err, mnw_stream stream) {
+  MNW_RANGE("mnw_attn_paged");
+  using namespace pattn;
+  if (B < 0 || T < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || blk < 1) return MNW_E_INVALID_ARG;
+  if (!(scale > 0.f) || !(scale < 3.0e38f)) return MNW_E_INVALID_ARG;
+  if (B == 0 || T == 0) return T == 0 ? MNW_OK : MNW_E_INVALID_ARG;
+  int rc = paged::check_cache(k_cache, v_cache, k_scale, v_scale, fmt, n_pages, page_size, Hkv, d, page_stride);
+  if (rc != MNW_OK) return rc;
+  rc = paged::check_batch(block_table, cache_lens, q_start, B, T, max_pages, page_size);
+  if (rc != MNW_OK) return rc;
+  if (!q || !out || !ws || !aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(ws, 256) ||
+      q_stride % 8 || q_stride < static_cast<long long>(Hq) * d)
+    return MNW_E_INVALID_ARG;
+  if (static_cast<long long>(T) * Hq > 0x7fffffffll / 8) return MNW_E_UNSUPPORTED;
+  if (ws_bytes < mnw_attn_paged_workspace_size(B, T, Hq, Hkv, d)) return MNW_E_WORKSPACE_TOO_SMALL;
+  Args a{};
+  a.bt = paged::Batch{block_table, cache_lens, q_start, B, T, max_pages, q_start ? 0 : T / B};
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.q_stride = q_stride;
+  a.kc = static_cast<const uint8_t*>(k_cache);
+  a.vc = static_cast<const uint8_t*>(v_cache);
+  a.ks = k_scale;
+  a.vs = v_scale;
+  const bool int8 = fmt == MNW_KV_INT8;
+  a.page_bytes = page_stride * (int8 ? 1 : 2);
+  a.page_div = paged::fast_div(page_size);
+  a.n_pages = n_pages;
+  a.page_size = page_size;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.G = Hq / Hkv;
+  a.blk = blk;
+  a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.lse = lse;
+  a.err = err;
+  const int rt = row_tile((static_cast<long long>(T) + B - 1) / B * a.G);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  auto* w = static_cast<uint8_t*>(ws);
+  cudaError_t e;
+  if (d == 128)
+    e = int8 ? launch_rows<128, true>(a, w, rt, st) : launch_rows<128, false>(a, w, rt, st);
+  else
+    e = int8 ? launch_rows<64, true>(a, w, rt, st) : launch_rows<64, false>(a, w, rt, st);
+  return e == cudaSuccess ? MNW_OK : MNW_E_CUDA;
+}
+
+}  // extern "C"

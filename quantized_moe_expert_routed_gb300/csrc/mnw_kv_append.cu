@@ -1,0 +1,326 @@
+// mnw_kv_append.cu -- new tokens' keys and values into a paged cache, with the
+// position rotation of q and k applied on the way.
+//
+// Rotation of pair i of a head at position p, angle a = p * inv_freq[i]:
+//   (u, w) -> m * (u cos a - w sin a, w cos a + u sin a)
+// where (u, w) are elements (i, i + rot/2) of the head (half layout) or
+// (2i, 2i + 1) (interleaved); elements past rot are copied.  FP32 arithmetic,
+// one rounding to BF16.  INT8 caches quantise the rounded row: s = max|x| /
+// 127, code = clamp(rne(x / s), -127, 127), as mnw_moe_quantize_act() does.
+//
+// The angle: at position 10^5 a radian's fraction lies 17 bits down, so a
+// plain FP32 product would leave 7 bits of it.  It is taken in turns, g =
+// inv_freq / (2 pi) as an unevaluated sum of two FP32 values, whole turns
+// removed exactly from each partial product, and sin and cos of the remaining
+// fraction come from sincospif; the error is about 2^-24 turns.
+//
+// Memory bound: every element is read and written once.
+#include <cuda_bf16.h>
+
+#include <cmath>
+
+#include "mnw_convert.cuh"
+#include "mnw_internal.h"
+#include "mnw_paged.cuh"
+#include "mnw_ptx.cuh"
+
+namespace mnw {
+namespace kvapp {
+
+using paged::Batch;
+using paged::FastDiv;
+using paged::Seq;
+
+constexpr int kThreads = 256;
+constexpr int kMaxPairs = 64;  // rot <= d <= 128
+
+struct Args {
+  Batch bt;
+  const __nv_bfloat16 *q, *k, *v;
+  long long q_stride, k_stride, v_stride;
+  __nv_bfloat16* q_out;
+  uint8_t *kc, *vc;
+  float *ks, *vs;
+  long long page_stride;  // elements
+  FastDiv page_div;
+  int n_pages, page_size, Hq, Hkv, rot, tokens;
+  const float* inv_freq;
+  float mscale;
+  uint32_t* err;
+};
+
+// Fraction of a turn, in [-1/2, 1/2], of position p at frequency f.
+__device__ __forceinline__ float turn_fraction(int p, float f) {
+  constexpr float kHi = 0.15915494309189535f;                                    // 1 / (2 pi)
+  constexpr float kLo = static_cast<float>(0.15915494309189535 - static_cast<double>(kHi));
+  const float g = f * kHi;
+  const float gl = fmaf(f, kLo, fmaf(f, kHi, -g));
+  const float ph = static_cast<float>(p & ~0xFFFF), pl = static_cast<float>(p & 0xFFFF);  // both exact
+  const float a = ph * g, ae = fmaf(ph, g, -a);
+  const float b = pl * g, be = fmaf(pl, g, -b);
+  float r = (a - rintf(a)) + (b - rintf(b));
+  r += ae + be + (ph + pl) * gl;
+  return r - rintf(r);
+}
+
+// One CTA per `tokens` tokens.  A head row is D/8 chunks of 16 bytes, one
+// thread each, so a row lies in D/8 neighbouring lanes: the other element of
+// a half-layout pair and the row maximum come by shuffles.
+template <int D, bool INT8, bool HALF>
+__global__ void __launch_bounds__(kThreads) kv_append_kernel(const Args a) {
+  constexpr int C = D / 8;  // chunks (threads) of a row
+  __shared__ float2 cs[4][kMaxPairs];
+  __shared__ long long slot_of[4];  // page * page_size... row index of the token's slot, or -1
+  __shared__ int page_of[4];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int t0 = blockIdx.x * a.tokens;
+  const int nt = min(a.tokens, a.bt.T - t0);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int pairs = a.rot / 2;
+  // a warp per token: its sequence, position, slot and angles
+  if (warp < nt) {
+    const int t = t0 + warp;
+    int b;
+    if (a.bt.q_start) {
+      int cnt = 0;  // sequences that end at or before t
+      for (int j = lane; j < a.bt.B; j += 32) cnt += __ldg(a.bt.q_start + j + 1) <= t ? 1 : 0;
+      b = __reduce_add_sync(0xffffffffu, cnt);
+    } else {
+      b = t / a.bt.n_uniform;
+    }
+    bool bad = b >= a.bt.B;
+    int pos = 0, page = -1, slot = 0;
+    if (!bad) {
+      const Seq s = paged::sequence(a.bt, b, a.page_size, &bad);
+      pos = s.len - s.n + (t - s.start);
+      const bool inside = t >= s.start && t < s.start + s.n && pos >= 0 && pos < s.len;
+      if (inside) {
+        const int pi = static_cast<int>(paged::quotient(pos, a.page_div));
+        slot = pos - pi * a.page_size;
+        page = __ldg(a.bt.block_table + static_cast<size_t>(b) * a.bt.max_pages + pi);
+        if (page < 0 || page >= a.n_pages) {
+          page = -1;
+          if (lane == 0 && a.err) atomicOr(a.err, MNW_DEVERR_BAD_PAGE);
+        }
+      } else {
+        bad = true;
+      }
+    }
+    if (bad && lane == 0 && a.err) atomicOr(a.err, MNW_DEVERR_BAD_LENGTH);
+    if (lane == 0) {
+      page_of[warp] = page;
+      slot_of[warp] = slot;
+    }
+    for (int i = lane; i < pairs; i += 32) {
+      float sn, co;
+      sincospif(2.f * turn_fraction(pos, __ldg(a.inv_freq + i)), &sn, &co);
+      cs[warp][i] = make_float2(co * a.mscale, sn * a.mscale);
+    }
+  }
+  __syncthreads();
+
+  const int rows = (a.q ? a.Hq : 0) + 2 * a.Hkv;  // q heads, k heads, v heads of a token
+  const int q_rows = a.q ? a.Hq : 0;
+  const int total = nt * rows * C;
+  const int step = kThreads;
+  for (int base = 0; base < total; base += step) {
+    const int idx = base + threadIdx.x;
+    const bool live = idx < total;  // a row's lanes are all live or all not (step and C are multiples)
+    const int c = idx % C;
+    const int rw = live ? idx / C : 0;
+    const int tk = rw / rows, row = rw - tk * rows;
+    const int t = t0 + tk;
+    const bool is_q = row < q_rows, is_k = !is_q && row < q_rows + a.Hkv;
+    const int h = is_q ? row : (is_k ? row - q_rows : row - q_rows - a.Hkv);
+    const __nv_bfloat16* src = is_q ? a.q + t * a.q_stride : (is_k ? a.k + t * a.k_stride : a.v + t * a.v_stride);
+    uint4 raw = make_uint4(0, 0, 0, 0);
+    if (live) raw = *reinterpret_cast<const uint4*>(src + h * D + c * 8);
+    float x[8];
+    const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(u[i] << 16);
+      x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+    }
+    const bool turned = (is_q || is_k) && c * 8 < a.rot;
+    if constexpr (HALF) {
+      const int hc = pairs / 8;  // chunks in half of the rotated part
+      const bool first = c < hc;
+      // partner chunk's lane; lanes that do not turn read their own
+      const int from = (turned && live) ? lane + (first ? hc : -hc) : lane;
+      const int pi = (first ? c : c - hc) * 8;
+      const uint32_t pu[4] = {__shfl_sync(0xffffffffu, raw.x, from), __shfl_sync(0xffffffffu, raw.y, from),
+                              __shfl_sync(0xffffffffu, raw.z, from), __shfl_sync(0xffffffffu, raw.w, from)};
+      if (turned && live) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float o = (i & 1) ? __uint_as_float(pu[i / 2] & 0xFFFF0000u) : __uint_as_float(pu[i / 2] << 16);
+          const float2 f = cs[tk][pi + i];
+          x[i] = first ? x[i] * f.x - o * f.y : x[i] * f.x + o * f.y;
+        }
+      }
+    } else {
+      if (turned && live) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = cs[tk][c * 4 + i];
+          const float p = x[2 * i], w = x[2 * i + 1];
+          x[2 * i] = p * f.x - w * f.y;
+          x[2 * i + 1] = w * f.x + p * f.y;
+        }
+      }
+    }
+    const uint4 out = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                                 pack_bf16x2(x[6], x[7]));
+    const int page = page_of[tk];
+    const size_t head_row =
+        (static_cast<size_t>(h) * a.page_size + static_cast<size_t>(slot_of[tk]));  // within the page
+    if (is_q) {
+      if (live) *reinterpret_cast<uint4*>(a.q_out + (static_cast<size_t>(t) * a.Hq + h) * D + c * 8) = out;
+    }
+    if constexpr (!INT8) {
+      if (live && !is_q && page >= 0) {
+        __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(is_k ? a.kc : a.vc) + page * a.page_stride + head_row * D;
+        *reinterpret_cast<uint4*>(dst + c * 8) = out;
+      }
+    } else {
+      float y[8];
+      const uint32_t o[4] = {out.x, out.y, out.z, out.w};
+      float amax = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        y[2 * i] = __uint_as_float(o[i] << 16);
+        y[2 * i + 1] = __uint_as_float(o[i] & 0xFFFF0000u);
+        amax = fmaxf(amax, fmaxf(fabsf(y[2 * i]), fabsf(y[2 * i + 1])));
+      }
+#pragma unroll
+      for (int s = C / 2; s > 0; s >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, s));
+      if (live && !is_q && page >= 0) {
+        uint32_t packed[2] = {0, 0};
+        float scale = 0.f;
+        if (amax > 0.f) {
+          scale = __fdiv_rn(amax, 127.0f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int qv = max(-127, min(127, __float2int_rn(__fdiv_rn(y[i], scale))));
+            packed[i >> 2] |= (static_cast<uint32_t>(qv) & 0xFFu) << (8 * (i & 3));
+          }
+        }
+        uint8_t* dst = (is_k ? a.kc : a.vc) + page * a.page_stride + head_row * D;
+        *reinterpret_cast<uint2*>(dst + c * 8) = make_uint2(packed[0], packed[1]);
+        if (c == 0)
+          (is_k ? a.ks : a.vs)[static_cast<size_t>(page) * a.Hkv * a.page_size + head_row] = scale;
+      }
+    }
+  }
+}
+
+template <int D, bool INT8>
+cudaError_t launch(const Args& a, bool half, cudaStream_t st) {
+  const dim3 grid((a.bt.T + a.tokens - 1) / a.tokens), block(kThreads);
+  return half ? launch_pdl(kv_append_kernel<D, INT8, true>, grid, block, 0, st, a)
+              : launch_pdl(kv_append_kernel<D, INT8, false>, grid, block, 0, st, a);
+}
+
+}  // namespace kvapp
+}  // namespace mnw
+
+using namespace mnw;
+
+extern "C" {
+
+int mnw_rope_frequencies(int rot, double base, int scale, double factor, double original_len, double beta_fast,
+                         double beta_slow, float* inv_freq_host, float* mscale) {
+  if (rot <= 0 || rot % 2 || !(base > 1.0) || !std::isfinite(base) || !inv_freq_host) return MNW_E_INVALID_ARG;
+  if (scale < MNW_ROPE_SCALE_NONE || scale > MNW_ROPE_SCALE_BY_PARTS) return MNW_E_INVALID_ARG;
+  if (scale != MNW_ROPE_SCALE_NONE && (!(factor >= 1.0) || !std::isfinite(factor))) return MNW_E_INVALID_ARG;
+  const bool parts = scale == MNW_ROPE_SCALE_BY_PARTS;
+  if (parts && (!(original_len > 0.0) || !(beta_slow > 0.0) || !(beta_fast > beta_slow) || !std::isfinite(beta_fast)))
+    return MNW_E_INVALID_ARG;
+  if (scale == MNW_ROPE_SCALE_NTK) {
+    if (rot < 4) return MNW_E_INVALID_ARG;
+    base *= std::pow(factor, static_cast<double>(rot) / (rot - 2));
+  }
+  const double two_pi = 6.283185307179586476925;
+  // pair (as a real number) that turns beta times within original_len
+  auto pair_of = [&](double beta) { return rot * std::log(original_len / (beta * two_pi)) / (2.0 * std::log(base)); };
+  double lo = 0.0, hi = 1.0;
+  if (parts) {
+    lo = std::fmax(std::floor(pair_of(beta_fast)), 0.0);
+    hi = std::fmin(std::ceil(pair_of(beta_slow)), rot - 1.0);
+    if (hi <= lo) hi = lo + 0.001;
+  }
+  for (int i = 0; i < rot / 2; ++i) {
+    double f = std::pow(base, -2.0 * i / rot);
+    if (scale == MNW_ROPE_SCALE_LINEAR) f /= factor;
+    if (parts) {
+      const double slow = std::fmin(1.0, std::fmax(0.0, (i - lo) / (hi - lo)));
+      f = f / factor * slow + f * (1.0 - slow);
+    }
+    inv_freq_host[i] = static_cast<float>(f);
+  }
+  if (mscale) *mscale = parts ? static_cast<float>(0.1 * std::log(factor) + 1.0) : 1.f;
+  return MNW_OK;
+}
+
+int mnw_kv_append(const void* q, long long q_stride, const void* k, long long k_stride, const void* v,
+                  long long v_stride, int B, int T, int Hq, int Hkv, int d, const float* inv_freq, int rot, int layout,
+                  float mscale, void* k_cache, void* v_cache, float* k_scale, float* v_scale, int fmt, int n_pages,
+                  int page_size, long long page_stride, const int32_t* block_table, int max_pages,
+                  const int32_t* cache_lens, const int32_t* q_start, void* q_out, uint32_t* err, mnw_stream stream) {
+  MNW_RANGE("mnw_kv_append");
+  if (B < 0 || T < 0) return MNW_E_INVALID_ARG;
+  if (B == 0 || T == 0) return T == 0 ? MNW_OK : MNW_E_INVALID_ARG;
+  int rc = paged::check_cache(k_cache, v_cache, k_scale, v_scale, fmt, n_pages, page_size, Hkv, d, page_stride);
+  if (rc != MNW_OK) return rc;
+  rc = paged::check_batch(block_table, cache_lens, q_start, B, T, max_pages, page_size);
+  if (rc != MNW_OK) return rc;
+  if (rot < 0 || rot > d || (rot > 0 && !inv_freq) || !aligned(inv_freq, 4)) return MNW_E_INVALID_ARG;
+  if (layout != MNW_ROPE_HALF && layout != MNW_ROPE_INTERLEAVED) return MNW_E_INVALID_ARG;
+  if (rot % 16) return MNW_E_UNSUPPORTED;
+  if (!(mscale > 0.f) || !(mscale < 3.0e38f)) return MNW_E_INVALID_ARG;
+  if (!k || !v || !aligned(k, 16) || !aligned(v, 16) || k_stride % 8 || v_stride % 8 ||
+      k_stride < static_cast<long long>(Hkv) * d || v_stride < static_cast<long long>(Hkv) * d)
+    return MNW_E_INVALID_ARG;
+  if (q) {
+    if (Hq <= 0 || !q_out || !aligned(q, 16) || !aligned(q_out, 16) || q_stride % 8 ||
+        q_stride < static_cast<long long>(Hq) * d)
+      return MNW_E_INVALID_ARG;
+    if (Hq > 1024) return MNW_E_UNSUPPORTED;
+  }
+  kvapp::Args a{};
+  a.bt = paged::Batch{block_table, cache_lens, q_start, B, T, max_pages, q_start ? 0 : T / B};
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.k = static_cast<const __nv_bfloat16*>(k);
+  a.v = static_cast<const __nv_bfloat16*>(v);
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.q_out = static_cast<__nv_bfloat16*>(q_out);
+  a.kc = static_cast<uint8_t*>(k_cache);
+  a.vc = static_cast<uint8_t*>(v_cache);
+  a.ks = k_scale;
+  a.vs = v_scale;
+  a.page_stride = page_stride;
+  a.page_div = paged::fast_div(page_size);
+  a.n_pages = n_pages;
+  a.page_size = page_size;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.rot = rot;
+  a.tokens = 1;
+  a.inv_freq = inv_freq;
+  a.mscale = mscale;
+  a.err = err;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool half = layout == MNW_ROPE_HALF, int8 = fmt == MNW_KV_INT8;
+  cudaError_t e;
+  if (d == 128)
+    e = int8 ? kvapp::launch<128, true>(a, half, st) : kvapp::launch<128, false>(a, half, st);
+  else
+    e = int8 ? kvapp::launch<64, true>(a, half, st) : kvapp::launch<64, false>(a, half, st);
+  return e == cudaSuccess ? MNW_OK : MNW_E_CUDA;
+}
+
+}  // extern "C"
