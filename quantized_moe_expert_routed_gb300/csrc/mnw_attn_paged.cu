@@ -12,13 +12,7 @@
 // (n * Hq / Hkv query rows), so up to ~100 rows the reads of the cache are the
 // floor.
 //
-// Work split: the unit is one tile of kTK keys of one item (sequence, kv
-// head, tile of query rows).  All units in order are cut into equal runs, one
-// per CTA, so ragged lengths load the CTAs evenly and one long sequence
-// spreads over the whole GPU.  A run that covers an item whole writes its
-// output; otherwise it leaves (maximum, sum, unnormalised output) in the
-// workspace, and a second kernel joins an item's parts in run order (the
-// result does not depend on timing).
+// The work's split over CTAs and the joining of its parts: mnw_attn_split.cuh.
 //
 // A CTA is WR x WK warps: WR row blocks of 16 query rows, each tile's keys cut
 // over WK warps.  Tiles arrive by 16-byte cp.async through a ring of kStages
@@ -40,47 +34,18 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <algorithm>
 #include <atomic>
+#include <ctime>
 
-#include "mnw_convert.cuh"
-#include "mnw_internal.h"
-#include "mnw_paged.cuh"
-#include "mnw_ptx.cuh"
+#include "mnw_attn_split.cuh"
 
 namespace mnw {
 namespace pattn {
 
-using paged::Batch;
-using paged::FastDiv;
-using paged::Seq;
+constexpr int kTK = 64;       // keys per tile
+constexpr int kMinUnits = 2;  // tiles of a run at least
 
-constexpr int kTK = 64;        // keys per tile
-constexpr int kMinUnits = 2;   // tiles per CTA at least, where there are few
-constexpr float kLn2 = 0.6931471805599453f;
-
-struct Args {
-  Batch bt;
-  const __nv_bfloat16* q;
-  long long q_stride;
-  const uint8_t *kc, *vc;
-  const float *ks, *vs;
-  long long page_bytes;  // bytes between pages of kc and vc
-  FastDiv page_div;
-  int n_pages, page_size, Hq, Hkv, G, blk;
-  float scale_log2;
-  __nv_bfloat16* out;
-  float* lse;
-  long long* starts;  // [B + 1] first unit of each sequence (workspace), [B + 1] = units per run
-  float* part_o;      // [2 * runs][RT][D]
-  float2* part_ml;    // [2 * runs][RT]
-  uint32_t* err;
-};
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
@@ -136,25 +101,6 @@ __device__ __forceinline__ void mma1688(float (&c)[4], const uint32_t (&a)[4], u
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Units of a sequence.
-struct Shape {
-  long long units;
-  int rt, kt;  // row tiles, key tiles (one at least, so that empty caches still write their rows)
-};
-template <int RT>
-__device__ __forceinline__ Shape shape_of(const Seq& s, int G, int Hkv) {
-  Shape h;
-  h.rt = static_cast<int>((static_cast<long long>(s.n) * G + RT - 1) / RT);
-  h.kt = max(1, (s.len + kTK - 1) / kTK);
-  h.units = static_cast<long long>(Hkv) * h.rt * h.kt;
-  return h;
-}
-
-__host__ __device__ __forceinline__ long long run_length(long long units, long long runs) {
-  const long long per = (units + runs - 1) / runs;
-  return per < kMinUnits ? kMinUnits : per;
-}
-
 template <int D, bool INT8, int WR, int WK>
 struct Cfg {
   static constexpr int kWarps = WR * WK, kThreads = kWarps * 32, kRT = WR * 16;
@@ -163,7 +109,9 @@ struct Cfg {
   static constexpr int kScaleBytes = INT8 ? 2 * kTK * 4 : 0;
   static constexpr int kStageBytes = 2 * kTileBytes + kScaleBytes;
   static constexpr int kStages = 3;
-  static constexpr int kMergeBytes = WK > 1 ? kWarps * 16 * (D + 2) * 4 : 0;
+  static constexpr int kMergeBytes = kWarps * 16 * (D + 2) * 4;
+  static constexpr int kJoinBytes = kThreads / (D / 4) * 2 * kJoinBatch * 4;
+  static_assert(WK > 1, "the ring holds the joining's weights");
   static constexpr int kRing = kStages * kStageBytes;
   static constexpr int kSmem = kRing > kMergeBytes ? kRing : kMergeBytes;
 };
@@ -188,9 +136,8 @@ __global__ void __launch_bounds__(WR* WK * 32) paged_attn_kernel(const Args a) {
   constexpr int kKW = kTK / WK;      // keys of a tile per warp
   constexpr int kNB = kKW / 16;      // 16-key blocks per warp
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ long long sh_scan[32];
-  __shared__ long long sh_first;  // first unit of sequence sh_b
-  __shared__ int sh_b;
+  __shared__ SplitShared split;
+  __shared__ int sh_last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int wr = warp / WK, wk = warp % WK;
   const int g8 = lane >> 2, t4 = lane & 3;
@@ -199,80 +146,26 @@ __global__ void __launch_bounds__(WR* WK * 32) paged_attn_kernel(const Args a) {
   pdl_launch_dependents();
   pdl_wait();
 
-  // ---- where this run begins ----
   const Batch& bt = a.bt;
-  long long total = 0;
-  for (int b = tid; b < bt.B; b += kThreads) {
-    bool bad;
-    const Seq s = paged::sequence(bt, b, a.page_size, &bad);
-    if (bad && blockIdx.x == 0 && a.err) atomicOr(a.err, MNW_DEVERR_BAD_LENGTH);
-    total += shape_of<kRT>(s, a.G, a.Hkv).units;
-  }
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
-  if (lane == 0) sh_scan[warp] = total;
-  __syncthreads();
-  total = 0;
-  for (int w = 0; w < C::kWarps; ++w) total += sh_scan[w];
-  const long long per = run_length(total, gridDim.x);
-  const long long u0 = blockIdx.x * per, u1 = min(total, u0 + per);
-  const bool scribe = blockIdx.x == 0;  // run 0 writes the sequences' first units for the joining kernel
-  if (scribe && tid == 0) a.starts[bt.B + 1] = per;
-  if (tid == 0) sh_b = -1;
-  if (u0 >= u1 && !scribe) return;
-  {
-    long long carry = 0;
-    for (int b0 = 0; b0 < bt.B; b0 += kThreads) {
-      const int b = b0 + tid;
-      long long mine = 0;
-      if (b < bt.B) {
-        bool bad;
-        mine = shape_of<kRT>(paged::sequence(bt, b, a.page_size, &bad), a.G, a.Hkv).units;
-      }
-      long long incl = mine;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const long long o = __shfl_up_sync(0xffffffffu, incl, d);
-        if (lane >= d) incl += o;
-      }
-      __syncthreads();
-      if (lane == 31) sh_scan[warp] = incl;
-      __syncthreads();
-      long long before = carry;
-      for (int w = 0; w < warp; ++w) before += sh_scan[w];
-      const long long first = before + incl - mine;
-      if (b < bt.B) {
-        if (scribe) a.starts[b] = first;
-        if (mine > 0 && first <= u0 && u0 < first + mine) {
-          sh_b = b;
-          sh_first = first;
-        }
-      }
-      for (int w = 0; w < C::kWarps; ++w) carry += sh_scan[w];
-    }
-    __syncthreads();
-  }
-  if (u0 >= u1) return;
-
-  int b = sh_b;
-  if (b < 0) return;  // the lengths changed under the kernel
-  long long u = u0, seq_first = sh_first;
+  const Run run = find_run<kRT, kTK, kThreads>(a, &split);
+  if (run.seq < 0) return;  // no units left for this run
+  int b = run.seq, u = run.u0, seq_first = run.first;
+  const int u1 = run.u1;
   bool bad;
   Seq s = paged::sequence(bt, b, a.page_size, &bad);
-  Shape sh = shape_of<kRT>(s, a.G, a.Hkv);
+  Shape sh = shape_of<kRT, kTK>(s, a.G, a.Hkv);
 
   while (u < u1) {
     while (u >= seq_first + sh.units) {
       seq_first += sh.units;
       if (++b >= bt.B) return;
       s = paged::sequence(bt, b, a.page_size, &bad);
-      sh = shape_of<kRT>(s, a.G, a.Hkv);
+      sh = shape_of<kRT, kTK>(s, a.G, a.Hkv);
     }
-    const long long in_seq = u - seq_first;
-    const long long item = in_seq / sh.kt;
-    const int kt0 = static_cast<int>(in_seq - item * sh.kt);
-    const int kt1 = static_cast<int>(min(static_cast<long long>(sh.kt), kt0 + (u1 - u)));
-    const int g = static_cast<int>(item / sh.rt), rt = static_cast<int>(item - static_cast<long long>(g) * sh.rt);
+    const int item = (u - seq_first) / sh.kt;
+    const int item_first = seq_first + item * sh.kt;
+    const int kt0 = u - item_first, kt1 = min(sh.kt, kt0 + (u1 - u));
+    const int g = item / sh.rt, rt = item - g * sh.rt;
     const bool whole = kt0 == 0 && kt1 == sh.kt;
     u += kt1 - kt0;
 
@@ -584,7 +477,7 @@ __global__ void __launch_bounds__(WR* WK * 32) paged_attn_kernel(const Args a) {
     // ---- join the warps' key slices ----
     // element column of accumulator (i, j): j = 0, 1
     auto col = [&](int i, int j) { return INT8 ? kNO * (2 * t4 + j) + i : 8 * i + 2 * t4 + j; };
-    if constexpr (WK > 1) {
+    {
       float* mo = reinterpret_cast<float*>(smem);                       // [warp][16][D]
       float2* ml = reinterpret_cast<float2*>(mo + C::kWarps * 16 * D);  // [warp][16]
 #pragma unroll
@@ -599,12 +492,7 @@ __global__ void __launch_bounds__(WR* WK * 32) paged_attn_kernel(const Args a) {
         ml[warp * 16 + g8 + 8] = make_float2(m1, l1);
       }
       __syncthreads();
-    }
-    const long long run = blockIdx.x;
-    const long long pslot = 2 * run + (kt0 > 0 ? 0 : 1);
-    if constexpr (WK > 1) {
-      const float* mo = reinterpret_cast<const float*>(smem);
-      const float2* ml = reinterpret_cast<const float2*>(mo + C::kWarps * 16 * D);
+      const long long pslot = 2ll * blockIdx.x + (kt0 > 0 ? 0 : 1);
       for (int e = tid * 4; e < rows * D; e += kThreads * 4) {
         const int r = e / D, c = e % D;
         const int w0 = (r >> 4) * WK, rr = r & 15;
@@ -626,123 +514,27 @@ __global__ void __launch_bounds__(WR* WK * 32) paged_attn_kernel(const Args a) {
           acc.w += f * v.w;
         }
         if (whole) {
-          const int ri = rt * kRT + r, i = ri / a.G, hh = ri - i * a.G;
-          const size_t row = static_cast<size_t>(s.start + i) * a.Hq + g * a.G + hh;
+          const size_t row = out_row<kRT>(a, s, g, rt, r);
           const float inv = L == 0.f ? 0.f : 1.f / L;
           *reinterpret_cast<uint2*>(a.out + row * D + c) =
               make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
           if (a.lse && c == 0) a.lse[row] = (M + log2f(L)) * kLn2;
         } else {
-          *reinterpret_cast<float4*>(a.part_o + (pslot * kRT + r) * D + c) = acc;
-          if (c == 0) a.part_ml[pslot * kRT + r] = make_float2(M, L);
-        }
-      }
-      __syncthreads();  // the next item's tiles go where the parts lay
-    } else {
-#pragma unroll
-      for (int hrow = 0; hrow < 2; ++hrow) {
-        const int r = hrow ? r1 : r0;
-        const float M = hrow ? m1 : m0, L = hrow ? l1 : l0;
-        if (r < rows) {
-          if (whole) {
-            const int ri = rt * kRT + r, i = ri / a.G, hh = ri - i * a.G;
-            const size_t row = static_cast<size_t>(s.start + i) * a.Hq + g * a.G + hh;
-            const float inv = L == 0.f ? 0.f : 1.f / L;
-            if constexpr (!INT8) {
-#pragma unroll
-              for (int n = 0; n < kNO; ++n)
-                *reinterpret_cast<uint32_t*>(a.out + row * D + col(n, 0)) =
-                    pack_bf16x2(o[n][2 * hrow] * inv, o[n][2 * hrow + 1] * inv);
-            } else {
-#pragma unroll
-              for (int n = 0; n < kNO; n += 2)
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                  *reinterpret_cast<uint32_t*>(a.out + row * D + col(n, j)) =
-                      pack_bf16x2(o[n][2 * hrow + j] * inv, o[n + 1][2 * hrow + j] * inv);
-            }
-            if (a.lse && t4 == 0) a.lse[row] = (M + log2f(L)) * kLn2;
-          } else {
-            float* dst = a.part_o + (pslot * kRT + r) * D;
-#pragma unroll
-            for (int n = 0; n < kNO; ++n) {
-              dst[col(n, 0)] = o[n][2 * hrow];
-              dst[col(n, 1)] = o[n][2 * hrow + 1];
-            }
-            if (t4 == 0) a.part_ml[pslot * kRT + r] = make_float2(M, L);
-          }
+          __stcg(reinterpret_cast<float4*>(a.part_o + (pslot * kRT + r) * D + c), acc);
+          if (c == 0) __stcg(a.part_ml + pslot * kRT + r, make_float2(M, L));
         }
       }
     }
-  }
-}
-
-// Joins the parts of items that several runs share: one warp per (token, query
-// head) row; rows of items that one run covered are done already.
-template <int D, int RT>
-__global__ void __launch_bounds__(256) paged_join_kernel(const Args a) {
-  pdl_launch_dependents();
-  pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const long long row = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  if (row >= static_cast<long long>(a.bt.T) * a.Hq) return;
-  const int t = static_cast<int>(row / a.Hq), h = static_cast<int>(row % a.Hq);
-  int b;
-  if (a.bt.q_start) {
-    int cnt = 0;
-    for (int j = lane; j < a.bt.B; j += 32) cnt += __ldg(a.bt.q_start + j + 1) <= t ? 1 : 0;
-    b = __reduce_add_sync(0xffffffffu, cnt);
-  } else {
-    b = t / a.bt.n_uniform;
-  }
-  if (b >= a.bt.B) return;
-  bool bad;
-  const Seq s = paged::sequence(a.bt, b, a.page_size, &bad);
-  if (t < s.start || t >= s.start + s.n) return;
-  const Shape sh = shape_of<RT>(s, a.G, a.Hkv);
-  const int g = h / a.G, ri = (t - s.start) * a.G + (h - g * a.G);
-  const int rt = ri / RT, r = ri % RT;
-  const long long per = a.starts[a.bt.B + 1];
-  const long long us = a.starts[b] + (static_cast<long long>(g) * sh.rt + rt) * sh.kt, ue = us + sh.kt;
-  const long long c0 = us / per, c1 = (ue - 1) / per;
-  if (c0 == c1) return;
-  auto slot_of = [&](long long c) { return 2 * c + (c * per > us ? 0 : 1); };
-  float M = -INFINITY;
-  for (long long c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, a.part_ml[slot_of(c) * RT + r].x);
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-  const float base = M == -INFINITY ? 0.f : M;
-  constexpr int V = D / 32;
-  float acc[V], L = 0.f;
-#pragma unroll
-  for (int i = 0; i < V; ++i) acc[i] = 0.f;
-#pragma unroll 4
-  for (long long c = c0; c <= c1; ++c) {
-    const long long p = slot_of(c) * RT + r;
-    const float2 ml = a.part_ml[p];
-    const float f = ex2(ml.x - base);
-    L += f * ml.y;
-    const float* src = a.part_o + p * D + lane * V;
-    if constexpr (V == 4) {
-      const float4 v = *reinterpret_cast<const float4*>(src);
-      acc[0] += f * v.x;
-      acc[1] += f * v.y;
-      acc[2] += f * v.z;
-      acc[3] += f * v.w;
-    } else {
-      const float2 v = *reinterpret_cast<const float2*>(src);
-      acc[0] += f * v.x;
-      acc[1] += f * v.y;
+    if (!whole && a.fused) {
+      const Span sp = span_of(item_first, sh.kt, run.per);
+      if (arrive_last(a, sp, &sh_last)) {
+        float* scratch = reinterpret_cast<float*>(smem) + tid / (D / 4) * 2 * kJoinBatch;
+        for (int r = tid / (D / 4); r < rows; r += kThreads / (D / 4))
+          join_row<D, kRT>(a, s, sp, run.per, g, rt, r, scratch);
+      }
     }
+    __syncthreads();  // the next item's tiles go where the parts lay
   }
-  const float inv = L == 0.f ? 0.f : 1.f / L;
-  __nv_bfloat16* dst = a.out + row * D + lane * V;
-  if constexpr (V == 4)
-    *reinterpret_cast<uint2*>(dst) =
-        make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
-  else
-    *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-  if (a.lse && lane == 0) a.lse[row] = (M + log2f(L)) * kLn2;
 }
 
 // ---- host ----
@@ -750,41 +542,75 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const Args a) {
 // Row tile for `rows` query rows per (sequence, kv head) on average.
 inline int row_tile(long long rows) { return rows <= 16 ? 16 : (rows <= 32 ? 32 : 64); }
 constexpr int kRunsPerSm = 2;  // CTAs resident on an SM
+// The last arrival joins where an item's parts are few: this many rows x parts of an item
+constexpr int kFusedRows = 512;
 
 inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
-inline size_t bytes_starts(int B) { return up256((static_cast<size_t>(B) + 2) * 8); }
-inline size_t bytes_ml(int rt) { return up256(static_cast<size_t>(2) * kRunsPerSm * current_sm_count() * rt * 8); }
-inline size_t bytes_o(int rt, int d) { return static_cast<size_t>(2) * kRunsPerSm * current_sm_count() * rt * d * 4; }
+inline int max_runs() { return kRunsPerSm * current_sm_count(); }
+struct Workspace {
+  size_t arrivals, starts, ml, o, bytes;
+};
+inline Workspace workspace_of(int B, int rt, int d) {
+  Workspace w;
+  const size_t slots = static_cast<size_t>(2) * max_runs();
+  w.arrivals = 0;
+  w.starts = up256(static_cast<size_t>(max_runs()) * 8);
+  w.ml = w.starts + up256((static_cast<size_t>(B) + 1) * 4);
+  w.o = w.ml + up256(slots * rt * 8);
+  w.bytes = w.o + up256(slots * rt * d * 4);
+  return w;
+}
+
+// The call's number in the arrival words: never the same twice in a process,
+// and begun anywhere, so that a word left by anything else does not match.
+inline unsigned long long next_tag() {
+  static std::atomic<unsigned long long> n{[] {
+    timespec ts;
+    clock_gettime(CLOCK_REALTIME, &ts);
+    return (static_cast<unsigned long long>(ts.tv_sec) * 1000000007ull + ts.tv_nsec) * 0x9E3779B97F4A7C15ull;
+  }()};
+  const unsigned long long v = n.fetch_add(1ull << 16, std::memory_order_relaxed) & ~0xFFFFull;
+  return v ? v : next_tag();
+}
 
 template <int D, bool INT8, int WR, int WK>
-cudaError_t launch(Args& a, uint8_t* ws, cudaStream_t st) {
+int launch(Args& a, uint8_t* ws, cudaStream_t st) {
   using C = Cfg<D, INT8, WR, WK>;
   auto kern = paged_attn_kernel<D, INT8, WR, WK>;
   static std::atomic<uint64_t> attr{0};
   uint64_t bit;
   if (attrs_needed(attr, &bit)) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-    if (e != cudaSuccess) return e;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
+      return MNW_E_CUDA;
     attrs_done(attr, bit);
   }
-  a.starts = reinterpret_cast<long long*>(ws);
-  a.part_ml = reinterpret_cast<float2*>(ws + bytes_starts(a.bt.B));
-  a.part_o = reinterpret_cast<float*>(ws + bytes_starts(a.bt.B) + bytes_ml(C::kRT));
+  const Workspace w = workspace_of(a.bt.B, C::kRT, D);
+  a.arrivals = reinterpret_cast<unsigned long long*>(ws + w.arrivals);
+  a.starts = reinterpret_cast<int*>(ws + w.starts);
+  a.part_ml = reinterpret_cast<float2*>(ws + w.ml);
+  a.part_o = reinterpret_cast<float*>(ws + w.o);
+  a.min_units = kMinUnits;
   // most units that the batch can have: every row tile over a full block table
   const long long kt = (static_cast<long long>(a.bt.max_pages) * a.page_size + kTK - 1) / kTK;
   const long long tiles = (static_cast<long long>(a.bt.T) * a.G) / C::kRT + a.bt.B;
-  const long long units = tiles * a.Hkv * (kt < 1 ? 1 : kt);
-  long long runs = static_cast<long long>(kRunsPerSm) * current_sm_count();
-  const long long most = (units + kMinUnits - 1) / kMinUnits;
-  if (runs > most) runs = most;
-  cudaError_t e = launch_pdl(kern, dim3(static_cast<unsigned>(runs)), dim3(C::kThreads), C::kSmem, st, a);
-  if (e != cudaSuccess || kt <= 1) return e;  // items of one tile are never shared
+  const long long items = tiles * a.Hkv, units = items * kt;
+  if (units > 0x7fffffffll - max_runs()) return MNW_E_UNSUPPORTED;
+  const int runs = static_cast<int>(std::min<long long>(max_runs(), (units + kMinUnits - 1) / kMinUnits));
   const long long rows = static_cast<long long>(a.bt.T) * a.Hq;
-  return launch_pdl(paged_join_kernel<D, C::kRT>, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0, st, a);
+  const long long item_rows = std::min<long long>(C::kRT, static_cast<long long>(a.bt.T) * a.G);
+  a.fused = item_rows * ((runs + items - 1) / items) <= kFusedRows;
+  a.tag = next_tag();
+  if (launch_pdl(kern, dim3(runs), dim3(C::kThreads), C::kSmem, st, a) != cudaSuccess) return MNW_E_CUDA;
+  if (a.fused || kt <= 1) return MNW_OK;  // items of one tile are never shared
+  constexpr int kJoinRows = kJoinThreads / (D / 4);
+  return launch_pdl(paged_join_kernel<D, C::kRT, kTK>, dim3(static_cast<unsigned>((rows + kJoinRows - 1) / kJoinRows)),
+                    dim3(kJoinThreads), 0, st, a) == cudaSuccess
+             ? MNW_OK
+             : MNW_E_CUDA;
 }
 
 template <int D, bool INT8>
-cudaError_t launch_rows(Args& a, uint8_t* ws, int rt, cudaStream_t st) {
+int launch_rows(Args& a, uint8_t* ws, int rt, cudaStream_t st) {
   if (rt == 16) return launch<D, INT8, 1, 4>(a, ws, st);
   if (rt == 32) return launch<D, INT8, 2, 2>(a, ws, st);
   return launch<D, INT8, 4, 2>(a, ws, st);
@@ -800,7 +626,7 @@ extern "C" {
 size_t mnw_attn_paged_workspace_size(int B, int T, int Hq, int Hkv, int d) {
   if (B <= 0 || T <= 0 || Hq <= 0 || Hkv <= 0 || d <= 0 || Hq % Hkv) return 0;
   const int rt = pattn::row_tile((static_cast<long long>(T) + B - 1) / B * (Hq / Hkv));
-  return pattn::up256(pattn::bytes_starts(B) + pattn::bytes_ml(rt) + pattn::bytes_o(rt, d));
+  return pattn::workspace_of(B, rt, d).bytes;
 }
 
 int mnw_attn_paged(const void* q, long long q_stride, int B, int T, int Hq, int Hkv, int d, const void* k_cache,
@@ -846,12 +672,8 @@ int mnw_attn_paged(const void* q, long long q_stride, int B, int T, int Hq, int 
   const int rt = row_tile((static_cast<long long>(T) + B - 1) / B * a.G);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   auto* w = static_cast<uint8_t*>(ws);
-  cudaError_t e;
-  if (d == 128)
-    e = int8 ? launch_rows<128, true>(a, w, rt, st) : launch_rows<128, false>(a, w, rt, st);
-  else
-    e = int8 ? launch_rows<64, true>(a, w, rt, st) : launch_rows<64, false>(a, w, rt, st);
-  return e == cudaSuccess ? MNW_OK : MNW_E_CUDA;
+  if (d == 128) return int8 ? launch_rows<128, true>(a, w, rt, st) : launch_rows<128, false>(a, w, rt, st);
+  return int8 ? launch_rows<64, true>(a, w, rt, st) : launch_rows<64, false>(a, w, rt, st);
 }
 
 }  // extern "C"
