@@ -43,8 +43,7 @@
 namespace mnw {
 namespace pattn {
 
-constexpr int kTK = 64;       // keys per tile
-constexpr int kMinUnits = 2;  // tiles of a run at least
+constexpr int kMinUnits = 1;  // tiles of a run at least
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -104,16 +103,16 @@ __device__ __forceinline__ void mma1688(float (&c)[4], const uint32_t (&a)[4], u
 template <int D, bool INT8, int WR, int WK>
 struct Cfg {
   static constexpr int kWarps = WR * WK, kThreads = kWarps * 32, kRT = WR * 16;
+  static constexpr int kTK = INT8 ? 128 : 64;  // keys per tile: 16 KB of keys either way (d = 128)
   static constexpr int kRowBytes = INT8 ? D : 2 * D;
   static constexpr int kTileBytes = kTK * kRowBytes;
   static constexpr int kScaleBytes = INT8 ? 2 * kTK * 4 : 0;
   static constexpr int kStageBytes = 2 * kTileBytes + kScaleBytes;
   static constexpr int kStages = 3;
-  static constexpr int kMergeBytes = kWarps * 16 * (D + 2) * 4;
-  static constexpr int kJoinBytes = kThreads / (D / 4) * 2 * kJoinBatch * 4;
-  static_assert(WK > 1, "the ring holds the joining's weights");
-  static constexpr int kRing = kStages * kStageBytes;
-  static constexpr int kSmem = kRing > kMergeBytes ? kRing : kMergeBytes;
+  static constexpr int kSmem = kStages * kStageBytes;
+  // at an item's end the warps' outputs meet in the stage just read
+  static_assert(kWarps * 16 * D * 4 <= kStageBytes && kTK <= kThreads && WK > 1);
+  static_assert(kThreads / (D / 4) * 2 * kJoinBatch * 4 <= kStageBytes);
 };
 
 // Byte offset of 16-byte chunk c of row r in a tile: chunks are exchanged by
@@ -130,14 +129,15 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
 template <int D, bool INT8, int WR, int WK>
 __global__ void __launch_bounds__(WR* WK * 32) paged_attn_kernel(const Args a) {
   using C = Cfg<D, INT8, WR, WK>;
-  constexpr int kRT = C::kRT, kThreads = C::kThreads, kStages = C::kStages;
+  constexpr int kRT = C::kRT, kThreads = C::kThreads, kStages = C::kStages, kTK = C::kTK;
   constexpr int kKS = D / 16;        // k steps of the first product
   constexpr int kNO = D / 8;         // output column tiles
   constexpr int kKW = kTK / WK;      // keys of a tile per warp
   constexpr int kNB = kKW / 16;      // 16-key blocks per warp
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ SplitShared split;
-  __shared__ int sh_last;
+  __shared__ float2 ml[C::kWarps * 16];
+  __shared__ int2 rows_at[kStages][kTK];  // (page or -1, head row within the page) of a tile's keys
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int wr = warp / WK, wk = warp % WK;
   const int g8 = lane >> 2, t4 = lane & 3;
@@ -146,50 +146,100 @@ __global__ void __launch_bounds__(WR* WK * 32) paged_attn_kernel(const Args a) {
   pdl_launch_dependents();
   pdl_wait();
 
-  const Batch& bt = a.bt;
   const Run run = find_run<kRT, kTK, kThreads>(a, &split);
   if (run.seq < 0) return;  // no units left for this run
-  int b = run.seq, u = run.u0, seq_first = run.first;
-  const int u1 = run.u1;
-  bool bad;
-  Seq s = paged::sequence(bt, b, a.page_size, &bad);
-  Shape sh = shape_of<kRT, kTK>(s, a.G, a.Hkv);
+  Cursor<kRT, kTK> cc;  // the tile computed
+  cc.set(a, run);
+  int item_first = run.u0 - cc.kt;  // first unit of its item
+  const int tiles = run.pad == 1 ? run.u1 - run.u0 : min(run.u1 - run.u0, cc.sh.kt - cc.kt);
+  if (tiles <= 0) return;
 
-  while (u < u1) {
-    while (u >= seq_first + sh.units) {
-      seq_first += sh.units;
-      if (++b >= bt.B) return;
-      s = paged::sequence(bt, b, a.page_size, &bad);
-      sh = shape_of<kRT, kTK>(s, a.G, a.Hkv);
+  // ---- tile loads: page lookups run one tile ahead of the copies, those kStages - 1 ahead of the products ----
+  Cursor<kRT, kTK> lc = cc;  // the tile looked up next
+  auto look = [&](int2& at) {  // raw page entry and head row of key tid of tile lc; then on to the next tile
+    const int p = lc.kt * kTK + tid;
+    at = make_int2(0, -1);
+    if (tid < kTK && p < lc.s.len) {
+      const int pi = static_cast<int>(paged::quotient(p, a.page_div));
+      at.x = __ldg(a.bt.block_table + static_cast<size_t>(lc.b) * a.bt.max_pages + pi);
+      at.y = lc.g * a.page_size + (p - pi * a.page_size);
     }
-    const int item = (u - seq_first) / sh.kt;
-    const int item_first = seq_first + item * sh.kt;
-    const int kt0 = u - item_first, kt1 = min(sh.kt, kt0 + (u1 - u));
-    const int g = item / sh.rt, rt = item - g * sh.rt;
-    const bool whole = kt0 == 0 && kt1 == sh.kt;
-    u += kt1 - kt0;
+    if (++lc.kt == lc.sh.kt) lc.next_item(a, run.pad);
+  };
+  auto keep = [&](int2 at, int slot) {
+    if (at.y < 0) {
+      at.x = -1;
+    } else if (static_cast<unsigned>(at.x) >= static_cast<unsigned>(a.n_pages)) {
+      at.x = -1;
+      if (a.err) atomicOr(a.err, MNW_DEVERR_BAD_PAGE);
+    }
+    if (tid < kTK) rows_at[slot][tid] = at;
+  };
+  auto load_tile = [&](int slot) {
+    const uint32_t st = sbase + slot * C::kStageBytes;
+    constexpr int kCh = C::kRowBytes / 16;  // chunks per row
+    constexpr int kRP = kThreads / kCh;     // rows per pass
+    const int c = tid % kCh;
+#pragma unroll
+    for (int i = 0; i < kTK / kRP; ++i) {
+      const int r = i * kRP + tid / kCh;
+      const int2 at = rows_at[slot][r];
+      const uint32_t n = at.x >= 0 ? 16u : 0u;
+      const long long off = n ? at.x * a.page_bytes + static_cast<long long>(at.y) * C::kRowBytes + c * 16 : 0;
+      const uint32_t to = st + chunk_at<D, INT8>(r, c);
+      cp_async16(to, a.kc + off, n);
+      cp_async16(to + C::kTileBytes, a.vc + off, n);
+    }
+    if constexpr (INT8) {
+      for (int r2 = tid; r2 < 2 * kTK; r2 += kThreads) {
+        const int2 at = rows_at[slot][r2 % kTK];
+        const uint32_t n = at.x >= 0 ? 4u : 0u;
+        const long long off = n ? static_cast<long long>(at.x) * a.Hkv * a.page_size + at.y : 0;
+        cp_async4(st + 2 * C::kTileBytes + r2 * 4, (r2 < kTK ? a.ks : a.vs) + off, n);
+      }
+    }
+  };
+  {
+    int2 at[kStages];
+#pragma unroll
+    for (int i = 0; i < kStages; ++i)
+      if (i < tiles) look(at[i]);
+#pragma unroll
+    for (int i = 0; i < kStages; ++i)
+      if (i < tiles) keep(at[i], i);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) {
+      if (i < tiles) load_tile(i);
+      cp_commit();
+    }
+  }
 
-    const int rows = min(kRT, s.n * a.G - rt * kRT);  // query rows of this tile (n * G < 2^31: checked by the host)
-    // limit of a query row r: its first forbidden position
-    auto limit = [&](int r) -> int {
-      const int i = (rt * kRT + r) / a.G;
-      const int p = s.len - s.n + i;
-      if (p < 0) return 0;
-      const long long e = (static_cast<long long>(p / a.blk) + 1) * a.blk;
-      return e < s.len ? static_cast<int>(e) : s.len;
-    };
-    const int lim_lo = limit(0), lim_hi = limit(rows - 1);
-    const int r0 = wr * 16 + g8, r1 = r0 + 8;
-    const int lim0 = r0 < rows ? limit(r0) : lim_hi, lim1 = r1 < rows ? limit(r1) : lim_hi;
-
+  // ---- state of the item in hand ----
+  uint32_t qf[kKS][4];
+  float qfac0 = a.scale_log2, qfac1 = a.scale_log2;  // score factor of rows r0, r1
+  const int r0 = wr * 16 + g8, r1 = r0 + 8;
+  int rows = 0, lim_lo = 0, lim_hi = 0, lim0 = 0, lim1 = 0;
+  float o[kNO][4];
+  float m0 = 0.f, m1 = 0.f, l0 = 0.f, l1 = 0.f;
+  int kt_begin = 0;
+  auto begin_item = [&]() {
+    kt_begin = cc.kt;
+    rows = min(kRT, cc.s.n * a.G - cc.rt * kRT);
+    lim_lo = row_limit(a, cc.s, cc.rt * kRT);
+    lim_hi = row_limit(a, cc.s, cc.rt * kRT + rows - 1);
+    lim0 = r0 < rows ? row_limit(a, cc.s, cc.rt * kRT + r0) : lim_hi;
+    lim1 = r1 < rows ? row_limit(a, cc.s, cc.rt * kRT + r1) : lim_hi;
+#pragma unroll
+    for (int i = 0; i < kNO; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    m0 = m1 = -INFINITY;
+    l0 = l1 = 0.f;
     // ---- query fragments ----
-    uint32_t qf[kKS][4];
-    float qfac0 = a.scale_log2, qfac1 = a.scale_log2;  // score factor of rows r0, r1
     {
       auto row_ptr = [&](int r) -> const __nv_bfloat16* {
-        const int ri = rt * kRT + r;
-        const int i = ri / a.G, hh = ri - i * a.G;
-        return a.q + static_cast<long long>(s.start + i) * a.q_stride + static_cast<long long>(g * a.G + hh) * D;
+        const int ri = cc.rt * kRT + r;
+        const int i = static_cast<int>(paged::quotient(ri, a.g_div)), hh = ri - i * a.G;
+        return a.q + static_cast<long long>(cc.s.start + i) * a.q_stride + static_cast<long long>(cc.g * a.G + hh) * D;
       };
       const bool ok0 = r0 < rows, ok1 = r1 < rows;
       const __nv_bfloat16 *p0 = row_ptr(ok0 ? r0 : 0), *p1 = row_ptr(ok1 ? r1 : 0);
@@ -242,83 +292,25 @@ __global__ void __launch_bounds__(WR* WK * 32) paged_attn_kernel(const Args a) {
           }
       }
     }
+  };
 
-    // ---- tile loads ----
-    const int32_t* table = bt.block_table + static_cast<size_t>(b) * bt.max_pages;
-    auto load_tile = [&](int kt, int stage) {
-      const uint32_t st = sbase + stage * C::kStageBytes;
-      constexpr int kCh = C::kRowBytes / 16;        // chunks per row
-      constexpr int kRP = kThreads / kCh;           // rows per pass
-      const int c = tid % kCh;
-#pragma unroll
-      for (int i = 0; i < kTK / kRP; ++i) {
-        const int r = i * kRP + tid / kCh;
-        const int p = kt * kTK + r;
-        const uint8_t *ks = a.kc, *vs = a.vc;
-        uint32_t n = 0;
-        if (p < s.len) {
-          const int pi = static_cast<int>(paged::quotient(p, a.page_div));
-          const int page = __ldg(table + pi);
-          if (static_cast<unsigned>(page) < static_cast<unsigned>(a.n_pages)) {
-            const long long off = page * a.page_bytes +
-                                  (static_cast<long long>(g) * a.page_size + (p - pi * a.page_size)) * C::kRowBytes + c * 16;
-            ks += off;
-            vs += off;
-            n = 16;
-          } else if (a.err) {
-            atomicOr(a.err, MNW_DEVERR_BAD_PAGE);
-          }
-        }
-        const uint32_t at = chunk_at<D, INT8>(r, c);
-        cp_async16(st + at, ks, n);
-        cp_async16(st + C::kTileBytes + at, vs, n);
-      }
-      if constexpr (INT8) {
-        for (int r2 = tid; r2 < 2 * kTK; r2 += kThreads) {
-          const int r = r2 % kTK;
-          const int p = kt * kTK + r;
-          const float* src = r2 < kTK ? a.ks : a.vs;
-          uint32_t n = 0;
-          if (p < s.len) {
-            const int pi = static_cast<int>(paged::quotient(p, a.page_div));
-            const int page = __ldg(table + pi);
-            if (static_cast<unsigned>(page) < static_cast<unsigned>(a.n_pages)) {
-              src += (static_cast<long long>(page) * a.Hkv + g) * a.page_size + (p - pi * a.page_size);
-              n = 4;
-            }
-          }
-          cp_async4(st + 2 * C::kTileBytes + r2 * 4, src, n);
-        }
-      }
-    };
-
-    // ---- main loop ----
-    float o[kNO][4];
-#pragma unroll
-    for (int i = 0; i < kNO; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-
-    // tiles past every row's limit add nothing
-    const int kte = min(kt1, (lim_hi + kTK - 1) / kTK);
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) {
-      if (kt0 + i < kte) load_tile(kt0 + i, i);
+  for (int t = 0, slot = 0; t < tiles; ++t) {
+    cp_wait<kStages - 2>();
+    __syncthreads();
+    {
+      int ns = slot + kStages - 1;
+      if (ns >= kStages) ns -= kStages;
+      if (t + kStages - 1 < tiles) load_tile(ns);
       cp_commit();
     }
-    int slot = 0;
-    for (int kt = kt0; kt < kte; ++kt) {
-      cp_wait<kStages - 2>();
-      __syncthreads();
-      {
-        int ns = slot + kStages - 1;
-        if (ns >= kStages) ns -= kStages;
-        if (kt + kStages - 1 < kte) load_tile(kt + kStages - 1, ns);
-        cp_commit();
-      }
-      const uint32_t kst = sbase + slot * C::kStageBytes, vst = kst + C::kTileBytes;
-      const uint8_t* stage = smem + slot * C::kStageBytes;
-      if (++slot == kStages) slot = 0;
+    int2 ahead;
+    const bool more = t + kStages < tiles;
+    if (more) look(ahead);
+    if (t == 0 || cc.kt == 0) begin_item();
+    const uint32_t kst = sbase + slot * C::kStageBytes, vst = kst + C::kTileBytes;
+    uint8_t* stage = smem + slot * C::kStageBytes;
 
+    if (cc.kt * kTK < lim_hi) {  // a tile past every row's limit adds nothing
       // scores of the warp's keys
       float sc[2 * kNB][4];
 #pragma unroll
@@ -359,8 +351,8 @@ __global__ void __launch_bounds__(WR* WK * 32) paged_attn_kernel(const Args a) {
           sc[i][3] *= f.y;
         }
       }
-      const int key_base = kt * kTK + wk * kKW + 2 * t4;
-      if ((kt + 1) * kTK > lim_lo) {  // some row's limit lies in this tile
+      const int key_base = cc.kt * kTK + wk * kKW + 2 * t4;
+      if ((cc.kt + 1) * kTK > lim_lo) {  // some row's limit lies in this tile
 #pragma unroll
         for (int i = 0; i < 2 * kNB; ++i) {
           const int k = key_base + 8 * i;
@@ -466,20 +458,21 @@ __global__ void __launch_bounds__(WR* WK * 32) paged_attn_kernel(const Args a) {
         }
       }
     }
-    cp_wait<0>();
-#pragma unroll
-    for (int d = 1; d < 4; d <<= 1) {
-      l0 += __shfl_xor_sync(0xffffffffu, l0, d);
-      l1 += __shfl_xor_sync(0xffffffffu, l1, d);
-    }
-    __syncthreads();  // the ring is free: every copy has landed and been read
 
-    // ---- join the warps' key slices ----
-    // element column of accumulator (i, j): j = 0, 1
-    auto col = [&](int i, int j) { return INT8 ? kNO * (2 * t4 + j) + i : 8 * i + 2 * t4 + j; };
-    {
-      float* mo = reinterpret_cast<float*>(smem);                       // [warp][16][D]
-      float2* ml = reinterpret_cast<float2*>(mo + C::kWarps * 16 * D);  // [warp][16]
+    if (more) keep(ahead, slot);  // this tile's entries are read
+
+    if (cc.kt + 1 == cc.sh.kt || t + 1 == tiles) {
+      // ---- the item's end, or the run's: join the warps' key slices ----
+      const bool whole = kt_begin == 0 && cc.kt + 1 == cc.sh.kt;
+#pragma unroll
+      for (int d = 1; d < 4; d <<= 1) {
+        l0 += __shfl_xor_sync(0xffffffffu, l0, d);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, d);
+      }
+      __syncthreads();  // the stage is read; copies into it begin behind the next barrier of the loop
+      float* mo = reinterpret_cast<float*>(stage);  // [warp][16][D]
+      // element column of accumulator (i, j): j = 0, 1
+      auto col = [&](int i, int j) { return INT8 ? kNO * (2 * t4 + j) + i : 8 * i + 2 * t4 + j; };
 #pragma unroll
       for (int i = 0; i < kNO; ++i)
 #pragma unroll
@@ -492,7 +485,7 @@ __global__ void __launch_bounds__(WR* WK * 32) paged_attn_kernel(const Args a) {
         ml[warp * 16 + g8 + 8] = make_float2(m1, l1);
       }
       __syncthreads();
-      const long long pslot = 2ll * blockIdx.x + (kt0 > 0 ? 0 : 1);
+      const long long pslot = 2ll * blockIdx.x + (kt_begin > 0 ? 0 : 1);
       for (int e = tid * 4; e < rows * D; e += kThreads * 4) {
         const int r = e / D, c = e % D;
         const int w0 = (r >> 4) * WK, rr = r & 15;
@@ -514,7 +507,7 @@ __global__ void __launch_bounds__(WR* WK * 32) paged_attn_kernel(const Args a) {
           acc.w += f * v.w;
         }
         if (whole) {
-          const size_t row = out_row<kRT>(a, s, g, rt, r);
+          const size_t row = out_row<kRT>(a, cc.s, cc.g, cc.rt, r);
           const float inv = L == 0.f ? 0.f : 1.f / L;
           *reinterpret_cast<uint2*>(a.out + row * D + c) =
               make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
@@ -524,23 +517,26 @@ __global__ void __launch_bounds__(WR* WK * 32) paged_attn_kernel(const Args a) {
           if (c == 0) __stcg(a.part_ml + pslot * kRT + r, make_float2(M, L));
         }
       }
-    }
-    if (!whole && a.fused) {
-      const Span sp = span_of(item_first, sh.kt, run.per);
-      if (arrive_last(a, sp, &sh_last)) {
-        float* scratch = reinterpret_cast<float*>(smem) + tid / (D / 4) * 2 * kJoinBatch;
-        for (int r = tid / (D / 4); r < rows; r += kThreads / (D / 4))
-          join_row<D, kRT>(a, s, sp, run.per, g, rt, r, scratch);
+      if (!whole && a.fused) {
+        const Span sp = span_of(item_first, cc.sh.ku, run.per);
+        if (all_arrived(a, sp, run.per, pslot)) {
+          float* scratch = reinterpret_cast<float*>(stage) + tid / (D / 4) * 2 * kJoinBatch;
+          for (int r = tid / (D / 4); r < rows; r += kThreads / (D / 4))
+            join_row<D, kRT>(a, cc.s, sp, run.per, cc.g, cc.rt, r, scratch);
+          clear_arrivals(a, sp, run.per);
+        }
       }
+      item_first += cc.sh.ku;
     }
-    __syncthreads();  // the next item's tiles go where the parts lay
+    if (++cc.kt == cc.sh.kt) cc.next_item(a, run.pad);
+    if (++slot == kStages) slot = 0;
   }
 }
 
 // ---- host ----
 
 // Row tile for `rows` query rows per (sequence, kv head) on average.
-inline int row_tile(long long rows) { return rows <= 16 ? 16 : (rows <= 32 ? 32 : 64); }
+inline int row_tile(long long rows) { return rows <= 16 ? 16 : 32; }
 constexpr int kRunsPerSm = 2;  // CTAs resident on an SM
 // The last arrival joins where an item's parts are few: this many rows x parts of an item
 constexpr int kFusedRows = 512;
@@ -554,14 +550,14 @@ inline Workspace workspace_of(int B, int rt, int d) {
   Workspace w;
   const size_t slots = static_cast<size_t>(2) * max_runs();
   w.arrivals = 0;
-  w.starts = up256(static_cast<size_t>(max_runs()) * 8);
-  w.ml = w.starts + up256((static_cast<size_t>(B) + 1) * 4);
+  w.starts = up256(slots * 8);
+  w.ml = w.starts + up256((static_cast<size_t>(B) + 2) * 4);
   w.o = w.ml + up256(slots * rt * 8);
   w.bytes = w.o + up256(slots * rt * d * 4);
   return w;
 }
 
-// The call's number in the arrival words: never the same twice in a process,
+// The call's number in the parts' marks: never the same twice in a process,
 // and begun anywhere, so that a word left by anything else does not match.
 inline unsigned long long next_tag() {
   static std::atomic<unsigned long long> n{[] {
@@ -569,7 +565,7 @@ inline unsigned long long next_tag() {
     clock_gettime(CLOCK_REALTIME, &ts);
     return (static_cast<unsigned long long>(ts.tv_sec) * 1000000007ull + ts.tv_nsec) * 0x9E3779B97F4A7C15ull;
   }()};
-  const unsigned long long v = n.fetch_add(1ull << 16, std::memory_order_relaxed) & ~0xFFFFull;
+  const unsigned long long v = n.fetch_add(1, std::memory_order_relaxed);
   return v ? v : next_tag();
 }
 
@@ -584,6 +580,7 @@ int launch(Args& a, uint8_t* ws, cudaStream_t st) {
       return MNW_E_CUDA;
     attrs_done(attr, bit);
   }
+  constexpr int kTK = C::kTK;
   const Workspace w = workspace_of(a.bt.B, C::kRT, D);
   a.arrivals = reinterpret_cast<unsigned long long*>(ws + w.arrivals);
   a.starts = reinterpret_cast<int*>(ws + w.starts);
@@ -612,8 +609,7 @@ int launch(Args& a, uint8_t* ws, cudaStream_t st) {
 template <int D, bool INT8>
 int launch_rows(Args& a, uint8_t* ws, int rt, cudaStream_t st) {
   if (rt == 16) return launch<D, INT8, 1, 4>(a, ws, st);
-  if (rt == 32) return launch<D, INT8, 2, 2>(a, ws, st);
-  return launch<D, INT8, 4, 2>(a, ws, st);
+  return launch<D, INT8, 2, 2>(a, ws, st);
 }
 
 }  // namespace pattn
@@ -664,7 +660,9 @@ int mnw_attn_paged(const void* q, long long q_stride, int B, int T, int Hq, int 
   a.Hq = Hq;
   a.Hkv = Hkv;
   a.G = Hq / Hkv;
+  a.g_div = paged::fast_div(a.G);
   a.blk = blk;
+  a.blk_div = paged::fast_div(blk);
   a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   a.out = static_cast<__nv_bfloat16*>(out);
   a.lse = lse;

@@ -11,11 +11,10 @@
 //
 // Joining: parts are added in run order, so the result does not depend on
 // timing.  Few parts and rows: the CTA that arrives last at an item joins it
-// (a launch less).  Otherwise a second kernel does, a CTA per few rows.
-// Arrivals are counted in a workspace word tagged with the call's number, so
-// the workspace needs no clearing: a word of another call or of anything else
-// counts as zero, and the last arrival leaves zero (a replayed graph has the
-// same number).
+// (a launch less).  Otherwise a second kernel does.  A part that is written is
+// marked with the call's number, so the workspace needs no clearing: a mark of
+// another call, or anything else, is none; the joining CTA clears the item's
+// marks (a replayed graph brings the same number).
 #pragma once
 #include <cuda_bf16.h>
 
@@ -41,17 +40,18 @@ struct Args {
   const float *ks, *vs;
   long long page_bytes;  // bytes between pages of kc and vc
   FastDiv page_div;
+  FastDiv g_div, blk_div;
   int n_pages, page_size, Hq, Hkv, G, blk;
   int min_units;  // units of a run at least, where there are few
   float scale_log2;
   __nv_bfloat16* out;
   float* lse;
   // workspace
-  unsigned long long* arrivals;  // [runs] of the item that begins in run c and goes on in the next
-  int* starts;                   // [B] first unit of each sequence, [B] = units per run (for the joining kernel)
+  unsigned long long* arrivals;  // [2 * runs] marks of the parts
+  int* starts;                   // [B + 2] first unit of each sequence, then units per run and their padding
   float* part_o;                 // [2 * runs][RT][D]
   float2* part_ml;               // [2 * runs][RT]
-  unsigned long long tag;        // the call's number << 16
+  unsigned long long tag;        // the call's number
   int fused;                     // the last arrival joins
   uint32_t* err;
 };
@@ -62,30 +62,35 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Units of a sequence (the host bounds their sum below 2^31).
+// Units of a sequence (the host bounds their sum below 2^31).  An item counts
+// as a multiple of `pad` units, so that with runs of `pad` none begins inside
+// one item and goes on in the next.
 struct Shape {
-  int units, rt, kt;  // row tiles, key tiles (one at least, so that empty caches still write their rows)
+  int units, rt, kt, ku;  // row tiles; key tiles of an item (one at least, so that empty caches still write their rows); its units
 };
 template <int RT, int TK>
-__device__ __forceinline__ Shape shape_of(const Seq& s, int G, int Hkv) {
+__device__ __forceinline__ Shape shape_of(const Seq& s, int G, int Hkv, int pad) {
   Shape h;
   h.rt = (s.n * G + RT - 1) / RT;
   h.kt = max(1, (s.len + TK - 1) / TK);
-  h.units = Hkv * h.rt * h.kt;
+  h.ku = pad == 1 ? h.kt : (h.kt + pad - 1) / pad * pad;
+  h.units = Hkv * h.rt * h.ku;
   return h;
 }
 
 struct SplitShared {
-  int scan[32];
+  int scan[32], pads[32];
   int seq, first;  // sequence of the run's first unit and its first unit
 };
 
 struct Run {
-  int u0, u1, per;   // units [u0, u1) of runs of `per`
-  int seq, first;    // sequence that holds u0 (-1: none) and its first unit
+  int u0, u1, per, pad;  // units [u0, u1) of runs of `per`
+  int seq, first;        // sequence that holds u0 (-1: none) and its first unit
 };
 
-// Where run blockIdx.x begins.  All threads call; ends with a barrier.
+// Where run blockIdx.x begins.  All threads call; ends with a barrier.  Where
+// all items, cut into runs of min_units each, fit the grid, runs do not cross
+// items (latency); otherwise the runs are equal (throughput).
 template <int RT, int TK, int THREADS>
 __device__ __forceinline__ Run find_run(const Args& a, SplitShared* sh) {
   constexpr int kWarps = THREADS / 32;
@@ -93,30 +98,44 @@ __device__ __forceinline__ Run find_run(const Args& a, SplitShared* sh) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const bool scribe = blockIdx.x == 0;  // run 0 reports bad lengths and writes the sequences' first units
   if (tid == 0) sh->seq = -1;
-  Run r;
-  int carry = 0, first = 0, mine = 0, total = 0;
-  // up to THREADS sequences a pass; beyond one pass, the total first
-  const int passes = (bt.B + THREADS - 1) / THREADS;
-  if (passes > 1) {
-    for (int b = tid; b < bt.B; b += THREADS) {
-      bool bad;
-      total += shape_of<RT, TK>(paged::sequence(bt, b, a.page_size, &bad), a.G, a.Hkv).units;
-    }
-    total = __reduce_add_sync(0xffffffffu, total);
-    if (lane == 0) sh->scan[warp] = total;
-    __syncthreads();
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) total += sh->scan[w];
-    __syncthreads();
+  int total = 0, padded = 0;
+  Seq s{};
+  for (int b = tid; b < bt.B; b += THREADS) {
+    bool bad;
+    s = paged::sequence(bt, b, a.page_size, &bad);
+    if (bad && scribe && a.err) atomicOr(a.err, MNW_DEVERR_BAD_LENGTH);
+    const Shape one = shape_of<RT, TK>(s, a.G, a.Hkv, 1);
+    total += one.units;
+    padded += a.Hkv * one.rt * ((one.kt + a.min_units - 1) / a.min_units);
   }
-  for (int p = 0; p < passes; ++p) {
-    const int b = p * THREADS + tid;
-    mine = 0;
+  const int tw = __reduce_add_sync(0xffffffffu, total), pw = __reduce_add_sync(0xffffffffu, min(padded, 1 << 20));
+  if (lane == 0) {
+    sh->scan[warp] = tw;
+    sh->pads[warp] = pw;
+  }
+  __syncthreads();
+  total = padded = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    total += sh->scan[w];
+    padded += sh->pads[w];
+  }
+  Run r;
+  const int runs = gridDim.x;
+  const bool aligned_runs = padded <= runs;
+  r.pad = aligned_runs ? a.min_units : 1;
+  r.per = aligned_runs ? a.min_units : max(a.min_units, (total + runs - 1) / runs);
+  const int limit = aligned_runs ? padded * a.min_units : total;
+  r.u0 = static_cast<int>(min(static_cast<long long>(blockIdx.x) * r.per, static_cast<long long>(limit)));
+  r.u1 = min(limit, r.u0 + r.per);
+  int carry = 0;
+  for (int b0 = 0; b0 < bt.B; b0 += THREADS) {
+    const int b = b0 + tid;
+    int mine = 0;
     if (b < bt.B) {
       bool bad;
-      mine = shape_of<RT, TK>(paged::sequence(bt, b, a.page_size, &bad), a.G, a.Hkv).units;
-      if (bad && scribe && a.err) atomicOr(a.err, MNW_DEVERR_BAD_LENGTH);
+      if (bt.B > THREADS) s = paged::sequence(bt, b, a.page_size, &bad);
+      mine = shape_of<RT, TK>(s, a.G, a.Hkv, r.pad).units;
     }
     int incl = mine;
 #pragma unroll
@@ -124,6 +143,7 @@ __device__ __forceinline__ Run find_run(const Args& a, SplitShared* sh) {
       const int o = __shfl_up_sync(0xffffffffu, incl, d);
       if (lane >= d) incl += o;
     }
+    __syncthreads();  // the sums above are read
     if (lane == 31) sh->scan[warp] = incl;
     __syncthreads();
     int before = carry;
@@ -133,11 +153,7 @@ __device__ __forceinline__ Run find_run(const Args& a, SplitShared* sh) {
       if (w < warp) before += v;
       carry += v;
     }
-    first = before + incl - mine;
-    if (passes == 1) total = carry;
-    r.per = max(a.min_units, (total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x));
-    r.u0 = static_cast<int>(min(static_cast<long long>(blockIdx.x) * r.per, static_cast<long long>(total)));
-    r.u1 = min(total, r.u0 + r.per);
+    const int first = before + incl - mine;
     if (b < bt.B) {
       if (scribe) a.starts[b] = first;
       if (mine > 0 && first <= r.u0 && r.u0 < first + mine) {
@@ -145,19 +161,64 @@ __device__ __forceinline__ Run find_run(const Args& a, SplitShared* sh) {
         sh->first = first;
       }
     }
-    __syncthreads();
   }
-  if (scribe && tid == 0) a.starts[bt.B] = r.per;
-  r.seq = sh->seq;
+  if (scribe && tid == 0) {
+    a.starts[bt.B] = r.per;
+    a.starts[bt.B + 1] = r.pad;
+  }
+  __syncthreads();
+  r.seq = r.u0 < r.u1 ? sh->seq : -1;
   r.first = sh->first;
   return r;
 }
 
-// An item's extent: units [us, us + kt), runs c0 .. c1.
+// A place in the order of units.
+template <int RT, int TK>
+struct Cursor {
+  Seq s;
+  Shape sh;
+  int b, g, rt, kt;  // sequence, kv head, row tile, key tile
+
+  __device__ __forceinline__ void set(const Args& a, const Run& r) {
+    bool bad;
+    b = r.seq;
+    s = paged::sequence(a.bt, b, a.page_size, &bad);
+    sh = shape_of<RT, TK>(s, a.G, a.Hkv, r.pad);
+    const int in = r.u0 - r.first, item = in / sh.ku;
+    kt = in - item * sh.ku;
+    g = sh.rt == 1 ? item : item / sh.rt;
+    rt = item - g * sh.rt;
+  }
+  // First tile of the next item; false past the last.
+  __device__ __forceinline__ bool next_item(const Args& a, int pad) {
+    kt = 0;
+    if (++rt < sh.rt) return true;
+    rt = 0;
+    if (++g < a.Hkv) return true;
+    g = 0;
+    do {
+      if (++b >= a.bt.B) return false;
+      bool bad;
+      s = paged::sequence(a.bt, b, a.page_size, &bad);
+      sh = shape_of<RT, TK>(s, a.G, a.Hkv, pad);
+    } while (sh.units == 0);
+    return true;
+  }
+};
+
+// First position that query row ri (token ri / G of the sequence) may not see.
+__device__ __forceinline__ int row_limit(const Args& a, const Seq& s, int ri) {
+  const int p = s.len - s.n + static_cast<int>(paged::quotient(ri, a.g_div));
+  if (p < 0) return 0;
+  const long long e = (static_cast<long long>(paged::quotient(p, a.blk_div)) + 1) * a.blk;
+  return e < s.len ? static_cast<int>(e) : s.len;
+}
+
+// An item's extent: units [us, us + ku), runs c0 .. c1.
 struct Span {
   int us, c0, c1;
 };
-__device__ __forceinline__ Span span_of(int us, int kt, int per) { return Span{us, us / per, (us + kt - 1) / per}; }
+__device__ __forceinline__ Span span_of(int us, int ku, int per) { return Span{us, us / per, (us + ku - 1) / per}; }
 __device__ __forceinline__ long long slot_of(const Span& sp, int c, int per) {
   return 2ll * c + (static_cast<long long>(c) * per > sp.us ? 0 : 1);
 }
@@ -165,32 +226,37 @@ __device__ __forceinline__ long long slot_of(const Span& sp, int c, int per) {
 // Row of the output that row r of row tile rt, kv head g, holds.
 template <int RT>
 __device__ __forceinline__ size_t out_row(const Args& a, const Seq& s, int g, int rt, int r) {
-  const int ri = rt * RT + r, i = ri / a.G;
+  const int ri = rt * RT + r, i = static_cast<int>(paged::quotient(ri, a.g_div));
   return static_cast<size_t>(s.start + i) * a.Hq + g * a.G + (ri - i * a.G);
 }
 
-// Counts this CTA's part of an item; true for the last of `need`.  All threads
-// call after writing the part.
-__device__ __forceinline__ bool arrive_last(const Args& a, const Span& sp, int* flag) {
-  __threadfence();
+// Marks this CTA's part of an item as written; true where every part of the
+// item is.  The mark is stored before the others are read, with a sequentially
+// consistent fence between, so the last CTA to mark sees all marks; CTAs that
+// mark at the same time may all see them, and then write the same result.  No
+// CTA waits.  All threads call, after writing the part.
+__device__ __forceinline__ bool all_arrived(const Args& a, const Span& sp, int per, long long mine) {
+  asm volatile("fence.acq_rel.gpu;" ::: "memory");  // each thread's share of the part, before the mark
   __syncthreads();
   if (threadIdx.x == 0) {
-    unsigned long long* w = a.arrivals + sp.c0;
-    const unsigned need = sp.c1 - sp.c0 + 1;
-    unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(w);
-    bool last;
-    for (;;) {  // an exchange fails only when another part arrived: at most `need` times
-      const unsigned n = ((old ^ a.tag) >> 16) == 0 ? static_cast<unsigned>(old & 0xFFFFu) : 0u;
-      last = n + 1 >= need;
-      const unsigned long long seen = atomicCAS(w, old, last ? 0ull : (a.tag | (n + 1)));
-      if (seen == old) break;
-      old = seen;
-    }
-    *flag = last;
-    __threadfence();
+    asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(a.arrivals + mine), "l"(a.tag) : "memory");
+    asm volatile("fence.sc.gpu;" ::: "memory");
   }
   __syncthreads();
-  return *flag != 0;
+  bool all = true;
+  for (int c = sp.c0 + static_cast<int>(threadIdx.x); c <= sp.c1; c += blockDim.x) {
+    unsigned long long v;
+    asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(a.arrivals + slot_of(sp, c, per)) : "memory");
+    all = all && v == a.tag;
+  }
+  const bool got = __syncthreads_and(all) != 0;
+  if (got) asm volatile("fence.acq_rel.gpu;" ::: "memory");
+  return got;
+}
+// After joining: a replayed graph brings the same number again.
+__device__ __forceinline__ void clear_arrivals(const Args& a, const Span& sp, int per) {
+  for (int c = sp.c0 + static_cast<int>(threadIdx.x); c <= sp.c1; c += blockDim.x)
+    a.arrivals[slot_of(sp, c, per)] = 0;
 }
 
 // Adds the parts of one row and writes it.  D / 4 neighbouring lanes work on a
@@ -204,8 +270,24 @@ __device__ __forceinline__ void join_row(const Args& a, const Seq& s, const Span
   const int j = threadIdx.x % kCols, col = j * 4;
   const uint32_t mask = kCols == 32 ? 0xffffffffu : 0xffffu << (threadIdx.x & 16);
   const int parts = sp.c1 - sp.c0 + 1;
+  auto load_o = [&](int c) {
+    return __ldcg(reinterpret_cast<const float4*>(a.part_o + (slot_of(sp, sp.c0 + c, per) * RT + r) * D + col));
+  };
+  // the first parts' loads go out together with those of the maxima
+  constexpr int kAhead = 8;
+  float4 v[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) v[i] = i < parts ? load_o(i) : make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int kMine = kJoinBatch / kCols;
+  float2 ml[kMine];  // of parts j, j + kCols, ... of the first batch
   float M = -INFINITY;
-  for (int c = j; c < parts; c += kCols) M = fmaxf(M, __ldcg(&a.part_ml[slot_of(sp, sp.c0 + c, per) * RT + r].x));
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) {
+    const int c = j + i * kCols;
+    ml[i] = c < parts ? __ldcg(a.part_ml + slot_of(sp, sp.c0 + c, per) * RT + r) : make_float2(-INFINITY, 0.f);
+    M = fmaxf(M, ml[i].x);
+  }
+  for (int c = j + kJoinBatch; c < parts; c += kCols) M = fmaxf(M, __ldcg(a.part_ml + slot_of(sp, sp.c0 + c, per) * RT + r).x);
 #pragma unroll
   for (int d = kCols / 2; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(mask, M, d));
   const float base = M == -INFINITY ? 0.f : M;
@@ -213,23 +295,29 @@ __device__ __forceinline__ void join_row(const Args& a, const Seq& s, const Span
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int cb = 0; cb < parts; cb += kJoinBatch) {
     const int nb = min(kJoinBatch, parts - cb);
-    for (int c = j; c < nb; c += kCols) {
-      const float2 ml = __ldcg(&a.part_ml[slot_of(sp, sp.c0 + cb + c, per) * RT + r]);
-      const float f = ex2(ml.x - base);
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      const int c = j + i * kCols;
+      if (cb > 0) ml[i] = c < nb ? __ldcg(a.part_ml + slot_of(sp, sp.c0 + cb + c, per) * RT + r) : make_float2(-INFINITY, 0.f);
+      const float f = ex2(ml[i].x - base);
       scratch[2 * c] = f;
-      scratch[2 * c + 1] = f * ml.y;
+      scratch[2 * c + 1] = f * ml[i].y;
     }
     __syncwarp(mask);
-#pragma unroll 8
-    for (int c = 0; c < nb; ++c) {
-      const float4 v =
-          __ldcg(reinterpret_cast<const float4*>(a.part_o + (slot_of(sp, sp.c0 + cb + c, per) * RT + r) * D + col));
-      const float f = scratch[2 * c];
-      L += scratch[2 * c + 1];
-      acc.x = fmaf(f, v.x, acc.x);
-      acc.y = fmaf(f, v.y, acc.y);
-      acc.z = fmaf(f, v.z, acc.z);
-      acc.w = fmaf(f, v.w, acc.w);
+    for (int c0 = 0; c0 < nb; c0 += kAhead) {
+      if (cb + c0 > 0) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) v[i] = c0 + i < nb ? load_o(cb + c0 + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const float f = scratch[2 * (c0 + i)];
+        L += scratch[2 * (c0 + i) + 1];
+        acc.x = fmaf(f, v[i].x, acc.x);
+        acc.y = fmaf(f, v[i].y, acc.y);
+        acc.z = fmaf(f, v[i].z, acc.z);
+        acc.w = fmaf(f, v[i].w, acc.w);
+      }
     }
     __syncwarp(mask);
   }
@@ -264,10 +352,11 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const Args a) 
   bool bad;
   const Seq s = paged::sequence(a.bt, b, a.page_size, &bad);
   if (t < s.start || t >= s.start + s.n) return;
-  const Shape sh = shape_of<RT, TK>(s, a.G, a.Hkv);
+  const int per = a.starts[a.bt.B];
+  const Shape sh = shape_of<RT, TK>(s, a.G, a.Hkv, a.starts[a.bt.B + 1]);
   const int g = h / a.G, ri = (t - s.start) * a.G + (h - g * a.G);
-  const int rt = ri / RT, per = a.starts[a.bt.B];
-  const Span sp = span_of(a.starts[b] + (g * sh.rt + rt) * sh.kt, sh.kt, per);
+  const int rt = ri / RT;
+  const Span sp = span_of(a.starts[b] + (g * sh.rt + rt) * sh.ku, sh.ku, per);
   if (sp.c0 == sp.c1) return;
   join_row<D, RT>(a, s, sp, per, g, rt, ri - rt * RT, scratch[rr]);
 }
