@@ -79,10 +79,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// Four unsigned-biased codes (code + 128 per byte) -> FP16 pairs: byte b under
-// the exponent byte 0x64 is the FP16 value 1024 + b.
-__device__ __forceinline__ uint32_t codes_lo(uint32_t w) { return f16x2_sub(prmt(w, 0x64646464u, 0x4140), 0x64806480u); }
-__device__ __forceinline__ uint32_t codes_hi(uint32_t w) { return f16x2_sub(prmt(w, 0x64646464u, 0x4342), 0x64806480u); }
 // Code `B` of four biased ones as FP32: the byte under the exponent of 2^23 is
 // the value 2^23 + byte.
 template <int B>
@@ -536,19 +532,20 @@ __global__ void __launch_bounds__(WR* WK * 32) paged_attn_kernel(const Args a) {
 // ---- host ----
 
 // Row tile for `rows` query rows per (sequence, kv head) on average.
-inline int row_tile(long long rows) { return rows <= 16 ? 16 : 32; }
-constexpr int kRunsPerSm = 2;  // CTAs resident on an SM
+inline int row_tile(long long rows) { return rows <= 16 ? 16 : (rows <= 32 ? 32 : kBlockRows); }
+// CTAs resident on an SM
+inline int runs_per_sm(int rt) { return rt == kBlockRows ? 1 : 2; }
 // The last arrival joins where an item's parts are few: this many rows x parts of an item
 constexpr int kFusedRows = 512;
 
 inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
-inline int max_runs() { return kRunsPerSm * current_sm_count(); }
+inline int max_runs(int rt) { return runs_per_sm(rt) * current_sm_count(); }
 struct Workspace {
   size_t arrivals, starts, ml, o, bytes;
 };
 inline Workspace workspace_of(int B, int rt, int d) {
   Workspace w;
-  const size_t slots = static_cast<size_t>(2) * max_runs();
+  const size_t slots = static_cast<size_t>(2) * max_runs(rt);
   w.arrivals = 0;
   w.starts = up256(slots * 8);
   w.ml = w.starts + up256((static_cast<size_t>(B) + 2) * 4);
@@ -569,6 +566,35 @@ inline unsigned long long next_tag() {
   return v ? v : next_tag();
 }
 
+// The launch's grid and workspace for row tiles of `rt` and key tiles of `tk`;
+// false where the units pass 32 bits.
+inline bool plan(Args& a, int rt, int tk, int d, uint8_t* ws, int* runs, bool* shared) {
+  const Workspace w = workspace_of(a.bt.B, rt, d);
+  a.arrivals = reinterpret_cast<unsigned long long*>(ws + w.arrivals);
+  a.starts = reinterpret_cast<int*>(ws + w.starts);
+  a.part_ml = reinterpret_cast<float2*>(ws + w.ml);
+  a.part_o = reinterpret_cast<float*>(ws + w.o);
+  a.min_units = kMinUnits;
+  // most units that the batch can have: every row tile over a full block table
+  const long long kt = (static_cast<long long>(a.bt.max_pages) * a.page_size + tk - 1) / tk;
+  const long long items = (static_cast<long long>(a.bt.T) * a.G / rt + a.bt.B) * a.Hkv, units = items * kt;
+  const int most = max_runs(rt);
+  if (units > 0x7fffffffll - most) return false;
+  *runs = static_cast<int>(std::min<long long>(most, (units + kMinUnits - 1) / kMinUnits));
+  *shared = kt > 1;  // items of one tile are never shared
+  const long long rows = std::min<long long>(rt, static_cast<long long>(a.bt.T) * a.G);
+  a.fused = rt != kBlockRows && rows * ((*runs + items - 1) / items) <= kFusedRows;
+  a.tag = next_tag();
+  return true;
+}
+
+template <int D, int RT, int TK>
+int launch_join(const Args& a, cudaStream_t st) {
+  constexpr int kRows = kJoinThreads / (D / 4);
+  const dim3 grid(static_cast<unsigned>((a.bt.T * a.Hq + kRows - 1) / kRows));
+  return launch_pdl(paged_join_kernel<D, RT, TK>, grid, dim3(kJoinThreads), 0, st, a) == cudaSuccess ? MNW_OK : MNW_E_CUDA;
+}
+
 template <int D, bool INT8, int WR, int WK>
 int launch(Args& a, uint8_t* ws, cudaStream_t st) {
   using C = Cfg<D, INT8, WR, WK>;
@@ -580,36 +606,22 @@ int launch(Args& a, uint8_t* ws, cudaStream_t st) {
       return MNW_E_CUDA;
     attrs_done(attr, bit);
   }
-  constexpr int kTK = C::kTK;
-  const Workspace w = workspace_of(a.bt.B, C::kRT, D);
-  a.arrivals = reinterpret_cast<unsigned long long*>(ws + w.arrivals);
-  a.starts = reinterpret_cast<int*>(ws + w.starts);
-  a.part_ml = reinterpret_cast<float2*>(ws + w.ml);
-  a.part_o = reinterpret_cast<float*>(ws + w.o);
-  a.min_units = kMinUnits;
-  // most units that the batch can have: every row tile over a full block table
-  const long long kt = (static_cast<long long>(a.bt.max_pages) * a.page_size + kTK - 1) / kTK;
-  const long long tiles = (static_cast<long long>(a.bt.T) * a.G) / C::kRT + a.bt.B;
-  const long long items = tiles * a.Hkv, units = items * kt;
-  if (units > 0x7fffffffll - max_runs()) return MNW_E_UNSUPPORTED;
-  const int runs = static_cast<int>(std::min<long long>(max_runs(), (units + kMinUnits - 1) / kMinUnits));
-  const long long rows = static_cast<long long>(a.bt.T) * a.Hq;
-  const long long item_rows = std::min<long long>(C::kRT, static_cast<long long>(a.bt.T) * a.G);
-  a.fused = item_rows * ((runs + items - 1) / items) <= kFusedRows;
-  a.tag = next_tag();
+  int runs;
+  bool shared;
+  if (!plan(a, C::kRT, C::kTK, D, ws, &runs, &shared)) return MNW_E_UNSUPPORTED;
   if (launch_pdl(kern, dim3(runs), dim3(C::kThreads), C::kSmem, st, a) != cudaSuccess) return MNW_E_CUDA;
-  if (a.fused || kt <= 1) return MNW_OK;  // items of one tile are never shared
-  constexpr int kJoinRows = kJoinThreads / (D / 4);
-  return launch_pdl(paged_join_kernel<D, C::kRT, kTK>, dim3(static_cast<unsigned>((rows + kJoinRows - 1) / kJoinRows)),
-                    dim3(kJoinThreads), 0, st, a) == cudaSuccess
-             ? MNW_OK
-             : MNW_E_CUDA;
+  return a.fused || !shared ? MNW_OK : launch_join<D, C::kRT, C::kTK>(a, st);
 }
 
 template <int D, bool INT8>
 int launch_rows(Args& a, uint8_t* ws, int rt, cudaStream_t st) {
   if (rt == 16) return launch<D, INT8, 1, 4>(a, ws, st);
-  return launch<D, INT8, 2, 2>(a, ws, st);
+  if (rt == 32) return launch<D, INT8, 2, 2>(a, ws, st);
+  int runs;
+  bool shared;
+  if (!plan(a, kBlockRows, kBlockKeys, D, ws, &runs, &shared)) return MNW_E_UNSUPPORTED;
+  const int rc = launch_block(a, D, INT8, runs, st);
+  return rc != MNW_OK || !shared ? rc : launch_join<D, kBlockRows, kBlockKeys>(a, st);
 }
 
 }  // namespace pattn

@@ -18,6 +18,8 @@
 #pragma once
 #include <cuda_bf16.h>
 
+#include <atomic>
+
 #include "mnw_convert.cuh"
 #include "mnw_internal.h"
 #include "mnw_paged.cuh"
@@ -31,6 +33,7 @@ using paged::FastDiv;
 using paged::Seq;
 
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kBlockRows = 128, kBlockKeys = 128;  // the block kernel's tiles (mnw_attn_paged_block.cu)
 
 struct Args {
   Batch bt;
@@ -62,6 +65,10 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// Four unsigned-biased codes (code + 128 per byte) -> FP16 pairs: byte b under
+// the exponent byte 0x64 is the FP16 value 1024 + b.
+__device__ __forceinline__ uint32_t codes_lo(uint32_t w) { return f16x2_sub(prmt(w, 0x64646464u, 0x4140), 0x64806480u); }
+__device__ __forceinline__ uint32_t codes_hi(uint32_t w) { return f16x2_sub(prmt(w, 0x64646464u, 0x4342), 0x64806480u); }
 // Units of a sequence (the host bounds their sum below 2^31).  An item counts
 // as a multiple of `pad` units, so that with runs of `pad` none begins inside
 // one item and goes on in the next.
@@ -327,6 +334,9 @@ __device__ __forceinline__ void join_row(const Args& a, const Seq& s, const Span
       make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
   if (a.lse && j == 0) a.lse[row] = (M + log2f(L)) * kLn2;
 }
+
+// The block kernel over `runs` runs (mnw_attn_paged_block.cu).
+int launch_block(const Args& a, int d, bool int8, int runs, cudaStream_t st);
 
 // The joining kernel: D / 4 lanes per (token, query head) row; rows of items
 // that one run covered are done already.

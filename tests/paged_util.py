@@ -86,13 +86,15 @@ def starts_of(counts):
 
 
 def attend_plain(q, counts, cache, blk, scale):
-    """(out, lse, sum of w |v|, largest sum of |scale q k|) in float64: [T, Hq, d], [T, Hq], [T, Hq, d], [T, Hq]."""
+    """(out, lse, sum of w |v|, largest sum of |scale q k|, largest w_j |v_j| times the keys) in float64: [T, Hq, d],
+    [T, Hq], [T, Hq, d], [T, Hq], [T, Hq]."""
     T, Hq, d = q.shape
     q = q.double()
     out = torch.zeros((T, Hq, d), dtype=torch.float64)
     mag = torch.zeros_like(out)
     lse = torch.full((T, Hq), -math.inf, dtype=torch.float64)
     top = torch.zeros((T, Hq), dtype=torch.float64)
+    peak = torch.zeros((T, Hq), dtype=torch.float64)
     G = Hq // cache.Hkv
     t = 0
     for b, n in enumerate(counts):
@@ -108,20 +110,22 @@ def attend_plain(q, counts, cache, blk, scale):
                     w = torch.exp(s - lse[t, h])
                     out[t, h] = w @ v[:end, h // G]
                     mag[t, h] = w @ v[:end, h // G].abs()
+                    peak[t, h] = (w * v[:end, h // G].abs().amax(1)).max() * end
                     top[t, h] = (scale * (k[:end, h // G].abs() @ q[t, h].abs())).max()
             t += 1
-    return out, lse, mag, top
+    return out, lse, mag, top, peak
 
 
-def check_attention(out, lse, q, counts, cache, blk, scale):
+def check_attention(out, lse, q, counts, cache, blk, scale, lost=0.0):
     """Each rounding counted once: the output's (2^-8 of the value), the probabilities' (2^-8 of each product in BF16,
-    2^-11 in FP16), and the scores' FP32 sums of d products (d 2^-24 of their magnitudes, twice: numerator and sum)."""
-    ref, ref_lse, mag, top = attend_plain(q.cpu(), counts, cache, blk, scale)
+    2^-11 in FP16), and the scores' FP32 sums of d products (d 2^-24 of their magnitudes, twice: numerator and sum).
+    lost: share of the row's largest product below which a product may be lost."""
+    ref, ref_lse, mag, top, peak = attend_plain(q.cpu(), counts, cache, blk, scale)
     got, got_lse = out.double().cpu(), lse.double().cpu()
     assert torch.isfinite(got).all()
     p_round = 2.0 ** -8 if cache.fmt == "bf16" else 2.0 ** -11
     score = 2.0 * cache.d * 2.0 ** -24 * top + 2.0 ** -18
-    tol = 2.0 ** -8 * ref.abs() + (p_round + score[..., None]) * (1 + 2.0 ** -8) * mag + 1e-30
+    tol = 2.0 ** -8 * ref.abs() + (p_round + score[..., None]) * (1 + 2.0 ** -8) * mag + lost * peak[..., None] + 1e-30
     bad = ((got - ref).abs() > tol).nonzero()
     assert bad.numel() == 0, (bad[:4].tolist(), float((got - ref).abs().max()))
     empty = torch.isinf(ref_lse)

@@ -307,6 +307,52 @@ def test_attn_paged_extreme_scores_and_scales(fmt):
         U.check_attention(out, lse, q, [1, 1], cache, 1, 0.2)
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "int8"])
+def test_attn_paged_blocks_long_split(fmt):
+    """32-token blocks of one long and one short sequence: runs end inside items, several parts a row."""
+    cache = U.Cache([9001, 77], 64, 2, 128, fmt, seed=18)
+    q, out, lse, scale = _attend(cache, [32, 32], 8, 32, False)
+    U.check_attention(out, lse, q, [32, 32], cache, 32, scale)
+    # many small items in one run: segments of a single tile
+    lens = [33 + (41 * i) % 200 for i in range(90)]
+    cache = U.Cache(lens, 16, 4, 64, fmt, seed=19)
+    q, out, lse, scale = _attend(cache, [9] * 90, 16, 4, False)
+    U.check_attention(out, lse, q, [9] * 90, cache, 4, scale)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "int8"])
+def test_attn_paged_blocks_extreme_scores_and_scales(fmt):
+    """As for single tokens, with 40 query rows: keys growing along the cache, value scales over 40 powers of two, tiles
+    of zero values after others.  The FP16 products of INT8 caches lose what is below 2^-38 of the row's largest."""
+    m = M()
+    cache = U.Cache([600, 290], 16, 1, 128, fmt, seed=22)
+    grow = torch.linspace(0.01, 30.0, 600).double()
+    for b, L in enumerate(cache.lens):
+        pos = torch.arange(L)
+        pg, sl = cache.table_host[b, pos // 16].long().cuda(), (pos % 16).cuda()
+        k, v = cache.rows[b]
+        if fmt == "bf16":
+            kk = (k * grow[:L, None, None]).bfloat16()
+            kk[L // 2] = 0
+            cache.k[pg, :, sl] = kk.cuda()
+            cache.rows[b] = (kk.double(), v)
+        else:
+            f = grow[:L].float()
+            f[L // 2] = 0
+            ks = cache.ks[pg, :, sl].cpu() * f[:, None]
+            vs = cache.vs[pg, :, sl].cpu() * torch.exp2((torch.arange(L) % 40 - 30).float())[:, None]
+            if b == 1:
+                vs[128:256] = 0
+            cache.ks[pg, :, sl], cache.vs[pg, :, sl] = ks.cuda(), vs.cuda()
+            kc, vc = cache.k[pg, :, sl].cpu().double(), cache.v[pg, :, sl].cpu().double()
+            cache.rows[b] = (kc * ks.double()[..., None], vc * vs.double()[..., None])
+    for size in (1e-3, 1.0, 8.0):
+        q = _randn((20, 4, 128), 3, size)
+        q[0, 1] = 0
+        out, lse = m.mnw_attn_paged(q, cache.k, cache.v, cache.table, cache.cache_lens, 1, 0.2, want_lse=True, **cache.kw())
+        U.check_attention(out, lse, q, [10, 10], cache, 1, 0.2, lost=2.0 ** -38 if fmt == "int8" else 0.0)
+
+
 def test_attn_paged_offsets_past_32_bits():
     m = M()
     page, Hkv, d = 64, 8, 128
