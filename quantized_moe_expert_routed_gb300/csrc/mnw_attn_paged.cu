@@ -516,9 +516,7 @@ __global__ void __launch_bounds__(WR* WK * 32) paged_attn_kernel(const Args a) {
       if (!whole && a.fused) {
         const Span sp = span_of(item_first, cc.sh.ku, run.per);
         if (all_arrived(a, sp, run.per, pslot)) {
-          float* scratch = reinterpret_cast<float*>(stage) + tid / (D / 4) * 2 * kJoinBatch;
-          for (int r = tid / (D / 4); r < rows; r += kThreads / (D / 4))
-            join_row<D, kRT>(a, cc.s, sp, run.per, cc.g, cc.rt, r, scratch);
+          join_item<D, kRT, kThreads>(a, cc.s, sp, run.per, cc.g, cc.rt, rows, reinterpret_cast<float*>(stage));
           clear_arrivals(a, sp, run.per);
         }
       }

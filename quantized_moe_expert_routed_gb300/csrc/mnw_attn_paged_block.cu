@@ -8,23 +8,29 @@
 // tensor instructions cannot feed (2046 of tcgen05's ~3800 multiply-adds a
 // clock, and every 16 rows would read the tile from shared memory again).
 //
-// Roles (512 threads):
-//   warps 0-3   loaders.  A tile that lies whole inside the length, of pages
-//               that divide it (or that it divides), comes by TMA, a lane per
-//               page, straight into operand tiles of the 128-byte-swizzle
-//               layout.  Other tiles (the last of a sequence, whose rows past
-//               the length must read as zeros; odd page sizes) come by 16-byte
-//               cp.async, each warp 32 keys, fenced to the tensor cores' proxy.
-//               INT8: codes land in a raw ring (bulk copies) and the four
-//               warps rewrite them as FP16 operand tiles (exact).  They also
-//               bring the query tile of each segment (a run's part of an item)
-//               and describe the segment to the other roles.
-//   warp 4      issues the MMAs (one thread): S_t = Q K_t^T, O_g += P_t V_t
+// Roles (416 threads):
+//   warps 0-1   key loaders, warps 2-3 value loaders.  A tile that lies whole
+//               inside the length, of pages that divide it (or that it
+//               divides), comes by TMA, a lane per page, straight into operand
+//               tiles of the 128-byte-swizzle layout.  Other tiles (the last of
+//               a sequence, whose rows past the length must read as zeros; odd
+//               page sizes) come by 16-byte cp.async, 64 keys a warp, fenced to
+//               the tensor cores' proxy.  INT8: codes land in a raw buffer
+//               (bulk copies), are taken into registers, and leave them as FP16
+//               operand tiles (exact) while the next codes land.  All four
+//               bring the query tile of each segment (a run's part of an
+//               item); the first describes the segment to the other roles.
+//   warp 12     issues the MMAs (its first lane): S_t = Q K_t^T, O_g += P_t V_t
 //               with P_t from tensor memory and V as it lies in the cache,
 //               [key][d], an operand whose N dimension is contiguous.
-//   warps 8-15  softmax, two groups of 4 warps: group t % 2 takes tile t, one
-//               row per thread, with its own O accumulator, maximum and sum,
-//               so that one group computes while the other's products run.
+//   warps 4-11  softmax, two groups of 4 warps: group t % 2 takes tile t, with
+//               its own O accumulator, maxima and sums, so that one group
+//               computes while the other's products run.  A warp takes its 32
+//               rows 16 at a time and 64 keys at a time, a thread 16 keys of two
+//               rows (so a key's scales serve two rows); scores are read from
+//               tensor memory once for the maximum and once for P.  More at
+//               once would spill, and with the shared memory this kernel takes
+//               there is next to no L1 for spills to hit.
 // Order of the products: S_0, S_1, then O += P_t V_t, S_{t+2}; a tile's
 // scores being complete therefore means that its group's earlier product into
 // O is complete too (one issuing thread, in order).
@@ -47,12 +53,13 @@ namespace pattn {
 namespace {
 
 constexpr int kRT = kBlockRows, kTK = kBlockKeys;
-constexpr int kThreads = 512;
-constexpr int kLoadWarps = 4, kWarpMma = 4, kWarpSm0 = 8;
+constexpr int kThreads = 416;
+constexpr int kLoadWarps = 4, kWarpSm0 = 4, kWarpMma = 12;
 constexpr int kTmemCols = 512;
 constexpr uint32_t kColO = 256;  // O_g at kColO + 128 g; S_g at 128 g
-constexpr int kMaxScaleSlots = 8, kMaxRawSlots = 3;
 constexpr int kMaxSegs = 8;      // segment descriptions held; at most four segments are under way
+constexpr int kMaxSlots = 4;
+constexpr int kMaxKScales = 8, kMaxVScales = 6;
 constexpr float kRescaleLog2 = 8.f;
 
 template <int D, bool INT8>
@@ -60,19 +67,19 @@ struct BCfg {
   static constexpr int kHalves = D / 64;                   // 64 elements = 128 bytes per operand row piece
   static constexpr uint32_t kPiece = kTK * 128;            // 128 rows of 128 bytes
   static constexpr uint32_t kTile = kHalves * kPiece;      // operand tile
-  static constexpr int kSlots = D == 64 ? 8 : (INT8 ? 4 : 5);
-  static constexpr int kAhead = 2;                         // items in flight behind the one being issued
-  static constexpr int kRawSlots = kAhead + 1;
-  // the scales of tile t + kScaleSlots are copied once P V of tile t was issued: the copy of keys t + n (item 2 (t + n) - 1)
-  // follows the release of the operand slot kAhead + 1 + kSlots items before it, and values of tile j are item 2 j + 2
-  static constexpr int kScaleSlots = kSlots == 8 ? 8 : 5;
-  static_assert(!INT8 || 2 * kScaleSlots - 1 - (kAhead + 1) - kSlots >= 2);
+  static constexpr int kSlotsK = D == 64 ? 4 : (INT8 ? 2 : 3), kSlotsV = D == 64 ? 4 : 2;
   static constexpr uint32_t kRaw = INT8 ? kTK * D : 0;     // raw codes of a tile
-  static constexpr uint32_t kScaleSlot = 3 * kTK * 4;      // scales of a tile's keys, of its values, log2 of the latter
-  static constexpr uint32_t kOffRing = kTile;              // Q first
-  static constexpr uint32_t kOffRaw = kOffRing + kSlots * kTile;
-  static constexpr uint32_t kOffScale = kOffRaw + kRawSlots * kRaw;
-  static constexpr uint32_t kOffBars = kOffScale + (INT8 ? kScaleSlots * kScaleSlot : 0);
+  // Scales are copied with a tile's codes, which are issued once the tile two before went into its operand slot, that
+  // is, once the product with the tile that held the slot before is complete; the softmax of a tile reads them last
+  // before P V of the tile is issued (and S of the tile two after follows that).
+  static constexpr int kScalesK = 4 + kSlotsK, kScalesV = 2 + kSlotsV;
+  static_assert(kScalesK <= kMaxKScales && kScalesV <= kMaxVScales && kSlotsK <= kMaxSlots && kSlotsV <= kMaxSlots);
+  static constexpr uint32_t kOffK = kTile;                 // Q first
+  static constexpr uint32_t kOffV = kOffK + kSlotsK * kTile;
+  static constexpr uint32_t kOffRaw = kOffV + kSlotsV * kTile;            // keys' codes, values' codes
+  static constexpr uint32_t kOffKS = kOffRaw + 2 * kRaw;                  // [kScalesK][kTK] scales of keys
+  static constexpr uint32_t kOffVS = kOffKS + (INT8 ? kScalesK * kTK * 4 : 0);  // [kScalesV][2][kTK] of values, and their log2
+  static constexpr uint32_t kOffBars = kOffVS + (INT8 ? kScalesV * 2 * kTK * 4 : 0);
 };
 
 // A run's part of one item.
@@ -84,12 +91,12 @@ struct Seg {
 };
 
 struct Bars {
-  uint64_t full[8], empty[8];           // operand ring
+  uint64_t full[2][kMaxSlots], empty[2][kMaxSlots];  // operand rings: keys, values
+  uint64_t raw_full[2], raw_empty[2];
   uint64_t q_full, q_empty;
   uint64_t s_full[2], p_full[2];        // per softmax group
   uint64_t o_full, epi;                 // a segment's output complete; read
-  uint64_t sc_full[kMaxScaleSlots];
-  uint64_t raw_full[kMaxRawSlots], raw_empty[kMaxRawSlots];
+  uint64_t ks_full[kMaxKScales], vs_full[kMaxVScales];
   uint64_t seg_full[kMaxSegs];
   uint64_t fin[4];                      // per lane quarter: both groups' maxima and sums written
   uint64_t drain;
@@ -124,10 +131,24 @@ template <int N>
 __device__ __forceinline__ void wait_copies() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-// The wait's slow side is a call: inlined at every wait of the roles it would
-// be a good part of the kernel's code, whose size shows (instruction fetches).
+// Waits poll without a suspend time: the library's bounded_wait() lets a
+// waiting thread sleep, and with a dozen hand-overs a tile the late wake-ups
+// were most of the kernel's time.  Bounded like it: gives up when *abort is
+// set, or after kWaitLimitNs, which sets it and reports.  The slow side is a call;
+// inlined at every wait it would be a good part of the kernel's code.
 __device__ __noinline__ bool slow_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* err) {
-  return bounded_wait(bar, parity, abort, err);
+  const uint64_t t0 = globaltimer();
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 255u) == 0) {
+      if (*abort) return false;
+      if (globaltimer() - t0 > kWaitLimitNs) {
+        *abort = 1;
+        if (err) atomicOr(err, MNW_DEVERR_TIMEOUT);
+        return false;
+      }
+    }
+  }
 }
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* err) {
   return mbar_try_wait(bar, parity) || slow_wait(bar, parity, abort, err);
@@ -159,6 +180,43 @@ __device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr, uint32_t piec
 }
 constexpr uint32_t kBMajorN = 1u << 16;  // instruction descriptor: B's N dimension contiguous
 
+// Both of two barriers, polled by different lanes.
+__device__ __forceinline__ bool warp_wait2(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, volatile int* abort, uint32_t* err) {
+  int ok = 1;
+  const int lane = threadIdx.x & 31;
+  if (lane < 2) ok = wait_for(lane ? b : a, lane ? pb : pa, abort, err) ? 1 : 0;
+  return __all_sync(0xffffffffu, ok) != 0;
+}
+// Tensor memory, 16 lanes from the address's: thread (g, t) = (lane / 4, lane % 4) gets of every 8 columns 2t and 2t + 1
+// of row g, then of row g + 8 (registers 4j .. 4j + 3 of columns 8j ..).
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+// As above with one register per row and 4 columns: column t of row g, of row g + 8 (registers 2j, 2j + 1 of columns 4j ..).
+__device__ __forceinline__ void tmem_st_pairs(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 __device__ __forceinline__ float lo32(uint64_t x) { return __uint_as_float(static_cast<uint32_t>(x)); }
 __device__ __forceinline__ float hi32(uint64_t x) { return __uint_as_float(static_cast<uint32_t>(x >> 32)); }
 __device__ __forceinline__ uint32_t half2_bits(float a, float b) {
@@ -172,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                        const int whole_pages) {
   using C = BCfg<D, INT8>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);  // (an offset: the pointer stays a shared-memory one)
   Bars* bars = reinterpret_cast<Bars*>(smem + C::kOffBars);
   volatile int* abort = &bars->abort;
   __shared__ SplitShared split;
@@ -181,24 +239,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   pdl_launch_dependents();
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::kSlots; ++i) {
-      mbar_init(&bars->full[i], kLoadWarps);
-      mbar_init(&bars->empty[i], 1);
+    for (int x = 0; x < 2; ++x) {
+      for (int i = 0; i < kMaxSlots; ++i) {
+        mbar_init(&bars->full[x][i], 2);
+        mbar_init(&bars->empty[x][i], 1);
+      }
+      mbar_init(&bars->raw_full[x], 1);
+      mbar_init(&bars->raw_empty[x], 2);
+      mbar_init(&bars->s_full[x], 1);
+      mbar_init(&bars->p_full[x], 4);
+      bars->has_part[x] = 0;
     }
     mbar_init(&bars->q_full, kLoadWarps);
     mbar_init(&bars->q_empty, 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars->s_full[i], 1);
-      mbar_init(&bars->p_full[i], 4);
-      bars->has_part[i] = 0;
-    }
     mbar_init(&bars->o_full, 1);
     mbar_init(&bars->epi, 8);
-    for (int i = 0; i < kMaxScaleSlots; ++i) mbar_init(&bars->sc_full[i], kLoadWarps);
-    for (int i = 0; i < kMaxRawSlots; ++i) {
-      mbar_init(&bars->raw_full[i], 1);
-      mbar_init(&bars->raw_empty[i], kLoadWarps);
-    }
+    for (int i = 0; i < kMaxKScales; ++i) mbar_init(&bars->ks_full[i], 2);
+    for (int i = 0; i < kMaxVScales; ++i) mbar_init(&bars->vs_full[i], 2);
     for (int i = 0; i < kMaxSegs; ++i) mbar_init(&bars->seg_full[i], 1);
     for (int i = 0; i < 4; ++i) mbar_init(&bars->fin[i], 2);
     mbar_init(&bars->drain, 1);
@@ -224,314 +281,360 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < kLoadWarps) {
     // ======================= loaders =======================
-    // One loop with one place for each step: the code of the roles together
-    // should stay near the instruction cache's size.
-    bool ok = true;
-    const int key = warp * 32 + lane;  // this lane's key of a tile copied row by row
-    // whole pages: page `lane` of a tile, `span` keys each
-    const int span = min(a.page_size, kTK), pieces = kTK / span;
-    struct Tile {
-      int b, g, kt, len;
-      int page;    // of this lane's piece
-      bool whole;  // by whole pages
-    } now{}, prev{}, next{};
-    int seg = -1, t_now = -1;
-    int us = run.u0 - kc.kt;  // first unit of kc's item
-    const uint32_t all = 2u * tiles;
-    uint32_t n_items = 0, sent = 0;  // items issued; given to the tensor cores
-    uint32_t by_rows = 0;            // bit i: item n_items - 1 - i was copied row by row
-    uint32_t raw_phase = 0;          // bit s: parity of raw slot s's next bulk landing
+    const bool values = warp >= 2;   // (uniform in the warp)
+    const int lw = warp & 1;         // which 64 keys of a tile
+    const int ring_slots = values ? C::kSlotsV : C::kSlotsK;
+    const uint32_t ring_at = values ? C::kOffV : C::kOffK;
+    uint64_t* const full = bars->full[values ? 1 : 0];
+    uint64_t* const empty = bars->empty[values ? 1 : 0];
+    const uint8_t* const base = values ? a.vc : a.kc;
     constexpr int kCh = (INT8 ? D : 2 * D) / 16;  // chunks of a cached row
     constexpr int kRows = 32 / kCh;               // rows per pass of the warp
+    // whole pages: page `lane` of a tile, `span` keys each
+    const int span = min(a.page_size, kTK), pieces = kTK / span;
+    bool ok = tiles > 0;
+    int seg = -1, us = run.u0 - kc.kt;  // segment of the keys; first unit of kc's item
+    RingPos ring;
     auto table_at = [&](int seq, int p) {
       return __ldg(a.bt.block_table + static_cast<size_t>(seq) * a.bt.max_pages + paged::quotient(p, a.page_div));
     };
-    // the tile at kc, its page looked up early
-    auto peek = [&](Tile& x) {
-      x.b = kc.b;
-      x.g = kc.g;
-      x.kt = kc.kt;
-      x.len = kc.s.len;
-      x.whole = whole_pages && (kc.kt + 1) * kTK <= kc.s.len;
-      x.page = x.whole && lane < pieces ? table_at(kc.b, kc.kt * kTK + lane * span) : 0;
+    // What is issued: the tile at kc; its pieces' pages are looked up a tile early.
+    bool whole;
+    int page;
+    auto peek = [&]() {
+      whole = whole_pages && (kc.kt + 1) * kTK <= kc.s.len;
+      page = whole && lane < pieces ? table_at(kc.b, kc.kt * kTK + lane * span) : 0;
     };
-    if (tiles > 0) peek(next);
-    while (ok) {
-      // item i: keys of tile 0, then keys of tile (i + 1) / 2 where i is odd, values of tile i / 2 - 1 where it is even;
-      // the values of the last tile end the order
-      const bool issue = n_items < all;
-      const bool values = n_items > 0 && ((n_items & 1) == 0 || n_items + 1 == all);
-      const bool seg_begin = issue && !values && (n_items == 0 || next.kt == 0);
-      // what is in flight lands and is given on: all of it before a segment's queries, which wait for its products
-      const uint32_t keep = !issue || seg_begin ? 0u : static_cast<uint32_t>(C::kAhead);
-      while (ok && n_items - sent > keep) {
-        const bool rows = (by_rows >> (n_items - 1 - sent)) & 1;
-        if (rows) {
-          if (keep == 0)
-            wait_copies<0>();
-          else
-            wait_copies<C::kAhead>();
-          __syncwarp();
-        }
-        const uint32_t it = sent++, slot = it % C::kSlots;
-        if constexpr (INT8) {
-          const uint32_t rs = it % C::kRawSlots;
-          if (!rows) {
-            if (!warp_wait(&bars->raw_full[rs], (raw_phase >> rs) & 1, abort, a.err)) { ok = false; break; }
-            raw_phase ^= 1u << rs;
-          }
-          if (!warp_wait(&bars->empty[slot], ((it / C::kSlots) & 1) ^ 1, abort, a.err)) { ok = false; break; }
-          const uint8_t* raw = smem + C::kOffRaw + rs * C::kRaw;
-          uint8_t* op = smem + C::kOffRing + slot * C::kTile;
-          uint4 w[kCh];
-#pragma unroll
-          for (int i = 0; i < kCh; ++i) w[i] = *reinterpret_cast<const uint4*>(raw + warp * 32 * D + (i * 32 + lane) * 16);
-#pragma unroll
-          for (int i = 0; i < kCh; ++i) {
-            const int row = warp * 32 + i * kRows + lane / kCh, c = lane % kCh;
-            const uint32_t ww[4] = {w[i].x ^ 0x80808080u, w[i].y ^ 0x80808080u, w[i].z ^ 0x80808080u, w[i].w ^ 0x80808080u};
-            const uint4 h0 = make_uint4(codes_lo(ww[0]), codes_hi(ww[0]), codes_lo(ww[1]), codes_hi(ww[1]));
-            const uint4 h1 = make_uint4(codes_lo(ww[2]), codes_hi(ww[2]), codes_lo(ww[3]), codes_hi(ww[3]));
-            uint8_t* piece = op + (c >> 2) * C::kPiece + row * 128;
-            const int o = (2 * c) & 7, first = (c >> 2) & 1;  // the two pieces' lanes start on different banks
-            *reinterpret_cast<uint4*>(piece + (((o + first) ^ (row & 7)) << 4)) = first ? h1 : h0;
-            *reinterpret_cast<uint4*>(piece + (((o + (first ^ 1)) ^ (row & 7)) << 4)) = first ? h0 : h1;
-          }
-          const bool keys = it == 0 || ((it & 1) && it + 1 < all);  // these came with their tile's scales
-          const uint32_t ss = (it + 1) / 2 % C::kScaleSlots;
-          if (keys) {
-            float* sc = reinterpret_cast<float*>(smem + C::kOffScale + ss * C::kScaleSlot);
-            sc[2 * kTK + key] = __log2f(sc[kTK + key]);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&bars->full[slot]);
-            mbar_arrive(&bars->raw_empty[rs]);
-            if (keys) mbar_arrive(&bars->sc_full[ss]);
-          }
-        } else if (rows) {
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars->full[slot]);
-        }
-      }
-      if (!ok || !issue) break;
-
-      if (seg_begin) {
-        // ---- the segment's description and its queries, one row per lane ----
-        ++seg;
-        if (threadIdx.x == 0) {
-          Seg d;
-          d.tiles = min(kc.sh.kt - kc.kt, tiles - (t_now + 1));
-          d.kt0 = kc.kt;
-          d.g = kc.g;
-          d.rt = kc.rt;
-          d.whole = kc.kt == 0 && d.tiles == kc.sh.kt;
-          d.us = us;
-          d.ku = kc.sh.ku;
-          d.s = kc.s;
-          bars->seg[seg % kMaxSegs] = d;
-          mbar_arrive(&bars->seg_full[seg % kMaxSegs]);
-        }
-        if (seg > 0 && !warp_wait(&bars->q_empty, (seg - 1) & 1, abort, a.err)) { ok = false; break; }
-        const int rows = min(kRT, kc.s.n * a.G - kc.rt * kRT);
-        const int r = key;
-        const bool live = r < rows;
-        const int ri = kc.rt * kRT + (live ? r : 0);
-        const int i = static_cast<int>(paged::quotient(ri, a.g_div)), hh = ri - i * a.G;
-        const uint4* src = reinterpret_cast<const uint4*>(a.q + static_cast<long long>(kc.s.start + i) * a.q_stride +
-                                                          static_cast<long long>(kc.g * a.G + hh) * D);
-        float f = 1.f;
-        if constexpr (INT8) {
-          uint32_t mag = 0;
-#pragma unroll 8
-          for (int c = 0; c < D / 8; ++c) {
-            const uint4 w = live ? src[c] : make_uint4(0, 0, 0, 0);
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int x = 0; x < 4; ++x) mag = max(mag, max(u[x] & 0x7FFFu, (u[x] >> 16) & 0x7FFFu));
-          }
-          // 2^e with the row's largest magnitude in [2^14, 2^15) after x * 2^-e
-          const int e = mag == 0 ? 0 : max(-110, min(113, static_cast<int>(mag >> 7) - 127 - 14));
-          f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-          bars->qfac[seg & 3][r] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-        }
-#pragma unroll 8
-        for (int c = 0; c < D / 8; ++c) {
-          uint4 w = live ? src[c] : make_uint4(0, 0, 0, 0);
-          if constexpr (INT8) {
-            auto half = [&](uint32_t u) { return half2_bits(__uint_as_float(u << 16) * f, __uint_as_float(u & 0xFFFF0000u) * f); };
-            w = make_uint4(half(w.x), half(w.y), half(w.z), half(w.w));
-          }
-          *reinterpret_cast<uint4*>(smem + (c >> 3) * C::kPiece + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = w;
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->q_full);
-      }
-      if (!values) {
-        prev = now;
-        now = next;
-        ++t_now;
-        if (++kc.kt == kc.sh.kt) {
-          us += kc.sh.ku;
-          kc.next_item(a, run.pad);
-        }
-        if (t_now + 1 < tiles) peek(next);
-      }
-
-      // ---- issue item n_items ----
-      const bool back = values && n_items + 1 != all;  // values of the tile before
-      const Tile x{back ? prev.b : now.b,     back ? prev.g : now.g,       back ? prev.kt : now.kt,
-                   back ? prev.len : now.len, back ? prev.page : now.page, back ? prev.whole : now.whole};
-      const uint32_t it = n_items++;
-      const uint32_t slot = it % C::kSlots, rs = it % C::kRawSlots;
-      const bool rows = !x.whole || __any_sync(0xffffffffu, static_cast<unsigned>(x.page) >= static_cast<unsigned>(a.n_pages));
-      by_rows = by_rows << 1 | (rows ? 1u : 0u);
-      if constexpr (!INT8) {
-        if (!warp_wait(&bars->empty[slot], ((it / C::kSlots) & 1) ^ 1, abort, a.err)) { ok = false; break; }
-      } else if (warp == 0) {  // all four warps have read the raw slot's last codes
-        if (!warp_wait(&bars->raw_empty[rs], ((it / C::kRawSlots) & 1) ^ 1, abort, a.err)) { ok = false; break; }
-      }
-      const uint8_t* base = values ? a.vc : a.kc;
-      const uint32_t scale_at = C::kOffScale + (t_now % C::kScaleSlots) * C::kScaleSlot;
-      if (rows) {
-        const int p = x.kt * kTK + key;
-        int page = -1, at = 0;
-        if (p < x.len) {
-          page = table_at(x.b, p);
-          at = x.g * a.page_size + (p - static_cast<int>(paged::quotient(p, a.page_div)) * a.page_size);
-          if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.n_pages)) {
-            page = -1;
+    // row by row: this warp's 64 keys of the tile, to `to` (operand tile, or raw codes) and its scales to `sc`
+    auto copy_rows = [&](uint32_t to, uint32_t sc) {
+#pragma unroll 1
+      for (int part = 0; part < 2; ++part) {
+        const int r0 = lw * 64 + part * 32;
+        const int p = kc.kt * kTK + r0 + lane;
+        int pg = -1, at = 0;
+        if (p < kc.s.len) {
+          pg = table_at(kc.b, p);
+          at = kc.g * a.page_size + (p - static_cast<int>(paged::quotient(p, a.page_div)) * a.page_size);
+          if (static_cast<unsigned>(pg) >= static_cast<unsigned>(a.n_pages)) {
+            pg = -1;
             if (a.err) atomicOr(a.err, MNW_DEVERR_BAD_PAGE);
           }
         }
-        const uint32_t to = INT8 ? sbase + C::kOffRaw + rs * C::kRaw : sbase + C::kOffRing + slot * C::kTile;
-        const long long mine = page >= 0 ? page * a.page_bytes + static_cast<long long>(at) * (kCh * 16) : -1;
+        const long long mine = pg >= 0 ? pg * a.page_bytes + static_cast<long long>(at) * (kCh * 16) : -1;
         const int c = lane % kCh;
 #pragma unroll 4
         for (int i = 0; i < 32 / kRows; ++i) {
-          const int r = i * kRows + lane / kCh;  // of the warp's 32
+          const int r = i * kRows + lane / kCh;
           const long long off = __shfl_sync(0xffffffffu, mine, r);
-          const int row = warp * 32 + r;
+          const int row = r0 + r;
           const uint32_t dst = INT8 ? to + row * D + c * 16
                                     : to + (c >> 3) * C::kPiece + row * 128 + (((c & 7) ^ (row & 7)) << 4);
           cp16(dst, base + (off >= 0 ? off + c * 16 : 0), off >= 0 ? 16u : 0u);
         }
-        if (INT8 && !values) {  // both scales of the tile, with its keys
-          const long long so = page >= 0 ? static_cast<long long>(page) * a.Hkv * a.page_size + at : 0;
-          const uint32_t n = page >= 0 ? 4u : 0u;
-          cp4(sbase + scale_at + key * 4, a.ks + so, n);
-          cp4(sbase + scale_at + kTK * 4 + key * 4, a.vs + so, n);
-        }
-      } else {
-        const int slot_in_page = a.page_size > kTK ? (x.kt * kTK) & (a.page_size - 1) : 0;
-        if constexpr (!INT8) {
-          if (lane == 0) {
-            if (warp == 0)
-              mbar_arrive_expect_tx(&bars->full[slot], C::kTile);
-            else
-              mbar_arrive(&bars->full[slot]);
-          }
-          __syncwarp();
-          if (warp == 0 && lane < pieces) {
-            uint8_t* dst = smem + C::kOffRing + slot * C::kTile + lane * span * 128;
-#pragma unroll
-            for (int h = 0; h < C::kHalves; ++h)
-              tma_load_4d(dst + h * C::kPiece, values ? &tm_v : &tm_k, &bars->full[slot], 64 * h, slot_in_page, x.g, x.page);
-          }
-        } else if (warp == 0) {
-          if (lane == 0) mbar_arrive_expect_tx(&bars->raw_full[rs], C::kRaw + (values ? 0 : 2 * kTK * 4));
-          __syncwarp();
-          if (lane < pieces) {
-            const int at = x.g * a.page_size + slot_in_page;
-            bulk_load(smem + C::kOffRaw + rs * C::kRaw + lane * span * D,
-                      base + x.page * a.page_bytes + static_cast<long long>(at) * D, span * D, &bars->raw_full[rs]);
-            if (!values) {
-              const long long so = static_cast<long long>(x.page) * a.Hkv * a.page_size + at;
-              bulk_load(smem + scale_at + lane * span * 4, a.ks + so, span * 4, &bars->raw_full[rs]);
-              bulk_load(smem + scale_at + kTK * 4 + lane * span * 4, a.vs + so, span * 4, &bars->raw_full[rs]);
-            }
-          }
-        }
+        if constexpr (INT8)
+          cp4(sc + (r0 + lane) * 4, (values ? a.vs : a.ks) + (pg >= 0 ? static_cast<long long>(pg) * a.Hkv * a.page_size + at : 0),
+              pg >= 0 ? 4u : 0u);
       }
       commit_copies();
-    }
-    wait_copies<0>();
-    if (*abort && warp == 0) {
-      // let every bulk copy already issued land before the CTA exits
-      for (uint32_t it = n_items > C::kSlots ? n_items - C::kSlots : 0; it < n_items; ++it) {
-        if ((by_rows >> (n_items - 1 - it)) & 1) continue;
-        if constexpr (INT8) {
-          if (it >= sent) drain_wait(&bars->raw_full[it % C::kRawSlots], (raw_phase >> (it % C::kRawSlots)) & 1);
-        } else {
-          drain_wait(&bars->full[it % C::kSlots], (it / C::kSlots) & 1);
+    };
+    // ---- a segment's description and its queries, before the segment's first tile ----
+    auto begin_segment = [&](int tiles_left) -> bool {
+      ++seg;
+      if (threadIdx.x == 0) {
+        Seg d;
+        d.tiles = min(kc.sh.kt - kc.kt, tiles_left);
+        d.kt0 = kc.kt;
+        d.g = kc.g;
+        d.rt = kc.rt;
+        d.whole = kc.kt == 0 && d.tiles == kc.sh.kt;
+        d.us = us;
+        d.ku = kc.sh.ku;
+        d.s = kc.s;
+        bars->seg[seg % kMaxSegs] = d;
+        mbar_arrive(&bars->seg_full[seg % kMaxSegs]);
+      }
+      if (seg > 0 && !warp_wait(&bars->q_empty, (seg - 1) & 1, abort, a.err)) return false;
+      // 32 query rows a warp, D / 8 lanes a row
+      constexpr int kQC = D / 8, kQR = 32 / kQC;
+      const int rows = min(kRT, kc.s.n * a.G - kc.rt * kRT);
+      const int c = lane % kQC;
+#pragma unroll 1
+      for (int r0 = warp * 32; r0 < warp * 32 + 32; r0 += 8 * kQR) {
+        uint4 w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = r0 + i * kQR + lane / kQC;
+          const int ri = kc.rt * kRT + r;
+          const int tok = static_cast<int>(paged::quotient(ri, a.g_div)), hh = ri - tok * a.G;
+          w[i] = make_uint4(0, 0, 0, 0);
+          if (r < rows)
+            w[i] = *reinterpret_cast<const uint4*>(a.q + static_cast<long long>(kc.s.start + tok) * a.q_stride +
+                                                   static_cast<long long>(kc.g * a.G + hh) * D + c * 8);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = r0 + i * kQR + lane / kQC;
+          if constexpr (INT8) {
+            const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+            uint32_t mag = 0;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) mag = max(mag, max(u[x] & 0x7FFFu, (u[x] >> 16) & 0x7FFFu));
+#pragma unroll
+            for (int d = kQC / 2; d > 0; d >>= 1) mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, d));
+            // 2^e with the row's largest magnitude in [2^14, 2^15) after x * 2^-e
+            const int e = mag == 0 ? 0 : max(-110, min(113, static_cast<int>(mag >> 7) - 127 - 14));
+            const float f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+            if (c == 0) bars->qfac[seg & 3][r] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+            auto half = [&](uint32_t y) { return half2_bits(__uint_as_float(y << 16) * f, __uint_as_float(y & 0xFFFF0000u) * f); };
+            w[i] = make_uint4(half(u[0]), half(u[1]), half(u[2]), half(u[3]));
+          }
+          *reinterpret_cast<uint4*>(smem + (c >> 3) * C::kPiece + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = w[i];
         }
       }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->q_full);
+      return true;
+    };
+    auto step = [&]() {
+      if (++kc.kt == kc.sh.kt) {
+        us += kc.sh.ku;
+        kc.next_item(a, run.pad);
+      }
+    };
+    if (ok) peek();
+    if constexpr (!INT8) {
+      uint64_t* pending = nullptr;  // the barrier of a tile copied row by row and not yet given on
+      auto give = [&]() {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(pending);
+        pending = nullptr;
+      };
+      for (int t = 0; ok && t < tiles; ++t) {
+        if (t == 0 || kc.kt == 0) {
+          if (pending) {  // products before this segment's wait for it
+            wait_copies<0>();
+            give();
+          }
+          if (!begin_segment(tiles - t)) { ok = false; break; }
+        }
+        if (!warp_wait(&empty[ring.slot], ring.phase ^ 1, abort, a.err)) { ok = false; break; }
+        uint64_t* bar = &full[ring.slot];
+        const uint32_t at = ring_at + ring.slot * C::kTile;
+        const bool rows = !whole || __any_sync(0xffffffffu, static_cast<unsigned>(page) >= static_cast<unsigned>(a.n_pages));
+        if (rows) {
+          copy_rows(sbase + at, 0);
+        } else {
+          if (lw == 0) {
+            if (lane == 0) mbar_arrive_expect_tx(bar, C::kTile);
+            __syncwarp();
+            if (lane < pieces) {
+              const int in_page = a.page_size > kTK ? (kc.kt * kTK) & (a.page_size - 1) : 0;
+              uint8_t* dst = smem + at + lane * span * 128;
+#pragma unroll
+              for (int h = 0; h < C::kHalves; ++h)
+                tma_load_4d(dst + h * C::kPiece, values ? &tm_v : &tm_k, bar, 64 * h, in_page, kc.g, page);
+            }
+            __syncwarp();
+          } else if (lane == 0) {
+            mbar_arrive(bar);
+          }
+        }
+        if (pending) {
+          if (rows)
+            wait_copies<1>();
+          else
+            wait_copies<0>();
+          give();
+        }
+        if (rows) pending = bar;
+        ring.advance(ring_slots);
+        step();
+        if (t + 1 < tiles) peek();
+      }
+      wait_copies<0>();
+      if (pending) give();
+      if (*abort && lw == 0) {
+        // let every bulk copy already issued land before the CTA exits
+        for (int i = 0; i < ring_slots; ++i) drain_wait(&full[i], i < static_cast<int>(ring.slot) ? ring.phase : ring.phase ^ 1);
+      }
+    } else {
+      uint64_t *const raw_full = &bars->raw_full[values ? 1 : 0], *const raw_empty = &bars->raw_empty[values ? 1 : 0];
+      const uint32_t raw_at = C::kOffRaw + (values ? C::kRaw : 0);
+      uint32_t raw_phase = 0;  // parity of the next bulk landing
+      int sc_issue = 0, sc_now = 0;  // scale slots of the tile issued next, of the tile converted
+      auto scales_at = [&](int slot) { return values ? C::kOffVS + slot * (2 * kTK * 4) : C::kOffKS + slot * (kTK * 4); };
+      const int sc_slots = values ? C::kScalesV : C::kScalesK;
+      bool landing_rows = false;
+      bool seg_first = true, seg_next = false;  // whether the tile converted now, next, begins a segment
+      Cursor<kRT, kTK> sc_cur = kc;             // its place, for the segment's description
+      // codes of the tile at kc into the raw buffer, whose last codes both warps have taken (uses counted by `uses`)
+      auto issue = [&](int uses) -> bool {
+        landing_rows = !whole || __any_sync(0xffffffffu, static_cast<unsigned>(page) >= static_cast<unsigned>(a.n_pages));
+        if (landing_rows) {
+          copy_rows(sbase + raw_at, sbase + scales_at(sc_issue));
+        } else if (lw == 0) {
+          if (!warp_wait(raw_empty, (uses & 1) ^ 1, abort, a.err)) return false;
+          if (lane == 0) mbar_arrive_expect_tx(raw_full, C::kRaw + kTK * 4);
+          __syncwarp();
+          if (lane < pieces) {
+            const int at = kc.g * a.page_size + (a.page_size > kTK ? (kc.kt * kTK) & (a.page_size - 1) : 0);
+            bulk_load(smem + raw_at + lane * span * D, base + page * a.page_bytes + static_cast<long long>(at) * D, span * D,
+                      raw_full);
+            bulk_load(smem + scales_at(sc_issue) + lane * span * 4,
+                      (values ? a.vs : a.ks) + static_cast<long long>(page) * a.Hkv * a.page_size + at, span * 4, raw_full);
+          }
+          __syncwarp();
+        }
+        if (++sc_issue == sc_slots) sc_issue = 0;
+        return true;
+      };
+      if (ok) ok = issue(0);
+      bool bulk_out = ok && !landing_rows;  // a bulk copy is under way
+      for (int t = 0; ok && t < tiles; ++t) {
+        // the codes land and are taken into registers
+        if (landing_rows) {
+          wait_copies<0>();
+          __syncwarp();
+        } else {
+          if (!warp_wait(raw_full, raw_phase, abort, a.err)) { ok = false; break; }
+          raw_phase ^= 1;
+          bulk_out = false;
+        }
+        constexpr int kW = 2 * kCh;  // 64 rows
+        uint4 w[kW];
+#pragma unroll
+        for (int i = 0; i < kW; ++i) w[i] = *reinterpret_cast<const uint4*>(smem + raw_at + lw * 64 * D + (i * 32 + lane) * 16);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(raw_empty);
+        // the next tile's copies go out
+        sc_cur = kc;
+        step();
+        seg_next = kc.kt == 0;
+        if (t + 1 < tiles) {
+          peek();
+        }
+        if (seg_first) {
+          const Cursor<kRT, kTK> ahead = kc;
+          const int us_ahead = us;
+          kc = sc_cur;
+          us = us_ahead - (seg_next ? kc.sh.ku : 0);
+          ok = begin_segment(tiles - t);
+          kc = ahead;
+          us = us_ahead;
+          if (!ok) break;
+        }
+        if (t + 1 < tiles) {
+          if (!issue(t + 1)) { ok = false; break; }
+          bulk_out = !landing_rows;
+        }
+        seg_first = seg_next;
+        // codes -> FP16 operand tile
+        if (!warp_wait(&empty[ring.slot], ring.phase ^ 1, abort, a.err)) { ok = false; break; }
+        uint8_t* op = smem + ring_at + ring.slot * C::kTile;
+#pragma unroll
+        for (int i = 0; i < kW; ++i) {
+          const int row = lw * 64 + i * kRows + lane / kCh, c = lane % kCh;
+          const uint32_t ww[4] = {w[i].x ^ 0x80808080u, w[i].y ^ 0x80808080u, w[i].z ^ 0x80808080u, w[i].w ^ 0x80808080u};
+          const uint4 h0 = make_uint4(codes_lo(ww[0]), codes_hi(ww[0]), codes_lo(ww[1]), codes_hi(ww[1]));
+          const uint4 h1 = make_uint4(codes_lo(ww[2]), codes_hi(ww[2]), codes_lo(ww[3]), codes_hi(ww[3]));
+          uint8_t* piece = op + (c >> 2) * C::kPiece + row * 128;
+          const int o = (2 * c) & 7, first = (c >> 2) & 1;  // the two pieces' lanes start on different banks
+          *reinterpret_cast<uint4*>(piece + (((o + first) ^ (row & 7)) << 4)) = first ? h1 : h0;
+          *reinterpret_cast<uint4*>(piece + (((o + (first ^ 1)) ^ (row & 7)) << 4)) = first ? h0 : h1;
+        }
+        if (values) {
+          float* sc = reinterpret_cast<float*>(smem + scales_at(sc_now)) + lw * 64 + lane;
+          sc[kTK] = __log2f(sc[0]);
+          sc[kTK + 32] = __log2f(sc[32]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&full[ring.slot]);
+          mbar_arrive(values ? &bars->vs_full[sc_now] : &bars->ks_full[sc_now]);
+        }
+        ring.advance(ring_slots);
+        if (++sc_now == sc_slots) sc_now = 0;
+      }
+      wait_copies<0>();
+      if (bulk_out && lw == 0) drain_wait(raw_full, raw_phase);  // (an abort) the copy lands before the CTA exits
     }
-  } else if (warp < kWarpSm0) {
-    if (warp == kWarpMma && lane == 0 && tiles > 0) {
+  } else if (warp == kWarpMma) {
+    if (tiles > 0) {
       // ======================= MMA issuer =======================
+      // The warp stays together and its first lane issues: a lane that runs on
+      // alone while the others wait at the CTA's barrier lost 2700 cycles a
+      // tile (of 2900) at its branches.
+      const bool lead = lane == 0;
       const uint32_t idesc = idesc_f16(kRT, kTK, !INT8);
       const uint32_t idesc_pv = idesc_f16(kRT, D, !INT8) | kBMajorN;
-      bool ok = true;
-      RingPos ring;
+      RingPos kr, vr;
       int s_seg = 0, s_left = 0;               // segment of the next scores, its tiles to go
       int p_seg = 0, p_left = 0, p_begin = 0;  // of the next product
       // step x: scores of tile x, then the product of tile x - 1 (so S_0, S_1, P V_0, S_2, P V_1, ...)
-      for (int x = 0; ok && x <= tiles; ++x) {
+      for (int x = 0; x <= tiles; ++x) {
         if (x < tiles) {
           if (s_left == 0) {
-            if (!wait_for(&bars->seg_full[s_seg % kMaxSegs], (s_seg / kMaxSegs) & 1, abort, a.err)) break;
+            if (!warp_wait(&bars->seg_full[s_seg % kMaxSegs], (s_seg / kMaxSegs) & 1, abort, a.err)) break;
             s_left = bars->seg[s_seg % kMaxSegs].tiles;
-            if (!wait_for(&bars->q_full, s_seg & 1, abort, a.err)) break;
+            if (!warp_wait(&bars->q_full, s_seg & 1, abort, a.err)) break;
           }
-          if (!wait_for(&bars->full[ring.slot], ring.phase, abort, a.err)) break;
+          if (!warp_wait(&bars->full[0][kr.slot], kr.phase, abort, a.err)) break;
           tc_fence_after();
-          const uint32_t k_s = sbase + C::kOffRing + ring.slot * C::kTile;
-          const uint32_t d = tmem + static_cast<uint32_t>(x & 1) * kTK;
+          --s_left;
+          if (lead) {
+            const uint32_t k_s = sbase + C::kOffK + kr.slot * C::kTile;
+            const uint32_t d = tmem + static_cast<uint32_t>(x & 1) * kTK;
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * C::kPiece + (kk & 3) * 32;
-            mma_ss(d, sdesc_sw128(sbase + off), sdesc_sw128(k_s + off), idesc, kk > 0);
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = (kk >> 2) * C::kPiece + (kk & 3) * 32;
+              mma_ss(d, sdesc_sw128(sbase + off), sdesc_sw128(k_s + off), idesc, kk > 0);
+            }
+            mma_commit(&bars->s_full[x & 1]);
+            mma_commit(&bars->empty[0][kr.slot]);
+            if (s_left == 0) mma_commit(&bars->q_empty);
           }
-          mma_commit(&bars->s_full[x & 1]);
-          mma_commit(&bars->empty[ring.slot]);
-          ring.advance(C::kSlots);
-          if (--s_left == 0) {
-            mma_commit(&bars->q_empty);
-            ++s_seg;
+          __syncwarp();
+          kr.advance(C::kSlotsK);
+          if (s_left == 0) ++s_seg;
+        }
+        if (x > 0) {
+          const int t = x - 1;
+          if (p_left == 0) {
+            p_left = bars->seg[p_seg % kMaxSegs].tiles;
+            // the segment before has been read out of O
+            if (p_seg > 0 && !warp_wait(&bars->epi, (p_seg - 1) & 1, abort, a.err)) break;
           }
-        }
-        if (x == 0) continue;
-        const int t = x - 1;
-        if (p_left == 0) {
-          p_left = bars->seg[p_seg % kMaxSegs].tiles;
-          // the segment before has been read out of O
-          if (p_seg > 0 && !wait_for(&bars->epi, (p_seg - 1) & 1, abort, a.err)) break;
-        }
-        if (!wait_for(&bars->full[ring.slot], ring.phase, abort, a.err)) break;
-        if (!wait_for(&bars->p_full[t & 1], (t >> 1) & 1, abort, a.err)) break;
-        tc_fence_after();
-        const uint32_t v_s = sbase + C::kOffRing + ring.slot * C::kTile;
-        const uint32_t p = tmem + static_cast<uint32_t>(t & 1) * kTK;  // two keys per column
-        const uint32_t o = tmem + kColO + static_cast<uint32_t>(t & 1) * 128;
-        const bool fresh = t - p_begin < 2;  // the group's first tile of the segment
+          if (!warp_wait2(&bars->full[1][vr.slot], vr.phase, &bars->p_full[t & 1], (t >> 1) & 1, abort, a.err)) break;
+          tc_fence_after();
+          --p_left;
+          if (lead) {
+            const uint32_t v_s = sbase + C::kOffV + vr.slot * C::kTile;
+            const uint32_t p = tmem + static_cast<uint32_t>(t & 1) * kTK;  // two keys per column
+            const uint32_t o = tmem + kColO + static_cast<uint32_t>(t & 1) * 128;
+            const bool fresh = t - p_begin < 2;  // the group's first tile of the segment
 #pragma unroll
-        for (int kk = 0; kk < kTK / 16; ++kk)
-          mma_ts(o, p + kk * 8, sdesc_mn_sw128(v_s + kk * 2048, C::kPiece), idesc_pv, !(fresh && kk == 0));
-        mma_commit(&bars->empty[ring.slot]);
-        ring.advance(C::kSlots);
-        if (--p_left == 0) {
-          mma_commit(&bars->o_full);
-          ++p_seg;
-          p_begin = t + 1;
+            for (int kk = 0; kk < kTK / 16; ++kk)
+              mma_ts(o, p + kk * 8, sdesc_mn_sw128(v_s + kk * 2048, C::kPiece), idesc_pv, !(fresh && kk == 0));
+            mma_commit(&bars->empty[1][vr.slot]);
+            if (p_left == 0) mma_commit(&bars->o_full);
+          }
+          __syncwarp();
+          vr.advance(C::kSlotsV);
+          if (p_left == 0) {
+            ++p_seg;
+            p_begin = t + 1;
+          }
         }
       }
       // every MMA has finished with shared and tensor memory before the CTA tears down
-      mma_commit(&bars->drain);
-      drain_wait(&bars->drain, 0);
+      if (lead) {
+        mma_commit(&bars->drain);
+        drain_wait(&bars->drain, 0);
+      }
+      __syncwarp();
     }
   } else {
     // ======================= softmax =======================
@@ -540,164 +643,223 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_bits = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t s_at = tmem + lane_bits + static_cast<uint32_t>(grp) * kTK;
     const uint32_t o_at = tmem + lane_bits + kColO + static_cast<uint32_t>(grp) * 128;
+    const int g8 = lane >> 2, t4 = lane & 3;
     bool ok = true;
-    int t = 0;
+    int t = 0, ks_slot = 0, vs_slot = 0;
+    uint32_t ks_phase = 0, vs_phase = 0;
     for (int seg = 0; ok && t < tiles; ++seg) {
       if (!warp_wait(&bars->seg_full[seg % kMaxSegs], (seg / kMaxSegs) & 1, abort, a.err)) break;
       const Seg& sg = bars->seg[seg % kMaxSegs];
       const int rows = min(kRT, sg.s.n * a.G - sg.rt * kRT);
-      const int lim = row_limit(a, sg.s, sg.rt * kRT + min(r, rows - 1));
       const int end = t + sg.tiles;
-      int left = lim - sg.kt0 * kTK;  // keys of the tile below it are seen
-      float m = -INFINITY, l = 0.f, unit = -INFINITY, fac = a.scale_log2;
+      // of rows 32 quarter + 16 h + g8 + 8 x: first key (of the tile at hand) not seen, maximum, sum of this thread's
+      // keys, log2 of O's unit
+      struct RowState {
+        int left;
+        float m, l, unit;
+      } st[2][2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          st[h][x] = RowState{row_limit(a, sg.s, sg.rt * kRT + min(quarter * 32 + 16 * h + g8 + 8 * x, rows - 1)) - sg.kt0 * kTK,
+                              -INFINITY, 0.f, -INFINITY};
       bool any = false;
-      for (; t < end; ++t, left -= kTK) {
-        if ((t & 1) != grp) continue;
-        if (!warp_wait(&bars->s_full[grp], (t >> 1) & 1, abort, a.err)) { ok = false; break; }
-        const float* scales = nullptr;
-        if constexpr (INT8) {
-          if (!warp_wait(&bars->sc_full[t % C::kScaleSlots], (t / C::kScaleSlots) & 1, abort, a.err)) { ok = false; break; }
-          scales = reinterpret_cast<const float*>(smem + C::kOffScale + (t % C::kScaleSlots) * C::kScaleSlot);
-          // the query rows' factors were written before q_full, which the scores waited for
-          fac = a.scale_log2 * bars->qfac[seg & 3][r];
-        }
-        tc_fence_after();
-        const uint64_t fac2 = f32x2_pack(__float_as_uint(fac), __float_as_uint(fac));
-        // 64 scores of the row, scaled (INT8) and masked.  Scores are read twice from tensor memory: all 128 at once
-        // would not fit the registers.
-        auto load_scores = [&](int h, uint32_t (&sv)[64]) {
-          tmem_ld32(s_at + 64 * h, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
-          tmem_ld32(s_at + 64 * h + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
-          tmem_wait_ld();
+      for (; t < end; ++t) {
+        if ((t & 1) == grp) {
+          if (!warp_wait(&bars->s_full[grp], (t >> 1) & 1, abort, a.err)) { ok = false; break; }
+          const float *ks = nullptr, *vs = nullptr;
           if constexpr (INT8) {
-#pragma unroll
-            for (int i = 0; i < 64; i += 4) {
-              const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(scales + 64 * h + i);
-              const uint64_t x0 = f32x2_mul(f32x2_pack(sv[i], sv[i + 1]), f.x), x1 = f32x2_mul(f32x2_pack(sv[i + 2], sv[i + 3]), f.y);
-              sv[i] = static_cast<uint32_t>(x0);
-              sv[i + 1] = static_cast<uint32_t>(x0 >> 32);
-              sv[i + 2] = static_cast<uint32_t>(x1);
-              sv[i + 3] = static_cast<uint32_t>(x1 >> 32);
-            }
+            if (!warp_wait2(&bars->ks_full[ks_slot], ks_phase, &bars->vs_full[vs_slot], vs_phase, abort, a.err)) { ok = false; break; }
+            ks = reinterpret_cast<const float*>(smem + C::kOffKS) + ks_slot * kTK + 2 * t4;
+            vs = reinterpret_cast<const float*>(smem + C::kOffVS) + vs_slot * 2 * kTK + 2 * t4;
           }
-          const int lh = left - 64 * h;
-          if (__any_sync(0xffffffffu, lh < 64)) {
-#pragma unroll
-            for (int i = 0; i < 64; ++i)
-              if (i >= lh) sv[i] = 0xff800000u;  // -inf
-          }
-        };
-        // the row's maximum; INT8: also log2 of its largest e^score times value scale
-        float top = -INFINITY, topv = -INFINITY;
+          tc_fence_after();
+          // 16 rows at a time (their state is st[0], the other rows' st[1]: exchanged after each), 64 keys at a time
 #pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          uint32_t sv[64];
-          load_scores(h, sv);
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, mv[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-          for (int i = 0; i < 64; i += 4) {
-            const int x = (i >> 1) & 2;
-            mx[x] = fmaxf(fmaxf(mx[x], __uint_as_float(sv[i])), __uint_as_float(sv[i + 1]));
-            mx[x + 1] = fmaxf(fmaxf(mx[x + 1], __uint_as_float(sv[i + 2])), __uint_as_float(sv[i + 3]));
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t half = static_cast<uint32_t>(16 * h) << 16;
+            float fac[2] = {a.scale_log2, a.scale_log2};
             if constexpr (INT8) {
-              const ulonglong2 g = *reinterpret_cast<const ulonglong2*>(scales + 2 * kTK + 64 * h + i);
-              const uint64_t y0 = f32x2_fma(f32x2_pack(sv[i], sv[i + 1]), fac2, g.x);
-              const uint64_t y1 = f32x2_fma(f32x2_pack(sv[i + 2], sv[i + 3]), fac2, g.y);
-              mv[0] = fmaxf(fmaxf(mv[0], lo32(y0)), hi32(y0));
-              mv[1] = fmaxf(fmaxf(mv[1], lo32(y1)), hi32(y1));
+              // the query rows' factors were written before q_full, which the scores waited for
+              const float* qf = &bars->qfac[seg & 3][quarter * 32 + 16 * h + g8];
+              fac[0] *= qf[0];
+              fac[1] *= qf[8];
             }
-          }
-          top = fmaxf(top, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
-          topv = fmaxf(topv, fmaxf(mv[0], mv[1]));
-        }
-        top *= fac;
-        float alpha = 1.f;  // what O is multiplied by
-        float lift = 1.f;
-        if constexpr (!INT8) {
-          if (top > m + kRescaleLog2 || m == -INFINITY) {
-            const float n = fmaxf(m, top);
-            alpha = n == -INFINITY ? 1.f : ex2(m - n);  // 0 where nothing was seen before
-            l *= alpha;
-            m = n;
-          }
-        } else {
-          const float n = fmaxf(m, top);
-          l *= n == -INFINITY ? 1.f : ex2(m - n);
-          m = n;
-          // held within 2^100 of e^m so that the lift stays finite
-          const float at = fmaxf(topv, m - 100.f);
-          if (m != -INFINITY && at > unit + 1.f) {
-            alpha = ex2(unit - at);  // 0 from -inf
-            unit = at;
-          }
-          lift = unit == -INFINITY ? 0.f : ex2(m - unit + 14.f);
-        }
-        const float base = m == -INFINITY ? 0.f : m;
-        if (any && __any_sync(0xffffffffu, alpha != 1.f)) {
-          // O_grp holds this group's earlier products, all complete (see above)
-#pragma unroll 1
-          for (int i = 0; i < D; i += 32) {
-            uint32_t o[32];
-            tmem_ld32(o_at + i, o);
-            tmem_wait_ld();
+            const uint64_t fac2[2] = {f32x2_pack(__float_as_uint(fac[0]), __float_as_uint(fac[0])),
+                                      f32x2_pack(__float_as_uint(fac[1]), __float_as_uint(fac[1]))};
+            const bool masked = __any_sync(0xffffffffu, min(st[0][0].left, st[0][1].left) < kTK);
+            // scores of 64 keys, scaled (INT8) and masked: register 4 i + 2 x + e is key 8 i + 2 t4 + e of row g8 + 8 x
+            auto load_scores = [&](int kb, uint32_t (&sv)[32]) {
+              tmem_ld_frag(s_at + half + 64 * kb, sv);
+              tmem_wait_ld();
+              if constexpr (INT8) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            tmem_st16(o_at + i, *reinterpret_cast<uint32_t(*)[16]>(&o[0]));
-            tmem_st16(o_at + i + 16, *reinterpret_cast<uint32_t(*)[16]>(&o[16]));
-          }
-        }
-        any = true;
-        // p = 2^(s fac - m), two keys per packed operation, its sum, and P over the first half of the group's S columns,
-        // two keys a column
-        const uint64_t neg2 = f32x2_pack(__float_as_uint(-base), __float_as_uint(-base));
-        const uint64_t lift2 = f32x2_pack(__float_as_uint(lift), __float_as_uint(lift));
-        uint64_t l2[2] = {0ull, 0ull};
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          uint32_t sv[64];
-          load_scores(h, sv);
+                for (int i = 0; i < 8; ++i) {
+                  const uint64_t f = *reinterpret_cast<const uint64_t*>(ks + 64 * kb + 8 * i);
 #pragma unroll
-          for (int i = 0; i < 64; i += 4) {
-            ulonglong2 w{};
-            if constexpr (INT8) w = *reinterpret_cast<const ulonglong2*>(scales + kTK + 64 * h + i);
+                  for (int x = 0; x < 2; ++x) {
+                    const uint64_t y = f32x2_mul(f32x2_pack(sv[4 * i + 2 * x], sv[4 * i + 2 * x + 1]), f);
+                    sv[4 * i + 2 * x] = static_cast<uint32_t>(y);
+                    sv[4 * i + 2 * x + 1] = static_cast<uint32_t>(y >> 32);
+                  }
+                }
+              }
+              if (masked) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if (64 * kb + 8 * (e >> 2) + 2 * t4 + (e & 1) >= st[0][(e >> 1) & 1].left) sv[e] = 0xff800000u;  // -inf
+              }
+            };
+            // the rows' maxima; INT8: also log2 of their largest e^score times value scale
+            float top[2] = {-INFINITY, -INFINITY}, topv[2] = {-INFINITY, -INFINITY};
+#pragma unroll 1
+            for (int kb = 0; kb < 2; ++kb) {
+              uint32_t sv[32];
+              load_scores(kb, sv);
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                  top[x] = fmaxf(fmaxf(top[x], __uint_as_float(sv[4 * i + 2 * x])), __uint_as_float(sv[4 * i + 2 * x + 1]));
+              if constexpr (INT8) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const uint64_t lv = *reinterpret_cast<const uint64_t*>(vs + kTK + 64 * kb + 8 * i);
+#pragma unroll
+                  for (int x = 0; x < 2; ++x) {
+                    const uint64_t y = f32x2_fma(f32x2_pack(sv[4 * i + 2 * x], sv[4 * i + 2 * x + 1]), fac2[x], lv);
+                    topv[x] = fmaxf(fmaxf(topv[x], lo32(y)), hi32(y));
+                  }
+                }
+              }
+            }
+            float alpha[2] = {1.f, 1.f}, lift[2] = {1.f, 1.f};
+            uint64_t neg2[2], l2[2] = {0ull, 0ull};
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              const uint64_t e2 = f32x2_fma(f32x2_pack(sv[i + 2 * x], sv[i + 2 * x + 1]), fac2, neg2);
-              uint64_t p2 = f32x2_pack(__float_as_uint(ex2(lo32(e2))), __float_as_uint(ex2(hi32(e2))));
-              l2[x] = f32x2_add(l2[x], p2);
-              if constexpr (INT8) p2 = f32x2_mul(f32x2_mul(p2, x ? w.y : w.x), lift2);
-              sv[i / 2 + x] = INT8 ? half2_bits(lo32(p2), hi32(p2)) : pack_bf16x2(lo32(p2), hi32(p2));
+#pragma unroll
+              for (int d = 1; d < 4; d <<= 1) {
+                top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], d));
+                if constexpr (INT8) topv[x] = fmaxf(topv[x], __shfl_xor_sync(0xffffffffu, topv[x], d));
+              }
+              top[x] *= fac[x];
+              RowState& rs = st[0][x];
+              if constexpr (!INT8) {
+                if (top[x] > rs.m + kRescaleLog2 || rs.m == -INFINITY) {
+                  const float n = fmaxf(rs.m, top[x]);
+                  alpha[x] = n == -INFINITY ? 1.f : ex2(rs.m - n);  // 0 where nothing was seen before
+                  rs.l *= alpha[x];
+                  rs.m = n;
+                }
+              } else {
+                const float n = fmaxf(rs.m, top[x]);
+                rs.l *= n == -INFINITY ? 1.f : ex2(rs.m - n);
+                rs.m = n;
+                // held within 2^100 of e^m so that the lift stays finite
+                const float at = fmaxf(topv[x], n - 100.f);
+                if (n != -INFINITY && at > rs.unit + 1.f) {
+                  alpha[x] = ex2(rs.unit - at);  // 0 from -inf
+                  rs.unit = at;
+                }
+                lift[x] = rs.unit == -INFINITY ? 0.f : ex2(n - rs.unit + 14.f);
+              }
+              const float base = rs.m == -INFINITY ? 0.f : rs.m;
+              neg2[x] = f32x2_pack(__float_as_uint(-base), __float_as_uint(-base));
+            }
+            if (any && __any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+              // O_grp holds this group's earlier products, all complete (see above)
+#pragma unroll 1
+              for (int i = 0; i < D; i += 64) {
+                uint32_t o[32];
+                tmem_ld_frag(o_at + half + i, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha[(e >> 1) & 1]);
+                tmem_st_frag(o_at + half + i, o);
+              }
+            }
+            // p = 2^(s fac - m), two keys per packed operation, its sum, and P, two keys a column, over the first half of
+            // the rows' S columns (read before: keys 64 .. 127 lie in the second half)
+#pragma unroll 1
+            for (int kb = 0; kb < 2; ++kb) {
+              uint32_t sv[32], pk[16];
+              load_scores(kb, sv);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                uint64_t w = 0;
+                if constexpr (INT8) w = *reinterpret_cast<const uint64_t*>(vs + 64 * kb + 8 * i);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                  const uint64_t e2 = f32x2_fma(f32x2_pack(sv[4 * i + 2 * x], sv[4 * i + 2 * x + 1]), fac2[x], neg2[x]);
+                  uint64_t p2 = f32x2_pack(__float_as_uint(ex2(lo32(e2))), __float_as_uint(ex2(hi32(e2))));
+                  l2[x] = f32x2_add(l2[x], p2);
+                  if constexpr (INT8)
+                    p2 = f32x2_mul(f32x2_mul(p2, w), f32x2_pack(__float_as_uint(lift[x]), __float_as_uint(lift[x])));
+                  pk[2 * i + x] = INT8 ? half2_bits(lo32(p2), hi32(p2)) : pack_bf16x2(lo32(p2), hi32(p2));
+                }
+              }
+              tmem_st_pairs(s_at + half + 32 * kb, pk);
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              st[0][x].l += lo32(l2[x]) + hi32(l2[x]);
+              const RowState other = st[1][x];
+              st[1][x] = st[0][x];
+              st[0][x] = other;
             }
           }
-          tmem_st16(s_at + 32 * h, *reinterpret_cast<uint32_t(*)[16]>(&sv[0]));
-          tmem_st16(s_at + 32 * h + 16, *reinterpret_cast<uint32_t(*)[16]>(&sv[16]));
+          any = true;
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->p_full[grp]);
         }
-        const uint64_t ls = f32x2_add(l2[0], l2[1]);
-        l += lo32(ls) + hi32(ls);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->p_full[grp]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) st[h][x].left -= kTK;
+        if constexpr (INT8) {
+          if (++ks_slot == C::kScalesK) {
+            ks_slot = 0;
+            ks_phase ^= 1;
+          }
+          if (++vs_slot == C::kScalesV) {
+            vs_slot = 0;
+            vs_phase ^= 1;
+          }
+        }
       }
       if (!ok) break;
       // ---- the segment's end: both groups' parts of a row meet ----
       const int par = seg & 1;
-      bars->st_m[par][grp][r] = m;
-      bars->st_l[par][grp][r] = l;
-      bars->st_u[par][grp][r] = INT8 && unit != -INFINITY ? unit - m - 14.f : 0.f;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          float sum = st[h][x].l;
+          sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+          if (t4 == 0) {
+            const int row = quarter * 32 + 16 * h + g8 + 8 * x;
+            bars->st_m[par][grp][row] = st[h][x].m;
+            bars->st_l[par][grp][row] = sum;
+            bars->st_u[par][grp][row] = INT8 && st[h][x].unit != -INFINITY ? st[h][x].unit - st[h][x].m - 14.f : 0.f;
+          }
+        }
       bars->st_any[par][grp] = any;  // the same for all rows
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->fin[quarter]);
       if (!warp_wait(&bars->fin[quarter], par, abort, a.err)) break;
       if (!warp_wait(&bars->o_full, par, abort, a.err)) break;
       tc_fence_after();
-      const float m0 = bars->st_m[par][0][r], m1 = bars->st_m[par][1][r];
-      const float M = fmaxf(m0, m1);  // a group without tiles has -inf
+      const float gm0 = bars->st_m[par][0][r], gm1 = bars->st_m[par][1][r];
+      const float M = fmaxf(gm0, gm1);  // a group without tiles has -inf
       const float bs = M == -INFINITY ? 0.f : M;
-      const float L = ex2(m0 - bs) * bars->st_l[par][0][r] + ex2(m1 - bs) * bars->st_l[par][1][r];
+      const float L = ex2(gm0 - bs) * bars->st_l[par][0][r] + ex2(gm1 - bs) * bars->st_l[par][1][r];
       const bool whole = sg.whole != 0;
       const float inv = whole ? (L == 0.f ? 0.f : 1.f / L) : 1.f;
-      const float f0 = ex2(m0 - bs + bars->st_u[par][0][r]) * inv, f1 = ex2(m1 - bs + bars->st_u[par][1][r]) * inv;
+      const float f0 = ex2(gm0 - bs + bars->st_u[par][0][r]) * inv, f1 = ex2(gm1 - bs + bars->st_u[par][1][r]) * inv;
       const bool has0 = bars->st_any[par][0] != 0, has1 = bars->st_any[par][1] != 0;
       const size_t row = out_row<kRT>(a, sg.s, sg.g, sg.rt, min(r, rows - 1));
       const int which = sg.kt0 > 0 ? 0 : 1;
@@ -766,9 +928,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Span sp = span_of(sg.us, sg.ku, run.per);
       if (!all_arrived(a, sp, run.per, 2ll * blockIdx.x + x)) continue;
       const int rows = min(kRT, sg.s.n * a.G - sg.rt * kRT);
-      float* scratch = reinterpret_cast<float*>(smem) + threadIdx.x / (D / 4) * 2 * kJoinBatch;
-      for (int r = threadIdx.x / (D / 4); r < rows; r += kThreads / (D / 4))
-        join_row<D, kRT>(a, sg.s, sp, run.per, sg.g, sg.rt, r, scratch);
+      join_item<D, kRT, kThreads>(a, sg.s, sp, run.per, sg.g, sg.rt, rows, reinterpret_cast<float*>(smem));
       clear_arrivals(a, sp, run.per);
     }
   }

@@ -335,6 +335,59 @@ __device__ __forceinline__ void join_row(const Args& a, const Seq& s, const Span
   if (a.lse && j == 0) a.lse[row] = (M + log2f(L)) * kLn2;
 }
 
+// The rows [0, rows) of an item by the whole CTA.  Up to kFewParts parts (the
+// usual case: runs are about as long as items), a row's loads all go out at
+// once, those of two rows together; one row after another, a latency each for
+// the maxima and the outputs, took 20 us for 128 rows.
+constexpr int kFewParts = 4;
+template <int D, int RT, int THREADS>
+__device__ __forceinline__ void join_item(const Args& a, const Seq& s, const Span& sp, int per, int g, int rt, int rows,
+                                          float* scratch) {
+  constexpr int kCols = D / 4, kStep = THREADS / kCols;
+  const int col = (threadIdx.x % kCols) * 4;
+  const int parts = sp.c1 - sp.c0 + 1;
+  if (parts > kFewParts) {
+#pragma unroll 1
+    for (int r = threadIdx.x / kCols; r < rows; r += kStep)
+      join_row<D, RT>(a, s, sp, per, g, rt, r, scratch + threadIdx.x / kCols * 2 * kJoinBatch);
+    return;
+  }
+#pragma unroll 2
+  for (int r = threadIdx.x / kCols; r < rows; r += kStep) {
+    float2 ml[kFewParts];
+    float4 v[kFewParts];
+#pragma unroll
+    for (int p = 0; p < kFewParts; ++p) {
+      ml[p] = make_float2(-INFINITY, 0.f);
+      v[p] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (p < parts) {
+        const long long at = slot_of(sp, sp.c0 + p, per) * RT + r;
+        ml[p] = __ldcg(a.part_ml + at);
+        v[p] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D + col));
+      }
+    }
+    float M = -INFINITY, L = 0.f;
+#pragma unroll
+    for (int p = 0; p < kFewParts; ++p) M = fmaxf(M, ml[p].x);
+    const float base = M == -INFINITY ? 0.f : M;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int p = 0; p < kFewParts; ++p) {
+      const float f = ex2(ml[p].x - base);
+      L += f * ml[p].y;
+      acc.x = fmaf(f, v[p].x, acc.x);
+      acc.y = fmaf(f, v[p].y, acc.y);
+      acc.z = fmaf(f, v[p].z, acc.z);
+      acc.w = fmaf(f, v[p].w, acc.w);
+    }
+    const size_t row = out_row<RT>(a, s, g, rt, r);
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    *reinterpret_cast<uint2*>(a.out + row * D + col) =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    if (a.lse && col == 0) a.lse[row] = (M + log2f(L)) * kLn2;
+  }
+}
+
 // The block kernel over `runs` runs (mnw_attn_paged_block.cu).
 int launch_block(const Args& a, int d, bool int8, int runs, cudaStream_t st);
 
