@@ -515,9 +515,9 @@ __global__ void __launch_bounds__(WR* WK * 32) paged_attn_kernel(const Args a) {
       }
       if (!whole && a.fused) {
         const Span sp = span_of(item_first, cc.sh.ku, run.per);
-        if (all_arrived(a, sp, run.per, pslot)) {
-          join_item<D, kRT, kThreads>(a, cc.s, sp, run.per, cc.g, cc.rt, rows, reinterpret_cast<float*>(stage));
-          clear_arrivals(a, sp, run.per);
+        if (all_arrived<0, kThreads>(a, sp, run.per, pslot, tid)) {
+          join_item<D, kRT, kThreads>(a, cc.s, sp, run.per, cc.g, cc.rt, rows, reinterpret_cast<float*>(stage), tid);
+          clear_arrivals<kThreads>(a, sp, run.per, tid);
         }
       }
       item_first += cc.sh.ku;

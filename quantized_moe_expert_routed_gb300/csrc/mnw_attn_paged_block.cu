@@ -8,7 +8,7 @@
 // tensor instructions cannot feed (2046 of tcgen05's ~3800 multiply-adds a
 // clock, and every 16 rows would read the tile from shared memory again).
 //
-// Roles (416 threads):
+// Roles (512 threads):
 //   warps 0-1   key loaders, warps 2-3 value loaders.  A tile that lies whole
 //               inside the length, of pages that divide it (or that it
 //               divides), comes by TMA, a lane per page, straight into operand
@@ -20,20 +20,20 @@
 //               operand tiles (exact) while the next codes land.  All four
 //               bring the query tile of each segment (a run's part of an
 //               item); the first describes the segment to the other roles.
-//   warp 12     issues the MMAs (its first lane): S_t = Q K_t^T, O_g += P_t V_t
-//               with P_t from tensor memory and V as it lies in the cache,
-//               [key][d], an operand whose N dimension is contiguous.
-//   warps 4-11  softmax, two groups of 4 warps: group t % 2 takes tile t, with
+//   warp 4      issues S_t = Q K_t^T, warp 5 O_g += P_t V_t, with P_t from
+//               tensor memory and V as it lies in the cache, [key][d], an
+//               operand whose N dimension is contiguous.  Two warps, because
+//               one accumulator's products follow each other at ~96 cycles
+//               and the two chains fill each other's gaps.
+//   warps 8-15  softmax, two groups of 4 warps: group t % 2 takes tile t, with
 //               its own O accumulator, maxima and sums, so that one group
 //               computes while the other's products run.  A warp takes its 32
-//               rows 16 at a time and 64 keys at a time, a thread 16 keys of two
-//               rows (so a key's scales serve two rows); scores are read from
-//               tensor memory once for the maximum and once for P.  More at
-//               once would spill, and with the shared memory this kernel takes
-//               there is next to no L1 for spills to hit.
-// Order of the products: S_0, S_1, then O += P_t V_t, S_{t+2}; a tile's
-// scores being complete therefore means that its group's earlier product into
-// O is complete too (one issuing thread, in order).
+//               rows 16 at a time, a thread 32 keys of two rows (so a key's
+//               scales serve two rows), kept in registers from the maximum to P.
+//               More at once would spill, and with the shared memory this
+//               kernel takes there is next to no L1 for spills to hit.
+// S of a tile goes into its score buffer once P V of the tile there before is
+// complete.
 //
 // BF16 caches: P is rounded to BF16 relative to a running maximum that moves
 // only when it grows by more than 2^8.  INT8 caches: scores times the key's
@@ -53,13 +53,13 @@ namespace pattn {
 namespace {
 
 constexpr int kRT = kBlockRows, kTK = kBlockKeys;
-constexpr int kThreads = 416;
-constexpr int kLoadWarps = 4, kWarpSm0 = 4, kWarpMma = 12;
+constexpr int kThreads = 512;
+constexpr int kLoadWarps = 4, kWarpS = 4, kWarpPv = 5, kWarpSm0 = 8;
 constexpr int kTmemCols = 512;
-constexpr uint32_t kColO = 256;  // O_g at kColO + 128 g; S_g at 128 g
 constexpr int kMaxSegs = 8;      // segment descriptions held; at most four segments are under way
 constexpr int kMaxSlots = 4;
-constexpr int kMaxKScales = 8, kMaxVScales = 6;
+constexpr int kMaxKScales = 9, kMaxVScales = 6;
+constexpr int kMaxBufs = 3;
 constexpr float kRescaleLog2 = 8.f;
 
 template <int D, bool INT8>
@@ -69,10 +69,15 @@ struct BCfg {
   static constexpr uint32_t kTile = kHalves * kPiece;      // operand tile
   static constexpr int kSlotsK = D == 64 ? 4 : (INT8 ? 2 : 3), kSlotsV = D == 64 ? 4 : 2;
   static constexpr uint32_t kRaw = INT8 ? kTK * D : 0;     // raw codes of a tile
+  // Tensor memory: score buffers (tile t in buffer t % kBufs, its P over the first half), then the two groups' O.  A
+  // third buffer lets a group's next scores be ready before its P is consumed; with 128-wide heads there is no room.
+  static constexpr int kBufs = D == 64 ? 3 : 2;
+  static constexpr uint32_t kColO = kBufs * kTK;           // O_g at kColO + D g
+  static_assert(kColO + 2 * D <= kTmemCols);
   // Scales are copied with a tile's codes, which are issued once the tile two before went into its operand slot, that
-  // is, once the product with the tile that held the slot before is complete; the softmax of a tile reads them last
-  // before P V of the tile is issued (and S of the tile two after follows that).
-  static constexpr int kScalesK = 4 + kSlotsK, kScalesV = 2 + kSlotsV;
+  // is, once the product with the tile that held the slot before is complete (S waits for P V of kBufs tiles before);
+  // the softmax of a tile reads them last before P V of the tile is issued.
+  static constexpr int kScalesK = 2 + kSlotsK + kBufs, kScalesV = 2 + kSlotsV;
   static_assert(kScalesK <= kMaxKScales && kScalesV <= kMaxVScales && kSlotsK <= kMaxSlots && kSlotsV <= kMaxSlots);
   static constexpr uint32_t kOffK = kTile;                 // Q first
   static constexpr uint32_t kOffV = kOffK + kSlotsK * kTile;
@@ -94,21 +99,35 @@ struct Bars {
   uint64_t full[2][kMaxSlots], empty[2][kMaxSlots];  // operand rings: keys, values
   uint64_t raw_full[2], raw_empty[2];
   uint64_t q_full, q_empty;
-  uint64_t s_full[2], p_full[2];        // per softmax group
+  uint64_t s_full[kMaxBufs], p_full[kMaxBufs], s_free[kMaxBufs];  // per score buffer: scores complete, P written, P consumed
   uint64_t o_full, epi;                 // a segment's output complete; read
   uint64_t ks_full[kMaxKScales], vs_full[kMaxVScales];
   uint64_t seg_full[kMaxSegs];
   uint64_t fin[4];                      // per lane quarter: both groups' maxima and sums written
-  uint64_t drain;
+  uint64_t drain[2];
   float st_m[2][2][kRT], st_l[2][2][kRT], st_u[2][2][kRT];  // [segment parity][group][row]: maximum, sum, log2 of O's unit over 2^maximum
   float qfac[4][kRT];                   // [segment % 4] INT8: the query rows' powers of two
   int st_any[2][2];                     // [segment parity][group]: whether the group had a tile
   Seg seg[kMaxSegs];
   Seg part[2];                          // the run's parts of shared items: the one that continues an item, that begins one
-  int has_part[2];
+  int has_part[2], joins;
   uint32_t tmem_base;
   int abort;
 };
+
+// The warpgroup's registers a thread from here on: more (N > 0, waits until
+// they are free) or fewer (N < 0).  The kernel is built for kRegsBuilt, and the
+// split must not pass that in sum.  Once a role: a second change would have to
+// meet the whole warpgroup first, and may wait for a contiguous range for ever.
+constexpr int kRegsBuilt = 128, kRegsLoad = 112, kRegsMma = 64, kRegsSoftmax = 168;
+static_assert(kRegsLoad + kRegsMma + 2 * kRegsSoftmax == 4 * kRegsBuilt);
+template <int N>
+__device__ __forceinline__ void registers() {
+  if constexpr (N > 0)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+  else
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(-N));
+}
 
 struct RingPos {
   uint32_t slot = 0, phase = 0;
@@ -136,7 +155,7 @@ __device__ __forceinline__ void wait_copies() {
 // were most of the kernel's time.  Bounded like it: gives up when *abort is
 // set, or after kWaitLimitNs, which sets it and reports.  The slow side is a call;
 // inlined at every wait it would be a good part of the kernel's code.
-__device__ __noinline__ bool slow_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* err) {
+__device__ __forceinline__ bool slow_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* err) {
   const uint64_t t0 = globaltimer();
   for (uint32_t it = 1;; ++it) {
     if (mbar_try_wait(bar, parity)) return true;
@@ -246,8 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       mbar_init(&bars->raw_full[x], 1);
       mbar_init(&bars->raw_empty[x], 2);
-      mbar_init(&bars->s_full[x], 1);
-      mbar_init(&bars->p_full[x], 4);
+      mbar_init(&bars->drain[x], 1);
       bars->has_part[x] = 0;
     }
     mbar_init(&bars->q_full, kLoadWarps);
@@ -258,11 +276,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kMaxVScales; ++i) mbar_init(&bars->vs_full[i], 2);
     for (int i = 0; i < kMaxSegs; ++i) mbar_init(&bars->seg_full[i], 1);
     for (int i = 0; i < 4; ++i) mbar_init(&bars->fin[i], 2);
-    mbar_init(&bars->drain, 1);
+    for (int i = 0; i < kMaxBufs; ++i) {
+      mbar_init(&bars->s_full[i], 1);
+      mbar_init(&bars->p_full[i], 4);
+      mbar_init(&bars->s_free[i], 1);
+    }
     bars->abort = 0;
     fence_barrier_init();
   }
-  if (warp == kWarpMma) {
+  if (warp == kWarpS) {
     tmem_alloc(&bars->tmem_base, kTmemCols);
     tmem_relinquish();
   }
@@ -281,6 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < kLoadWarps) {
     // ======================= loaders =======================
+    registers<-kRegsLoad>();
     const bool values = warp >= 2;   // (uniform in the warp)
     const int lw = warp & 1;         // which 64 keys of a tile
     const int ring_slots = values ? C::kSlotsV : C::kSlotsK;
@@ -467,8 +490,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto scales_at = [&](int slot) { return values ? C::kOffVS + slot * (2 * kTK * 4) : C::kOffKS + slot * (kTK * 4); };
       const int sc_slots = values ? C::kScalesV : C::kScalesK;
       bool landing_rows = false;
-      bool seg_first = true, seg_next = false;  // whether the tile converted now, next, begins a segment
-      Cursor<kRT, kTK> sc_cur = kc;             // its place, for the segment's description
       // codes of the tile at kc into the raw buffer, whose last codes both warps have taken (uses counted by `uses`)
       auto issue = [&](int uses) -> bool {
         landing_rows = !whole || __any_sync(0xffffffffu, static_cast<unsigned>(page) >= static_cast<unsigned>(a.n_pages));
@@ -493,6 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok) ok = issue(0);
       bool bulk_out = ok && !landing_rows;  // a bulk copy is under way
       for (int t = 0; ok && t < tiles; ++t) {
+        if ((t == 0 || kc.kt == 0) && !begin_segment(tiles - t)) { ok = false; break; }
         // the codes land and are taken into registers
         if (landing_rows) {
           wait_copies<0>();
@@ -509,27 +531,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(raw_empty);
         // the next tile's copies go out
-        sc_cur = kc;
         step();
-        seg_next = kc.kt == 0;
         if (t + 1 < tiles) {
           peek();
-        }
-        if (seg_first) {
-          const Cursor<kRT, kTK> ahead = kc;
-          const int us_ahead = us;
-          kc = sc_cur;
-          us = us_ahead - (seg_next ? kc.sh.ku : 0);
-          ok = begin_segment(tiles - t);
-          kc = ahead;
-          us = us_ahead;
-          if (!ok) break;
-        }
-        if (t + 1 < tiles) {
           if (!issue(t + 1)) { ok = false; break; }
           bulk_out = !landing_rows;
         }
-        seg_first = seg_next;
         // codes -> FP16 operand tile
         if (!warp_wait(&empty[ring.slot], ring.phase ^ 1, abort, a.err)) { ok = false; break; }
         uint8_t* op = smem + ring_at + ring.slot * C::kTile;
@@ -561,92 +568,95 @@ __global__ void __launch_bounds__(kThreads, 1)
       wait_copies<0>();
       if (bulk_out && lw == 0) drain_wait(raw_full, raw_phase);  // (an abort) the copy lands before the CTA exits
     }
-  } else if (warp == kWarpMma) {
-    if (tiles > 0) {
-      // ======================= MMA issuer =======================
-      // The warp stays together and its first lane issues: a lane that runs on
-      // alone while the others wait at the CTA's barrier lost 2700 cycles a
-      // tile (of 2900) at its branches.
-      const bool lead = lane == 0;
+  } else if (warp < kWarpSm0) {
+    registers<-kRegsMma>();
+    // ======================= MMA issuers =======================
+    // The warps stay together and their first lanes issue.
+    const bool lead = lane == 0;
+    if (warp == kWarpS && tiles > 0) {
       const uint32_t idesc = idesc_f16(kRT, kTK, !INT8);
-      const uint32_t idesc_pv = idesc_f16(kRT, D, !INT8) | kBMajorN;
-      RingPos kr, vr;
-      int s_seg = 0, s_left = 0;               // segment of the next scores, its tiles to go
-      int p_seg = 0, p_left = 0, p_begin = 0;  // of the next product
-      // step x: scores of tile x, then the product of tile x - 1 (so S_0, S_1, P V_0, S_2, P V_1, ...)
-      for (int x = 0; x <= tiles; ++x) {
-        if (x < tiles) {
-          if (s_left == 0) {
-            if (!warp_wait(&bars->seg_full[s_seg % kMaxSegs], (s_seg / kMaxSegs) & 1, abort, a.err)) break;
-            s_left = bars->seg[s_seg % kMaxSegs].tiles;
-            if (!warp_wait(&bars->q_full, s_seg & 1, abort, a.err)) break;
-          }
-          if (!warp_wait(&bars->full[0][kr.slot], kr.phase, abort, a.err)) break;
-          tc_fence_after();
-          --s_left;
-          if (lead) {
-            const uint32_t k_s = sbase + C::kOffK + kr.slot * C::kTile;
-            const uint32_t d = tmem + static_cast<uint32_t>(x & 1) * kTK;
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t off = (kk >> 2) * C::kPiece + (kk & 3) * 32;
-              mma_ss(d, sdesc_sw128(sbase + off), sdesc_sw128(k_s + off), idesc, kk > 0);
-            }
-            mma_commit(&bars->s_full[x & 1]);
-            mma_commit(&bars->empty[0][kr.slot]);
-            if (s_left == 0) mma_commit(&bars->q_empty);
-          }
-          __syncwarp();
-          kr.advance(C::kSlotsK);
-          if (s_left == 0) ++s_seg;
+      RingPos kr, buf;
+      int seg = 0, left = 0;  // segment of the next scores, its tiles to go
+      for (int t = 0; t < tiles; ++t) {
+        if (left == 0) {
+          if (!warp_wait(&bars->seg_full[seg % kMaxSegs], (seg / kMaxSegs) & 1, abort, a.err)) break;
+          left = bars->seg[seg % kMaxSegs].tiles;
+          if (!warp_wait(&bars->q_full, seg & 1, abort, a.err)) break;
         }
-        if (x > 0) {
-          const int t = x - 1;
-          if (p_left == 0) {
-            p_left = bars->seg[p_seg % kMaxSegs].tiles;
-            // the segment before has been read out of O
-            if (p_seg > 0 && !warp_wait(&bars->epi, (p_seg - 1) & 1, abort, a.err)) break;
-          }
-          if (!warp_wait2(&bars->full[1][vr.slot], vr.phase, &bars->p_full[t & 1], (t >> 1) & 1, abort, a.err)) break;
-          tc_fence_after();
-          --p_left;
-          if (lead) {
-            const uint32_t v_s = sbase + C::kOffV + vr.slot * C::kTile;
-            const uint32_t p = tmem + static_cast<uint32_t>(t & 1) * kTK;  // two keys per column
-            const uint32_t o = tmem + kColO + static_cast<uint32_t>(t & 1) * 128;
-            const bool fresh = t - p_begin < 2;  // the group's first tile of the segment
+        if (!warp_wait2(&bars->full[0][kr.slot], kr.phase, &bars->s_free[buf.slot], buf.phase ^ 1, abort, a.err)) break;
+        tc_fence_after();
+        --left;
+        if (lead) {
+          const uint32_t k_s = sbase + C::kOffK + kr.slot * C::kTile;
+          const uint32_t d = tmem + buf.slot * kTK;
 #pragma unroll
-            for (int kk = 0; kk < kTK / 16; ++kk)
-              mma_ts(o, p + kk * 8, sdesc_mn_sw128(v_s + kk * 2048, C::kPiece), idesc_pv, !(fresh && kk == 0));
-            mma_commit(&bars->empty[1][vr.slot]);
-            if (p_left == 0) mma_commit(&bars->o_full);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * C::kPiece + (kk & 3) * 32;
+            mma_ss(d, sdesc_sw128(sbase + off), sdesc_sw128(k_s + off), idesc, kk > 0);
           }
-          __syncwarp();
-          vr.advance(C::kSlotsV);
-          if (p_left == 0) {
-            ++p_seg;
-            p_begin = t + 1;
-          }
+          mma_commit(&bars->s_full[buf.slot]);
+          mma_commit(&bars->empty[0][kr.slot]);
+          if (left == 0) mma_commit(&bars->q_empty);
         }
+        __syncwarp();
+        kr.advance(C::kSlotsK);
+        buf.advance(C::kBufs);
+        if (left == 0) ++seg;
       }
-      // every MMA has finished with shared and tensor memory before the CTA tears down
-      if (lead) {
-        mma_commit(&bars->drain);
-        drain_wait(&bars->drain, 0);
-      }
-      __syncwarp();
     }
+    if (warp == kWarpPv && tiles > 0) {
+      const uint32_t idesc = idesc_f16(kRT, D, !INT8) | kBMajorN;
+      RingPos vr, buf;
+      int seg = 0, left = 0, begin = 0;  // segment of the next product, its tiles to go, its first tile
+      for (int t = 0; t < tiles; ++t) {
+        if (left == 0) {
+          if (!warp_wait(&bars->seg_full[seg % kMaxSegs], (seg / kMaxSegs) & 1, abort, a.err)) break;
+          left = bars->seg[seg % kMaxSegs].tiles;
+          // the segment before has been read out of O
+          if (seg > 0 && !warp_wait(&bars->epi, (seg - 1) & 1, abort, a.err)) break;
+        }
+        if (!warp_wait2(&bars->full[1][vr.slot], vr.phase, &bars->p_full[buf.slot], buf.phase, abort, a.err)) break;
+        tc_fence_after();
+        --left;
+        if (lead) {
+          const uint32_t v_s = sbase + C::kOffV + vr.slot * C::kTile;
+          const uint32_t p = tmem + buf.slot * kTK;  // two keys per column
+          const uint32_t o = tmem + C::kColO + static_cast<uint32_t>(t & 1) * D;
+          const bool fresh = t - begin < 2;  // the group's first tile of the segment
+#pragma unroll
+          for (int kk = 0; kk < kTK / 16; ++kk)
+            mma_ts(o, p + kk * 8, sdesc_mn_sw128(v_s + kk * 2048, C::kPiece), idesc, !(fresh && kk == 0));
+          mma_commit(&bars->s_free[buf.slot]);
+          mma_commit(&bars->empty[1][vr.slot]);
+          if (left == 0) mma_commit(&bars->o_full);
+        }
+        __syncwarp();
+        vr.advance(C::kSlotsV);
+        buf.advance(C::kBufs);
+        if (left == 0) {
+          ++seg;
+          begin = t + 1;
+        }
+      }
+    }
+    if ((warp == kWarpS || warp == kWarpPv) && lead) {
+      // every MMA has finished with shared and tensor memory before the CTA tears down
+      mma_commit(&bars->drain[warp - kWarpS]);
+      drain_wait(&bars->drain[warp - kWarpS], 0);
+    }
+    __syncwarp();
   } else {
     // ======================= softmax =======================
+    registers<kRegsSoftmax>();
     const int grp = (warp - kWarpSm0) >> 2;  // tiles grp, grp + 2, ... of the run
     const int quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lane_bits = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t s_at = tmem + lane_bits + static_cast<uint32_t>(grp) * kTK;
-    const uint32_t o_at = tmem + lane_bits + kColO + static_cast<uint32_t>(grp) * 128;
+    const uint32_t o_at = tmem + lane_bits + C::kColO + static_cast<uint32_t>(grp) * D;
     const int g8 = lane >> 2, t4 = lane & 3;
     bool ok = true;
     int t = 0, ks_slot = 0, vs_slot = 0;
     uint32_t ks_phase = 0, vs_phase = 0;
+    RingPos buf;  // tile t's score buffer
     for (int seg = 0; ok && t < tiles; ++seg) {
       if (!warp_wait(&bars->seg_full[seg % kMaxSegs], (seg / kMaxSegs) & 1, abort, a.err)) break;
       const Seg& sg = bars->seg[seg % kMaxSegs];
@@ -667,7 +677,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool any = false;
       for (; t < end; ++t) {
         if ((t & 1) == grp) {
-          if (!warp_wait(&bars->s_full[grp], (t >> 1) & 1, abort, a.err)) { ok = false; break; }
+          if (!warp_wait(&bars->s_full[buf.slot], buf.phase, abort, a.err)) { ok = false; break; }
+          const uint32_t s_at = tmem + lane_bits + buf.slot * kTK;
           const float *ks = nullptr, *vs = nullptr;
           if constexpr (INT8) {
             if (!warp_wait2(&bars->ks_full[ks_slot], ks_phase, &bars->vs_full[vs_slot], vs_phase, abort, a.err)) { ok = false; break; }
@@ -675,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             vs = reinterpret_cast<const float*>(smem + C::kOffVS) + vs_slot * 2 * kTK + 2 * t4;
           }
           tc_fence_after();
-          // 16 rows at a time (their state is st[0], the other rows' st[1]: exchanged after each), 64 keys at a time
+          // 16 rows at a time: their state is st[0], the other rows' st[1], exchanged after each
 #pragma unroll 1
           for (int h = 0; h < 2; ++h) {
             const uint32_t half = static_cast<uint32_t>(16 * h) << 16;
@@ -688,49 +699,48 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const uint64_t fac2[2] = {f32x2_pack(__float_as_uint(fac[0]), __float_as_uint(fac[0])),
                                       f32x2_pack(__float_as_uint(fac[1]), __float_as_uint(fac[1]))};
-            const bool masked = __any_sync(0xffffffffu, min(st[0][0].left, st[0][1].left) < kTK);
-            // scores of 64 keys, scaled (INT8) and masked: register 4 i + 2 x + e is key 8 i + 2 t4 + e of row g8 + 8 x
-            auto load_scores = [&](int kb, uint32_t (&sv)[32]) {
-              tmem_ld_frag(s_at + half + 64 * kb, sv);
-              tmem_wait_ld();
-              if constexpr (INT8) {
+            // the rows' scores, scaled (INT8) and masked: register 4 i + 2 x + e is key 8 i + 2 t4 + e of row g8 + 8 x
+            uint32_t sv[64];
+            tmem_ld_frag(s_at + half, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
+            tmem_ld_frag(s_at + half + 64, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
+            tmem_wait_ld();
+            if constexpr (INT8) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  const uint64_t f = *reinterpret_cast<const uint64_t*>(ks + 64 * kb + 8 * i);
+              for (int i = 0; i < 16; ++i) {
+                const uint64_t f = *reinterpret_cast<const uint64_t*>(ks + 8 * i);
 #pragma unroll
-                  for (int x = 0; x < 2; ++x) {
-                    const uint64_t y = f32x2_mul(f32x2_pack(sv[4 * i + 2 * x], sv[4 * i + 2 * x + 1]), f);
-                    sv[4 * i + 2 * x] = static_cast<uint32_t>(y);
-                    sv[4 * i + 2 * x + 1] = static_cast<uint32_t>(y >> 32);
-                  }
+                for (int x = 0; x < 2; ++x) {
+                  const uint64_t y = f32x2_mul(f32x2_pack(sv[4 * i + 2 * x], sv[4 * i + 2 * x + 1]), f);
+                  sv[4 * i + 2 * x] = static_cast<uint32_t>(y);
+                  sv[4 * i + 2 * x + 1] = static_cast<uint32_t>(y >> 32);
                 }
               }
-              if (masked) {
+            }
+            if (__any_sync(0xffffffffu, min(st[0][0].left, st[0][1].left) < kTK)) {
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  if (64 * kb + 8 * (e >> 2) + 2 * t4 + (e & 1) >= st[0][(e >> 1) & 1].left) sv[e] = 0xff800000u;  // -inf
-              }
-            };
+              for (int e = 0; e < 64; ++e)
+                if (8 * (e >> 2) + 2 * t4 + (e & 1) >= st[0][(e >> 1) & 1].left) sv[e] = 0xff800000u;  // -inf
+            }
             // the rows' maxima; INT8: also log2 of their largest e^score times value scale
             float top[2] = {-INFINITY, -INFINITY}, topv[2] = {-INFINITY, -INFINITY};
-#pragma unroll 1
-            for (int kb = 0; kb < 2; ++kb) {
-              uint32_t sv[32];
-              load_scores(kb, sv);
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
+            for (int x = 0; x < 2; ++x) {
+              float other = -INFINITY;  // two chains
 #pragma unroll
-                for (int x = 0; x < 2; ++x)
-                  top[x] = fmaxf(fmaxf(top[x], __uint_as_float(sv[4 * i + 2 * x])), __uint_as_float(sv[4 * i + 2 * x + 1]));
-              if constexpr (INT8) {
+              for (int i = 0; i < 16; i += 2) {
+                top[x] = fmaxf(fmaxf(top[x], __uint_as_float(sv[4 * i + 2 * x])), __uint_as_float(sv[4 * i + 2 * x + 1]));
+                other = fmaxf(fmaxf(other, __uint_as_float(sv[4 * i + 4 + 2 * x])), __uint_as_float(sv[4 * i + 4 + 2 * x + 1]));
+              }
+              top[x] = fmaxf(top[x], other);
+            }
+            if constexpr (INT8) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  const uint64_t lv = *reinterpret_cast<const uint64_t*>(vs + kTK + 64 * kb + 8 * i);
+              for (int i = 0; i < 16; ++i) {
+                const uint64_t lv = *reinterpret_cast<const uint64_t*>(vs + kTK + 8 * i);
 #pragma unroll
-                  for (int x = 0; x < 2; ++x) {
-                    const uint64_t y = f32x2_fma(f32x2_pack(sv[4 * i + 2 * x], sv[4 * i + 2 * x + 1]), fac2[x], lv);
-                    topv[x] = fmaxf(fmaxf(topv[x], lo32(y)), hi32(y));
-                  }
+                for (int x = 0; x < 2; ++x) {
+                  const uint64_t y = f32x2_fma(f32x2_pack(sv[4 * i + 2 * x], sv[4 * i + 2 * x + 1]), fac2[x], lv);
+                  topv[x] = fmaxf(fmaxf(topv[x], lo32(y)), hi32(y));
                 }
               }
             }
@@ -768,7 +778,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               neg2[x] = f32x2_pack(__float_as_uint(-base), __float_as_uint(-base));
             }
             if (any && __any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
-              // O_grp holds this group's earlier products, all complete (see above)
+              // O_grp holds this group's earlier products: the last, P V of tile t - 2, has to be complete
+              if (!warp_wait(&bars->s_free[(t - 2) % C::kBufs], ((t - 2) / C::kBufs) & 1, abort, a.err)) { ok = false; break; }
+              tc_fence_after();
 #pragma unroll 1
               for (int i = 0; i < D; i += 64) {
                 uint32_t o[32];
@@ -780,27 +792,23 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
             // p = 2^(s fac - m), two keys per packed operation, its sum, and P, two keys a column, over the first half of
-            // the rows' S columns (read before: keys 64 .. 127 lie in the second half)
-#pragma unroll 1
-            for (int kb = 0; kb < 2; ++kb) {
-              uint32_t sv[32], pk[16];
-              load_scores(kb, sv);
+            // the rows' S columns
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                uint64_t w = 0;
-                if constexpr (INT8) w = *reinterpret_cast<const uint64_t*>(vs + 64 * kb + 8 * i);
+            for (int i = 0; i < 16; ++i) {
+              uint64_t w = 0;
+              if constexpr (INT8) w = *reinterpret_cast<const uint64_t*>(vs + 8 * i);
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                  const uint64_t e2 = f32x2_fma(f32x2_pack(sv[4 * i + 2 * x], sv[4 * i + 2 * x + 1]), fac2[x], neg2[x]);
-                  uint64_t p2 = f32x2_pack(__float_as_uint(ex2(lo32(e2))), __float_as_uint(ex2(hi32(e2))));
-                  l2[x] = f32x2_add(l2[x], p2);
-                  if constexpr (INT8)
-                    p2 = f32x2_mul(f32x2_mul(p2, w), f32x2_pack(__float_as_uint(lift[x]), __float_as_uint(lift[x])));
-                  pk[2 * i + x] = INT8 ? half2_bits(lo32(p2), hi32(p2)) : pack_bf16x2(lo32(p2), hi32(p2));
-                }
+              for (int x = 0; x < 2; ++x) {
+                const uint64_t e2 = f32x2_fma(f32x2_pack(sv[4 * i + 2 * x], sv[4 * i + 2 * x + 1]), fac2[x], neg2[x]);
+                uint64_t p2 = f32x2_pack(__float_as_uint(ex2(lo32(e2))), __float_as_uint(ex2(hi32(e2))));
+                l2[x] = f32x2_add(l2[x], p2);
+                if constexpr (INT8)
+                  p2 = f32x2_mul(f32x2_mul(p2, w), f32x2_pack(__float_as_uint(lift[x]), __float_as_uint(lift[x])));
+                sv[2 * i + x] = INT8 ? half2_bits(lo32(p2), hi32(p2)) : pack_bf16x2(lo32(p2), hi32(p2));
               }
-              tmem_st_pairs(s_at + half + 32 * kb, pk);
             }
+            tmem_st_pairs(s_at + half, *reinterpret_cast<uint32_t(*)[16]>(&sv[0]));
+            tmem_st_pairs(s_at + half + 32, *reinterpret_cast<uint32_t(*)[16]>(&sv[16]));
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
               st[0][x].l += lo32(l2[x]) + hi32(l2[x]);
@@ -809,12 +817,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               st[0][x] = other;
             }
           }
+          if (!ok) break;
           any = true;
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&bars->p_full[grp]);
+          if (lane == 0) mbar_arrive(&bars->p_full[buf.slot]);
         }
+        buf.advance(C::kBufs);
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -873,13 +883,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int e = 0; e < 16; ++e) v[e] = 0.f;
         uint32_t o[16];
         if (has0) {
-          tmem_ld16(tmem + lane_bits + kColO + col, o);
+          tmem_ld16(tmem + lane_bits + C::kColO + col, o);
           tmem_wait_ld();
 #pragma unroll
           for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(o[e]) * f0;
         }
         if (has1) {
-          tmem_ld16(tmem + lane_bits + kColO + 128 + col, o);
+          tmem_ld16(tmem + lane_bits + C::kColO + D + col, o);
           tmem_wait_ld();
 #pragma unroll
           for (int e = 0; e < 16; ++e) v[e] = fmaf(__uint_as_float(o[e]), f1, v[e]);
@@ -912,25 +922,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->epi);
     }
+    // ---- the run's parts of shared items ----
+    // By these warps alone: the others have given up registers that this needs.
+    constexpr int kJoiners = 256;
+    const int tid = threadIdx.x - kWarpSm0 * 32;
+    group_sync<1, kJoiners>();
+    if (tid == 0) bars->joins = a.fused && !*abort;
+    group_sync<1, kJoiners>();
+    if (bars->joins) {
+#pragma unroll 1
+      for (int x = 0; x < 2; ++x) {
+        if (!bars->has_part[x]) continue;
+        const Seg sg = bars->part[x];
+        const Span sp = span_of(sg.us, sg.ku, run.per);
+        if (!all_arrived<1, kJoiners>(a, sp, run.per, 2ll * blockIdx.x + x, tid)) continue;
+        const int rows = min(kRT, sg.s.n * a.G - sg.rt * kRT);
+        join_item<D, kRT, kJoiners>(a, sg.s, sp, run.per, sg.g, sg.rt, rows, reinterpret_cast<float*>(smem), tid);
+        clear_arrivals<kJoiners>(a, sp, run.per, tid);
+      }
+    }
   }
 
   tc_fence_before();
   __syncthreads();
-  if (warp == kWarpMma) {
+  if (warp == kWarpS) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
-  }
-  if (a.fused && !*abort) {
-#pragma unroll 1
-    for (int x = 0; x < 2; ++x) {
-      if (!bars->has_part[x]) continue;
-      const Seg sg = bars->part[x];
-      const Span sp = span_of(sg.us, sg.ku, run.per);
-      if (!all_arrived(a, sp, run.per, 2ll * blockIdx.x + x)) continue;
-      const int rows = min(kRT, sg.s.n * a.G - sg.rt * kRT);
-      join_item<D, kRT, kThreads>(a, sg.s, sp, run.per, sg.g, sg.rt, rows, reinterpret_cast<float*>(smem));
-      clear_arrivals(a, sp, run.per);
-    }
   }
 }
 
@@ -944,6 +961,9 @@ int launch(const Args& a, int runs, cudaStream_t st) {
   if (attrs_needed(attr, &bit)) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem)) != cudaSuccess)
       return MNW_E_CUDA;
+    // the roles' register split waits forever if the kernel was built for fewer
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess || fa.numRegs != kRegsBuilt) return MNW_E_CUDA;
     attrs_done(attr, bit);
   }
   // tiles of whole pages: the page divides the tile in pieces of 8 rows at least (a swizzle atom), or holds tiles

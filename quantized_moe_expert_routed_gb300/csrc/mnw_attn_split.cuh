@@ -237,33 +237,51 @@ __device__ __forceinline__ size_t out_row(const Args& a, const Seq& s, int g, in
   return static_cast<size_t>(s.start + i) * a.Hq + g * a.G + (ri - i * a.G);
 }
 
+// Barrier BAR among THREADS threads of the CTA (a multiple of 32).
+template <int BAR, int THREADS>
+__device__ __forceinline__ void group_sync() {
+  asm volatile("barrier.cta.sync %0, %1;" ::"n"(BAR), "n"(THREADS) : "memory");
+}
+template <int BAR, int THREADS>
+__device__ __forceinline__ bool group_and(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(x ? 1u : 0u), "n"(BAR), "n"(THREADS)
+      : "memory");
+  return r != 0;
+}
+
 // Marks this CTA's part of an item as written; true where every part of the
 // item is.  The mark is stored before the others are read, with a sequentially
 // consistent fence between, so the last CTA to mark sees all marks; CTAs that
 // mark at the same time may all see them, and then write the same result.  No
-// CTA waits.  All threads call, after writing the part.
-__device__ __forceinline__ bool all_arrived(const Args& a, const Span& sp, int per, long long mine) {
+// CTA waits.  THREADS threads call (`tid` their index, meeting at barrier BAR),
+// after writing the part.
+template <int BAR, int THREADS>
+__device__ __forceinline__ bool all_arrived(const Args& a, const Span& sp, int per, long long mine, int tid) {
   asm volatile("fence.acq_rel.gpu;" ::: "memory");  // each thread's share of the part, before the mark
-  __syncthreads();
-  if (threadIdx.x == 0) {
+  group_sync<BAR, THREADS>();
+  if (tid == 0) {
     asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(a.arrivals + mine), "l"(a.tag) : "memory");
     asm volatile("fence.sc.gpu;" ::: "memory");
   }
-  __syncthreads();
+  group_sync<BAR, THREADS>();
   bool all = true;
-  for (int c = sp.c0 + static_cast<int>(threadIdx.x); c <= sp.c1; c += blockDim.x) {
+  for (int c = sp.c0 + tid; c <= sp.c1; c += THREADS) {
     unsigned long long v;
     asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(a.arrivals + slot_of(sp, c, per)) : "memory");
     all = all && v == a.tag;
   }
-  const bool got = __syncthreads_and(all) != 0;
+  const bool got = group_and<BAR, THREADS>(all);
   if (got) asm volatile("fence.acq_rel.gpu;" ::: "memory");
   return got;
 }
 // After joining: a replayed graph brings the same number again.
-__device__ __forceinline__ void clear_arrivals(const Args& a, const Span& sp, int per) {
-  for (int c = sp.c0 + static_cast<int>(threadIdx.x); c <= sp.c1; c += blockDim.x)
-    a.arrivals[slot_of(sp, c, per)] = 0;
+template <int THREADS>
+__device__ __forceinline__ void clear_arrivals(const Args& a, const Span& sp, int per, int tid) {
+  for (int c = sp.c0 + tid; c <= sp.c1; c += THREADS) a.arrivals[slot_of(sp, c, per)] = 0;
 }
 
 // Adds the parts of one row and writes it.  D / 4 neighbouring lanes work on a
@@ -335,25 +353,25 @@ __device__ __forceinline__ void join_row(const Args& a, const Seq& s, const Span
   if (a.lse && j == 0) a.lse[row] = (M + log2f(L)) * kLn2;
 }
 
-// The rows [0, rows) of an item by the whole CTA.  Up to kFewParts parts (the
+// The rows [0, rows) of an item by THREADS threads (`tid` their index).  Up to kFewParts parts (the
 // usual case: runs are about as long as items), a row's loads all go out at
 // once, those of two rows together; one row after another, a latency each for
 // the maxima and the outputs, took 20 us for 128 rows.
 constexpr int kFewParts = 4;
 template <int D, int RT, int THREADS>
 __device__ __forceinline__ void join_item(const Args& a, const Seq& s, const Span& sp, int per, int g, int rt, int rows,
-                                          float* scratch) {
+                                          float* scratch, int tid) {
   constexpr int kCols = D / 4, kStep = THREADS / kCols;
-  const int col = (threadIdx.x % kCols) * 4;
+  const int col = (tid % kCols) * 4;
   const int parts = sp.c1 - sp.c0 + 1;
   if (parts > kFewParts) {
 #pragma unroll 1
-    for (int r = threadIdx.x / kCols; r < rows; r += kStep)
-      join_row<D, RT>(a, s, sp, per, g, rt, r, scratch + threadIdx.x / kCols * 2 * kJoinBatch);
+    for (int r = tid / kCols; r < rows; r += kStep)
+      join_row<D, RT>(a, s, sp, per, g, rt, r, scratch + tid / kCols * 2 * kJoinBatch);
     return;
   }
 #pragma unroll 2
-  for (int r = threadIdx.x / kCols; r < rows; r += kStep) {
+  for (int r = tid / kCols; r < rows; r += kStep) {
     float2 ml[kFewParts];
     float4 v[kFewParts];
 #pragma unroll
