@@ -515,9 +515,9 @@ __global__ void __launch_bounds__(WR* WK * 32) paged_attn_kernel(const Args a) {
       }
       if (!whole && a.fused) {
         const Span sp = span_of(item_first, cc.sh.ku, run.per);
-        if (all_arrived<0, kThreads>(a, sp, run.per, pslot, tid)) {
+        if (all_arrived(a, sp, run.per, pslot)) {
           join_item<D, kRT, kThreads>(a, cc.s, sp, run.per, cc.g, cc.rt, rows, reinterpret_cast<float*>(stage), tid);
-          clear_arrivals<kThreads>(a, sp, run.per, tid);
+          clear_arrivals(a, sp, run.per);
         }
       }
       item_first += cc.sh.ku;
@@ -581,7 +581,7 @@ inline bool plan(Args& a, int rt, int tk, int d, uint8_t* ws, int* runs, bool* s
   *runs = static_cast<int>(std::min<long long>(most, (units + kMinUnits - 1) / kMinUnits));
   *shared = kt > 1;  // items of one tile are never shared
   const long long rows = std::min<long long>(rt, static_cast<long long>(a.bt.T) * a.G);
-  a.fused = rows * ((*runs + items - 1) / items) <= kFusedRows;
+  a.fused = rt != kBlockRows && rows * ((*runs + items - 1) / items) <= kFusedRows;
   a.tag = next_tag();
   return true;
 }
@@ -619,7 +619,7 @@ int launch_rows(Args& a, uint8_t* ws, int rt, cudaStream_t st) {
   bool shared;
   if (!plan(a, kBlockRows, kBlockKeys, D, ws, &runs, &shared)) return MNW_E_UNSUPPORTED;
   const int rc = launch_block(a, D, INT8, runs, st);
-  return rc != MNW_OK || a.fused || !shared ? rc : launch_join<D, kBlockRows, kBlockKeys>(a, st);
+  return rc != MNW_OK || !shared ? rc : launch_join<D, kBlockRows, kBlockKeys>(a, st);
 }
 
 }  // namespace pattn

@@ -91,7 +91,6 @@ struct BCfg {
 struct Seg {
   int tiles, kt0;       // tiles of the run, from key tile kt0
   int g, rt, whole;     // kv head, row tile; whether it is the item whole
-  int us, ku;           // the item's units
   Seq s;
 };
 
@@ -109,8 +108,6 @@ struct Bars {
   float qfac[4][kRT];                   // [segment % 4] INT8: the query rows' powers of two
   int st_any[2][2];                     // [segment parity][group]: whether the group had a tile
   Seg seg[kMaxSegs];
-  Seg part[2];                          // the run's parts of shared items: the one that continues an item, that begins one
-  int has_part[2], joins;
   uint32_t tmem_base;
   int abort;
 };
@@ -119,7 +116,7 @@ struct Bars {
 // they are free) or fewer (N < 0).  The kernel is built for kRegsBuilt, and the
 // split must not pass that in sum.  Once a role: a second change would have to
 // meet the whole warpgroup first, and may wait for a contiguous range for ever.
-constexpr int kRegsBuilt = 128, kRegsLoad = 112, kRegsMma = 64, kRegsSoftmax = 168;
+constexpr int kRegsBuilt = 128, kRegsLoad = 96, kRegsMma = 64, kRegsSoftmax = 176;
 static_assert(kRegsLoad + kRegsMma + 2 * kRegsSoftmax == 4 * kRegsBuilt);
 template <int N>
 __device__ __forceinline__ void registers() {
@@ -266,7 +263,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars->raw_full[x], 1);
       mbar_init(&bars->raw_empty[x], 2);
       mbar_init(&bars->drain[x], 1);
-      bars->has_part[x] = 0;
     }
     mbar_init(&bars->q_full, kLoadWarps);
     mbar_init(&bars->q_empty, 1);
@@ -316,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // whole pages: page `lane` of a tile, `span` keys each
     const int span = min(a.page_size, kTK), pieces = kTK / span;
     bool ok = tiles > 0;
-    int seg = -1, us = run.u0 - kc.kt;  // segment of the keys; first unit of kc's item
+    int seg = -1;
     RingPos ring;
     auto table_at = [&](int seq, int p) {
       return __ldg(a.bt.block_table + static_cast<size_t>(seq) * a.bt.max_pages + paged::quotient(p, a.page_div));
@@ -370,8 +366,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         d.g = kc.g;
         d.rt = kc.rt;
         d.whole = kc.kt == 0 && d.tiles == kc.sh.kt;
-        d.us = us;
-        d.ku = kc.sh.ku;
         d.s = kc.s;
         bars->seg[seg % kMaxSegs] = d;
         mbar_arrive(&bars->seg_full[seg % kMaxSegs]);
@@ -381,11 +375,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr int kQC = D / 8, kQR = 32 / kQC;
       const int rows = min(kRT, kc.s.n * a.G - kc.rt * kRT);
       const int c = lane % kQC;
-#pragma unroll 1
-      for (int r0 = warp * 32; r0 < warp * 32 + 32; r0 += 8 * kQR) {
-        uint4 w[8];
+      {
+        const int r0 = warp * 32;
+        uint4 w[kQC];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < kQC; ++i) {
           const int r = r0 + i * kQR + lane / kQC;
           const int ri = kc.rt * kRT + r;
           const int tok = static_cast<int>(paged::quotient(ri, a.g_div)), hh = ri - tok * a.G;
@@ -395,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                    static_cast<long long>(kc.g * a.G + hh) * D + c * 8);
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < kQC; ++i) {
           const int r = r0 + i * kQR + lane / kQC;
           if constexpr (INT8) {
             const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
@@ -420,10 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       return true;
     };
     auto step = [&]() {
-      if (++kc.kt == kc.sh.kt) {
-        us += kc.sh.ku;
-        kc.next_item(a, run.pad);
-      }
+      if (++kc.kt == kc.sh.kt) kc.next_item(a, run.pad);
     };
     if (ok) peek();
     if constexpr (!INT8) {
@@ -699,6 +690,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const uint64_t fac2[2] = {f32x2_pack(__float_as_uint(fac[0]), __float_as_uint(fac[0])),
                                       f32x2_pack(__float_as_uint(fac[1]), __float_as_uint(fac[1]))};
+            // scales are loaded in one go ahead of their use: a load before each use waited for it 48 times a half
+            uint64_t f[16];
+            if constexpr (INT8) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) f[i] = *reinterpret_cast<const uint64_t*>(ks + 8 * i);
+            }
             // the rows' scores, scaled (INT8) and masked: register 4 i + 2 x + e is key 8 i + 2 t4 + e of row g8 + 8 x
             uint32_t sv[64];
             tmem_ld_frag(s_at + half, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
@@ -707,10 +704,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if constexpr (INT8) {
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
-                const uint64_t f = *reinterpret_cast<const uint64_t*>(ks + 8 * i);
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                  const uint64_t y = f32x2_mul(f32x2_pack(sv[4 * i + 2 * x], sv[4 * i + 2 * x + 1]), f);
+                  const uint64_t y = f32x2_mul(f32x2_pack(sv[4 * i + 2 * x], sv[4 * i + 2 * x + 1]), f[i]);
                   sv[4 * i + 2 * x] = static_cast<uint32_t>(y);
                   sv[4 * i + 2 * x + 1] = static_cast<uint32_t>(y >> 32);
                 }
@@ -735,11 +731,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if constexpr (INT8) {
 #pragma unroll
+              for (int i = 0; i < 16; ++i) f[i] = *reinterpret_cast<const uint64_t*>(vs + kTK + 8 * i);
+#pragma unroll
               for (int i = 0; i < 16; ++i) {
-                const uint64_t lv = *reinterpret_cast<const uint64_t*>(vs + kTK + 8 * i);
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                  const uint64_t y = f32x2_fma(f32x2_pack(sv[4 * i + 2 * x], sv[4 * i + 2 * x + 1]), fac2[x], lv);
+                  const uint64_t y = f32x2_fma(f32x2_pack(sv[4 * i + 2 * x], sv[4 * i + 2 * x + 1]), fac2[x], f[i]);
                   topv[x] = fmaxf(fmaxf(topv[x], lo32(y)), hi32(y));
                 }
               }
@@ -791,19 +788,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_st_frag(o_at + half + i, o);
               }
             }
+            if constexpr (INT8) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) f[i] = *reinterpret_cast<const uint64_t*>(vs + 8 * i);
+            }
             // p = 2^(s fac - m), two keys per packed operation, its sum, and P, two keys a column, over the first half of
             // the rows' S columns
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              uint64_t w = 0;
-              if constexpr (INT8) w = *reinterpret_cast<const uint64_t*>(vs + 8 * i);
 #pragma unroll
               for (int x = 0; x < 2; ++x) {
                 const uint64_t e2 = f32x2_fma(f32x2_pack(sv[4 * i + 2 * x], sv[4 * i + 2 * x + 1]), fac2[x], neg2[x]);
                 uint64_t p2 = f32x2_pack(__float_as_uint(ex2(lo32(e2))), __float_as_uint(ex2(hi32(e2))));
                 l2[x] = f32x2_add(l2[x], p2);
                 if constexpr (INT8)
-                  p2 = f32x2_mul(f32x2_mul(p2, w), f32x2_pack(__float_as_uint(lift[x]), __float_as_uint(lift[x])));
+                  p2 = f32x2_mul(f32x2_mul(p2, f[i]), f32x2_pack(__float_as_uint(lift[x]), __float_as_uint(lift[x])));
                 sv[2 * i + x] = INT8 ? half2_bits(lo32(p2), hi32(p2)) : pack_bf16x2(lo32(p2), hi32(p2));
               }
             }
@@ -872,39 +871,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float f0 = ex2(gm0 - bs + bars->st_u[par][0][r]) * inv, f1 = ex2(gm1 - bs + bars->st_u[par][1][r]) * inv;
       const bool has0 = bars->st_any[par][0] != 0, has1 = bars->st_any[par][1] != 0;
       const size_t row = out_row<kRT>(a, sg.s, sg.g, sg.rt, min(r, rows - 1));
-      const int which = sg.kt0 > 0 ? 0 : 1;
-      const long long pslot = 2ll * blockIdx.x + which;
-      // group g writes columns g D/2 ... of its quarter's rows, 16 at a time
+      const long long pslot = 2ll * blockIdx.x + (sg.kt0 > 0 ? 0 : 1);
+      // group g writes columns g D/2 ... of its quarter's rows, 32 at a time
 #pragma unroll 1
-      for (int i = 0; i < D / 2; i += 16) {
+      for (int i = 0; i < D / 2; i += 32) {
         const int col = grp * (D / 2) + i;
-        float v[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = 0.f;
-        uint32_t o[16];
+        float v[32];
+        uint32_t o[32];
         if (has0) {
-          tmem_ld16(tmem + lane_bits + C::kColO + col, o);
+          tmem_ld32(tmem + lane_bits + C::kColO + col, o);
           tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(o[e]) * f0;
         }
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = has0 ? __uint_as_float(o[e]) * f0 : 0.f;
         if (has1) {
-          tmem_ld16(tmem + lane_bits + C::kColO + D + col, o);
+          tmem_ld32(tmem + lane_bits + C::kColO + D + col, o);
           tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] = fmaf(__uint_as_float(o[e]), f1, v[e]);
+          for (int e = 0; e < 32; ++e) v[e] = fmaf(__uint_as_float(o[e]), f1, v[e]);
         }
         if (r < rows) {
           if (whole) {
             uint4* dst = reinterpret_cast<uint4*>(a.out + row * D + col);
-            dst[0] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                                pack_bf16x2(v[6], v[7]));
-            dst[1] = make_uint4(pack_bf16x2(v[8], v[9]), pack_bf16x2(v[10], v[11]), pack_bf16x2(v[12], v[13]),
-                                pack_bf16x2(v[14], v[15]));
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              dst[e] = make_uint4(pack_bf16x2(v[8 * e], v[8 * e + 1]), pack_bf16x2(v[8 * e + 2], v[8 * e + 3]),
+                                  pack_bf16x2(v[8 * e + 4], v[8 * e + 5]), pack_bf16x2(v[8 * e + 6], v[8 * e + 7]));
           } else {
             float4* dst = reinterpret_cast<float4*>(a.part_o + (pslot * kRT + r) * D + col);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) __stcg(dst + e, make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]));
+            for (int e = 0; e < 8; ++e) __stcg(dst + e, make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]));
           }
         }
       }
@@ -914,32 +910,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         else if (a.lse)
           a.lse[row] = (M + log2f(L)) * kLn2;
       }
-      if (!whole && warp == kWarpSm0 && lane == 0) {
-        bars->part[which] = sg;
-        bars->has_part[which] = 1;
-      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->epi);
-    }
-    // ---- the run's parts of shared items ----
-    // By these warps alone: the others have given up registers that this needs.
-    constexpr int kJoiners = 256;
-    const int tid = threadIdx.x - kWarpSm0 * 32;
-    group_sync<1, kJoiners>();
-    if (tid == 0) bars->joins = a.fused && !*abort;
-    group_sync<1, kJoiners>();
-    if (bars->joins) {
-#pragma unroll 1
-      for (int x = 0; x < 2; ++x) {
-        if (!bars->has_part[x]) continue;
-        const Seg sg = bars->part[x];
-        const Span sp = span_of(sg.us, sg.ku, run.per);
-        if (!all_arrived<1, kJoiners>(a, sp, run.per, 2ll * blockIdx.x + x, tid)) continue;
-        const int rows = min(kRT, sg.s.n * a.G - sg.rt * kRT);
-        join_item<D, kRT, kJoiners>(a, sg.s, sp, run.per, sg.g, sg.rt, rows, reinterpret_cast<float*>(smem), tid);
-        clear_arrivals<kJoiners>(a, sp, run.per, tid);
-      }
     }
   }
 

@@ -237,51 +237,32 @@ __device__ __forceinline__ size_t out_row(const Args& a, const Seq& s, int g, in
   return static_cast<size_t>(s.start + i) * a.Hq + g * a.G + (ri - i * a.G);
 }
 
-// Barrier BAR among THREADS threads of the CTA (a multiple of 32).
-template <int BAR, int THREADS>
-__device__ __forceinline__ void group_sync() {
-  asm volatile("barrier.cta.sync %0, %1;" ::"n"(BAR), "n"(THREADS) : "memory");
-}
-template <int BAR, int THREADS>
-__device__ __forceinline__ bool group_and(bool x) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(x ? 1u : 0u), "n"(BAR), "n"(THREADS)
-      : "memory");
-  return r != 0;
-}
-
 // Marks this CTA's part of an item as written; true where every part of the
 // item is.  The mark is stored before the others are read, with a sequentially
 // consistent fence between, so the last CTA to mark sees all marks; CTAs that
 // mark at the same time may all see them, and then write the same result.  No
-// CTA waits.  THREADS threads call (`tid` their index, meeting at barrier BAR),
-// after writing the part.
-template <int BAR, int THREADS>
-__device__ __forceinline__ bool all_arrived(const Args& a, const Span& sp, int per, long long mine, int tid) {
+// CTA waits.  All threads call, after writing the part.
+__device__ __forceinline__ bool all_arrived(const Args& a, const Span& sp, int per, long long mine) {
   asm volatile("fence.acq_rel.gpu;" ::: "memory");  // each thread's share of the part, before the mark
-  group_sync<BAR, THREADS>();
-  if (tid == 0) {
+  __syncthreads();
+  if (threadIdx.x == 0) {
     asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(a.arrivals + mine), "l"(a.tag) : "memory");
     asm volatile("fence.sc.gpu;" ::: "memory");
   }
-  group_sync<BAR, THREADS>();
+  __syncthreads();
   bool all = true;
-  for (int c = sp.c0 + tid; c <= sp.c1; c += THREADS) {
+  for (int c = sp.c0 + static_cast<int>(threadIdx.x); c <= sp.c1; c += blockDim.x) {
     unsigned long long v;
     asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(a.arrivals + slot_of(sp, c, per)) : "memory");
     all = all && v == a.tag;
   }
-  const bool got = group_and<BAR, THREADS>(all);
+  const bool got = __syncthreads_and(all) != 0;
   if (got) asm volatile("fence.acq_rel.gpu;" ::: "memory");
   return got;
 }
 // After joining: a replayed graph brings the same number again.
-template <int THREADS>
-__device__ __forceinline__ void clear_arrivals(const Args& a, const Span& sp, int per, int tid) {
-  for (int c = sp.c0 + tid; c <= sp.c1; c += THREADS) a.arrivals[slot_of(sp, c, per)] = 0;
+__device__ __forceinline__ void clear_arrivals(const Args& a, const Span& sp, int per) {
+  for (int c = sp.c0 + static_cast<int>(threadIdx.x); c <= sp.c1; c += blockDim.x) a.arrivals[slot_of(sp, c, per)] = 0;
 }
 
 // Adds the parts of one row and writes it.  D / 4 neighbouring lanes work on a
@@ -353,56 +334,56 @@ __device__ __forceinline__ void join_row(const Args& a, const Seq& s, const Span
   if (a.lse && j == 0) a.lse[row] = (M + log2f(L)) * kLn2;
 }
 
-// The rows [0, rows) of an item by THREADS threads (`tid` their index).  Up to kFewParts parts (the
-// usual case: runs are about as long as items), a row's loads all go out at
-// once, those of two rows together; one row after another, a latency each for
-// the maxima and the outputs, took 20 us for 128 rows.
+// As join_row for at most kFewParts parts (the usual case: runs are about as
+// long as items): all loads go out at once, without a maximum first.
 constexpr int kFewParts = 4;
+template <int D, int RT>
+__device__ __forceinline__ void join_few(const Args& a, const Seq& s, const Span& sp, int per, int g, int rt, int r, int col) {
+  float2 ml[kFewParts];
+  float4 v[kFewParts];
+#pragma unroll
+  for (int p = 0; p < kFewParts; ++p) {
+    ml[p] = make_float2(-INFINITY, 0.f);
+    v[p] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (sp.c0 + p <= sp.c1) {
+      const long long at = slot_of(sp, sp.c0 + p, per) * RT + r;
+      ml[p] = __ldcg(a.part_ml + at);
+      v[p] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D + col));
+    }
+  }
+  float M = -INFINITY, L = 0.f;
+#pragma unroll
+  for (int p = 0; p < kFewParts; ++p) M = fmaxf(M, ml[p].x);
+  const float base = M == -INFINITY ? 0.f : M;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int p = 0; p < kFewParts; ++p) {
+    const float f = ex2(ml[p].x - base);
+    L += f * ml[p].y;
+    acc.x = fmaf(f, v[p].x, acc.x);
+    acc.y = fmaf(f, v[p].y, acc.y);
+    acc.z = fmaf(f, v[p].z, acc.z);
+    acc.w = fmaf(f, v[p].w, acc.w);
+  }
+  const size_t row = out_row<RT>(a, s, g, rt, r);
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  *reinterpret_cast<uint2*>(a.out + row * D + col) =
+      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  if (a.lse && col == 0) a.lse[row] = (M + log2f(L)) * kLn2;
+}
+
+// The rows [0, rows) of an item by THREADS threads (`tid` their index).
 template <int D, int RT, int THREADS>
 __device__ __forceinline__ void join_item(const Args& a, const Seq& s, const Span& sp, int per, int g, int rt, int rows,
                                           float* scratch, int tid) {
-  constexpr int kCols = D / 4, kStep = THREADS / kCols;
-  const int col = (tid % kCols) * 4;
-  const int parts = sp.c1 - sp.c0 + 1;
-  if (parts > kFewParts) {
+  constexpr int kCols = D / 4;
+  const bool few = sp.c1 - sp.c0 < kFewParts;
 #pragma unroll 1
-    for (int r = tid / kCols; r < rows; r += kStep)
+  for (int r = tid / kCols; r < rows; r += THREADS / kCols) {
+    if (few)
+      join_few<D, RT>(a, s, sp, per, g, rt, r, (tid % kCols) * 4);
+    else
       join_row<D, RT>(a, s, sp, per, g, rt, r, scratch + tid / kCols * 2 * kJoinBatch);
-    return;
-  }
-#pragma unroll 2
-  for (int r = tid / kCols; r < rows; r += kStep) {
-    float2 ml[kFewParts];
-    float4 v[kFewParts];
-#pragma unroll
-    for (int p = 0; p < kFewParts; ++p) {
-      ml[p] = make_float2(-INFINITY, 0.f);
-      v[p] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (p < parts) {
-        const long long at = slot_of(sp, sp.c0 + p, per) * RT + r;
-        ml[p] = __ldcg(a.part_ml + at);
-        v[p] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D + col));
-      }
-    }
-    float M = -INFINITY, L = 0.f;
-#pragma unroll
-    for (int p = 0; p < kFewParts; ++p) M = fmaxf(M, ml[p].x);
-    const float base = M == -INFINITY ? 0.f : M;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int p = 0; p < kFewParts; ++p) {
-      const float f = ex2(ml[p].x - base);
-      L += f * ml[p].y;
-      acc.x = fmaf(f, v[p].x, acc.x);
-      acc.y = fmaf(f, v[p].y, acc.y);
-      acc.z = fmaf(f, v[p].z, acc.z);
-      acc.w = fmaf(f, v[p].w, acc.w);
-    }
-    const size_t row = out_row<RT>(a, s, g, rt, r);
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    *reinterpret_cast<uint2*>(a.out + row * D + col) =
-        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-    if (a.lse && col == 0) a.lse[row] = (M + log2f(L)) * kLn2;
   }
 }
 
@@ -439,7 +420,10 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const Args a) 
   const int rt = ri / RT;
   const Span sp = span_of(a.starts[b] + (g * sh.rt + rt) * sh.ku, sh.ku, per);
   if (sp.c0 == sp.c1) return;
-  join_row<D, RT>(a, s, sp, per, g, rt, ri - rt * RT, scratch[rr]);
+  if (sp.c1 - sp.c0 < kFewParts)
+    join_few<D, RT>(a, s, sp, per, g, rt, ri - rt * RT, threadIdx.x % (D / 4) * 4);
+  else
+    join_row<D, RT>(a, s, sp, per, g, rt, ri - rt * RT, scratch[rr]);
 }
 
 }  // namespace pattn
