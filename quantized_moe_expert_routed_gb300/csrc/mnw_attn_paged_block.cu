@@ -148,26 +148,23 @@ __device__ __forceinline__ void wait_copies() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 // Waits poll without a suspend time: the library's bounded_wait() lets a
-// waiting thread sleep, and with a dozen hand-overs a tile the late wake-ups
-// were most of the kernel's time.  Bounded like it: gives up when *abort is
-// set, or after kWaitLimitNs, which sets it and reports.  The slow side is a call;
-// inlined at every wait it would be a good part of the kernel's code.
-__device__ __forceinline__ bool slow_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* err) {
-  const uint64_t t0 = globaltimer();
-  for (uint32_t it = 1;; ++it) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((it & 255u) == 0) {
-      if (*abort) return false;
-      if (globaltimer() - t0 > kWaitLimitNs) {
-        *abort = 1;
-        if (err) atomicOr(err, MNW_DEVERR_TIMEOUT);
-        return false;
-      }
+// waiting thread sleep, which with a dozen hand-overs a tile costs.  They are
+// bounded by a count of polls (of a hundred cycles or so: about a second), after
+// which, or when another warp gave up, *abort is set and the wait fails.  Short,
+// because it is inlined at every wait of the roles, and the kernel's code has to
+// stay below the instruction cache's size: at 142 KB the INT8 form stalled for
+// thousands of cycles at a time.
+constexpr uint32_t kMaxPolls = 1u << 24;
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* err) {
+  uint32_t polls = 0;
+  while (!mbar_try_wait(bar, parity)) {
+    if ((++polls & 1023u) == 0 && (polls >= kMaxPolls || *abort)) {
+      if (!*abort && err) atomicOr(err, MNW_DEVERR_TIMEOUT);
+      *abort = 1;
+      return false;
     }
   }
-}
-__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* err) {
-  return mbar_try_wait(bar, parity) || slow_wait(bar, parity, abort, err);
+  return true;
 }
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* err) {
   int ok = 1;
@@ -341,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const long long mine = pg >= 0 ? pg * a.page_bytes + static_cast<long long>(at) * (kCh * 16) : -1;
         const int c = lane % kCh;
-#pragma unroll 4
+#pragma unroll 2
         for (int i = 0; i < 32 / kRows; ++i) {
           const int r = i * kRows + lane / kCh;
           const long long off = __shfl_sync(0xffffffffu, mine, r);
@@ -375,11 +372,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr int kQC = D / 8, kQR = 32 / kQC;
       const int rows = min(kRT, kc.s.n * a.G - kc.rt * kRT);
       const int c = lane % kQC;
-      {
-        const int r0 = warp * 32;
-        uint4 w[kQC];
+#pragma unroll 1
+      for (int r0 = warp * 32; r0 < warp * 32 + 32; r0 += 8 * kQR) {
+        uint4 w[8];
 #pragma unroll
-        for (int i = 0; i < kQC; ++i) {
+        for (int i = 0; i < 8; ++i) {
           const int r = r0 + i * kQR + lane / kQC;
           const int ri = kc.rt * kRT + r;
           const int tok = static_cast<int>(paged::quotient(ri, a.g_div)), hh = ri - tok * a.G;
@@ -389,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                    static_cast<long long>(kc.g * a.G + hh) * D + c * 8);
         }
 #pragma unroll
-        for (int i = 0; i < kQC; ++i) {
+        for (int i = 0; i < 8; ++i) {
           const int r = r0 + i * kQR + lane / kQC;
           if constexpr (INT8) {
             const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
@@ -502,59 +499,71 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (++sc_issue == sc_slots) sc_issue = 0;
         return true;
       };
-      if (ok) ok = issue(0);
-      bool bulk_out = ok && !landing_rows;  // a bulk copy is under way
-      for (int t = 0; ok && t < tiles; ++t) {
-        if ((t == 0 || kc.kt == 0) && !begin_segment(tiles - t)) { ok = false; break; }
-        // the codes land and are taken into registers
-        if (landing_rows) {
-          wait_copies<0>();
+      bool bulk_out = false;  // a bulk copy is under way
+      constexpr int kW = 4 * kCh, kOC = D / 8;  // 64 rows, 8 codes a lane: one 16-byte chunk of the operand row
+      // step t: tile t lands and is converted in two halves, each by way of registers; the copies of tile t + 1 go out as
+      // soon as the second is there
+      for (int t = -1; ok && t < tiles; ++t) {
+        if (t >= 0) {
+          if (landing_rows) {
+            wait_copies<0>();
+            __syncwarp();
+          } else {
+            if (!warp_wait(raw_full, raw_phase, abort, a.err)) { ok = false; break; }
+            raw_phase ^= 1;
+            bulk_out = false;
+          }
+          if (!warp_wait(&empty[ring.slot], ring.phase ^ 1, abort, a.err)) { ok = false; break; }
+        }
+        uint8_t* op = smem + ring_at + ring.slot * C::kTile + lw * 64 * 128;
+        const uint8_t* raw = smem + raw_at + lw * 64 * D + lane * 8;
+#pragma unroll 1
+        for (int part = t < 0 ? 1 : 0; part < 2; ++part) {
+          uint2 w[kW / 2];
+          if (t >= 0) {
+#pragma unroll
+            for (int i = 0; i < kW / 2; ++i) w[i] = *reinterpret_cast<const uint2*>(raw + part * (32 * D) + i * 256);
+          }
+          if (part == 1) {
+            if (t >= 0) {
+              __syncwarp();
+              if (lane == 0) mbar_arrive(raw_empty);
+              step();
+              if (t + 1 < tiles) peek();
+            }
+            if (t + 1 < tiles) {
+              if (!issue(t + 1)) { ok = false; break; }
+              bulk_out = !landing_rows;
+            }
+          }
+          if (t >= 0) {
+#pragma unroll
+            for (int i = 0; i < kW / 2; ++i) {
+              const int row = part * 32 + i * (32 / kOC) + lane / kOC, c = lane % kOC;  // of the warp's 64
+              const uint32_t x = w[i].x ^ 0x80808080u, y = w[i].y ^ 0x80808080u;
+              *reinterpret_cast<uint4*>(op + (c >> 3) * C::kPiece + row * 128 + (((c & 7) ^ (row & 7)) << 4)) =
+                  make_uint4(codes_lo(x), codes_hi(x), codes_lo(y), codes_hi(y));
+            }
+          }
+        }
+        if (!ok) break;
+        if (t >= 0) {
+          if (values) {
+            float* sc = reinterpret_cast<float*>(smem + scales_at(sc_now)) + lw * 64 + lane;
+            sc[kTK] = __log2f(sc[0]);
+            sc[kTK + 32] = __log2f(sc[32]);
+          }
+          fence_proxy_async_smem();
           __syncwarp();
-        } else {
-          if (!warp_wait(raw_full, raw_phase, abort, a.err)) { ok = false; break; }
-          raw_phase ^= 1;
-          bulk_out = false;
+          if (lane == 0) {
+            mbar_arrive(&full[ring.slot]);
+            mbar_arrive(values ? &bars->vs_full[sc_now] : &bars->ks_full[sc_now]);
+          }
+          ring.advance(ring_slots);
+          if (++sc_now == sc_slots) sc_now = 0;
         }
-        constexpr int kW = 2 * kCh;  // 64 rows
-        uint4 w[kW];
-#pragma unroll
-        for (int i = 0; i < kW; ++i) w[i] = *reinterpret_cast<const uint4*>(smem + raw_at + lw * 64 * D + (i * 32 + lane) * 16);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(raw_empty);
-        // the next tile's copies go out
-        step();
-        if (t + 1 < tiles) {
-          peek();
-          if (!issue(t + 1)) { ok = false; break; }
-          bulk_out = !landing_rows;
-        }
-        // codes -> FP16 operand tile
-        if (!warp_wait(&empty[ring.slot], ring.phase ^ 1, abort, a.err)) { ok = false; break; }
-        uint8_t* op = smem + ring_at + ring.slot * C::kTile;
-#pragma unroll
-        for (int i = 0; i < kW; ++i) {
-          const int row = lw * 64 + i * kRows + lane / kCh, c = lane % kCh;
-          const uint32_t ww[4] = {w[i].x ^ 0x80808080u, w[i].y ^ 0x80808080u, w[i].z ^ 0x80808080u, w[i].w ^ 0x80808080u};
-          const uint4 h0 = make_uint4(codes_lo(ww[0]), codes_hi(ww[0]), codes_lo(ww[1]), codes_hi(ww[1]));
-          const uint4 h1 = make_uint4(codes_lo(ww[2]), codes_hi(ww[2]), codes_lo(ww[3]), codes_hi(ww[3]));
-          uint8_t* piece = op + (c >> 2) * C::kPiece + row * 128;
-          const int o = (2 * c) & 7, first = (c >> 2) & 1;  // the two pieces' lanes start on different banks
-          *reinterpret_cast<uint4*>(piece + (((o + first) ^ (row & 7)) << 4)) = first ? h1 : h0;
-          *reinterpret_cast<uint4*>(piece + (((o + (first ^ 1)) ^ (row & 7)) << 4)) = first ? h0 : h1;
-        }
-        if (values) {
-          float* sc = reinterpret_cast<float*>(smem + scales_at(sc_now)) + lw * 64 + lane;
-          sc[kTK] = __log2f(sc[0]);
-          sc[kTK + 32] = __log2f(sc[32]);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&full[ring.slot]);
-          mbar_arrive(values ? &bars->vs_full[sc_now] : &bars->ks_full[sc_now]);
-        }
-        ring.advance(ring_slots);
-        if (++sc_now == sc_slots) sc_now = 0;
+        // the next tile's segment, once this tile is given on (its queries wait for the products of the segment before)
+        if (t + 1 < tiles && (t < 0 || kc.kt == 0)) ok = begin_segment(tiles - (t + 1));
       }
       wait_copies<0>();
       if (bulk_out && lw == 0) drain_wait(raw_full, raw_phase);  // (an abort) the copy lands before the CTA exits
