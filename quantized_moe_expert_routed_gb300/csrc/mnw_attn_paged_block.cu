@@ -372,37 +372,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr int kQC = D / 8, kQR = 32 / kQC;
       const int rows = min(kRT, kc.s.n * a.G - kc.rt * kRT);
       const int c = lane % kQC;
-#pragma unroll 1
-      for (int r0 = warp * 32; r0 < warp * 32 + 32; r0 += 8 * kQR) {
-        uint4 w[8];
+      auto chunk = [&](int r) { return (c >> 3) * C::kPiece + r * 128 + (((c & 7) ^ (r & 7)) << 4); };
+#pragma unroll 4
+      for (int r = warp * 32 + lane / kQC; r < warp * 32 + 32; r += kQR) {
+        const int ri = kc.rt * kRT + (r < rows ? r : 0);
+        const int tok = static_cast<int>(paged::quotient(ri, a.g_div)), hh = ri - tok * a.G;
+        cp16(sbase + chunk(r), a.q + static_cast<long long>(kc.s.start + tok) * a.q_stride +
+                                   static_cast<long long>(kc.g * a.G + hh) * D + c * 8,
+             r < rows ? 16u : 0u);
+      }
+      commit_copies();
+      wait_copies<0>();
+      if constexpr (INT8) {  // in place: FP16 times a power of two
+#pragma unroll 2
+        for (int r = warp * 32 + lane / kQC; r < warp * 32 + 32; r += kQR) {
+          uint4 w = *reinterpret_cast<const uint4*>(smem + chunk(r));
+          const uint32_t hi = max(max(w.x & 0x7FFF0000u, w.y & 0x7FFF0000u), max(w.z & 0x7FFF0000u, w.w & 0x7FFF0000u));
+          const uint32_t lo = max(max(w.x & 0x7FFFu, w.y & 0x7FFFu), max(w.z & 0x7FFFu, w.w & 0x7FFFu));
+          uint32_t mag = max(hi >> 16, lo);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = r0 + i * kQR + lane / kQC;
-          const int ri = kc.rt * kRT + r;
-          const int tok = static_cast<int>(paged::quotient(ri, a.g_div)), hh = ri - tok * a.G;
-          w[i] = make_uint4(0, 0, 0, 0);
-          if (r < rows)
-            w[i] = *reinterpret_cast<const uint4*>(a.q + static_cast<long long>(kc.s.start + tok) * a.q_stride +
-                                                   static_cast<long long>(kc.g * a.G + hh) * D + c * 8);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = r0 + i * kQR + lane / kQC;
-          if constexpr (INT8) {
-            const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-            uint32_t mag = 0;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) mag = max(mag, max(u[x] & 0x7FFFu, (u[x] >> 16) & 0x7FFFu));
-#pragma unroll
-            for (int d = kQC / 2; d > 0; d >>= 1) mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, d));
-            // 2^e with the row's largest magnitude in [2^14, 2^15) after x * 2^-e
-            const int e = mag == 0 ? 0 : max(-110, min(113, static_cast<int>(mag >> 7) - 127 - 14));
-            const float f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-            if (c == 0) bars->qfac[seg & 3][r] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-            auto half = [&](uint32_t y) { return half2_bits(__uint_as_float(y << 16) * f, __uint_as_float(y & 0xFFFF0000u) * f); };
-            w[i] = make_uint4(half(u[0]), half(u[1]), half(u[2]), half(u[3]));
-          }
-          *reinterpret_cast<uint4*>(smem + (c >> 3) * C::kPiece + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = w[i];
+          for (int d = kQC / 2; d > 0; d >>= 1) mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, d));
+          // 2^e with the row's largest magnitude in [2^14, 2^15) after x * 2^-e
+          const int e = mag == 0 ? 0 : max(-110, min(113, static_cast<int>(mag >> 7) - 127 - 14));
+          const float f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+          if (c == 0) bars->qfac[seg & 3][r] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+          auto half = [&](uint32_t y) { return half2_bits(__uint_as_float(y << 16) * f, __uint_as_float(y & 0xFFFF0000u) * f); };
+          *reinterpret_cast<uint4*>(smem + chunk(r)) = make_uint4(half(w.x), half(w.y), half(w.z), half(w.w));
         }
       }
       fence_proxy_async_smem();
