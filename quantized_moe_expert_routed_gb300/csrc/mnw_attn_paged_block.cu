@@ -17,14 +17,14 @@
 //               page sizes) come by 16-byte cp.async, 64 keys a warp, fenced to
 //               the tensor cores' proxy.  INT8: codes land in a raw buffer
 //               (bulk copies), are taken into registers, and leave them as FP16
-//               operand tiles (exact) while the next codes land.  All four
-//               bring the query tile of each segment (a run's part of an
-//               item); the first describes the segment to the other roles.
+//               operand tiles (exact) while the next codes land.
 //   warp 4      issues S_t = Q K_t^T, warp 5 O_g += P_t V_t, with P_t from
 //               tensor memory and V as it lies in the cache, [key][d], an
 //               operand whose N dimension is contiguous.  Two warps, because
 //               one accumulator's products follow each other at ~96 cycles
 //               and the two chains fill each other's gaps.
+//   warps 6-7   the query tile of each segment (a run's part of an item), and
+//               the segment's description for the other roles.
 //   warps 8-15  softmax, two groups of 4 warps: group t % 2 takes tile t, with
 //               its own O accumulator, maxima and sums, so that one group
 //               computes while the other's products run.  A warp takes its 32
@@ -54,7 +54,7 @@ namespace {
 
 constexpr int kRT = kBlockRows, kTK = kBlockKeys;
 constexpr int kThreads = 512;
-constexpr int kLoadWarps = 4, kWarpS = 4, kWarpPv = 5, kWarpSm0 = 8;
+constexpr int kLoadWarps = 4, kWarpS = 4, kWarpPv = 5, kWarpQ = 6, kWarpSm0 = 8;
 constexpr int kTmemCols = 512;
 constexpr int kMaxSegs = 8;      // segment descriptions held; at most four segments are under way
 constexpr int kMaxSlots = 4;
@@ -116,7 +116,7 @@ struct Bars {
 // they are free) or fewer (N < 0).  The kernel is built for kRegsBuilt, and the
 // split must not pass that in sum.  Once a role: a second change would have to
 // meet the whole warpgroup first, and may wait for a contiguous range for ever.
-constexpr int kRegsBuilt = 128, kRegsLoad = 96, kRegsMma = 64, kRegsSoftmax = 176;
+constexpr int kRegsBuilt = 128, kRegsLoad = 88, kRegsMma = 72, kRegsSoftmax = 176;
 static_assert(kRegsLoad + kRegsMma + 2 * kRegsSoftmax == 4 * kRegsBuilt);
 template <int N>
 __device__ __forceinline__ void registers() {
@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars->raw_empty[x], 2);
       mbar_init(&bars->drain[x], 1);
     }
-    mbar_init(&bars->q_full, kLoadWarps);
+    mbar_init(&bars->q_full, 2);
     mbar_init(&bars->q_empty, 1);
     mbar_init(&bars->o_full, 1);
     mbar_init(&bars->epi, 8);
@@ -309,7 +309,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     // whole pages: page `lane` of a tile, `span` keys each
     const int span = min(a.page_size, kTK), pieces = kTK / span;
     bool ok = tiles > 0;
-    int seg = -1;
     RingPos ring;
     auto table_at = [&](int seq, int p) {
       return __ldg(a.bt.block_table + static_cast<size_t>(seq) * a.bt.max_pages + paged::quotient(p, a.page_div));
@@ -353,58 +352,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       commit_copies();
     };
-    // ---- a segment's description and its queries, before the segment's first tile ----
-    auto begin_segment = [&](int tiles_left) -> bool {
-      ++seg;
-      if (threadIdx.x == 0) {
-        Seg d;
-        d.tiles = min(kc.sh.kt - kc.kt, tiles_left);
-        d.kt0 = kc.kt;
-        d.g = kc.g;
-        d.rt = kc.rt;
-        d.whole = kc.kt == 0 && d.tiles == kc.sh.kt;
-        d.s = kc.s;
-        bars->seg[seg % kMaxSegs] = d;
-        mbar_arrive(&bars->seg_full[seg % kMaxSegs]);
-      }
-      if (seg > 0 && !warp_wait(&bars->q_empty, (seg - 1) & 1, abort, a.err)) return false;
-      // 32 query rows a warp, D / 8 lanes a row
-      constexpr int kQC = D / 8, kQR = 32 / kQC;
-      const int rows = min(kRT, kc.s.n * a.G - kc.rt * kRT);
-      const int c = lane % kQC;
-      auto chunk = [&](int r) { return (c >> 3) * C::kPiece + r * 128 + (((c & 7) ^ (r & 7)) << 4); };
-#pragma unroll 4
-      for (int r = warp * 32 + lane / kQC; r < warp * 32 + 32; r += kQR) {
-        const int ri = kc.rt * kRT + (r < rows ? r : 0);
-        const int tok = static_cast<int>(paged::quotient(ri, a.g_div)), hh = ri - tok * a.G;
-        cp16(sbase + chunk(r), a.q + static_cast<long long>(kc.s.start + tok) * a.q_stride +
-                                   static_cast<long long>(kc.g * a.G + hh) * D + c * 8,
-             r < rows ? 16u : 0u);
-      }
-      commit_copies();
-      wait_copies<0>();
-      if constexpr (INT8) {  // in place: FP16 times a power of two
-#pragma unroll 2
-        for (int r = warp * 32 + lane / kQC; r < warp * 32 + 32; r += kQR) {
-          uint4 w = *reinterpret_cast<const uint4*>(smem + chunk(r));
-          const uint32_t hi = max(max(w.x & 0x7FFF0000u, w.y & 0x7FFF0000u), max(w.z & 0x7FFF0000u, w.w & 0x7FFF0000u));
-          const uint32_t lo = max(max(w.x & 0x7FFFu, w.y & 0x7FFFu), max(w.z & 0x7FFFu, w.w & 0x7FFFu));
-          uint32_t mag = max(hi >> 16, lo);
-#pragma unroll
-          for (int d = kQC / 2; d > 0; d >>= 1) mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, d));
-          // 2^e with the row's largest magnitude in [2^14, 2^15) after x * 2^-e
-          const int e = mag == 0 ? 0 : max(-110, min(113, static_cast<int>(mag >> 7) - 127 - 14));
-          const float f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-          if (c == 0) bars->qfac[seg & 3][r] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-          auto half = [&](uint32_t y) { return half2_bits(__uint_as_float(y << 16) * f, __uint_as_float(y & 0xFFFF0000u) * f); };
-          *reinterpret_cast<uint4*>(smem + chunk(r)) = make_uint4(half(w.x), half(w.y), half(w.z), half(w.w));
-        }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->q_full);
-      return true;
-    };
     auto step = [&]() {
       if (++kc.kt == kc.sh.kt) kc.next_item(a, run.pad);
     };
@@ -418,13 +365,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         pending = nullptr;
       };
       for (int t = 0; ok && t < tiles; ++t) {
-        if (t == 0 || kc.kt == 0) {
-          if (pending) {  // products before this segment's wait for it
-            wait_copies<0>();
-            give();
-          }
-          if (!begin_segment(tiles - t)) { ok = false; break; }
-        }
         if (!warp_wait(&empty[ring.slot], ring.phase ^ 1, abort, a.err)) { ok = false; break; }
         uint64_t* bar = &full[ring.slot];
         const uint32_t at = ring_at + ring.slot * C::kTile;
@@ -557,8 +497,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           ring.advance(ring_slots);
           if (++sc_now == sc_slots) sc_now = 0;
         }
-        // the next tile's segment, once this tile is given on (its queries wait for the products of the segment before)
-        if (t + 1 < tiles && (t < 0 || kc.kt == 0)) ok = begin_segment(tiles - (t + 1));
       }
       wait_copies<0>();
       if (bulk_out && lw == 0) drain_wait(raw_full, raw_phase);  // (an abort) the copy lands before the CTA exits
@@ -632,6 +570,62 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++seg;
           begin = t + 1;
         }
+      }
+    }
+    if (warp >= kWarpQ) {
+      // ======================= queries =======================
+      const int qw = warp - kWarpQ;                 // which 64 rows
+      constexpr int kQC = D / 8, kQR = 32 / kQC;    // lanes of a row, rows at a time
+      int t = 0;
+      for (int seg = 0; t < tiles; ++seg) {
+        const int n = min(kc.sh.kt - kc.kt, tiles - t);
+        if (qw == 0 && lane == 0) {
+          Seg d;
+          d.tiles = n;
+          d.kt0 = kc.kt;
+          d.g = kc.g;
+          d.rt = kc.rt;
+          d.whole = kc.kt == 0 && n == kc.sh.kt;
+          d.s = kc.s;
+          bars->seg[seg % kMaxSegs] = d;
+          mbar_arrive(&bars->seg_full[seg % kMaxSegs]);
+        }
+        if (seg > 0 && !warp_wait(&bars->q_empty, (seg - 1) & 1, abort, a.err)) break;
+        const int rows = min(kRT, kc.s.n * a.G - kc.rt * kRT);
+        const int c = lane % kQC;
+        auto chunk = [&](int r) { return (c >> 3) * C::kPiece + r * 128 + (((c & 7) ^ (r & 7)) << 4); };
+#pragma unroll 4
+        for (int r = qw * 64 + lane / kQC; r < qw * 64 + 64; r += kQR) {
+          const int ri = kc.rt * kRT + (r < rows ? r : 0);
+          const int tok = static_cast<int>(paged::quotient(ri, a.g_div)), hh = ri - tok * a.G;
+          cp16(sbase + chunk(r), a.q + static_cast<long long>(kc.s.start + tok) * a.q_stride +
+                                     static_cast<long long>(kc.g * a.G + hh) * D + c * 8,
+               r < rows ? 16u : 0u);
+        }
+        commit_copies();
+        wait_copies<0>();
+        if constexpr (INT8) {  // in place: FP16 times a power of two
+#pragma unroll 2
+          for (int r = qw * 64 + lane / kQC; r < qw * 64 + 64; r += kQR) {
+            uint4 w = *reinterpret_cast<const uint4*>(smem + chunk(r));
+            const uint32_t hi = max(max(w.x & 0x7FFF0000u, w.y & 0x7FFF0000u), max(w.z & 0x7FFF0000u, w.w & 0x7FFF0000u));
+            const uint32_t lo = max(max(w.x & 0x7FFFu, w.y & 0x7FFFu), max(w.z & 0x7FFFu, w.w & 0x7FFFu));
+            uint32_t mag = max(hi >> 16, lo);
+#pragma unroll
+            for (int d = kQC / 2; d > 0; d >>= 1) mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, d));
+            // 2^e with the row's largest magnitude in [2^14, 2^15) after x * 2^-e
+            const int e = mag == 0 ? 0 : max(-110, min(113, static_cast<int>(mag >> 7) - 127 - 14));
+            const float f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+            if (c == 0) bars->qfac[seg & 3][r] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+            auto half = [&](uint32_t y) { return half2_bits(__uint_as_float(y << 16) * f, __uint_as_float(y & 0xFFFF0000u) * f); };
+            *reinterpret_cast<uint4*>(smem + chunk(r)) = make_uint4(half(w.x), half(w.y), half(w.z), half(w.w));
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->q_full);
+        t += n;
+        if (t < tiles) kc.next_item(a, run.pad);
       }
     }
     if ((warp == kWarpS || warp == kWarpPv) && lead) {
