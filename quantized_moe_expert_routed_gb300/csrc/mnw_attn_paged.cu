@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(WR* WK * 32) paged_attn_kernel(const Args a) {
   pdl_launch_dependents();
   pdl_wait();
 
-  const Run run = find_run<kRT, kTK, kThreads>(a, &split);
+  const Run run = find_run<kRT, kTK, kThreads, 0>(a, &split);
   if (run.seq < 0) return;  // no units left for this run
   Cursor<kRT, kTK> cc;  // the tile computed
   cc.set(a, run);

@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   pdl_wait();
-  const Run run = find_run<kRT, kTK, kThreads>(a, &split);
+  const Run run = find_run<kRT, kTK, kThreads, kMaxSlack>(a, &split);
   Cursor<kRT, kTK> kc{};
   int tiles = 0;
   if (run.seq >= 0) {
@@ -594,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int rows = min(kRT, kc.s.n * a.G - kc.rt * kRT);
         const int c = lane % kQC;
         auto chunk = [&](int r) { return (c >> 3) * C::kPiece + r * 128 + (((c & 7) ^ (r & 7)) << 4); };
-#pragma unroll 4
+#pragma unroll 8
         for (int r = qw * 64 + lane / kQC; r < qw * 64 + 64; r += kQR) {
           const int ri = kc.rt * kRT + (r < rows ? r : 0);
           const int tok = static_cast<int>(paged::quotient(ri, a.g_div)), hh = ri - tok * a.G;
@@ -604,21 +604,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         commit_copies();
         wait_copies<0>();
-        if constexpr (INT8) {  // in place: FP16 times a power of two
-#pragma unroll 2
-          for (int r = qw * 64 + lane / kQC; r < qw * 64 + 64; r += kQR) {
-            uint4 w = *reinterpret_cast<const uint4*>(smem + chunk(r));
-            const uint32_t hi = max(max(w.x & 0x7FFF0000u, w.y & 0x7FFF0000u), max(w.z & 0x7FFF0000u, w.w & 0x7FFF0000u));
-            const uint32_t lo = max(max(w.x & 0x7FFFu, w.y & 0x7FFFu), max(w.z & 0x7FFFu, w.w & 0x7FFFu));
-            uint32_t mag = max(hi >> 16, lo);
+        if constexpr (INT8) {  // in place: FP16 times a power of two; 8 rows a lane at once, one by one is a chain of latencies
+#pragma unroll 1
+          for (int r0 = qw * 64 + lane / kQC; r0 < qw * 64 + 64; r0 += 8 * kQR) {
+            uint4 w[8];
+            uint32_t mag[8];
 #pragma unroll
-            for (int d = kQC / 2; d > 0; d >>= 1) mag = max(mag, __shfl_xor_sync(0xffffffffu, mag, d));
-            // 2^e with the row's largest magnitude in [2^14, 2^15) after x * 2^-e
-            const int e = mag == 0 ? 0 : max(-110, min(113, static_cast<int>(mag >> 7) - 127 - 14));
-            const float f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-            if (c == 0) bars->qfac[seg & 3][r] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-            auto half = [&](uint32_t y) { return half2_bits(__uint_as_float(y << 16) * f, __uint_as_float(y & 0xFFFF0000u) * f); };
-            *reinterpret_cast<uint4*>(smem + chunk(r)) = make_uint4(half(w.x), half(w.y), half(w.z), half(w.w));
+            for (int i = 0; i < 8; ++i) w[i] = *reinterpret_cast<const uint4*>(smem + chunk(r0 + i * kQR));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint32_t hi = max(max(w[i].x & 0x7FFF0000u, w[i].y & 0x7FFF0000u), max(w[i].z & 0x7FFF0000u, w[i].w & 0x7FFF0000u));
+              const uint32_t lo = max(max(w[i].x & 0x7FFFu, w[i].y & 0x7FFFu), max(w[i].z & 0x7FFFu, w[i].w & 0x7FFFu));
+              mag[i] = max(hi >> 16, lo);
+            }
+#pragma unroll
+            for (int d = kQC / 2; d > 0; d >>= 1)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) mag[i] = max(mag[i], __shfl_xor_sync(0xffffffffu, mag[i], d));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              // 2^e with the row's largest magnitude in [2^14, 2^15) after x * 2^-e
+              const int e = mag[i] == 0 ? 0 : max(-110, min(113, static_cast<int>(mag[i] >> 7) - 127 - 14));
+              const float f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+              auto half = [&](uint32_t y) { return half2_bits(__uint_as_float(y << 16) * f, __uint_as_float(y & 0xFFFF0000u) * f); };
+              const int r = r0 + i * kQR;
+              *reinterpret_cast<uint4*>(smem + chunk(r)) = make_uint4(half(w[i].x), half(w[i].y), half(w[i].z), half(w[i].w));
+              if (c == 0) bars->qfac[seg & 3][r] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+            }
           }
         }
         fence_proxy_async_smem();

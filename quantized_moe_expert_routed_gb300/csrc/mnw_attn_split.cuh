@@ -85,8 +85,9 @@ __device__ __forceinline__ Shape shape_of(const Seq& s, int G, int Hkv, int pad)
   return h;
 }
 
+constexpr int kMaxSlack = 4;
 struct SplitShared {
-  int scan[32], pads[32];
+  int scan[32], pads[kMaxSlack + 1][32];
   int seq, first;  // sequence of the run's first unit and its first unit
 };
 
@@ -96,15 +97,21 @@ struct Run {
 };
 
 // Where run blockIdx.x begins.  All threads call; ends with a barrier.  Where
-// all items, cut into runs of min_units each, fit the grid, runs do not cross
-// items (latency); otherwise the runs are equal (throughput).
-template <int RT, int TK, int THREADS>
+// all items, cut into runs of some length each, fit the grid, runs do not cross
+// items; tried are the shortest runs (latency) and up to SLACK lengths from the equal share
+// on, for a kernel that pays more for a second item in a run than for SLACK
+// more tiles.  Otherwise the runs are equal shares of the units.
+template <int RT, int TK, int THREADS, int SLACK>
 __device__ __forceinline__ Run find_run(const Args& a, SplitShared* sh) {
   constexpr int kWarps = THREADS / 32;
+  static_assert(SLACK <= kMaxSlack);
   const Batch& bt = a.bt;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const bool scribe = blockIdx.x == 0;  // run 0 reports bad lengths and writes the sequences' first units
   if (tid == 0) sh->seq = -1;
+  const int runs = gridDim.x;
+  // runs that the items of sequence s make at p units each (few enough to add up: the sums are clipped)
+  auto runs_of = [&](const Shape& one, int p) { return min(a.Hkv * one.rt * ((one.kt + p - 1) / p), 1 << 20); };
   int total = 0, padded = 0;
   Seq s{};
   for (int b = tid; b < bt.B; b += THREADS) {
@@ -113,26 +120,56 @@ __device__ __forceinline__ Run find_run(const Args& a, SplitShared* sh) {
     if (bad && scribe && a.err) atomicOr(a.err, MNW_DEVERR_BAD_LENGTH);
     const Shape one = shape_of<RT, TK>(s, a.G, a.Hkv, 1);
     total += one.units;
-    padded += a.Hkv * one.rt * ((one.kt + a.min_units - 1) / a.min_units);
+    padded = min(padded + runs_of(one, a.min_units), 1 << 20);
   }
-  const int tw = __reduce_add_sync(0xffffffffu, total), pw = __reduce_add_sync(0xffffffffu, min(padded, 1 << 20));
+  const int tw = __reduce_add_sync(0xffffffffu, total), pw = __reduce_add_sync(0xffffffffu, padded);
   if (lane == 0) {
     sh->scan[warp] = tw;
-    sh->pads[warp] = pw;
+    sh->pads[0][warp] = pw;
   }
   __syncthreads();
   total = padded = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
     total += sh->scan[w];
-    padded += sh->pads[w];
+    padded += sh->pads[0][w];
   }
   Run r;
-  const int runs = gridDim.x;
-  const bool aligned_runs = padded <= runs;
-  r.pad = aligned_runs ? a.min_units : 1;
-  r.per = aligned_runs ? a.min_units : max(a.min_units, (total + runs - 1) / runs);
-  const int limit = aligned_runs ? padded * a.min_units : total;
+  r.per = max(a.min_units, (total + runs - 1) / runs);
+  r.pad = 1;
+  int limit = total;
+  if (padded <= runs) {
+    r.pad = r.per = a.min_units;
+    limit = padded * a.min_units;
+  } else if (SLACK > 0) {
+    int sums[SLACK > 0 ? SLACK : 1];
+#pragma unroll
+    for (int k = 0; k < SLACK; ++k) sums[k] = 0;
+    for (int b = tid; b < bt.B; b += THREADS) {
+      bool bad;
+      if (bt.B > THREADS) s = paged::sequence(bt, b, a.page_size, &bad);
+      const Shape one = shape_of<RT, TK>(s, a.G, a.Hkv, 1);
+#pragma unroll
+      for (int k = 0; k < SLACK; ++k) sums[k] = min(sums[k] + runs_of(one, r.per + k), 1 << 20);
+    }
+#pragma unroll
+    for (int k = 0; k < SLACK; ++k) {
+      const int v = __reduce_add_sync(0xffffffffu, sums[k]);
+      if (lane == 0) sh->pads[k + 1][warp] = v;
+    }
+    __syncthreads();
+    const int share = r.per;
+#pragma unroll
+    for (int k = SLACK - 1; k >= 0; --k) {
+      int v = 0;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) v += sh->pads[k + 1][w];
+      if (v <= runs) {
+        r.pad = r.per = share + k;
+        limit = v * (share + k);
+      }
+    }
+  }
   r.u0 = static_cast<int>(min(static_cast<long long>(blockIdx.x) * r.per, static_cast<long long>(limit)));
   r.u1 = min(limit, r.u0 + r.per);
   int carry = 0;
