@@ -352,7 +352,7 @@ def mnw_rmsnorm(x, weight, eps=1e-6, residual=None, residual_out=None, y=None, c
             scales = _new((T, H // 128), torch.float32, dev, stream)
         cp = _whole(codes, torch.int8, shape, "codes")
         sp = _whole(scales, torch.float32, (T, H // 128), "scales")
-    stride = x.stride(0) if T > 1 else max(H, x.stride(0))
+    stride = x.stride(0) if T > 1 else max(H, x.stride(0) // 8 * 8)
     rc = load().mnw_rmsnorm(xp, stride, rp, wp, T, H, eps, ro, yp, cp, sp, _stream_of(x, stream))
     if rc:
         _check(rc, "mnw_rmsnorm")

@@ -78,6 +78,25 @@ def test_rmsnorm_strided_rows_in_place_and_special_rows():
     assert torch.isnan(y[2]).all()
 
 
+def test_rmsnorm_codes_at_the_ends_of_the_range():
+    """Groups from subnormal (whose scales hold few bits) to huge: the codes are those of y, bit for bit."""
+    H = 1024
+    x = _randn((40, H), 3)
+    w = torch.tensor([2.0 ** e for e in (-133, -130, -126, -120, -100, 0, 60, 122)]).repeat_interleave(128)
+    y, _, codes, scales = M().mnw_rmsnorm(x, w.bfloat16().cuda(), 1e-5, int8=True)
+    assert torch.isfinite(y.float()).all()
+    want, ws = U.quantise_rows(y.float().cpu().view(40, -1, 128).numpy())
+    assert np.array_equal(scales.cpu().numpy(), ws)
+    assert np.array_equal(codes.cpu().numpy().reshape(want.shape), want)
+
+
+def test_rmsnorm_one_row_of_a_wider_tensor():
+    """A single row's stride is not looked at, whatever the tensor it was cut from."""
+    big = _randn((4, 1003), 4)
+    x, w = big[:1, :1000], _randn((1000,), 5)
+    assert torch.equal(M().mnw_rmsnorm(x, w)[0], M().mnw_rmsnorm(x.clone(), w)[0])
+
+
 # ---- append ----
 
 
