@@ -23,8 +23,8 @@
 //               operand whose N dimension is contiguous.  Two warps, because
 //               one accumulator's products follow each other at ~96 cycles
 //               and the two chains fill each other's gaps.
-//   warps 6-7   the query tile of each segment (a run's part of an item), and
-//               the segment's description for the other roles.
+//   warps 6-7   the query tile of each segment (a run's part of an item) but
+//               the first, and the segment's description for the other roles.
 //   warps 8-15  softmax, two groups of 4 warps: group t % 2 takes tile t, with
 //               its own O accumulator, maxima and sums, so that one group
 //               computes while the other's products run.  A warp takes its 32
@@ -97,7 +97,7 @@ struct Seg {
 struct Bars {
   uint64_t full[2][kMaxSlots], empty[2][kMaxSlots];  // operand rings: keys, values
   uint64_t raw_full[2], raw_empty[2];
-  uint64_t q_full, q_empty;
+  uint64_t q0_full, q_full, q_empty;                 // the first query tile is there, a later one; consumed
   uint64_t s_full[kMaxBufs], p_full[kMaxBufs], s_free[kMaxBufs];  // per score buffer: scores complete, P written, P consumed
   uint64_t o_full, epi;                 // a segment's output complete; read
   uint64_t ks_full[kMaxKScales], vs_full[kMaxVScales];
@@ -261,6 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars->raw_empty[x], 2);
       mbar_init(&bars->drain[x], 1);
     }
+    mbar_init(&bars->q0_full, 8);
     mbar_init(&bars->q_full, 2);
     mbar_init(&bars->q_empty, 1);
     mbar_init(&bars->o_full, 1);
@@ -293,6 +294,57 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
+
+  // A warp's part of segment `seg`'s query tile, the item at kc: rows r0 .. r0 + n, n a multiple of 16.
+  auto query_rows = [&](int seg, int r0, int n) {
+    constexpr int kQC = D / 8, kQR = 32 / kQC;  // lanes of a row, rows at a time
+    constexpr int kQB = 16 / kQR;               // rows of a lane at once; one by one is a chain of latencies
+    const int rows = min(kRT, kc.s.n * a.G - kc.rt * kRT);
+    const int c = lane % kQC;
+    auto chunk = [&](int r) { return (c >> 3) * C::kPiece + r * 128 + (((c & 7) ^ (r & 7)) << 4); };
+#pragma unroll kQB
+    for (int i = 0; i < n / kQR; ++i) {
+      const int r = r0 + lane / kQC + i * kQR;
+      const int ri = kc.rt * kRT + (r < rows ? r : 0);
+      const int tok = static_cast<int>(paged::quotient(ri, a.g_div)), hh = ri - tok * a.G;
+      cp16(sbase + chunk(r), a.q + static_cast<long long>(kc.s.start + tok) * a.q_stride +
+                                 static_cast<long long>(kc.g * a.G + hh) * D + c * 8,
+           r < rows ? 16u : 0u);
+    }
+    commit_copies();
+    wait_copies<0>();
+    if constexpr (INT8) {  // in place: FP16 times a power of two
+#pragma unroll 1
+      for (int rb = r0 + lane / kQC; rb < r0 + n; rb += 16) {
+        uint4 w[kQB];
+        uint32_t mag[kQB];
+#pragma unroll
+        for (int i = 0; i < kQB; ++i) w[i] = *reinterpret_cast<const uint4*>(smem + chunk(rb + i * kQR));
+#pragma unroll
+        for (int i = 0; i < kQB; ++i) {
+          const uint32_t m = __vmaxu2(__vmaxu2(w[i].x & 0x7FFF7FFFu, w[i].y & 0x7FFF7FFFu),
+                                      __vmaxu2(w[i].z & 0x7FFF7FFFu, w[i].w & 0x7FFF7FFFu));
+          mag[i] = max(m >> 16, m & 0xFFFFu);
+        }
+#pragma unroll
+        for (int d = kQC / 2; d > 0; d >>= 1)
+#pragma unroll
+          for (int i = 0; i < kQB; ++i) mag[i] = max(mag[i], __shfl_xor_sync(0xffffffffu, mag[i], d));
+#pragma unroll
+        for (int i = 0; i < kQB; ++i) {
+          // 2^e with the row's largest magnitude in [2^14, 2^15) after x * 2^-e
+          const int e = mag[i] == 0 ? 0 : max(-110, min(113, static_cast<int>(mag[i] >> 7) - 127 - 14));
+          const float f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+          auto half = [&](uint32_t y) { return half2_bits(__uint_as_float(y << 16) * f, __uint_as_float(y & 0xFFFF0000u) * f); };
+          const int r = rb + i * kQR;
+          *reinterpret_cast<uint4*>(smem + chunk(r)) = make_uint4(half(w[i].x), half(w[i].y), half(w[i].z), half(w[i].w));
+          if (c == 0) bars->qfac[seg & 3][r] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+        }
+      }
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+  };
 
   if (warp < kLoadWarps) {
     // ======================= loaders =======================
@@ -409,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint64_t *const raw_full = &bars->raw_full[values ? 1 : 0], *const raw_empty = &bars->raw_empty[values ? 1 : 0];
       const uint32_t raw_at = C::kOffRaw + (values ? C::kRaw : 0);
       uint32_t raw_phase = 0;  // parity of the next bulk landing
-      int sc_issue = 0, sc_now = 0;  // scale slots of the tile issued next, of the tile converted
+      int sc_issue = 0, sc_now = 0;  // scale slots of the tile issued next, of the tile that lands next
       auto scales_at = [&](int slot) { return values ? C::kOffVS + slot * (2 * kTK * 4) : C::kOffKS + slot * (kTK * 4); };
       const int sc_slots = values ? C::kScalesV : C::kScalesK;
       bool landing_rows = false;
@@ -448,6 +500,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             raw_phase ^= 1;
             bulk_out = false;
           }
+          // the scales are given on at once: the softmax of a tile runs while its values still wait for their operand slot
+          if (values) {
+            float* sc = reinterpret_cast<float*>(smem + scales_at(sc_now)) + lw * 64 + lane;
+            sc[kTK] = __log2f(sc[0]);
+            sc[kTK + 32] = __log2f(sc[32]);
+            __syncwarp();
+          }
+          if (lane == 0) mbar_arrive(values ? &bars->vs_full[sc_now] : &bars->ks_full[sc_now]);
+          if (++sc_now == sc_slots) sc_now = 0;
           if (!warp_wait(&empty[ring.slot], ring.phase ^ 1, abort, a.err)) { ok = false; break; }
         }
         uint8_t* op = smem + ring_at + ring.slot * C::kTile + lw * 64 * 128;
@@ -483,19 +544,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) break;
         if (t >= 0) {
-          if (values) {
-            float* sc = reinterpret_cast<float*>(smem + scales_at(sc_now)) + lw * 64 + lane;
-            sc[kTK] = __log2f(sc[0]);
-            sc[kTK + 32] = __log2f(sc[32]);
-          }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&full[ring.slot]);
-            mbar_arrive(values ? &bars->vs_full[sc_now] : &bars->ks_full[sc_now]);
-          }
+          if (lane == 0) mbar_arrive(&full[ring.slot]);
           ring.advance(ring_slots);
-          if (++sc_now == sc_slots) sc_now = 0;
         }
       }
       wait_copies<0>();
@@ -514,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (left == 0) {
           if (!warp_wait(&bars->seg_full[seg % kMaxSegs], (seg / kMaxSegs) & 1, abort, a.err)) break;
           left = bars->seg[seg % kMaxSegs].tiles;
-          if (!warp_wait(&bars->q_full, seg & 1, abort, a.err)) break;
+          if (!warp_wait(seg ? &bars->q_full : &bars->q0_full, seg ? (seg - 1) & 1 : 0, abort, a.err)) break;
         }
         if (!warp_wait2(&bars->full[0][kr.slot], kr.phase, &bars->s_free[buf.slot], buf.phase ^ 1, abort, a.err)) break;
         tc_fence_after();
@@ -574,8 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (warp >= kWarpQ) {
       // ======================= queries =======================
-      const int qw = warp - kWarpQ;                 // which 64 rows
-      constexpr int kQC = D / 8, kQR = 32 / kQC;    // lanes of a row, rows at a time
+      const int qw = warp - kWarpQ;  // which 64 rows
       int t = 0;
       for (int seg = 0; t < tiles; ++seg) {
         const int n = min(kc.sh.kt - kc.kt, tiles - t);
@@ -590,52 +641,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           bars->seg[seg % kMaxSegs] = d;
           mbar_arrive(&bars->seg_full[seg % kMaxSegs]);
         }
-        if (seg > 0 && !warp_wait(&bars->q_empty, (seg - 1) & 1, abort, a.err)) break;
-        const int rows = min(kRT, kc.s.n * a.G - kc.rt * kRT);
-        const int c = lane % kQC;
-        auto chunk = [&](int r) { return (c >> 3) * C::kPiece + r * 128 + (((c & 7) ^ (r & 7)) << 4); };
-#pragma unroll 8
-        for (int r = qw * 64 + lane / kQC; r < qw * 64 + 64; r += kQR) {
-          const int ri = kc.rt * kRT + (r < rows ? r : 0);
-          const int tok = static_cast<int>(paged::quotient(ri, a.g_div)), hh = ri - tok * a.G;
-          cp16(sbase + chunk(r), a.q + static_cast<long long>(kc.s.start + tok) * a.q_stride +
-                                     static_cast<long long>(kc.g * a.G + hh) * D + c * 8,
-               r < rows ? 16u : 0u);
+        if (seg > 0) {  // (the first segment's: the softmax warps)
+          if (!warp_wait(&bars->q_empty, (seg - 1) & 1, abort, a.err)) break;
+          query_rows(seg, qw * 64, 64);
+          if (lane == 0) mbar_arrive(&bars->q_full);
         }
-        commit_copies();
-        wait_copies<0>();
-        if constexpr (INT8) {  // in place: FP16 times a power of two; 8 rows a lane at once, one by one is a chain of latencies
-#pragma unroll 1
-          for (int r0 = qw * 64 + lane / kQC; r0 < qw * 64 + 64; r0 += 8 * kQR) {
-            uint4 w[8];
-            uint32_t mag[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = *reinterpret_cast<const uint4*>(smem + chunk(r0 + i * kQR));
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const uint32_t hi = max(max(w[i].x & 0x7FFF0000u, w[i].y & 0x7FFF0000u), max(w[i].z & 0x7FFF0000u, w[i].w & 0x7FFF0000u));
-              const uint32_t lo = max(max(w[i].x & 0x7FFFu, w[i].y & 0x7FFFu), max(w[i].z & 0x7FFFu, w[i].w & 0x7FFFu));
-              mag[i] = max(hi >> 16, lo);
-            }
-#pragma unroll
-            for (int d = kQC / 2; d > 0; d >>= 1)
-#pragma unroll
-              for (int i = 0; i < 8; ++i) mag[i] = max(mag[i], __shfl_xor_sync(0xffffffffu, mag[i], d));
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              // 2^e with the row's largest magnitude in [2^14, 2^15) after x * 2^-e
-              const int e = mag[i] == 0 ? 0 : max(-110, min(113, static_cast<int>(mag[i] >> 7) - 127 - 14));
-              const float f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-              auto half = [&](uint32_t y) { return half2_bits(__uint_as_float(y << 16) * f, __uint_as_float(y & 0xFFFF0000u) * f); };
-              const int r = r0 + i * kQR;
-              *reinterpret_cast<uint4*>(smem + chunk(r)) = make_uint4(half(w[i].x), half(w[i].y), half(w[i].z), half(w[i].w));
-              if (c == 0) bars->qfac[seg & 3][r] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-            }
-          }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->q_full);
         t += n;
         if (t < tiles) kc.next_item(a, run.pad);
       }
@@ -649,6 +659,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ======================= softmax =======================
     registers<kRegsSoftmax>();
+    // nothing to do yet: the first segment's queries, 16 rows each (by the two query warps alone they were the last thing
+    // the first scores waited for)
+    if (tiles > 0) {
+      query_rows(0, (warp - kWarpSm0) * 16, 16);
+      if (lane == 0) mbar_arrive(&bars->q0_full);
+    }
     const int grp = (warp - kWarpSm0) >> 2;  // tiles grp, grp + 2, ... of the run
     const int quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lane_bits = static_cast<uint32_t>(quarter * 32) << 16;
