@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int rows = min(kRT, kc.s.n * a.G - kc.rt * kRT);
     const int c = lane % kQC;
     auto chunk = [&](int r) { return (c >> 3) * C::kPiece + r * 128 + (((c & 7) ^ (r & 7)) << 4); };
-#pragma unroll kQB
+#pragma unroll 2
     for (int i = 0; i < n / kQR; ++i) {
       const int r = r0 + lane / kQC + i * kQR;
       const int ri = kc.rt * kRT + (r < rows ? r : 0);
@@ -488,8 +488,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       bool bulk_out = false;  // a bulk copy is under way
       constexpr int kW = 4 * kCh, kOC = D / 8;  // 64 rows, 8 codes a lane: one 16-byte chunk of the operand row
-      // step t: tile t lands and is converted in two halves, each by way of registers; the copies of tile t + 1 go out as
-      // soon as the second is there
+      // step t: tile t lands and is converted in parts, each by way of registers; the copies of tile t + 1 go out as soon
+      // as the last is there
+      constexpr int kParts = 4, kPW = kW / kParts, kPR = 64 / kParts;
       for (int t = -1; ok && t < tiles; ++t) {
         if (t >= 0) {
           if (landing_rows) {
@@ -514,13 +515,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint8_t* op = smem + ring_at + ring.slot * C::kTile + lw * 64 * 128;
         const uint8_t* raw = smem + raw_at + lw * 64 * D + lane * 8;
 #pragma unroll 1
-        for (int part = t < 0 ? 1 : 0; part < 2; ++part) {
-          uint2 w[kW / 2];
+        for (int part = t < 0 ? kParts - 1 : 0; part < kParts; ++part) {
+          uint2 w[kPW];
           if (t >= 0) {
 #pragma unroll
-            for (int i = 0; i < kW / 2; ++i) w[i] = *reinterpret_cast<const uint2*>(raw + part * (32 * D) + i * 256);
+            for (int i = 0; i < kPW; ++i) w[i] = *reinterpret_cast<const uint2*>(raw + part * (kPR * D) + i * 256);
           }
-          if (part == 1) {
+          if (part == kParts - 1) {
             if (t >= 0) {
               __syncwarp();
               if (lane == 0) mbar_arrive(raw_empty);
@@ -534,8 +535,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (t >= 0) {
 #pragma unroll
-            for (int i = 0; i < kW / 2; ++i) {
-              const int row = part * 32 + i * (32 / kOC) + lane / kOC, c = lane % kOC;  // of the warp's 64
+            for (int i = 0; i < kPW; ++i) {
+              const int row = part * kPR + i * (32 / kOC) + lane / kOC, c = lane % kOC;  // of the warp's 64
               const uint32_t x = w[i].x ^ 0x80808080u, y = w[i].y ^ 0x80808080u;
               *reinterpret_cast<uint4*>(op + (c >> 3) * C::kPiece + row * 128 + (((c & 7) ^ (row & 7)) << 4)) =
                   make_uint4(codes_lo(x), codes_hi(x), codes_lo(y), codes_hi(y));
@@ -557,6 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     registers<-kRegsMma>();
     // ======================= MMA issuers =======================
     // The warps stay together and their first lanes issue.
+    constexpr int kUnrollMma = INT8 ? 1 : 8;  // (the INT8 form is bound by its instruction cache)
     const bool lead = lane == 0;
     if (warp == kWarpS && tiles > 0) {
       const uint32_t idesc = idesc_f16(kRT, kTK, !INT8);
@@ -574,10 +576,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lead) {
           const uint32_t k_s = sbase + C::kOffK + kr.slot * C::kTile;
           const uint32_t d = tmem + buf.slot * kTK;
-#pragma unroll
+          // (descriptors count 16 bytes)
+          uint64_t da = sdesc_sw128(sbase), db = sdesc_sw128(k_s);
+#pragma unroll kUnrollMma
           for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * C::kPiece + (kk & 3) * 32;
-            mma_ss(d, sdesc_sw128(sbase + off), sdesc_sw128(k_s + off), idesc, kk > 0);
+            mma_ss(d, da, db, idesc, kk > 0);
+            const uint32_t next = (kk & 3) == 3 ? (C::kPiece - 96) >> 4 : 2;
+            da += next;
+            db += next;
           }
           mma_commit(&bars->s_full[buf.slot]);
           mma_commit(&bars->empty[0][kr.slot]);
@@ -608,9 +614,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t p = tmem + buf.slot * kTK;  // two keys per column
           const uint32_t o = tmem + C::kColO + static_cast<uint32_t>(t & 1) * D;
           const bool fresh = t - begin < 2;  // the group's first tile of the segment
-#pragma unroll
-          for (int kk = 0; kk < kTK / 16; ++kk)
-            mma_ts(o, p + kk * 8, sdesc_mn_sw128(v_s + kk * 2048, C::kPiece), idesc, !(fresh && kk == 0));
+          uint64_t db = sdesc_mn_sw128(v_s, C::kPiece);
+#pragma unroll kUnrollMma
+          for (int kk = 0; kk < kTK / 16; ++kk, db += 2048 >> 4) mma_ts(o, p + kk * 8, db, idesc, !(fresh && kk == 0));
           mma_commit(&bars->s_free[buf.slot]);
           mma_commit(&bars->empty[1][vr.slot]);
           if (left == 0) mma_commit(&bars->o_full);
