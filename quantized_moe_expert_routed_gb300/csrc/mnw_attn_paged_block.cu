@@ -25,13 +25,9 @@
 //               and the two chains fill each other's gaps.
 //   warps 6-7   the query tile of each segment (a run's part of an item) but
 //               the first, and the segment's description for the other roles.
-//   warps 8-15  softmax, two groups of 4 warps: group t % 2 takes tile t, with
-//               its own O accumulator, maxima and sums, so that one group
-//               computes while the other's products run.  A warp takes its 32
-//               rows 16 at a time, a thread 32 keys of two rows (so a key's
-//               scales serve two rows), kept in registers from the maximum to P.
-//               More at once would spill, and with the shared memory this
-//               kernel takes there is next to no L1 for spills to hit.
+//   warps 8-15  softmax, 16 rows a warp, a thread 32 keys of two rows (so a
+//               key's scales serve two rows), kept in registers from the
+//               maximum to P; the next tiles' scores are computed meanwhile.
 // S of a tile goes into its score buffer once P V of the tile there before is
 // complete.
 //
@@ -69,11 +65,11 @@ struct BCfg {
   static constexpr uint32_t kTile = kHalves * kPiece;      // operand tile
   static constexpr int kSlotsK = D == 64 ? 4 : (INT8 ? 2 : 3), kSlotsV = D == 64 ? 4 : 2;
   static constexpr uint32_t kRaw = INT8 ? kTK * D : 0;     // raw codes of a tile
-  // Tensor memory: score buffers (tile t in buffer t % kBufs, its P over the first half), then the two groups' O.  A
-  // third buffer lets a group's next scores be ready before its P is consumed; with 128-wide heads there is no room.
-  static constexpr int kBufs = D == 64 ? 3 : 2;
-  static constexpr uint32_t kColO = kBufs * kTK;           // O_g at kColO + D g
-  static_assert(kColO + 2 * D <= kTmemCols);
+  // Tensor memory: score buffers (tile t in buffer t % kBufs, its P over the first half), then O.  Three: one in the
+  // softmax, one whose P is being consumed, one being computed.
+  static constexpr int kBufs = 3;
+  static constexpr uint32_t kColO = kBufs * kTK;
+  static_assert(kColO + D <= kTmemCols && kBufs <= kMaxBufs);
   // Scales are copied with a tile's codes, which are issued once the tile two before went into its operand slot, that
   // is, once the product with the tile that held the slot before is complete (S waits for P V of kBufs tiles before);
   // the softmax of a tile reads them last before P V of the tile is issued.
@@ -102,11 +98,10 @@ struct Bars {
   uint64_t o_full, epi;                 // a segment's output complete; read
   uint64_t ks_full[kMaxKScales], vs_full[kMaxVScales];
   uint64_t seg_full[kMaxSegs];
-  uint64_t fin[4];                      // per lane quarter: both groups' maxima and sums written
+  uint64_t fin[4];                      // per lane quarter: both warps' maxima and sums written
   uint64_t drain[2];
-  float st_m[2][2][kRT], st_l[2][2][kRT], st_u[2][2][kRT];  // [segment parity][group][row]: maximum, sum, log2 of O's unit over 2^maximum
+  float st_m[2][kRT], st_l[2][kRT], st_u[2][kRT];  // [segment parity][row]: maximum, sum, log2 of O's unit over 2^maximum
   float qfac[4][kRT];                   // [segment % 4] INT8: the query rows' powers of two
-  int st_any[2][2];                     // [segment parity][group]: whether the group had a tile
   Seg seg[kMaxSegs];
   uint32_t tmem_base;
   int abort;
@@ -272,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 4; ++i) mbar_init(&bars->fin[i], 2);
     for (int i = 0; i < kMaxBufs; ++i) {
       mbar_init(&bars->s_full[i], 1);
-      mbar_init(&bars->p_full[i], 4);
+      mbar_init(&bars->p_full[i], 8);
       mbar_init(&bars->s_free[i], 1);
     }
     bars->abort = 0;
@@ -612,8 +607,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lead) {
           const uint32_t v_s = sbase + C::kOffV + vr.slot * C::kTile;
           const uint32_t p = tmem + buf.slot * kTK;  // two keys per column
-          const uint32_t o = tmem + C::kColO + static_cast<uint32_t>(t & 1) * D;
-          const bool fresh = t - begin < 2;  // the group's first tile of the segment
+          const uint32_t o = tmem + C::kColO;
+          const bool fresh = t == begin;
           uint64_t db = sdesc_mn_sw128(v_s, C::kPiece);
 #pragma unroll kUnrollMma
           for (int kk = 0; kk < kTK / 16; ++kk, db += 2048 >> 4) mma_ts(o, p + kk * 8, db, idesc, !(fresh && kk == 0));
@@ -671,11 +666,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       query_rows(0, (warp - kWarpSm0) * 16, 16);
       if (lane == 0) mbar_arrive(&bars->q0_full);
     }
-    const int grp = (warp - kWarpSm0) >> 2;  // tiles grp, grp + 2, ... of the run
+    const int grp = (warp - kWarpSm0) >> 2;  // rows 16 grp .. of the lane quarter's 32
     const int quarter = warp & 3, r = quarter * 32 + lane;
-    const uint32_t lane_bits = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t o_at = tmem + lane_bits + C::kColO + static_cast<uint32_t>(grp) * D;
     const int g8 = lane >> 2, t4 = lane & 3;
+    const int r16 = quarter * 32 + 16 * grp + g8;  // this thread's rows: r16, r16 + 8
+    const uint32_t lane_bits = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t at16 = tmem + (static_cast<uint32_t>(quarter * 32 + 16 * grp) << 16);
     bool ok = true;
     int t = 0, ks_slot = 0, vs_slot = 0;
     uint32_t ks_phase = 0, vs_phase = 0;
@@ -685,181 +681,161 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Seg& sg = bars->seg[seg % kMaxSegs];
       const int rows = min(kRT, sg.s.n * a.G - sg.rt * kRT);
       const int end = t + sg.tiles;
-      // of rows 32 quarter + 16 h + g8 + 8 x: first key (of the tile at hand) not seen, maximum, sum of this thread's
-      // keys, log2 of O's unit
+      // of rows r16 + 8 x: first key (of the tile at hand) not seen, maximum, sum of this thread's keys, log2 of O's unit
       struct RowState {
         int left;
         float m, l, unit;
-      } st[2][2];
+      } st[2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-          st[h][x] = RowState{row_limit(a, sg.s, sg.rt * kRT + min(quarter * 32 + 16 * h + g8 + 8 * x, rows - 1)) - sg.kt0 * kTK,
-                              -INFINITY, 0.f, -INFINITY};
-      bool any = false;
+      for (int x = 0; x < 2; ++x)
+        st[x] = RowState{row_limit(a, sg.s, sg.rt * kRT + min(r16 + 8 * x, rows - 1)) - sg.kt0 * kTK, -INFINITY, 0.f, -INFINITY};
+      const int begin = t;
       for (; t < end; ++t) {
-        if ((t & 1) == grp) {
-          if (!warp_wait(&bars->s_full[buf.slot], buf.phase, abort, a.err)) { ok = false; break; }
-          const uint32_t s_at = tmem + lane_bits + buf.slot * kTK;
-          const float *ks = nullptr, *vs = nullptr;
-          if constexpr (INT8) {
-            if (!warp_wait2(&bars->ks_full[ks_slot], ks_phase, &bars->vs_full[vs_slot], vs_phase, abort, a.err)) { ok = false; break; }
-            ks = reinterpret_cast<const float*>(smem + C::kOffKS) + ks_slot * kTK + 2 * t4;
-            vs = reinterpret_cast<const float*>(smem + C::kOffVS) + vs_slot * 2 * kTK + 2 * t4;
-          }
-          tc_fence_after();
-          // 16 rows at a time: their state is st[0], the other rows' st[1], exchanged after each
-#pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t half = static_cast<uint32_t>(16 * h) << 16;
-            float fac[2] = {a.scale_log2, a.scale_log2};
-            if constexpr (INT8) {
-              // the query rows' factors were written before q_full, which the scores waited for
-              const float* qf = &bars->qfac[seg & 3][quarter * 32 + 16 * h + g8];
-              fac[0] *= qf[0];
-              fac[1] *= qf[8];
-            }
-            const uint64_t fac2[2] = {f32x2_pack(__float_as_uint(fac[0]), __float_as_uint(fac[0])),
-                                      f32x2_pack(__float_as_uint(fac[1]), __float_as_uint(fac[1]))};
-            // scales are loaded in one go ahead of their use: a load before each use waited for it 48 times a half
-            uint64_t f[16];
-            if constexpr (INT8) {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) f[i] = *reinterpret_cast<const uint64_t*>(ks + 8 * i);
-            }
-            // the rows' scores, scaled (INT8) and masked: register 4 i + 2 x + e is key 8 i + 2 t4 + e of row g8 + 8 x
-            uint32_t sv[64];
-            tmem_ld_frag(s_at + half, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
-            tmem_ld_frag(s_at + half + 64, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
-            tmem_wait_ld();
-            if constexpr (INT8) {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                  const uint64_t y = f32x2_mul(f32x2_pack(sv[4 * i + 2 * x], sv[4 * i + 2 * x + 1]), f[i]);
-                  sv[4 * i + 2 * x] = static_cast<uint32_t>(y);
-                  sv[4 * i + 2 * x + 1] = static_cast<uint32_t>(y >> 32);
-                }
-              }
-            }
-            if (__any_sync(0xffffffffu, min(st[0][0].left, st[0][1].left) < kTK)) {
-#pragma unroll
-              for (int e = 0; e < 64; ++e)
-                if (8 * (e >> 2) + 2 * t4 + (e & 1) >= st[0][(e >> 1) & 1].left) sv[e] = 0xff800000u;  // -inf
-            }
-            // the rows' maxima; INT8: also log2 of their largest e^score times value scale
-            float top[2] = {-INFINITY, -INFINITY}, topv[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              float other = -INFINITY;  // two chains
-#pragma unroll
-              for (int i = 0; i < 16; i += 2) {
-                top[x] = fmaxf(fmaxf(top[x], __uint_as_float(sv[4 * i + 2 * x])), __uint_as_float(sv[4 * i + 2 * x + 1]));
-                other = fmaxf(fmaxf(other, __uint_as_float(sv[4 * i + 4 + 2 * x])), __uint_as_float(sv[4 * i + 4 + 2 * x + 1]));
-              }
-              top[x] = fmaxf(top[x], other);
-            }
-            if constexpr (INT8) {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) f[i] = *reinterpret_cast<const uint64_t*>(vs + kTK + 8 * i);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                  const uint64_t y = f32x2_fma(f32x2_pack(sv[4 * i + 2 * x], sv[4 * i + 2 * x + 1]), fac2[x], f[i]);
-                  topv[x] = fmaxf(fmaxf(topv[x], lo32(y)), hi32(y));
-                }
-              }
-            }
-            float alpha[2] = {1.f, 1.f}, lift[2] = {1.f, 1.f};
-            uint64_t neg2[2], l2[2] = {0ull, 0ull};
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-#pragma unroll
-              for (int d = 1; d < 4; d <<= 1) {
-                top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], d));
-                if constexpr (INT8) topv[x] = fmaxf(topv[x], __shfl_xor_sync(0xffffffffu, topv[x], d));
-              }
-              top[x] *= fac[x];
-              RowState& rs = st[0][x];
-              if constexpr (!INT8) {
-                if (top[x] > rs.m + kRescaleLog2 || rs.m == -INFINITY) {
-                  const float n = fmaxf(rs.m, top[x]);
-                  alpha[x] = n == -INFINITY ? 1.f : ex2(rs.m - n);  // 0 where nothing was seen before
-                  rs.l *= alpha[x];
-                  rs.m = n;
-                }
-              } else {
-                const float n = fmaxf(rs.m, top[x]);
-                rs.l *= n == -INFINITY ? 1.f : ex2(rs.m - n);
-                rs.m = n;
-                // held within 2^100 of e^m so that the lift stays finite
-                const float at = fmaxf(topv[x], n - 100.f);
-                if (n != -INFINITY && at > rs.unit + 1.f) {
-                  alpha[x] = ex2(rs.unit - at);  // 0 from -inf
-                  rs.unit = at;
-                }
-                lift[x] = rs.unit == -INFINITY ? 0.f : ex2(n - rs.unit + 14.f);
-              }
-              const float base = rs.m == -INFINITY ? 0.f : rs.m;
-              neg2[x] = f32x2_pack(__float_as_uint(-base), __float_as_uint(-base));
-            }
-            if (any && __any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
-              // O_grp holds this group's earlier products: the last, P V of tile t - 2, has to be complete
-              if (!warp_wait(&bars->s_free[(t - 2) % C::kBufs], ((t - 2) / C::kBufs) & 1, abort, a.err)) { ok = false; break; }
-              tc_fence_after();
-#pragma unroll 1
-              for (int i = 0; i < D; i += 64) {
-                uint32_t o[32];
-                tmem_ld_frag(o_at + half + i, o);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha[(e >> 1) & 1]);
-                tmem_st_frag(o_at + half + i, o);
-              }
-            }
-            if constexpr (INT8) {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) f[i] = *reinterpret_cast<const uint64_t*>(vs + 8 * i);
-            }
-            // p = 2^(s fac - m), two keys per packed operation, its sum, and P, two keys a column, over the first half of
-            // the rows' S columns
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-#pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                const uint64_t e2 = f32x2_fma(f32x2_pack(sv[4 * i + 2 * x], sv[4 * i + 2 * x + 1]), fac2[x], neg2[x]);
-                uint64_t p2 = f32x2_pack(__float_as_uint(ex2(lo32(e2))), __float_as_uint(ex2(hi32(e2))));
-                l2[x] = f32x2_add(l2[x], p2);
-                if constexpr (INT8)
-                  p2 = f32x2_mul(f32x2_mul(p2, f[i]), f32x2_pack(__float_as_uint(lift[x]), __float_as_uint(lift[x])));
-                sv[2 * i + x] = INT8 ? half2_bits(lo32(p2), hi32(p2)) : pack_bf16x2(lo32(p2), hi32(p2));
-              }
-            }
-            tmem_st_pairs(s_at + half, *reinterpret_cast<uint32_t(*)[16]>(&sv[0]));
-            tmem_st_pairs(s_at + half + 32, *reinterpret_cast<uint32_t(*)[16]>(&sv[16]));
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              st[0][x].l += lo32(l2[x]) + hi32(l2[x]);
-              const RowState other = st[1][x];
-              st[1][x] = st[0][x];
-              st[0][x] = other;
-            }
-          }
-          if (!ok) break;
-          any = true;
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars->p_full[buf.slot]);
+        if (!warp_wait(&bars->s_full[buf.slot], buf.phase, abort, a.err)) { ok = false; break; }
+        const uint32_t s_at = at16 + buf.slot * kTK;
+        const float *ks = nullptr, *vs = nullptr;
+        if constexpr (INT8) {
+          if (!warp_wait2(&bars->ks_full[ks_slot], ks_phase, &bars->vs_full[vs_slot], vs_phase, abort, a.err)) { ok = false; break; }
+          ks = reinterpret_cast<const float*>(smem + C::kOffKS) + ks_slot * kTK + 2 * t4;
+          vs = reinterpret_cast<const float*>(smem + C::kOffVS) + vs_slot * 2 * kTK + 2 * t4;
         }
+        tc_fence_after();
+        float fac[2] = {a.scale_log2, a.scale_log2};
+        if constexpr (INT8) {
+          // the query rows' factors were written before q_full, which the scores waited for
+          const float* qf = &bars->qfac[seg & 3][r16];
+          fac[0] *= qf[0];
+          fac[1] *= qf[8];
+        }
+        const uint64_t fac2[2] = {f32x2_pack(__float_as_uint(fac[0]), __float_as_uint(fac[0])),
+                                  f32x2_pack(__float_as_uint(fac[1]), __float_as_uint(fac[1]))};
+        // scales are loaded in one go ahead of their use: a load before each use waited for it 48 times a half
+        uint64_t f[16];
+        if constexpr (INT8) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) f[i] = *reinterpret_cast<const uint64_t*>(ks + 8 * i);
+        }
+        // the rows' scores, scaled (INT8) and masked: register 4 i + 2 x + e is key 8 i + 2 t4 + e of row g8 + 8 x
+        uint32_t sv[64];
+        tmem_ld_frag(s_at, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
+        tmem_ld_frag(s_at + 64, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
+        tmem_wait_ld();
+        if constexpr (INT8) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const uint64_t y = f32x2_mul(f32x2_pack(sv[4 * i + 2 * x], sv[4 * i + 2 * x + 1]), f[i]);
+              sv[4 * i + 2 * x] = static_cast<uint32_t>(y);
+              sv[4 * i + 2 * x + 1] = static_cast<uint32_t>(y >> 32);
+            }
+          }
+        }
+        if (__any_sync(0xffffffffu, min(st[0].left, st[1].left) < kTK)) {
+#pragma unroll
+          for (int e = 0; e < 64; ++e)
+            if (8 * (e >> 2) + 2 * t4 + (e & 1) >= st[(e >> 1) & 1].left) sv[e] = 0xff800000u;  // -inf
+        }
+        // the rows' maxima; INT8: also log2 of their largest e^score times value scale
+        float top[2] = {-INFINITY, -INFINITY}, topv[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          float other = -INFINITY;  // two chains
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) {
+            top[x] = fmaxf(fmaxf(top[x], __uint_as_float(sv[4 * i + 2 * x])), __uint_as_float(sv[4 * i + 2 * x + 1]));
+            other = fmaxf(fmaxf(other, __uint_as_float(sv[4 * i + 4 + 2 * x])), __uint_as_float(sv[4 * i + 4 + 2 * x + 1]));
+          }
+          top[x] = fmaxf(top[x], other);
+        }
+        if constexpr (INT8) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) f[i] = *reinterpret_cast<const uint64_t*>(vs + kTK + 8 * i);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const uint64_t y = f32x2_fma(f32x2_pack(sv[4 * i + 2 * x], sv[4 * i + 2 * x + 1]), fac2[x], f[i]);
+              topv[x] = fmaxf(fmaxf(topv[x], lo32(y)), hi32(y));
+            }
+          }
+        }
+        float alpha[2] = {1.f, 1.f}, lift[2] = {1.f, 1.f};
+        uint64_t neg2[2], l2[2] = {0ull, 0ull};
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+#pragma unroll
+          for (int d = 1; d < 4; d <<= 1) {
+            top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], d));
+            if constexpr (INT8) topv[x] = fmaxf(topv[x], __shfl_xor_sync(0xffffffffu, topv[x], d));
+          }
+          top[x] *= fac[x];
+          RowState& rs = st[x];
+          if constexpr (!INT8) {
+            if (top[x] > rs.m + kRescaleLog2 || rs.m == -INFINITY) {
+              const float n = fmaxf(rs.m, top[x]);
+              alpha[x] = n == -INFINITY ? 1.f : ex2(rs.m - n);  // 0 where nothing was seen before
+              rs.l *= alpha[x];
+              rs.m = n;
+            }
+          } else {
+            const float n = fmaxf(rs.m, top[x]);
+            rs.l *= n == -INFINITY ? 1.f : ex2(rs.m - n);
+            rs.m = n;
+            // held within 2^100 of e^m so that the lift stays finite
+            const float at = fmaxf(topv[x], n - 100.f);
+            if (n != -INFINITY && at > rs.unit + 1.f) {
+              alpha[x] = ex2(rs.unit - at);  // 0 from -inf
+              rs.unit = at;
+            }
+            lift[x] = rs.unit == -INFINITY ? 0.f : ex2(n - rs.unit + 14.f);
+          }
+          const float base = rs.m == -INFINITY ? 0.f : rs.m;
+          neg2[x] = f32x2_pack(__float_as_uint(-base), __float_as_uint(-base));
+        }
+        if (t > begin && __any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+          // the product before has to be complete
+          if (!warp_wait(&bars->s_free[(t - 1) % C::kBufs], ((t - 1) / C::kBufs) & 1, abort, a.err)) { ok = false; break; }
+          tc_fence_after();
+#pragma unroll 1
+          for (int i = 0; i < D; i += 64) {
+            uint32_t o[32];
+            tmem_ld_frag(at16 + C::kColO + i, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha[(e >> 1) & 1]);
+            tmem_st_frag(at16 + C::kColO + i, o);
+          }
+        }
+        if constexpr (INT8) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) f[i] = *reinterpret_cast<const uint64_t*>(vs + 8 * i);
+        }
+        // p = 2^(s fac - m), two keys per packed operation, its sum, and P, two keys a column, over the first half of
+        // the rows' S columns
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const uint64_t e2 = f32x2_fma(f32x2_pack(sv[4 * i + 2 * x], sv[4 * i + 2 * x + 1]), fac2[x], neg2[x]);
+            uint64_t p2 = f32x2_pack(__float_as_uint(ex2(lo32(e2))), __float_as_uint(ex2(hi32(e2))));
+            l2[x] = f32x2_add(l2[x], p2);
+            if constexpr (INT8)
+              p2 = f32x2_mul(f32x2_mul(p2, f[i]), f32x2_pack(__float_as_uint(lift[x]), __float_as_uint(lift[x])));
+            sv[2 * i + x] = INT8 ? half2_bits(lo32(p2), hi32(p2)) : pack_bf16x2(lo32(p2), hi32(p2));
+          }
+        }
+        tmem_st_pairs(s_at, *reinterpret_cast<uint32_t(*)[16]>(&sv[0]));
+        tmem_st_pairs(s_at + 32, *reinterpret_cast<uint32_t(*)[16]>(&sv[16]));
+#pragma unroll
+        for (int x = 0; x < 2; ++x) st[x].l += lo32(l2[x]) + hi32(l2[x]);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->p_full[buf.slot]);
         buf.advance(C::kBufs);
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int x = 0; x < 2; ++x) st[h][x].left -= kTK;
+        for (int x = 0; x < 2; ++x) st[x].left -= kTK;
         if constexpr (INT8) {
           if (++ks_slot == C::kScalesK) {
             ks_slot = 0;
@@ -872,56 +848,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) break;
-      // ---- the segment's end: both groups' parts of a row meet ----
+      // ---- the segment's end ----
       const int par = seg & 1;
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          float sum = st[h][x].l;
-          sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-          sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-          if (t4 == 0) {
-            const int row = quarter * 32 + 16 * h + g8 + 8 * x;
-            bars->st_m[par][grp][row] = st[h][x].m;
-            bars->st_l[par][grp][row] = sum;
-            bars->st_u[par][grp][row] = INT8 && st[h][x].unit != -INFINITY ? st[h][x].unit - st[h][x].m - 14.f : 0.f;
-          }
+      for (int x = 0; x < 2; ++x) {
+        float sum = st[x].l;
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        if (t4 == 0) {
+          bars->st_m[par][r16 + 8 * x] = st[x].m;
+          bars->st_l[par][r16 + 8 * x] = sum;
+          bars->st_u[par][r16 + 8 * x] = INT8 && st[x].unit != -INFINITY ? st[x].unit - st[x].m - 14.f : 0.f;
         }
-      bars->st_any[par][grp] = any;  // the same for all rows
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->fin[quarter]);
       if (!warp_wait(&bars->fin[quarter], par, abort, a.err)) break;
       if (!warp_wait(&bars->o_full, par, abort, a.err)) break;
       tc_fence_after();
-      const float gm0 = bars->st_m[par][0][r], gm1 = bars->st_m[par][1][r];
-      const float M = fmaxf(gm0, gm1);  // a group without tiles has -inf
-      const float bs = M == -INFINITY ? 0.f : M;
-      const float L = ex2(gm0 - bs) * bars->st_l[par][0][r] + ex2(gm1 - bs) * bars->st_l[par][1][r];
+      const float M = bars->st_m[par][r], L = bars->st_l[par][r];
       const bool whole = sg.whole != 0;
       const float inv = whole ? (L == 0.f ? 0.f : 1.f / L) : 1.f;
-      const float f0 = ex2(gm0 - bs + bars->st_u[par][0][r]) * inv, f1 = ex2(gm1 - bs + bars->st_u[par][1][r]) * inv;
-      const bool has0 = bars->st_any[par][0] != 0, has1 = bars->st_any[par][1] != 0;
+      const float f = ex2(bars->st_u[par][r]) * inv;
       const size_t row = out_row<kRT>(a, sg.s, sg.g, sg.rt, min(r, rows - 1));
       const long long pslot = 2ll * blockIdx.x + (sg.kt0 > 0 ? 0 : 1);
-      // group g writes columns g D/2 ... of its quarter's rows, 32 at a time
+      // warp grp of a quarter writes columns grp D/2 ... of its 32 rows, 32 at a time
 #pragma unroll 1
       for (int i = 0; i < D / 2; i += 32) {
         const int col = grp * (D / 2) + i;
         float v[32];
         uint32_t o[32];
-        if (has0) {
-          tmem_ld32(tmem + lane_bits + C::kColO + col, o);
-          tmem_wait_ld();
-        }
+        tmem_ld32(tmem + lane_bits + C::kColO + col, o);
+        tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] = has0 ? __uint_as_float(o[e]) * f0 : 0.f;
-        if (has1) {
-          tmem_ld32(tmem + lane_bits + C::kColO + D + col, o);
-          tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = fmaf(__uint_as_float(o[e]), f1, v[e]);
-        }
+        for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(o[e]) * f;
         if (r < rows) {
           if (whole) {
             uint4* dst = reinterpret_cast<uint4*>(a.out + row * D + col);
