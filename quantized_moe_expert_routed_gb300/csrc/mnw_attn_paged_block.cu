@@ -98,9 +98,7 @@ struct Bars {
   uint64_t o_full, epi;                 // a segment's output complete; read
   uint64_t ks_full[kMaxKScales], vs_full[kMaxVScales];
   uint64_t seg_full[kMaxSegs];
-  uint64_t fin[4];                      // per lane quarter: both warps' maxima and sums written
   uint64_t drain[2];
-  float st_m[2][kRT], st_l[2][kRT], st_u[2][kRT];  // [segment parity][row]: maximum, sum, log2 of O's unit over 2^maximum
   float qfac[4][kRT];                   // [segment % 4] INT8: the query rows' powers of two
   Seg seg[kMaxSegs];
   uint32_t tmem_base;
@@ -264,7 +262,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kMaxKScales; ++i) mbar_init(&bars->ks_full[i], 2);
     for (int i = 0; i < kMaxVScales; ++i) mbar_init(&bars->vs_full[i], 2);
     for (int i = 0; i < kMaxSegs; ++i) mbar_init(&bars->seg_full[i], 1);
-    for (int i = 0; i < 4; ++i) mbar_init(&bars->fin[i], 2);
     for (int i = 0; i < kMaxBufs; ++i) {
       mbar_init(&bars->s_full[i], 1);
       mbar_init(&bars->p_full[i], 8);
@@ -667,10 +664,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&bars->q0_full);
     }
     const int grp = (warp - kWarpSm0) >> 2;  // rows 16 grp .. of the lane quarter's 32
-    const int quarter = warp & 3, r = quarter * 32 + lane;
+    const int quarter = warp & 3;
     const int g8 = lane >> 2, t4 = lane & 3;
     const int r16 = quarter * 32 + 16 * grp + g8;  // this thread's rows: r16, r16 + 8
-    const uint32_t lane_bits = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t at16 = tmem + (static_cast<uint32_t>(quarter * 32 + 16 * grp) << 16);
     bool ok = true;
     int t = 0, ks_slot = 0, vs_slot = 0;
@@ -849,58 +845,50 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       // ---- the segment's end ----
-      const int par = seg & 1;
+      const bool whole = sg.whole != 0;
+      const long long pslot = 2ll * blockIdx.x + (sg.kt0 > 0 ? 0 : 1);
+      float f[2];
+      size_t row[2];
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        float sum = st[x].l;
+        const RowState& rs = st[x];
+        float sum = rs.l;
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        if (t4 == 0) {
-          bars->st_m[par][r16 + 8 * x] = st[x].m;
-          bars->st_l[par][r16 + 8 * x] = sum;
-          bars->st_u[par][r16 + 8 * x] = INT8 && st[x].unit != -INFINITY ? st[x].unit - st[x].m - 14.f : 0.f;
+        f[x] = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
+        if (INT8 && rs.unit != -INFINITY) f[x] *= ex2(rs.unit - rs.m - 14.f);
+        const int r = r16 + 8 * x;
+        row[x] = out_row<kRT>(a, sg.s, sg.g, sg.rt, min(r, rows - 1));
+        if (r < rows && t4 == 0) {
+          if (!whole)
+            __stcg(a.part_ml + pslot * kRT + r, make_float2(rs.m, sum));
+          else if (a.lse)
+            a.lse[row[x]] = (rs.m + log2f(sum)) * kLn2;
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->fin[quarter]);
-      if (!warp_wait(&bars->fin[quarter], par, abort, a.err)) break;
-      if (!warp_wait(&bars->o_full, par, abort, a.err)) break;
+      if (!warp_wait(&bars->o_full, seg & 1, abort, a.err)) break;
       tc_fence_after();
-      const float M = bars->st_m[par][r], L = bars->st_l[par][r];
-      const bool whole = sg.whole != 0;
-      const float inv = whole ? (L == 0.f ? 0.f : 1.f / L) : 1.f;
-      const float f = ex2(bars->st_u[par][r]) * inv;
-      const size_t row = out_row<kRT>(a, sg.s, sg.g, sg.rt, min(r, rows - 1));
-      const long long pslot = 2ll * blockIdx.x + (sg.kt0 > 0 ? 0 : 1);
-      // warp grp of a quarter writes columns grp D/2 ... of its 32 rows, 32 at a time
 #pragma unroll 1
-      for (int i = 0; i < D / 2; i += 32) {
-        const int col = grp * (D / 2) + i;
-        float v[32];
+      for (int i = 0; i < D; i += 64) {
         uint32_t o[32];
-        tmem_ld32(tmem + lane_bits + C::kColO + col, o);
+        tmem_ld_frag(at16 + C::kColO + i, o);
         tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(o[e]) * f;
-        if (r < rows) {
-          if (whole) {
-            uint4* dst = reinterpret_cast<uint4*>(a.out + row * D + col);
+        for (int x = 0; x < 2; ++x) {
+          if (r16 + 8 * x < rows) {
+            if (whole) {
+              uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + row[x] * D + i + 2 * t4);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              dst[e] = make_uint4(pack_bf16x2(v[8 * e], v[8 * e + 1]), pack_bf16x2(v[8 * e + 2], v[8 * e + 3]),
-                                  pack_bf16x2(v[8 * e + 4], v[8 * e + 5]), pack_bf16x2(v[8 * e + 6], v[8 * e + 7]));
-          } else {
-            float4* dst = reinterpret_cast<float4*>(a.part_o + (pslot * kRT + r) * D + col);
+              for (int j = 0; j < 8; ++j)
+                dst[4 * j] = pack_bf16x2(__uint_as_float(o[4 * j + 2 * x]) * f[x], __uint_as_float(o[4 * j + 2 * x + 1]) * f[x]);
+            } else {
+              float2* dst = reinterpret_cast<float2*>(a.part_o + (pslot * kRT + r16 + 8 * x) * D + i + 2 * t4);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) __stcg(dst + e, make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]));
+              for (int j = 0; j < 8; ++j)
+                __stcg(dst + 4 * j, make_float2(__uint_as_float(o[4 * j + 2 * x]) * f[x], __uint_as_float(o[4 * j + 2 * x + 1]) * f[x]));
+            }
           }
         }
-      }
-      if (r < rows && grp == 0) {
-        if (!whole)
-          __stcg(a.part_ml + pslot * kRT + r, make_float2(M, L));
-        else if (a.lse)
-          a.lse[row] = (M + log2f(L)) * kLn2;
       }
       tc_fence_before();
       __syncwarp();
