@@ -489,11 +489,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             wait_copies<0>();
             __syncwarp();
           } else {
-            if (!warp_wait(raw_full, raw_phase, abort, a.err)) { ok = false; break; }
+            if (!(values ? warp_wait(raw_full, raw_phase, abort, a.err)
+                         : warp_wait2(raw_full, raw_phase, &empty[ring.slot], ring.phase ^ 1, abort, a.err))) { ok = false; break; }
             raw_phase ^= 1;
             bulk_out = false;
           }
-          // the scales are given on at once: the softmax of a tile runs while its values still wait for their operand slot
+          // the values' scales are given on at once: the softmax of a tile runs while its values still wait for their slot
           if (values) {
             float* sc = reinterpret_cast<float*>(smem + scales_at(sc_now)) + lw * 64 + lane;
             sc[kTK] = __log2f(sc[0]);
@@ -502,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (lane == 0) mbar_arrive(values ? &bars->vs_full[sc_now] : &bars->ks_full[sc_now]);
           if (++sc_now == sc_slots) sc_now = 0;
-          if (!warp_wait(&empty[ring.slot], ring.phase ^ 1, abort, a.err)) { ok = false; break; }
+          if ((values || landing_rows) && !warp_wait(&empty[ring.slot], ring.phase ^ 1, abort, a.err)) { ok = false; break; }
         }
         uint8_t* op = smem + ring_at + ring.slot * C::kTile + lw * 64 * 128;
         const uint8_t* raw = smem + raw_at + lw * 64 * D + lane * 8;
