@@ -10,12 +10,17 @@
 //
 // Bound: every cached key and value is read once for all rows of its kv head
 // (n * Hq / Hkv query rows), so up to ~100 rows the reads of the cache are the
-// floor.
+// floor.  Measured on one GB300: 2 single tokens over 200,000 BF16 positions, 32
+// query and 8 key heads of 128 (1.64 GB): 245 us, 6.7 TB/s, the copy rate;
+// 32 over 2048 to 8192 positions in pages of 16, 16 and 4 heads (336 MB): 66 us,
+// 5.1 TB/s, of which ~10 us are the head (split, first page lookups) and the
+// joining kernel; one over 777 positions: 7.9 us, the chain split -> page ->
+// tile -> products -> join.
 //
 // The work's split over CTAs and the joining of its parts: mnw_attn_split.cuh.
 //
-// A CTA is WR x WK warps: WR row blocks of 16 query rows, each tile's keys cut
-// over WK warps.  Tiles arrive by 16-byte cp.async through a ring of kStages
+// Up to 16 query rows (INT8: 32) go here, more to the block kernel.  A CTA is
+// WR x WK warps: WR row blocks of 16 query rows, each tile's keys cut over WK warps.  Tiles arrive by 16-byte cp.async through a ring of kStages
 // stages, one page lookup per row piece, so pages of any size may end inside
 // a tile; rows past the length are filled with zeros (a masked probability of
 // 0 then meets a finite value, whatever the page holds there).  Both products
@@ -42,8 +47,6 @@
 
 namespace mnw {
 namespace pattn {
-
-constexpr int kMinUnits = 1;  // tiles of a run at least
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -529,12 +532,21 @@ __global__ void __launch_bounds__(WR* WK * 32) paged_attn_kernel(const Args a) {
 
 // ---- host ----
 
-// Row tile for `rows` query rows per (sequence, kv head) on average.
-inline int row_tile(long long rows) { return rows <= 16 ? 16 : (rows <= 32 ? 32 : kBlockRows); }
+// Row tile for `rows` query rows per (sequence, kv head) on average: the block
+// kernel where a warp-level tile would have to read the cache's tiles again for
+// each 16 rows.  BF16, 32 rows: 2 sequences of 200,000 positions 275 us
+// warp-level, 247 block; 16 of up to 4000 27 and 22; at 16 rows 250 and 246, 23
+// and 22, with 64-wide heads 42 and 44.  INT8, where the block kernel has to
+// convert the codes: 32 rows 335 and 537, 34 and 40; 64 rows 54 and 40.
+inline int row_tile(long long rows, bool int8) { return rows <= 16 ? 16 : (int8 && rows <= 32 ? 32 : kBlockRows); }
 // CTAs resident on an SM
 inline int runs_per_sm(int rt) { return rt == kBlockRows ? 1 : 2; }
-// The last arrival joins where an item's parts are few: this many rows x parts of an item
-constexpr int kFusedRows = 512;
+// The last arrival joins items of at most this many rows (on average over the
+// sequences), which its threads take in one pass: no slower on the GPU (one token over 777 positions 7.7 us
+// either way, 2 over 200,000 246.5 and 247.3) and a launch (2 us of the
+// host's time) less.  With more rows the joining kernel is faster: 8 rows 249.4
+// and 248.1 us, 16 rows of 16 sequences 27.2 and 23.3 us, 32 rows 34.1 and 26.8.
+constexpr int kFusedRows = 4;
 
 inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 inline int max_runs(int rt) { return runs_per_sm(rt) * current_sm_count(); }
@@ -572,16 +584,14 @@ inline bool plan(Args& a, int rt, int tk, int d, uint8_t* ws, int* runs, bool* s
   a.starts = reinterpret_cast<int*>(ws + w.starts);
   a.part_ml = reinterpret_cast<float2*>(ws + w.ml);
   a.part_o = reinterpret_cast<float*>(ws + w.o);
-  a.min_units = kMinUnits;
   // most units that the batch can have: every row tile over a full block table
   const long long kt = (static_cast<long long>(a.bt.max_pages) * a.page_size + tk - 1) / tk;
   const long long items = (static_cast<long long>(a.bt.T) * a.G / rt + a.bt.B) * a.Hkv, units = items * kt;
   const int most = max_runs(rt);
   if (units > 0x7fffffffll - most) return false;
-  *runs = static_cast<int>(std::min<long long>(most, (units + kMinUnits - 1) / kMinUnits));
+  *runs = static_cast<int>(std::min<long long>(most, units));
   *shared = kt > 1;  // items of one tile are never shared
-  const long long rows = std::min<long long>(rt, static_cast<long long>(a.bt.T) * a.G);
-  a.fused = rt != kBlockRows && rows * ((*runs + items - 1) / items) <= kFusedRows;
+  a.fused = rt != kBlockRows && (a.bt.T + a.bt.B - 1) / a.bt.B * a.G <= kFusedRows;
   a.tag = next_tag();
   return true;
 }
@@ -614,7 +624,9 @@ int launch(Args& a, uint8_t* ws, cudaStream_t st) {
 template <int D, bool INT8>
 int launch_rows(Args& a, uint8_t* ws, int rt, cudaStream_t st) {
   if (rt == 16) return launch<D, INT8, 1, 4>(a, ws, st);
-  if (rt == 32) return launch<D, INT8, 2, 2>(a, ws, st);
+  if constexpr (INT8) {
+    if (rt == 32) return launch<D, INT8, 2, 2>(a, ws, st);
+  }
   int runs;
   bool shared;
   if (!plan(a, kBlockRows, kBlockKeys, D, ws, &runs, &shared)) return MNW_E_UNSUPPORTED;
@@ -631,8 +643,9 @@ extern "C" {
 
 size_t mnw_attn_paged_workspace_size(int B, int T, int Hq, int Hkv, int d) {
   if (B <= 0 || T <= 0 || Hq <= 0 || Hkv <= 0 || d <= 0 || Hq % Hkv) return 0;
-  const int rt = pattn::row_tile((static_cast<long long>(T) + B - 1) / B * (Hq / Hkv));
-  return pattn::workspace_of(B, rt, d).bytes;
+  const long long rows = (static_cast<long long>(T) + B - 1) / B * (Hq / Hkv);
+  return std::max(pattn::workspace_of(B, pattn::row_tile(rows, false), d).bytes,
+                  pattn::workspace_of(B, pattn::row_tile(rows, true), d).bytes);
 }
 
 int mnw_attn_paged(const void* q, long long q_stride, int B, int T, int Hq, int Hkv, int d, const void* k_cache,
@@ -677,7 +690,7 @@ int mnw_attn_paged(const void* q, long long q_stride, int B, int T, int Hq, int 
   a.out = static_cast<__nv_bfloat16*>(out);
   a.lse = lse;
   a.err = err;
-  const int rt = row_tile((static_cast<long long>(T) + B - 1) / B * a.G);
+  const int rt = row_tile((static_cast<long long>(T) + B - 1) / B * a.G, int8);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   auto* w = static_cast<uint8_t*>(ws);
   if (d == 128) return int8 ? launch_rows<128, true>(a, w, rt, st) : launch_rows<128, false>(a, w, rt, st);

@@ -10,8 +10,8 @@
 // continues an item, 2c + 1 for one that begins it.
 //
 // Joining: parts are added in run order, so the result does not depend on
-// timing.  Few parts and rows: the CTA that arrives last at an item joins it
-// (a launch less).  Otherwise a second kernel does.  A part that is written is
+// timing.  Items of a few rows: the CTA that arrives last at an item joins it
+// (a launch less).  Otherwise a second kernel does, over the whole GPU.  A part that is written is
 // marked with the call's number, so the workspace needs no clearing: a mark of
 // another call, or anything else, is none; the joining CTA clears the item's
 // marks (a replayed graph brings the same number).
@@ -45,7 +45,6 @@ struct Args {
   FastDiv page_div;
   FastDiv g_div, blk_div;
   int n_pages, page_size, Hq, Hkv, G, blk;
-  int min_units;  // units of a run at least, where there are few
   float scale_log2;
   __nv_bfloat16* out;
   float* lse;
@@ -87,7 +86,7 @@ __device__ __forceinline__ Shape shape_of(const Seq& s, int G, int Hkv, int pad)
 
 constexpr int kMaxSlack = 4;
 struct SplitShared {
-  int scan[32], pads[kMaxSlack + 1][32];
+  int scan[32], pads[kMaxSlack][32];
   int seq, first;  // sequence of the run's first unit and its first unit
 };
 
@@ -96,11 +95,12 @@ struct Run {
   int seq, first;        // sequence that holds u0 (-1: none) and its first unit
 };
 
-// Where run blockIdx.x begins.  All threads call; ends with a barrier.  Where
-// all items, cut into runs of some length each, fit the grid, runs do not cross
-// items; tried are the shortest runs (latency) and up to SLACK lengths from the equal share
-// on, for a kernel that pays more for a second item in a run than for SLACK
-// more tiles.  Otherwise the runs are equal shares of the units.
+// Where run blockIdx.x begins.  All threads call; ends with a barrier.  Runs
+// are equal shares of the units.  With SLACK > 0, for a kernel that pays more
+// for a second item in a run than for a few more tiles, the SLACK lengths from
+// the equal share on are tried, and the first at which runs that do not cross
+// items fit the grid is taken (block kernel, 16 sequences of up to 4000 INT8
+// positions, 64 items on 152 CTAs: 65 us with equal shares, 56 with SLACK 4).
 template <int RT, int TK, int THREADS, int SLACK>
 __device__ __forceinline__ Run find_run(const Args& a, SplitShared* sh) {
   constexpr int kWarps = THREADS / 32;
@@ -110,38 +110,27 @@ __device__ __forceinline__ Run find_run(const Args& a, SplitShared* sh) {
   const bool scribe = blockIdx.x == 0;  // run 0 reports bad lengths and writes the sequences' first units
   if (tid == 0) sh->seq = -1;
   const int runs = gridDim.x;
-  // runs that the items of sequence s make at p units each (few enough to add up: the sums are clipped)
+  // runs that the items of a sequence make at p units each (clipped: they are added up)
   auto runs_of = [&](const Shape& one, int p) { return min(a.Hkv * one.rt * ((one.kt + p - 1) / p), 1 << 20); };
-  int total = 0, padded = 0;
+  int total = 0;
   Seq s{};
   for (int b = tid; b < bt.B; b += THREADS) {
     bool bad;
     s = paged::sequence(bt, b, a.page_size, &bad);
     if (bad && scribe && a.err) atomicOr(a.err, MNW_DEVERR_BAD_LENGTH);
-    const Shape one = shape_of<RT, TK>(s, a.G, a.Hkv, 1);
-    total += one.units;
-    padded = min(padded + runs_of(one, a.min_units), 1 << 20);
+    total += shape_of<RT, TK>(s, a.G, a.Hkv, 1).units;
   }
-  const int tw = __reduce_add_sync(0xffffffffu, total), pw = __reduce_add_sync(0xffffffffu, padded);
-  if (lane == 0) {
-    sh->scan[warp] = tw;
-    sh->pads[0][warp] = pw;
-  }
+  const int tw = __reduce_add_sync(0xffffffffu, total);
+  if (lane == 0) sh->scan[warp] = tw;
   __syncthreads();
-  total = padded = 0;
+  total = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    total += sh->scan[w];
-    padded += sh->pads[0][w];
-  }
+  for (int w = 0; w < kWarps; ++w) total += sh->scan[w];
   Run r;
-  r.per = max(a.min_units, (total + runs - 1) / runs);
+  r.per = max(1, (total + runs - 1) / runs);
   r.pad = 1;
   int limit = total;
-  if (padded <= runs) {
-    r.pad = r.per = a.min_units;
-    limit = padded * a.min_units;
-  } else if (SLACK > 0) {
+  if (SLACK > 0 && total > runs) {
     int sums[SLACK > 0 ? SLACK : 1];
 #pragma unroll
     for (int k = 0; k < SLACK; ++k) sums[k] = 0;
@@ -155,7 +144,7 @@ __device__ __forceinline__ Run find_run(const Args& a, SplitShared* sh) {
 #pragma unroll
     for (int k = 0; k < SLACK; ++k) {
       const int v = __reduce_add_sync(0xffffffffu, sums[k]);
-      if (lane == 0) sh->pads[k + 1][warp] = v;
+      if (lane == 0) sh->pads[k][warp] = v;
     }
     __syncthreads();
     const int share = r.per;
@@ -163,7 +152,7 @@ __device__ __forceinline__ Run find_run(const Args& a, SplitShared* sh) {
     for (int k = SLACK - 1; k >= 0; --k) {
       int v = 0;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) v += sh->pads[k + 1][w];
+      for (int w = 0; w < kWarps; ++w) v += sh->pads[k][w];
       if (v <= runs) {
         r.pad = r.per = share + k;
         limit = v * (share + k);
@@ -371,8 +360,8 @@ __device__ __forceinline__ void join_row(const Args& a, const Seq& s, const Span
   if (a.lse && j == 0) a.lse[row] = (M + log2f(L)) * kLn2;
 }
 
-// As join_row for at most kFewParts parts (the usual case: runs are about as
-// long as items): all loads go out at once, without a maximum first.
+// As join_row for at most kFewParts parts, the usual case where runs are about
+// as long as items: all loads go out at once, without a maximum first.
 constexpr int kFewParts = 4;
 template <int D, int RT>
 __device__ __forceinline__ void join_few(const Args& a, const Seq& s, const Span& sp, int per, int g, int rt, int r, int col) {
