@@ -40,7 +40,7 @@ using paged::Seq;
 constexpr int kThreads = 256;
 constexpr int kMaxPairs = 64;  // rot <= d <= 128
 constexpr int kMaxTokens = 4;  // of a CTA
-constexpr int kBatch = 6;      // chunks of a thread under way
+constexpr int kBatch = 3;      // pieces of a thread under way
 
 struct Args {
   Batch bt;
@@ -71,22 +71,17 @@ __device__ __forceinline__ float turn_fraction(int p, float f) {
   return r - rintf(r);
 }
 
-// Where pair i's sine and cosine lie: a row's lanes read pairs 8 (half layout)
-// or 4 (interleaved) apart at the same time, which are neighbours here.
-template <bool HALF>
-__device__ __forceinline__ int pair_at(int i) {
-  return HALF ? ((i & 7) << 3) | (i >> 3) : ((i & 3) << 4) | (i >> 2);
-}
-
-// One CTA per `tokens` tokens.  A head row is D/8 chunks of 16 bytes, one
-// thread each, so a row lies in D/8 neighbouring lanes: the other element of
-// a half-layout pair and the row maximum come by shuffles.  kBatch chunks of a
-// thread are under way at a time, and the first batch is requested before the
-// tokens' positions, pages and angles are worked out.
+// One CTA per `tokens` tokens.  A head row is D/16 pieces of two 16-byte
+// chunks, one thread each: the two that hold both elements of 8 rotation pairs
+// (half layout: chunks p and p + rot/16; elsewhere, and past rot, neighbours),
+// so a rotation stays in a thread.  kBatch pieces of a thread are under way at
+// a time, and the first batch is requested before the tokens' positions, pages
+// and angles are worked out.
 template <int D, bool INT8, bool HALF>
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(const Args a) {
-  constexpr int C = D / 8;  // chunks (threads) of a row
-  __shared__ float2 cs[kMaxTokens][kMaxPairs];
+  constexpr int P = D / 16;  // pieces (threads) of a row
+  // sine and cosine, two pairs a word: pairs 8 p + 2 j, 8 p + 2 j + 1 at [j][p], so that a row's lanes read neighbours
+  __shared__ float4 cs[kMaxTokens][4][kMaxPairs / 8];
   __shared__ int page_of[kMaxTokens], slot_of[kMaxTokens];  // the token's page (-1: none) and its slot there
   pdl_launch_dependents();
   pdl_wait();
@@ -96,32 +91,35 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const Args a) {
   const int pairs = a.rot / 2;
   const int q_rows = a.q ? a.Hq : 0;
   const int rows = q_rows + 2 * a.Hkv;  // q heads, k heads, v heads of a token
-  const int total = nt * rows * C;
-  const int c = threadIdx.x % C;  // (kThreads is a multiple of C)
+  const int total = nt * rows * P;
+  const int p = threadIdx.x % P;  // (kThreads is a multiple of P)
+  const bool in_rot = 16 * p < a.rot;
+  const int c0 = HALF && in_rot ? p : 2 * p, c1 = HALF && in_rot ? p + a.rot / 16 : 2 * p + 1;  // chunks
 
   struct Row {
     int tk, row;  // token of the CTA, head row of the token
   };
   auto row_at = [&](int idx) {
-    const int rw = idx / C;
+    const int rw = idx / P;
     Row x;
     x.tk = static_cast<int>(paged::quotient(rw, a.row_div));
     x.row = rw - x.tk * rows;
     return x;
   };
-  uint4 raw[kBatch];
+  uint4 raw[kBatch][2];
   auto load_batch = [&](int base) {
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       const int idx = base + i * kThreads + threadIdx.x;
-      raw[i] = make_uint4(0, 0, 0, 0);
+      raw[i][0] = raw[i][1] = make_uint4(0, 0, 0, 0);
       if (idx < total) {  // a row's lanes are all live or all not
         const Row x = row_at(idx);
         const long long t = t0 + x.tk;
         const __nv_bfloat16* src = x.row < q_rows           ? a.q + t * a.q_stride + x.row * D
                                    : x.row < q_rows + a.Hkv ? a.k + t * a.k_stride + (x.row - q_rows) * D
                                                             : a.v + t * a.v_stride + (x.row - q_rows - a.Hkv) * D;
-        raw[i] = *reinterpret_cast<const uint4*>(src + c * 8);
+        raw[i][0] = *reinterpret_cast<const uint4*>(src + c0 * 8);
+        raw[i][1] = *reinterpret_cast<const uint4*>(src + c1 * 8);
       }
     }
   };
@@ -164,7 +162,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const Args a) {
     for (int i = lane; i < pairs; i += 32) {
       float sn, co;
       sincospif(2.f * turn_fraction(pos, __ldg(a.inv_freq + i)), &sn, &co);
-      cs[warp][pair_at<HALF>(i)] = make_float2(co * a.mscale, sn * a.mscale);
+      reinterpret_cast<float2*>(&cs[warp][(i & 7) >> 1][i >> 3])[i & 1] = make_float2(co * a.mscale, sn * a.mscale);
     }
   }
   __syncthreads();
@@ -181,77 +179,68 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const Args a) {
       const int tk = at.tk, row = at.row;
       const bool is_q = row < q_rows, is_k = !is_q && row < q_rows + a.Hkv;
       const int h = is_q ? row : (is_k ? row - q_rows : row - q_rows - a.Hkv);
-      float x[8];
-      const uint32_t u[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+      uint32_t u[2][4] = {{raw[i][0].x, raw[i][0].y, raw[i][0].z, raw[i][0].w}, {raw[i][1].x, raw[i][1].y, raw[i][1].z, raw[i][1].w}};
+      if (in_rot && (is_q || is_k)) {
+        auto lo = [](uint32_t w) { return __uint_as_float(w << 16); };
+        auto hi = [](uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); };
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        x[2 * j] = __uint_as_float(u[j] << 16);
-        x[2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
-      }
-      const bool turned = live && (is_q || is_k) && c * 8 < a.rot;
-      if constexpr (HALF) {
-        const int hc = pairs / 8;  // chunks in half of the rotated part
-        const bool first = c < hc;
-        const int from = turned ? lane + (first ? hc : -hc) : lane;  // partner chunk's lane
-        const int pi = (first ? c : c - hc) * 8;
-        const uint32_t pu[4] = {__shfl_sync(0xffffffffu, u[0], from), __shfl_sync(0xffffffffu, u[1], from),
-                                __shfl_sync(0xffffffffu, u[2], from), __shfl_sync(0xffffffffu, u[3], from)};
-        if (turned) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float o = (j & 1) ? __uint_as_float(pu[j / 2] & 0xFFFF0000u) : __uint_as_float(pu[j / 2] << 16);
-            const float2 f = cs[tk][pair_at<HALF>(pi + j)];
-            x[j] = x[j] * f.x + o * (first ? -f.y : f.y);
-          }
-        }
-      } else {
-        if (turned) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 f = cs[tk][pair_at<HALF>(c * 4 + j)];
-            const float p = x[2 * j], w = x[2 * j + 1];
-            x[2 * j] = p * f.x - w * f.y;
-            x[2 * j + 1] = w * f.x + p * f.y;
+        for (int j = 0; j < 4; ++j) {  // pairs 8 p + 2 j, 8 p + 2 j + 1
+          const float4 f = cs[tk][j][p];
+          if constexpr (HALF) {
+            const float x0 = lo(u[0][j]), x1 = hi(u[0][j]), w0 = lo(u[1][j]), w1 = hi(u[1][j]);
+            u[0][j] = pack_bf16x2(x0 * f.x - w0 * f.y, x1 * f.z - w1 * f.w);
+            u[1][j] = pack_bf16x2(w0 * f.x + x0 * f.y, w1 * f.z + x1 * f.w);
+          } else {
+            uint32_t &a0 = u[j >> 1][2 * (j & 1)], &a1 = u[j >> 1][2 * (j & 1) + 1];
+            const float x0 = lo(a0), w0 = hi(a0), x1 = lo(a1), w1 = hi(a1);
+            a0 = pack_bf16x2(x0 * f.x - w0 * f.y, w0 * f.x + x0 * f.y);
+            a1 = pack_bf16x2(x1 * f.z - w1 * f.w, w1 * f.z + x1 * f.w);
           }
         }
       }
-      const uint4 out = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                                   pack_bf16x2(x[6], x[7]));
+      const uint4 out0 = make_uint4(u[0][0], u[0][1], u[0][2], u[0][3]), out1 = make_uint4(u[1][0], u[1][1], u[1][2], u[1][3]);
       const int page = page_of[tk];
       const size_t head_row = static_cast<size_t>(h) * a.page_size + slot_of[tk];  // within the page
-      if (is_q && live)
-        *reinterpret_cast<uint4*>(a.q_out + (static_cast<size_t>(t0 + tk) * a.Hq + h) * D + c * 8) = out;
+      if (is_q && live) {
+        __nv_bfloat16* dst = a.q_out + (static_cast<size_t>(t0 + tk) * a.Hq + h) * D;
+        *reinterpret_cast<uint4*>(dst + c0 * 8) = out0;
+        *reinterpret_cast<uint4*>(dst + c1 * 8) = out1;
+      }
       if constexpr (!INT8) {
         if (live && !is_q && page >= 0) {
           __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(is_k ? a.kc : a.vc) + page * a.page_stride + head_row * D;
-          *reinterpret_cast<uint4*>(dst + c * 8) = out;
+          *reinterpret_cast<uint4*>(dst + c0 * 8) = out0;
+          *reinterpret_cast<uint4*>(dst + c1 * 8) = out1;
         }
       } else {
-        float y[8];
-        const uint32_t o[4] = {out.x, out.y, out.z, out.w};
+        float y[2][8];
         float amax = 0.f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          y[2 * j] = __uint_as_float(o[j] << 16);
-          y[2 * j + 1] = __uint_as_float(o[j] & 0xFFFF0000u);
-          amax = fmaxf(amax, fmaxf(fabsf(y[2 * j]), fabsf(y[2 * j + 1])));
-        }
+        for (int e = 0; e < 2; ++e)
 #pragma unroll
-        for (int d = C / 2; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+          for (int j = 0; j < 4; ++j) {
+            y[e][2 * j] = __uint_as_float(u[e][j] << 16);
+            y[e][2 * j + 1] = __uint_as_float(u[e][j] & 0xFFFF0000u);
+            amax = fmaxf(amax, fmaxf(fabsf(y[e][2 * j]), fabsf(y[e][2 * j + 1])));
+          }
+#pragma unroll
+        for (int d = P / 2; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
         if (live && !is_q && page >= 0) {
-          uint32_t packed[2] = {0, 0};
+          uint32_t packed[2][2] = {{0, 0}, {0, 0}};
           float scale = 0.f;
           if (amax > 0.f) {
             scale = __fdiv_rn(amax, 127.0f);
+            const float rs = __frcp_rn(scale);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const int qv = max(-127, min(127, __float2int_rn(__fdiv_rn(y[j], scale))));
-              packed[j >> 2] |= (static_cast<uint32_t>(qv) & 0xFFu) << (8 * (j & 3));
-            }
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                packed[e][j >> 2] |= (static_cast<uint32_t>(int8_code(y[e][j], scale, rs)) & 0xFFu) << (8 * (j & 3));
           }
           uint8_t* dst = (is_k ? a.kc : a.vc) + page * a.page_stride + head_row * D;
-          *reinterpret_cast<uint2*>(dst + c * 8) = make_uint2(packed[0], packed[1]);
-          if (c == 0) (is_k ? a.ks : a.vs)[static_cast<size_t>(page) * a.Hkv * a.page_size + head_row] = scale;
+          *reinterpret_cast<uint2*>(dst + c0 * 8) = make_uint2(packed[0][0], packed[0][1]);
+          *reinterpret_cast<uint2*>(dst + c1 * 8) = make_uint2(packed[1][0], packed[1][1]);
+          if (p == 0) (is_k ? a.ks : a.vs)[static_cast<size_t>(page) * a.Hkv * a.page_size + head_row] = scale;
         }
       }
     }

@@ -52,18 +52,6 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
                     pack_bf16x2(v[6], v[7]));
 }
 
-// clamp(rne(y / s)), s = max|y| / 127 of the group and rs = 1 / s.  y * rs is
-// within 2^-16 of y / s (two roundings of a value below 128), so it rounds to
-// the same integer unless it lies that close to a half; there, and where rs is
-// infinite or y not finite, the division decides.
-__device__ __forceinline__ int code_of(float y, float s, float rs) {
-  const float r = y * rs;
-  const float n = rintf(r);
-  if (fabsf(fabsf(r - n) - 0.5f) < 0x1p-14f || !(fabsf(r) < 128.f))
-    return max(-127, min(127, __float2int_rn(__fdiv_rn(y, s))));
-  return max(-127, min(127, static_cast<int>(n)));
-}
-
 // One CTA per row, the row kept in registers: thread t holds the 16-byte
 // words t, t + blockDim, ... (NV of them).  blockDim is a multiple of 16 words
 // = 128 values, so a quantisation group lies in one half-warp.
@@ -139,7 +127,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const Args a) {
         const float rs = __frcp_rn(scale);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          packed[j >> 2] |= (static_cast<uint32_t>(code_of(v[j], scale, rs)) & 0xFFu) << (8 * (j & 3));
+          packed[j >> 2] |= (static_cast<uint32_t>(int8_code(v[j], scale, rs)) & 0xFFu) << (8 * (j & 3));
       }
       if (c < words) {
         reinterpret_cast<uint2*>(a.codes + row)[c] = make_uint2(packed[0], packed[1]);
