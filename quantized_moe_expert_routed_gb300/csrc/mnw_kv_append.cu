@@ -16,11 +16,10 @@
 //
 // Every element is read and written once, so memory bounds it.  Measured on
 // one GB300 with 16 query, 4 key and 4 value heads of 128: 8192 BF16 tokens
-// (101 MB) in 21.0 us, 4.8 TB/s and 71 % of the copy rate, bound by the
-// arithmetic and shuffles of a chunk; 512 tokens into INT8 pages in 4.1 us and
-// four in 2.7 us, bound by the chain of loads length -> page -> store.
-// The angle table is laid out so that a warp's lanes read neighbouring pairs
-// (in order of the pair, eight ways of conflict: 29.8 us for the 8192).
+// (101 MB) in 15.7 us, 6.4 TB/s, 96 % of the copy rate; 512 tokens into INT8
+// pages in 3.8 us and four tokens in 2.4 us, bound by the chain of loads length
+// -> page -> store.  One 16-byte chunk a thread, with the other element of a
+// pair by shuffles, took 21.0 us for the 8192 (issue slots).
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -340,8 +339,8 @@ int mnw_kv_append(const void* q, long long q_stride, const void* k, long long k_
   a.Hq = Hq;
   a.Hkv = Hkv;
   a.rot = rot;
-  // One token a CTA while the batch does not fill the GPU several times over (512 INT8 tokens: 4.1 us), four from there
-  // on, whose loads are under way together (8192 tokens: 35 us with one, 21.0 with four, 20.7 with eight).
+  // One token a CTA while the batch does not fill the GPU several times over (512 INT8 tokens: 3.8 us), four from there
+  // on, whose loads are under way together (8192 tokens: 24.4 us with one, 19.6 two, 15.7 four, 15.5 eight).
   a.tokens = T >= 8 * current_sm_count() ? kvapp::kMaxTokens : 1;
   a.row_div = paged::fast_div((q ? Hq : 0) + 2 * Hkv);
   a.inv_freq = inv_freq;
