@@ -74,11 +74,11 @@ __device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
 template <bool F16>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   if constexpr (F16)
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   else
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -94,7 +94,7 @@ __device__ __forceinline__ uint32_t tf32(float x) {
   return y;
 }
 __device__ __forceinline__ void mma1688(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -136,7 +136,8 @@ __global__ void __launch_bounds__(WR* WK * 32) paged_attn_kernel(const Args a) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ SplitShared split;
   __shared__ float2 ml[C::kWarps * 16];
-  __shared__ int2 rows_at[kStages][kTK];  // (page or -1, head row within the page) of a tile's keys
+  __shared__ long long row_at[kStages][kTK];                // byte offset of a tile's keys' cached rows, -1: none
+  __shared__ long long scale_at[INT8 ? kStages : 1][kTK];   // INT8: and of their scales
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int wr = warp / WK, wk = warp % WK;
   const int g8 = lane >> 2, t4 = lane & 3;
@@ -166,13 +167,14 @@ __global__ void __launch_bounds__(WR* WK * 32) paged_attn_kernel(const Args a) {
     if (++lc.kt == lc.sh.kt) lc.next_item(a, run.pad);
   };
   auto keep = [&](int2 at, int slot) {
-    if (at.y < 0) {
-      at.x = -1;
-    } else if (static_cast<unsigned>(at.x) >= static_cast<unsigned>(a.n_pages)) {
-      at.x = -1;
+    if (tid >= kTK) return;
+    bool has = at.y >= 0;
+    if (has && static_cast<unsigned>(at.x) >= static_cast<unsigned>(a.n_pages)) {
+      has = false;
       if (a.err) atomicOr(a.err, MNW_DEVERR_BAD_PAGE);
     }
-    if (tid < kTK) rows_at[slot][tid] = at;
+    row_at[slot][tid] = has ? at.x * a.page_bytes + static_cast<long long>(at.y) * C::kRowBytes : -1;
+    if constexpr (INT8) scale_at[slot][tid] = (static_cast<long long>(at.x) * a.Hkv * a.page_size + at.y) * 4;
   };
   auto load_tile = [&](int slot) {
     const uint32_t st = sbase + slot * C::kStageBytes;
@@ -182,19 +184,18 @@ __global__ void __launch_bounds__(WR* WK * 32) paged_attn_kernel(const Args a) {
 #pragma unroll
     for (int i = 0; i < kTK / kRP; ++i) {
       const int r = i * kRP + tid / kCh;
-      const int2 at = rows_at[slot][r];
-      const uint32_t n = at.x >= 0 ? 16u : 0u;
-      const long long off = n ? at.x * a.page_bytes + static_cast<long long>(at.y) * C::kRowBytes + c * 16 : 0;
+      const long long at = row_at[slot][r];
+      const uint32_t n = at >= 0 ? 16u : 0u;
+      const long long off = n ? at + c * 16 : 0;
       const uint32_t to = st + chunk_at<D, INT8>(r, c);
       cp_async16(to, a.kc + off, n);
       cp_async16(to + C::kTileBytes, a.vc + off, n);
     }
     if constexpr (INT8) {
       for (int r2 = tid; r2 < 2 * kTK; r2 += kThreads) {
-        const int2 at = rows_at[slot][r2 % kTK];
-        const uint32_t n = at.x >= 0 ? 4u : 0u;
-        const long long off = n ? static_cast<long long>(at.x) * a.Hkv * a.page_size + at.y : 0;
-        cp_async4(st + 2 * C::kTileBytes + r2 * 4, (r2 < kTK ? a.ks : a.vs) + off, n);
+        const uint32_t n = row_at[slot][r2 % kTK] >= 0 ? 4u : 0u;
+        const long long off = n ? scale_at[slot][r2 % kTK] : 0;
+        cp_async4(st + 2 * C::kTileBytes + r2 * 4, reinterpret_cast<const char*>(r2 < kTK ? a.ks : a.vs) + off, n);
       }
     }
   };
@@ -314,11 +315,10 @@ __global__ void __launch_bounds__(WR* WK * 32) paged_attn_kernel(const Args a) {
       float sc[2 * kNB][4];
 #pragma unroll
       for (int i = 0; i < 2 * kNB; ++i) sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.f;
+      if constexpr (!INT8) {
 #pragma unroll
-      for (int nb = 0; nb < kNB; ++nb) {
-        const int key0 = wk * kKW + nb * 16;
-        if constexpr (!INT8) {
-          const int row = key0 + (lane & 7) + ((lane >> 4) << 3);
+        for (int nb = 0; nb < kNB; ++nb) {
+          const int row = wk * kKW + nb * 16 + (lane & 7) + ((lane >> 4) << 3);
 #pragma unroll
           for (int ks = 0; ks < kKS; ++ks) {
             uint32_t kf[4];
@@ -326,17 +326,23 @@ __global__ void __launch_bounds__(WR* WK * 32) paged_attn_kernel(const Args a) {
             mma16816<false>(sc[2 * nb], qf[ks], kf[0], kf[1]);
             mma16816<false>(sc[2 * nb + 1], qf[ks], kf[2], kf[3]);
           }
-        } else {
+        }
+      } else {
+        // the accumulators' chains in turn: one after the other they are kKS products' latencies each
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+        for (int j = 0; j < D / 64; ++j) {
+          uint4 w[2 * kNB];
 #pragma unroll
-            for (int j = 0; j < D / 64; ++j) {
-              const uint4 w = *reinterpret_cast<const uint4*>(stage + chunk_at<D, INT8>(key0 + 8 * h + g8, t4 + 4 * j));
-              const uint32_t ww[4] = {w.x ^ 0x80808080u, w.y ^ 0x80808080u, w.z ^ 0x80808080u, w.w ^ 0x80808080u};
+          for (int i = 0; i < 2 * kNB; ++i)
+            w[i] = *reinterpret_cast<const uint4*>(stage + chunk_at<D, INT8>(wk * kKW + 8 * i + g8, t4 + 4 * j));
 #pragma unroll
-              for (int s4 = 0; s4 < 4; ++s4)
-                mma16816<true>(sc[2 * nb + h], qf[4 * j + s4], codes_lo(ww[s4]), codes_hi(ww[s4]));
+          for (int s4 = 0; s4 < 4; ++s4) {
+#pragma unroll
+            for (int i = 0; i < 2 * kNB; ++i) {
+              const uint32_t x = (s4 == 0 ? w[i].x : s4 == 1 ? w[i].y : s4 == 2 ? w[i].z : w[i].w) ^ 0x80808080u;
+              mma16816<true>(sc[i], qf[4 * j + s4], codes_lo(x), codes_hi(x));
             }
+          }
         }
       }
       if constexpr (INT8) {
@@ -399,12 +405,14 @@ __global__ void __launch_bounds__(WR* WK * 32) paged_attn_kernel(const Args a) {
           sc[i][3] *= f.y;
         }
       }
+      if (__any_sync(0xffffffffu, c0 != 1.f || c1 != 1.f)) {  // (rare along a long cache)
 #pragma unroll
-      for (int i = 0; i < kNO; ++i) {
-        o[i][0] *= c0;
-        o[i][1] *= c0;
-        o[i][2] *= c1;
-        o[i][3] *= c1;
+        for (int i = 0; i < kNO; ++i) {
+          o[i][0] *= c0;
+          o[i][1] *= c0;
+          o[i][2] *= c1;
+          o[i][3] *= c1;
+        }
       }
 #pragma unroll
       for (int nb = 0; nb < kNB; ++nb) {
