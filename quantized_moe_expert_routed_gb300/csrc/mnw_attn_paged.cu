@@ -11,31 +11,34 @@
 // Bound: every cached key and value is read once for all rows of its kv head
 // (n * Hq / Hkv query rows), so up to ~100 rows the reads of the cache are the
 // floor.  Measured on one GB300: 2 single tokens over 200,000 BF16 positions, 32
-// query and 8 key heads of 128 (1.64 GB): 245 us, 6.7 TB/s, the copy rate;
-// 32 over 2048 to 8192 positions in pages of 16, 16 and 4 heads (336 MB): 66 us,
-// 5.1 TB/s, of which ~10 us are the head (split, first page lookups) and the
-// joining kernel; one over 777 positions: 7.9 us, the chain split -> page ->
-// tile -> products -> join.
+// query and 8 key heads of 128 (1.64 GB): 239 us, 6.8 TB/s, the copy rate;
+// 32 over 2048 to 8192 positions in pages of 16, 16 and 4 heads (336 MB): 64 us,
+// 5.2 TB/s, of which ~10 us are the head (split, first page lookups) and the
+// join; one over 777 positions: 7.8 us, the chain split -> page -> tile ->
+// products -> join.  INT8, 2 over 200,000 (0.84 GB): 209 us, 4.0 TB/s, bound by
+// the conversion of codes and by latency at 8 warps an SM (issue slots 50 %);
+// three CTAs of two stages instead of two of three: 230 us.
 //
 // The work's split over CTAs and the joining of its parts: mnw_attn_split.cuh.
 //
 // Up to 16 query rows (INT8: 32) go here, more to the block kernel.  A CTA is
-// WR x WK warps: WR row blocks of 16 query rows, each tile's keys cut over WK warps.  Tiles arrive by 16-byte cp.async through a ring of kStages
-// stages, one page lookup per row piece, so pages of any size may end inside
-// a tile; rows past the length are filled with zeros (a masked probability of
-// 0 then meets a finite value, whatever the page holds there).  Both products
-// are mma.sync m16n8k16 with FP32 accumulation.
+// WR x WK warps: WR row blocks of 16 query rows, each tile's keys cut over WK
+// warps.  Tiles arrive by 16-byte cp.async through a ring of kStages stages,
+// one page lookup per key, so pages of any size may end inside a tile; rows
+// past the length are filled with zeros (a masked probability of 0 then meets
+// a finite value, whatever the page holds there).  Both products are mma.sync
+// with FP32 accumulation.
 //
-// BF16 caches: probabilities enter the second product rounded to BF16 (2^-9
+// BF16 caches: probabilities enter the second product rounded to BF16 (2^-8
 // relative each, independent, so the sum's error stays near the output's own
 // rounding); the sum of probabilities is taken before that rounding.
 // INT8 caches: the first product runs on FP16 operands: codes are exact there,
 // and q is re-encoded per row as FP16 times a power of two (exact for values
 // within 2^28 of the row's largest); the keys' scales multiply the FP32 scores.
 // The second runs on TF32: codes are exact, and the probabilities times the
-// values' scales, rounded to 11 bits (2^-12), keep FP32's exponents, so value scales
-// of any spread keep the sum's accuracy (FP16 would lose weights 2^-24 below
-// the largest).
+// values' scales, rounded to 11 bits (2^-11), keep FP32's exponents, so value
+// scales of any spread keep the sum's accuracy (FP16 would lose weights 2^-24
+// below the largest).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -18,7 +18,7 @@
 //               the tensor cores' proxy.  INT8: codes land in a raw buffer
 //               (bulk copies), are taken into registers, and leave them as FP16
 //               operand tiles (exact) while the next codes land.
-//   warp 4      issues S_t = Q K_t^T, warp 5 O_g += P_t V_t, with P_t from
+//   warp 4      issues S_t = Q K_t^T, warp 5 O += P_t V_t, with P_t from
 //               tensor memory and V as it lies in the cache, [key][d], an
 //               operand whose N dimension is contiguous.  Two warps, because
 //               one accumulator's products follow each other at ~96 cycles
