@@ -25,6 +25,7 @@
 #include <cmath>
 
 #include "mnw_convert.cuh"
+#include "mnw_int8_code.cuh"
 #include "mnw_internal.h"
 #include "mnw_paged.cuh"
 #include "mnw_ptx.cuh"

@@ -18,6 +18,7 @@
 #include <cuda_bf16.h>
 
 #include "mnw_convert.cuh"
+#include "mnw_int8_code.cuh"
 #include "mnw_internal.h"
 #include "mnw_ptx.cuh"
 

@@ -434,3 +434,62 @@ def test_decode_ops_streams_graph_and_repeat():
     got = [t.clone() for t in (y, qo, out)]
     want = step()
     assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+# ---- the forms that large batches and middling row counts take ----
+
+
+@pytest.mark.parametrize("H", [136, 1152, 4096])
+def test_rmsnorm_many_rows(H):
+    """Enough rows that a thread takes two words of one."""
+    T = 3000
+    x, r = _randn((T, H), H), _randn((T, H), H + 1, 3.0)
+    w = (1 + _randn((H,), H + 2, 0.2).float()).bfloat16()
+    y, ro, codes, scales = M().mnw_rmsnorm(x, w, 1e-5, residual=r, int8=H % 128 == 0)
+    want = (x.float() + r.float()).bfloat16()
+    assert torch.equal(ro, want)
+    z = want.double()
+    ref = z / (z.square().mean(1, keepdim=True) + 1e-5).sqrt() * w.double()
+    # BF16's rounding, and FP32's: a sum of H squares in partial sums of at most 16 and two products
+    assert ((y.double() - ref).abs() <= (2.0 ** -8 + 2.0 ** -18) * ref.abs()).all()
+    if H % 128 == 0:
+        c, s = U.quantise_rows(y.float().cpu().view(T, -1, 128).numpy())
+        assert np.array_equal(scales.cpu().numpy(), s) and np.array_equal(codes.cpu().numpy().reshape(c.shape), c)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "int8"])
+@pytest.mark.parametrize("layout,d,rot", [("half", 128, 128), ("half", 64, 48), ("interleaved", 128, 32)])
+def test_kv_append_many_tokens_as_few(fmt, layout, d, rot):
+    """One call over ragged sequences with several tokens a CTA, and a call per sequence with one: the same bits."""
+    m = M()
+    counts, Hq, Hkv, page = [701, 1, 0, 898, 3], 6, 2, 20
+    lens = [900, 1, 33, 898, 77]
+    cache = U.Cache(lens, page, Hkv, d, fmt, seed=9, stale=0.0)
+    T = sum(counts)
+    q, k, v = _randn((T, Hq, d), 1), _randn((T, Hkv, d), 2), _randn((T, Hkv, d), 3)
+    f, _ = m.mnw_rope_frequencies(rot, 1e4, device="cuda")
+    kw = dict(inv_freq=f, layout=m.ROPE_HALF if layout == "half" else m.ROPE_INTERLEAVED)
+    start = U.starts_of(counts)
+    few = [t.clone() for t in (cache.k, cache.v)] + [None if t is None else t.clone() for t in (cache.ks, cache.vs)]
+    got = m.mnw_kv_append(q, k, v, cache.k, cache.v, cache.table, cache.cache_lens,
+                          q_start=torch.tensor(start, dtype=torch.int32, device="cuda"), **kw, **cache.kw())
+    for b, n in enumerate(counts):
+        if n:
+            at = slice(start[b], start[b + 1])
+            one = m.mnw_kv_append(q[at], k[at], v[at], few[0], few[1], cache.table[b:b + 1], cache.cache_lens[b:b + 1],
+                                  k_scale=few[2], v_scale=few[3], **kw)
+            assert torch.equal(got[at], one)
+    assert torch.equal(cache.k, few[0]) and torch.equal(cache.v, few[1])
+    if fmt == "int8":
+        assert torch.equal(cache.ks, few[2]) and torch.equal(cache.vs, few[3])
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "int8"])
+@pytest.mark.parametrize("page,d", [(16, 128), (20, 128), (64, 64)])
+@pytest.mark.parametrize("counts,lens", [([5], [700]), ([8], [8]), ([7, 3, 11], [300, 3, 1111])])
+def test_attn_paged_17_to_32_rows(fmt, page, d, counts, lens):
+    cache = U.Cache(lens, page, 2, d, fmt, seed=len(lens))
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q, out, lse, scale = _attend(cache, counts, 8, 1, len(set(counts)) > 1, err=err)
+    assert int(err.item()) == 0
+    U.check_attention(out, lse, q, counts, cache, 1, scale)
