@@ -96,7 +96,7 @@ enum mnw_status {
 #define MNW_DEVERR_BAD_EXPERT_ID 0x1u  /* an id outside [0, E); that assignment was dropped */
 #define MNW_DEVERR_TIMEOUT 0x2u        /* a kernel-internal wait ran out; its output is invalid */
 #define MNW_DEVERR_BAD_LENGTH 0x4u     /* a cache length or token range that does not fit; what does not fit was left out */
-#define MNW_DEVERR_BAD_PAGE 0x8u       /* a page number outside [0, n_pages); not written, and read as zeros */
+#define MNW_DEVERR_BAD_PAGE 0x8u       /* no page, or a page number outside [0, n_pages); not written, and read as zeros */
 
 enum mnw_wfmt { MNW_FMT_BF16 = 0, MNW_FMT_INT8_G128 = 1, MNW_FMT_INT4_G128 = 2, MNW_FMT_NVFP4_G16 = 3 };
 /* MNW_ACT_F16_ROWS is an operand form, not a layer mode: BF16 rows re-encoded
@@ -454,9 +454,13 @@ int mnw_rmsnorm(const void* x, long long x_stride, const void* residual, const v
  * [q_start[b], q_start[b+1]) (int32 [B+1], ascending from 0 to T), or T / B
  * each where q_start is NULL.  All of these are device memory.
  * A length below zero, above max_pages * page_size or below the sequence's new
- * tokens, or a q_start out of order, ORs MNW_DEVERR_BAD_LENGTH into *err (device, nullable);
- * tokens without a position are left out.  A page outside [0, n_pages) ORs
- * MNW_DEVERR_BAD_PAGE: nothing is written there, and it reads as zeros. */
+ * tokens, or a q_start out of order or past T, ORs MNW_DEVERR_BAD_LENGTH into
+ * *err (device, nullable).  Positions are those of the values as given (row t
+ * of sequence b: cache_lens[b] - (q_start[b + 1] - t)); tokens whose position
+ * lies below 0 or past the table are left out: not written (past the table
+ * mnw_kv_append ORs MNW_DEVERR_BAD_PAGE too: they have no page), and rows that
+ * see nothing.  A page outside [0, n_pages) ORs MNW_DEVERR_BAD_PAGE: nothing is
+ * written there, and it reads as zeros. */
 enum mnw_kvfmt { MNW_KV_BF16 = 0, MNW_KV_INT8 = 1 };
 enum mnw_rope { MNW_ROPE_HALF = 0, MNW_ROPE_INTERLEAVED = 1 };
 

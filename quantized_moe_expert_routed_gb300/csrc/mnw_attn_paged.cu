@@ -229,8 +229,10 @@ __global__ void __launch_bounds__(WR* WK * 32) paged_attn_kernel(const Args a) {
   auto begin_item = [&]() {
     kt_begin = cc.kt;
     rows = min(kRT, cc.s.n * a.G - cc.rt * kRT);
-    lim_lo = row_limit(a, cc.s, cc.rt * kRT);
-    lim_hi = row_limit(a, cc.s, cc.rt * kRT + rows - 1);
+    // limits ascend with the rows, but for tokens past the table at the end, which have none
+    const int first = row_limit(a, cc.s, cc.rt * kRT), last = row_limit(a, cc.s, cc.rt * kRT + rows - 1);
+    lim_lo = min(first, last);
+    lim_hi = last == 0 && first > 0 ? cc.s.len : last;
     lim0 = r0 < rows ? row_limit(a, cc.s, cc.rt * kRT + r0) : lim_hi;
     lim1 = r1 < rows ? row_limit(a, cc.s, cc.rt * kRT + r1) : lim_hi;
 #pragma unroll

@@ -239,10 +239,11 @@ struct Cursor {
   }
 };
 
-// First position that query row ri (token ri / G of the sequence) may not see.
+// First position that query row ri (token ri / G of the sequence) may not see;
+// 0 for a token without a cached position.
 __device__ __forceinline__ int row_limit(const Args& a, const Seq& s, int ri) {
-  const int p = s.len - s.n + static_cast<int>(paged::quotient(ri, a.g_div));
-  if (p < 0) return 0;
+  const int p = s.first + static_cast<int>(paged::quotient(ri, a.g_div));
+  if (p < 0 || p >= s.len) return 0;
   const long long e = (static_cast<long long>(paged::quotient(p, a.blk_div)) + 1) * a.blk;
   return e < s.len ? static_cast<int>(e) : s.len;
 }

@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const Args a) {
     int pos = 0, page = -1, slot = 0;
     if (!bad) {
       const Seq s = paged::sequence(a.bt, b, a.page_size, &bad);
-      pos = s.len - s.n + (t - s.start);
+      pos = s.first + (t - s.start);
       const bool inside = t >= s.start && t < s.start + s.n && pos >= 0 && pos < s.len;
       if (inside) {
         const int pi = static_cast<int>(paged::quotient(pos, a.page_div));
@@ -152,6 +152,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const Args a) {
         }
       } else {
         bad = true;
+        if (pos >= s.len && lane == 0 && a.err) atomicOr(a.err, MNW_DEVERR_BAD_PAGE);  // past the table: no page
       }
     }
     if (bad && lane == 0 && a.err) atomicOr(a.err, MNW_DEVERR_BAD_LENGTH);

@@ -39,27 +39,34 @@ struct Batch {
 };
 
 struct Seq {
-  int start, n, len;  // first token row, new tokens, cached length
+  int start, n, len;  // first token row, new tokens, cached positions (those that the block table holds)
+  int first;          // position of the first new token
 };
 
 // Sequence b, with values that would lead out of the token rows or of the
-// block table brought back inside (*bad tells).
+// block table brought back inside (*bad tells).  Positions come from the values
+// as they are given: a length past the table, or rows past the last, must not
+// move the other tokens to slots that hold earlier ones.  So positions below 0
+// or from `len` on can occur; their tokens have no slot.
 __device__ __forceinline__ Seq sequence(const Batch& bt, int b, int page_size, bool* bad) {
   Seq s;
+  int given;  // new tokens from row `start` on
   if (bt.q_start) {
     const int lo = __ldg(bt.q_start + b), hi = __ldg(bt.q_start + b + 1);
     s.start = max(0, min(lo, bt.T));
     s.n = max(0, min(hi, bt.T) - s.start);
-    *bad = lo != s.start || hi - lo != s.n;
+    *bad = lo != s.start || hi != s.start + s.n;
+    given = s.n > 0 ? hi - s.start : 0;
   } else {
     s.start = b * bt.n_uniform;
-    s.n = bt.n_uniform;
+    s.n = given = bt.n_uniform;
     *bad = false;
   }
   const int len = __ldg(bt.cache_lens + b);
   const long long room = static_cast<long long>(bt.max_pages) * page_size;
   s.len = len < 0 ? 0 : (len > room ? static_cast<int>(room) : len);
-  *bad = *bad || s.len != len || len < s.n;
+  s.first = max(len, 0) - given;
+  *bad = *bad || s.len != len || len < given;
   return s;
 }
 

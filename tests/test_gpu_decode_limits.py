@@ -1,0 +1,103 @@
+"""The decode step's operators at the ends of their ranges: lengths past the
+block table, token ranges past the rows."""
+import numpy as np
+import pytest
+import torch
+
+import paged_util as U
+
+pytestmark = pytest.mark.gpu
+
+
+def M():
+    import quantized_moe_expert_routed_gb300 as m
+    return m
+
+
+def _randn(shape, seed, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(shape, generator=g) * scale).bfloat16().cuda()
+
+
+def _ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def _bits(cache_tensors):
+    return [t.view(torch.int8 if t.dtype is torch.int8 else torch.int32 if t.dtype is torch.float32 else torch.int16)
+            for t in cache_tensors if t is not None]
+
+
+# ---- lengths past the table: the tokens that have no slot are left out, the others stay where they belong ----
+
+
+def _full_cache(fmt, page, pages, Hkv, d, other):
+    """A cache whose first sequence fills every page of its table, all of them valid, and a second of `other` positions."""
+    cache = U.Cache([page * pages, other], page, Hkv, d, fmt, seed=31, stale=0.0)
+    table = cache.table[:, :pages].clone()
+    spare = [x for x in range(cache.k.shape[0]) if not bool((table == x).any())]
+    need = -(-other // page)
+    for i in range(need, pages):  # valid pages in the rest of the second row, too
+        table[1, i] = spare[(i - need) % len(spare)]
+    cache.table = table
+    return cache
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "int8"])
+@pytest.mark.parametrize("n,over", [(1, 1), (1, 2), (4, 1), (4, 3), (4, 4), (4, 9), (32, 1), (32, 40)])
+def test_append_past_the_table_leaves_cached_slots(fmt, n, over):
+    m = M()
+    page, pages, Hq, Hkv, d, other = 16, 4, 4, 2, 128, 50
+    cap = page * pages
+    cache = _full_cache(fmt, page, pages, Hkv, d, other)
+    q, k, v = _randn((2 * n, Hq, d), 1), _randn((2 * n, Hkv, d), 2), _randn((2 * n, Hkv, d), 3)
+    f, _ = m.mnw_rope_frequencies(d, 1e4, device="cuda")
+    keep = max(0, n - over)  # tokens of the first sequence that have a slot
+    want = [None if t is None else t.clone() for t in (cache.k, cache.v, cache.ks, cache.vs)]
+    rows = torch.cat([torch.arange(keep), torch.arange(n, 2 * n)]).cuda()
+    want_q = m.mnw_kv_append(q[rows], k[rows], v[rows], want[0], want[1], cache.table, _ints([cap, other]), inv_freq=f,
+                             k_scale=want[2], v_scale=want[3], q_start=_ints([0, keep, keep + n]))
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got_q = m.mnw_kv_append(q, k, v, cache.k, cache.v, cache.table, _ints([cap + over, other]), inv_freq=f, err=err,
+                            **cache.kw())
+    for a, b in zip(_bits((cache.k, cache.v, cache.ks, cache.vs)), _bits(want)):
+        assert torch.equal(a, b)
+    assert torch.equal(got_q[rows], want_q)
+    assert m.mnw_moe_read_error(err) == m.DEVERR_BAD_LENGTH | m.DEVERR_BAD_PAGE
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "int8"])
+def test_append_rows_past_the_last_keep_the_others_positions(fmt):
+    """The second sequence claims 5 rows more than there are: the rows that exist are its first ones."""
+    m = M()
+    n, page, pages, Hkv, d = 6, 16, 4, 2, 64
+    cache = _full_cache(fmt, page, pages, Hkv, d, 50)
+    k, v = _randn((2 * n, Hkv, d), 2), _randn((2 * n, Hkv, d), 3)
+    want = [None if t is None else t.clone() for t in (cache.k, cache.v, cache.ks, cache.vs)]
+    m.mnw_kv_append(None, k, v, want[0], want[1], cache.table, _ints([64, 45]), k_scale=want[2], v_scale=want[3])
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    m.mnw_kv_append(None, k, v, cache.k, cache.v, cache.table, _ints([64, 50]), q_start=_ints([0, n, 2 * n + 5]), err=err,
+                    **cache.kw())
+    assert m.mnw_moe_read_error(err) == m.DEVERR_BAD_LENGTH
+    for a, b in zip(_bits((cache.k, cache.v, cache.ks, cache.vs)), _bits(want)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "int8"])
+@pytest.mark.parametrize("n,over", [(1, 1), (4, 1), (4, 3), (4, 7), (7, 2), (32, 5), (40, 1), (40, 39)])
+@pytest.mark.parametrize("blk", [1, 32])
+def test_attention_past_the_table(fmt, n, over, blk):
+    """Tokens past the table see nothing, the others what they saw; one to two row tiles of each kernel."""
+    m = M()
+    page, pages, Hq, Hkv, d, other = 16, 20, 8, 2, 128, 77
+    cap = page * pages
+    cache = _full_cache(fmt, page, pages, Hkv, d, other)
+    q = _randn((2 * n, Hq, d), 1)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = m.mnw_attn_paged(q, cache.k, cache.v, cache.table, _ints([cap + over, other]), blk, 0.09, want_lse=True,
+                                err=err, **cache.kw())
+    assert m.mnw_moe_read_error(err) == m.DEVERR_BAD_LENGTH
+    keep = max(0, n - over)
+    assert (out[keep:n] == 0).all() and (lse[keep:n] == -np.inf).all()
+    rows = torch.cat([torch.arange(keep), torch.arange(n, 2 * n)]).cuda()
+    U.check_attention(out[rows], lse[rows], q[rows], [keep, n], cache, blk, 0.09, lost=2.0 ** -38 if fmt == "int8" else 0.0)
