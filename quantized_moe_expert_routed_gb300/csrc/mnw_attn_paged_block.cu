@@ -468,7 +468,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto scales_at = [&](int slot) { return values ? C::kOffVS + slot * (2 * kTK * 4) : C::kOffKS + slot * (kTK * 4); };
       const int sc_slots = values ? C::kScalesV : C::kScalesK;
       bool landing_rows = false;
-      // codes of the tile at kc into the raw buffer, whose last codes both warps have taken (uses counted by `uses`)
+      // codes of the tile at kc into the raw buffer, whose last codes both warps have taken (uses counted by `uses`); rows
+      // into the warp's own half, whose last codes it has taken itself
       auto issue = [&](int uses) -> bool {
         landing_rows = !whole || __any_sync(0xffffffffu, static_cast<unsigned>(page) >= static_cast<unsigned>(a.n_pages));
         if (landing_rows) {
@@ -498,6 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (t >= 0) {
           if (landing_rows) {
             wait_copies<0>();
+            fence_proxy_async_smem();  // rows came by this proxy, the next codes may come by the other
             __syncwarp();
           } else {
             if (!(values ? warp_wait(raw_full, raw_phase, abort, a.err)
@@ -514,7 +516,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (lane == 0) mbar_arrive(values ? &bars->vs_full[sc_now] : &bars->ks_full[sc_now]);
           if (++sc_now == sc_slots) sc_now = 0;
-          if ((values || landing_rows) && !warp_wait(&empty[ring.slot], ring.phase ^ 1, abort, a.err)) { ok = false; break; }
+          // The slot; for rows also that both warps have taken the codes before (raw_full implies it for bulk copies).  A
+          // warp that went ahead alone through tiles of rows would complete raw_empty's phases in the other's place, and
+          // the parity that a later bulk copy waits for would stand for another phase.
+          if ((values || landing_rows) &&
+              !warp_wait2(&empty[ring.slot], ring.phase ^ 1, landing_rows ? raw_empty : &empty[ring.slot],
+                          (landing_rows ? t & 1 : ring.phase) ^ 1, abort, a.err)) { ok = false; break; }
         }
         uint8_t* op = smem + ring_at + ring.slot * C::kTile + lw * 64 * 128;
         const uint8_t* raw = smem + raw_at + lw * 64 * D + lane * 8;

@@ -101,3 +101,37 @@ def test_attention_past_the_table(fmt, n, over, blk):
     assert (out[keep:n] == 0).all() and (lse[keep:n] == -np.inf).all()
     rows = torch.cat([torch.arange(keep), torch.arange(n, 2 * n)]).cuda()
     U.check_attention(out[rows], lse[rows], q[rows], [keep, n], cache, blk, 0.09, lost=2.0 ** -38 if fmt == "int8" else 0.0)
+
+
+# ---- tiles that come row by row and tiles that come whole, in turn ----
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "int8"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("short", [3, 5])
+def test_attention_short_and_whole_tiles_in_turn(fmt, d, short):
+    """Sequences of one partly filled tile (copied row by row) in groups of `short`, each group before one of whole tiles,
+    enough of them that a CTA's run takes several: the two ways of copying follow each other in the same buffers."""
+    page, Hq, Hkv, n, groups = 16, 16, 4, 12, 90
+    lens = []
+    for i in range(groups):
+        lens += [65 + (29 * i + 17 * j) % 63 for j in range(short)] + [128 * (1 + i % 5)]
+    counts = [n] * len(lens)
+    cache = U.Cache(lens, page, Hkv, d, fmt, seed=short)
+    q = _randn((n * len(lens), Hq, d), 5)
+    m = M()
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    call = lambda: m.mnw_attn_paged(q, cache.k, cache.v, cache.table, cache.cache_lens, 4, d ** -0.5, want_lse=True,
+                                    err=err, **cache.kw())
+    out, lse = call()
+    for _ in range(20):  # the same bits, whatever the warps' order
+        again, lse2 = call()
+        assert torch.equal(out.view(torch.int16), again.view(torch.int16)) and torch.equal(lse, lse2)
+    assert m.mnw_moe_read_error(err) == 0
+    some = list(range(0, len(lens), 7)) + [len(lens) - 1]
+    pick = torch.cat([torch.arange(n * b, n * b + n) for b in some]).cuda()
+    part = U.Cache.__new__(U.Cache)
+    part.__dict__.update(cache.__dict__)
+    part.lens, part.rows = [lens[b] for b in some], [cache.rows[b] for b in some]
+    U.check_attention(out[pick], lse[pick], q[pick], [n] * len(some), part, 4, d ** -0.5,
+                      lost=2.0 ** -38 if fmt == "int8" else 0.0)
