@@ -490,9 +490,10 @@ int mnw_kv_append(const void* q, long long q_stride, const void* k, long long k_
  * h / (Hq / Hkv).  q as above (rotated); out: bf16 [T, Hq, d]; lse (f32
  * [T, Hq], nullable): log of the row's sum of e^(scale * q . k).  A row that
  * sees nothing gives zeros and lse = -inf; rows of no sequence are not
- * written.  Slots past the length may hold anything, NaN included; keys and
- * values inside it have to be finite, those that a mask hides from a row too
- * (a probability of zero times infinity is not zero).  Scores, softmax and
+ * written, and none at all where q_start descends.  Slots past the length may
+ * hold anything, NaN included; keys and values inside it have to be finite,
+ * those that a mask hides from a row too (a probability of zero times infinity
+ * is not zero).  Scores, softmax and
  * sums are FP32; results do not depend on timing.  Probabilities enter the
  * second product as BF16 (BF16 caches), TF32 (INT8 caches, up to 32 query rows
  * a kv head: new tokens of a sequence * Hq / Hkv) or FP16 (INT8, more rows:

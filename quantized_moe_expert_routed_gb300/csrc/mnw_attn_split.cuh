@@ -68,7 +68,8 @@ __device__ __forceinline__ float ex2(float x) {
 // the exponent byte 0x64 is the FP16 value 1024 + b.
 __device__ __forceinline__ uint32_t codes_lo(uint32_t w) { return f16x2_sub(prmt(w, 0x64646464u, 0x4140), 0x64806480u); }
 __device__ __forceinline__ uint32_t codes_hi(uint32_t w) { return f16x2_sub(prmt(w, 0x64646464u, 0x4342), 0x64806480u); }
-// Units of a sequence (the host bounds their sum below 2^31).  An item counts
+// Units of a sequence (the host bounds their sum below 2^31 for ranges of rows
+// in order; others are not computed at all, see find_run).  An item counts
 // as a multiple of `pad` units, so that with runs of `pad` none begins inside
 // one item and goes on in the next.
 struct Shape {
@@ -113,19 +114,29 @@ __device__ __forceinline__ Run find_run(const Args& a, SplitShared* sh) {
   // runs that the items of a sequence make at p units each (clipped: they are added up)
   auto runs_of = [&](const Shape& one, int p) { return min(a.Hkv * one.rt * ((one.kt + p - 1) / p), 1 << 20); };
   int total = 0;
+  bool back = false;
   Seq s{};
   for (int b = tid; b < bt.B; b += THREADS) {
     bool bad;
     s = paged::sequence(bt, b, a.page_size, &bad);
     if (bad && scribe && a.err) atomicOr(a.err, MNW_DEVERR_BAD_LENGTH);
+    back = back || paged::backwards(bt, b);
     total += shape_of<RT, TK>(s, a.G, a.Hkv, 1).units;
   }
+  // Rows counted by several sequences could pass the 32-bit units, and every run's and join's place with them: then no
+  // run has anything to do, and the joining kernel is told by a share of 0.
   const int tw = __reduce_add_sync(0xffffffffu, total);
-  if (lane == 0) sh->scan[warp] = tw;
+  back = __any_sync(0xffffffffu, back);
+  if (lane == 0) sh->scan[warp] = back ? -1 : tw;
   __syncthreads();
   total = 0;
+  int least = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) total += sh->scan[w];
+  for (int w = 0; w < kWarps; ++w) {
+    total += sh->scan[w];
+    least = min(least, sh->scan[w]);
+  }
+  if (least < 0) total = 0;
   Run r;
   r.per = max(1, (total + runs - 1) / runs);
   r.pad = 1;
@@ -196,7 +207,7 @@ __device__ __forceinline__ Run find_run(const Args& a, SplitShared* sh) {
     }
   }
   if (scribe && tid == 0) {
-    a.starts[bt.B] = r.per;
+    a.starts[bt.B] = r.u1 > 0 ? r.per : 0;
     a.starts[bt.B + 1] = r.pad;
   }
   __syncthreads();
@@ -442,6 +453,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const Args a) 
   const Seq s = paged::sequence(a.bt, b, a.page_size, &bad);
   if (t < s.start || t >= s.start + s.n) return;
   const int per = a.starts[a.bt.B];
+  if (per == 0) return;
   const Shape sh = shape_of<RT, TK>(s, a.G, a.Hkv, a.starts[a.bt.B + 1]);
   const int g = h / a.G, ri = (t - s.start) * a.G + (h - g * a.G);
   const int rt = ri / RT;

@@ -70,6 +70,13 @@ __device__ __forceinline__ Seq sequence(const Batch& bt, int b, int page_size, b
   return s;
 }
 
+// Whether sequence b's range of rows runs backwards.  Where none does, the
+// ranges are disjoint and hold at most T rows together, which bounds the work
+// that the host planned for.
+__device__ __forceinline__ bool backwards(const Batch& bt, int b) {
+  return bt.q_start && __ldg(bt.q_start + b) > __ldg(bt.q_start + b + 1);
+}
+
 // Argument checks shared by the calls on a cache.
 inline int check_cache(const void* k, const void* v, const float* ks, const float* vs, int fmt, int n_pages,
                        int page_size, int Hkv, int d, long long page_stride) {

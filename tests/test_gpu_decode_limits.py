@@ -135,3 +135,26 @@ def test_attention_short_and_whole_tiles_in_turn(fmt, d, short):
     part.lens, part.rows = [lens[b] for b in some], [cache.rows[b] for b in some]
     U.check_attention(out[pick], lse[pick], q[pick], [n] * len(some), part, 4, d ** -0.5,
                       lost=2.0 ** -38 if fmt == "int8" else 0.0)
+
+
+# ---- token ranges out of order ----
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "int8"])
+@pytest.mark.parametrize("G", [2, 16])
+@pytest.mark.parametrize("starts", [[0, 9, 0, 9], [0, 3, 2, 9], [9, 0, 9, 9], [0, 50, -4, 9]])
+def test_attention_writes_nothing_where_token_ranges_descend(fmt, G, starts):
+    """Rows that several sequences claim: the outputs keep what they held, and the next call is not disturbed."""
+    m = M()
+    cache = U.Cache([500, 40, 333], 16, 2, 128, fmt, seed=6)
+    q = _randn((9, 2 * G, 128), 2)
+    out = torch.full_like(q, 7.0)
+    lse = torch.full((9, 2 * G), 7.0, device="cuda")
+    ws = torch.full((m.mnw_attn_paged_workspace_size(3, 9, 2 * G, 2, 128),), 255, dtype=torch.uint8, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    args = (q, cache.k, cache.v, cache.table, cache.cache_lens, 1, 0.1)
+    m.mnw_attn_paged(*args, q_start=_ints(starts), out=out, lse=lse, ws=ws, err=err, **cache.kw())
+    assert m.mnw_moe_read_error(err) == m.DEVERR_BAD_LENGTH
+    assert (out == 7.0).all() and (lse == 7.0).all()
+    m.mnw_attn_paged(*args, q_start=_ints([0, 2, 3, 9]), out=out, lse=lse, ws=ws, **cache.kw())
+    U.check_attention(out, lse, q, [2, 1, 6], cache, 1, 0.1, lost=2.0 ** -38 if fmt == "int8" else 0.0)
