@@ -276,31 +276,35 @@ __device__ __forceinline__ size_t out_row(const Args& a, const Seq& s, int g, in
 }
 
 // Marks this CTA's part of an item as written; true where every part of the
-// item is.  The mark is stored before the others are read, with a sequentially
-// consistent fence between, so the last CTA to mark sees all marks; CTAs that
-// mark at the same time may all see them, and then write the same result.  No
-// CTA waits.  All threads call, after writing the part.
+// item is.  All threads call, after writing the part.  The mark is a release
+// for the whole CTA: the barrier orders the other threads' writes before the
+// fence of the thread that stores it.  The mark is stored before the others are
+// read, with a sequentially consistent fence between, so the last CTA to mark
+// sees all marks; CTAs that mark at the same time may all see them, and then
+// write the same result.  A thread that reads marks fences before the barrier
+// that lets the others read the parts.  No CTA waits.
 __device__ __forceinline__ bool all_arrived(const Args& a, const Span& sp, int per, long long mine) {
-  asm volatile("fence.acq_rel.gpu;" ::: "memory");  // each thread's share of the part, before the mark
   __syncthreads();
   if (threadIdx.x == 0) {
+    asm volatile("fence.acq_rel.gpu;" ::: "memory");
     asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(a.arrivals + mine), "l"(a.tag) : "memory");
     asm volatile("fence.sc.gpu;" ::: "memory");
   }
   __syncthreads();
   bool all = true;
-  for (int c = sp.c0 + static_cast<int>(threadIdx.x); c <= sp.c1; c += blockDim.x) {
+  const int first = sp.c0 + static_cast<int>(threadIdx.x);
+  for (int c = first; c <= sp.c1; c += blockDim.x) {
     unsigned long long v;
     asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(a.arrivals + slot_of(sp, c, per)) : "memory");
     all = all && v == a.tag;
   }
-  const bool got = __syncthreads_and(all) != 0;
-  if (got) asm volatile("fence.acq_rel.gpu;" ::: "memory");
-  return got;
+  if (first <= sp.c1) asm volatile("fence.acq_rel.gpu;" ::: "memory");
+  return __syncthreads_and(all) != 0;
 }
 // After joining: a replayed graph brings the same number again.
 __device__ __forceinline__ void clear_arrivals(const Args& a, const Span& sp, int per) {
-  for (int c = sp.c0 + static_cast<int>(threadIdx.x); c <= sp.c1; c += blockDim.x) a.arrivals[slot_of(sp, c, per)] = 0;
+  for (int c = sp.c0 + static_cast<int>(threadIdx.x); c <= sp.c1; c += blockDim.x)
+    asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(a.arrivals + slot_of(sp, c, per)), "l"(0ull) : "memory");
 }
 
 // Adds the parts of one row and writes it.  D / 4 neighbouring lanes work on a
