@@ -158,3 +158,34 @@ def test_attention_writes_nothing_where_token_ranges_descend(fmt, G, starts):
     assert (out == 7.0).all() and (lse == 7.0).all()
     m.mnw_attn_paged(*args, q_start=_ints([0, 2, 3, 9]), out=out, lse=lse, ws=ws, **cache.kw())
     U.check_attention(out, lse, q, [2, 1, 6], cache, 1, 0.1, lost=2.0 ** -38 if fmt == "int8" else 0.0)
+
+
+# ---- the fused join: a replayed graph brings the same call number again ----
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "int8"])
+@pytest.mark.parametrize("G", [1, 4])
+def test_attention_graph_replayed_on_new_data(fmt, G):
+    """At most 4 query rows a kv head, items shared by several runs, the workspace kept between replays: each replay
+    gives the bits of an eager call on another workspace."""
+    m = M()
+    lens = [4000, 1333]
+    cache = U.Cache(lens, 16, 4, 128, fmt, seed=3)
+    q = _randn((2, 4 * G, 128), 2)
+    size = m.mnw_attn_paged_workspace_size(2, 2, 4 * G, 4, 128)
+    ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+    out, lse = torch.empty_like(q), torch.empty((2, 4 * G), device="cuda")
+    args = (q, cache.k, cache.v, cache.table, cache.cache_lens, 1, 0.09)
+    m.mnw_attn_paged(*args, out=out, lse=lse, ws=ws, **cache.kw())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(2):  # two nodes share a workspace, one after the other
+            m.mnw_attn_paged(*args, out=out, lse=lse, ws=ws, **cache.kw())
+    for i, now in enumerate([[4000, 1333], [900, 1], [40, 1000], [4000, 1333], [3999, 1332], [1, 1], [4000, 64]] * 4):
+        cache.cache_lens.copy_(torch.tensor(now, dtype=torch.int32))
+        q.copy_(_randn(q.shape, 100 + i))
+        cache.v.copy_(cache.v.flip(-1))
+        out.fill_(3.0)
+        graph.replay()
+        want, want_lse = m.mnw_attn_paged(*args, want_lse=True, **cache.kw())
+        assert torch.equal(out, want) and torch.equal(lse, want_lse), i
