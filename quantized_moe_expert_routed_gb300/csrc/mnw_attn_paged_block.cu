@@ -197,12 +197,18 @@ __device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr, uint32_t piec
 }
 constexpr uint32_t kBMajorN = 1u << 16;  // instruction descriptor: B's N dimension contiguous
 
-// Both of two barriers, polled by different lanes.
-__device__ __forceinline__ bool warp_wait2(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, volatile int* abort, uint32_t* err) {
+// Both of two barriers, polled by different lanes.  A vote orders no memory accesses: what the polling lanes saw is
+// before what the others do only behind the next __syncwarp().
+__device__ __forceinline__ bool warp_poll2(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, volatile int* abort, uint32_t* err) {
   int ok = 1;
   const int lane = threadIdx.x & 31;
   if (lane < 2) ok = wait_for(lane ? b : a, lane ? pb : pa, abort, err) ? 1 : 0;
   return __all_sync(0xffffffffu, ok) != 0;
+}
+__device__ __forceinline__ bool warp_wait2(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, volatile int* abort, uint32_t* err) {
+  const bool both = warp_poll2(a, pa, b, pb, abort, err);
+  __syncwarp();
+  return both;
 }
 // Tensor memory, 16 lanes from the address's: thread (g, t) = (lane / 4, lane % 4) gets of every 8 columns 2t and 2t + 1
 // of row g, then of row g + 8 (registers 4j .. 4j + 3 of columns 8j ..).
@@ -706,11 +712,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         st[x] = RowState{row_limit(a, sg.s, sg.rt * kRT + min(r16 + 8 * x, rows - 1)) - sg.kt0 * kTK, -INFINITY, 0.f, -INFINITY};
       const int begin = t;
       for (; t < end; ++t) {
+        if constexpr (INT8) {
+          if (!warp_poll2(&bars->ks_full[ks_slot], ks_phase, &bars->vs_full[vs_slot], vs_phase, abort, a.err)) { ok = false; break; }
+        }
         if (!warp_wait(&bars->s_full[buf.slot], buf.phase, abort, a.err)) { ok = false; break; }
         const uint32_t s_at = at16 + buf.slot * kTK;
         const float *ks = nullptr, *vs = nullptr;
         if constexpr (INT8) {
-          if (!warp_wait2(&bars->ks_full[ks_slot], ks_phase, &bars->vs_full[vs_slot], vs_phase, abort, a.err)) { ok = false; break; }
           ks = reinterpret_cast<const float*>(smem + C::kOffKS) + ks_slot * kTK + 2 * t4;
           vs = reinterpret_cast<const float*>(smem + C::kOffVS) + vs_slot * 2 * kTK + 2 * t4;
         }
