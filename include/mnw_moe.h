@@ -392,6 +392,9 @@ int mnw_moe_forward_static(const mnw_moe_layer* layer, int act, const void* x, c
  * usable.  Both words are caller-owned device memory, zeroed beforehand.
  * Returns MNW_E_INVALID_ARG for null pointers or a limit out of range. */
 int mnw_moe_selftest_wait_timeout(uint32_t limit_us, uint32_t* err, uint32_t* left_early, mnw_stream stream);
+/* The same for the wait of the paged attention's block kernel, which retries
+ * without long suspensions. */
+int mnw_moe_selftest_polled_wait_timeout(uint32_t limit_us, uint32_t* err, uint32_t* left_early, mnw_stream stream);
 /* Self-test of the wait on a token-tile counter that a dependent launch uses
  * (the down launch behind the gate/up launch of a forward): one thread waits
  * up to limit_us (1 us .. 1 s) for *counter (device u32) >= need.  If the

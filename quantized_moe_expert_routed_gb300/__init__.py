@@ -65,6 +65,7 @@ SIGNATURES = {
     "mnw_moe_launch_count": (ctypes.c_uint64, []),
     "mnw_moe_forward_static": (_I, [_P, _I, _P, _P, _P, _I, _I, _P, _U32P, _P]),
     "mnw_moe_selftest_wait_timeout": (_I, [ctypes.c_uint32, _U32P, _U32P, _P]),
+    "mnw_moe_selftest_polled_wait_timeout": (_I, [ctypes.c_uint32, _U32P, _U32P, _P]),
     "mnw_moe_selftest_counter_timeout": (_I, [ctypes.c_uint32, _U32P, ctypes.c_uint32, _U32P, _P]),
     "mnw_rmsnorm": (_I, [_P, _LL, _P, _P, _I, _I, ctypes.c_float, _P, _P, _P, _P, _P]),
     "mnw_kv_append": (_I, [_P, _LL, _P, _LL, _P, _LL, _I, _I, _I, _I, _I, _P, _I, _I, ctypes.c_float, _P, _P, _P, _P,
@@ -653,6 +654,13 @@ def mnw_moe_selftest_wait_timeout(limit_us, err, left_early, stream=None):
     left_early are zeroed int32 device tensors of one element."""
     _check(load().mnw_moe_selftest_wait_timeout(limit_us, _ptr(err), _ptr(left_early), _stream(stream)),
            "mnw_moe_selftest_wait_timeout")
+
+
+def mnw_moe_selftest_polled_wait_timeout(limit_us, err, left_early, stream=None):
+    """As mnw_moe_selftest_wait_timeout, for the wait of the paged attention's
+    block kernel."""
+    _check(load().mnw_moe_selftest_polled_wait_timeout(limit_us, _ptr(err), _ptr(left_early), _stream(stream)),
+           "mnw_moe_selftest_polled_wait_timeout")
 
 
 def mnw_moe_selftest_counter_timeout(limit_us, counter, need, err, stream=None):

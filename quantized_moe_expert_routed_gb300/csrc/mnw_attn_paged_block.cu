@@ -151,28 +151,12 @@ template <int N>
 __device__ __forceinline__ void wait_copies() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-// Waits poll without a suspend time: the library's bounded_wait() lets a
-// waiting thread sleep, which with a dozen hand-overs a tile costs.  They are
-// bounded by a count of polls (of a hundred cycles or so: about a second), after
-// which, or when another warp gave up, *abort is set and the wait fails.  Short,
-// because it is inlined at every wait of the roles, and the kernel's code has to
-// stay below the instruction cache's size: at 142 KB the INT8 form stalled for
-// thousands of cycles at a time.
-constexpr uint32_t kMaxPolls = 1u << 24;
-__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* err) {
-  uint32_t polls = 0;
-  while (!mbar_try_wait(bar, parity)) {
-    if ((++polls & 1023u) == 0 && (polls >= kMaxPolls || *abort)) {
-      if (!*abort && err) atomicOr(err, MNW_DEVERR_TIMEOUT);
-      *abort = 1;
-      return false;
-    }
-  }
-  return true;
-}
+// The roles' waits are polled_wait()s, short in code: the kernel's has to stay
+// below the instruction cache's size (at 142 KB the INT8 form stalled for
+// thousands of cycles at a time).
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* err) {
   int ok = 1;
-  if ((threadIdx.x & 31) == 0) ok = wait_for(bar, parity, abort, err) ? 1 : 0;
+  if ((threadIdx.x & 31) == 0) ok = polled_wait(bar, parity, abort, err) ? 1 : 0;
   ok = __shfl_sync(0xffffffffu, ok, 0);
   __syncwarp();
   return ok != 0;
@@ -202,7 +186,7 @@ constexpr uint32_t kBMajorN = 1u << 16;  // instruction descriptor: B's N dimens
 __device__ __forceinline__ bool warp_poll2(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, volatile int* abort, uint32_t* err) {
   int ok = 1;
   const int lane = threadIdx.x & 31;
-  if (lane < 2) ok = wait_for(lane ? b : a, lane ? pb : pa, abort, err) ? 1 : 0;
+  if (lane < 2) ok = polled_wait(lane ? b : a, lane ? pb : pa, abort, err) ? 1 : 0;
   return __all_sync(0xffffffffu, ok) != 0;
 }
 __device__ __forceinline__ bool warp_wait2(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, volatile int* abort, uint32_t* err) {

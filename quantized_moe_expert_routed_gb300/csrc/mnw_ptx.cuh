@@ -1,6 +1,7 @@
 // mnw_ptx.cuh -- inline-PTX building blocks for sm_103a: mbarriers, TMA bulk
 // tensor copies, tcgen05 (TMEM allocation, MMA, loads/stores), and waits
-// bounded in time.  Every spin in this library goes through bounded_wait().
+// bounded in time: every spin in this library is a bounded_wait(), a
+// polled_wait(), a bounded_poll_ge() or a loop that looks at kWaitLimitNs.
 #pragma once
 #include <cstdint>
 #include <cuda.h>
@@ -99,6 +100,32 @@ __device__ __forceinline__ bool bounded_wait_for(uint64_t* bar, uint32_t parity,
 // The library's kernels wait at most kWaitLimitNs.
 __device__ __forceinline__ bool bounded_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* err) {
   return bounded_wait_for(bar, parity, abort, err, kWaitLimitNs);
+}
+
+// As bounded_wait_for, for kernels with a dozen short hand-overs a tile, which
+// the longer suspensions cost: every retry is the plain instruction, which gives
+// up by itself after 2 to 4 us (measured), and the clock and the abort flag are
+// looked at every 64 retries (128 us), from the first time on.  Short, because
+// such kernels inline it at every wait of their roles.
+__device__ __forceinline__ bool polled_wait_for(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* err,
+                                                uint64_t limit_ns) {
+  uint64_t t0 = 0;
+  for (uint32_t it = 1; !mbar_try_wait(bar, parity); ++it) {
+    if ((it & 63u) == 0) {
+      const uint64_t now = globaltimer();
+      if (it == 64u) t0 = now;
+      if (*abort) return false;
+      if (now - t0 > limit_ns) {
+        *abort = 1;
+        if (err) atomicOr(err, MNW_DEVERR_TIMEOUT);
+        return false;
+      }
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ bool polled_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* err) {
+  return polled_wait_for(bar, parity, abort, err, kWaitLimitNs);
 }
 
 // ---- cross-kernel dependency counters ----------------------------------------

@@ -1,7 +1,7 @@
 // mnw_selftest.cu -- a self-test of the library's failure detection on the GPU.
 //
-// Every wait inside the library's kernels is bounded (bounded_wait in
-// mnw_ptx.cuh): when one runs out it ORs MNW_DEVERR_TIMEOUT into the caller's
+// Every wait inside the library's kernels is bounded (bounded_wait and
+// polled_wait in mnw_ptx.cuh): when one runs out it ORs MNW_DEVERR_TIMEOUT into the caller's
 // error word and raises the CTA's abort flag, and every other role of the CTA
 // leaves its own wait when it sees the flag.  This entry point exercises
 // exactly that code without any fault: one CTA of two warps, each waiting on
@@ -15,6 +15,7 @@
 namespace mnw {
 namespace {
 
+template <bool POLLED>
 __global__ void __launch_bounds__(64, 1) wait_timeout_kernel(uint64_t limit_ns, uint32_t* err, uint32_t* left_early) {
   __shared__ uint64_t bars[2];
   __shared__ int abort_flag;
@@ -30,10 +31,10 @@ __global__ void __launch_bounds__(64, 1) wait_timeout_kernel(uint64_t limit_ns, 
   if (lane != 0) return;
   // phase 0 of both barriers never completes: nobody arrives
   if (warp == 0) {
-    bounded_wait_for(&bars[0], 0, abort, err, limit_ns);
+    POLLED ? polled_wait_for(&bars[0], 0, abort, err, limit_ns) : bounded_wait_for(&bars[0], 0, abort, err, limit_ns);
   } else {
     const uint64_t t0 = globaltimer();
-    const bool done = bounded_wait(&bars[1], 0, abort, err);
+    const bool done = POLLED ? polled_wait(&bars[1], 0, abort, err) : bounded_wait(&bars[1], 0, abort, err);
     if (!done && globaltimer() - t0 < kWaitLimitNs / 2) atomicOr(left_early, 1u);
   }
 }
@@ -48,14 +49,26 @@ __global__ void __launch_bounds__(32, 1) counter_timeout_kernel(const uint32_t* 
 }  // namespace
 }  // namespace mnw
 
-extern "C" int mnw_moe_selftest_wait_timeout(uint32_t limit_us, uint32_t* err, uint32_t* left_early,
-                                             mnw_stream stream) {
+namespace {
+template <bool POLLED>
+int wait_timeout(uint32_t limit_us, uint32_t* err, uint32_t* left_early, mnw_stream stream) {
   if (!err || !left_early || limit_us == 0 || limit_us > 1000000u) return MNW_E_INVALID_ARG;
-  mnw::wait_timeout_kernel<<<1, 64, 0, static_cast<cudaStream_t>(stream)>>>(static_cast<uint64_t>(limit_us) * 1000u,
-                                                                            err, left_early);
+  mnw::wait_timeout_kernel<POLLED><<<1, 64, 0, static_cast<cudaStream_t>(stream)>>>(
+      static_cast<uint64_t>(limit_us) * 1000u, err, left_early);
   if (cudaGetLastError() != cudaSuccess) return MNW_E_CUDA;
   mnw::note_launch();
   return MNW_OK;
+}
+}  // namespace
+
+extern "C" int mnw_moe_selftest_wait_timeout(uint32_t limit_us, uint32_t* err, uint32_t* left_early,
+                                             mnw_stream stream) {
+  return wait_timeout<false>(limit_us, err, left_early, stream);
+}
+
+extern "C" int mnw_moe_selftest_polled_wait_timeout(uint32_t limit_us, uint32_t* err, uint32_t* left_early,
+                                                    mnw_stream stream) {
+  return wait_timeout<true>(limit_us, err, left_early, stream);
 }
 
 extern "C" int mnw_moe_selftest_counter_timeout(uint32_t limit_us, const uint32_t* counter, uint32_t need,
