@@ -473,8 +473,8 @@ enum mnw_rope { MNW_ROPE_HALF = 0, MNW_ROPE_INTERLEAVED = 1 };
  * (u, w) are elements (i, i + rot/2) (MNW_ROPE_HALF) or (2i, 2i + 1)
  * (MNW_ROPE_INTERLEAVED); elements from rot on are copied.  inv_freq: device
  * f32 [rot/2] (scaled as long contexts want: mnw_rope_frequencies); rot = 0
- * rotates nothing.  The angle keeps its fraction of a turn to about 2^-24 at
- * any 32-bit position.  q [T, Hq, d], k, v [T, Hkv, d] bf16, a token's heads
+ * rotates nothing.  The angle keeps its fraction of a turn to 2^-25 at any
+ * 32-bit position (inv_freq up to 16).  q [T, Hq, d], k, v [T, Hkv, d] bf16, a token's heads
  * contiguous, tokens *_stride elements apart (multiples of 8), so the
  * slices of one fused projection can be passed.  q_out: bf16 [T, Hq, d] contiguous;
  * may be q itself where q_stride == Hq * d.  q NULL: keys and values only.

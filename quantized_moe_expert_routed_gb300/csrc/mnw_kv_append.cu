@@ -9,10 +9,10 @@
 // 127, code = clamp(rne(x / s), -127, 127), as mnw_moe_quantize_act() does.
 //
 // The angle: at position 10^5 a radian's fraction lies 17 bits down, so a
-// plain FP32 product would leave 7 bits of it.  It is taken in turns, g =
-// inv_freq / (2 pi) as an unevaluated sum of two FP32 values, whole turns
-// removed exactly from each partial product, and sin and cos of the remaining
-// fraction come from sincospif; the error is about 2^-24 turns.
+// plain FP32 product would leave 7 bits of it.  It is taken in turns and in
+// fixed point: inv_freq / (2 pi) as a 64-bit fraction, times the position
+// modulo 2^64, loses whole turns and nothing else (2^-32 of a turn).  The upper
+// 32 bits, rounded to FP32's 24, go to sincospif: 2^-25 turns at any position.
 //
 // Every element is read and written once, so memory bounds it.  Measured on
 // one GB300 with 16 query, 4 key and 4 value heads of 128: 8192 BF16 tokens
@@ -57,18 +57,17 @@ struct Args {
   uint32_t* err;
 };
 
-// Fraction of a turn, in [-1/2, 1/2], of position p at frequency f.
-__device__ __forceinline__ float turn_fraction(int p, float f) {
-  constexpr float kHi = 0.15915494309189535f;                                    // 1 / (2 pi)
-  constexpr float kLo = static_cast<float>(0.15915494309189535 - static_cast<double>(kHi));
-  const float g = f * kHi;
-  const float gl = fmaf(f, kLo, fmaf(f, kHi, -g));
-  const float ph = static_cast<float>(p & ~0xFFFF), pl = static_cast<float>(p & 0xFFFF);  // both exact
-  const float a = ph * g, ae = fmaf(ph, g, -a);
-  const float b = pl * g, be = fmaf(pl, g, -b);
-  float r = (a - rintf(a)) + (b - rintf(b));
-  r += ae + be + (ph + pl) * gl;
-  return r - rintf(r);
+// Fraction of a turn, in [-1/2, 1/2], of position p >= 0 at frequency f (NaN and
+// infinite frequencies give NaN).
+__device__ __forceinline__ float turn_fraction(uint32_t p, float f) {
+  constexpr uint32_t kHi = 0x28BE60DBu, kLo = 0x9391054Au;  // 2^64 / (2 pi)
+  const uint32_t bits = __float_as_uint(f), m = bits << 8 | 0x80000000u;  // |f| = m 2^(e - 158)
+  const int e = static_cast<int>(bits >> 23 & 0xFFu);
+  const uint64_t mt = static_cast<uint64_t>(m) * kHi + __umulhi(m, kLo);  // m 2^32 / (2 pi)
+  // |f| / (2 pi) in units of 2^-64, whole turns lost
+  const uint64_t g = e <= 126 ? mt >> min(126 - e, 63) : mt << min(e - 126, 63);
+  const float r = static_cast<float>(static_cast<int>((g * p) >> 32)) * 0x1p-32f;
+  return fmaf(f, 0.f, f < 0.f ? -r : r);
 }
 
 // One CTA per `tokens` tokens.  A head row is D/16 pieces of two 16-byte
@@ -162,7 +161,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const Args a) {
     }
     for (int i = lane; i < pairs; i += 32) {
       float sn, co;
-      sincospif(2.f * turn_fraction(pos, __ldg(a.inv_freq + i)), &sn, &co);
+      sincospif(2.f * turn_fraction(static_cast<uint32_t>(pos), __ldg(a.inv_freq + i)), &sn, &co);
       reinterpret_cast<float2*>(&cs[warp][(i & 7) >> 1][i >> 3])[i & 1] = make_float2(co * a.mscale, sn * a.mscale);
     }
   }

@@ -1,5 +1,7 @@
 """The decode step's operators at the ends of their ranges: lengths past the
 block table, token ranges past the rows."""
+from fractions import Fraction
+
 import numpy as np
 import pytest
 import torch
@@ -189,3 +191,60 @@ def test_attention_graph_replayed_on_new_data(fmt, G):
         graph.replay()
         want, want_lse = m.mnw_attn_paged(*args, want_lse=True, **cache.kw())
         assert torch.equal(out, want) and torch.equal(lse, want_lse), i
+
+
+# ---- angles of far positions ----
+
+INV_2PI = Fraction(15915494309189533576888376337251436203445964574046, 10 ** 50)
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("low,high", [(0, 1 << 16), (1 << 16, 10 ** 7), (10 ** 7, 1 << 27), (1 << 27, 1 << 30),
+                                      (1 << 30, (1 << 31) - 131072)])
+def test_rotation_angle_error(low, high, layout):
+    """Positions whose angle lies next to a border of a quarter turn: there the small one of sine and cosine shows the
+    angle's error, however coarse BF16 is.  Bound: 2^-25 of a turn, BF16's half step, and sine's own 2^-22."""
+    m = M()
+    rot, page = 64, 65536
+    pairs = rot // 2
+    f, _ = m.mnw_rope_frequencies(rot, 1e4, device="cuda")
+    rng = np.random.default_rng(low + 1)
+    some = rng.integers(low, high, 200000)
+    turns = [Fraction(float(x)) * INV_2PI for x in f.cpu().tolist()]
+    at = []  # for every pair a position next to a whole turn and one next to a quarter
+    for quarter in (0.0, 0.25):
+        for t in turns:
+            frac = (some.astype(np.uint64) * np.uint64(int(t * 2 ** 64) % 2 ** 64)).astype(np.float64) / 2.0 ** 64
+            off = np.abs((frac - quarter + 0.5) % 1.0 - 0.5)
+            at.append(int(some[int(off.argmin())]))
+    B, most = len(at), (high + page - 1) // page
+    table = torch.zeros((B, most), dtype=torch.int32, device="cuda")
+    k, v = (torch.empty((1, 1, page, rot), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    q = torch.zeros((B, 1, rot), dtype=torch.bfloat16, device="cuda")
+    first, second = ((lambda i: i), (lambda i: i + pairs)) if layout == "half" else ((lambda i: 2 * i), (lambda i: 2 * i + 1))
+    for i in range(pairs):
+        q[:, 0, first(i)] = 1.0
+    kv = torch.zeros((B, 1, rot), dtype=torch.bfloat16, device="cuda")
+    got = m.mnw_kv_append(q, kv, kv, k, v, table, _ints([p + 1 for p in at]), inv_freq=f,
+                          layout=m.ROPE_HALF if layout == "half" else m.ROPE_INTERLEAVED).double().cpu()[:, 0]
+    for b, p in enumerate(at):
+        i = b % pairs
+        t = p * turns[i]
+        a = float(2 * (t - round(t)) / (2 * INV_2PI))  # radians, in [-pi, pi]
+        for x, want in ((first(i), np.cos(a) if b < pairs else float(np.sin(np.pi / 2 - a))), (second(i), np.sin(a))):
+            tol = 2.0 ** -8 * abs(want) + 2 * np.pi * 2.0 ** -25 + 2.0 ** -22 * abs(want)
+            assert abs(got[b, x].item() - want) <= tol, (p, i, got[b, x].item(), want)
+
+
+def test_rotation_of_odd_frequencies():
+    """Negative, zero, tiny, large and NaN entries of the table."""
+    m = M()
+    f = torch.tensor([-0.5, 0.0, -0.0, 1e-30, 1e-42, 100.0, float("nan"), 1.0], device="cuda")
+    k, v = (torch.zeros((1, 1, 64, 64), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    q, kv = _randn((5, 1, 64), 3), _randn((5, 1, 64), 4)
+    got = m.mnw_kv_append(q, kv, kv, k, v, torch.zeros((1, 1), dtype=torch.int32, device="cuda"), _ints([37]), inv_freq=f)
+    ref, size = U.rotate_plain(q, np.arange(32, 37), f, 16, "half", 1.0)
+    seen = torch.tensor([i for i in range(64) if i not in (6, 14)])
+    tol = 2.0 ** -8 * ref.abs() + 2.0 ** -18 * size
+    assert ((got.double().cpu() - ref).abs() <= tol)[..., seen].all()
+    assert torch.isnan(got[..., [6, 14]]).all()
