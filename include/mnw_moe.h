@@ -435,8 +435,11 @@ int mnw_attn_prefill(const void* q, const void* k, const void* v, int B, int T, 
  * residual_out (nullable; only with a residual) receives r' and may be
  * `residual` itself, or x where x_stride == H.  y may be NULL if codes is not.
  * codes (int8 [T, H]) and scales (f32 [T, H/128]), both or neither, receive
- * the INT8 form of y, the operand of the W8A8 / W4A8 GEMMs, bit for bit what
- * mnw_moe_quantize_act(MNW_ACT_INT8_G128) gives for y.  The sum of squares is
+ * the INT8 form of y, bit for bit what mnw_moe_quantize_act(MNW_ACT_INT8_G128)
+ * gives for y, a row a token.  The W8A8 / W4A8 GEMMs take rows sorted by
+ * expert: row p is token sorted_assign[p] / k of these.  mnw_moe_forward and
+ * its variants take BF16 x and quantise it themselves, so a caller of those
+ * has no use for the codes.  The sum of squares is
  * FP32 in a fixed order.  H % 8 == 0 (codes: H % 128 == 0), H <= 16384.
  * T = 0 is a no-op. */
 int mnw_rmsnorm(const void* x, long long x_stride, const void* residual, const void* w, int T, int H, float eps,

@@ -320,12 +320,14 @@ def _stream_of(t, stream):
 
 
 def mnw_rmsnorm(x, weight, eps=1e-6, residual=None, residual_out=None, y=None, codes=None, scales=None, int8=False,
-                stream=None):
+                stream=None, want_y=True):
     """Root-mean-square norm of bf16 x [T, H] with the residual's addition
     (see include/mnw_moe.h).  Returns (y bf16 [T, H], residual_out bf16 [T, H]
     or None, codes int8 [T, H] or None, scales f32 [T, H/128] or None); with
     int8 the last two are the INT8 groups of y, as mnw_moe_quantize_act gives
-    them.  residual_out may be `residual` (in place)."""
+    them for the rows of y (the W8A8 / W4A8 GEMMs take them gathered by
+    sorted_assign // k; the forward calls take y), and want_y=False leaves y
+    itself out (None).  residual_out may be `residual` (in place)."""
     bf16 = torch.bfloat16
     xp = _need(x, bf16, "x", 2)
     shape = T, H = x.shape
@@ -341,11 +343,13 @@ def mnw_rmsnorm(x, weight, eps=1e-6, residual=None, residual_out=None, y=None, c
             ro = _whole(residual_out, bf16, shape, "residual_out")
     elif residual_out is not None:
         raise MnwError("residual_out needs a residual")
-    if y is None:
+    if y is not None:
+        yp = _whole(y, bf16, shape, "y")
+    elif want_y:
         y = _new(shape, bf16, dev, stream)
         yp = y.data_ptr()
     else:
-        yp = _whole(y, bf16, shape, "y")
+        yp = None
     if int8 or codes is not None or scales is not None:
         if codes is None:
             codes = _new(shape, torch.int8, dev, stream)
