@@ -248,3 +248,25 @@ def test_rotation_of_odd_frequencies():
     tol = 2.0 ** -8 * ref.abs() + 2.0 ** -18 * size
     assert ((got.double().cpu() - ref).abs() <= tol)[..., seen].all()
     assert torch.isnan(got[..., [6, 14]]).all()
+
+
+# ---- prompt chunks: many row tiles over many key tiles ----
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "int8"])
+@pytest.mark.parametrize("counts,lens,blk,d", [
+    ([700], [700], 1, 128),               # into an empty cache
+    ([512], [5000], 32, 128),             # behind cached positions
+    ([300, 1, 450, 2], [300, 4000, 2100, 2], 1, 64),  # a mixed batch
+    ([257], [6001], 1 << 20, 64),         # every row sees everything
+])
+def test_attention_of_prompt_chunks(fmt, counts, lens, blk, d):
+    """Several row tiles of 128 query rows (4 query heads on one kv head: 32 tokens a tile) over up to 47 key tiles."""
+    m = M()
+    cache = U.Cache(lens, 64, 1, d, fmt, seed=41)
+    q = _randn((sum(counts), 4, d), 42)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = m.mnw_attn_paged(q, cache.k, cache.v, cache.table, cache.cache_lens, blk, d ** -0.5,
+                                q_start=_ints(U.starts_of(counts)), want_lse=True, err=err, **cache.kw())
+    assert m.mnw_moe_read_error(err) == 0
+    U.check_attention(out, lse, q, counts, cache, blk, d ** -0.5, lost=2.0 ** -38 if fmt == "int8" else 0.0)
