@@ -270,3 +270,23 @@ def test_attention_of_prompt_chunks(fmt, counts, lens, blk, d):
                                 q_start=_ints(U.starts_of(counts)), want_lse=True, err=err, **cache.kw())
     assert m.mnw_moe_read_error(err) == 0
     U.check_attention(out, lse, q, counts, cache, blk, d ** -0.5, lost=2.0 ** -38 if fmt == "int8" else 0.0)
+
+
+# ---- pages smaller and larger than a tile, keys and values in one allocation ----
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "int8"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("page", [4, 8, 128, 256, 1024, 24])
+@pytest.mark.parametrize("joint", [False, True])
+def test_attention_page_sizes(fmt, d, page, joint):
+    """Blocks (48 and 128 query rows a kv head) and single tokens over pages of every way of copying."""
+    m = M()
+    for counts, lens in (([32, 12], [1100, 257]), ([1, 1], [777, 2049])):
+        cache = U.Cache(lens, page, 3, d, fmt, seed=page, joint=joint)
+        q = _randn((sum(counts), 12, d), 44)
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out, lse = m.mnw_attn_paged(q, cache.k, cache.v, cache.table, cache.cache_lens, 8, d ** -0.5, want_lse=True,
+                                    q_start=_ints(U.starts_of(counts)), err=err, **cache.kw())
+        assert m.mnw_moe_read_error(err) == 0
+        U.check_attention(out, lse, q, counts, cache, 8, d ** -0.5, lost=2.0 ** -38 if fmt == "int8" else 0.0)
