@@ -290,3 +290,33 @@ def test_attention_page_sizes(fmt, d, page, joint):
                                     q_start=_ints(U.starts_of(counts)), err=err, **cache.kw())
         assert m.mnw_moe_read_error(err) == 0
         U.check_attention(out, lse, q, counts, cache, 8, d ** -0.5, lost=2.0 ** -38 if fmt == "int8" else 0.0)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "int8"])
+@pytest.mark.parametrize("n", [1, 40])
+def test_offsets_past_32_bits(fmt, n):
+    """Pages behind 2^32 bytes (BF16: elements) of keys: tiles copied whole and row by row, and an append there."""
+    m = M()
+    page, Hkv, d = 64, 8, 128
+    n_pages = (1 << 32) // (page * Hkv * d) + 40
+    small = U.Cache([300], page, Hkv, d, fmt, seed=2, shuffle=False)
+    k, v = (torch.empty((n_pages,) + small.k.shape[1:], dtype=small.k.dtype, device="cuda") for _ in range(2))
+    far = torch.arange(n_pages - 8, n_pages, device="cuda")[:5]
+    k[far], v[far] = small.k[:5], small.v[:5]
+    kw = {}
+    if fmt == "int8":
+        kw = {x: torch.empty((n_pages, Hkv, page), device="cuda") for x in ("k_scale", "v_scale")}
+        kw["k_scale"][far], kw["v_scale"][far] = small.ks[:5], small.vs[:5]
+    table = torch.full((1, 8), -1, dtype=torch.int32, device="cuda")
+    table[0, :5] = far.to(torch.int32)
+    q = _randn((n, Hkv, d), 5)
+    out, lse = m.mnw_attn_paged(q, k, v, table, small.cache_lens, 1, 0.09, want_lse=True, **kw)
+    U.check_attention(out, lse, q, [n], small, 1, 0.09, lost=2.0 ** -38 if fmt == "int8" else 0.0)
+    kv = _randn((n, Hkv, d), 6)
+    m.mnw_kv_append(None, kv, kv, k, v, table, small.cache_lens, **kw)
+    m.mnw_kv_append(None, kv, kv, small.k, small.v, small.table, small.cache_lens, **small.kw())
+    assert torch.equal(k[far].view(torch.int8), small.k[:5].view(torch.int8))
+    assert torch.equal(v[far].view(torch.int8), small.v[:5].view(torch.int8))
+    if fmt == "int8":
+        own = small.table_host[0, :5].long().cuda()
+        assert torch.equal(kw["k_scale"][far, :, :44], small.ks[own][:, :, :44])
