@@ -51,17 +51,6 @@
 namespace mnw {
 namespace pattn {
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -279,13 +268,10 @@ __global__ void __launch_bounds__(WR* WK * 32) paged_attn_kernel(const Args a) {
           m0 = max(m0, __shfl_xor_sync(0xffffffffu, m0, d));
           m1 = max(m1, __shfl_xor_sync(0xffffffffu, m1, d));
         }
-        // 2^e with the row's largest magnitude in [2^14, 2^15) after x * 2^-e
-        auto expo = [](uint32_t m) { return m == 0 ? 0 : max(-110, min(113, static_cast<int>(m >> 7) - 127 - 14)); };
-        const int e0 = expo(m0), e1 = expo(m1);
-        const float i0 = __uint_as_float(static_cast<uint32_t>(127 - e0) << 23);
-        const float i1 = __uint_as_float(static_cast<uint32_t>(127 - e1) << 23);
-        qfac0 = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e0) << 23);
-        qfac1 = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e1) << 23);
+        const int e0 = row_exponent(m0), e1 = row_exponent(m1);
+        const float i0 = two_to(-e0), i1 = two_to(-e1);
+        qfac0 = a.scale_log2 * two_to(e0);
+        qfac1 = a.scale_log2 * two_to(e1);
 #pragma unroll
         for (int ks = 0; ks < kKS; ++ks)
 #pragma unroll

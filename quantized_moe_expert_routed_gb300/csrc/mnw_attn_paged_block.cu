@@ -140,17 +140,6 @@ struct RingPos {
   }
 };
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp4(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void wait_copies() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 // The roles' waits are polled_wait()s, short in code: the kernel's has to stay
 // below the instruction cache's size (at 142 KB the INT8 form stalled for
 // thousands of cycles at a time).
@@ -300,12 +289,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int r = r0 + lane / kQC + i * kQR;
       const int ri = kc.rt * kRT + (r < rows ? r : 0);
       const int tok = static_cast<int>(paged::quotient(ri, a.g_div)), hh = ri - tok * a.G;
-      cp16(sbase + chunk(r), a.q + static_cast<long long>(kc.s.start + tok) * a.q_stride +
+      cp_async16(sbase + chunk(r), a.q + static_cast<long long>(kc.s.start + tok) * a.q_stride +
                                  static_cast<long long>(kc.g * a.G + hh) * D + c * 8,
            r < rows ? 16u : 0u);
     }
-    commit_copies();
-    wait_copies<0>();
+    cp_commit();
+    cp_wait<0>();
     if constexpr (INT8) {  // in place: FP16 times a power of two
 #pragma unroll 1
       for (int rb = r0 + lane / kQC; rb < r0 + n; rb += 16) {
@@ -325,13 +314,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < kQB; ++i) mag[i] = max(mag[i], __shfl_xor_sync(0xffffffffu, mag[i], d));
 #pragma unroll
         for (int i = 0; i < kQB; ++i) {
-          // 2^e with the row's largest magnitude in [2^14, 2^15) after x * 2^-e
-          const int e = mag[i] == 0 ? 0 : max(-110, min(113, static_cast<int>(mag[i] >> 7) - 127 - 14));
-          const float f = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+          const int e = row_exponent(mag[i]);
+          const float f = two_to(-e);
           auto half = [&](uint32_t y) { return half2_bits(__uint_as_float(y << 16) * f, __uint_as_float(y & 0xFFFF0000u) * f); };
           const int r = rb + i * kQR;
           *reinterpret_cast<uint4*>(smem + chunk(r)) = make_uint4(half(w[i].x), half(w[i].y), half(w[i].z), half(w[i].w));
-          if (c == 0) bars->qfac[seg & 3][r] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+          if (c == 0) bars->qfac[seg & 3][r] = two_to(e);
         }
       }
     }
@@ -389,13 +377,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int row = r0 + r;
           const uint32_t dst = INT8 ? to + row * D + c * 16
                                     : to + (c >> 3) * C::kPiece + row * 128 + (((c & 7) ^ (row & 7)) << 4);
-          cp16(dst, base + (off >= 0 ? off + c * 16 : 0), off >= 0 ? 16u : 0u);
+          cp_async16(dst, base + (off >= 0 ? off + c * 16 : 0), off >= 0 ? 16u : 0u);
         }
         if constexpr (INT8)
-          cp4(sc + (r0 + lane) * 4, (values ? a.vs : a.ks) + (pg >= 0 ? static_cast<long long>(pg) * a.Hkv * a.page_size + at : 0),
+          cp_async4(sc + (r0 + lane) * 4, (values ? a.vs : a.ks) + (pg >= 0 ? static_cast<long long>(pg) * a.Hkv * a.page_size + at : 0),
               pg >= 0 ? 4u : 0u);
       }
-      commit_copies();
+      cp_commit();
     };
     auto step = [&]() {
       if (++kc.kt == kc.sh.kt) kc.next_item(a, run.pad);
@@ -434,9 +422,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (pending) {
           if (rows)
-            wait_copies<1>();
+            cp_wait<1>();
           else
-            wait_copies<0>();
+            cp_wait<0>();
           give();
         }
         if (rows) pending = bar;
@@ -444,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         step();
         if (t + 1 < tiles) peek();
       }
-      wait_copies<0>();
+      cp_wait<0>();
       if (pending) give();
       if (*abort && lw == 0) {
         // let every bulk copy already issued land before the CTA exits
@@ -488,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int t = -1; ok && t < tiles; ++t) {
         if (t >= 0) {
           if (landing_rows) {
-            wait_copies<0>();
+            cp_wait<0>();
             fence_proxy_async_smem();  // rows came by this proxy, the next codes may come by the other
             __syncwarp();
           } else {
@@ -552,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ring.advance(ring_slots);
         }
       }
-      wait_copies<0>();
+      cp_wait<0>();
       if (bulk_out && lw == 0) drain_wait(raw_full, raw_phase);  // (an abort) the copy lands before the CTA exits
     }
   } else if (warp < kWarpSm0) {

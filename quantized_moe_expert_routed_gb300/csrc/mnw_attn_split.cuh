@@ -64,6 +64,26 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// 16- and 4-byte asynchronous copies; bytes 0: zeros.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// INT8: q enters the first product as FP16 times a power of two a row: e with the
+// row's largest magnitude (given as BF16 bits) in [2^14, 2^15) after x * 2^-e.
+__device__ __forceinline__ int row_exponent(uint32_t largest) {
+  return largest == 0 ? 0 : max(-110, min(113, static_cast<int>(largest >> 7) - 127 - 14));
+}
+__device__ __forceinline__ float two_to(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+
 // Four unsigned-biased codes (code + 128 per byte) -> FP16 pairs: byte b under
 // the exponent byte 0x64 is the FP16 value 1024 + b.
 __device__ __forceinline__ uint32_t codes_lo(uint32_t w) { return f16x2_sub(prmt(w, 0x64646464u, 0x4140), 0x64806480u); }
