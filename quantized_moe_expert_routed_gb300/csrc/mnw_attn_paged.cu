@@ -11,13 +11,13 @@
 // Bound: every cached key and value is read once for all rows of its kv head
 // (n * Hq / Hkv query rows), so up to ~100 rows the reads of the cache are the
 // floor.  Measured on one GB300: 2 single tokens over 200,000 BF16 positions, 32
-// query and 8 key heads of 128 (1.64 GB): 239 us, 6.8 TB/s, the copy rate;
-// 32 over 2048 to 8192 positions in pages of 16, 16 and 4 heads (336 MB): 64 us,
-// 5.2 TB/s, of which ~10 us are the head (split, first page lookups) and the
-// join; one over 777 positions: 7.8 us, the chain split -> page -> tile ->
-// products -> join.  INT8, 2 over 200,000 (0.84 GB): 209 us, 4.0 TB/s, bound by
-// the conversion of codes and by latency at 8 warps an SM (issue slots 50 %);
-// three CTAs of two stages instead of two of three: 230 us.
+// query and 8 key heads of 128 (1.64 GB): 243 us, 6.7 TB/s, 94 % of the rate of
+// reads alone; 32 over 2048 to 8192 positions in pages of 16, 16 and 4 heads
+// (336 MB): 65 us, 5.2 TB/s, of which ~10 us are the head (split, first page
+// lookups) and the join; one over 777 positions: 7.9 us, the chain split -> page
+// -> tile -> products -> join.  INT8, 2 over 200,000 (0.84 GB): 210 us, 4.0 TB/s,
+// bound by the conversion of codes and by latency at 8 warps an SM (issue slots
+// 50 %); three CTAs of two stages instead of two of three: 230 us.
 //
 // The work's split over CTAs and the joining of its parts: mnw_attn_split.cuh.
 //

@@ -32,15 +32,17 @@
 // complete.
 //
 // Measured on one GB300: 16 sequences of 32 tokens over up to 4000 INT8
-// positions, 16 query and 4 key heads of 128 (42 MB of cache): 42.4 us; 8 of 32
-// over up to 16384 BF16 positions, 32 and 8 heads of 64 (170 MB): 46.1 us,
-// 3.7 TB/s.  About 10 us of each are a run's head (split, first tiles) and
-// tail and the joining kernel.  In between INT8 is bound by the loaders'
-// conversion (about 4500 clocks a tile) and by instruction fetches, BF16 by the
-// softmax (about 1700).  Tried: two softmax groups of 4 warps on alternate
-// tiles, an accumulator each (48 and 51 us), twice the loader warps with fewer
-// registers for the rest (44 and 51, when this form took 45 and 47), 64 keys at
-// a time in the softmax (5 us more).
+// positions, 16 query and 4 key heads of 128 (42 MB of cache): 43.2 us; 8 of 32
+// over up to 16384 BF16 positions, 32 and 8 heads of 64 (170 MB): 45.1 us,
+// 3.8 TB/s.  About 10 us of each are a run's head (split, first tiles) and
+// tail and the joining kernel.  In between BF16 is bound by the softmax (about
+// 1700 clocks a tile), INT8 by the loaders' step (about 4500): the conversion,
+// the wait for the next codes, which are asked for only when the one raw
+// buffer's last quarter is in registers, and instruction fetches, not told
+// apart.  Tried: two softmax groups of 4 warps on alternate tiles, an accumulator
+// each (48 and 51 us), twice the loader warps with fewer registers for the rest
+// (44 and 51, when this form took 45 and 47: the conversion alone does not bound
+// it), 64 keys at a time in the softmax (5 us more).
 //
 // BF16 caches: P is rounded to BF16 relative to a running maximum that moves
 // only when it grows by more than 2^8.  INT8 caches: scores times the key's

@@ -16,8 +16,8 @@
 //
 // Every element is read and written once, so memory bounds it.  Measured on
 // one GB300 with 16 query, 4 key and 4 value heads of 128: 8192 BF16 tokens
-// (101 MB) in 15.7 us, 6.4 TB/s, 96 % of the copy rate; 512 tokens into INT8
-// pages in 3.8 us and four tokens in 2.4 us, bound by the chain of loads length
+// (101 MB) in 16.0 us, 6.3 TB/s, 94 % of the copy rate; 512 tokens into INT8
+// pages in 3.9 us and four tokens in 2.7 us, bound by the chain of loads length
 // -> page -> store.  One 16-byte chunk a thread, with the other element of a
 // pair by shuffles, took 21.0 us for the 8192 (issue slots).
 #include <cuda_bf16.h>

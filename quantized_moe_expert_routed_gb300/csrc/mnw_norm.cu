@@ -12,9 +12,9 @@
 //
 // Every element is read and written once, the row staying in registers
 // between the sum and the product, so memory bounds it: 8192 rows of 4096 with
-// residual and codes (303 MB) in 46.7 us, 6.5 TB/s and 97 % of the copy rate.
+// residual and codes (303 MB) in 46.9 us, 6.5 TB/s and 97 % of the copy rate.
 // Few rows are bound by one row's chain of load, two reductions and store:
-// 1.4 us for one row of 2048, 2.1 us for 32 with codes.
+// 1.4 us for one row of 2048, 2.2 us for 32 with codes.
 #include <cuda_bf16.h>
 
 #include "mnw_convert.cuh"
