@@ -480,7 +480,8 @@ enum mnw_rope { MNW_ROPE_HALF = 0, MNW_ROPE_INTERLEAVED = 1 };
  * 32-bit position (inv_freq up to 16).  q [T, Hq, d], k, v [T, Hkv, d] bf16, a token's heads
  * contiguous, tokens *_stride elements apart (multiples of 8), so the
  * slices of one fused projection can be passed.  q_out: bf16 [T, Hq, d] contiguous;
- * may be q itself where q_stride == Hq * d.  q NULL: keys and values only.
+ * may be q itself where q_stride == Hq * d; rows of tokens that are left out
+ * are written, turned by no particular angle.  q NULL: keys and values only.
  * FP32 arithmetic, rounded to BF16 once; INT8 caches quantise the rounded
  * rows.  rot % 16 == 0, rot <= d. */
 int mnw_kv_append(const void* q, long long q_stride, const void* k, long long k_stride, const void* v,

@@ -219,9 +219,12 @@ __global__ void __launch_bounds__(WR* WK * 32) paged_attn_kernel(const Args a) {
     kt_begin = cc.kt;
     rows = min(kRT, cc.s.n * a.G - cc.rt * kRT);
     // limits ascend with the rows, but for tokens past the table at the end, which have none
-    const int first = row_limit(a, cc.s, cc.rt * kRT), last = row_limit(a, cc.s, cc.rt * kRT + rows - 1);
+    const int ri = cc.rt * kRT, first = row_limit(a, cc.s, ri), last = row_limit(a, cc.s, ri + rows - 1);
     lim_lo = min(first, last);
-    lim_hi = last == 0 && first > 0 ? cc.s.len : last;
+    lim_hi = last;
+    if (last == 0 && cc.s.first + static_cast<int>(paged::quotient(ri + rows - 1, a.g_div)) >= cc.s.len &&
+        cc.s.first + static_cast<int>(paged::quotient(ri, a.g_div)) < cc.s.len)
+      lim_hi = cc.s.len;  // the row of the last position is between
     lim0 = r0 < rows ? row_limit(a, cc.s, cc.rt * kRT + r0) : lim_hi;
     lim1 = r1 < rows ? row_limit(a, cc.s, cc.rt * kRT + r1) : lim_hi;
 #pragma unroll

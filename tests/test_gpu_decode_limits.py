@@ -105,6 +105,22 @@ def test_attention_past_the_table(fmt, n, over, blk):
     U.check_attention(out[rows], lse[rows], q[rows], [keep, n], cache, blk, 0.09, lost=2.0 ** -38 if fmt == "int8" else 0.0)
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "int8"])
+@pytest.mark.parametrize("G", [1, 2, 4, 9])
+def test_attention_more_tokens_than_the_table_has_positions(fmt, G):
+    """One tile of query rows from before the first position to past the table: the ones between see what is there."""
+    m = M()
+    cache = U.Cache([4], 4, 2, 128, fmt, seed=8)
+    q = _randn((8, 2 * G, 128), 9)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = m.mnw_attn_paged(q, cache.k, cache.v, cache.table[:, :1].contiguous(), _ints([6]), 1, 0.09, want_lse=True,
+                                err=err, **cache.kw())  # positions -2 .. 5 over 4 slots
+    assert m.mnw_moe_read_error(err) == m.DEVERR_BAD_LENGTH
+    U.check_attention(out[2:6], lse[2:6], q[2:6], [4], cache, 1, 0.09, lost=2.0 ** -38 if fmt == "int8" else 0.0)
+    rest = [0, 1, 6, 7]
+    assert (out[rest] == 0).all() and (lse[rest] == -np.inf).all()
+
+
 # ---- tiles that come row by row and tiles that come whole, in turn ----
 
 
