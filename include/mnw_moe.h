@@ -451,7 +451,17 @@ int mnw_rmsnorm(const void* x, long long x_stride, const void* residual, const v
  * keys and values, may share one allocation.  fmt MNW_KV_BF16: bf16.
  * MNW_KV_INT8: int8 codes, with k_scale and v_scale f32
  * [n_pages][Hkv][page_size], one scale per cached head row (max / 127, the
- * rule of MNW_ACT_INT8_G128).  d is 64 or 128, page_size 1 .. 65536.
+ * rule of MNW_ACT_INT8_G128).
+ * MNW_KV_INT4: two codes a byte (page_stride counts codes, as elements; a
+ * multiple of 32), and k_scale and v_scale point to a record of 8 bytes per
+ * cached head row, [n_pages][Hkv][page_size], 8-byte aligned: a float32 S, then
+ * four 8-bit multipliers m of the row's quarters.  An element is code * m * S,
+ * code in -7 .. 7, held as code + 8; of eight elements, element e lies at bits
+ * 4 (e / 2) + 16 (e % 2) of a 32-bit word.  S is the smallest BF16 value with
+ * 1785 S >= the row's largest magnitude, m = max(1, ceil(the quarter's largest
+ * / (7 S))), code = rne(x / (S m)).  A row below 2^-100 is stored as zeros; one
+ * with an infinity or a NaN gets S = NaN, and reads as NaN.
+ * d is 64 or 128, page_size 1 .. 65536.
  * block_table int32 [B, max_pages]: position p of sequence b lies in page
  * block_table[b][p / page_size], slot p % page_size; entries past the length
  * are not read.  cache_lens int32 [B]: cached positions of each sequence,
@@ -467,7 +477,7 @@ int mnw_rmsnorm(const void* x, long long x_stride, const void* residual, const v
  * mnw_kv_append ORs MNW_DEVERR_BAD_PAGE too: they have no page), and rows that
  * see nothing.  A page outside [0, n_pages) ORs MNW_DEVERR_BAD_PAGE: nothing is
  * written there, and it reads as zeros. */
-enum mnw_kvfmt { MNW_KV_BF16 = 0, MNW_KV_INT8 = 1 };
+enum mnw_kvfmt { MNW_KV_BF16 = 0, MNW_KV_INT8 = 1, MNW_KV_INT4 = 2 };
 enum mnw_rope { MNW_ROPE_HALF = 0, MNW_ROPE_INTERLEAVED = 1 };
 
 /* Writes the new tokens' keys and values to their slots, keys rotated by
@@ -482,7 +492,7 @@ enum mnw_rope { MNW_ROPE_HALF = 0, MNW_ROPE_INTERLEAVED = 1 };
  * slices of one fused projection can be passed.  q_out: bf16 [T, Hq, d] contiguous;
  * may be q itself where q_stride == Hq * d; rows of tokens that are left out
  * are written, turned by no particular angle.  q NULL: keys and values only.
- * FP32 arithmetic, rounded to BF16 once; INT8 caches quantise the rounded
+ * FP32 arithmetic, rounded to BF16 once; INT8 and INT4 caches quantise the rounded
  * rows.  rot % 16 == 0, rot <= d. */
 int mnw_kv_append(const void* q, long long q_stride, const void* k, long long k_stride, const void* v,
                   long long v_stride, int B, int T, int Hq, int Hkv, int d, const float* inv_freq, int rot, int layout,
@@ -504,7 +514,8 @@ int mnw_kv_append(const void* q, long long q_stride, const void* k, long long k_
  * sums are FP32; results do not depend on timing.  Probabilities enter the
  * second product as BF16 (BF16 caches), TF32 (INT8 caches, up to 32 query rows
  * a kv head: new tokens of a sequence * Hq / Hkv) or FP16 (INT8, more rows:
- * products with values below 2^-38 of the row's largest are lost).  Row tiles
+ * products with values below 2^-38 of the row's largest are lost; INT4: below
+ * 2^-30).  Row tiles
  * times key tiles of the full block table have to stay below 2^31
  * (MNW_E_UNSUPPORTED).  ws: device, 256-byte aligned,
  * >= mnw_attn_paged_workspace_size() bytes, any contents; calls that overlap
@@ -515,6 +526,13 @@ int mnw_attn_paged(const void* q, long long q_stride, int B, int T, int Hq, int 
                    int page_size, long long page_stride, const int32_t* block_table, int max_pages,
                    const int32_t* cache_lens, const int32_t* q_start, int blk, float scale, void* out, float* lse,
                    void* ws, size_t ws_bytes, uint32_t* err, mnw_stream stream);
+
+/* The BF16 values of all pages of a quantised cache (k or v with its scales or
+ * records; fmt MNW_KV_INT8 or MNW_KV_INT4, the other arguments as above):
+ * out, device bf16 [n_pages][Hkv][page_size][d] contiguous, as a BF16 cache
+ * holds them.  Every slot is converted, whatever it holds. */
+int mnw_kv_values(const void* cache, const void* scale, int fmt, int n_pages, int page_size, int Hkv, int d,
+                  long long page_stride, void* out, mnw_stream stream);
 
 /* Rotation frequencies, on the host: inv_freq_host f32 [rot/2] receives
  * base^(-2i/rot), scaled for contexts `factor` times the original_len that a

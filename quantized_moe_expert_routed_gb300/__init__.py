@@ -23,7 +23,7 @@ FMT_BF16, FMT_INT8_G128, FMT_INT4_G128, FMT_NVFP4_G16 = 0, 1, 2, 3
 ACT_BF16, ACT_INT8_G128, ACT_NVFP4_G16, ACT_F16_ROWS = 0, 1, 2, 3
 KIND_GATE_UP, KIND_DOWN, KIND_GATE, KIND_UP = 0, 1, 2, 3
 DEVERR_BAD_EXPERT_ID, DEVERR_TIMEOUT, DEVERR_BAD_LENGTH, DEVERR_BAD_PAGE = 0x1, 0x2, 0x4, 0x8
-KV_BF16, KV_INT8 = 0, 1
+KV_BF16, KV_INT8, KV_INT4 = 0, 1, 2
 ROPE_HALF, ROPE_INTERLEAVED = 0, 1
 ROPE_SCALE_NONE, ROPE_SCALE_LINEAR, ROPE_SCALE_NTK, ROPE_SCALE_BY_PARTS = 0, 1, 2, 3
 PATH_AUTO, PATH_TCGEN05, PATH_WARP_MMA, PATH_ROWS = 0, 1, 2, 3
@@ -73,6 +73,7 @@ SIGNATURES = {
     "mnw_attn_paged_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
     "mnw_attn_paged": (_I, [_P, _LL, _I, _I, _I, _I, _I, _P, _P, _P, _P, _I, _I, _I, _LL, _P, _I, _P, _P, _I,
                             ctypes.c_float, _P, _P, _P, _SZ, _U32P, _P]),
+    "mnw_kv_values": (_I, [_P, _P, _I, _I, _I, _I, _I, _LL, _P, _P]),
     "mnw_rope_frequencies": (_I, [_I, ctypes.c_double, _I, ctypes.c_double, ctypes.c_double, ctypes.c_double,
                                   ctypes.c_double, _P, _P]),
     "mnw_attn_workspace_size": (_SZ, [_I, _I, _I, _I]),
@@ -380,8 +381,10 @@ def _cache_args(k_cache, v_cache, k_scale, v_scale):
         fmt = KV_BF16
     elif dtype is torch.int8:
         fmt = KV_INT8
+    elif dtype is torch.uint8:
+        fmt = KV_INT4
     else:
-        raise MnwError("the cache is bf16 or int8")
+        raise MnwError("the cache is bf16, int8, or uint8 (two 4-bit codes a byte)")
     kp, vp = _need(k_cache, dtype, "k_cache", 4), _need(v_cache, dtype, "v_cache", 4)
     n, h, page, d = k_cache.shape
     st = k_cache.stride()
@@ -390,14 +393,20 @@ def _cache_args(k_cache, v_cache, k_scale, v_scale):
     if (page > 1 and st[2] != d) or (h > 1 and st[1] != page * d):
         raise MnwError("a page of the cache [Hkv, page_size, d] has to be contiguous")
     ks = vs = None
-    if fmt == KV_INT8:
-        if k_scale is None or v_scale is None:
-            raise MnwError("an int8 cache needs k_scale and v_scale")
+    page_stride = st[0] if n > 1 else h * page * d
+    if fmt == KV_BF16:
+        if k_scale is not None or v_scale is not None:
+            raise MnwError("a bf16 cache has no scales")
+    elif k_scale is None or v_scale is None:
+        raise MnwError("a quantised cache needs k_scale and v_scale")
+    elif fmt == KV_INT8:
         ks = _whole(k_scale, torch.float32, (n, h, page), "k_scale")
         vs = _whole(v_scale, torch.float32, (n, h, page), "v_scale")
-    elif k_scale is not None or v_scale is not None:
-        raise MnwError("a bf16 cache has no scales")
-    return kp, vp, ks, vs, fmt, n, page, (st[0] if n > 1 else h * page * d), h, d
+    else:
+        ks = _whole(k_scale, torch.uint8, (n, h, page, 8), "k_scale")
+        vs = _whole(v_scale, torch.uint8, (n, h, page, 8), "v_scale")
+        d, page_stride = 2 * d, 2 * page_stride
+    return kp, vp, ks, vs, fmt, n, page, page_stride, h, d
 
 
 def _batch_args(block_table, cache_lens, q_start):
@@ -416,7 +425,9 @@ def mnw_kv_append(q, k, v, k_cache, v_cache, block_table, cache_lens, inv_freq=N
     position; returns the rotated queries [T, Hq, d] (None where q is None).
     q [T, Hq, d], k and v [T, Hkv, d] bf16, slices of one projection's output
     at will; caches [n_pages, Hkv, page_size, d] bf16, or int8 with scales f32
-    [n_pages, Hkv, page_size]; block_table int32 [B, max_pages]; cache_lens
+    [n_pages, Hkv, page_size], or uint8 [n_pages, Hkv, page_size, d / 2] (two
+    4-bit codes a byte) with records uint8 [n_pages, Hkv, page_size, 8] as
+    scales; block_table int32 [B, max_pages]; cache_lens
     int32 [B], the new tokens included; q_start int32 [B + 1] or None (T / B
     tokens each).  inv_freq f32 [rot / 2] (None: no rotation); see
     mnw_rope_frequencies and include/mnw_moe.h."""
@@ -485,6 +496,24 @@ def mnw_attn_paged(q, k_cache, v_cache, block_table, cache_lens, blk, scale, k_s
     if rc:
         _check(rc, "mnw_attn_paged")
     return out if lse is None else (out, lse)
+
+
+def mnw_kv_values(cache, scale, out=None, stream=None):
+    """The bf16 values [n_pages, Hkv, page_size, d] of all pages of a quantised
+    cache: int8 [n_pages, Hkv, page_size, d] with scales f32, or uint8
+    [n_pages, Hkv, page_size, d / 2] with records uint8 [n_pages, Hkv,
+    page_size, 8] (arguments as mnw_kv_append's)."""
+    if cache.dtype is torch.bfloat16:
+        raise MnwError("a bf16 cache holds its values as they are")
+    cp, _, sp, _, fmt, n_pages, page, page_stride, Hkv, d = _cache_args(cache, cache, scale, scale)
+    shape = (n_pages, Hkv, page, d)
+    if out is None:
+        out = _new(shape, torch.bfloat16, cache.device, stream)
+    rc = load().mnw_kv_values(cp, sp, fmt, n_pages, page, Hkv, d, page_stride, _whole(out, torch.bfloat16, shape, "out"),
+                              _stream_of(cache, stream))
+    if rc:
+        _check(rc, "mnw_kv_values")
+    return out
 
 
 def mnw_rope_frequencies(rot, base=10000.0, scale=ROPE_SCALE_NONE, factor=1.0, original_len=4096, beta_fast=32.0,

@@ -541,8 +541,10 @@ __global__ void __launch_bounds__(WR* WK * 32) paged_attn_kernel(const Args a) {
 // and 22, with 64-wide heads 42 and 44.  INT8, where the block kernel has to
 // convert the codes: 32 rows 335 and 537, 34 and 40; 64 rows 54 and 40.
 inline int row_tile(long long rows, bool int8) { return rows <= 16 ? 16 : (int8 && rows <= 32 ? 32 : kBlockRows); }
+// INT4: the tiles of the transposed kernel
+inline int row_tile_int4(long long rows) { return rows <= 8 ? 8 : (rows <= 16 ? 16 : 32); }
 // CTAs resident on an SM
-inline int runs_per_sm(int rt) { return rt == kBlockRows ? 1 : 2; }
+inline int runs_per_sm(int rt, bool int4) { return int4 ? int4_runs_per_sm(rt) : (rt == kBlockRows ? 1 : 2); }
 // The last arrival joins items of at most this many rows (on average over the
 // sequences), which its threads take in one pass: no slower on the GPU (one token over 777 positions 7.7 us
 // either way, 2 over 200,000 246.5 and 247.3) and a launch (2 us of the
@@ -551,13 +553,13 @@ inline int runs_per_sm(int rt) { return rt == kBlockRows ? 1 : 2; }
 constexpr int kFusedRows = 4;
 
 inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
-inline int max_runs(int rt) { return runs_per_sm(rt) * current_sm_count(); }
+inline int max_runs(int rt, bool int4) { return runs_per_sm(rt, int4) * current_sm_count(); }
 struct Workspace {
   size_t arrivals, starts, ml, o, bytes;
 };
-inline Workspace workspace_of(int B, int rt, int d) {
+inline Workspace workspace_of(int B, int rt, int d, bool int4) {
   Workspace w;
-  const size_t slots = static_cast<size_t>(2) * max_runs(rt);
+  const size_t slots = static_cast<size_t>(2) * max_runs(rt, int4);
   w.arrivals = 0;
   w.starts = up256(slots * 8);
   w.ml = w.starts + up256((static_cast<size_t>(B) + 2) * 4);
@@ -580,8 +582,8 @@ inline unsigned long long next_tag() {
 
 // The launch's grid and workspace for row tiles of `rt` and key tiles of `tk`;
 // false where the units pass 32 bits.
-inline bool plan(Args& a, int rt, int tk, int d, uint8_t* ws, int* runs, bool* shared) {
-  const Workspace w = workspace_of(a.bt.B, rt, d);
+inline bool plan(Args& a, int rt, int tk, int d, bool int4, uint8_t* ws, int* runs, bool* shared) {
+  const Workspace w = workspace_of(a.bt.B, rt, d, int4);
   a.arrivals = reinterpret_cast<unsigned long long*>(ws + w.arrivals);
   a.starts = reinterpret_cast<int*>(ws + w.starts);
   a.part_ml = reinterpret_cast<float2*>(ws + w.ml);
@@ -589,7 +591,7 @@ inline bool plan(Args& a, int rt, int tk, int d, uint8_t* ws, int* runs, bool* s
   // most units that the batch can have: every row tile over a full block table
   const long long kt = (static_cast<long long>(a.bt.max_pages) * a.page_size + tk - 1) / tk;
   const long long items = (static_cast<long long>(a.bt.T) * a.G / rt + a.bt.B) * a.Hkv, units = items * kt;
-  const int most = max_runs(rt);
+  const int most = max_runs(rt, int4);
   if (units > 0x7fffffffll - most) return false;
   *runs = static_cast<int>(std::min<long long>(most, units));
   *shared = kt > 1;  // items of one tile are never shared
@@ -618,7 +620,7 @@ int launch(Args& a, uint8_t* ws, cudaStream_t st) {
   }
   int runs;
   bool shared;
-  if (!plan(a, C::kRT, C::kTK, D, ws, &runs, &shared)) return MNW_E_UNSUPPORTED;
+  if (!plan(a, C::kRT, C::kTK, D, false, ws, &runs, &shared)) return MNW_E_UNSUPPORTED;
   if (launch_pdl(kern, dim3(runs), dim3(C::kThreads), C::kSmem, st, a) != cudaSuccess) return MNW_E_CUDA;
   return a.fused || !shared ? MNW_OK : launch_join<D, C::kRT, C::kTK>(a, st);
 }
@@ -631,9 +633,20 @@ int launch_rows(Args& a, uint8_t* ws, int rt, cudaStream_t st) {
   }
   int runs;
   bool shared;
-  if (!plan(a, kBlockRows, kBlockKeys, D, ws, &runs, &shared)) return MNW_E_UNSUPPORTED;
+  if (!plan(a, kBlockRows, kBlockKeys, D, false, ws, &runs, &shared)) return MNW_E_UNSUPPORTED;
   const int rc = launch_block(a, D, INT8, runs, st);
   return rc != MNW_OK || !shared ? rc : launch_join<D, kBlockRows, kBlockKeys>(a, st);
+}
+
+template <int D>
+int launch_rows_int4(Args& a, uint8_t* ws, int rt, cudaStream_t st) {
+  int runs;
+  bool shared;
+  if (!plan(a, rt, kInt4Keys, D, true, ws, &runs, &shared)) return MNW_E_UNSUPPORTED;
+  const int rc = launch_int4(a, D, rt, runs, st);
+  if (rc != MNW_OK || a.fused || !shared) return rc;
+  return rt == 8 ? launch_join<D, 8, kInt4Keys>(a, st)
+                 : (rt == 16 ? launch_join<D, 16, kInt4Keys>(a, st) : launch_join<D, 32, kInt4Keys>(a, st));
 }
 
 }  // namespace pattn
@@ -646,8 +659,9 @@ extern "C" {
 size_t mnw_attn_paged_workspace_size(int B, int T, int Hq, int Hkv, int d) {
   if (B <= 0 || T <= 0 || Hq <= 0 || Hkv <= 0 || d <= 0 || Hq % Hkv) return 0;
   const long long rows = (static_cast<long long>(T) + B - 1) / B * (Hq / Hkv);
-  return std::max(pattn::workspace_of(B, pattn::row_tile(rows, false), d).bytes,
-                  pattn::workspace_of(B, pattn::row_tile(rows, true), d).bytes);
+  return std::max({pattn::workspace_of(B, pattn::row_tile(rows, false), d, false).bytes,
+                   pattn::workspace_of(B, pattn::row_tile(rows, true), d, false).bytes,
+                   pattn::workspace_of(B, pattn::row_tile_int4(rows), d, true).bytes});
 }
 
 int mnw_attn_paged(const void* q, long long q_stride, int B, int T, int Hq, int Hkv, int d, const void* k_cache,
@@ -678,7 +692,7 @@ int mnw_attn_paged(const void* q, long long q_stride, int B, int T, int Hq, int 
   a.ks = k_scale;
   a.vs = v_scale;
   const bool int8 = fmt == MNW_KV_INT8;
-  a.page_bytes = page_stride * (int8 ? 1 : 2);
+  a.page_bytes = fmt == MNW_KV_INT4 ? page_stride / 2 : page_stride * (int8 ? 1 : 2);
   a.page_div = paged::fast_div(page_size);
   a.n_pages = n_pages;
   a.page_size = page_size;
@@ -692,9 +706,12 @@ int mnw_attn_paged(const void* q, long long q_stride, int B, int T, int Hq, int 
   a.out = static_cast<__nv_bfloat16*>(out);
   a.lse = lse;
   a.err = err;
-  const int rt = row_tile((static_cast<long long>(T) + B - 1) / B * a.G, int8);
+  const long long rows = (static_cast<long long>(T) + B - 1) / B * a.G;
+  const int rt = row_tile(rows, int8);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   auto* w = static_cast<uint8_t*>(ws);
+  if (fmt == MNW_KV_INT4)
+    return d == 128 ? launch_rows_int4<128>(a, w, row_tile_int4(rows), st) : launch_rows_int4<64>(a, w, row_tile_int4(rows), st);
   if (d == 128) return int8 ? launch_rows<128, true>(a, w, rt, st) : launch_rows<128, false>(a, w, rt, st);
   return int8 ? launch_rows<64, true>(a, w, rt, st) : launch_rows<64, false>(a, w, rt, st);
 }

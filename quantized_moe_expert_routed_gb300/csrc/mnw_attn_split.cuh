@@ -34,6 +34,8 @@ using paged::Seq;
 
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kBlockRows = 128, kBlockKeys = 128;  // the block kernel's tiles (mnw_attn_paged_block.cu)
+constexpr int kInt4Keys = 128;                     // the INT4 kernel's (mnw_attn_paged_int4.cu), and its CTAs on an SM
+constexpr int int4_runs_per_sm(int rt) { return rt <= 16 ? 3 : 2; }
 
 struct Args {
   Batch bt;
@@ -451,6 +453,8 @@ __device__ __forceinline__ void join_item(const Args& a, const Seq& s, const Spa
 
 // The block kernel over `runs` runs (mnw_attn_paged_block.cu).
 int launch_block(const Args& a, int d, bool int8, int runs, cudaStream_t st);
+// The INT4 kernel for row tiles of rt = 8, 16 or 32 (mnw_attn_paged_int4.cu).
+int launch_int4(const Args& a, int d, int rt, int runs, cudaStream_t st);
 
 // The joining kernel: D / 4 lanes per (token, query head) row; rows of items
 // that one run covered are done already.

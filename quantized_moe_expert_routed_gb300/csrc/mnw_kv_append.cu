@@ -7,6 +7,12 @@
 // (2i, 2i + 1) (interleaved); elements past rot are copied.  FP32 arithmetic,
 // one rounding to BF16.  INT8 caches quantise the rounded row: s = max|x| /
 // 127, code = clamp(rne(x / s), -127, 127), as mnw_moe_quantize_act() does.
+// INT4 caches (mnw_int4_row.cuh): S is the smallest BF16 value with 1785 S >=
+// max|x| (1785 = 7 * 255), a group's multiplier m = max(1, ceil(max|group| /
+// (7 S))), code = rne(x / (S m)).  S of 8 bits makes all of it exact in FP32: 7
+// S m has 19 bits and is compared as it is, and x / (S m) is either half way
+// between two integers or 2^-20 of itself away from it, so rounding the
+// quotient to FP32 does not move it there.
 //
 // The angle: at position 10^5 a radian's fraction lies 17 bits down, so a
 // plain FP32 product would leave 7 bits of it.  It is taken in turns and in
@@ -25,6 +31,7 @@
 #include <cmath>
 
 #include "mnw_convert.cuh"
+#include "mnw_int4_row.cuh"
 #include "mnw_int8_code.cuh"
 #include "mnw_internal.h"
 #include "mnw_paged.cuh"
@@ -76,7 +83,7 @@ __device__ __forceinline__ float turn_fraction(uint32_t p, float f) {
 // so a rotation stays in a thread.  kBatch pieces of a thread are under way at
 // a time, and the first batch is requested before the tokens' positions, pages
 // and angles are worked out.
-template <int D, bool INT8, bool HALF>
+template <int D, int FMT, bool HALF>
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(const Args a) {
   constexpr int P = D / 16;  // pieces (threads) of a row
   // sine and cosine, two pairs a word: pairs 8 p + 2 j, 8 p + 2 j + 1 at [j][p], so that a row's lanes read neighbours
@@ -206,11 +213,71 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const Args a) {
         *reinterpret_cast<uint4*>(dst + c0 * 8) = out0;
         *reinterpret_cast<uint4*>(dst + c1 * 8) = out1;
       }
-      if constexpr (!INT8) {
+      if constexpr (FMT == MNW_KV_BF16) {
         if (live && !is_q && page >= 0) {
           __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(is_k ? a.kc : a.vc) + page * a.page_stride + head_row * D;
           *reinterpret_cast<uint4*>(dst + c0 * 8) = out0;
           *reinterpret_cast<uint4*>(dst + c1 * 8) = out1;
+        }
+      } else if constexpr (FMT == MNW_KV_INT4) {
+        // the groups' largest magnitudes, as BF16 bits (in whose order NaN is above infinity), two a word
+        constexpr int kGC = D / 32;  // chunks of a group
+        uint32_t top[2] = {0, 0};
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t m = __vmaxu2(__vmaxu2(u[e][0] & 0x7FFF7FFFu, u[e][1] & 0x7FFF7FFFu),
+                                      __vmaxu2(u[e][2] & 0x7FFF7FFFu, u[e][3] & 0x7FFF7FFFu));
+          const int g = (e ? c1 : c0) / kGC;
+          const uint32_t at16 = max(m >> 16, m & 0xFFFFu) << (16 * (g & 1));
+          top[0] = __vmaxu2(top[0], g < 2 ? at16 : 0u);
+          top[1] = __vmaxu2(top[1], g < 2 ? 0u : at16);
+        }
+#pragma unroll
+        for (int d = P / 2; d > 0; d >>= 1) {
+          top[0] = __vmaxu2(top[0], __shfl_xor_sync(0xffffffffu, top[0], d));
+          top[1] = __vmaxu2(top[1], __shfl_xor_sync(0xffffffffu, top[1], d));
+        }
+        if (live && !is_q && page >= 0) {
+          const float gmax[4] = {__uint_as_float(top[0] << 16), __uint_as_float(top[0] & 0xFFFF0000u),
+                                 __uint_as_float(top[1] << 16), __uint_as_float(top[1] & 0xFFFF0000u)};
+          const uint32_t most = __vmaxu2(top[0], top[1]);
+          const float amax = __uint_as_float(max(most >> 16, most & 0xFFFFu) << 16);
+          float scale = 0.f;
+          uint32_t mul = 0x01010101u, words[2] = {0x88888888u, 0x88888888u};
+          if (!(amax < INFINITY)) {
+            scale = __uint_as_float(0x7FC00000u);  // the row is not finite, and reads as NaN
+          } else if (amax >= 0x1p-100f) {
+            scale = __uint_as_float((__float_as_uint(__fdiv_rn(amax, 1785.f)) + 0xFFFFu) & 0xFFFF0000u);
+            const float s7 = 7.f * scale, r7 = __frcp_rn(s7) * (1.f - 0x1p-20f);
+            int m[4];
+            mul = 0;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {  // from at most the quotient, and at most one and a bit below it
+              m[g] = static_cast<int>(gmax[g] * r7);
+              m[g] += m[g] * s7 < gmax[g] ? 1 : 0;
+              m[g] += m[g] * s7 < gmax[g] ? 1 : 0;
+              m[g] = max(m[g], 1);
+              mul |= static_cast<uint32_t>(m[g]) << (8 * g);
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int g = (e ? c1 : c0) / kGC;
+              const float step = scale * static_cast<float>(g & 2 ? (g & 1 ? m[3] : m[2]) : (g & 1 ? m[1] : m[0]));
+              const float rs = __frcp_rn(step);
+              words[e] = 0;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                words[e] |= static_cast<uint32_t>(int8_code(__uint_as_float(u[e][j] << 16), step, rs) + 8) << (4 * j);
+                words[e] |= static_cast<uint32_t>(int8_code(__uint_as_float(u[e][j] & 0xFFFF0000u), step, rs) + 8) << (4 * j + 16);
+              }
+            }
+          }
+          uint8_t* dst = (is_k ? a.kc : a.vc) + ((page * a.page_stride + static_cast<long long>(head_row) * D) >> 1);
+          *reinterpret_cast<uint32_t*>(dst + c0 * 4) = words[0];
+          *reinterpret_cast<uint32_t*>(dst + c1 * 4) = words[1];
+          if (p == 0)
+            reinterpret_cast<uint2*>(is_k ? a.ks : a.vs)[static_cast<size_t>(page) * a.Hkv * a.page_size + head_row] =
+                make_uint2(__float_as_uint(scale), mul);
         }
       } else {
         float y[2][8];
@@ -247,11 +314,16 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const Args a) {
   }
 }
 
-template <int D, bool INT8>
+template <int D, int FMT>
 cudaError_t launch(const Args& a, bool half, cudaStream_t st) {
   const dim3 grid((a.bt.T + a.tokens - 1) / a.tokens), block(kThreads);
-  return half ? launch_pdl(kv_append_kernel<D, INT8, true>, grid, block, 0, st, a)
-              : launch_pdl(kv_append_kernel<D, INT8, false>, grid, block, 0, st, a);
+  return half ? launch_pdl(kv_append_kernel<D, FMT, true>, grid, block, 0, st, a)
+              : launch_pdl(kv_append_kernel<D, FMT, false>, grid, block, 0, st, a);
+}
+template <int D>
+cudaError_t launch_fmt(const Args& a, int fmt, bool half, cudaStream_t st) {
+  if (fmt == MNW_KV_INT4) return launch<D, MNW_KV_INT4>(a, half, st);
+  return fmt == MNW_KV_INT8 ? launch<D, MNW_KV_INT8>(a, half, st) : launch<D, MNW_KV_BF16>(a, half, st);
 }
 
 }  // namespace kvapp
@@ -348,12 +420,8 @@ int mnw_kv_append(const void* q, long long q_stride, const void* k, long long k_
   a.mscale = mscale;
   a.err = err;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const bool half = layout == MNW_ROPE_HALF, int8 = fmt == MNW_KV_INT8;
-  cudaError_t e;
-  if (d == 128)
-    e = int8 ? kvapp::launch<128, true>(a, half, st) : kvapp::launch<128, false>(a, half, st);
-  else
-    e = int8 ? kvapp::launch<64, true>(a, half, st) : kvapp::launch<64, false>(a, half, st);
+  const bool half = layout == MNW_ROPE_HALF;
+  const cudaError_t e = d == 128 ? kvapp::launch_fmt<128>(a, fmt, half, st) : kvapp::launch_fmt<64>(a, fmt, half, st);
   return e == cudaSuccess ? MNW_OK : MNW_E_CUDA;
 }
 

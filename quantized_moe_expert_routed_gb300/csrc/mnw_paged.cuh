@@ -4,7 +4,8 @@
 // Cache: k and v [n_pages][Hkv][page_size][d] (a page of one head is
 // contiguous), consecutive pages page_stride elements apart; INT8 caches hold
 // codes and k_scale, v_scale [n_pages][Hkv][page_size] f32, one scale per
-// cached head row.  Position p of sequence b lives in page
+// cached head row, INT4 caches two codes a byte and a record of 8 bytes a row
+// (mnw_int4_row.cuh) in their place.  Position p of sequence b lives in page
 // block_table[b][p / page_size], slot p % page_size.
 #pragma once
 #include <cstdint>
@@ -80,16 +81,17 @@ __device__ __forceinline__ bool backwards(const Batch& bt, int b) {
 // Argument checks shared by the calls on a cache.
 inline int check_cache(const void* k, const void* v, const float* ks, const float* vs, int fmt, int n_pages,
                        int page_size, int Hkv, int d, long long page_stride) {
-  if (fmt != MNW_KV_BF16 && fmt != MNW_KV_INT8) return MNW_E_INVALID_ARG;
+  if (fmt != MNW_KV_BF16 && fmt != MNW_KV_INT8 && fmt != MNW_KV_INT4) return MNW_E_INVALID_ARG;
   if (n_pages <= 0 || page_size <= 0 || Hkv <= 0 || d <= 0) return MNW_E_INVALID_ARG;
   if (d != 64 && d != 128) return MNW_E_UNSUPPORTED;
   if (page_size > 65536 || Hkv > 1024) return MNW_E_UNSUPPORTED;
-  const int unit = fmt == MNW_KV_BF16 ? 8 : 16;  // 16 bytes
+  const int unit = fmt == MNW_KV_BF16 ? 8 : (fmt == MNW_KV_INT8 ? 16 : 32);  // 16 bytes
   if (page_stride < static_cast<long long>(Hkv) * page_size * d || page_stride % unit) return MNW_E_INVALID_ARG;
   if (!k || !v || (reinterpret_cast<uintptr_t>(k) & 15) || (reinterpret_cast<uintptr_t>(v) & 15))
     return MNW_E_INVALID_ARG;
-  if (fmt == MNW_KV_INT8 &&
-      (!ks || !vs || (reinterpret_cast<uintptr_t>(ks) & 3) || (reinterpret_cast<uintptr_t>(vs) & 3)))
+  const uintptr_t apart = fmt == MNW_KV_INT4 ? 7 : 3;
+  if (fmt != MNW_KV_BF16 &&
+      (!ks || !vs || (reinterpret_cast<uintptr_t>(ks) & apart) || (reinterpret_cast<uintptr_t>(vs) & apart)))
     return MNW_E_INVALID_ARG;
   return MNW_OK;
 }
