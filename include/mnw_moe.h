@@ -97,6 +97,7 @@ enum mnw_status {
 #define MNW_DEVERR_TIMEOUT 0x2u        /* a kernel-internal wait ran out; its output is invalid */
 #define MNW_DEVERR_BAD_LENGTH 0x4u     /* a cache length or token range that does not fit; what does not fit was left out */
 #define MNW_DEVERR_BAD_PAGE 0x8u       /* no page, or a page number outside [0, n_pages); not written, and read as zeros */
+#define MNW_DEVERR_BAD_ADAPTER 0x10u   /* an adapter outside [-1, n), taken as none; a rank outside [0, R], brought back */
 
 enum mnw_wfmt { MNW_FMT_BF16 = 0, MNW_FMT_INT8_G128 = 1, MNW_FMT_INT4_G128 = 2, MNW_FMT_NVFP4_G16 = 3 };
 /* MNW_ACT_F16_ROWS is an operand form, not a layer mode: BF16 rows re-encoded
@@ -533,6 +534,29 @@ int mnw_attn_paged(const void* q, long long q_stride, int B, int T, int Hq, int 
  * holds them.  Every slot is converted, whatever it holds. */
 int mnw_kv_values(const void* cache, const void* scale, int fmt, int n_pages, int page_size, int Hkv, int d,
                   long long page_stride, void* out, mnw_stream stream);
+
+/* Low-rank adapters of many requests, beside a projection that they share:
+ *   out[t] = bf16(y[t] + scale[i] * B_i (A_i x[t])),  i = adapter[t]
+ * x: device bf16 [T, H]; y (the shared projection's output) and out: device
+ * bf16 [T, N]; rows *_stride elements apart (multiples of 8), so that slices of
+ * a wider tensor can be passed; out may be y itself (with its stride), and else
+ * must not overlap it.  a: device bf16 [n_adapters, R, H]; b: device bf16
+ * [n_adapters, N, R]; adapter: device int32 [T], -1 for a token without one
+ * (out = y).  scale: device f32 [n_adapters], NULL for 1.  ranks: device int32
+ * [n_adapters], NULL for R: of adapter i the first ranks[i] rows of A and
+ * columns of B count, and the others are not used, whatever they hold.  An
+ * adapter outside [-1, n_adapters) counts as -1, a rank outside [0, R] as the
+ * nearer end, and MNW_DEVERR_BAD_ADAPTER is OR-ed into *err (device, nullable).
+ * Sums are FP32; A x enters the second product to 2^-16 of itself.  Tokens may
+ * have adapters in any order; neighbours of one adapter cost least.
+ * H, N and R are multiples of 8, R <= 128, n_adapters <= 1024, T <= 2^24,
+ * N <= 2^20.  ws: device, 256-byte aligned, >= mnw_lora_workspace_size() bytes,
+ * any contents; calls that overlap need one each.  T = 0 is a no-op. */
+size_t mnw_lora_workspace_size(int T, int H, int R, int n_adapters);
+int mnw_lora_add(const void* x, long long x_stride, const void* a, const void* b, const float* scale,
+                 const int32_t* ranks, int n_adapters, int R, const int32_t* adapter, int T, int H, int N,
+                 const void* y, long long y_stride, void* out, long long out_stride, void* ws, size_t ws_bytes,
+                 uint32_t* err, mnw_stream stream);
 
 /* Rotation frequencies, on the host: inv_freq_host f32 [rot/2] receives
  * base^(-2i/rot), scaled for contexts `factor` times the original_len that a

@@ -22,7 +22,7 @@ MNW_OK = 0
 FMT_BF16, FMT_INT8_G128, FMT_INT4_G128, FMT_NVFP4_G16 = 0, 1, 2, 3
 ACT_BF16, ACT_INT8_G128, ACT_NVFP4_G16, ACT_F16_ROWS = 0, 1, 2, 3
 KIND_GATE_UP, KIND_DOWN, KIND_GATE, KIND_UP = 0, 1, 2, 3
-DEVERR_BAD_EXPERT_ID, DEVERR_TIMEOUT, DEVERR_BAD_LENGTH, DEVERR_BAD_PAGE = 0x1, 0x2, 0x4, 0x8
+DEVERR_BAD_EXPERT_ID, DEVERR_TIMEOUT, DEVERR_BAD_LENGTH, DEVERR_BAD_PAGE, DEVERR_BAD_ADAPTER = 0x1, 0x2, 0x4, 0x8, 0x10
 KV_BF16, KV_INT8, KV_INT4 = 0, 1, 2
 ROPE_HALF, ROPE_INTERLEAVED = 0, 1
 ROPE_SCALE_NONE, ROPE_SCALE_LINEAR, ROPE_SCALE_NTK, ROPE_SCALE_BY_PARTS = 0, 1, 2, 3
@@ -74,6 +74,8 @@ SIGNATURES = {
     "mnw_attn_paged": (_I, [_P, _LL, _I, _I, _I, _I, _I, _P, _P, _P, _P, _I, _I, _I, _LL, _P, _I, _P, _P, _I,
                             ctypes.c_float, _P, _P, _P, _SZ, _U32P, _P]),
     "mnw_kv_values": (_I, [_P, _P, _I, _I, _I, _I, _I, _LL, _P, _P]),
+    "mnw_lora_workspace_size": (_SZ, [_I, _I, _I, _I]),
+    "mnw_lora_add": (_I, [_P, _LL, _P, _P, _P, _P, _I, _I, _P, _I, _I, _I, _P, _LL, _P, _LL, _P, _SZ, _U32P, _P]),
     "mnw_rope_frequencies": (_I, [_I, ctypes.c_double, _I, ctypes.c_double, ctypes.c_double, ctypes.c_double,
                                   ctypes.c_double, _P, _P]),
     "mnw_attn_workspace_size": (_SZ, [_I, _I, _I, _I]),
@@ -513,6 +515,56 @@ def mnw_kv_values(cache, scale, out=None, stream=None):
                               _stream_of(cache, stream))
     if rc:
         _check(rc, "mnw_kv_values")
+    return out
+
+
+def mnw_lora_workspace_size(T, H, R, n_adapters) -> int:
+    return int(load().mnw_lora_workspace_size(T, H, R, n_adapters))
+
+
+@functools.lru_cache(maxsize=256)
+def _lora_workspace(T, H, R, n, device):
+    return max(256, mnw_lora_workspace_size(T, H, R, n))
+
+
+def _rows(t, what):
+    """(address, rows, columns, elements between rows) of a bf16 matrix whose rows are contiguous."""
+    p = _need(t, torch.bfloat16, what, 2)
+    T, n = t.shape
+    return p, T, n, t.stride(0) if T > 1 else max(n, t.stride(0) // 8 * 8)
+
+
+def mnw_lora_add(y, x, a, b, adapter, scale=None, ranks=None, out=None, ws=None, err=None, stream=None):
+    """Low-rank adapters beside a shared projection: bf16(y[t] + scale[i] *
+    b[i] (a[i] x[t])), i = adapter[t], or y[t] where that is -1.  y bf16 [T, N]
+    (the projection's output), x bf16 [T, H], rows at any stride that is a
+    multiple of 8; a bf16 [n, R, H]; b bf16 [n, N, R]; adapter int32 [T]; scale
+    f32 [n] or None (1); ranks int32 [n] or None (R): the rows of a and columns
+    of b that count.  out may be y (in place).  ws: a uint8 device tensor of at
+    least mnw_lora_workspace_size bytes, 256-byte aligned."""
+    yp, T, N, y_stride = _rows(y, "y")
+    xp, Tx, H, x_stride = _rows(x, "x")
+    if Tx != T:
+        raise MnwError("x and y have different numbers of tokens")
+    if a.dim() != 3 or b.dim() != 3:
+        raise MnwError("a and b have to be [n, R, H] and [n, N, R]")
+    n, R = a.shape[:2]
+    ap, bp = _whole(a, torch.bfloat16, (n, R, H), "a"), _whole(b, torch.bfloat16, (n, N, R), "b")
+    ip = _whole(adapter, torch.int32, (T,), "adapter")
+    sp = None if scale is None else _whole(scale, torch.float32, (n,), "scale")
+    kp = None if ranks is None else _whole(ranks, torch.int32, (n,), "ranks")
+    if out is None:
+        out = _new((T, N), torch.bfloat16, y.device, stream)
+    op, To, No, out_stride = _rows(out, "out")
+    if (To, No) != (T, N):
+        raise MnwError("out has another shape than y")
+    if ws is None:
+        ws = _new((_lora_workspace(T, H, R, n, y.get_device()),), torch.uint8, y.device, stream)
+    rc = load().mnw_lora_add(xp, x_stride, ap, bp, sp, kp, n, R, ip, T, H, N, yp, y_stride, op, out_stride,
+                             _need(ws, torch.uint8, "ws"), ws.numel(), None if err is None else _ptr(err),
+                             _stream_of(y, stream))
+    if rc:
+        _check(rc, "mnw_lora_add")
     return out
 
 

@@ -1,0 +1,436 @@
+// mnw_lora.cu -- low-rank adapters of many requests beside a shared projection.
+//
+//   out[t] = bf16(y[t] + s_i B_i (A_i x[t])),   i = adapter[t]
+// y is the shared projection's output; a token of adapter -1 keeps y.
+//
+// The inner product v = A_i x is summed in FP32 and enters the second product
+// as two BF16 terms (v to 2^-16), so the output's rounding is the only one that
+// counts.
+//
+// Tokens are grouped by adapter first (in order, so results do not depend on
+// timing), then cut into tiles of one adapter.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "mnw_convert.cuh"
+#include "mnw_internal.h"
+#include "mnw_ptx.cuh"
+
+namespace mnw {
+namespace lora {
+
+struct Args {
+  const __nv_bfloat16 *x, *a, *b, *y;
+  __nv_bfloat16* out;
+  long long x_stride, y_stride, out_stride;
+  const float* scale;      // [n] or null: 1
+  const int32_t* ranks;    // [n] or null: R
+  const int32_t* adapter;  // [T]
+  int n, R, T, H, N;
+  int splits;              // of H in the first product
+  // workspace
+  int32_t* starts;   // [n + 2] first place of each adapter's tokens in `order`, of those without one, and T
+  int32_t* order;    // [T] tokens grouped by adapter
+  float* v;          // [splits][T][padded R], by place
+  uint32_t* err;
+};
+
+__device__ __forceinline__ int bin_of(const Args& a, int t) {
+  const int id = __ldg(a.adapter + t);
+  return static_cast<unsigned>(id) < static_cast<unsigned>(a.n) ? id : a.n;
+}
+__device__ __forceinline__ int rank_of(const Args& a, int i) {
+  const int r = a.ranks ? __ldg(a.ranks + i) : a.R;
+  if (static_cast<unsigned>(r) > static_cast<unsigned>(a.R)) {
+    if (threadIdx.x == 0 && a.err) atomicOr(a.err, MNW_DEVERR_BAD_ADAPTER);
+    return r < 0 ? 0 : a.R;
+  }
+  return r;
+}
+
+// ---- grouping: CTA e lists the tokens of adapter e (e = n: of none) ----
+constexpr int kGroupThreads = 256;
+__global__ void __launch_bounds__(kGroupThreads) lora_group_kernel(const Args a) {
+  constexpr int kWarps = kGroupThreads / 32;
+  __shared__ int sums[kWarps][2];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int e = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int before = 0, mine = 0;
+  for (int t = tid; t < a.T; t += kGroupThreads) {
+    const int id = __ldg(a.adapter + t), b = bin_of(a, t);
+    before += b < e ? 1 : 0;
+    mine += b == e ? 1 : 0;
+    if (e == a.n && b == a.n && id != -1 && a.err) atomicOr(a.err, MNW_DEVERR_BAD_ADAPTER);
+  }
+  before = __reduce_add_sync(0xffffffffu, before);
+  mine = __reduce_add_sync(0xffffffffu, mine);
+  if (lane == 0) {
+    sums[warp][0] = before;
+    sums[warp][1] = mine;
+  }
+  __syncthreads();
+  before = mine = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    before += sums[w][0];
+    mine += sums[w][1];
+  }
+  if (tid == 0) {
+    a.starts[e] = before;
+    if (e == a.n) a.starts[e + 1] = a.T;
+  }
+  if (mine == 0) return;
+  int at = before;
+  for (int t0 = 0; t0 < a.T; t0 += kGroupThreads) {
+    const int t = t0 + tid;
+    const bool is = t < a.T && bin_of(a, t) == e;
+    const uint32_t m = __ballot_sync(0xffffffffu, is);
+    __syncthreads();  // the sums before are read
+    if (lane == 0) sums[warp][0] = __popc(m);
+    __syncthreads();
+    int pos = at;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      pos += w < warp ? sums[w][0] : 0;
+      at += sums[w][0];
+    }
+    if (is) a.order[pos + __popc(m & ((1u << lane) - 1u))] = t;
+  }
+}
+
+// ---- tiles of kTT tokens of one adapter ----
+// Adapter e's tiles are numbered from starts[e] / kTT + e on, which leaves room for each (a few numbers stay unused).
+constexpr int kTT = 128, kThreads = 256;
+struct Tile {
+  int bin, first, count;  // adapter (n: none), place of the first token, tokens (0: no such tile)
+};
+__device__ __forceinline__ Tile find_tile(const Args& a, int q, Tile* sh) {
+  if (threadIdx.x == 0) sh->count = 0;
+  __syncthreads();
+  for (int e = threadIdx.x; e <= a.n; e += kThreads) {
+    const int lo = a.starts[e], hi = a.starts[e + 1];
+    const int j = q - (lo / kTT + e);
+    if (j >= 0 && j * kTT < hi - lo) *sh = Tile{e, lo + j * kTT, min(kTT, hi - lo - j * kTT)};
+  }
+  __syncthreads();
+  return *sh;
+}
+inline int tile_numbers(int T, int n) { return T / kTT + n + 1; }
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// ---- v = A x: a tile of tokens and a share of H ----
+// A warp takes 16 tokens and all ranks.  Steps of 64 elements of H arrive by cp.async, 128-byte rows whose 16-byte chunks
+// are exchanged by the row.  Of 32 elements, lane t of a fragment takes chunk t: two k steps, in an order of its own
+// that both operands share.
+template <int NR>
+struct ShrinkCfg {
+  static constexpr int kStages = 3;
+  static constexpr int kXBytes = kTT * 128, kABytes = NR * 8 * 128, kStageBytes = kXBytes + kABytes;
+  static constexpr int kSmem = kStages * kStageBytes;
+};
+template <int NR>
+__global__ void __launch_bounds__(kThreads) lora_shrink_kernel(const Args a) {
+  using C = ShrinkCfg<NR>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ Tile tile_sh;
+  __shared__ int tokens[kTT];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2, t4 = lane & 3;
+  pdl_launch_dependents();
+  pdl_wait();
+  const Tile tl = find_tile(a, blockIdx.x, &tile_sh);
+  if (tl.count == 0 || tl.bin == a.n) return;
+  if (tid < kTT) tokens[tid] = tid < tl.count ? a.order[tl.first + tid] : -1;
+  const int rank = rank_of(a, tl.bin);
+  __syncthreads();
+  const uint32_t sbase = smem_u32(smem);
+  const int steps_all = (a.H + 63) / 64;
+  const int s0 = static_cast<int>(static_cast<long long>(steps_all) * blockIdx.y / a.splits);
+  const int s1 = static_cast<int>(static_cast<long long>(steps_all) * (blockIdx.y + 1) / a.splits);
+  const __nv_bfloat16* wa = a.a + static_cast<long long>(tl.bin) * a.R * a.H;
+  auto load = [&](int s, int slot) {
+    const uint32_t st = sbase + slot * C::kStageBytes;
+    const int c = tid & 7, k = s * 64 + c * 8;
+#pragma unroll
+    for (int i = 0; i < kTT / 32; ++i) {
+      const int r = i * 32 + (tid >> 3), t = tokens[r];
+      const bool on = t >= 0 && k < a.H;
+      cp_async16(sw128(st, r, c), on ? a.x + t * a.x_stride + k : a.x, on ? 16u : 0u);
+    }
+#pragma unroll
+    for (int i = 0; i < (NR * 8 + 31) / 32; ++i) {
+      const int r = i * 32 + (tid >> 3);
+      const bool on = r < rank && k < a.H;
+      if (NR * 8 >= 32 || r < NR * 8)
+        cp_async16(sw128(st + C::kXBytes, r, c), on ? wa + static_cast<long long>(r) * a.H + k : wa, on ? 16u : 0u);
+    }
+  };
+  float acc[NR][4];
+#pragma unroll
+  for (int i = 0; i < NR; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+#pragma unroll
+  for (int i = 0; i < C::kStages - 1; ++i) {
+    if (s0 + i < s1) load(s0 + i, i);
+    cp_commit();
+  }
+  for (int s = s0, slot = 0; s < s1; ++s) {
+    cp_wait<C::kStages - 2>();
+    __syncthreads();
+    {
+      int ns = slot + C::kStages - 1;
+      if (ns >= C::kStages) ns -= C::kStages;
+      if (s + C::kStages - 1 < s1) load(s + C::kStages - 1, ns);
+      cp_commit();
+    }
+    if (warp * 16 < tl.count) {
+      const uint32_t st = sbase + slot * C::kStageBytes;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint4 x0 = lds128(sw128(st, warp * 16 + g8, h * 4 + t4)), x1 = lds128(sw128(st, warp * 16 + g8 + 8, h * 4 + t4));
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+          const uint4 w = lds128(sw128(st + C::kXBytes, i * 8 + g8, h * 4 + t4));
+          mma_bf16(acc[i], x0.x, x1.x, x0.y, x1.y, w.x, w.y);
+          mma_bf16(acc[i], x0.z, x1.z, x0.w, x1.w, w.z, w.w);
+        }
+      }
+    }
+    if (++slot == C::kStages) slot = 0;
+  }
+  float* v = a.v + (static_cast<long long>(blockIdx.y) * a.T + tl.first) * (NR * 8);
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int r = warp * 16 + g8 + 8 * x;
+    if (r < tl.count) {
+#pragma unroll
+      for (int i = 0; i < NR; ++i)
+        *reinterpret_cast<float2*>(v + static_cast<long long>(r) * (NR * 8) + i * 8 + 2 * t4) = make_float2(acc[i][2 * x], acc[i][2 * x + 1]);
+    }
+  }
+}
+
+// ---- out = y + s B v: a tile of tokens and kCols columns ----
+// A warp takes 16 tokens and, at a time, 32 columns in an order that gives a lane 8 neighbouring ones (column 8 t + 2 j +
+// 0, 1 as columns 2 t + 0, 1 of instruction j), so that y and out move in 16-byte pieces.
+constexpr int kCols = 256;
+template <int NR>
+struct ExpandCfg {
+  static constexpr int kRow = NR * 16;  // bytes of a row of B
+  static constexpr int kSmem = kCols * kRow;
+};
+// 16-byte chunk c of column n: rows of 128 bytes or more exchange halves of 128 bytes by the row
+template <int NR>
+__device__ __forceinline__ uint32_t b_at(int n, int c) {
+  return static_cast<uint32_t>(n * (NR * 16) + ((NR >= 8 ? c ^ ((n & 1) << 2) : c) << 4));
+}
+template <int NR>
+__global__ void __launch_bounds__(kThreads) lora_expand_kernel(const Args a) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ Tile tile_sh;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2, t4 = lane & 3;
+  pdl_launch_dependents();
+  pdl_wait();
+  const Tile tl = find_tile(a, blockIdx.x, &tile_sh);
+  if (tl.count == 0) return;
+  const int col0 = blockIdx.y * kCols;
+  const bool none = tl.bin == a.n;
+  if (none && a.out == a.y && a.out_stride == a.y_stride) return;
+  const int rank = none ? 0 : rank_of(a, tl.bin);
+  const uint32_t sbase = smem_u32(smem);
+  if (!none) {
+    const __nv_bfloat16* wb = a.b + static_cast<long long>(tl.bin) * a.N * a.R;
+    for (int i = tid; i < kCols * NR; i += kThreads) {
+      const int n = i / NR, c = i % NR, left = min(16, 2 * (rank - c * 8));  // (a rank need not be a multiple of 8)
+      const bool on = col0 + n < a.N && left > 0;
+      cp_async16(sbase + b_at<NR>(n, c), on ? wb + static_cast<long long>(col0 + n) * a.R + c * 8 : wb, on ? left : 0);
+    }
+  }
+  cp_commit();
+  const int r0 = warp * 16 + g8;
+  const bool on0 = r0 < tl.count, on1 = r0 + 8 < tl.count;
+  const long long tok0 = on0 ? a.order[tl.first + r0] : 0, tok1 = on1 ? a.order[tl.first + r0 + 8] : 0;
+  constexpr int kKS = NR / 2;  // k steps
+  uint32_t hi[kKS][4], lo[kKS][4];
+#pragma unroll
+  for (int s = 0; s < kKS; ++s)
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      // elements 8 t + 4 (s % 2) .. + 3 of every 32, or 4 t .. + 3 of 16
+      const int e = NR == 2 ? 4 * t4 : 32 * (s >> 1) + 8 * t4 + 4 * (s & 1);
+      float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+      if ((x ? on1 : on0) && !none) {
+        for (int p = 0; p < a.splits; ++p) {
+          const float4 z = __ldcg(reinterpret_cast<const float4*>(a.v + (static_cast<long long>(p) * a.T + tl.first + r0 + 8 * x) * (NR * 8) + e));
+          f.x += z.x;
+          f.y += z.y;
+          f.z += z.z;
+          f.w += z.w;
+        }
+      }
+      const uint32_t h0 = pack_bf16x2(f.x, f.y), h1 = pack_bf16x2(f.z, f.w);
+      hi[s][x] = h0;
+      hi[s][2 + x] = h1;
+      lo[s][x] = pack_bf16x2(f.x - __uint_as_float(h0 << 16), f.y - __uint_as_float(h0 & 0xFFFF0000u));
+      lo[s][2 + x] = pack_bf16x2(f.z - __uint_as_float(h1 << 16), f.w - __uint_as_float(h1 & 0xFFFF0000u));
+    }
+  const float scale = none ? 0.f : (a.scale ? __ldg(a.scale + tl.bin) : 1.f);
+  const __nv_bfloat16 *y0 = a.y + tok0 * a.y_stride, *y1 = a.y + tok1 * a.y_stride;
+  __nv_bfloat16 *o0 = a.out + tok0 * a.out_stride, *o1 = a.out + tok1 * a.out_stride;
+  cp_wait<0>();
+  __syncthreads();
+  if (warp * 16 >= tl.count) return;
+#pragma unroll 2
+  for (int n0 = 0; n0 < kCols; n0 += 32) {
+    const int col = col0 + n0 + 8 * t4;
+    if (col0 + n0 >= a.N) break;
+    const bool in0 = on0 && col < a.N, in1 = on1 && col < a.N;
+    uint4 u0 = make_uint4(0, 0, 0, 0), u1 = u0;
+    if (in0) u0 = *reinterpret_cast<const uint4*>(y0 + col);
+    if (in1) u1 = *reinterpret_cast<const uint4*>(y1 + col);
+    if (!none) {
+      float acc[4][4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+        const int n = n0 + 8 * (g8 >> 1) + 2 * j + (g8 & 1);
+#pragma unroll
+        for (int s = 0; s < kKS; s += 2) {
+          if constexpr (NR == 2) {
+            const uint2 w = *reinterpret_cast<const uint2*>(smem + b_at<NR>(n, t4 >> 1) + 8 * (t4 & 1));
+            mma_bf16(acc[j], hi[0][0], hi[0][1], hi[0][2], hi[0][3], w.x, w.y);
+            mma_bf16(acc[j], lo[0][0], lo[0][1], lo[0][2], lo[0][3], w.x, w.y);
+          } else {
+            const uint4 w = *reinterpret_cast<const uint4*>(smem + b_at<NR>(n, 2 * s + t4));
+            mma_bf16(acc[j], hi[s][0], hi[s][1], hi[s][2], hi[s][3], w.x, w.y);
+            mma_bf16(acc[j], lo[s][0], lo[s][1], lo[s][2], lo[s][3], w.x, w.y);
+            mma_bf16(acc[j], hi[s + 1][0], hi[s + 1][1], hi[s + 1][2], hi[s + 1][3], w.z, w.w);
+            mma_bf16(acc[j], lo[s + 1][0], lo[s + 1][1], lo[s + 1][2], lo[s + 1][3], w.z, w.w);
+          }
+        }
+      }
+      auto add = [&](uint32_t u, float p, float q) {
+        return pack_bf16x2(fmaf(scale, p, __uint_as_float(u << 16)), fmaf(scale, q, __uint_as_float(u & 0xFFFF0000u)));
+      };
+      u0 = make_uint4(add(u0.x, acc[0][0], acc[0][1]), add(u0.y, acc[1][0], acc[1][1]), add(u0.z, acc[2][0], acc[2][1]), add(u0.w, acc[3][0], acc[3][1]));
+      u1 = make_uint4(add(u1.x, acc[0][2], acc[0][3]), add(u1.y, acc[1][2], acc[1][3]), add(u1.z, acc[2][2], acc[2][3]), add(u1.w, acc[3][2], acc[3][3]));
+    }
+    if (in0) *reinterpret_cast<uint4*>(o0 + col) = u0;
+    if (in1) *reinterpret_cast<uint4*>(o1 + col) = u1;
+  }
+}
+
+// ---- host ----
+
+inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+inline int padded(int R) { return R <= 16 ? 16 : (R <= 32 ? 32 : (R <= 64 ? 64 : 128)); }
+// Shares of H in the first product: as many as fill the GPU, 256 elements each at least.
+inline int splits_of(int T, int H) {
+  const int tiles = (T + kTT - 1) / kTT;
+  return std::max(1, std::min({2 * current_sm_count() / tiles, H / 256, 16}));
+}
+struct Workspace {
+  size_t starts, order, v, bytes;
+};
+inline Workspace workspace_of(int T, int H, int R, int n) {
+  Workspace w;
+  w.starts = 0;
+  w.order = up256((static_cast<size_t>(n) + 2) * 4);
+  w.v = w.order + up256(static_cast<size_t>(T) * 4);
+  w.bytes = w.v + up256(static_cast<size_t>(splits_of(T, H)) * T * padded(R) * 4);
+  return w;
+}
+
+template <int NR>
+int launch(Args& a, uint8_t* ws, cudaStream_t st) {
+  const Workspace w = workspace_of(a.T, a.H, a.R, a.n);
+  a.starts = reinterpret_cast<int32_t*>(ws + w.starts);
+  a.order = reinterpret_cast<int32_t*>(ws + w.order);
+  a.v = reinterpret_cast<float*>(ws + w.v);
+  a.splits = splits_of(a.T, a.H);
+  auto shrink = lora_shrink_kernel<NR>;
+  auto expand = lora_expand_kernel<NR>;
+  static std::atomic<uint64_t> attr{0};
+  uint64_t bit;
+  if (attrs_needed(attr, &bit)) {
+    if (cudaFuncSetAttribute(shrink, cudaFuncAttributeMaxDynamicSharedMemorySize, ShrinkCfg<NR>::kSmem) != cudaSuccess ||
+        cudaFuncSetAttribute(expand, cudaFuncAttributeMaxDynamicSharedMemorySize, ExpandCfg<NR>::kSmem) != cudaSuccess)
+      return MNW_E_CUDA;
+    attrs_done(attr, bit);
+  }
+  const unsigned tiles = tile_numbers(a.T, a.n);
+  if (launch_pdl(lora_group_kernel, dim3(a.n + 1), dim3(kGroupThreads), 0, st, a) != cudaSuccess ||
+      launch_pdl(shrink, dim3(tiles, a.splits), dim3(kThreads), ShrinkCfg<NR>::kSmem, st, a) != cudaSuccess ||
+      launch_pdl(expand, dim3(tiles, (a.N + kCols - 1) / kCols), dim3(kThreads), ExpandCfg<NR>::kSmem, st, a) != cudaSuccess)
+    return MNW_E_CUDA;
+  return MNW_OK;
+}
+
+}  // namespace lora
+}  // namespace mnw
+
+using namespace mnw;
+
+extern "C" {
+
+size_t mnw_lora_workspace_size(int T, int H, int R, int n_adapters) {
+  if (T <= 0 || H <= 0 || R <= 0 || R > 128 || n_adapters <= 0) return 0;
+  return lora::workspace_of(T, H, R, n_adapters).bytes;
+}
+
+int mnw_lora_add(const void* x, long long x_stride, const void* a, const void* b, const float* scale,
+                 const int32_t* ranks, int n_adapters, int R, const int32_t* adapter, int T, int H, int N,
+                 const void* y, long long y_stride, void* out, long long out_stride, void* ws, size_t ws_bytes,
+                 uint32_t* err, mnw_stream stream) {
+  MNW_RANGE("mnw_lora_add");
+  if (T < 0 || H <= 0 || N <= 0 || R <= 0 || n_adapters <= 0) return MNW_E_INVALID_ARG;
+  if (T == 0) return MNW_OK;
+  if (H % 8 || N % 8 || R % 8 || R > 128 || n_adapters > 1024 || T > (1 << 24) || N > (1 << 20)) return MNW_E_UNSUPPORTED;
+  if (!x || !a || !b || !adapter || !y || !out || !ws || !aligned(x, 16) || !aligned(a, 16) || !aligned(b, 16) ||
+      !aligned(y, 16) || !aligned(out, 16) || !aligned(ws, 256) || !aligned(adapter, 4) || !aligned(ranks, 4) ||
+      !aligned(scale, 4) || x_stride % 8 || y_stride % 8 || out_stride % 8 || x_stride < H || y_stride < N || out_stride < N)
+    return MNW_E_INVALID_ARG;
+  if (y == out && y_stride != out_stride && T > 1) return MNW_E_INVALID_ARG;  // rows of one over others of the other
+  if (ws_bytes < mnw_lora_workspace_size(T, H, R, n_adapters)) return MNW_E_WORKSPACE_TOO_SMALL;
+  lora::Args p{};
+  p.x = static_cast<const __nv_bfloat16*>(x);
+  p.a = static_cast<const __nv_bfloat16*>(a);
+  p.b = static_cast<const __nv_bfloat16*>(b);
+  p.y = static_cast<const __nv_bfloat16*>(y);
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.x_stride = x_stride;
+  p.y_stride = y_stride;
+  p.out_stride = out_stride;
+  p.scale = scale;
+  p.ranks = ranks;
+  p.adapter = adapter;
+  p.n = n_adapters;
+  p.R = R;
+  p.T = T;
+  p.H = H;
+  p.N = N;
+  p.err = err;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  auto* w = static_cast<uint8_t*>(ws);
+  switch (lora::padded(R)) {
+    case 16: return lora::launch<2>(p, w, st);
+    case 32: return lora::launch<4>(p, w, st);
+    case 64: return lora::launch<8>(p, w, st);
+    default: return lora::launch<16>(p, w, st);
+  }
+}
+
+}  // extern "C"
