@@ -9,17 +9,22 @@
 // rows; P^T goes in with keys along k, which is that tile transposed
 // (movmatrix).
 //
-// A CTA is four warps, each with 32 keys of a tile of 128 and all 8 NT query
-// rows.  Tiles arrive by cp.async through a ring, one page lookup a key, so
-// pages of any size may end inside a tile; rows past the length are zeros.
+// A CTA is four warps, each with 64 keys of a tile of 256 and all 8 NT query
+// rows.  The warps meet only at an item's end: each loads its own keys through
+// a ring of its own, as bulk copies (a lane per page, waited for on a barrier
+// of the ring's slot) where its keys lie inside the length in whole pieces of
+// pages, and else by 16-byte cp.async with a page lookup per key, so pages of
+// any size may end inside a tile; rows past the length are zeros.
 //
 // Operands are FP16 and exact but for the probabilities: codes times the
 // group's multiplier (as multiples of 2^-24), q as FP16 times a power of two a
 // row; the keys' scales multiply the FP32 scores.  A probability times its
 // value's scale is rounded to FP16 (2^-11 relative) relative to the row's
 // largest such product so far, lifted by 2^6, so one 2^-30 of the largest is
-// still held.  Maximum and unit of a row move only when a score passes them by
-// more than 2^8, so that most tiles need no reduction over the warp.
+// still held.  Maximum and unit of a row move only when a probability passes
+// 2^8 or a product 2^14; that is looked for in what was computed, and the tile's
+// probabilities are then computed again, so most tiles need no reduction over
+// the warp.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -31,36 +36,25 @@ namespace pattn {
 namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32, kTK = kInt4Keys;
-constexpr int kStages = 3;
-constexpr float kLow = -1e30f;   // a maximum of nothing: finite, so that -inf minus it is -inf
-constexpr float kStep = 8.f;     // log2 by which scores may pass a row's maximum and unit
+constexpr int kWK = kTK / kWarps;  // keys of a warp
+constexpr int kMT = 2, kSubs = kWK / (16 * kMT);  // 16-key operand tiles computed together, and such groups
+constexpr int kStages = 2;
 constexpr float kHalfUnit = 4096.f;  // the operands' 2^-24 is taken back half with the keys' scales, half with the queries' factors
-constexpr float kLift = 6.f;     // log2: the largest FP16 value is 2^(kStep + kLift) = 2^14
+constexpr float kLow = -1e30f;   // a maximum of nothing: finite, so that -inf minus it is -inf
+constexpr float kLift = 6.f;     // log2 of the unit's own product as FP16
+constexpr float kMostP = 256.f, kMostW = 16384.f;  // probabilities and products that a row's maximum and unit allow
 
 template <int D, int NT>
 struct Cfg4 {
   static constexpr int kRT = 8 * NT;
   static constexpr int kRowBytes = D / 2;
-  static constexpr int kTileBytes = kTK * kRowBytes;
-  static constexpr int kStageBytes = 2 * kTileBytes + 2 * kTK * int4row::kRecord;
+  static constexpr int kTileBytes = kWK * kRowBytes, kRecBytes = kWK * int4row::kRecord;  // of a warp's keys
+  static constexpr int kSlotBytes = 2 * (kTileBytes + kRecBytes);  // keys, values, their records
   static constexpr int kQBytes = NT > 2 ? (D / 16) * NT * 32 * 8 : 0;  // query fragments, where registers cannot hold them
-  static constexpr int kSmem = kStages * kStageBytes + kQBytes;
-  static constexpr int kPad = D + 4;  // of a row where the warps' outputs meet, in the stage just read
-  static_assert(kWarps * 8 * kPad * 4 <= kStageBytes);
-  static_assert(kThreads / (D / 4) * 2 * kJoinBatch * 4 <= kStageBytes);
+  static constexpr int kSmem = kWarps * kStages * kSlotBytes + kQBytes;
+  static constexpr int kPad = D + 4;  // floats of a row where the warps' outputs meet, in the slots just read
+  static_assert(8 * kPad * 4 <= kSlotBytes && kThreads / (D / 4) * 2 * kJoinBatch * 4 <= kSlotBytes);
 };
-
-// Values lie with neighbouring keys' rows apart, so that the lanes of a load (keys 2 t, pieces g of a row) fall into
-// different banks.
-template <int D>
-__device__ __forceinline__ uint32_t v_at(int r, int byte) {
-  if constexpr (D == 128) {
-    const int p = r ^ ((r >> 1) & 1);
-    return static_cast<uint32_t>(p * 64 + (byte ^ ((p & 4) << 3)));
-  } else {
-    return static_cast<uint32_t>((r ^ ((r >> 2) & 1)) * 32 + byte);
-  }
-}
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -79,30 +73,43 @@ __device__ __forceinline__ uint32_t half2_of(float a, float b) {
 __device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
+// Two FP32 values in a 64-bit register.
+__device__ __forceinline__ uint64_t two(float lo, float hi) { return f32x2_pack(__float_as_uint(lo), __float_as_uint(hi)); }
+__device__ __forceinline__ float lo32(uint64_t x) { return __uint_as_float(static_cast<uint32_t>(x)); }
+__device__ __forceinline__ float hi32(uint64_t x) { return __uint_as_float(static_cast<uint32_t>(x >> 32)); }
+
+// Row i of a warp's 16-key operand tiles is key i ^ (i / 2 % 2): the keys that a load's lanes read then lie in rows of
+// both parities, whose 64 bytes are the two halves of the banks.
+__device__ __forceinline__ int key_of(int i) { return i ^ ((i >> 1) & 1); }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, int4_runs_per_sm(8 * NT)) paged_int4_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, int4_runs_per_sm(8 * NT)) paged_int4_kernel(const Args a, const int whole_pages) {
   using C = Cfg4<D, NT>;
   constexpr int kRT = C::kRT;
   constexpr int kKS = D / 16;   // k steps of the first product
   constexpr int kNO = D / 16;   // row tiles of the second
-  constexpr int kMT = kTK / kWarps / 16;  // 16-key tiles of a warp
   constexpr int kW = D / 64;    // words of a lane's piece of a value row; half of those of a key's
   constexpr bool kQRegs = NT <= 2;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ SplitShared split;
   __shared__ float2 ml[kWarps][kRT];
-  __shared__ long long row_at[kStages][kTK];  // byte offset of a tile's keys' cached rows, -1: none
-  __shared__ long long rec_at[kStages][kTK];  // and of their records
+  __shared__ uint64_t full[kWarps][kStages];  // a slot's bulk copies have landed
+  __shared__ int abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g8 = lane >> 2, t4 = lane & 3;
-  const uint32_t sbase = smem_u32(smem);
-  uint2* const qs = reinterpret_cast<uint2*>(smem + kStages * C::kStageBytes);  // [k step][n tile][lane]
+  uint8_t* const mine = smem + warp * (kStages * C::kSlotBytes);  // the warp's ring
+  uint2* const qs = reinterpret_cast<uint2*>(smem + kWarps * kStages * C::kSlotBytes);  // [k step][n tile][lane]
 
   pdl_launch_dependents();
+  if (tid == 0) {
+    for (int w = 0; w < kWarps; ++w)
+      for (int i = 0; i < kStages; ++i) mbar_init(&full[w][i], 1);
+    abort_flag = 0;
+    fence_barrier_init();
+  }
   pdl_wait();
 
-  const Run run = find_run<kRT, kTK, kThreads, 0>(a, &split);
+  const Run run = find_run<kRT, kTK, kThreads, 0>(a, &split);  // (with barriers, behind which full[] is set up)
   if (run.seq < 0) return;  // no units left for this run
   Cursor<kRT, kTK> cc;  // the tile computed
   cc.set(a, run);
@@ -110,69 +117,91 @@ __global__ void __launch_bounds__(kThreads, int4_runs_per_sm(8 * NT)) paged_int4
   const int tiles = run.pad == 1 ? run.u1 - run.u0 : min(run.u1 - run.u0, cc.sh.kt - cc.kt);
   if (tiles <= 0) return;
 
-  // ---- tile loads: page lookups run one tile ahead of the copies, those kStages - 1 ahead of the products ----
+  // ---- loads of the warp's keys: whole pieces of pages are looked up a tile before they are copied ----
   Cursor<kRT, kTK> lc = cc;  // the tile looked up next
-  auto look = [&](int2& at) {  // raw page entry and head row of key tid of tile lc; then on to the next tile
-    const int p = lc.kt * kTK + tid;
-    at = make_int2(0, -1);
-    if (p < lc.s.len) {
-      const int pi = static_cast<int>(paged::quotient(p, a.page_div));
-      at.x = __ldg(a.bt.block_table + static_cast<size_t>(lc.b) * a.bt.max_pages + pi);
-      at.y = lc.g * a.page_size + (p - pi * a.page_size);
+  const int span = min(a.page_size, kWK);  // keys of a piece
+  auto row_of = [&](int p, int& entry, int& row) {  // page table entry of position p, and its row in the page
+    const int pi = static_cast<int>(paged::quotient(p, a.page_div));
+    entry = __ldg(a.bt.block_table + static_cast<size_t>(lc.b) * a.bt.max_pages + pi);
+    row = lc.g * a.page_size + (p - pi * a.page_size);
+  };
+  int entry = 0, row = 0;  // of lane i's piece
+  bool bulk;
+  auto look = [&]() {
+    const int p0 = lc.kt * kTK + warp * kWK;
+    bulk = whole_pages && p0 + kWK <= lc.s.len;
+    if (bulk && lane * span < kWK) row_of(p0 + lane * span, entry, row);
+  };
+  uint32_t phases = 0, bulks = 0;  // per slot: parity of its barrier's next phase; whether bulk copies are under way to it
+  bool gave_up = false;            // a wait ran out: reported, and the result is void
+  auto fill = [&](int slot) {  // what look() found, into a slot that the whole warp has read; then on to the next tile
+    uint8_t* to = mine + slot * C::kSlotBytes;
+    const bool piece = lane * span < kWK;
+    if (bulk && !__any_sync(0xffffffffu, piece && static_cast<unsigned>(entry) >= static_cast<unsigned>(a.n_pages))) {
+      bulks |= 1u << slot;
+      uint64_t* bar = &full[warp][slot];
+      if (lane == 0) mbar_arrive_expect_tx(bar, C::kSlotBytes);
+      __syncwarp();
+      if (piece) {
+        const long long at = entry * a.page_bytes + static_cast<long long>(row) * C::kRowBytes;
+        const long long rec = (static_cast<long long>(entry) * (a.Hkv * a.page_size) + row) * int4row::kRecord;
+        const uint32_t nrow = span * C::kRowBytes, nrec = span * int4row::kRecord;
+        bulk_load(to + lane * nrow, a.kc + at, nrow, bar);
+        bulk_load(to + C::kTileBytes + lane * nrow, a.vc + at, nrow, bar);
+        bulk_load(to + 2 * C::kTileBytes + lane * nrec, reinterpret_cast<const uint8_t*>(a.ks) + rec, nrec, bar);
+        bulk_load(to + 2 * C::kTileBytes + C::kRecBytes + lane * nrec, reinterpret_cast<const uint8_t*>(a.vs) + rec, nrec, bar);
+      }
+    } else {
+      constexpr int kCh = C::kRowBytes / 16, kRows = 32 / kCh;
+      const int c = lane % kCh;
+      const uint32_t st = smem_u32(to);
+#pragma unroll 1
+      for (int k0 = 0; k0 < kWK; k0 += 32) {  // a key a lane
+        const int p = lc.kt * kTK + warp * kWK + k0 + lane;
+        int e = -1, r = 0;
+        if (p < lc.s.len) {
+          row_of(p, e, r);
+          if (static_cast<unsigned>(e) >= static_cast<unsigned>(a.n_pages)) {
+            e = -1;
+            if (a.err) atomicOr(a.err, MNW_DEVERR_BAD_PAGE);
+          }
+        }
+        const bool has = e >= 0;
+        const long long at = has ? e * a.page_bytes + static_cast<long long>(r) * C::kRowBytes : -1;
+#pragma unroll 1
+        for (int i = 0; i < 32 / kRows; ++i) {
+          const int key = i * kRows + lane / kCh;
+          const long long from = __shfl_sync(0xffffffffu, at, key);
+          const uint32_t n = from >= 0 ? 16u : 0u, dst = st + (k0 + key) * C::kRowBytes + c * 16;
+          const long long off = n ? from + c * 16 : 0;
+          cp_async16(dst, a.kc + off, n);
+          cp_async16(dst + C::kTileBytes, a.vc + off, n);
+        }
+        const long long rec = has ? (static_cast<long long>(e) * (a.Hkv * a.page_size) + r) * int4row::kRecord : 0;
+        const uint32_t dst = st + 2 * C::kTileBytes + (k0 + lane) * int4row::kRecord;
+        cp_async8(dst, reinterpret_cast<const uint8_t*>(a.ks) + rec, has ? 8u : 0u);
+        cp_async8(dst + C::kRecBytes, reinterpret_cast<const uint8_t*>(a.vs) + rec, has ? 8u : 0u);
+      }
     }
+    cp_commit();
     if (++lc.kt == lc.sh.kt) lc.next_item(a, run.pad);
   };
-  auto keep = [&](int2 at, int slot) {
-    bool has = at.y >= 0;
-    if (has && static_cast<unsigned>(at.x) >= static_cast<unsigned>(a.n_pages)) {
-      has = false;
-      if (a.err) atomicOr(a.err, MNW_DEVERR_BAD_PAGE);
-    }
-    row_at[slot][tid] = has ? at.x * a.page_bytes + static_cast<long long>(at.y) * C::kRowBytes : -1;
-    rec_at[slot][tid] = (static_cast<long long>(at.x) * a.Hkv * a.page_size + at.y) * int4row::kRecord;
-  };
-  auto load_tile = [&](int slot) {
-    const uint32_t st = sbase + slot * C::kStageBytes;
-    constexpr int kCh = C::kRowBytes / 16;  // chunks per row
-    constexpr int kRP = kThreads / kCh;     // rows per pass
-    const int c = tid % kCh;
-#pragma unroll
-    for (int i = 0; i < kTK / kRP; ++i) {
-      const int r = i * kRP + tid / kCh;
-      const long long at = row_at[slot][r];
-      const uint32_t n = at >= 0 ? 16u : 0u;
-      const long long off = n ? at + c * 16 : 0;
-      cp_async16(st + r * C::kRowBytes + c * 16, a.kc + off, n);
-      cp_async16(st + C::kTileBytes + v_at<D>(r, c * 16), a.vc + off, n);
-    }
-    const uint32_t n = row_at[slot][tid] >= 0 ? 8u : 0u;
-    const long long off = n ? rec_at[slot][tid] : 0;
-    const uint32_t to = st + 2 * C::kTileBytes + tid * int4row::kRecord;
-    cp_async8(to, reinterpret_cast<const char*>(a.ks) + off, n);
-    cp_async8(to + kTK * int4row::kRecord, reinterpret_cast<const char*>(a.vs) + off, n);
-  };
-  {
-    int2 at[kStages];
-#pragma unroll
-    for (int i = 0; i < kStages; ++i)
-      if (i < tiles) look(at[i]);
-#pragma unroll
-    for (int i = 0; i < kStages; ++i)
-      if (i < tiles) keep(at[i], i);
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) {
-      if (i < tiles) load_tile(i);
+#pragma unroll 1
+  for (int i = 0; i < kStages; ++i) {
+    if (i < tiles) {
+      look();
+      fill(i);
+    } else {
       cp_commit();
     }
   }
 
-  // ---- state of the item in hand; of rows 8 nt + 2 t4 + x ----
+  // ---- state of the item in hand; of rows 8 nt + 2 t4 and + 1, packed ----
   uint32_t qf[kQRegs ? kKS : 1][kQRegs ? NT : 1][2];
-  float qfac[NT][2];                      // score factor
-  float m[NT][2], l[NT][2], unit[NT][2];  // log2 of the weights' reference, sum, log2 of the products' reference
-  float lift[NT][2];
-  int lim[NT][2];                         // first key that is not seen
+  uint64_t qfac[NT];                    // score factors
+  uint64_t neg[NT], sum[NT], lift[NT];  // minus the maximum (log2), sum, 2^(maximum - unit + kLift)
+  float unit[NT][2];                    // log2 of the products' reference
+  int lim[NT][2];                       // first key that is not seen
   float o[kNO][NT][4];
   int rows = 0, lim_lo = 0, lim_hi = 0, kt_begin = 0;
   auto begin_item = [&]() {
@@ -195,10 +224,10 @@ __global__ void __launch_bounds__(kThreads, int4_runs_per_sm(8 * NT)) paged_int4
       for (int x = 0; x < 2; ++x) {
         const int r = 8 * nt + 2 * t4 + x;
         lim[nt][x] = r < rows ? row_limit(a, cc.s, ri + r) : lim_hi;
-        m[nt][x] = unit[nt][x] = kLow;
-        l[nt][x] = 0.f;
-        lift[nt][x] = 0.f;
+        unit[nt][x] = kLow;
       }
+      neg[nt] = two(-kLow, -kLow);
+      sum[nt] = lift[nt] = 0ull;
       // Row 8 nt + g8 as the right operand: k step s takes elements (D / 4) t4 + 4 s .. + 3 of lane t4, the order in
       // which a lane's words of codes hold them.
       const int r = 8 * nt + g8, rr = ri + (r < rows ? r : 0);
@@ -231,43 +260,53 @@ __global__ void __launch_bounds__(kThreads, int4_runs_per_sm(8 * NT)) paged_int4
           }
         }
       }
-#pragma unroll
-      for (int x = 0; x < 2; ++x)
-        qfac[nt][x] = a.scale_log2 * kHalfUnit * two_to(__shfl_sync(0xffffffffu, e, 4 * (2 * t4 + x)));
+      const float f0 = two_to(__shfl_sync(0xffffffffu, e, 4 * (2 * t4))), f1 = two_to(__shfl_sync(0xffffffffu, e, 4 * (2 * t4 + 1)));
+      qfac[nt] = two(a.scale_log2 * kHalfUnit * f0, a.scale_log2 * kHalfUnit * f1);
     }
     if constexpr (!kQRegs) __syncthreads();
   };
 
-  for (int t = 0, slot = 0; t < tiles; ++t) {
-    cp_wait<kStages - 2>();
-    __syncthreads();
-    {
-      int ns = slot + kStages - 1;
-      if (ns >= kStages) ns -= kStages;
-      if (t + kStages - 1 < tiles) load_tile(ns);
-      cp_commit();
-    }
-    int2 ahead;
-    const bool more = t + kStages < tiles;
-    if (more) look(ahead);
-    if (t == 0 || cc.kt == 0) begin_item();
-    uint8_t* stage = smem + slot * C::kStageBytes;
+  // byte offsets of what a lane reads: keys' and values' rows and records
+  const int k_row = key_of(g8) * C::kRowBytes + t4 * (D / 8), k_rec = key_of(g8) * int4row::kRecord;
+  const int v_key0 = key_of(2 * t4), v_key1 = key_of(2 * t4 + 1);
+  const uint32_t ksel = t4 * 0x101u;                      // the lane's codes of a key are of group t4,
+  const uint32_t vsel = (g8 >> 1) * 0x101u + 0x400u;      // its elements of a value of group g8 / 2
 
-    if (cc.kt * kTK < lim_hi) {  // a tile past every row's limit adds nothing
-      const uint8_t *krec = stage + 2 * C::kTileBytes, *vrec = krec + kTK * int4row::kRecord;
-      const int k0 = warp * (kTK / kWarps);  // the warp's first key of the tile
-      // ---- scores: keys 16 mt + g8 (+ 8) in rows, query rows 8 nt + 2 t4 (+ 1) in columns ----
+#pragma unroll 1
+  for (int t = 0, slot = 0; t < tiles; ++t) {
+    const bool more = t + kStages < tiles;
+    if (more) look();
+    if (t == 0 || cc.kt == 0) begin_item();
+    cp_wait<kStages - 1>();
+    const bool by_rows = !(bulks >> slot & 1);
+    if (!by_rows && !gave_up) {
+      bool there = mbar_try_wait(&full[warp][slot], phases >> slot & 1);
+      if (!there) there = polled_wait(&full[warp][slot], phases >> slot & 1, &abort_flag, a.err);
+      gave_up = !__all_sync(0xffffffffu, there);
+      if (!gave_up) {
+        phases ^= 1u << slot;
+        bulks ^= 1u << slot;
+      }
+    }
+    __syncwarp();
+#pragma unroll 1
+    for (int sub = 0; sub < kSubs; ++sub) {
+      const int p0 = cc.kt * kTK + warp * kWK + sub * (16 * kMT);  // the first position
+      if (p0 >= lim_hi) break;                                     // keys past every row's limit add nothing
+      const uint8_t* const st = mine + slot * C::kSlotBytes + sub * (16 * kMT) * C::kRowBytes;
+      const uint8_t* const krec = mine + slot * C::kSlotBytes + 2 * C::kTileBytes + sub * (16 * kMT) * int4row::kRecord;
+      const uint8_t* const vrec = krec + C::kRecBytes;
+      // ---- scores: keys 16 mt + 8 h + g8 in rows, query rows 8 nt + 2 t4 (+ 1) in columns ----
       float sc[kMT][NT][4];
+      uint64_t fac[kMT][NT][2];
       {
         uint32_t kw[kMT][2][2 * kW];
         int4row::Mul km[kMT][2];
-        float ks[kMT][2];
 #pragma unroll
         for (int mt = 0; mt < kMT; ++mt) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const int key = k0 + 16 * mt + 8 * h + g8;
-            const uint8_t* at = stage + key * C::kRowBytes + t4 * (D / 8);
+            const uint8_t* at = st + k_row + (16 * mt + 8 * h) * C::kRowBytes;
             if constexpr (D == 128) {
               const uint4 w = *reinterpret_cast<const uint4*>(at);
               kw[mt][h][0] = w.x; kw[mt][h][1] = w.y; kw[mt][h][2] = w.z; kw[mt][h][3] = w.w;
@@ -275,9 +314,11 @@ __global__ void __launch_bounds__(kThreads, int4_runs_per_sm(8 * NT)) paged_int4
               const uint2 w = *reinterpret_cast<const uint2*>(at);
               kw[mt][h][0] = w.x; kw[mt][h][1] = w.y;
             }
-            const uint2 rec = *reinterpret_cast<const uint2*>(krec + key * int4row::kRecord);
-            ks[mt][h] = __uint_as_float(rec.x) * kHalfUnit;
-            km[mt][h] = int4row::multipliers(prmt(rec.y, 0u, t4 * 0x101u));  // the lane's codes are of group t4
+            const uint2 rec = *reinterpret_cast<const uint2*>(krec + k_rec + (16 * mt + 8 * h) * int4row::kRecord);
+            const float ks = __uint_as_float(rec.x) * kHalfUnit;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) fac[mt][nt][h] = two(ks * lo32(qfac[nt]), ks * hi32(qfac[nt]));
+            km[mt][h] = int4row::multipliers(prmt(rec.y, 0u, ksel));
           }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) sc[mt][nt][0] = sc[mt][nt][1] = sc[mt][nt][2] = sc[mt][nt][3] = 0.f;
@@ -307,43 +348,53 @@ __global__ void __launch_bounds__(kThreads, int4_runs_per_sm(8 * NT)) paged_int4
             }
           }
         }
+      }
+      if (p0 + 16 * kMT > lim_lo) {  // some row's limit lies among these keys
 #pragma unroll
         for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sc[mt][nt][e] *= ks[mt][e >> 1] * qfac[nt][e & 1];
+            for (int h = 0; h < 2; ++h) {
+              const int p = p0 + 16 * mt + 8 * h + key_of(g8);
+              sc[mt][nt][2 * h] = p >= lim[nt][0] ? -INFINITY : sc[mt][nt][2 * h] * lo32(fac[mt][nt][h]);
+              sc[mt][nt][2 * h + 1] = p >= lim[nt][1] ? -INFINITY : sc[mt][nt][2 * h + 1] * hi32(fac[mt][nt][h]);
+              fac[mt][nt][h] = two(1.f, 1.f);
+            }
+          }
       }
-      if ((cc.kt + 1) * kTK > lim_lo) {  // some row's limit lies in this tile
-#pragma unroll
-        for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (cc.kt * kTK + k0 + 16 * mt + 8 * (e >> 1) + g8 >= lim[nt][e & 1]) sc[mt][nt][e] = -INFINITY;
-      }
-      // ---- maximum and unit, where a score passes them ----
-      float vs[kMT][2], lv[kMT][2];
+      // ---- probabilities, and their products with the values' scales as FP16 ----
+      float vs[kMT][2];
 #pragma unroll
       for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          vs[mt][h] = *reinterpret_cast<const float*>(vrec + (k0 + 16 * mt + 8 * h + g8) * int4row::kRecord);
-          lv[mt][h] = __log2f(fabsf(vs[mt][h]));
+        for (int h = 0; h < 2; ++h) vs[mt][h] = *reinterpret_cast<const float*>(vrec + k_rec + (16 * mt + 8 * h) * int4row::kRecord);
+      uint32_t pw[kMT][NT][2];
+      uint64_t now[NT];
+#pragma unroll 1
+      for (int pass = 0; pass < 2; ++pass) {
+        float most_p = 0.f, most_w = 0.f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          now[nt] = sum[nt];
+#pragma unroll
+          for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint64_t e2 = f32x2_fma(two(sc[mt][nt][2 * h], sc[mt][nt][2 * h + 1]), fac[mt][nt][h], neg[nt]);
+              const uint64_t p2 = two(ex2(lo32(e2)), ex2(hi32(e2)));
+              now[nt] = f32x2_add(now[nt], p2);
+              const uint64_t w2 = f32x2_mul(p2, two(vs[mt][h] * lo32(lift[nt]), vs[mt][h] * hi32(lift[nt])));
+              most_p = fmaxf(fmaxf(most_p, lo32(p2)), hi32(p2));
+              most_w = fmaxf(fmaxf(most_w, fabsf(lo32(w2))), fabsf(hi32(w2)));
+              pw[mt][nt][h] = half2_of(lo32(w2), hi32(w2));
+            }
         }
-      bool over = false;
-#pragma unroll
-      for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            over = over || sc[mt][nt][e] > m[nt][e & 1] + kStep || sc[mt][nt][e] + lv[mt][e >> 1] > unit[nt][e & 1] + kStep;
-      if (__any_sync(0xffffffffu, over)) {
+        if (!__any_sync(0xffffffffu, most_p > kMostP || most_w > kMostW)) break;
         float alpha[NT][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
+          float c[2], n[2];
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             float top = kLow, topv = kLow;
@@ -351,23 +402,27 @@ __global__ void __launch_bounds__(kThreads, int4_runs_per_sm(8 * NT)) paged_int4
             for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                top = fmaxf(top, sc[mt][nt][2 * h + x]);
-                topv = fmaxf(topv, sc[mt][nt][2 * h + x] + lv[mt][h]);
+                const float s = sc[mt][nt][2 * h + x] * (x ? hi32(fac[mt][nt][h]) : lo32(fac[mt][nt][h]));
+                top = fmaxf(top, s);
+                topv = fmaxf(topv, s + __log2f(fabsf(vs[mt][h])));
               }
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) {
               top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
               topv = fmaxf(topv, __shfl_xor_sync(0xffffffffu, topv, d));
             }
-            const float n = fmaxf(m[nt][x], top);
+            const float m = x ? -hi32(neg[nt]) : -lo32(neg[nt]);
+            n[x] = fmaxf(m, top);
             // held within 2^100 of the maximum so that the lift stays finite
-            const float u = fmaxf(fmaxf(unit[nt][x], topv), n - 100.f);
-            l[nt][x] *= ex2(m[nt][x] - n);
+            const float u = fmaxf(fmaxf(unit[nt][x], topv), n[x] - 100.f);
+            c[x] = ex2(m - n[x]);
             alpha[nt][x] = ex2(unit[nt][x] - u);
-            lift[nt][x] = ex2(n - u + kLift);
-            m[nt][x] = n;
             unit[nt][x] = u;
           }
+          neg[nt] = two(-n[0], -n[1]);
+          sum[nt] = f32x2_mul(sum[nt], two(c[0], c[1]));
+          lift[nt] = two(ex2(n[0] - unit[nt][0] + kLift), ex2(n[1] - unit[nt][1] + kLift));
+        }
 #pragma unroll
         for (int i = 0; i < kNO; ++i)
 #pragma unroll
@@ -375,46 +430,40 @@ __global__ void __launch_bounds__(kThreads, int4_runs_per_sm(8 * NT)) paged_int4
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[i][nt][e] *= alpha[nt][e & 1];
       }
-      // ---- probabilities, and the second product, 16 keys at a time ----
-      const uint32_t vsel = static_cast<uint32_t>(g8 >> 1) * 0x101u + 0x400u;  // the lane's elements are of group g8 / 2
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) sum[nt] = now[nt];
+      // ---- the second product, 16 keys at a time ----
 #pragma unroll
       for (int mt = 0; mt < kMT; ++mt) {
         uint32_t pb[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float p[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            p[e] = ex2(sc[mt][nt][e] - m[nt][e & 1]);
-            l[nt][e & 1] += p[e];
-            p[e] *= vs[mt][e >> 1] * lift[nt][e & 1];
-          }
-          pb[nt][0] = transposed(half2_of(p[0], p[1]));
-          pb[nt][1] = transposed(half2_of(p[2], p[3]));
+          pb[nt][0] = transposed(pw[mt][nt][0]);
+          pb[nt][1] = transposed(pw[mt][nt][1]);
         }
-        // keys 2 t4, 2 t4 + 1 (h = 0) and 8 further (h = 1), in the halves of a register
+        // rows 2 t4 and 2 t4 + 1 (h = 0) and 8 further (h = 1), in the halves of a register
         uint32_t vl[2][kW], vh[2][kW];  // even and odd elements of the lane's words
         int4row::Mul vm[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int key = k0 + 16 * mt + 8 * h + 2 * t4;
+          const uint8_t* at = st + C::kTileBytes + g8 * (D / 16) + (16 * mt + 8 * h) * C::kRowBytes;
           uint32_t w0[kW], w1[kW];
-          const uint8_t *at0 = stage + C::kTileBytes + v_at<D>(key, g8 * (D / 16)), *at1 = stage + C::kTileBytes + v_at<D>(key + 1, g8 * (D / 16));
           if constexpr (D == 128) {
-            const uint2 y0 = *reinterpret_cast<const uint2*>(at0), y1 = *reinterpret_cast<const uint2*>(at1);
+            const uint2 y0 = *reinterpret_cast<const uint2*>(at + v_key0 * C::kRowBytes), y1 = *reinterpret_cast<const uint2*>(at + v_key1 * C::kRowBytes);
             w0[0] = y0.x; w0[1] = y0.y;
             w1[0] = y1.x; w1[1] = y1.y;
           } else {
-            w0[0] = *reinterpret_cast<const uint32_t*>(at0);
-            w1[0] = *reinterpret_cast<const uint32_t*>(at1);
+            w0[0] = *reinterpret_cast<const uint32_t*>(at + v_key0 * C::kRowBytes);
+            w1[0] = *reinterpret_cast<const uint32_t*>(at + v_key1 * C::kRowBytes);
           }
 #pragma unroll
           for (int i = 0; i < kW; ++i) {
             vl[h][i] = prmt(w0[i], w1[i], 0x5410u);
             vh[h][i] = prmt(w0[i], w1[i], 0x7632u);
           }
-          const uint32_t m0 = *reinterpret_cast<const uint32_t*>(vrec + key * int4row::kRecord + 4);
-          const uint32_t m1 = *reinterpret_cast<const uint32_t*>(vrec + (key + 1) * int4row::kRecord + 4);
+          const uint8_t* rec = vrec + (16 * mt + 8 * h) * int4row::kRecord + 4;
+          const uint32_t m0 = *reinterpret_cast<const uint32_t*>(rec + v_key0 * int4row::kRecord);
+          const uint32_t m1 = *reinterpret_cast<const uint32_t*>(rec + v_key1 * int4row::kRecord);
           vm[h] = int4row::multipliers(prmt(m0, m1, vsel));
         }
         auto tile = [&](int i, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
@@ -432,32 +481,34 @@ __global__ void __launch_bounds__(kThreads, int4_runs_per_sm(8 * NT)) paged_int4
       }
     }
 
-    if (more) keep(ahead, slot);  // this tile's entries are read
-
     if (cc.kt + 1 == cc.sh.kt || t + 1 == tiles) {
       // ---- the item's end, or the run's: join the warps' key slices, 8 rows at a time ----
       const bool whole = kt_begin == 0 && cc.kt + 1 == cc.sh.kt;
       const long long pslot = 2ll * blockIdx.x + (kt_begin > 0 ? 0 : 1);
-      float* mo = reinterpret_cast<float*>(stage);  // [warp][8][kPad]
+      // the warps' outputs meet in the slots just read: [8][kPad] of each warp
+      auto meet = [&](int w) { return reinterpret_cast<float*>(smem + (w * kStages + slot) * C::kSlotBytes); };
+      __syncwarp();
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float fac[2];
+        if (nt > 0) __syncthreads();  // the rows before are read
+        float back[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          float sum = l[nt][x];
+          float all = x ? hi32(sum[nt]) : lo32(sum[nt]);
 #pragma unroll
-          for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+          for (int d = 4; d < 32; d <<= 1) all += __shfl_xor_sync(0xffffffffu, all, d);
+          const float m = x ? -hi32(neg[nt]) : -lo32(neg[nt]);
           // sums relative to the maximum again
-          fac[x] = ex2(unit[nt][x] - m[nt][x] - kLift) * int4row::kUnit;
-          if (g8 == 0) ml[warp][8 * nt + 2 * t4 + x] = make_float2(m[nt][x] == kLow ? -INFINITY : m[nt][x], sum);
+          back[x] = ex2(unit[nt][x] - m - kLift) * int4row::kUnit;
+          if (g8 == 0) ml[warp][8 * nt + 2 * t4 + x] = make_float2(m == kLow ? -INFINITY : m, all);
         }
-        __syncthreads();  // the stage is read (copies into it begin behind the next barrier of the loop), or the rows before are
+        float* const mo = meet(warp);
 #pragma unroll
         for (int i = 0; i < kNO; ++i)
 #pragma unroll
           for (int x = 0; x < 2; ++x)
-            *reinterpret_cast<float2*>(mo + (warp * 8 + 2 * t4 + x) * C::kPad + (D / 8) * g8 + 2 * i) =
-                make_float2(o[i][nt][x] * fac[x], o[i][nt][2 + x] * fac[x]);
+            *reinterpret_cast<float2*>(mo + (2 * t4 + x) * C::kPad + (D / 8) * g8 + 2 * i) =
+                make_float2(o[i][nt][x] * back[x], o[i][nt][2 + x] * back[x]);
         __syncthreads();
         const int here = min(8, rows - 8 * nt);
         for (int e = tid * 4; e < here * D; e += kThreads * 4) {
@@ -472,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, int4_runs_per_sm(8 * NT)) paged_int4
           for (int w = 0; w < kWarps; ++w) {
             const float2 q = ml[w][r];
             const float f = ex2(q.x - base);
-            const float4 v = *reinterpret_cast<const float4*>(mo + (w * 8 + rr) * C::kPad + c);
+            const float4 v = *reinterpret_cast<const float4*>(meet(w) + rr * C::kPad + c);
             L += f * q.y;
             acc.x += f * v.x;
             acc.y += f * v.y;
@@ -494,15 +545,32 @@ __global__ void __launch_bounds__(kThreads, int4_runs_per_sm(8 * NT)) paged_int4
       if (!whole && a.fused) {
         const Span sp = span_of(item_first, cc.sh.ku, run.per);
         if (all_arrived(a, sp, run.per, pslot)) {
-          join_item<D, kRT, kThreads>(a, cc.s, sp, run.per, cc.g, cc.rt, rows, reinterpret_cast<float*>(stage), tid);
+          join_item<D, kRT, kThreads>(a, cc.s, sp, run.per, cc.g, cc.rt, rows, meet(0), tid);
           clear_arrivals(a, sp, run.per);
         }
       }
       item_first += cc.sh.ku;
+      // what was written here comes before the slot's next copies
+      fence_proxy_async_smem();
+      __syncthreads();
+    }
+    __syncwarp();  // the slot is read
+    if (more && !gave_up) {
+      if (by_rows) fence_proxy_async_smem();
+      __syncwarp();
+      fill(slot);
+    } else {
+      cp_commit();
     }
     if (++cc.kt == cc.sh.kt) cc.next_item(a, run.pad);
     if (++slot == kStages) slot = 0;
   }
+  for (int i = 0; i < kStages; ++i)  // (a wait that ran out) copies under way land before the CTA exits
+    if (bulks >> i & 1) {
+      const uint64_t t0 = globaltimer();
+      while (!mbar_try_wait(&full[warp][i], phases >> i & 1) && globaltimer() - t0 <= kWaitLimitNs) {
+      }
+    }
 }
 
 template <int D, int NT>
@@ -516,7 +584,10 @@ int launch(const Args& a, int runs, cudaStream_t st) {
       return MNW_E_CUDA;
     attrs_done(attr, bit);
   }
-  return launch_pdl(kern, dim3(runs), dim3(kThreads), C::kSmem, st, a) == cudaSuccess ? MNW_OK : MNW_E_CUDA;
+  // bulk copies: pages that divide a warp's keys, in pieces of 4 keys at least, or hold them; records on 16 bytes
+  const int ps = a.page_size;
+  const int whole = (ps & (ps - 1)) == 0 && ps >= 4 && aligned(a.ks, 16) && aligned(a.vs, 16) ? 1 : 0;
+  return launch_pdl(kern, dim3(runs), dim3(kThreads), C::kSmem, st, a, whole) == cudaSuccess ? MNW_OK : MNW_E_CUDA;
 }
 template <int D>
 int launch_rt(const Args& a, int rt, int runs, cudaStream_t st) {

@@ -34,7 +34,7 @@ using paged::Seq;
 
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kBlockRows = 128, kBlockKeys = 128;  // the block kernel's tiles (mnw_attn_paged_block.cu)
-constexpr int kInt4Keys = 128;                     // the INT4 kernel's (mnw_attn_paged_int4.cu), and its CTAs on an SM
+constexpr int kInt4Keys = 256;                     // the INT4 kernel's (mnw_attn_paged_int4.cu), and its CTAs on an SM
 constexpr int int4_runs_per_sm(int rt) { return rt <= 16 ? 3 : 2; }
 
 struct Args {
