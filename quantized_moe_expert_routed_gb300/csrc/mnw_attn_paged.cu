@@ -542,9 +542,9 @@ __global__ void __launch_bounds__(WR* WK * 32) paged_attn_kernel(const Args a) {
 // convert the codes: 32 rows 335 and 537, 34 and 40; 64 rows 54 and 40.
 inline int row_tile(long long rows, bool int8) { return rows <= 16 ? 16 : (int8 && rows <= 32 ? 32 : kBlockRows); }
 // INT4: the tiles of the transposed kernel
-inline int row_tile_int4(long long rows) { return rows <= 8 ? 8 : (rows <= 16 ? 16 : 32); }
+inline int row_tile_int4(long long rows) { return rows <= 8 ? 8 : (rows <= 16 ? 16 : (rows <= 32 ? 32 : kBlockRows)); }
 // CTAs resident on an SM
-inline int runs_per_sm(int rt, bool int4) { return int4 ? int4_runs_per_sm(rt) : (rt == kBlockRows ? 1 : 2); }
+inline int runs_per_sm(int rt, bool int4) { return rt == kBlockRows ? 1 : (int4 ? int4_runs_per_sm(rt) : 2); }
 // The last arrival joins items of at most this many rows (on average over the
 // sequences), which its threads take in one pass: no slower on the GPU (one token over 777 positions 7.7 us
 // either way, 2 over 200,000 246.5 and 247.3) and a launch (2 us of the
@@ -634,7 +634,7 @@ int launch_rows(Args& a, uint8_t* ws, int rt, cudaStream_t st) {
   int runs;
   bool shared;
   if (!plan(a, kBlockRows, kBlockKeys, D, false, ws, &runs, &shared)) return MNW_E_UNSUPPORTED;
-  const int rc = launch_block(a, D, INT8, runs, st);
+  const int rc = launch_block(a, D, INT8 ? MNW_KV_INT8 : MNW_KV_BF16, runs, st);
   return rc != MNW_OK || !shared ? rc : launch_join<D, kBlockRows, kBlockKeys>(a, st);
 }
 
@@ -642,9 +642,10 @@ template <int D>
 int launch_rows_int4(Args& a, uint8_t* ws, int rt, cudaStream_t st) {
   int runs;
   bool shared;
-  if (!plan(a, rt, kInt4Keys, D, true, ws, &runs, &shared)) return MNW_E_UNSUPPORTED;
-  const int rc = launch_int4(a, D, rt, runs, st);
+  if (!plan(a, rt, rt == kBlockRows ? kBlockKeys : kInt4Keys, D, true, ws, &runs, &shared)) return MNW_E_UNSUPPORTED;
+  const int rc = rt == kBlockRows ? launch_block(a, D, MNW_KV_INT4, runs, st) : launch_int4(a, D, rt, runs, st);
   if (rc != MNW_OK || a.fused || !shared) return rc;
+  if (rt == kBlockRows) return launch_join<D, kBlockRows, kBlockKeys>(a, st);
   return rt == 8 ? launch_join<D, 8, kInt4Keys>(a, st)
                  : (rt == 16 ? launch_join<D, 16, kInt4Keys>(a, st) : launch_join<D, 32, kInt4Keys>(a, st));
 }

@@ -56,6 +56,7 @@
 #include <cstring>
 
 #include "mnw_attn_split.cuh"
+#include "mnw_int4_row.cuh"
 
 namespace mnw {
 namespace pattn {
@@ -69,15 +70,32 @@ constexpr int kMaxSegs = 8;      // segment descriptions held; at most four segm
 constexpr int kMaxSlots = 4;
 constexpr int kMaxKScales = 9, kMaxVScales = 6;
 constexpr int kMaxBufs = 3;
+constexpr int kMaxRaws = 6;
 constexpr float kRescaleLog2 = 8.f;
+// INT4: log2 of the largest product of a probability and a value's scale where a row's unit is set, as FP16; the FP16 bits
+// above which it is set anew (2^14); the log2 that a value's scale counts for at least.
+constexpr float kLift4 = 7.f, kLeastLog2 = -95.f;
+constexpr uint32_t kMostBits = 0x7400u;
 
-template <int D, bool INT8>
+// INT8 below stands for both quantised formats: FP16 operands from converted codes, scales a key.
+template <int D, int FMT>
 struct BCfg {
+  static constexpr bool INT8 = FMT != MNW_KV_BF16, INT4 = FMT == MNW_KV_INT4;
   static constexpr int kHalves = D / 64;                   // 64 elements = 128 bytes per operand row piece
   static constexpr uint32_t kPiece = kTK * 128;            // 128 rows of 128 bytes
   static constexpr uint32_t kTile = kHalves * kPiece;      // operand tile
   static constexpr int kSlotsK = D == 64 ? 4 : (INT8 ? 2 : 3), kSlotsV = D == 64 ? 4 : 2;
-  static constexpr uint32_t kRaw = INT8 ? kTK * D : 0;     // raw codes of a tile
+  static constexpr uint32_t kCodes = INT4 ? kTK * D / 2 : (INT8 ? kTK * D : 0);  // raw codes of a tile,
+  static constexpr uint32_t kRaw = kCodes + (INT4 ? kTK * int4row::kRecord : 0);   // INT4: and its records
+  // raw buffers, keys' and values' each.  INT4: as many as fit, for what has to be under way to cover the memory's latency
+  // (with one landing while one is converted: 44.8 us, and 96.7 with 64-wide heads)
+  static constexpr int kRaws = !INT4 ? 1 : (D == 64 ? 6 : 3);
+  // INT4: the loader warps take tiles in turn, so that what a tile costs a warp besides the conversion comes once in two
+  // (64-wide heads 97 -> 73 us with little to do in the softmax); two operand slots are too few for that, as a tile
+  // would then hold its slot twice as long (128: 66 -> 86 us), and each warp takes a half of each.
+  static constexpr bool kTurns = INT4 && kSlotsV > 2;
+  static constexpr int kGivers = kTurns ? 1 : 2;  // warps that give a tile on
+  static_assert(kRaws <= kMaxRaws);
   // Tensor memory: score buffers (tile t in buffer t % kBufs, its P over the first half), then O.  Three: one in the
   // softmax, one whose P is being consumed, one being computed.
   static constexpr int kBufs = 3;
@@ -91,7 +109,7 @@ struct BCfg {
   static constexpr uint32_t kOffK = kTile;                 // Q first
   static constexpr uint32_t kOffV = kOffK + kSlotsK * kTile;
   static constexpr uint32_t kOffRaw = kOffV + kSlotsV * kTile;            // keys' codes, values' codes
-  static constexpr uint32_t kOffKS = kOffRaw + 2 * kRaw;                  // [kScalesK][kTK] scales of keys
+  static constexpr uint32_t kOffKS = kOffRaw + 2 * kRaws * kRaw;          // [kScalesK][kTK] scales of keys
   static constexpr uint32_t kOffVS = kOffKS + (INT8 ? kScalesK * kTK * 4 : 0);  // [kScalesV][2][kTK] of values, and their log2
   static constexpr uint32_t kOffBars = kOffVS + (INT8 ? kScalesV * 2 * kTK * 4 : 0);
 };
@@ -105,7 +123,7 @@ struct Seg {
 
 struct Bars {
   uint64_t full[2][kMaxSlots], empty[2][kMaxSlots];  // operand rings: keys, values
-  uint64_t raw_full[2], raw_empty[2];
+  uint64_t raw_full[2][kMaxRaws], raw_empty[2][kMaxRaws];  // keys', values'; of each raw buffer
   uint64_t q0_full, q_full, q_empty;                 // the first query tile is there, a later one; consumed
   uint64_t s_full[kMaxBufs], p_full[kMaxBufs], s_free[kMaxBufs];  // per score buffer: scores complete, P written, P consumed
   uint64_t o_full, epi;                 // a segment's output complete; read
@@ -222,11 +240,12 @@ __device__ __forceinline__ uint32_t half2_bits(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-template <int D, bool INT8>
+template <int D, int FMT>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const Args a,
                        const int whole_pages) {
-  using C = BCfg<D, INT8>;
+  using C = BCfg<D, FMT>;
+  constexpr bool INT8 = C::INT8, INT4 = C::INT4;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);  // (an offset: the pointer stays a shared-memory one)
   Bars* bars = reinterpret_cast<Bars*>(smem + C::kOffBars);
@@ -239,11 +258,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int x = 0; x < 2; ++x) {
       for (int i = 0; i < kMaxSlots; ++i) {
-        mbar_init(&bars->full[x][i], 2);
+        mbar_init(&bars->full[x][i], C::kGivers);
         mbar_init(&bars->empty[x][i], 1);
       }
-      mbar_init(&bars->raw_full[x], 1);
-      mbar_init(&bars->raw_empty[x], 2);
+      for (int i = 0; i < kMaxRaws; ++i) {
+        mbar_init(&bars->raw_full[x][i], 1);
+        mbar_init(&bars->raw_empty[x][i], C::kGivers);
+      }
       mbar_init(&bars->drain[x], 1);
     }
     mbar_init(&bars->q0_full, 8);
@@ -251,8 +272,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&bars->q_empty, 1);
     mbar_init(&bars->o_full, 1);
     mbar_init(&bars->epi, 8);
-    for (int i = 0; i < kMaxKScales; ++i) mbar_init(&bars->ks_full[i], 2);
-    for (int i = 0; i < kMaxVScales; ++i) mbar_init(&bars->vs_full[i], 2);
+    for (int i = 0; i < kMaxKScales; ++i) mbar_init(&bars->ks_full[i], C::kGivers);
+    for (int i = 0; i < kMaxVScales; ++i) mbar_init(&bars->vs_full[i], C::kGivers);
     for (int i = 0; i < kMaxSegs; ++i) mbar_init(&bars->seg_full[i], 1);
     for (int i = 0; i < kMaxBufs; ++i) {
       mbar_init(&bars->s_full[i], 1);
@@ -339,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* const full = bars->full[values ? 1 : 0];
     uint64_t* const empty = bars->empty[values ? 1 : 0];
     const uint8_t* const base = values ? a.vc : a.kc;
-    constexpr int kCh = (INT8 ? D : 2 * D) / 16;  // chunks of a cached row
+    constexpr int kCh = (INT4 ? D / 2 : INT8 ? D : 2 * D) / 16;  // chunks of a cached row
     constexpr int kRows = 32 / kCh;               // rows per pass of the warp
     // whole pages: page `lane` of a tile, `span` keys each
     const int span = min(a.page_size, kTK), pieces = kTK / span;
@@ -355,11 +376,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       whole = whole_pages && (kc.kt + 1) * kTK <= kc.s.len;
       page = whole && lane < pieces ? table_at(kc.b, kc.kt * kTK + lane * span) : 0;
     };
-    // row by row: this warp's 64 keys of the tile, to `to` (operand tile, or raw codes) and its scales to `sc`
-    auto copy_rows = [&](uint32_t to, uint32_t sc) {
+    // row by row: keys 32 first .. 32 last of the tile, to `to` (operand tile, or raw codes) and their scales to `sc`
+    auto copy_rows = [&](int first, int last, uint32_t to, uint32_t sc) {
 #pragma unroll 1
-      for (int part = 0; part < 2; ++part) {
-        const int r0 = lw * 64 + part * 32;
+      for (int part = first; part < last; ++part) {
+        const int r0 = part * 32;
         const int p = kc.kt * kTK + r0 + lane;
         int pg = -1, at = 0;
         if (p < kc.s.len) {
@@ -377,11 +398,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int r = i * kRows + lane / kCh;
           const long long off = __shfl_sync(0xffffffffu, mine, r);
           const int row = r0 + r;
-          const uint32_t dst = INT8 ? to + row * D + c * 16
+          const uint32_t dst = INT8 ? to + row * (kCh * 16) + c * 16
                                     : to + (c >> 3) * C::kPiece + row * 128 + (((c & 7) ^ (row & 7)) << 4);
           cp_async16(dst, base + (off >= 0 ? off + c * 16 : 0), off >= 0 ? 16u : 0u);
         }
-        if constexpr (INT8)
+        if constexpr (INT4)
+          cp_async8(sc + (r0 + lane) * int4row::kRecord, reinterpret_cast<const char*>(values ? a.vs : a.ks) +
+                    (pg >= 0 ? (static_cast<long long>(pg) * a.Hkv * a.page_size + at) * int4row::kRecord : 0), pg >= 0 ? 8u : 0u);
+        else if constexpr (INT8)
           cp_async4(sc + (r0 + lane) * 4, (values ? a.vs : a.ks) + (pg >= 0 ? static_cast<long long>(pg) * a.Hkv * a.page_size + at : 0),
               pg >= 0 ? 4u : 0u);
       }
@@ -405,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t at = ring_at + ring.slot * C::kTile;
         const bool rows = !whole || __any_sync(0xffffffffu, static_cast<unsigned>(page) >= static_cast<unsigned>(a.n_pages));
         if (rows) {
-          copy_rows(sbase + at, 0);
+          copy_rows(2 * lw, 2 * lw + 2, sbase + at, 0);
         } else {
           if (lw == 0) {
             if (lane == 0) mbar_arrive_expect_tx(bar, C::kTile);
@@ -440,8 +464,146 @@ __global__ void __launch_bounds__(kThreads, 1)
         // let every bulk copy already issued land before the CTA exits
         for (int i = 0; i < ring_slots; ++i) drain_wait(&full[i], i < static_cast<int>(ring.slot) ? ring.phase : ring.phase ^ 1);
       }
+    } else if constexpr (INT4) {
+      // A ring of raw buffers, codes and then records of a tile, which the tiles take in turn.  A warp has kAhead of its
+      // tiles copied ahead of the one that it converts.
+      uint64_t *const raw_full = bars->raw_full[values ? 1 : 0], *const raw_empty = bars->raw_empty[values ? 1 : 0];
+      const uint32_t raw_at = C::kOffRaw + (values ? C::kRaws * C::kRaw : 0);
+      constexpr int kStep = C::kTurns ? 2 : 1, kAhead = (C::kRaws - 1) / kStep;
+      constexpr int kMine = C::kTurns ? kTK : kTK / 2;  // keys of a tile that are this warp's, from key0 on
+      const int first = C::kTurns ? lw : 0, key0 = C::kTurns ? 0 : lw * kMine;
+      const bool copier = C::kTurns || lw == 0;  // of whole tiles
+      uint32_t by_rows = 0, under_way = 0, parity = 0;  // of buffer i, bit i: filled row by row; bulk copies under way, on which parity
+      RingPos put, get;  // the tiles' uses of the buffers: each completes a phase of raw_full and of raw_empty
+      int next = 0;      // tile at kc, issued next
+      auto skip = [&]() {
+        step();
+        put.advance(C::kRaws);
+        ++next;
+      };
+      auto issue = [&]() -> bool {  // once the buffer's last tile is converted
+        const uint32_t b = put.slot, to = raw_at + b * C::kRaw;
+        if (!warp_wait(&raw_empty[b], put.phase ^ 1, abort, a.err)) return false;
+        if (!whole || __any_sync(0xffffffffu, static_cast<unsigned>(page) >= static_cast<unsigned>(a.n_pages))) {
+          by_rows |= 1u << b;
+          copy_rows(key0 / 32, (key0 + kMine) / 32, sbase + to, sbase + to + C::kCodes);  // (with the group's commit)
+        } else {
+          by_rows &= ~(1u << b);
+          if (copier) {
+            under_way |= 1u << b;
+            parity = (parity & ~(1u << b)) | put.phase << b;
+            if (lane == 0) mbar_arrive_expect_tx(&raw_full[b], C::kRaw);
+            __syncwarp();
+            if (lane < pieces) {
+              const int at = kc.g * a.page_size + (a.page_size > kTK ? (kc.kt * kTK) & (a.page_size - 1) : 0);
+              bulk_load(smem + to + lane * span * (D / 2), base + page * a.page_bytes + static_cast<long long>(at) * (D / 2),
+                        span * (D / 2), &raw_full[b]);
+              bulk_load(smem + to + C::kCodes + lane * span * int4row::kRecord,
+                        reinterpret_cast<const uint8_t*>(values ? a.vs : a.ks) +
+                            (static_cast<long long>(page) * a.Hkv * a.page_size + at) * int4row::kRecord,
+                        span * int4row::kRecord, &raw_full[b]);
+            }
+            __syncwarp();
+          }
+          cp_commit();
+        }
+        skip();
+        if (kStep == 2 && next < tiles) skip();
+        if (next < tiles) peek();
+        return true;
+      };
+      // A lane converts the codes of one group of a row, D / 32 chunks of the operand row.  With 128 bytes a piece,
+      // lanes of the row's upper half take their chunks in another order, or two would meet in a bank.
+      constexpr int kGC = D / 32;
+      const int row0 = key0 + (lane >> 2), g = lane & 3;
+      const bool turn = D == 128 && g >= 2;
+      const uint32_t msel = g * 0x101u;
+      const int sc_slots = values ? C::kScalesV : C::kScalesK;
+      int sc_now = first;
+      if (first > 0) {
+        ring.advance(ring_slots);
+        get.advance(C::kRaws);
+        if (ok) skip();
+        ok = ok && next < tiles;
+        if (ok) peek();
+      }
+      for (int t = first - kStep * kAhead; ok && t < tiles; t += kStep) {
+        if (next < tiles && !issue()) { ok = false; break; }
+        if (t < 0) continue;
+        const uint32_t b = get.slot;
+        if (by_rows >> b & 1) {
+          if (t + kStep * kAhead < tiles)
+            cp_wait<kAhead>();
+          else
+            cp_wait<0>();
+          fence_proxy_async_smem();  // rows came by this proxy, the next codes may come by the other
+          __syncwarp();
+          if (copier && lane == 0) mbar_arrive(&raw_full[b]);
+        } else {
+          if (!warp_wait(&raw_full[b], get.phase, abort, a.err)) { ok = false; break; }
+          under_way &= ~(1u << b);
+        }
+        const uint8_t* const raw = smem + raw_at + b * C::kRaw;
+        const uint8_t* const rec = raw + C::kCodes;
+        {  // the scales, for the softmax; the values' at once, as it runs while they still wait for their slot
+          float* sc = reinterpret_cast<float*>(smem + (values ? C::kOffVS + sc_now * (2 * kTK * 4) : C::kOffKS + sc_now * (kTK * 4)));
+#pragma unroll
+          for (int i = 0; i < kMine; i += 32) {
+            const int key = key0 + i + lane;
+            const float s = *reinterpret_cast<const float*>(rec + key * int4row::kRecord);
+            // a key of zeros keeps a scale: a masked score of -inf has to stay one
+            sc[key] = values ? s : (s == 0.f ? 0x1p-126f : s * kHalfUnit);
+            if (values) sc[kTK + key] = fmaxf(__log2f(s), kLeastLog2);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(values ? &bars->vs_full[sc_now] : &bars->ks_full[sc_now]);
+          sc_now += kStep;
+          if (sc_now >= sc_slots) sc_now -= sc_slots;
+        }
+        if (!warp_wait(&empty[ring.slot], ring.phase ^ 1, abort, a.err)) { ok = false; break; }
+        uint8_t* const op = smem + ring_at + ring.slot * C::kTile;
+#pragma unroll 2
+        for (int i = 0; i < kMine / 8; ++i) {
+          const int row = row0 + 8 * i;
+          uint32_t w[kGC];
+          if constexpr (D == 128) {
+            const uint4 v = *reinterpret_cast<const uint4*>(raw + row * 64 + g * 16);
+            w[0] = turn ? v.z : v.x;
+            w[1] = turn ? v.w : v.y;
+            w[2] = turn ? v.x : v.z;
+            w[3] = turn ? v.y : v.w;
+          } else {
+            const uint2 v = *reinterpret_cast<const uint2*>(raw + row * 32 + g * 8);
+            w[0] = v.x;
+            w[1] = v.y;
+          }
+          const int4row::Mul m = int4row::multipliers(prmt(*reinterpret_cast<const uint32_t*>(rec + row * int4row::kRecord + 4), 0u, msel));
+#pragma unroll
+          for (int j = 0; j < kGC; ++j) {
+            const int c = g * kGC + (turn ? j ^ 2 : j);
+            using int4row::pair;
+            *reinterpret_cast<uint4*>(op + (c >> 3) * C::kPiece + row * 128 + (((c & 7) ^ (row & 7)) << 4)) =
+                make_uint4(pair<0>(w[j], m), pair<1>(w[j], m), pair<2>(w[j], m), pair<3>(w[j], m));
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&full[ring.slot]);
+          mbar_arrive(&raw_empty[b]);
+        }
+#pragma unroll
+        for (int i = 0; i < kStep; ++i) {
+          get.advance(C::kRaws);
+          ring.advance(ring_slots);
+        }
+      }
+      cp_wait<0>();
+      // (an abort) copies under way land before the CTA exits
+      for (int i = 0; i < C::kRaws; ++i)
+        if (under_way >> i & 1) drain_wait(&raw_full[i], parity >> i & 1);
     } else {
-      uint64_t *const raw_full = &bars->raw_full[values ? 1 : 0], *const raw_empty = &bars->raw_empty[values ? 1 : 0];
+      uint64_t *const raw_full = bars->raw_full[values ? 1 : 0], *const raw_empty = bars->raw_empty[values ? 1 : 0];
       const uint32_t raw_at = C::kOffRaw + (values ? C::kRaw : 0);
       uint32_t raw_phase = 0;  // parity of the next bulk landing
       int sc_issue = 0, sc_now = 0;  // scale slots of the tile issued next, of the tile that lands next
@@ -453,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto issue = [&](int uses) -> bool {
         landing_rows = !whole || __any_sync(0xffffffffu, static_cast<unsigned>(page) >= static_cast<unsigned>(a.n_pages));
         if (landing_rows) {
-          copy_rows(sbase + raw_at, sbase + scales_at(sc_issue));
+          copy_rows(2 * lw, 2 * lw + 2, sbase + raw_at, sbase + scales_at(sc_issue));
         } else if (lw == 0) {
           if (!warp_wait(raw_empty, (uses & 1) ^ 1, abort, a.err)) return false;
           if (lane == 0) mbar_arrive_expect_tx(raw_full, C::kRaw + kTK * 4);
@@ -697,7 +859,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           vs = reinterpret_cast<const float*>(smem + C::kOffVS) + vs_slot * 2 * kTK + 2 * t4;
         }
         tc_fence_after();
-        float fac[2] = {a.scale_log2, a.scale_log2};
+        constexpr float kTake = INT4 ? kHalfUnit : 1.f;
+        float fac[2] = {a.scale_log2 * kTake, a.scale_log2 * kTake};
         if constexpr (INT8) {
           // the query rows' factors were written before q_full, which the scores waited for
           const float* qf = &bars->qfac[seg & 3][r16];
@@ -708,7 +871,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                   f32x2_pack(__float_as_uint(fac[1]), __float_as_uint(fac[1]))};
         // scales are loaded in one go ahead of their use: a load before each use waited for it 48 times a half
         uint64_t f[16];
-        if constexpr (INT8) {
+        if constexpr (INT8 && !INT4) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) f[i] = *reinterpret_cast<const uint64_t*>(ks + 8 * i);
         }
@@ -717,7 +880,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld_frag(s_at, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
         tmem_ld_frag(s_at + 64, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
         tmem_wait_ld();
-        if constexpr (INT8) {
+        if constexpr (INT8 && !INT4) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
 #pragma unroll
@@ -733,66 +896,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int e = 0; e < 64; ++e)
             if (8 * (e >> 2) + 2 * t4 + (e & 1) >= st[(e >> 1) & 1].left) sv[e] = 0xff800000u;  // -inf
         }
-        // the rows' maxima; INT8: also log2 of their largest e^score times value scale
-        float top[2] = {-INFINITY, -INFINITY}, topv[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          float other = -INFINITY;  // two chains
-#pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            top[x] = fmaxf(fmaxf(top[x], __uint_as_float(sv[4 * i + 2 * x])), __uint_as_float(sv[4 * i + 2 * x + 1]));
-            other = fmaxf(fmaxf(other, __uint_as_float(sv[4 * i + 4 + 2 * x])), __uint_as_float(sv[4 * i + 4 + 2 * x + 1]));
-          }
-          top[x] = fmaxf(top[x], other);
-        }
-        if constexpr (INT8) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) f[i] = *reinterpret_cast<const uint64_t*>(vs + kTK + 8 * i);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const uint64_t y = f32x2_fma(f32x2_pack(sv[4 * i + 2 * x], sv[4 * i + 2 * x + 1]), fac2[x], f[i]);
-              topv[x] = fmaxf(fmaxf(topv[x], lo32(y)), hi32(y));
-            }
-          }
-        }
-        float alpha[2] = {1.f, 1.f}, lift[2] = {1.f, 1.f};
-        uint64_t neg2[2], l2[2] = {0ull, 0ull};
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-#pragma unroll
-          for (int d = 1; d < 4; d <<= 1) {
-            top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], d));
-            if constexpr (INT8) topv[x] = fmaxf(topv[x], __shfl_xor_sync(0xffffffffu, topv[x], d));
-          }
-          top[x] *= fac[x];
-          RowState& rs = st[x];
-          if constexpr (!INT8) {
-            if (top[x] > rs.m + kRescaleLog2 || rs.m == -INFINITY) {
-              const float n = fmaxf(rs.m, top[x]);
-              alpha[x] = n == -INFINITY ? 1.f : ex2(rs.m - n);  // 0 where nothing was seen before
-              rs.l *= alpha[x];
-              rs.m = n;
-            }
-          } else {
-            const float n = fmaxf(rs.m, top[x]);
-            rs.l *= n == -INFINITY ? 1.f : ex2(rs.m - n);
-            rs.m = n;
-            // held within 2^100 of e^m so that the lift stays finite
-            const float at = fmaxf(topv[x], n - 100.f);
-            if (n != -INFINITY && at > rs.unit + 1.f) {
-              alpha[x] = ex2(rs.unit - at);  // 0 from -inf
-              rs.unit = at;
-            }
-            lift[x] = rs.unit == -INFINITY ? 0.f : ex2(n - rs.unit + 14.f);
-          }
-          const float base = rs.m == -INFINITY ? 0.f : rs.m;
-          neg2[x] = f32x2_pack(__float_as_uint(-base), __float_as_uint(-base));
-        }
-        if (t > begin && __any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
-          // the product before has to be complete
-          if (!warp_wait(&bars->s_free[(t - 1) % C::kBufs], ((t - 1) / C::kBufs) & 1, abort, a.err)) { ok = false; break; }
+        // O and the rows' sums to another unit; the product before has to be complete
+        auto rescale = [&](const float (&alpha)[2]) -> bool {
+          if (t == begin || !__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) return true;
+          if (!warp_wait(&bars->s_free[(t - 1) % C::kBufs], ((t - 1) / C::kBufs) & 1, abort, a.err)) return false;
           tc_fence_after();
 #pragma unroll 1
           for (int i = 0; i < D; i += 64) {
@@ -803,29 +910,151 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha[(e >> 1) & 1]);
             tmem_st_frag(at16 + C::kColO + i, o);
           }
-        }
-        if constexpr (INT8) {
+          return true;
+        };
+        if constexpr (INT4) {
+          // p = 2^(s fac - unit + kLift4), so that p times the value's scale is the FP16 product as it is.  The unit of
+          // before serves as long as no product passes 2^14, which is looked for in the products; then, and for a row's
+          // first keys, the unit is set and the products are computed (again).
+          bool set = t == begin || __any_sync(0xffffffffu, st[0].unit == -INFINITY || st[1].unit == -INFINITY);
+          uint32_t pw[32];
+          uint64_t l2[2];
+#pragma unroll 1
+          for (;;) {
+            if (set) {
+              float top[2] = {-INFINITY, -INFINITY}, alpha[2];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) f[i] = *reinterpret_cast<const uint64_t*>(vs + 8 * i);
-        }
-        // p = 2^(s fac - m), two keys per packed operation, its sum, and P, two keys a column, over the first half of
-        // the rows' S columns
+              for (int i = 0; i < 16; ++i) {
+                const uint64_t kf = *reinterpret_cast<const uint64_t*>(ks + 8 * i), lf = *reinterpret_cast<const uint64_t*>(vs + kTK + 8 * i);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+                for (int x = 0; x < 2; ++x) {
+                  const uint64_t y = f32x2_fma(f32x2_mul(f32x2_pack(sv[4 * i + 2 * x], sv[4 * i + 2 * x + 1]), kf), fac2[x], lf);
+                  top[x] = fmaxf(fmaxf(top[x], lo32(y)), hi32(y));
+                }
+              }
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 1));
+                top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 2));
+                const float u = fmaxf(st[x].unit, top[x]);
+                alpha[x] = u == -INFINITY ? 1.f : ex2(st[x].unit - u);  // 0 where nothing was seen before
+                st[x].unit = u;
+                st[x].l *= alpha[x];
+              }
+              if (!rescale(alpha)) { ok = false; break; }
+            }
+            uint64_t neg2[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const float base = st[x].unit == -INFINITY ? 0.f : kLift4 - st[x].unit;
+              neg2[x] = f32x2_pack(__float_as_uint(base), __float_as_uint(base));
+              l2[x] = 0ull;
+            }
+            uint32_t most = 0;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const uint64_t kf = *reinterpret_cast<const uint64_t*>(ks + 8 * i), vf = *reinterpret_cast<const uint64_t*>(vs + 8 * i);
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                const uint64_t e2 = f32x2_fma(f32x2_mul(f32x2_pack(sv[4 * i + 2 * x], sv[4 * i + 2 * x + 1]), kf), fac2[x], neg2[x]);
+                const uint64_t p2 = f32x2_pack(__float_as_uint(ex2(lo32(e2))), __float_as_uint(ex2(hi32(e2))));
+                l2[x] = f32x2_add(l2[x], p2);
+                const uint64_t w2 = f32x2_mul(p2, vf);
+                pw[2 * i + x] = half2_bits(lo32(w2), hi32(w2));
+                most = __vmaxu2(most, pw[2 * i + x]);
+              }
+            }
+            if (set) break;
+            set = __any_sync(0xffffffffu, max(most >> 16, most & 0xFFFFu) > kMostBits) != 0;
+            if (!set) break;
+          }
+          if (!ok) break;
+          tmem_st_pairs(s_at, *reinterpret_cast<uint32_t(*)[16]>(&pw[0]));
+          tmem_st_pairs(s_at + 32, *reinterpret_cast<uint32_t(*)[16]>(&pw[16]));
+#pragma unroll
+          for (int x = 0; x < 2; ++x) st[x].l += lo32(l2[x]) + hi32(l2[x]);
+        } else {
+          // the rows' maxima; INT8: also log2 of their largest e^score times value scale
+          float top[2] = {-INFINITY, -INFINITY}, topv[2] = {-INFINITY, -INFINITY};
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const uint64_t e2 = f32x2_fma(f32x2_pack(sv[4 * i + 2 * x], sv[4 * i + 2 * x + 1]), fac2[x], neg2[x]);
-            uint64_t p2 = f32x2_pack(__float_as_uint(ex2(lo32(e2))), __float_as_uint(ex2(hi32(e2))));
-            l2[x] = f32x2_add(l2[x], p2);
-            if constexpr (INT8)
-              p2 = f32x2_mul(f32x2_mul(p2, f[i]), f32x2_pack(__float_as_uint(lift[x]), __float_as_uint(lift[x])));
-            sv[2 * i + x] = INT8 ? half2_bits(lo32(p2), hi32(p2)) : pack_bf16x2(lo32(p2), hi32(p2));
-          }
-        }
-        tmem_st_pairs(s_at, *reinterpret_cast<uint32_t(*)[16]>(&sv[0]));
-        tmem_st_pairs(s_at + 32, *reinterpret_cast<uint32_t(*)[16]>(&sv[16]));
+            float other = -INFINITY;  // two chains
 #pragma unroll
-        for (int x = 0; x < 2; ++x) st[x].l += lo32(l2[x]) + hi32(l2[x]);
+            for (int i = 0; i < 16; i += 2) {
+              top[x] = fmaxf(fmaxf(top[x], __uint_as_float(sv[4 * i + 2 * x])), __uint_as_float(sv[4 * i + 2 * x + 1]));
+              other = fmaxf(fmaxf(other, __uint_as_float(sv[4 * i + 4 + 2 * x])), __uint_as_float(sv[4 * i + 4 + 2 * x + 1]));
+            }
+            top[x] = fmaxf(top[x], other);
+          }
+          if constexpr (INT8) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) f[i] = *reinterpret_cast<const uint64_t*>(vs + kTK + 8 * i);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                const uint64_t y = f32x2_fma(f32x2_pack(sv[4 * i + 2 * x], sv[4 * i + 2 * x + 1]), fac2[x], f[i]);
+                topv[x] = fmaxf(fmaxf(topv[x], lo32(y)), hi32(y));
+              }
+            }
+          }
+          float alpha[2] = {1.f, 1.f}, lift[2] = {1.f, 1.f};
+          uint64_t neg2[2], l2[2] = {0ull, 0ull};
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+#pragma unroll
+            for (int d = 1; d < 4; d <<= 1) {
+              top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], d));
+              if constexpr (INT8) topv[x] = fmaxf(topv[x], __shfl_xor_sync(0xffffffffu, topv[x], d));
+            }
+            top[x] *= fac[x];
+            RowState& rs = st[x];
+            if constexpr (!INT8) {
+              if (top[x] > rs.m + kRescaleLog2 || rs.m == -INFINITY) {
+                const float n = fmaxf(rs.m, top[x]);
+                alpha[x] = n == -INFINITY ? 1.f : ex2(rs.m - n);  // 0 where nothing was seen before
+                rs.l *= alpha[x];
+                rs.m = n;
+              }
+            } else {
+              const float n = fmaxf(rs.m, top[x]);
+              rs.l *= n == -INFINITY ? 1.f : ex2(rs.m - n);
+              rs.m = n;
+              // held within 2^100 of e^m so that the lift stays finite
+              const float at = fmaxf(topv[x], n - 100.f);
+              if (n != -INFINITY && at > rs.unit + 1.f) {
+                alpha[x] = ex2(rs.unit - at);  // 0 from -inf
+                rs.unit = at;
+              }
+              lift[x] = rs.unit == -INFINITY ? 0.f : ex2(n - rs.unit + 14.f);
+            }
+            const float base = rs.m == -INFINITY ? 0.f : rs.m;
+            neg2[x] = f32x2_pack(__float_as_uint(-base), __float_as_uint(-base));
+          }
+          if (!rescale(alpha)) { ok = false; break; }
+          if constexpr (INT8) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) f[i] = *reinterpret_cast<const uint64_t*>(vs + 8 * i);
+          }
+          // p = 2^(s fac - m), two keys per packed operation, its sum, and P, two keys a column, over the first half of
+          // the rows' S columns
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const uint64_t e2 = f32x2_fma(f32x2_pack(sv[4 * i + 2 * x], sv[4 * i + 2 * x + 1]), fac2[x], neg2[x]);
+              uint64_t p2 = f32x2_pack(__float_as_uint(ex2(lo32(e2))), __float_as_uint(ex2(hi32(e2))));
+              l2[x] = f32x2_add(l2[x], p2);
+              if constexpr (INT8)
+                p2 = f32x2_mul(f32x2_mul(p2, f[i]), f32x2_pack(__float_as_uint(lift[x]), __float_as_uint(lift[x])));
+              sv[2 * i + x] = INT8 ? half2_bits(lo32(p2), hi32(p2)) : pack_bf16x2(lo32(p2), hi32(p2));
+            }
+          }
+          tmem_st_pairs(s_at, *reinterpret_cast<uint32_t(*)[16]>(&sv[0]));
+          tmem_st_pairs(s_at + 32, *reinterpret_cast<uint32_t(*)[16]>(&sv[16]));
+#pragma unroll
+          for (int x = 0; x < 2; ++x) st[x].l += lo32(l2[x]) + hi32(l2[x]);
+        }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -856,15 +1085,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         float sum = rs.l;
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        f[x] = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
-        if (INT8 && rs.unit != -INFINITY) f[x] *= ex2(rs.unit - rs.m - 14.f);
+        f[x] = whole || INT4 ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
+        if (INT8 && !INT4 && rs.unit != -INFINITY) f[x] *= ex2(rs.unit - rs.m - 14.f);
+        // INT4: parts are normalised, as the sums' unit says nothing of the scores
+        const float all = INT4 ? rs.unit - kLift4 + log2f(sum) : 0.f;
+        if (INT4) f[x] *= int4row::kUnit;
         const int r = r16 + 8 * x;
         row[x] = out_row<kRT>(a, sg.s, sg.g, sg.rt, min(r, rows - 1));
         if (r < rows && t4 == 0) {
           if (!whole)
-            __stcg(a.part_ml + pslot * kRT + r, make_float2(rs.m, sum));
+            __stcg(a.part_ml + pslot * kRT + r, INT4 ? (sum == 0.f ? make_float2(-INFINITY, 0.f) : make_float2(all, 1.f)) : make_float2(rs.m, sum));
           else if (a.lse)
-            a.lse[row[x]] = (rs.m + log2f(sum)) * kLn2;
+            a.lse[row[x]] = (INT4 ? (sum == 0.f ? -INFINITY : all) : rs.m + log2f(sum)) * kLn2;
         }
       }
       if (!warp_wait(&bars->o_full, seg & 1, abort, a.err)) break;
@@ -905,11 +1137,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D, bool INT8>
+template <int D, int FMT>
 int launch(const Args& a, int runs, cudaStream_t st) {
-  constexpr size_t kSmem = BCfg<D, INT8>::kOffBars + sizeof(Bars) + 1024;
+  constexpr size_t kSmem = BCfg<D, FMT>::kOffBars + sizeof(Bars) + 1024;
   static_assert(kSmem <= 232448 - 512, "shared memory of a CTA");
-  auto kern = paged_block_kernel<D, INT8>;
+  auto kern = paged_block_kernel<D, FMT>;
   static std::atomic<uint64_t> attr{0};
   uint64_t bit;
   if (attrs_needed(attr, &bit)) {
@@ -925,7 +1157,7 @@ int launch(const Args& a, int runs, cudaStream_t st) {
   bool whole = (ps & (ps - 1)) == 0 && ps >= 8;
   CUtensorMap maps[2];
   memset(maps, 0, sizeof(maps));
-  if constexpr (INT8) {
+  if constexpr (FMT != MNW_KV_BF16) {
     whole = whole && aligned(a.ks, 16) && aligned(a.vs, 16);
   } else if (whole) {
     const uint64_t dims[4] = {static_cast<uint64_t>(D), static_cast<uint64_t>(ps), static_cast<uint64_t>(a.Hkv),
@@ -940,11 +1172,16 @@ int launch(const Args& a, int runs, cudaStream_t st) {
              : MNW_E_CUDA;
 }
 
+template <int D>
+int launch_fmt(const Args& a, int fmt, int runs, cudaStream_t st) {
+  if (fmt == MNW_KV_INT4) return launch<D, MNW_KV_INT4>(a, runs, st);
+  return fmt == MNW_KV_INT8 ? launch<D, MNW_KV_INT8>(a, runs, st) : launch<D, MNW_KV_BF16>(a, runs, st);
+}
+
 }  // namespace
 
-int launch_block(const Args& a, int d, bool int8, int runs, cudaStream_t st) {
-  if (d == 128) return int8 ? launch<128, true>(a, runs, st) : launch<128, false>(a, runs, st);
-  return int8 ? launch<64, true>(a, runs, st) : launch<64, false>(a, runs, st);
+int launch_block(const Args& a, int d, int fmt, int runs, cudaStream_t st) {
+  return d == 128 ? launch_fmt<128>(a, fmt, runs, st) : launch_fmt<64>(a, fmt, runs, st);
 }
 
 }  // namespace pattn

@@ -39,7 +39,6 @@ constexpr int kWarps = 4, kThreads = kWarps * 32, kTK = kInt4Keys;
 constexpr int kWK = kTK / kWarps;  // keys of a warp
 constexpr int kMT = 2, kSubs = kWK / (16 * kMT);  // 16-key operand tiles computed together, and such groups
 constexpr int kStages = 2;
-constexpr float kHalfUnit = 4096.f;  // the operands' 2^-24 is taken back half with the keys' scales, half with the queries' factors
 constexpr float kLow = -1e30f;   // a maximum of nothing: finite, so that -inf minus it is -inf
 constexpr float kLift = 6.f;     // log2 of the unit's own product as FP16
 constexpr float kMostP = 256.f, kMostW = 16384.f;  // probabilities and products that a row's maximum and unit allow
@@ -69,9 +68,6 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
 __device__ __forceinline__ uint32_t half2_of(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 // Two FP32 values in a 64-bit register.
 __device__ __forceinline__ uint64_t two(float lo, float hi) { return f32x2_pack(__float_as_uint(lo), __float_as_uint(hi)); }

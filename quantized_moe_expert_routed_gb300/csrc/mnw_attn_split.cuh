@@ -35,6 +35,8 @@ using paged::Seq;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kBlockRows = 128, kBlockKeys = 128;  // the block kernel's tiles (mnw_attn_paged_block.cu)
 constexpr int kInt4Keys = 256;                     // the INT4 kernel's (mnw_attn_paged_int4.cu), and its CTAs on an SM
+// INT4: the operands' 2^-24 is taken back half with the keys' scales, half with the queries' factors.
+constexpr float kHalfUnit = 4096.f;
 constexpr int int4_runs_per_sm(int rt) { return rt <= 16 ? 3 : 2; }
 
 struct Args {
@@ -66,12 +68,15 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// 16- and 4-byte asynchronous copies; bytes 0: zeros.
+// 16-, 8- and 4-byte asynchronous copies; bytes 0: zeros.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -452,7 +457,7 @@ __device__ __forceinline__ void join_item(const Args& a, const Seq& s, const Spa
 }
 
 // The block kernel over `runs` runs (mnw_attn_paged_block.cu).
-int launch_block(const Args& a, int d, bool int8, int runs, cudaStream_t st);
+int launch_block(const Args& a, int d, int fmt, int runs, cudaStream_t st);
 // The INT4 kernel for row tiles of rt = 8, 16 or 32 (mnw_attn_paged_int4.cu).
 int launch_int4(const Args& a, int d, int rt, int runs, cudaStream_t st);
 
