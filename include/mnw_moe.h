@@ -550,8 +550,9 @@ int mnw_kv_values(const void* cache, const void* scale, int fmt, int n_pages, in
  * Sums are FP32; A x enters the second product to 2^-16 of itself.  Tokens may
  * have adapters in any order; neighbours of one adapter cost least.
  * H, N and R are multiples of 8, R <= 128, n_adapters <= 1024, T <= 2^24,
- * N <= 2^20.  ws: device, 256-byte aligned, >= mnw_lora_workspace_size() bytes,
- * any contents; calls that overlap need one each.  T = 0 is a no-op. */
+ * N <= 2^20.  ws: device, 256-byte aligned, >= mnw_lora_workspace_size() bytes
+ * (0 up to 512 tokens: ws may be NULL), any contents; calls that overlap need
+ * one each.  T = 0 is a no-op. */
 size_t mnw_lora_workspace_size(int T, int H, int R, int n_adapters);
 int mnw_lora_add(const void* x, long long x_stride, const void* a, const void* b, const float* scale,
                  const int32_t* ranks, int n_adapters, int R, const int32_t* adapter, int T, int H, int N,

@@ -322,6 +322,27 @@ def _stream_of(t, stream):
     return _raw_stream(t.get_device()) if _raw_stream else torch.cuda.current_stream(t.device).cuda_stream
 
 
+# A call's scratch memory, straight from torch's caching allocator: allocated on the call's stream and given back behind
+# the launches, so the next user on that stream comes after them (a tensor for it costs 4 us of the host's time more).
+_raw_alloc = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc", None)
+_raw_delete = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_delete", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
+def _scratch(n, t, stream, handle):
+    """(address, what has to be given to _give_back) of n bytes for a call on tensor t's device and the given stream."""
+    if _raw_alloc and _raw_delete and _current_device and _current_device() == t.get_device():
+        p = _raw_alloc(n, handle)
+        return p, p
+    ws = _new((n,), torch.uint8, t.device, stream)
+    return ws.data_ptr(), ws
+
+
+def _give_back(held):
+    if held.__class__ is int:
+        _raw_delete(held)
+
+
 def mnw_rmsnorm(x, weight, eps=1e-6, residual=None, residual_out=None, y=None, codes=None, scales=None, int8=False,
                 stream=None, want_y=True):
     """Root-mean-square norm of bf16 x [T, H] with the residual's addition
@@ -378,37 +399,34 @@ def _token_rows(t, what, d=None):
 
 def _cache_args(k_cache, v_cache, k_scale, v_scale):
     """The cache's part of the C arguments: k, v, k_scale, v_scale, fmt, n_pages, page_size, page_stride; Hkv and d."""
-    dtype = k_cache.dtype
+    dtype, shape, st = k_cache.dtype, k_cache.shape, k_cache.stride()
+    if not (k_cache.is_cuda and v_cache.is_cuda) or v_cache.dtype is not dtype or len(shape) != 4:
+        raise MnwError("k_cache and v_cache: expected CUDA tensors of one type and 4 dimensions")
+    if v_cache.shape != shape or v_cache.stride() != st:
+        raise MnwError("k_cache and v_cache differ in shape or strides")
+    n, h, page, d = shape
+    if (page > 1 and st[2] != d) or (h > 1 and st[1] != page * d) or (d > 1 and st[3] != 1):
+        raise MnwError("a page of the cache [Hkv, page_size, d] has to be contiguous")
+    page_stride = st[0] if n > 1 else h * page * d
+    ks = vs = None
     if dtype is torch.bfloat16:
         fmt = KV_BF16
-    elif dtype is torch.int8:
-        fmt = KV_INT8
-    elif dtype is torch.uint8:
-        fmt = KV_INT4
-    else:
-        raise MnwError("the cache is bf16, int8, or uint8 (two 4-bit codes a byte)")
-    kp, vp = _need(k_cache, dtype, "k_cache", 4), _need(v_cache, dtype, "v_cache", 4)
-    n, h, page, d = k_cache.shape
-    st = k_cache.stride()
-    if v_cache.shape != k_cache.shape or v_cache.stride() != st:
-        raise MnwError("k_cache and v_cache differ in shape or strides")
-    if (page > 1 and st[2] != d) or (h > 1 and st[1] != page * d):
-        raise MnwError("a page of the cache [Hkv, page_size, d] has to be contiguous")
-    ks = vs = None
-    page_stride = st[0] if n > 1 else h * page * d
-    if fmt == KV_BF16:
         if k_scale is not None or v_scale is not None:
             raise MnwError("a bf16 cache has no scales")
+    elif dtype is not torch.int8 and dtype is not torch.uint8:
+        raise MnwError("the cache is bf16, int8, or uint8 (two 4-bit codes a byte)")
     elif k_scale is None or v_scale is None:
         raise MnwError("a quantised cache needs k_scale and v_scale")
-    elif fmt == KV_INT8:
+    elif dtype is torch.int8:
+        fmt = KV_INT8
         ks = _whole(k_scale, torch.float32, (n, h, page), "k_scale")
-        vs = _whole(v_scale, torch.float32, (n, h, page), "v_scale")
+        vs = ks if v_scale is k_scale else _whole(v_scale, torch.float32, (n, h, page), "v_scale")
     else:
+        fmt = KV_INT4
         ks = _whole(k_scale, torch.uint8, (n, h, page, 8), "k_scale")
-        vs = _whole(v_scale, torch.uint8, (n, h, page, 8), "v_scale")
+        vs = ks if v_scale is k_scale else _whole(v_scale, torch.uint8, (n, h, page, 8), "v_scale")
         d, page_stride = 2 * d, 2 * page_stride
-    return kp, vp, ks, vs, fmt, n, page, page_stride, h, d
+    return k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, fmt, n, page, page_stride, h, d
 
 
 def _batch_args(block_table, cache_lens, q_start):
@@ -490,11 +508,17 @@ def mnw_attn_paged(q, k_cache, v_cache, block_table, cache_lens, blk, scale, k_s
     if lse is None and want_lse:
         lse = _new((T, Hq), torch.float32, dev, stream)
     ep = None if err is None else _ptr(err)
+    lsp = None if lse is None else _whole(lse, torch.float32, (T, Hq), "lse")
+    st, held = _stream_of(q, stream), None
     if ws is None:
-        ws = _new((_paged_workspace(B, T, Hq, Hkv, d, q.get_device()),), torch.uint8, dev, stream)
+        wn = _paged_workspace(B, T, Hq, Hkv, d, q.get_device())
+        wp, held = _scratch(wn, q, stream, st)
+    else:
+        wp, wn = _need(ws, torch.uint8, "ws"), ws.numel()
     rc = load().mnw_attn_paged(qp, qst, B, T, Hq, Hkv, d, kc, vc, ks, vs, fmt, n_pages, page, page_stride, tp, most, lp, sp,
-                            blk, scale, op, None if lse is None else _whole(lse, torch.float32, (T, Hq), "lse"),
-                            _need(ws, torch.uint8, "ws"), ws.numel(), ep, _stream_of(q, stream))
+                               blk, scale, op, lsp, wp, wn, ep, st)
+    if held is not None:
+        _give_back(held)
     if rc:
         _check(rc, "mnw_attn_paged")
     return out if lse is None else (out, lse)
@@ -524,7 +548,7 @@ def mnw_lora_workspace_size(T, H, R, n_adapters) -> int:
 
 @functools.lru_cache(maxsize=256)
 def _lora_workspace(T, H, R, n, device):
-    return max(256, mnw_lora_workspace_size(T, H, R, n))
+    return mnw_lora_workspace_size(T, H, R, n)
 
 
 def _rows(t, what):
@@ -558,11 +582,17 @@ def mnw_lora_add(y, x, a, b, adapter, scale=None, ranks=None, out=None, ws=None,
     op, To, No, out_stride = _rows(out, "out")
     if (To, No) != (T, N):
         raise MnwError("out has another shape than y")
+    ep = None if err is None else _ptr(err)
+    st, held, wp = _stream_of(y, stream), None, None
     if ws is None:
-        ws = _new((_lora_workspace(T, H, R, n, y.get_device()),), torch.uint8, y.device, stream)
-    rc = load().mnw_lora_add(xp, x_stride, ap, bp, sp, kp, n, R, ip, T, H, N, yp, y_stride, op, out_stride,
-                             _need(ws, torch.uint8, "ws"), ws.numel(), None if err is None else _ptr(err),
-                             _stream_of(y, stream))
+        wn = _lora_workspace(T, H, R, n, y.get_device())
+        if wn:
+            wp, held = _scratch(wn, y, stream, st)
+    else:
+        wp, wn = _need(ws, torch.uint8, "ws"), ws.numel()
+    rc = load().mnw_lora_add(xp, x_stride, ap, bp, sp, kp, n, R, ip, T, H, N, yp, y_stride, op, out_stride, wp, wn, ep, st)
+    if held is not None:
+        _give_back(held)
     if rc:
         _check(rc, "mnw_lora_add")
     return out

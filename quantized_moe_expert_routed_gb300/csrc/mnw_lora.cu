@@ -333,6 +333,287 @@ __global__ void __launch_bounds__(kThreads) lora_expand_kernel(const Args a) {
   }
 }
 
+// ---- a batch of few tokens: all in one kernel ----
+// A cluster of kCluster CTAs takes a tile of kTF tokens of one adapter.  Every CTA works out by itself which (the list is
+// short), takes a share of H in the first product, reads the others' shares of v from their shared memory, and takes a
+// share of N in the second.  Operands go from global memory to the instructions' registers, in an order of k that gives a
+// lane 16 neighbouring bytes; what the second product reads is asked for before the exchange.
+constexpr int kFewTokens = 512, kCluster = 8;
+template <int NR>
+struct FewCfg {
+  static constexpr int kMT = NR <= 4 ? 2 : 1;       // 16-token operand tiles
+  static constexpr int kTF = 16 * kMT;
+  static constexpr int kRp = NR * 8, kWarps = kThreads / 32;
+  static constexpr int kOffOwn = kWarps * kTF * kRp * 4;       // [kTF][kRp] the CTA's share of v, behind its warps' shares
+  static constexpr int kOffV = kOffOwn + kTF * kRp * 4;        // [2][kTF][kRp + 8] v's two terms
+  static constexpr int kRowV = kRp + 8;
+  static constexpr int kSmem = kOffV + 2 * kTF * kRowV * 2;
+};
+inline int few_tiles(int T, int n, int tf) { return T / tf + std::min(n + 1, T); }
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ float4 ld_cluster(uint32_t addr, int cta) {
+  uint32_t there;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(addr), "r"(cta));
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(there) : "memory");
+  return v;
+}
+// Elements of a chunk of 8 that lie below `left`.
+__device__ __forceinline__ uint4 first_of(uint4 w, int left) {
+  auto keep = [&](uint32_t x, int e) { return left >= e + 2 ? x : (left == e + 1 ? x & 0xFFFFu : 0u); };
+  return make_uint4(keep(w.x, 0), keep(w.y, 2), keep(w.z, 4), keep(w.w, 6));
+}
+
+template <int NR>
+__global__ void __launch_bounds__(kThreads) lora_few_kernel(const Args a) {
+  using C = FewCfg<NR>;
+  constexpr int kMT = C::kMT, kTF = C::kTF, kRp = C::kRp, kWarps = C::kWarps;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int counts[1025];
+  __shared__ short bins[kFewTokens], places[kFewTokens];
+  __shared__ int tokens[kTF];
+  __shared__ int tile_bin, tile_base, tile_count;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2, t4 = lane & 3;
+  const int cta = blockIdx.x % kCluster, q = blockIdx.x / kCluster;
+  pdl_launch_dependents();
+  for (int e = tid; e <= a.n; e += kThreads) counts[e] = 0;
+  if (tid < kTF) tokens[tid] = -1;
+  if (tid == 0) {
+    tile_bin = -1;
+    tile_count = 0;
+  }
+  __syncthreads();
+  pdl_wait();
+
+  // ---- the tile: tokens are numbered within their adapter; every kTF-th begins one ----
+  if (warp == 0) {
+    int heads = 0;
+    for (int t0 = 0; t0 < a.T; t0 += 32) {
+      const int t = t0 + lane;
+      const bool on = t < a.T;
+      const int bin = on ? bin_of(a, t) : -1;
+      if (on && bin == a.n && blockIdx.x == 0 && a.err && __ldg(a.adapter + t) != -1) atomicOr(a.err, MNW_DEVERR_BAD_ADAPTER);
+      const uint32_t same = __match_any_sync(0xffffffffu, bin), below = same & ((1u << lane) - 1u);
+      const int place = (on ? counts[bin] : 0) + __popc(below);
+      __syncwarp();
+      if (on && below == 0) counts[bin] = place + __popc(same);
+      if (on) {
+        bins[t] = static_cast<short>(bin);
+        places[t] = static_cast<short>(place);
+      }
+      const bool head = on && place % kTF == 0;
+      const uint32_t hm = __ballot_sync(0xffffffffu, head);
+      if (head && heads + __popc(hm & ((1u << lane) - 1u)) == q) {
+        tile_bin = bin;
+        tile_base = place;
+      }
+      heads += __popc(hm);
+      __syncwarp();
+    }
+  }
+  __syncthreads();
+  const int bin = tile_bin;
+  if (bin < 0) return;  // (the whole cluster)
+  const bool none = bin == a.n;
+  if (none && a.out == a.y) return;
+  for (int t = tid; t < a.T; t += kThreads) {
+    const int r = places[t] - tile_base;
+    if (bins[t] == bin && static_cast<unsigned>(r) < static_cast<unsigned>(kTF)) {
+      tokens[r] = t;
+      atomicAdd(&tile_count, 1);
+    }
+  }
+  const int rank = none ? 0 : rank_of(a, bin);
+  const float scale = none ? 0.f : (a.scale ? __ldg(a.scale + bin) : 1.f);
+  __syncthreads();
+  const int count = tile_count;
+
+  // ---- the second product's operands, asked for ahead: 32 columns at a time, as in the kernel for many tokens ----
+  const int groups = (a.N + 31) / 32;
+  const int g0 = groups * cta / kCluster + warp, g1 = groups * (cta + 1) / kCluster;
+  const __nv_bfloat16* wb = a.b + static_cast<long long>(none ? 0 : bin) * a.N * a.R;
+  constexpr int kB = NR == 2 ? 1 : NR / 4;  // chunks of a lane in a row of B
+  uint4 bw[4][kB], yw[kMT][2];
+  auto fetch = [&](int g) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int n = g * 32 + 8 * (g8 >> 1) + 2 * j + (g8 & 1);
+#pragma unroll
+      for (int c = 0; c < kB; ++c) {
+        const int r = NR == 2 ? 4 * t4 : 32 * c + 8 * t4;
+        bw[j][c] = make_uint4(0, 0, 0, 0);
+        if (n < a.N && r < rank) {
+          const __nv_bfloat16* src = wb + static_cast<long long>(n) * a.R + r;
+          if constexpr (NR == 2) {
+            const uint2 w = __ldg(reinterpret_cast<const uint2*>(src));
+            bw[j][c].x = w.x;
+            bw[j][c].y = w.y;
+          } else {
+            bw[j][c] = __ldg(reinterpret_cast<const uint4*>(src));
+          }
+        }
+      }
+    }
+    const int col = g * 32 + 8 * t4;
+#pragma unroll
+    for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int t = tokens[16 * mt + 8 * x + g8];
+        yw[mt][x] = make_uint4(0, 0, 0, 0);
+        if (t >= 0 && col < a.N) yw[mt][x] = *reinterpret_cast<const uint4*>(a.y + t * a.y_stride + col);
+      }
+  };
+  if (g0 < g1) fetch(g0);
+
+  // ---- v: this CTA's share of H ----
+  const uint32_t sbase = smem_u32(smem);
+  if (!none) {
+    const __nv_bfloat16* wa = a.a + static_cast<long long>(bin) * a.R * a.H;
+    const int blocks = (a.H + 31) / 32;
+    const int b1 = blocks * (cta + 1) / kCluster;
+    float acc[kMT][NR][4];
+#pragma unroll
+    for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+      for (int i = 0; i < NR; ++i) acc[mt][i][0] = acc[mt][i][1] = acc[mt][i][2] = acc[mt][i][3] = 0.f;
+#pragma unroll(NR <= 4 ? 2 : 1)
+    for (int b = blocks * cta / kCluster + warp; b < b1; b += kWarps) {
+      const int k = b * 32 + 8 * t4;
+      uint4 xw[kMT][2], w[NR];
+#pragma unroll
+      for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int t = tokens[16 * mt + 8 * x + g8];
+          xw[mt][x] = make_uint4(0, 0, 0, 0);
+          if (t >= 0 && k < a.H) xw[mt][x] = *reinterpret_cast<const uint4*>(a.x + t * a.x_stride + k);
+        }
+#pragma unroll
+      for (int i = 0; i < NR; ++i) {
+        const int r = 8 * i + g8;
+        w[i] = make_uint4(0, 0, 0, 0);
+        if (r < rank && k < a.H) w[i] = __ldg(reinterpret_cast<const uint4*>(wa + static_cast<long long>(r) * a.H + k));
+      }
+#pragma unroll
+      for (int i = 0; i < NR; ++i)
+#pragma unroll
+        for (int mt = 0; mt < kMT; ++mt) {
+          mma_bf16(acc[mt][i], xw[mt][0].x, xw[mt][1].x, xw[mt][0].y, xw[mt][1].y, w[i].x, w[i].y);
+          mma_bf16(acc[mt][i], xw[mt][0].z, xw[mt][1].z, xw[mt][0].w, xw[mt][1].w, w[i].z, w[i].w);
+        }
+    }
+    float* part = reinterpret_cast<float*>(smem) + warp * (kTF * kRp);
+#pragma unroll
+    for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int r = 16 * mt + 8 * x + g8;
+#pragma unroll
+        for (int i = 0; i < NR; ++i)
+          *reinterpret_cast<float2*>(part + r * kRp + 8 * i + 2 * t4) = make_float2(acc[mt][i][2 * x], acc[mt][i][2 * x + 1]);
+      }
+    __syncthreads();
+    const int used = count * kRp;  // rows of other tokens are not looked at
+    for (int e = tid * 4; e < used; e += kThreads * 4) {
+      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float4 z = *reinterpret_cast<const float4*>(smem + (w * (kTF * kRp) + e) * 4);
+        s.x += z.x;
+        s.y += z.y;
+        s.z += z.z;
+        s.w += z.w;
+      }
+      *reinterpret_cast<float4*>(smem + C::kOffOwn + e * 4) = s;
+    }
+    cluster_arrive();
+    cluster_wait();
+    for (int e = tid * 4; e < kTF * kRp; e += kThreads * 4) {
+      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (e < used) {
+#pragma unroll
+        for (int c = 0; c < kCluster; ++c) {
+          const float4 z = ld_cluster(sbase + C::kOffOwn + e * 4, c);
+          s.x += z.x;
+          s.y += z.y;
+          s.z += z.z;
+          s.w += z.w;
+        }
+      }
+      const uint32_t h0 = pack_bf16x2(s.x, s.y), h1 = pack_bf16x2(s.z, s.w);
+      const uint32_t l0 = pack_bf16x2(s.x - __uint_as_float(h0 << 16), s.y - __uint_as_float(h0 & 0xFFFF0000u));
+      const uint32_t l1 = pack_bf16x2(s.z - __uint_as_float(h1 << 16), s.w - __uint_as_float(h1 & 0xFFFF0000u));
+      uint8_t* to = smem + C::kOffV + (e / kRp * C::kRowV + e % kRp) * 2;
+      *reinterpret_cast<uint2*>(to) = make_uint2(h0, h1);
+      *reinterpret_cast<uint2*>(to + kTF * C::kRowV * 2) = make_uint2(l0, l1);
+    }
+    cluster_arrive();  // the others' shares are read
+    __syncthreads();
+  }
+
+  // ---- out = y + s B v ----
+  for (int g = g0; g < g1; g += kWarps) {
+    float acc[kMT][4][4];
+#pragma unroll
+    for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[mt][j][0] = acc[mt][j][1] = acc[mt][j][2] = acc[mt][j][3] = 0.f;
+    if (!none) {
+#pragma unroll
+      for (int c = 0; c < kB; ++c) {
+        const int e = NR == 2 ? 4 * t4 : 32 * c + 8 * t4;  // the lane's elements of v and B
+        if (rank & 7) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) bw[j][c] = first_of(bw[j][c], rank - e);
+        }
+#pragma unroll
+        for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+          for (int term = 0; term < 2; ++term) {
+            const uint8_t* at = smem + C::kOffV + ((term * kTF + 16 * mt + g8) * C::kRowV + e) * 2;
+            if constexpr (NR == 2) {
+              const uint2 v0 = *reinterpret_cast<const uint2*>(at), v1 = *reinterpret_cast<const uint2*>(at + 8 * C::kRowV * 2);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) mma_bf16(acc[mt][j], v0.x, v1.x, v0.y, v1.y, bw[j][c].x, bw[j][c].y);
+            } else {
+              const uint4 v0 = *reinterpret_cast<const uint4*>(at), v1 = *reinterpret_cast<const uint4*>(at + 8 * C::kRowV * 2);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                mma_bf16(acc[mt][j], v0.x, v1.x, v0.y, v1.y, bw[j][c].x, bw[j][c].y);
+                mma_bf16(acc[mt][j], v0.z, v1.z, v0.w, v1.w, bw[j][c].z, bw[j][c].w);
+              }
+            }
+          }
+      }
+    }
+    const int col = g * 32 + 8 * t4;
+    auto add = [&](uint32_t u, float p, float r) {
+      return pack_bf16x2(fmaf(scale, p, __uint_as_float(u << 16)), fmaf(scale, r, __uint_as_float(u & 0xFFFF0000u)));
+    };
+    uint4 ow[kMT][2];
+#pragma unroll
+    for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const uint4 u = yw[mt][x];
+        ow[mt][x] = none ? u : make_uint4(add(u.x, acc[mt][0][2 * x], acc[mt][0][2 * x + 1]), add(u.y, acc[mt][1][2 * x], acc[mt][1][2 * x + 1]),
+                                          add(u.z, acc[mt][2][2 * x], acc[mt][2][2 * x + 1]), add(u.w, acc[mt][3][2 * x], acc[mt][3][2 * x + 1]));
+      }
+    if (g + kWarps < g1) fetch(g + kWarps);
+#pragma unroll
+    for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int t = tokens[16 * mt + 8 * x + g8];
+        if (t >= 0 && col < a.N) *reinterpret_cast<uint4*>(a.out + t * a.out_stride + col) = ow[mt][x];
+      }
+  }
+  if (!none) cluster_wait();  // a CTA's memory stays until the others have read it
+}
+
 // ---- host ----
 
 inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
@@ -346,7 +627,8 @@ struct Workspace {
   size_t starts, order, v, bytes;
 };
 inline Workspace workspace_of(int T, int H, int R, int n) {
-  Workspace w;
+  Workspace w{};
+  if (T <= kFewTokens) return w;
   w.starts = 0;
   w.order = up256((static_cast<size_t>(n) + 2) * 4);
   w.v = w.order + up256(static_cast<size_t>(T) * 4);
@@ -355,7 +637,36 @@ inline Workspace workspace_of(int T, int H, int R, int n) {
 }
 
 template <int NR>
+int launch_few(const Args& a, cudaStream_t st) {
+  using C = FewCfg<NR>;
+  auto kern = lora_few_kernel<NR>;
+  static std::atomic<uint64_t> attr{0};
+  uint64_t bit;
+  if (attrs_needed(attr, &bit)) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess) return MNW_E_CUDA;
+    attrs_done(attr, bit);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(few_tiles(a.T, a.n, C::kTF) * kCluster);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = kCluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, kern, a) != cudaSuccess) return MNW_E_CUDA;
+  note_launch();
+  return MNW_OK;
+}
+
+template <int NR>
 int launch(Args& a, uint8_t* ws, cudaStream_t st) {
+  if (a.T <= kFewTokens) return launch_few<NR>(a, st);
   const Workspace w = workspace_of(a.T, a.H, a.R, a.n);
   a.starts = reinterpret_cast<int32_t*>(ws + w.starts);
   a.order = reinterpret_cast<int32_t*>(ws + w.order);
@@ -399,12 +710,13 @@ int mnw_lora_add(const void* x, long long x_stride, const void* a, const void* b
   if (T < 0 || H <= 0 || N <= 0 || R <= 0 || n_adapters <= 0) return MNW_E_INVALID_ARG;
   if (T == 0) return MNW_OK;
   if (H % 8 || N % 8 || R % 8 || R > 128 || n_adapters > 1024 || T > (1 << 24) || N > (1 << 20)) return MNW_E_UNSUPPORTED;
-  if (!x || !a || !b || !adapter || !y || !out || !ws || !aligned(x, 16) || !aligned(a, 16) || !aligned(b, 16) ||
+  const size_t need = mnw_lora_workspace_size(T, H, R, n_adapters);
+  if (!x || !a || !b || !adapter || !y || !out || (need > 0 && !ws) || !aligned(x, 16) || !aligned(a, 16) || !aligned(b, 16) ||
       !aligned(y, 16) || !aligned(out, 16) || !aligned(ws, 256) || !aligned(adapter, 4) || !aligned(ranks, 4) ||
       !aligned(scale, 4) || x_stride % 8 || y_stride % 8 || out_stride % 8 || x_stride < H || y_stride < N || out_stride < N)
     return MNW_E_INVALID_ARG;
   if (y == out && y_stride != out_stride && T > 1) return MNW_E_INVALID_ARG;  // rows of one over others of the other
-  if (ws_bytes < mnw_lora_workspace_size(T, H, R, n_adapters)) return MNW_E_WORKSPACE_TOO_SMALL;
+  if (ws_bytes < need) return MNW_E_WORKSPACE_TOO_SMALL;
   lora::Args p{};
   p.x = static_cast<const __nv_bfloat16*>(x);
   p.a = static_cast<const __nv_bfloat16*>(a);
