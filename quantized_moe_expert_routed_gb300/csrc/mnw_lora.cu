@@ -41,7 +41,7 @@ __device__ __forceinline__ int bin_of(const Args& a, int t) {
   return static_cast<unsigned>(id) < static_cast<unsigned>(a.n) ? id : a.n;
 }
 __device__ __forceinline__ int rank_of(const Args& a, int i) {
-  const int r = a.ranks ? __ldg(a.ranks + i) : a.R;
+  const int r = a.ranks ? __ldcg(a.ranks + i) : a.R;
   if (static_cast<unsigned>(r) > static_cast<unsigned>(a.R)) {
     if (threadIdx.x == 0 && a.err) atomicOr(a.err, MNW_DEVERR_BAD_ADAPTER);
     return r < 0 ? 0 : a.R;
@@ -50,53 +50,74 @@ __device__ __forceinline__ int rank_of(const Args& a, int i) {
 }
 
 // ---- grouping: CTA e lists the tokens of adapter e (e = n: of none) ----
-constexpr int kGroupThreads = 256;
+// A thread looks at kRun neighbouring tokens and remembers which are the adapter's.
+constexpr int kGroupThreads = 1024, kRun = 16;
 __global__ void __launch_bounds__(kGroupThreads) lora_group_kernel(const Args a) {
   constexpr int kWarps = kGroupThreads / 32;
-  __shared__ int sums[kWarps][2];
-  pdl_launch_dependents();
+  __shared__ int sums[2][kWarps];
+  __shared__ int total[2];
   pdl_wait();
+  pdl_launch_dependents();
   const int e = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  int before = 0, mine = 0;
-  for (int t = tid; t < a.T; t += kGroupThreads) {
-    const int id = __ldg(a.adapter + t), b = bin_of(a, t);
-    before += b < e ? 1 : 0;
-    mine += b == e ? 1 : 0;
-    if (e == a.n && b == a.n && id != -1 && a.err) atomicOr(a.err, MNW_DEVERR_BAD_ADAPTER);
-  }
-  before = __reduce_add_sync(0xffffffffu, before);
-  mine = __reduce_add_sync(0xffffffffu, mine);
-  if (lane == 0) {
-    sums[warp][0] = before;
-    sums[warp][1] = mine;
-  }
-  __syncthreads();
-  before = mine = 0;
+  // Tokens of lower numbers come first; with more tokens than the threads hold at a time, they are counted beforehand.
+  int at = 0, mine_all = 0;
+  for (int pass = a.T <= kGroupThreads * kRun ? 1 : 0; pass < 2; ++pass) {
+    for (int t0 = 0; t0 < a.T; t0 += kGroupThreads * kRun) {
+      const int first = t0 + tid * kRun;
+      uint32_t bits = 0;
+      int before = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    before += sums[w][0];
-    mine += sums[w][1];
+      for (int i = 0; i < kRun; ++i) {
+        const int t = first + i;
+        if (t >= a.T) break;
+        const int id = __ldg(a.adapter + t), bin = static_cast<unsigned>(id) < static_cast<unsigned>(a.n) ? id : a.n;
+        bits |= (bin == e ? 1u : 0u) << i;
+        before += bin < e ? 1 : 0;
+        if (e == a.n && pass == 1 && bin == a.n && id != -1 && a.err) atomicOr(a.err, MNW_DEVERR_BAD_ADAPTER);
+      }
+      const int mine = __popc(bits);
+      int incl = mine;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += o;
+      }
+      before = __reduce_add_sync(0xffffffffu, before);
+      __syncthreads();  // the sums before are read
+      if (lane == 31) {
+        sums[0][warp] = incl;
+        sums[1][warp] = before;
+      }
+      __syncthreads();
+      if (warp == 0) {
+        const int m = sums[0][lane];
+        int mi = m;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int o = __shfl_up_sync(0xffffffffu, mi, d);
+          if (lane >= d) mi += o;
+        }
+        const int b = __reduce_add_sync(0xffffffffu, sums[1][lane]);
+        sums[0][lane] = mi - m;
+        if (lane == 31) {
+          total[0] = mi;
+          total[1] = b;
+        }
+      }
+      __syncthreads();
+      if (pass == 0 || a.T <= kGroupThreads * kRun) at += total[1];
+      if (pass == 1) {
+        int to = at + mine_all + sums[0][warp] + incl - mine;
+#pragma unroll
+        for (int i = 0; i < kRun; ++i)
+          if (bits >> i & 1) a.order[to++] = first + i;
+        mine_all += total[0];
+      }
+    }
   }
   if (tid == 0) {
-    a.starts[e] = before;
+    a.starts[e] = at;
     if (e == a.n) a.starts[e + 1] = a.T;
-  }
-  if (mine == 0) return;
-  int at = before;
-  for (int t0 = 0; t0 < a.T; t0 += kGroupThreads) {
-    const int t = t0 + tid;
-    const bool is = t < a.T && bin_of(a, t) == e;
-    const uint32_t m = __ballot_sync(0xffffffffu, is);
-    __syncthreads();  // the sums before are read
-    if (lane == 0) sums[warp][0] = __popc(m);
-    __syncthreads();
-    int pos = at;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      pos += w < warp ? sums[w][0] : 0;
-      at += sums[w][0];
-    }
-    if (is) a.order[pos + __popc(m & ((1u << lane) - 1u))] = t;
   }
 }
 
@@ -110,7 +131,7 @@ __device__ __forceinline__ Tile find_tile(const Args& a, int q, Tile* sh) {
   if (threadIdx.x == 0) sh->count = 0;
   __syncthreads();
   for (int e = threadIdx.x; e <= a.n; e += kThreads) {
-    const int lo = a.starts[e], hi = a.starts[e + 1];
+    const int lo = __ldcg(a.starts + e), hi = __ldcg(a.starts + e + 1);
     const int j = q - (lo / kTT + e);
     if (j >= 0 && j * kTT < hi - lo) *sh = Tile{e, lo + j * kTT, min(kTT, hi - lo - j * kTT)};
   }
@@ -134,24 +155,29 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
 }
 
 // ---- v = A x: a tile of tokens and a share of H ----
-// A warp takes 16 tokens and all ranks.  Steps of 64 elements of H arrive by cp.async, 128-byte rows whose 16-byte chunks
-// are exchanged by the row.  Of 32 elements, lane t of a fragment takes chunk t: two k steps, in an order of its own
-// that both operands share.
+// Steps of 64 elements of H arrive by cp.async, as 128-byte rows that exchange halves by the row (the lanes of a load read
+// 64 bytes of two rows).  A warp takes 32 tokens, all ranks and one half of each step, so that a row of A is read from
+// shared memory once for 32 tokens.  Of 32 elements, lane t of a fragment takes chunk t: two k steps, in an order of its
+// own that both operands share.  The halves' sums meet in shared memory at the end.
 template <int NR>
 struct ShrinkCfg {
   static constexpr int kStages = 3;
   static constexpr int kXBytes = kTT * 128, kABytes = NR * 8 * 128, kStageBytes = kXBytes + kABytes;
   static constexpr int kSmem = kStages * kStageBytes;
+  static constexpr int kPad = NR * 8 + 4;  // floats of a token where the halves meet
+  static_assert(kTT * kPad * 4 <= kSmem);
 };
+__device__ __forceinline__ uint32_t step_at(int r, int c) { return static_cast<uint32_t>(r * 128 + ((c ^ ((r & 1) << 2)) << 4)); }
 template <int NR>
-__global__ void __launch_bounds__(kThreads) lora_shrink_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, NR <= 8 ? 2 : 1) lora_shrink_kernel(const Args a) {
   using C = ShrinkCfg<NR>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Tile tile_sh;
   __shared__ int tokens[kTT];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2, t4 = lane & 3;
-  pdl_launch_dependents();
   pdl_wait();
+  // The kernel behind this one begins with inputs that are complete by now, the grouping among them; only v it waits for.
+  pdl_launch_dependents();
   const Tile tl = find_tile(a, blockIdx.x, &tile_sh);
   if (tl.count == 0 || tl.bin == a.n) return;
   if (tid < kTT) tokens[tid] = tid < tl.count ? a.order[tl.first + tid] : -1;
@@ -162,26 +188,32 @@ __global__ void __launch_bounds__(kThreads) lora_shrink_kernel(const Args a) {
   const int s0 = static_cast<int>(static_cast<long long>(steps_all) * blockIdx.y / a.splits);
   const int s1 = static_cast<int>(static_cast<long long>(steps_all) * (blockIdx.y + 1) / a.splits);
   const __nv_bfloat16* wa = a.a + static_cast<long long>(tl.bin) * a.R * a.H;
+  const int lr = tid >> 3, lc = tid & 7;  // row (of 32) and chunk that this thread copies
+  int tok[kTT / 32];
+#pragma unroll
+  for (int i = 0; i < kTT / 32; ++i) tok[i] = tokens[i * 32 + lr];
   auto load = [&](int s, int slot) {
     const uint32_t st = sbase + slot * C::kStageBytes;
-    const int c = tid & 7, k = s * 64 + c * 8;
+    const int k = s * 64 + lc * 8;
 #pragma unroll
     for (int i = 0; i < kTT / 32; ++i) {
-      const int r = i * 32 + (tid >> 3), t = tokens[r];
-      const bool on = t >= 0 && k < a.H;
-      cp_async16(sw128(st, r, c), on ? a.x + t * a.x_stride + k : a.x, on ? 16u : 0u);
+      const bool on = tok[i] >= 0 && k < a.H;
+      cp_async16(st + step_at(i * 32 + lr, lc), on ? a.x + tok[i] * a.x_stride + k : a.x, on ? 16u : 0u);
     }
 #pragma unroll
     for (int i = 0; i < (NR * 8 + 31) / 32; ++i) {
-      const int r = i * 32 + (tid >> 3);
+      const int r = i * 32 + lr;
       const bool on = r < rank && k < a.H;
       if (NR * 8 >= 32 || r < NR * 8)
-        cp_async16(sw128(st + C::kXBytes, r, c), on ? wa + static_cast<long long>(r) * a.H + k : wa, on ? 16u : 0u);
+        cp_async16(st + C::kXBytes + step_at(r, lc), on ? wa + static_cast<long long>(r) * a.H + k : wa, on ? 16u : 0u);
     }
   };
-  float acc[NR][4];
+  const int part = warp & 3, half = warp >> 2;
+  float acc[2][NR][4];
 #pragma unroll
-  for (int i = 0; i < NR; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+  for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+    for (int i = 0; i < NR; ++i) acc[mt][i][0] = acc[mt][i][1] = acc[mt][i][2] = acc[mt][i][3] = 0.f;
 #pragma unroll
   for (int i = 0; i < C::kStages - 1; ++i) {
     if (s0 + i < s1) load(s0 + i, i);
@@ -196,30 +228,52 @@ __global__ void __launch_bounds__(kThreads) lora_shrink_kernel(const Args a) {
       if (s + C::kStages - 1 < s1) load(s + C::kStages - 1, ns);
       cp_commit();
     }
-    if (warp * 16 < tl.count) {
+    if (part * 32 < tl.count) {
       const uint32_t st = sbase + slot * C::kStageBytes;
+      const int c = half * 4 + t4;
+      uint4 xw[2][2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint4 x0 = lds128(sw128(st, warp * 16 + g8, h * 4 + t4)), x1 = lds128(sw128(st, warp * 16 + g8 + 8, h * 4 + t4));
+      for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-        for (int i = 0; i < NR; ++i) {
-          const uint4 w = lds128(sw128(st + C::kXBytes, i * 8 + g8, h * 4 + t4));
-          mma_bf16(acc[i], x0.x, x1.x, x0.y, x1.y, w.x, w.y);
-          mma_bf16(acc[i], x0.z, x1.z, x0.w, x1.w, w.z, w.w);
+        for (int x = 0; x < 2; ++x) xw[mt][x] = lds128(st + step_at(part * 32 + 16 * mt + 8 * x + g8, c));
+#pragma unroll
+      for (int i = 0; i < NR; ++i) {
+        const uint4 w = lds128(st + C::kXBytes + step_at(i * 8 + g8, c));
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+          mma_bf16(acc[mt][i], xw[mt][0].x, xw[mt][1].x, xw[mt][0].y, xw[mt][1].y, w.x, w.y);
+          mma_bf16(acc[mt][i], xw[mt][0].z, xw[mt][1].z, xw[mt][0].w, xw[mt][1].w, w.z, w.w);
         }
       }
     }
     if (++slot == C::kStages) slot = 0;
   }
+  cp_wait<0>();
+  __syncthreads();
+  float* const meet = reinterpret_cast<float*>(smem);
   float* v = a.v + (static_cast<long long>(blockIdx.y) * a.T + tl.first) * (NR * 8);
 #pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    const int r = warp * 16 + g8 + 8 * x;
-    if (r < tl.count) {
+  for (int pass = 0; pass < 2; ++pass) {
+    if (half != pass) {  // first the upper half leaves its sums, then the lower adds them
 #pragma unroll
-      for (int i = 0; i < NR; ++i)
-        *reinterpret_cast<float2*>(v + static_cast<long long>(r) * (NR * 8) + i * 8 + 2 * t4) = make_float2(acc[i][2 * x], acc[i][2 * x + 1]);
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int r = part * 32 + 16 * mt + 8 * x + g8;
+#pragma unroll
+          for (int i = 0; i < NR; ++i) {
+            float2* m = reinterpret_cast<float2*>(meet + r * C::kPad + i * 8 + 2 * t4);
+            float2 z = make_float2(acc[mt][i][2 * x], acc[mt][i][2 * x + 1]);
+            if (pass == 0) {
+              *m = z;
+            } else if (r < tl.count) {
+              const float2 o = *m;
+              __stcg(reinterpret_cast<float2*>(v + static_cast<long long>(r) * (NR * 8) + i * 8 + 2 * t4), make_float2(z.x + o.x, z.y + o.y));
+            }
+          }
+        }
     }
+    __syncthreads();
   }
 }
 
@@ -238,17 +292,19 @@ __device__ __forceinline__ uint32_t b_at(int n, int c) {
   return static_cast<uint32_t>(n * (NR * 16) + ((NR >= 8 ? c ^ ((n & 1) << 2) : c) << 4));
 }
 template <int NR>
-__global__ void __launch_bounds__(kThreads) lora_expand_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, NR <= 4 ? 3 : 2) lora_expand_kernel(const Args a) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Tile tile_sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2, t4 = lane & 3;
-  pdl_launch_dependents();
-  pdl_wait();
+  // Everything but v was complete before the kernel ahead let this one start; it is read past L1, which may hold lines of
+  // before.
   const Tile tl = find_tile(a, blockIdx.x, &tile_sh);
-  if (tl.count == 0) return;
-  const int col0 = blockIdx.y * kCols;
   const bool none = tl.bin == a.n;
-  if (none && a.out == a.y && a.out_stride == a.y_stride) return;
+  if (tl.count == 0 || (none && a.out == a.y)) {
+    pdl_wait();  // (the kernels behind this one count on the ones ahead of it)
+    return;
+  }
+  const int col0 = blockIdx.y * kCols;
   const int rank = none ? 0 : rank_of(a, tl.bin);
   const uint32_t sbase = smem_u32(smem);
   if (!none) {
@@ -262,7 +318,23 @@ __global__ void __launch_bounds__(kThreads) lora_expand_kernel(const Args a) {
   cp_commit();
   const int r0 = warp * 16 + g8;
   const bool on0 = r0 < tl.count, on1 = r0 + 8 < tl.count;
-  const long long tok0 = on0 ? a.order[tl.first + r0] : 0, tok1 = on1 ? a.order[tl.first + r0 + 8] : 0;
+  const long long tok0 = on0 ? __ldcg(a.order + tl.first + r0) : 0, tok1 = on1 ? __ldcg(a.order + tl.first + r0 + 8) : 0;
+  const float scale = none ? 0.f : (a.scale ? __ldcg(a.scale + tl.bin) : 1.f);
+  const __nv_bfloat16 *y0 = a.y + tok0 * a.y_stride, *y1 = a.y + tok1 * a.y_stride;
+  __nv_bfloat16 *o0 = a.out + tok0 * a.out_stride, *o1 = a.out + tok1 * a.out_stride;
+  // y is asked for kDeep groups of 32 columns ahead
+  constexpr int kDeep = 4, kGroups = kCols / 32;
+  uint4 u[kDeep][2];
+  auto fetch = [&](int g, uint4 (&w)[2]) {
+    const int col = col0 + g * 32 + 8 * t4;
+    w[0] = w[1] = make_uint4(0, 0, 0, 0);
+    if (on0 && col < a.N) w[0] = __ldcg(reinterpret_cast<const uint4*>(y0 + col));
+    if (on1 && col < a.N) w[1] = __ldcg(reinterpret_cast<const uint4*>(y1 + col));
+  };
+#pragma unroll
+  for (int g = 0; g < kDeep; ++g) fetch(g, u[g]);
+  pdl_wait();
+  pdl_launch_dependents();
   constexpr int kKS = NR / 2;  // k steps
   uint32_t hi[kKS][4], lo[kKS][4];
 #pragma unroll
@@ -287,49 +359,48 @@ __global__ void __launch_bounds__(kThreads) lora_expand_kernel(const Args a) {
       lo[s][x] = pack_bf16x2(f.x - __uint_as_float(h0 << 16), f.y - __uint_as_float(h0 & 0xFFFF0000u));
       lo[s][2 + x] = pack_bf16x2(f.z - __uint_as_float(h1 << 16), f.w - __uint_as_float(h1 & 0xFFFF0000u));
     }
-  const float scale = none ? 0.f : (a.scale ? __ldg(a.scale + tl.bin) : 1.f);
-  const __nv_bfloat16 *y0 = a.y + tok0 * a.y_stride, *y1 = a.y + tok1 * a.y_stride;
-  __nv_bfloat16 *o0 = a.out + tok0 * a.out_stride, *o1 = a.out + tok1 * a.out_stride;
   cp_wait<0>();
   __syncthreads();
   if (warp * 16 >= tl.count) return;
-#pragma unroll 2
-  for (int n0 = 0; n0 < kCols; n0 += 32) {
-    const int col = col0 + n0 + 8 * t4;
-    if (col0 + n0 >= a.N) break;
-    const bool in0 = on0 && col < a.N, in1 = on1 && col < a.N;
-    uint4 u0 = make_uint4(0, 0, 0, 0), u1 = u0;
-    if (in0) u0 = *reinterpret_cast<const uint4*>(y0 + col);
-    if (in1) u1 = *reinterpret_cast<const uint4*>(y1 + col);
-    if (!none) {
-      float acc[4][4];
+#pragma unroll 1
+  for (int gb = 0; gb < kGroups; gb += kDeep) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
-        const int n = n0 + 8 * (g8 >> 1) + 2 * j + (g8 & 1);
+    for (int d = 0; d < kDeep; ++d) {
+      const int n0 = (gb + d) * 32, col = col0 + n0 + 8 * t4;
+      if (col0 + n0 >= a.N) break;
+      if (!none) {
+        float acc[4][4];
 #pragma unroll
-        for (int s = 0; s < kKS; s += 2) {
-          if constexpr (NR == 2) {
-            const uint2 w = *reinterpret_cast<const uint2*>(smem + b_at<NR>(n, t4 >> 1) + 8 * (t4 & 1));
-            mma_bf16(acc[j], hi[0][0], hi[0][1], hi[0][2], hi[0][3], w.x, w.y);
-            mma_bf16(acc[j], lo[0][0], lo[0][1], lo[0][2], lo[0][3], w.x, w.y);
-          } else {
-            const uint4 w = *reinterpret_cast<const uint4*>(smem + b_at<NR>(n, 2 * s + t4));
-            mma_bf16(acc[j], hi[s][0], hi[s][1], hi[s][2], hi[s][3], w.x, w.y);
-            mma_bf16(acc[j], lo[s][0], lo[s][1], lo[s][2], lo[s][3], w.x, w.y);
-            mma_bf16(acc[j], hi[s + 1][0], hi[s + 1][1], hi[s + 1][2], hi[s + 1][3], w.z, w.w);
-            mma_bf16(acc[j], lo[s + 1][0], lo[s + 1][1], lo[s + 1][2], lo[s + 1][3], w.z, w.w);
+        for (int j = 0; j < 4; ++j) {
+          acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+          const int n = n0 + 8 * (g8 >> 1) + 2 * j + (g8 & 1);
+#pragma unroll
+          for (int s = 0; s < kKS; s += 2) {
+            if constexpr (NR == 2) {
+              const uint2 w = *reinterpret_cast<const uint2*>(smem + b_at<NR>(n, t4 >> 1) + 8 * (t4 & 1));
+              mma_bf16(acc[j], hi[0][0], hi[0][1], hi[0][2], hi[0][3], w.x, w.y);
+              mma_bf16(acc[j], lo[0][0], lo[0][1], lo[0][2], lo[0][3], w.x, w.y);
+            } else {
+              const uint4 w = *reinterpret_cast<const uint4*>(smem + b_at<NR>(n, 2 * s + t4));
+              mma_bf16(acc[j], hi[s][0], hi[s][1], hi[s][2], hi[s][3], w.x, w.y);
+              mma_bf16(acc[j], lo[s][0], lo[s][1], lo[s][2], lo[s][3], w.x, w.y);
+              mma_bf16(acc[j], hi[s + 1][0], hi[s + 1][1], hi[s + 1][2], hi[s + 1][3], w.z, w.w);
+              mma_bf16(acc[j], lo[s + 1][0], lo[s + 1][1], lo[s + 1][2], lo[s + 1][3], w.z, w.w);
+            }
           }
         }
+        auto add = [&](uint32_t w, float p, float q) {
+          return pack_bf16x2(fmaf(scale, p, __uint_as_float(w << 16)), fmaf(scale, q, __uint_as_float(w & 0xFFFF0000u)));
+        };
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          u[d][x] = make_uint4(add(u[d][x].x, acc[0][2 * x], acc[0][2 * x + 1]), add(u[d][x].y, acc[1][2 * x], acc[1][2 * x + 1]),
+                               add(u[d][x].z, acc[2][2 * x], acc[2][2 * x + 1]), add(u[d][x].w, acc[3][2 * x], acc[3][2 * x + 1]));
       }
-      auto add = [&](uint32_t u, float p, float q) {
-        return pack_bf16x2(fmaf(scale, p, __uint_as_float(u << 16)), fmaf(scale, q, __uint_as_float(u & 0xFFFF0000u)));
-      };
-      u0 = make_uint4(add(u0.x, acc[0][0], acc[0][1]), add(u0.y, acc[1][0], acc[1][1]), add(u0.z, acc[2][0], acc[2][1]), add(u0.w, acc[3][0], acc[3][1]));
-      u1 = make_uint4(add(u1.x, acc[0][2], acc[0][3]), add(u1.y, acc[1][2], acc[1][3]), add(u1.z, acc[2][2], acc[2][3]), add(u1.w, acc[3][2], acc[3][3]));
+      if (on0 && col < a.N) *reinterpret_cast<uint4*>(o0 + col) = u[d][0];
+      if (on1 && col < a.N) *reinterpret_cast<uint4*>(o1 + col) = u[d][1];
+      if (gb + kDeep < kGroups) fetch(gb + kDeep + d, u[d]);
     }
-    if (in0) *reinterpret_cast<uint4*>(o0 + col) = u0;
-    if (in1) *reinterpret_cast<uint4*>(o1 + col) = u1;
   }
 }
 
@@ -367,18 +438,18 @@ __device__ __forceinline__ uint4 first_of(uint4 w, int left) {
 }
 
 template <int NR>
-__global__ void __launch_bounds__(kThreads) lora_few_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, NR <= 8 ? 2 : 1) lora_few_kernel(const Args a) {
   using C = FewCfg<NR>;
   constexpr int kMT = C::kMT, kTF = C::kTF, kRp = C::kRp, kWarps = C::kWarps;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int counts[1025];
-  __shared__ short bins[kFewTokens], places[kFewTokens];
+  __shared__ short counts[kWarps][1026];
+  __shared__ int warp_heads[kWarps];
   __shared__ int tokens[kTF];
   __shared__ int tile_bin, tile_base, tile_count;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2, t4 = lane & 3;
   const int cta = blockIdx.x % kCluster, q = blockIdx.x / kCluster;
   pdl_launch_dependents();
-  for (int e = tid; e <= a.n; e += kThreads) counts[e] = 0;
+  for (int e = lane; e <= a.n; e += 32) counts[warp][e] = 0;
   if (tid < kTF) tokens[tid] = -1;
   if (tid == 0) {
     tile_bin = -1;
@@ -388,40 +459,58 @@ __global__ void __launch_bounds__(kThreads) lora_few_kernel(const Args a) {
   pdl_wait();
 
   // ---- the tile: tokens are numbered within their adapter; every kTF-th begins one ----
-  if (warp == 0) {
-    int heads = 0;
-    for (int t0 = 0; t0 < a.T; t0 += 32) {
-      const int t = t0 + lane;
-      const bool on = t < a.T;
-      const int bin = on ? bin_of(a, t) : -1;
-      if (on && bin == a.n && blockIdx.x == 0 && a.err && __ldg(a.adapter + t) != -1) atomicOr(a.err, MNW_DEVERR_BAD_ADAPTER);
-      const uint32_t same = __match_any_sync(0xffffffffu, bin), below = same & ((1u << lane) - 1u);
-      const int place = (on ? counts[bin] : 0) + __popc(below);
-      __syncwarp();
-      if (on && below == 0) counts[bin] = place + __popc(same);
-      if (on) {
-        bins[t] = static_cast<short>(bin);
-        places[t] = static_cast<short>(place);
-      }
-      const bool head = on && place % kTF == 0;
-      const uint32_t hm = __ballot_sync(0xffffffffu, head);
-      if (head && heads + __popc(hm & ((1u << lane) - 1u)) == q) {
-        tile_bin = bin;
-        tile_base = place;
-      }
-      heads += __popc(hm);
-      __syncwarp();
+  // A warp numbers its share of the tokens by counts of its own, to which those of the warps before are added.
+  const int share = (a.T + kThreads - 1) / kThreads * 32;
+  constexpr int kMost = kFewTokens / kThreads;  // tokens of a lane
+  int bin_t[kMost], place_t[kMost];
+#pragma unroll
+  for (int i = 0; i < kMost; ++i) {
+    const int t = warp * share + i * 32 + lane;
+    const bool on = i * 32 < share && t < a.T;
+    bin_t[i] = on ? bin_of(a, t) : -1;
+    if (on && bin_t[i] == a.n && blockIdx.x == 0 && a.err && __ldg(a.adapter + t) != -1) atomicOr(a.err, MNW_DEVERR_BAD_ADAPTER);
+  }
+#pragma unroll
+  for (int i = 0; i < kMost; ++i) {
+    const bool on = bin_t[i] >= 0;
+    const uint32_t same = __match_any_sync(0xffffffffu, bin_t[i]), below = same & ((1u << lane) - 1u);
+    place_t[i] = on ? counts[warp][bin_t[i]] + __popc(below) : 1;
+    __syncwarp();
+    if (on && below == 0) counts[warp][bin_t[i]] = static_cast<short>(place_t[i] + __popc(same));
+    __syncwarp();
+  }
+  __syncthreads();
+  int heads = 0;
+#pragma unroll
+  for (int i = 0; i < kMost; ++i) {
+    if (bin_t[i] >= 0)
+      for (int w = 0; w < warp; ++w) place_t[i] += counts[w][bin_t[i]];
+    heads += __popc(__ballot_sync(0xffffffffu, bin_t[i] >= 0 && place_t[i] % kTF == 0));
+  }
+  if (lane == 0) warp_heads[warp] = heads;
+  __syncthreads();
+  heads = 0;
+  for (int w = 0; w < warp; ++w) heads += warp_heads[w];
+#pragma unroll
+  for (int i = 0; i < kMost; ++i) {
+    const bool head = bin_t[i] >= 0 && place_t[i] % kTF == 0;
+    const uint32_t hm = __ballot_sync(0xffffffffu, head);
+    if (head && heads + __popc(hm & ((1u << lane) - 1u)) == q) {
+      tile_bin = bin_t[i];
+      tile_base = place_t[i];
     }
+    heads += __popc(hm);
   }
   __syncthreads();
   const int bin = tile_bin;
   if (bin < 0) return;  // (the whole cluster)
   const bool none = bin == a.n;
   if (none && a.out == a.y) return;
-  for (int t = tid; t < a.T; t += kThreads) {
-    const int r = places[t] - tile_base;
-    if (bins[t] == bin && static_cast<unsigned>(r) < static_cast<unsigned>(kTF)) {
-      tokens[r] = t;
+#pragma unroll
+  for (int i = 0; i < kMost; ++i) {
+    const int r = place_t[i] - tile_base;
+    if (bin_t[i] == bin && static_cast<unsigned>(r) < static_cast<unsigned>(kTF)) {
+      tokens[r] = warp * share + i * 32 + lane;
       atomicAdd(&tile_count, 1);
     }
   }
