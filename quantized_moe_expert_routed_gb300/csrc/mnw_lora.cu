@@ -12,6 +12,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <climits>
 
 #include "mnw_convert.cuh"
 #include "mnw_internal.h"
@@ -29,6 +30,7 @@ struct Args {
   const int32_t* adapter;  // [T]
   int n, R, T, H, N;
   int splits;              // of H in the first product
+  int col_blocks;          // blocks of columns of a CTA of the second
   // workspace
   int32_t* starts;   // [n + 2] first place of each adapter's tokens in `order`, of those without one, and T
   int32_t* order;    // [T] tokens grouped by adapter
@@ -50,73 +52,69 @@ __device__ __forceinline__ int rank_of(const Args& a, int i) {
 }
 
 // ---- grouping: CTA e lists the tokens of adapter e (e = n: of none) ----
-// A thread looks at kRun neighbouring tokens and remembers which are the adapter's.
-constexpr int kGroupThreads = 1024, kRun = 16;
+constexpr int kGroupThreads = 1024, kRun = 16;  // tokens of a thread at a time
 __global__ void __launch_bounds__(kGroupThreads) lora_group_kernel(const Args a) {
   constexpr int kWarps = kGroupThreads / 32;
-  __shared__ int sums[2][kWarps];
-  __shared__ int total[2];
+  __shared__ int sums[kRun][kWarps + 1], befores[kWarps], totals[kRun];
   pdl_wait();
   pdl_launch_dependents();
   const int e = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // Tokens of lower numbers come first; with more tokens than the threads hold at a time, they are counted beforehand.
-  int at = 0, mine_all = 0;
-  for (int pass = a.T <= kGroupThreads * kRun ? 1 : 0; pass < 2; ++pass) {
+  // Adapters of lower numbers come first; with more tokens than the threads take at a time, theirs are counted beforehand.
+  const bool once = a.T <= kGroupThreads * kRun;
+  int start = 0, done = 0;
+  for (int pass = once ? 1 : 0; pass < 2; ++pass) {
     for (int t0 = 0; t0 < a.T; t0 += kGroupThreads * kRun) {
-      const int first = t0 + tid * kRun;
-      uint32_t bits = 0;
-      int before = 0;
+      int id[kRun];
 #pragma unroll
       for (int i = 0; i < kRun; ++i) {
-        const int t = first + i;
-        if (t >= a.T) break;
-        const int id = __ldg(a.adapter + t), bin = static_cast<unsigned>(id) < static_cast<unsigned>(a.n) ? id : a.n;
-        bits |= (bin == e ? 1u : 0u) << i;
-        before += bin < e ? 1 : 0;
-        if (e == a.n && pass == 1 && bin == a.n && id != -1 && a.err) atomicOr(a.err, MNW_DEVERR_BAD_ADAPTER);
+        const int t = t0 + i * kGroupThreads + tid;
+        id[i] = t < a.T ? __ldg(a.adapter + t) : INT_MAX;
       }
-      const int mine = __popc(bits);
-      int incl = mine;
+      uint32_t bits = 0;  // which of this thread's tokens are the adapter's
+      int before = 0, warp_sum = 0;
+      __syncthreads();  // the sums before are read
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, incl, d);
-        if (lane >= d) incl += o;
+      for (int i = 0; i < kRun; ++i) {
+        const bool on = t0 + i * kGroupThreads + tid < a.T;
+        const int bin = static_cast<unsigned>(id[i]) < static_cast<unsigned>(a.n) ? id[i] : a.n;
+        const bool is = on && bin == e;
+        bits |= (is ? 1u : 0u) << i;
+        before += on && bin < e ? 1 : 0;
+        if (is && e == a.n && pass == 1 && id[i] != -1 && a.err) atomicOr(a.err, MNW_DEVERR_BAD_ADAPTER);
+        const int c = __popc(__ballot_sync(0xffffffffu, is));
+        if (lane == i) warp_sum = c;
       }
       before = __reduce_add_sync(0xffffffffu, before);
-      __syncthreads();  // the sums before are read
-      if (lane == 31) {
-        sums[0][warp] = incl;
-        sums[1][warp] = before;
-      }
+      if (lane < kRun) sums[lane][warp] = warp_sum;
+      if (lane == 0) befores[warp] = before;
       __syncthreads();
-      if (warp == 0) {
-        const int m = sums[0][lane];
-        int mi = m;
+      if (warp < kRun) {  // a warp per row of sums
+        const int m = sums[warp][lane];
+        int incl = m;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-          const int o = __shfl_up_sync(0xffffffffu, mi, d);
-          if (lane >= d) mi += o;
+          const int o = __shfl_up_sync(0xffffffffu, incl, d);
+          if (lane >= d) incl += o;
         }
-        const int b = __reduce_add_sync(0xffffffffu, sums[1][lane]);
-        sums[0][lane] = mi - m;
-        if (lane == 31) {
-          total[0] = mi;
-          total[1] = b;
-        }
+        sums[warp][lane] = incl - m;
+        if (lane == 31) totals[warp] = incl;
       }
       __syncthreads();
-      if (pass == 0 || a.T <= kGroupThreads * kRun) at += total[1];
+      if (pass == 0 || once)
+        for (int w = 0; w < kWarps; ++w) start += befores[w];
       if (pass == 1) {
-        int to = at + mine_all + sums[0][warp] + incl - mine;
 #pragma unroll
-        for (int i = 0; i < kRun; ++i)
-          if (bits >> i & 1) a.order[to++] = first + i;
-        mine_all += total[0];
+        for (int i = 0; i < kRun; ++i) {
+          const bool is = bits >> i & 1;
+          const uint32_t m = __ballot_sync(0xffffffffu, is);
+          if (is) a.order[start + done + sums[i][warp] + __popc(m & ((1u << lane) - 1u))] = t0 + i * kGroupThreads + tid;
+          done += totals[i];
+        }
       }
     }
   }
   if (tid == 0) {
-    a.starts[e] = at;
+    a.starts[e] = start;
     if (e == a.n) a.starts[e + 1] = a.T;
   }
 }
@@ -161,7 +159,7 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
 // own that both operands share.  The halves' sums meet in shared memory at the end.
 template <int NR>
 struct ShrinkCfg {
-  static constexpr int kStages = 3;
+  static constexpr int kStages = NR <= 8 ? 4 : 3;
   static constexpr int kXBytes = kTT * 128, kABytes = NR * 8 * 128, kStageBytes = kXBytes + kABytes;
   static constexpr int kSmem = kStages * kStageBytes;
   static constexpr int kPad = NR * 8 + 4;  // floats of a token where the halves meet
@@ -277,14 +275,15 @@ __global__ void __launch_bounds__(kThreads, NR <= 8 ? 2 : 1) lora_shrink_kernel(
   }
 }
 
-// ---- out = y + s B v: a tile of tokens and kCols columns ----
+// ---- out = y + s B v: a tile of tokens and some columns ----
 // A warp takes 16 tokens and, at a time, 32 columns in an order that gives a lane 8 neighbouring ones (column 8 t + 2 j +
 // 0, 1 as columns 2 t + 0, 1 of instruction j), so that y and out move in 16-byte pieces.
-constexpr int kCols = 256;
+// B arrives kCols columns at a time, two such blocks under way; a CTA takes several, so that v is read for all of them.
 template <int NR>
 struct ExpandCfg {
-  static constexpr int kRow = NR * 16;  // bytes of a row of B
-  static constexpr int kSmem = kCols * kRow;
+  static constexpr int kCols = NR <= 8 ? 256 : 128;
+  static constexpr int kBytes = kCols * NR * 16;  // of a block of B
+  static constexpr int kSmem = 2 * kBytes;
 };
 // 16-byte chunk c of column n: rows of 128 bytes or more exchange halves of 128 bytes by the row
 template <int NR>
@@ -293,6 +292,8 @@ __device__ __forceinline__ uint32_t b_at(int n, int c) {
 }
 template <int NR>
 __global__ void __launch_bounds__(kThreads, NR <= 4 ? 3 : 2) lora_expand_kernel(const Args a) {
+  using C = ExpandCfg<NR>;
+  constexpr int kCols = C::kCols;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Tile tile_sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2, t4 = lane & 3;
@@ -304,18 +305,23 @@ __global__ void __launch_bounds__(kThreads, NR <= 4 ? 3 : 2) lora_expand_kernel(
     pdl_wait();  // (the kernels behind this one count on the ones ahead of it)
     return;
   }
-  const int col0 = blockIdx.y * kCols;
+  const int col0 = blockIdx.y * a.col_blocks * kCols;
+  const int blocks = min(a.col_blocks, (a.N - col0 + kCols - 1) / kCols);
   const int rank = none ? 0 : rank_of(a, tl.bin);
   const uint32_t sbase = smem_u32(smem);
-  if (!none) {
-    const __nv_bfloat16* wb = a.b + static_cast<long long>(tl.bin) * a.N * a.R;
-    for (int i = tid; i < kCols * NR; i += kThreads) {
-      const int n = i / NR, c = i % NR, left = min(16, 2 * (rank - c * 8));  // (a rank need not be a multiple of 8)
-      const bool on = col0 + n < a.N && left > 0;
-      cp_async16(sbase + b_at<NR>(n, c), on ? wb + static_cast<long long>(col0 + n) * a.R + c * 8 : wb, on ? left : 0);
+  auto load_b = [&](int block) {
+    if (!none && block < blocks) {
+      const __nv_bfloat16* wb = a.b + static_cast<long long>(tl.bin) * a.N * a.R;
+      const uint32_t to = sbase + (block & 1) * C::kBytes;
+      for (int i = tid; i < kCols * NR; i += kThreads) {
+        const int n = i / NR, c = i % NR, col = col0 + block * kCols + n, left = min(16, 2 * (rank - c * 8));
+        const bool on = col < a.N && left > 0;  // (a rank need not be a multiple of 8)
+        cp_async16(to + b_at<NR>(n, c), on ? wb + static_cast<long long>(col) * a.R + c * 8 : wb, on ? left : 0);
+      }
     }
-  }
-  cp_commit();
+    cp_commit();
+  };
+  load_b(0);
   const int r0 = warp * 16 + g8;
   const bool on0 = r0 < tl.count, on1 = r0 + 8 < tl.count;
   const long long tok0 = on0 ? __ldcg(a.order + tl.first + r0) : 0, tok1 = on1 ? __ldcg(a.order + tl.first + r0 + 8) : 0;
@@ -324,6 +330,7 @@ __global__ void __launch_bounds__(kThreads, NR <= 4 ? 3 : 2) lora_expand_kernel(
   __nv_bfloat16 *o0 = a.out + tok0 * a.out_stride, *o1 = a.out + tok1 * a.out_stride;
   // y is asked for kDeep groups of 32 columns ahead
   constexpr int kDeep = 4, kGroups = kCols / 32;
+  const int groups = blocks * kGroups;
   uint4 u[kDeep][2];
   auto fetch = [&](int g, uint4 (&w)[2]) {
     const int col = col0 + g * 32 + 8 * t4;
@@ -359,11 +366,15 @@ __global__ void __launch_bounds__(kThreads, NR <= 4 ? 3 : 2) lora_expand_kernel(
       lo[s][x] = pack_bf16x2(f.x - __uint_as_float(h0 << 16), f.y - __uint_as_float(h0 & 0xFFFF0000u));
       lo[s][2 + x] = pack_bf16x2(f.z - __uint_as_float(h1 << 16), f.w - __uint_as_float(h1 & 0xFFFF0000u));
     }
-  cp_wait<0>();
-  __syncthreads();
-  if (warp * 16 >= tl.count) return;
 #pragma unroll 1
-  for (int gb = 0; gb < kGroups; gb += kDeep) {
+  for (int gb = 0; gb < groups; gb += kDeep) {
+    if (gb % kGroups == 0) {  // the next block of B is there, the one before is read
+      cp_wait<0>();
+      __syncthreads();
+      load_b(gb / kGroups + 1);
+    }
+    if (warp * 16 >= tl.count) continue;
+    const uint8_t* const bs = smem + (gb / kGroups & 1) * C::kBytes;
 #pragma unroll
     for (int d = 0; d < kDeep; ++d) {
       const int n0 = (gb + d) * 32, col = col0 + n0 + 8 * t4;
@@ -373,15 +384,15 @@ __global__ void __launch_bounds__(kThreads, NR <= 4 ? 3 : 2) lora_expand_kernel(
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
-          const int n = n0 + 8 * (g8 >> 1) + 2 * j + (g8 & 1);
+          const int n = n0 % kCols + 8 * (g8 >> 1) + 2 * j + (g8 & 1);
 #pragma unroll
           for (int s = 0; s < kKS; s += 2) {
             if constexpr (NR == 2) {
-              const uint2 w = *reinterpret_cast<const uint2*>(smem + b_at<NR>(n, t4 >> 1) + 8 * (t4 & 1));
+              const uint2 w = *reinterpret_cast<const uint2*>(bs + b_at<NR>(n, t4 >> 1) + 8 * (t4 & 1));
               mma_bf16(acc[j], hi[0][0], hi[0][1], hi[0][2], hi[0][3], w.x, w.y);
               mma_bf16(acc[j], lo[0][0], lo[0][1], lo[0][2], lo[0][3], w.x, w.y);
             } else {
-              const uint4 w = *reinterpret_cast<const uint4*>(smem + b_at<NR>(n, 2 * s + t4));
+              const uint4 w = *reinterpret_cast<const uint4*>(bs + b_at<NR>(n, 2 * s + t4));
               mma_bf16(acc[j], hi[s][0], hi[s][1], hi[s][2], hi[s][3], w.x, w.y);
               mma_bf16(acc[j], lo[s][0], lo[s][1], lo[s][2], lo[s][3], w.x, w.y);
               mma_bf16(acc[j], hi[s + 1][0], hi[s + 1][1], hi[s + 1][2], hi[s + 1][3], w.z, w.w);
@@ -399,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, NR <= 4 ? 3 : 2) lora_expand_kernel(
       }
       if (on0 && col < a.N) *reinterpret_cast<uint4*>(o0 + col) = u[d][0];
       if (on1 && col < a.N) *reinterpret_cast<uint4*>(o1 + col) = u[d][1];
-      if (gb + kDeep < kGroups) fetch(gb + kDeep + d, u[d]);
+      if (gb + kDeep < groups) fetch(gb + kDeep + d, u[d]);
     }
   }
 }
@@ -772,9 +783,12 @@ int launch(Args& a, uint8_t* ws, cudaStream_t st) {
     attrs_done(attr, bit);
   }
   const unsigned tiles = tile_numbers(a.T, a.n);
+  const int blocks = (a.N + ExpandCfg<NR>::kCols - 1) / ExpandCfg<NR>::kCols;
+  // as many as leave each SM two CTAs
+  a.col_blocks = std::max(1, std::min(blocks, static_cast<int>(static_cast<long long>((a.T + kTT - 1) / kTT) * blocks / (2 * current_sm_count()))));
   if (launch_pdl(lora_group_kernel, dim3(a.n + 1), dim3(kGroupThreads), 0, st, a) != cudaSuccess ||
       launch_pdl(shrink, dim3(tiles, a.splits), dim3(kThreads), ShrinkCfg<NR>::kSmem, st, a) != cudaSuccess ||
-      launch_pdl(expand, dim3(tiles, (a.N + kCols - 1) / kCols), dim3(kThreads), ExpandCfg<NR>::kSmem, st, a) != cudaSuccess)
+      launch_pdl(expand, dim3(tiles, (blocks + a.col_blocks - 1) / a.col_blocks), dim3(kThreads), ExpandCfg<NR>::kSmem, st, a) != cudaSuccess)
     return MNW_E_CUDA;
   return MNW_OK;
 }

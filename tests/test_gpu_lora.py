@@ -54,7 +54,7 @@ SHAPES = [
     (2, 64, 40, 16, 1000, "random"), (3, 1000, 264, 24, 2, "random"), (16, 512, 512, 16, 4, "random"), (33, 2056, 1000, 40, 5, "runs"),
     (64, 4096, 2048, 16, 24, "random"), (127, 256, 128, 32, 2, "one"), (128, 264, 136, 64, 1, "one"), (129, 72, 520, 72, 1, "one"),
     (200, 1024, 1280, 128, 7, "runs"), (256, 512, 256, 8, 64, "random"), (257, 520, 248, 56, 3, "random"), (700, 640, 768, 32, 12, "runs"),
-    (1024, 512, 512, 16, 16, "random"), (1025, 512, 512, 64, 16, "runs"), (3000, 256, 264, 16, 1024, "random"), (2500, 1536, 1000, 64, 4, "runs"),
+    (1024, 512, 512, 16, 16, "random"), (1025, 512, 512, 64, 16, "runs"), (3000, 256, 264, 16, 1024, "random"), (2500, 1536, 1000, 64, 4, "runs"), (40000, 64, 40, 8, 5, "random"), (600, 128, 2600, 128, 3, "random"),
 ]
 
 
