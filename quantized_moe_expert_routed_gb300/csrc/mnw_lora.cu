@@ -30,7 +30,7 @@ struct Args {
   const int32_t* adapter;  // [T]
   int n, R, T, H, N;
   int splits;              // of H in the first product
-  int col_blocks;          // blocks of columns of a CTA of the second
+  int spans;               // shares of N in the second
   // workspace
   int32_t* starts;   // [n + 2] first place of each adapter's tokens in `order`, of those without one, and T
   int32_t* order;    // [T] tokens grouped by adapter
@@ -152,151 +152,164 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// ---- v = A x: a tile of tokens and a share of H ----
-// Steps of 64 elements of H arrive by cp.async, as 128-byte rows that exchange halves by the row (the lanes of a load read
-// 64 bytes of two rows).  A warp takes 32 tokens, all ranks and one half of each step, so that a row of A is read from
-// shared memory once for 32 tokens.  Of 32 elements, lane t of a fragment takes chunk t: two k steps, in an order of its
-// own that both operands share.  The halves' sums meet in shared memory at the end.
+// ---- v = A x on tcgen05: a tile of tokens and a share of H ----
+// Tokens are the rows of the product, ranks its columns.  Steps of 64 elements of H arrive by cp.async in the operands'
+// 128-byte swizzle; one thread issues the instructions, and the sums lie in tensor memory until the end.  The warps do
+// nothing but copy.
 template <int NR>
 struct ShrinkCfg {
-  static constexpr int kStages = NR <= 8 ? 4 : 3;
+  static constexpr int kStages = 4;
   static constexpr int kXBytes = kTT * 128, kABytes = NR * 8 * 128, kStageBytes = kXBytes + kABytes;
-  static constexpr int kSmem = kStages * kStageBytes;
-  static constexpr int kPad = NR * 8 + 4;  // floats of a token where the halves meet
-  static_assert(kTT * kPad * 4 <= kSmem);
+  static constexpr int kSmem = kStages * kStageBytes + 1024;
+  static constexpr int kTmemCols = NR * 8 < 32 ? 32 : NR * 8;
 };
-__device__ __forceinline__ uint32_t step_at(int r, int c) { return static_cast<uint32_t>(r * 128 + ((c ^ ((r & 1) << 2)) << 4)); }
 template <int NR>
 __global__ void __launch_bounds__(kThreads, NR <= 8 ? 2 : 1) lora_shrink_kernel(const Args a) {
   using C = ShrinkCfg<NR>;
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ Tile tile_sh;
   __shared__ int tokens[kTT];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2, t4 = lane & 3;
+  __shared__ uint64_t empty[C::kStages], done;
+  __shared__ uint32_t tmem_base;
+  __shared__ int abort_flag;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_wait();
   // The kernel behind this one begins with inputs that are complete by now, the grouping among them; only v it waits for.
   pdl_launch_dependents();
   const Tile tl = find_tile(a, blockIdx.x, &tile_sh);
   if (tl.count == 0 || tl.bin == a.n) return;
   if (tid < kTT) tokens[tid] = tid < tl.count ? a.order[tl.first + tid] : -1;
+  if (tid == 0) {
+    for (int i = 0; i < C::kStages; ++i) mbar_init(&empty[i], 1);
+    mbar_init(&done, 1);
+    abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(&tmem_base, C::kTmemCols);
+    tmem_relinquish();
+  }
   const int rank = rank_of(a, tl.bin);
+  tc_fence_before();
   __syncthreads();
-  const uint32_t sbase = smem_u32(smem);
+  tc_fence_after();
+  const uint32_t tmem = tmem_base;
+  const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const int steps_all = (a.H + 63) / 64;
   const int s0 = static_cast<int>(static_cast<long long>(steps_all) * blockIdx.y / a.splits);
   const int s1 = static_cast<int>(static_cast<long long>(steps_all) * (blockIdx.y + 1) / a.splits);
   const __nv_bfloat16* wa = a.a + static_cast<long long>(tl.bin) * a.R * a.H;
   const int lr = tid >> 3, lc = tid & 7;  // row (of 32) and chunk that this thread copies
-  int tok[kTT / 32];
+  const __nv_bfloat16* xp[kTT / 32];
 #pragma unroll
-  for (int i = 0; i < kTT / 32; ++i) tok[i] = tokens[i * 32 + lr];
+  for (int i = 0; i < kTT / 32; ++i) {
+    const int t = tokens[i * 32 + lr];
+    xp[i] = t >= 0 ? a.x + t * a.x_stride + lc * 8 : nullptr;
+  }
   auto load = [&](int s, int slot) {
     const uint32_t st = sbase + slot * C::kStageBytes;
-    const int k = s * 64 + lc * 8;
+    const int k = s * 64;
+    const bool in = k + lc * 8 < a.H;
 #pragma unroll
     for (int i = 0; i < kTT / 32; ++i) {
-      const bool on = tok[i] >= 0 && k < a.H;
-      cp_async16(st + step_at(i * 32 + lr, lc), on ? a.x + tok[i] * a.x_stride + k : a.x, on ? 16u : 0u);
+      const bool on = in && xp[i];
+      cp_async16(sw128(st, i * 32 + lr, lc), on ? xp[i] + k : a.x, on ? 16u : 0u);
     }
 #pragma unroll
     for (int i = 0; i < (NR * 8 + 31) / 32; ++i) {
       const int r = i * 32 + lr;
-      const bool on = r < rank && k < a.H;
+      const bool on = in && r < rank;
       if (NR * 8 >= 32 || r < NR * 8)
-        cp_async16(st + C::kXBytes + step_at(r, lc), on ? wa + static_cast<long long>(r) * a.H + k : wa, on ? 16u : 0u);
+        cp_async16(sw128(st + C::kXBytes, r, lc), on ? wa + static_cast<long long>(r) * a.H + k + lc * 8 : wa, on ? 16u : 0u);
     }
   };
-  const int part = warp & 3, half = warp >> 2;
-  float acc[2][NR][4];
-#pragma unroll
-  for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-    for (int i = 0; i < NR; ++i) acc[mt][i][0] = acc[mt][i][1] = acc[mt][i][2] = acc[mt][i][3] = 0.f;
 #pragma unroll
   for (int i = 0; i < C::kStages - 1; ++i) {
     if (s0 + i < s1) load(s0 + i, i);
     cp_commit();
   }
-  for (int s = s0, slot = 0; s < s1; ++s) {
+  constexpr uint32_t idesc = idesc_f16(kTT, NR * 8, true);
+  int slot = 0, use = 0;  // slot of step s, and how often the ring has gone round
+  for (int s = s0; s < s1; ++s) {
     cp_wait<C::kStages - 2>();
+    fence_proxy_async_smem();
     __syncthreads();
-    {
-      int ns = slot + C::kStages - 1;
-      if (ns >= C::kStages) ns -= C::kStages;
-      if (s + C::kStages - 1 < s1) load(s + C::kStages - 1, ns);
-      cp_commit();
-    }
-    if (part * 32 < tl.count) {
+    if (tid == 0) {
+      tc_fence_after();
       const uint32_t st = sbase + slot * C::kStageBytes;
-      const int c = half * 4 + t4;
-      uint4 xw[2][2];
+      uint64_t da = sdesc_sw128(st), db = sdesc_sw128(st + C::kXBytes);
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
+      for (int kk = 0; kk < 4; ++kk, da += 2, db += 2) mma_ss(tmem, da, db, idesc, s > s0 || kk > 0);
+      mma_commit(&empty[slot]);
+    }
+    // the slot of the step before, once its product is complete
+    const int ns = slot == 0 ? C::kStages - 1 : slot - 1;
+    if (s + C::kStages - 1 < s1) {
+      if (s > s0) bounded_wait(&empty[ns], (slot == 0 ? use - 1 : use) & 1, &abort_flag, a.err);
+      load(s + C::kStages - 1, ns);
+    }
+    cp_commit();
+    if (++slot == C::kStages) {
+      slot = 0;
+      ++use;
+    }
+  }
+  if (tid == 0) mma_commit(&done);
+  bounded_wait(&done, 0, &abort_flag, a.err);
+  __syncwarp();
+  tc_fence_after();
+  // a thread: one token, its share of the ranks
+  float* v = a.v + (static_cast<long long>(blockIdx.y) * a.T + tl.first) * (NR * 8);
+  const int r = (warp & 3) * 32 + lane;
+  constexpr int kShare = NR >= 4 ? NR * 4 : 16;  // columns of a warp
+  if (NR >= 4 || warp < 4) {
 #pragma unroll
-        for (int x = 0; x < 2; ++x) xw[mt][x] = lds128(st + step_at(part * 32 + 16 * mt + 8 * x + g8, c));
+    for (int c = 0; c < kShare; c += 16) {
+      const int col = (NR >= 4 ? (warp >> 2) * kShare : 0) + c;
+      uint32_t o[16];
+      tmem_ld16(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + col, o);
+      tmem_wait_ld();
+      if (r < tl.count) {
 #pragma unroll
-      for (int i = 0; i < NR; ++i) {
-        const uint4 w = lds128(st + C::kXBytes + step_at(i * 8 + g8, c));
-#pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
-          mma_bf16(acc[mt][i], xw[mt][0].x, xw[mt][1].x, xw[mt][0].y, xw[mt][1].y, w.x, w.y);
-          mma_bf16(acc[mt][i], xw[mt][0].z, xw[mt][1].z, xw[mt][0].w, xw[mt][1].w, w.z, w.w);
-        }
+        for (int e = 0; e < 16; e += 4)
+          __stcg(reinterpret_cast<uint4*>(v + static_cast<long long>(r) * (NR * 8) + col + e), make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]));
       }
     }
-    if (++slot == C::kStages) slot = 0;
   }
   cp_wait<0>();
+  tc_fence_before();
   __syncthreads();
-  float* const meet = reinterpret_cast<float*>(smem);
-  float* v = a.v + (static_cast<long long>(blockIdx.y) * a.T + tl.first) * (NR * 8);
-#pragma unroll
-  for (int pass = 0; pass < 2; ++pass) {
-    if (half != pass) {  // first the upper half leaves its sums, then the lower adds them
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int r = part * 32 + 16 * mt + 8 * x + g8;
-#pragma unroll
-          for (int i = 0; i < NR; ++i) {
-            float2* m = reinterpret_cast<float2*>(meet + r * C::kPad + i * 8 + 2 * t4);
-            float2 z = make_float2(acc[mt][i][2 * x], acc[mt][i][2 * x + 1]);
-            if (pass == 0) {
-              *m = z;
-            } else if (r < tl.count) {
-              const float2 o = *m;
-              __stcg(reinterpret_cast<float2*>(v + static_cast<long long>(r) * (NR * 8) + i * 8 + 2 * t4), make_float2(z.x + o.x, z.y + o.y));
-            }
-          }
-        }
-    }
-    __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
   }
 }
 
-// ---- out = y + s B v: a tile of tokens and some columns ----
-// A warp takes 16 tokens and, at a time, 32 columns in an order that gives a lane 8 neighbouring ones (column 8 t + 2 j +
-// 0, 1 as columns 2 t + 0, 1 of instruction j), so that y and out move in 16-byte pieces.
-// B arrives kCols columns at a time, two such blocks under way; a CTA takes several, so that v is read for all of them.
+// ---- out = y + s B v on tcgen05: a tile of tokens and some columns, a block of kCols at a time ----
+// y comes by cp.async, whole rows of a block, into shared memory, where the product is added, and leaves from there in
+// rows; v lies there as two operands, its two terms.  While one block is worked on, the next one's y and B are under way.
+// (Rows of 384 bytes as bulk copies, in and out: 59 us for the case below; so: BULK_TIME.)
 template <int NR>
 struct ExpandCfg {
-  static constexpr int kCols = NR <= 8 ? 256 : 128;
-  static constexpr int kBytes = kCols * NR * 16;  // of a block of B
-  static constexpr int kSmem = 2 * kBytes;
+  static constexpr int kPieces = NR <= 8 ? 1 : 2;         // of 64 ranks: 128-byte rows of an operand
+  static constexpr int kCols = kPieces == 1 ? 192 : 128;  // what shared memory holds
+  static constexpr uint32_t kPieceA = kTT * 128, kPieceB = kCols * 128;
+  static constexpr uint32_t kOffB = 2 * kPieces * kPieceA, kBytesB = kPieces * kPieceB;
+  static constexpr uint32_t kRowY = kCols * 2 + 16;       // so that a column's rows fall into different banks
+  static constexpr uint32_t kOffY = kOffB + 2 * kBytesB, kBytesY = kTT * kRowY;
+  static constexpr uint32_t kSmem = kOffY + 2 * kBytesY + 1024;
 };
-// 16-byte chunk c of column n: rows of 128 bytes or more exchange halves of 128 bytes by the row
 template <int NR>
-__device__ __forceinline__ uint32_t b_at(int n, int c) {
-  return static_cast<uint32_t>(n * (NR * 16) + ((NR >= 8 ? c ^ ((n & 1) << 2) : c) << 4));
-}
-template <int NR>
-__global__ void __launch_bounds__(kThreads, NR <= 4 ? 3 : 2) lora_expand_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, 1) lora_expand_kernel(const Args a) {
   using C = ExpandCfg<NR>;
   constexpr int kCols = C::kCols;
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ Tile tile_sh;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2, t4 = lane & 3;
+  __shared__ uint64_t d_full[2];
+  __shared__ int tokens[kTT];
+  __shared__ uint32_t tmem_base;
+  __shared__ int abort_flag;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // Everything but v was complete before the kernel ahead let this one start; it is read past L1, which may hold lines of
   // before.
   const Tile tl = find_tile(a, blockIdx.x, &tile_sh);
@@ -305,55 +318,73 @@ __global__ void __launch_bounds__(kThreads, NR <= 4 ? 3 : 2) lora_expand_kernel(
     pdl_wait();  // (the kernels behind this one count on the ones ahead of it)
     return;
   }
-  const int col0 = blockIdx.y * a.col_blocks * kCols;
-  const int blocks = min(a.col_blocks, (a.N - col0 + kCols - 1) / kCols);
-  const int rank = none ? 0 : rank_of(a, tl.bin);
-  const uint32_t sbase = smem_u32(smem);
-  auto load_b = [&](int block) {
-    if (!none && block < blocks) {
-      const __nv_bfloat16* wb = a.b + static_cast<long long>(tl.bin) * a.N * a.R;
-      const uint32_t to = sbase + (block & 1) * C::kBytes;
-      for (int i = tid; i < kCols * NR; i += kThreads) {
-        const int n = i / NR, c = i % NR, col = col0 + block * kCols + n, left = min(16, 2 * (rank - c * 8));
-        const bool on = col < a.N && left > 0;  // (a rank need not be a multiple of 8)
-        cp_async16(to + b_at<NR>(n, c), on ? wb + static_cast<long long>(col) * a.R + c * 8 : wb, on ? left : 0);
-      }
+  const int blocks_all = (a.N + kCols - 1) / kCols;
+  const int b0 = static_cast<int>(static_cast<long long>(blocks_all) * blockIdx.y / a.spans);
+  const int b1 = static_cast<int>(static_cast<long long>(blocks_all) * (blockIdx.y + 1) / a.spans);
+  if (tid < kTT) tokens[tid] = tid < tl.count ? __ldcg(a.order + tl.first + tid) : 0;
+  if (none) {  // y as it is
+    pdl_wait();
+    __syncthreads();
+    const int c0 = b0 * kCols / 8, c1 = min(b1 * kCols, a.N) / 8, w = c1 - c0;
+    for (long long i = tid; i < static_cast<long long>(tl.count) * w; i += kThreads) {
+      const int r = static_cast<int>(i / w), c = c0 + static_cast<int>(i % w);
+      const long long t = tokens[r];
+      *reinterpret_cast<uint4*>(a.out + t * a.out_stride + c * 8) = __ldcg(reinterpret_cast<const uint4*>(a.y + t * a.y_stride + c * 8));
     }
-    cp_commit();
+    return;
+  }
+  uint8_t* const smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
+  const uint32_t sbase = smem_u32(smem);
+  const int rank = rank_of(a, tl.bin);
+  const __nv_bfloat16* const wb = a.b + static_cast<long long>(tl.bin) * a.N * a.R;
+  constexpr int kChunks = kCols / 8;  // of a row of a block
+  const uint32_t y_at = C::kOffY;
+  // y's rows into shared memory (in), or out's from there
+  auto rows = [&](int b, bool in) {
+    const int left = (a.N - b * kCols) / 8;  // chunks to the end
+    const uint32_t slot = y_at + ((b - b0) & 1) * C::kBytesY;
+    for (int i = tid; i < tl.count * kChunks; i += kThreads) {
+      const int r = i / kChunks, c = i % kChunks;
+      if (c >= left) continue;
+      const long long t = tokens[r], col = static_cast<long long>(b) * kCols + c * 8;
+      const uint32_t at = slot + r * C::kRowY + c * 16;
+      if (in)
+        cp_async16(sbase + at, a.y + t * a.y_stride + col, 16);
+      else
+        *reinterpret_cast<uint4*>(a.out + t * a.out_stride + col) = *reinterpret_cast<const uint4*>(smem + at);
+    }
   };
-  load_b(0);
-  const int r0 = warp * 16 + g8;
-  const bool on0 = r0 < tl.count, on1 = r0 + 8 < tl.count;
-  const long long tok0 = on0 ? __ldcg(a.order + tl.first + r0) : 0, tok1 = on1 ? __ldcg(a.order + tl.first + r0 + 8) : 0;
-  const float scale = none ? 0.f : (a.scale ? __ldcg(a.scale + tl.bin) : 1.f);
-  const __nv_bfloat16 *y0 = a.y + tok0 * a.y_stride, *y1 = a.y + tok1 * a.y_stride;
-  __nv_bfloat16 *o0 = a.out + tok0 * a.out_stride, *o1 = a.out + tok1 * a.out_stride;
-  // y is asked for kDeep groups of 32 columns ahead
-  constexpr int kDeep = 4, kGroups = kCols / 32;
-  const int groups = blocks * kGroups;
-  uint4 u[kDeep][2];
-  auto fetch = [&](int g, uint4 (&w)[2]) {
-    const int col = col0 + g * 32 + 8 * t4;
-    w[0] = w[1] = make_uint4(0, 0, 0, 0);
-    if (on0 && col < a.N) w[0] = __ldcg(reinterpret_cast<const uint4*>(y0 + col));
-    if (on1 && col < a.N) w[1] = __ldcg(reinterpret_cast<const uint4*>(y1 + col));
+  auto load_b = [&](int b) {
+    const uint32_t to = sbase + C::kOffB + ((b - b0) & 1) * C::kBytesB;
+    for (int i = tid; i < kCols * NR; i += kThreads) {
+      const int n = i / NR, c = i % NR, col = b * kCols + n, left = min(16, 2 * (rank - c * 8));  // (a rank need not be a multiple of 8)
+      const bool on = col < a.N && left > 0;
+      cp_async16(sw128(to + (c >> 3) * C::kPieceB, n, c & 7), on ? wb + static_cast<long long>(col) * a.R + c * 8 : wb, on ? left : 0);
+    }
   };
-#pragma unroll
-  for (int g = 0; g < kDeep; ++g) fetch(g, u[g]);
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) mbar_init(&d_full[i], 1);
+    abort_flag = 0;
+    fence_barrier_init();
+  }
+  load_b(b0);
+  __syncthreads();
+  rows(b0, true);
+  cp_commit();
   pdl_wait();
   pdl_launch_dependents();
-  constexpr int kKS = NR / 2;  // k steps
-  uint32_t hi[kKS][4], lo[kKS][4];
-#pragma unroll
-  for (int s = 0; s < kKS; ++s)
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      // elements 8 t + 4 (s % 2) .. + 3 of every 32, or 4 t .. + 3 of 16
-      const int e = NR == 2 ? 4 * t4 : 32 * (s >> 1) + 8 * t4 + 4 * (s & 1);
+  if (warp == 0) {  // (not before the wait: the kernel ahead may still have to allocate)
+    tmem_alloc(&tmem_base, 512);
+    tmem_relinquish();
+  }
+  {  // v's two terms: 4 ranks a thread and step, rows without a token are zeros
+    constexpr int kQ = NR * 2;  // quads of a row
+    for (int i = tid; i < kTT * kQ; i += kThreads) {
+      const int r = i / kQ, e = i % kQ * 4;
       float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-      if ((x ? on1 : on0) && !none) {
+      if (r < tl.count) {
         for (int p = 0; p < a.splits; ++p) {
-          const float4 z = __ldcg(reinterpret_cast<const float4*>(a.v + (static_cast<long long>(p) * a.T + tl.first + r0 + 8 * x) * (NR * 8) + e));
+          const float4 z = __ldcg(reinterpret_cast<const float4*>(a.v + (static_cast<long long>(p) * a.T + tl.first + r) * (NR * 8) + e));
           f.x += z.x;
           f.y += z.y;
           f.z += z.z;
@@ -361,57 +392,72 @@ __global__ void __launch_bounds__(kThreads, NR <= 4 ? 3 : 2) lora_expand_kernel(
         }
       }
       const uint32_t h0 = pack_bf16x2(f.x, f.y), h1 = pack_bf16x2(f.z, f.w);
-      hi[s][x] = h0;
-      hi[s][2 + x] = h1;
-      lo[s][x] = pack_bf16x2(f.x - __uint_as_float(h0 << 16), f.y - __uint_as_float(h0 & 0xFFFF0000u));
-      lo[s][2 + x] = pack_bf16x2(f.z - __uint_as_float(h1 << 16), f.w - __uint_as_float(h1 & 0xFFFF0000u));
+      const uint32_t l0 = pack_bf16x2(f.x - __uint_as_float(h0 << 16), f.y - __uint_as_float(h0 & 0xFFFF0000u));
+      const uint32_t l1 = pack_bf16x2(f.z - __uint_as_float(h1 << 16), f.w - __uint_as_float(h1 & 0xFFFF0000u));
+      uint8_t* to = smem + (e >> 6) * C::kPieceA + r * 128 + ((((e & 63) >> 3) ^ (r & 7)) << 4) + (e & 4) * 2;
+      *reinterpret_cast<uint2*>(to) = make_uint2(h0, h1);
+      *reinterpret_cast<uint2*>(to + C::kPieces * C::kPieceA) = make_uint2(l0, l1);
     }
+  }
+  const float scale = a.scale ? __ldcg(a.scale + tl.bin) : 1.f;
+  constexpr uint32_t idesc = idesc_f16(kTT, kCols, true);
+  const int row = (warp & 3) * 32 + lane;  // of the product, in the end
+  for (int b = b0; b < b1; ++b) {
+    const int at = (b - b0) & 1;
+    const uint32_t phase = (b - b0) >> 1 & 1;
+    cp_wait<0>();
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    const uint32_t tmem = tmem_base;
+    if (tid == 0) {
+      tc_fence_after();
+      const uint32_t bs = sbase + C::kOffB + at * C::kBytesB;
 #pragma unroll 1
-  for (int gb = 0; gb < groups; gb += kDeep) {
-    if (gb % kGroups == 0) {  // the next block of B is there, the one before is read
-      cp_wait<0>();
-      __syncthreads();
-      load_b(gb / kGroups + 1);
+      for (int term = 0; term < 2; ++term)
+#pragma unroll
+        for (int kk = 0; kk < NR / 2; ++kk)
+          mma_ss(tmem + at * kCols, sdesc_sw128(sbase + (term * C::kPieces + kk / 4) * C::kPieceA + (kk & 3) * 32),
+                 sdesc_sw128(bs + kk / 4 * C::kPieceB + (kk & 3) * 32), idesc, term > 0 || kk > 0);
+      mma_commit(&d_full[at]);
     }
-    if (warp * 16 >= tl.count) continue;
-    const uint8_t* const bs = smem + (gb / kGroups & 1) * C::kBytes;
+    if (b + 1 < b1) {
+      rows(b + 1, true);
+      load_b(b + 1);
+    }
+    cp_commit();
+    bounded_wait(&d_full[at], phase, &abort_flag, a.err);
+    __syncwarp();
+    tc_fence_after();
+    uint8_t* const mine = smem + y_at + at * C::kBytesY + row * C::kRowY + (warp >> 2) * kCols;  // (kCols / 2 columns of two bytes)
 #pragma unroll
-    for (int d = 0; d < kDeep; ++d) {
-      const int n0 = (gb + d) * 32, col = col0 + n0 + 8 * t4;
-      if (col0 + n0 >= a.N) break;
-      if (!none) {
-        float acc[4][4];
+    for (int c = 0; c < kCols / 2; c += 32) {
+      uint32_t d[32];
+      tmem_ld32(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + at * kCols + (warp >> 2) * (kCols / 2) + c, d);
+      tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
-          const int n = n0 % kCols + 8 * (g8 >> 1) + 2 * j + (g8 & 1);
-#pragma unroll
-          for (int s = 0; s < kKS; s += 2) {
-            if constexpr (NR == 2) {
-              const uint2 w = *reinterpret_cast<const uint2*>(bs + b_at<NR>(n, t4 >> 1) + 8 * (t4 & 1));
-              mma_bf16(acc[j], hi[0][0], hi[0][1], hi[0][2], hi[0][3], w.x, w.y);
-              mma_bf16(acc[j], lo[0][0], lo[0][1], lo[0][2], lo[0][3], w.x, w.y);
-            } else {
-              const uint4 w = *reinterpret_cast<const uint4*>(bs + b_at<NR>(n, 2 * s + t4));
-              mma_bf16(acc[j], hi[s][0], hi[s][1], hi[s][2], hi[s][3], w.x, w.y);
-              mma_bf16(acc[j], lo[s][0], lo[s][1], lo[s][2], lo[s][3], w.x, w.y);
-              mma_bf16(acc[j], hi[s + 1][0], hi[s + 1][1], hi[s + 1][2], hi[s + 1][3], w.z, w.w);
-              mma_bf16(acc[j], lo[s + 1][0], lo[s + 1][1], lo[s + 1][2], lo[s + 1][3], w.z, w.w);
-            }
-          }
-        }
-        auto add = [&](uint32_t w, float p, float q) {
-          return pack_bf16x2(fmaf(scale, p, __uint_as_float(w << 16)), fmaf(scale, q, __uint_as_float(w & 0xFFFF0000u)));
+      for (int e = 0; e < 32; e += 8) {
+        uint4* const p = reinterpret_cast<uint4*>(mine + (c + e) * 2);
+        uint4 u = *p;
+        auto add = [&](uint32_t w, uint32_t lo, uint32_t hi) {
+          return pack_bf16x2(fmaf(scale, __uint_as_float(lo), __uint_as_float(w << 16)),
+                             fmaf(scale, __uint_as_float(hi), __uint_as_float(w & 0xFFFF0000u)));
         };
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-          u[d][x] = make_uint4(add(u[d][x].x, acc[0][2 * x], acc[0][2 * x + 1]), add(u[d][x].y, acc[1][2 * x], acc[1][2 * x + 1]),
-                               add(u[d][x].z, acc[2][2 * x], acc[2][2 * x + 1]), add(u[d][x].w, acc[3][2 * x], acc[3][2 * x + 1]));
+        u.x = add(u.x, d[e], d[e + 1]);
+        u.y = add(u.y, d[e + 2], d[e + 3]);
+        u.z = add(u.z, d[e + 4], d[e + 5]);
+        u.w = add(u.w, d[e + 6], d[e + 7]);
+        *p = u;
       }
-      if (on0 && col < a.N) *reinterpret_cast<uint4*>(o0 + col) = u[d][0];
-      if (on1 && col < a.N) *reinterpret_cast<uint4*>(o1 + col) = u[d][1];
-      if (gb + kDeep < groups) fetch(gb + kDeep + d, u[d]);
     }
+    tc_fence_before();
+    __syncthreads();
+    rows(b, false);
+  }
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, 512);
   }
 }
 
@@ -723,6 +769,21 @@ inline int splits_of(int T, int H) {
   const int tiles = (T + kTT - 1) / kTT;
   return std::max(1, std::min({2 * current_sm_count() / tiles, H / 256, 16}));
 }
+// Shares of N in the second product, for about `tiles` tiles and one CTA an SM: fewest rounds of blocks, where a CTA's
+// beginning and end cost about one more.
+inline int spans_of(int tiles, int blocks) {
+  const int sms = current_sm_count();
+  int best = 1;
+  long long least = 0;
+  for (int s = 1; s <= blocks && s <= 64; ++s) {
+    const long long cost = static_cast<long long>((tiles * static_cast<long long>(s) + sms - 1) / sms) * ((blocks + s - 1) / s + 1);
+    if (s == 1 || cost < least) {
+      best = s;
+      least = cost;
+    }
+  }
+  return best;
+}
 struct Workspace {
   size_t starts, order, v, bytes;
 };
@@ -783,12 +844,10 @@ int launch(Args& a, uint8_t* ws, cudaStream_t st) {
     attrs_done(attr, bit);
   }
   const unsigned tiles = tile_numbers(a.T, a.n);
-  const int blocks = (a.N + ExpandCfg<NR>::kCols - 1) / ExpandCfg<NR>::kCols;
-  // as many as leave each SM two CTAs
-  a.col_blocks = std::max(1, std::min(blocks, static_cast<int>(static_cast<long long>((a.T + kTT - 1) / kTT) * blocks / (2 * current_sm_count()))));
+  a.spans = spans_of((a.T + kTT - 1) / kTT + std::min(a.n, a.T / kTT) / 2, (a.N + ExpandCfg<NR>::kCols - 1) / ExpandCfg<NR>::kCols);
   if (launch_pdl(lora_group_kernel, dim3(a.n + 1), dim3(kGroupThreads), 0, st, a) != cudaSuccess ||
       launch_pdl(shrink, dim3(tiles, a.splits), dim3(kThreads), ShrinkCfg<NR>::kSmem, st, a) != cudaSuccess ||
-      launch_pdl(expand, dim3(tiles, (blocks + a.col_blocks - 1) / a.col_blocks), dim3(kThreads), ExpandCfg<NR>::kSmem, st, a) != cudaSuccess)
+      launch_pdl(expand, dim3(tiles, a.spans), dim3(kThreads), ExpandCfg<NR>::kSmem, st, a) != cudaSuccess)
     return MNW_E_CUDA;
   return MNW_OK;
 }
