@@ -128,7 +128,7 @@ struct Tile {
 __device__ __forceinline__ Tile find_tile(const Args& a, int q, Tile* sh) {
   if (threadIdx.x == 0) sh->count = 0;
   __syncthreads();
-  for (int e = threadIdx.x; e <= a.n; e += kThreads) {
+  for (int e = threadIdx.x; e <= a.n; e += blockDim.x) {
     const int lo = __ldcg(a.starts + e), hi = __ldcg(a.starts + e + 1);
     const int j = q - (lo / kTT + e);
     if (j >= 0 && j * kTT < hi - lo) *sh = Tile{e, lo + j * kTT, min(kTT, hi - lo - j * kTT)};
@@ -289,6 +289,7 @@ __global__ void __launch_bounds__(kThreads, NR <= 8 ? 2 : 1) lora_shrink_kernel(
 // y comes by cp.async, whole rows of a block, into shared memory, where the product is added, and leaves from there in
 // rows; v lies there as two operands, its two terms.  While one block is worked on, the next one's y and B are under way.
 // (Rows of 384 bytes as bulk copies, in and out: 59 us for the case below; so: BULK_TIME.)
+constexpr int kExpandThreads = 512;
 template <int NR>
 struct ExpandCfg {
   static constexpr int kPieces = NR <= 8 ? 1 : 2;         // of 64 ranks: 128-byte rows of an operand
@@ -300,7 +301,7 @@ struct ExpandCfg {
   static constexpr uint32_t kSmem = kOffY + 2 * kBytesY + 1024;
 };
 template <int NR>
-__global__ void __launch_bounds__(kThreads, 1) lora_expand_kernel(const Args a) {
+__global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const Args a) {
   using C = ExpandCfg<NR>;
   constexpr int kCols = C::kCols;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -326,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1) lora_expand_kernel(const Args a) 
     pdl_wait();
     __syncthreads();
     const int c0 = b0 * kCols / 8, c1 = min(b1 * kCols, a.N) / 8, w = c1 - c0;
-    for (long long i = tid; i < static_cast<long long>(tl.count) * w; i += kThreads) {
+    for (long long i = tid; i < static_cast<long long>(tl.count) * w; i += kExpandThreads) {
       const int r = static_cast<int>(i / w), c = c0 + static_cast<int>(i % w);
       const long long t = tokens[r];
       *reinterpret_cast<uint4*>(a.out + t * a.out_stride + c * 8) = __ldcg(reinterpret_cast<const uint4*>(a.y + t * a.y_stride + c * 8));
@@ -343,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1) lora_expand_kernel(const Args a) 
   auto rows = [&](int b, bool in) {
     const int left = (a.N - b * kCols) / 8;  // chunks to the end
     const uint32_t slot = y_at + ((b - b0) & 1) * C::kBytesY;
-    for (int i = tid; i < tl.count * kChunks; i += kThreads) {
+    for (int i = tid; i < tl.count * kChunks; i += kExpandThreads) {
       const int r = i / kChunks, c = i % kChunks;
       if (c >= left) continue;
       const long long t = tokens[r], col = static_cast<long long>(b) * kCols + c * 8;
@@ -356,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1) lora_expand_kernel(const Args a) 
   };
   auto load_b = [&](int b) {
     const uint32_t to = sbase + C::kOffB + ((b - b0) & 1) * C::kBytesB;
-    for (int i = tid; i < kCols * NR; i += kThreads) {
+    for (int i = tid; i < kCols * NR; i += kExpandThreads) {
       const int n = i / NR, c = i % NR, col = b * kCols + n, left = min(16, 2 * (rank - c * 8));  // (a rank need not be a multiple of 8)
       const bool on = col < a.N && left > 0;
       cp_async16(sw128(to + (c >> 3) * C::kPieceB, n, c & 7), on ? wb + static_cast<long long>(col) * a.R + c * 8 : wb, on ? left : 0);
@@ -379,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1) lora_expand_kernel(const Args a) 
   }
   {  // v's two terms: 4 ranks a thread and step, rows without a token are zeros
     constexpr int kQ = NR * 2;  // quads of a row
-    for (int i = tid; i < kTT * kQ; i += kThreads) {
+    for (int i = tid; i < kTT * kQ; i += kExpandThreads) {
       const int r = i / kQ, e = i % kQ * 4;
       float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
       if (r < tl.count) {
@@ -401,7 +402,8 @@ __global__ void __launch_bounds__(kThreads, 1) lora_expand_kernel(const Args a) 
   }
   const float scale = a.scale ? __ldcg(a.scale + tl.bin) : 1.f;
   constexpr uint32_t idesc = idesc_f16(kTT, kCols, true);
-  const int row = (warp & 3) * 32 + lane;  // of the product, in the end
+  const int row = (warp & 3) * 32 + lane;  // of the product, in the end, and kShare columns of it
+  constexpr int kShare = kCols * 4 / (kExpandThreads / 32);
   for (int b = b0; b < b1; ++b) {
     const int at = (b - b0) & 1;
     const uint32_t phase = (b - b0) >> 1 & 1;
@@ -429,14 +431,14 @@ __global__ void __launch_bounds__(kThreads, 1) lora_expand_kernel(const Args a) 
     bounded_wait(&d_full[at], phase, &abort_flag, a.err);
     __syncwarp();
     tc_fence_after();
-    uint8_t* const mine = smem + y_at + at * C::kBytesY + row * C::kRowY + (warp >> 2) * kCols;  // (kCols / 2 columns of two bytes)
+    uint8_t* const mine = smem + y_at + at * C::kBytesY + row * C::kRowY + (warp >> 2) * (kShare * 2);
 #pragma unroll
-    for (int c = 0; c < kCols / 2; c += 32) {
-      uint32_t d[32];
-      tmem_ld32(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + at * kCols + (warp >> 2) * (kCols / 2) + c, d);
+    for (int c = 0; c < kShare; c += 16) {
+      uint32_t d[16];
+      tmem_ld16(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + at * kCols + (warp >> 2) * kShare + c, d);
       tmem_wait_ld();
 #pragma unroll
-      for (int e = 0; e < 32; e += 8) {
+      for (int e = 0; e < 16; e += 8) {
         uint4* const p = reinterpret_cast<uint4*>(mine + (c + e) * 2);
         uint4 u = *p;
         auto add = [&](uint32_t w, uint32_t lo, uint32_t hi) {
@@ -847,7 +849,7 @@ int launch(Args& a, uint8_t* ws, cudaStream_t st) {
   a.spans = spans_of((a.T + kTT - 1) / kTT + std::min(a.n, a.T / kTT) / 2, (a.N + ExpandCfg<NR>::kCols - 1) / ExpandCfg<NR>::kCols);
   if (launch_pdl(lora_group_kernel, dim3(a.n + 1), dim3(kGroupThreads), 0, st, a) != cudaSuccess ||
       launch_pdl(shrink, dim3(tiles, a.splits), dim3(kThreads), ShrinkCfg<NR>::kSmem, st, a) != cudaSuccess ||
-      launch_pdl(expand, dim3(tiles, a.spans), dim3(kThreads), ExpandCfg<NR>::kSmem, st, a) != cudaSuccess)
+      launch_pdl(expand, dim3(tiles, a.spans), dim3(kExpandThreads), ExpandCfg<NR>::kSmem, st, a) != cudaSuccess)
     return MNW_E_CUDA;
   return MNW_OK;
 }
