@@ -37,8 +37,6 @@ namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32, kTK = kInt4Keys;
 constexpr int kWK = kTK / kWarps;  // keys of a warp
-constexpr int kMT = 2, kSubs = kWK / (16 * kMT);  // 16-key operand tiles computed together, and such groups
-constexpr int kStages = 2;
 constexpr float kLow = -1e30f;   // a maximum of nothing: finite, so that -inf minus it is -inf
 constexpr float kLift = 6.f;     // log2 of the unit's own product as FP16
 constexpr float kMostP = 256.f, kMostW = 16384.f;  // probabilities and products that a row's maximum and unit allow
@@ -46,6 +44,9 @@ constexpr float kMostP = 256.f, kMostW = 16384.f;  // probabilities and products
 template <int D, int NT>
 struct Cfg4 {
   static constexpr int kRT = 8 * NT;
+  // 16-key operand tiles computed together, and such groups: one where 32 rows' sums leave registers for no more
+  static constexpr int kMT = NT <= 2 ? 2 : 1, kSubs = kWK / (16 * kMT);
+  static constexpr int kStages = NT == 2 ? 3 : 2;  // what the CTAs of an SM have room for
   static constexpr int kRowBytes = D / 2;
   static constexpr int kTileBytes = kWK * kRowBytes, kRecBytes = kWK * int4row::kRecord;  // of a warp's keys
   static constexpr int kSlotBytes = 2 * (kTileBytes + kRecBytes);  // keys, values, their records
@@ -81,7 +82,7 @@ __device__ __forceinline__ int key_of(int i) { return i ^ ((i >> 1) & 1); }
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, int4_runs_per_sm(8 * NT)) paged_int4_kernel(const Args a, const int whole_pages) {
   using C = Cfg4<D, NT>;
-  constexpr int kRT = C::kRT;
+  constexpr int kRT = C::kRT, kMT = C::kMT, kSubs = C::kSubs, kStages = C::kStages;
   constexpr int kKS = D / 16;   // k steps of the first product
   constexpr int kNO = D / 16;   // row tiles of the second
   constexpr int kW = D / 64;    // words of a lane's piece of a value row; half of those of a key's

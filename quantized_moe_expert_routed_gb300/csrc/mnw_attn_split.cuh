@@ -37,7 +37,7 @@ constexpr int kBlockRows = 128, kBlockKeys = 128;  // the block kernel's tiles (
 constexpr int kInt4Keys = 256;                     // the INT4 kernel's (mnw_attn_paged_int4.cu), and its CTAs on an SM
 // INT4: the operands' 2^-24 is taken back half with the keys' scales, half with the queries' factors.
 constexpr float kHalfUnit = 4096.f;
-constexpr int int4_runs_per_sm(int rt) { return rt <= 16 ? 3 : 2; }
+constexpr int int4_runs_per_sm(int rt) { return rt <= 8 ? 3 : 2; }
 
 struct Args {
   Batch bt;
