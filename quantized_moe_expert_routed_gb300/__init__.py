@@ -390,11 +390,13 @@ def mnw_rmsnorm(x, weight, eps=1e-6, residual=None, residual_out=None, y=None, c
 
 def _token_rows(t, what, d=None):
     """(address, tokens, heads, d, elements between tokens) of bf16 [T, heads, d], a token's heads contiguous."""
-    p = _need(t, torch.bfloat16, what, 3)
-    T, h, dd = t.shape
-    if (d is not None and dd != d) or (h > 1 and t.stride(1) != dd):
+    shape, st = t.shape, t.stride()
+    if not t.is_cuda or t.dtype is not torch.bfloat16 or len(shape) != 3 or (st[2] != 1 and shape[2] > 1):
+        raise MnwError(f"{what}: expected a CUDA tensor of torch.bfloat16 with 3 dimensions, the last one contiguous")
+    T, h, dd = shape
+    if (d is not None and dd != d) or (h > 1 and st[1] != dd):
         raise MnwError(f"{what}: expected [T, heads, {d or 'd'}] with a token's heads contiguous")
-    return p, T, h, dd, t.stride(0) if T > 1 else max(h * dd, t.stride(0) // 8 * 8)
+    return t.data_ptr(), T, h, dd, st[0] if T > 1 else max(h * dd, st[0] // 8 * 8)
 
 
 def _cache_args(k_cache, v_cache, k_scale, v_scale):
@@ -420,23 +422,23 @@ def _cache_args(k_cache, v_cache, k_scale, v_scale):
     elif dtype is torch.int8:
         fmt = KV_INT8
         ks = _whole(k_scale, torch.float32, (n, h, page), "k_scale")
-        vs = ks if v_scale is k_scale else _whole(v_scale, torch.float32, (n, h, page), "v_scale")
+        vs = _whole(v_scale, torch.float32, (n, h, page), "v_scale")
     else:
         fmt = KV_INT4
         ks = _whole(k_scale, torch.uint8, (n, h, page, 8), "k_scale")
-        vs = ks if v_scale is k_scale else _whole(v_scale, torch.uint8, (n, h, page, 8), "v_scale")
+        vs = _whole(v_scale, torch.uint8, (n, h, page, 8), "v_scale")
         d, page_stride = 2 * d, 2 * page_stride
     return k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, fmt, n, page, page_stride, h, d
 
 
 def _batch_args(block_table, cache_lens, q_start):
-    tp = _need(block_table, torch.int32, "block_table", 2)
-    B, most = block_table.shape
-    if not block_table.is_contiguous():
-        raise MnwError("block_table has to be contiguous")
+    shape = block_table.shape
+    if not block_table.is_cuda or block_table.dtype is not torch.int32 or len(shape) != 2 or not block_table.is_contiguous():
+        raise MnwError("block_table: expected a contiguous CUDA tensor of torch.int32 with 2 dimensions")
+    B, most = shape
     lp = _whole(cache_lens, torch.int32, (B,), "cache_lens")
     sp = None if q_start is None else _whole(q_start, torch.int32, (B + 1,), "q_start")
-    return B, most, tp, lp, sp
+    return B, most, block_table.data_ptr(), lp, sp
 
 
 def mnw_kv_append(q, k, v, k_cache, v_cache, block_table, cache_lens, inv_freq=None, layout=ROPE_HALF, mscale=1.0,
@@ -529,13 +531,22 @@ def mnw_kv_values(cache, scale, out=None, stream=None):
     cache: int8 [n_pages, Hkv, page_size, d] with scales f32, or uint8
     [n_pages, Hkv, page_size, d / 2] with records uint8 [n_pages, Hkv,
     page_size, 8] (arguments as mnw_kv_append's)."""
-    if cache.dtype is torch.bfloat16:
-        raise MnwError("a bf16 cache holds its values as they are")
-    cp, _, sp, _, fmt, n_pages, page, page_stride, Hkv, d = _cache_args(cache, cache, scale, scale)
+    dtype, shape, st = cache.dtype, cache.shape, cache.stride()
+    if not cache.is_cuda or (dtype is not torch.int8 and dtype is not torch.uint8) or len(shape) != 4:
+        raise MnwError("cache: expected a CUDA tensor of int8, or uint8 (two 4-bit codes a byte), and 4 dimensions")
+    n_pages, Hkv, page, d = shape
+    if (page > 1 and st[2] != d) or (Hkv > 1 and st[1] != page * d) or (d > 1 and st[3] != 1):
+        raise MnwError("a page of the cache [Hkv, page_size, d] has to be contiguous")
+    page_stride = st[0] if n_pages > 1 else Hkv * page * d
+    if dtype is torch.int8:
+        fmt, sp = KV_INT8, _whole(scale, torch.float32, (n_pages, Hkv, page), "scale")
+    else:
+        fmt, sp = KV_INT4, _whole(scale, torch.uint8, (n_pages, Hkv, page, 8), "scale")
+        d, page_stride = 2 * d, 2 * page_stride
     shape = (n_pages, Hkv, page, d)
     if out is None:
         out = _new(shape, torch.bfloat16, cache.device, stream)
-    rc = load().mnw_kv_values(cp, sp, fmt, n_pages, page, Hkv, d, page_stride, _whole(out, torch.bfloat16, shape, "out"),
+    rc = load().mnw_kv_values(cache.data_ptr(), sp, fmt, n_pages, page, Hkv, d, page_stride, _whole(out, torch.bfloat16, shape, "out"),
                               _stream_of(cache, stream))
     if rc:
         _check(rc, "mnw_kv_values")

@@ -77,6 +77,13 @@ __device__ __forceinline__ float turn_fraction(uint32_t p, float f) {
   return fmaf(f, 0.f, f < 0.f ? -r : r);
 }
 
+// 1 / x to about 2^-23 of itself.
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // One CTA per `tokens` tokens.  A head row is D/16 pieces of two 16-byte
 // chunks, one thread each: the two that hold both elements of 8 rotation pairs
 // (half layout: chunks p and p + rot/16; elsewhere, and past rot, neighbours),
@@ -84,7 +91,7 @@ __device__ __forceinline__ float turn_fraction(uint32_t p, float f) {
 // a time, and the first batch is requested before the tokens' positions, pages
 // and angles are worked out.
 template <int D, int FMT, bool HALF>
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, FMT == MNW_KV_INT4 ? 4 : 1) kv_append_kernel(const Args a) {
   constexpr int P = D / 16;  // pieces (threads) of a row
   // sine and cosine, two pairs a word: pairs 8 p + 2 j, 8 p + 2 j + 1 at [j][p], so that a row's lanes read neighbours
   __shared__ float4 cs[kMaxTokens][4][kMaxPairs / 8];
@@ -237,41 +244,62 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const Args a) {
           top[0] = __vmaxu2(top[0], __shfl_xor_sync(0xffffffffu, top[0], d));
           top[1] = __vmaxu2(top[1], __shfl_xor_sync(0xffffffffu, top[1], d));
         }
-        if (live && !is_q && page >= 0) {
-          const float gmax[4] = {__uint_as_float(top[0] << 16), __uint_as_float(top[0] & 0xFFFF0000u),
-                                 __uint_as_float(top[1] << 16), __uint_as_float(top[1] & 0xFFFF0000u)};
-          const uint32_t most = __vmaxu2(top[0], top[1]);
-          const float amax = __uint_as_float(max(most >> 16, most & 0xFFFFu) << 16);
-          float scale = 0.f;
-          uint32_t mul = 0x01010101u, words[2] = {0x88888888u, 0x88888888u};
-          if (!(amax < INFINITY)) {
-            scale = __uint_as_float(0x7FC00000u);  // the row is not finite, and reads as NaN
-          } else if (amax >= 0x1p-100f) {
-            scale = __uint_as_float((__float_as_uint(__fdiv_rn(amax, 1785.f)) + 0xFFFFu) & 0xFFFF0000u);
-            const float s7 = 7.f * scale, r7 = __frcp_rn(s7) * (1.f - 0x1p-20f);
-            int m[4];
-            mul = 0;
+        if (!__any_sync(0xffffffffu, live && !is_q && page >= 0)) continue;
+        const uint32_t most = __vmaxu2(top[0], top[1]);
+        const float amax = __uint_as_float(max(most >> 16, most & 0xFFFFu) << 16);
+        // a row below 2^-100 is stored as zeros; one that is not finite gets a NaN for its scale
+        const bool some = amax >= 0x1p-100f && amax < INFINITY;
+        // (a product that lies a little below the quotient, rounded up to 8 bits, is the scale or the value before it)
+        uint32_t sb = (__float_as_uint(amax * (0x1p-20f - 1.f) * (-1.f / 1785.f)) + 0xFFFFu) & 0xFFFF0000u;
+        sb += __uint_as_float(sb) * 1785.f < amax ? 0x10000u : 0u;
+        const float scale = some ? __uint_as_float(sb) : (amax < INFINITY ? 0.f : __uint_as_float(0x7FC00000u));
+        const float unit = some ? scale : 1.f;
+        // each of a row's lanes works out the multiplier of one group, from at most the quotient, and at most one and a bit
+        // below it, up; then all have the four
+        uint32_t mul;
+        {
+          const int g = p * 4 / P;
+          const float gmax = __uint_as_float((g & 1 ? top[g >> 1] >> 16 : top[g >> 1] & 0xFFFFu) << 16);
+          const float s7 = 7.f * unit;
+          float m = some ? truncf(gmax * (rcp(s7) * (1.f - 0x1p-20f))) : 1.f;
+          m += m * s7 < gmax ? 1.f : 0.f;
+          m += m * s7 < gmax ? 1.f : 0.f;
+          mul = static_cast<uint32_t>(fmaxf(m, 1.f)) << (8 * g);
+          if (!some) mul = 1u << (8 * g);
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {  // from at most the quotient, and at most one and a bit below it
-              m[g] = static_cast<int>(gmax[g] * r7);
-              m[g] += m[g] * s7 < gmax[g] ? 1 : 0;
-              m[g] += m[g] * s7 < gmax[g] ? 1 : 0;
-              m[g] = max(m[g], 1);
-              mul |= static_cast<uint32_t>(m[g]) << (8 * g);
+          for (int d = P / 2; d > 0; d >>= 1) mul |= __shfl_xor_sync(0xffffffffu, mul, d);
+        }
+        uint32_t words[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float step = unit * static_cast<float>(mul >> (8 * ((e ? c1 : c0) / kGC)) & 0xFFu);
+          const float rs = some ? rcp(step) : 0.f;
+          // the codes of even and odd elements, a nibble each: rounded to an integer by the sum with 1.5 * 2^23
+          constexpr float kRound = 12582912.f;
+          float part[2] = {0.f, 0.f}, far = 0.f;
+#pragma unroll
+          for (int j = 3; j >= 0; --j)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const float y = __uint_as_float(x ? u[e][j] & 0xFFFF0000u : u[e][j] << 16);
+              const float r = y * rs, n = __fadd_rn(__fadd_rn(r, kRound), -kRound);
+              far = fmaxf(far, fabsf(r - n));
+              part[x] = fmaf(part[x], 16.f, n);
             }
+          // + 8 in each nibble
+          words[e] = (__float_as_uint(part[0] + (kRound + 34952.f)) & 0xFFFFu) | __float_as_uint(part[1] + (kRound + 34952.f)) << 16;
+          // y rs is within 2^-19 of y / step: a quotient that lies that close to a half is worked out exactly
+          if (far > 0.5f - 0x1p-17f) {
+            words[e] = 0;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int g = (e ? c1 : c0) / kGC;
-              const float step = scale * static_cast<float>(g & 2 ? (g & 1 ? m[3] : m[2]) : (g & 1 ? m[1] : m[0]));
-              const float rs = __frcp_rn(step);
-              words[e] = 0;
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                words[e] |= static_cast<uint32_t>(int8_code(__uint_as_float(u[e][j] << 16), step, rs) + 8) << (4 * j);
-                words[e] |= static_cast<uint32_t>(int8_code(__uint_as_float(u[e][j] & 0xFFFF0000u), step, rs) + 8) << (4 * j + 16);
-              }
+            for (int j = 0; j < 4; ++j) {
+              words[e] |= static_cast<uint32_t>(int8_code(__uint_as_float(u[e][j] << 16), step, rs) + 8) << (4 * j);
+              words[e] |= static_cast<uint32_t>(int8_code(__uint_as_float(u[e][j] & 0xFFFF0000u), step, rs) + 8) << (4 * j + 16);
             }
           }
+        }
+        if (!some) words[0] = words[1] = 0x88888888u;
+        if (live && !is_q && page >= 0) {
           uint8_t* dst = (is_k ? a.kc : a.vc) + ((page * a.page_stride + static_cast<long long>(head_row) * D) >> 1);
           *reinterpret_cast<uint32_t*>(dst + c0 * 4) = words[0];
           *reinterpret_cast<uint32_t*>(dst + c1 * 4) = words[1];

@@ -26,9 +26,11 @@ struct Args {
   long long page_bytes;     // between pages of the cache
   long long chunks;         // of all pages
   int page_chunks;
+  paged::FastDiv page_div;  // by page_chunks
 };
 
-template <int D, bool INT4>
+// BIG: more than 2^31 chunks, whose places take 64 bits.
+template <int D, bool INT4, bool BIG>
 __global__ void __launch_bounds__(kThreads) kv_values_kernel(const Args a) {
   constexpr int kBytes = INT4 ? 4 : 8;  // of a chunk's codes
   constexpr int kPerRow = D / 8;
@@ -41,7 +43,7 @@ __global__ void __launch_bounds__(kThreads) kv_values_kernel(const Args a) {
     const long long at = at0 + i * kThreads;
     raw[i] = rec[i] = make_uint2(0, 0);
     if (at < a.chunks) {
-      const long long page = at / a.page_chunks;
+      const long long page = BIG ? at / a.page_chunks : static_cast<int>(paged::quotient(static_cast<uint32_t>(at), a.page_div));
       const uint8_t* src = a.cache + page * a.page_bytes + (at - page * a.page_chunks) * kBytes;
       const long long row = at / kPerRow;
       if constexpr (INT4) {
@@ -78,7 +80,9 @@ __global__ void __launch_bounds__(kThreads) kv_values_kernel(const Args a) {
 template <int D, bool INT4>
 cudaError_t launch(const Args& a, cudaStream_t st) {
   constexpr int kPer = kThreads * kBatch;
-  return launch_pdl(kv_values_kernel<D, INT4>, dim3(static_cast<unsigned>((a.chunks + kPer - 1) / kPer)), dim3(kThreads), 0, st, a);
+  const dim3 grid(static_cast<unsigned>((a.chunks + kPer - 1) / kPer));
+  return a.chunks > 0x7fffffffll ? launch_pdl(kv_values_kernel<D, INT4, true>, grid, dim3(kThreads), 0, st, a)
+                                 : launch_pdl(kv_values_kernel<D, INT4, false>, grid, dim3(kThreads), 0, st, a);
 }
 
 }  // namespace kvval
@@ -105,6 +109,7 @@ int mnw_kv_values(const void* cache, const void* scale, int fmt, int n_pages, in
   if (page_chunks > 0x7fffffffll) return MNW_E_UNSUPPORTED;
   a.page_chunks = static_cast<int>(page_chunks);
   a.chunks = page_chunks * n_pages;
+  a.page_div = paged::fast_div(static_cast<uint32_t>(page_chunks));
   if (a.chunks > 0x7fffffffll * 256) return MNW_E_UNSUPPORTED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
