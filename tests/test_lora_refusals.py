@@ -24,7 +24,7 @@ def call(lib, **kw):  # noqa: F811
     (dict(x=None), INVALID), (dict(a=None), INVALID), (dict(b=None), INVALID), (dict(i=None), INVALID), (dict(y=None), INVALID),
     (dict(o=None), INVALID), (dict(x=P(8)), INVALID), (dict(a=P(8)), INVALID), (dict(b=P(24)), INVALID),
     (dict(i=P(2)), INVALID), (dict(s=P(2)), INVALID), (dict(r=P(2)), INVALID), (dict(y=P(8)), INVALID), (dict(o=P(8)), INVALID),
-    (dict(T=600, ws=None), INVALID), (dict(T=600, wsb=100), SMALL), (dict(ws=P(128)), INVALID), (dict(xs=248), INVALID), (dict(xs=260), INVALID), (dict(ys=120), INVALID), (dict(ys=132), INVALID),
+    (dict(T=1100, ws=None), INVALID), (dict(T=1100, wsb=100), SMALL), (dict(ws=P(128)), INVALID), (dict(xs=248), INVALID), (dict(xs=260), INVALID), (dict(ys=120), INVALID), (dict(ys=132), INVALID),
     (dict(os=120), INVALID), (dict(os=132), INVALID), (dict(o=BIG, os=256), INVALID),
 ])
 def test_refusals(lib, kw, want):  # noqa: F811
@@ -35,7 +35,7 @@ def test_workspace_size(lib):  # noqa: F811
     f = lib.mnw_lora_workspace_size
     assert f(0, 256, 16, 4) == f(1, 0, 16, 4) == f(1, 256, 0, 4) == f(1, 256, 136, 4) == f(1, 256, 16, 0) == 0
     assert f(1, 256, 16, 4) == 0  # few tokens need none
-    assert 0 < f(600, 256, 16, 4) <= f(600, 4096, 64, 4) and f(1000, 4096, 64, 4) % 256 == 0
+    assert 0 < f(1100, 256, 16, 4) <= f(1100, 4096, 64, 4) and f(2000, 4096, 64, 4) % 256 == 0
 
 
 def test_the_binding_refuses_before_the_library(lib):  # noqa: F811
