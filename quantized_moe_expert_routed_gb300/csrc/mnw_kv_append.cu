@@ -12,7 +12,12 @@
 // (7 S))), code = rne(x / (S m)).  S of 8 bits makes all of it exact in FP32: 7
 // S m has 19 bits and is compared as it is, and x / (S m) is either half way
 // between two integers or 2^-20 of itself away from it, so rounding the
-// quotient to FP32 does not move it there.
+// quotient to FP32 does not move it there.  A code is a seventh of a group's
+// largest value, so a rotated key that comes out one BF16 step beside the exact
+// one can move an element by that much: for INT4 caches sine and cosine are
+// rounded as the exact ones would be (mnw_turns.cuh), and every operation of the
+// rotation is rounded by itself, so rows are those that the formula gives in
+// FP32.
 //
 // The angle: at position 10^5 a radian's fraction lies 17 bits down, so a
 // plain FP32 product would leave 7 bits of it.  It is taken in turns and in
@@ -36,6 +41,7 @@
 #include "mnw_internal.h"
 #include "mnw_paged.cuh"
 #include "mnw_ptx.cuh"
+#include "mnw_turns.cuh"
 
 namespace mnw {
 namespace kvapp {
@@ -64,16 +70,19 @@ struct Args {
   uint32_t* err;
 };
 
-// Fraction of a turn, in [-1/2, 1/2], of position p >= 0 at frequency f (NaN and
-// infinite frequencies give NaN).
-__device__ __forceinline__ float turn_fraction(uint32_t p, float f) {
+// Fraction of a turn, in units of 2^-64, of position p >= 0 at frequency |f|.
+__device__ __forceinline__ uint64_t turn_bits(uint32_t p, float f) {
   constexpr uint32_t kHi = 0x28BE60DBu, kLo = 0x9391054Au;  // 2^64 / (2 pi)
   const uint32_t bits = __float_as_uint(f), m = bits << 8 | 0x80000000u;  // |f| = m 2^(e - 158)
   const int e = static_cast<int>(bits >> 23 & 0xFFu);
   const uint64_t mt = static_cast<uint64_t>(m) * kHi + __umulhi(m, kLo);  // m 2^32 / (2 pi)
   // |f| / (2 pi) in units of 2^-64, whole turns lost
   const uint64_t g = e <= 126 ? mt >> min(126 - e, 63) : mt << min(e - 126, 63);
-  const float r = static_cast<float>(static_cast<int>((g * p) >> 32)) * 0x1p-32f;
+  return g * p;
+}
+// In turns, in [-1/2, 1/2] (NaN and infinite frequencies give NaN).
+__device__ __forceinline__ float turn_fraction(uint32_t p, float f) {
+  const float r = static_cast<float>(static_cast<int>(turn_bits(p, f) >> 32)) * 0x1p-32f;
   return fmaf(f, 0.f, f < 0.f ? -r : r);
 }
 
@@ -91,7 +100,7 @@ __device__ __forceinline__ float rcp(float x) {
 // a time, and the first batch is requested before the tokens' positions, pages
 // and angles are worked out.
 template <int D, int FMT, bool HALF>
-__global__ void __launch_bounds__(kThreads, FMT == MNW_KV_INT4 ? 4 : 1) kv_append_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, FMT == MNW_KV_INT4 ? 4 : 0) kv_append_kernel(const Args a) {
   constexpr int P = D / 16;  // pieces (threads) of a row
   // sine and cosine, two pairs a word: pairs 8 p + 2 j, 8 p + 2 j + 1 at [j][p], so that a row's lanes read neighbours
   __shared__ float4 cs[kMaxTokens][4][kMaxPairs / 8];
@@ -175,7 +184,14 @@ __global__ void __launch_bounds__(kThreads, FMT == MNW_KV_INT4 ? 4 : 1) kv_appen
     }
     for (int i = lane; i < pairs; i += 32) {
       float sn, co;
-      sincospif(2.f * turn_fraction(static_cast<uint32_t>(pos), __ldg(a.inv_freq + i)), &sn, &co);
+      const float f = __ldg(a.inv_freq + i);
+      if constexpr (FMT == MNW_KV_INT4) {
+        turns::sincos_turns(turn_bits(static_cast<uint32_t>(pos), f), &sn, &co);
+        sn = fmaf(f, 0.f, f < 0.f ? -sn : sn);
+        co = fmaf(f, 0.f, co);
+      } else {
+        sincospif(2.f * turn_fraction(static_cast<uint32_t>(pos), f), &sn, &co);
+      }
       reinterpret_cast<float2*>(&cs[warp][(i & 7) >> 1][i >> 3])[i & 1] = make_float2(co * a.mscale, sn * a.mscale);
     }
   }
@@ -195,6 +211,13 @@ __global__ void __launch_bounds__(kThreads, FMT == MNW_KV_INT4 ? 4 : 1) kv_appen
       const int h = is_q ? row : (is_k ? row - q_rows : row - q_rows - a.Hkv);
       uint32_t u[2][4] = {{raw[i][0].x, raw[i][0].y, raw[i][0].z, raw[i][0].w}, {raw[i][1].x, raw[i][1].y, raw[i][1].z, raw[i][1].w}};
       if (in_rot && (is_q || is_k)) {
+        // u cos a - w sin a and u cos a + w sin a (INT4: each operation rounded, see above)
+        auto less = [](float u, float c, float w, float s) {
+          return FMT == MNW_KV_INT4 ? __fsub_rn(__fmul_rn(u, c), __fmul_rn(w, s)) : u * c - w * s;
+        };
+        auto plus = [](float u, float c, float w, float s) {
+          return FMT == MNW_KV_INT4 ? __fadd_rn(__fmul_rn(u, c), __fmul_rn(w, s)) : u * c + w * s;
+        };
         auto lo = [](uint32_t w) { return __uint_as_float(w << 16); };
         auto hi = [](uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); };
 #pragma unroll
@@ -202,13 +225,13 @@ __global__ void __launch_bounds__(kThreads, FMT == MNW_KV_INT4 ? 4 : 1) kv_appen
           const float4 f = cs[tk][j][p];
           if constexpr (HALF) {
             const float x0 = lo(u[0][j]), x1 = hi(u[0][j]), w0 = lo(u[1][j]), w1 = hi(u[1][j]);
-            u[0][j] = pack_bf16x2(x0 * f.x - w0 * f.y, x1 * f.z - w1 * f.w);
-            u[1][j] = pack_bf16x2(w0 * f.x + x0 * f.y, w1 * f.z + x1 * f.w);
+            u[0][j] = pack_bf16x2(less(x0, f.x, w0, f.y), less(x1, f.z, w1, f.w));
+            u[1][j] = pack_bf16x2(plus(w0, f.x, x0, f.y), plus(w1, f.z, x1, f.w));
           } else {
             uint32_t &a0 = u[j >> 1][2 * (j & 1)], &a1 = u[j >> 1][2 * (j & 1) + 1];
             const float x0 = lo(a0), w0 = hi(a0), x1 = lo(a1), w1 = hi(a1);
-            a0 = pack_bf16x2(x0 * f.x - w0 * f.y, w0 * f.x + x0 * f.y);
-            a1 = pack_bf16x2(x1 * f.z - w1 * f.w, w1 * f.z + x1 * f.w);
+            a0 = pack_bf16x2(less(x0, f.x, w0, f.y), plus(w0, f.x, x0, f.y));
+            a1 = pack_bf16x2(less(x1, f.z, w1, f.w), plus(w1, f.z, x1, f.w));
           }
         }
       }

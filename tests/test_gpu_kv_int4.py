@@ -25,12 +25,10 @@ def _empty(cache):
 
 @pytest.mark.parametrize("case", APPEND, ids=lambda c: f"n{c[0]}-p{c[2]}-d{c[5]}-r{c[6]}{c[7][0]}")
 def test_append_stores_what_the_rule_gives(case):
-    """Against the rows that a BF16 cache gets from the same call, quantised with exact integers."""
+    """Against the rotation in FP32, operation by operation, quantised with exact integers."""
     m = M()
     counts, lens, page, Hq, Hkv, d, rot, layout, ragged = case
     cache = I4.Cache(lens, page, Hkv, d, seed=5, joint=page % 2 == 0)
-    plain = U.Cache(lens, page, Hkv, d, "bf16", seed=5)
-    assert torch.equal(cache.table, plain.table)
     T = sum(counts)
     qkv = _randn((T, Hq + 2 * Hkv, d), 6, 2.0)
     qkv[..., 3] *= 40  # a channel far above the rest
@@ -38,16 +36,28 @@ def test_append_stores_what_the_rule_gives(case):
     f = None if rot == 0 else m.mnw_rope_frequencies(rot, 1e4, device="cuda")[0]
     start = torch.tensor(U.starts_of(counts), dtype=torch.int32, device="cuda") if ragged else None
     kw = dict(inv_freq=f, layout=m.ROPE_HALF if layout == "half" else m.ROPE_INTERLEAVED, mscale=1.25, q_start=start)
+    pos = np.concatenate([np.arange(L - n, L) for n, L in zip(counts, lens)])
+    seq = np.repeat(np.arange(len(lens)), counts)
+
+    def rotated(x):  # (sine and cosine as rounded from 64 bits, but for a few in 10^4, where a row may differ)
+        y = x.float().cpu().numpy().copy()
+        if rot:
+            a = pos[:, None] * f.double().cpu().numpy()
+            c, s = ((g(a).astype(np.float32) * np.float32(1.25))[:, None] for g in (np.cos, np.sin))
+            i = np.arange(rot // 2)
+            first, second = (i, i + rot // 2) if layout == "half" else (2 * i, 2 * i + 1)
+            u, w = y[..., first].copy(), y[..., second].copy()
+            y[..., first], y[..., second] = u * c - w * s, w * c + u * s
+        return torch.from_numpy(y).bfloat16()
     before = [t.clone() for t in (cache.k, cache.v, cache.ks, cache.vs)]
     err = torch.zeros(1, dtype=torch.int32, device="cuda")
     got = m.mnw_kv_append(q, k, v, cache.k, cache.v, cache.table, cache.cache_lens, err=err, **kw, **cache.kw())
-    want = m.mnw_kv_append(q, k, v, plain.k, plain.v, plain.table, plain.cache_lens, **kw)
-    assert int(err.item()) == 0 and torch.equal(got, want)
-    pos = np.concatenate([np.arange(L - n, L) for n, L in zip(counts, lens)])
-    seq = np.repeat(np.arange(len(lens)), counts)
+    assert int(err.item()) == 0
+    differ = (got.cpu() != rotated(q)).float().mean()
+    assert differ <= 2e-5  # a step of FP32 beside, in a few of 10^4, moves a BF16 value in 2^-15 of them
     pg, sl = cache.table_host[seq, pos // page].long().cuda(), torch.as_tensor(pos % page).cuda()
-    for data, rec, rows in ((cache.k, cache.ks, plain.k), (cache.v, cache.vs, plain.v)):
-        want_data, want_rec = I4.quantise(rows[pg, :, sl].double().cpu().numpy())
+    for data, rec, rows in ((cache.k, cache.ks, rotated(k)), (cache.v, cache.vs, v)):
+        want_data, want_rec = I4.quantise(rows.double().cpu().numpy())
         assert np.array_equal(rec[pg, :, sl].cpu().numpy(), want_rec)
         assert np.array_equal(data[pg, :, sl].cpu().numpy(), want_data)
     kept = torch.ones((cache.k.shape[0], page), dtype=torch.bool, device="cuda")
@@ -279,3 +289,24 @@ def test_append_and_attention_in_a_replayed_graph(d, n, Hq, Hkv):
         lens.copy_(start + i * n)
         graph.replay()
         assert torch.equal(out, want[i]), i
+
+
+@pytest.mark.parametrize("at", [1000, 131071, 16777217, 1 << 30])
+def test_rotation_keeps_far_positions(at):
+    """Angles at far positions, by a table that sends every page to page 0; negative frequencies turn the other way."""
+    m = M()
+    page = 65536
+    table = torch.zeros((1, at // page + 1), dtype=torch.int32, device="cuda")
+    kc, vc = (torch.zeros((1, 1, page, 32), dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.zeros((1, 1, page, 8), dtype=torch.uint8, device="cuda") for _ in range(2))
+    q, kv = _randn((3, 2, 64), 1), _randn((3, 1, 64), 2)
+    f, _ = m.mnw_rope_frequencies(64, 1e4, device="cuda")
+    f[5] *= -1
+    lens = torch.tensor([at], dtype=torch.int32, device="cuda")
+    for layout in ("half", "interleaved"):
+        got = m.mnw_kv_append(q, kv, kv, kc, vc, table, lens, inv_freq=f, k_scale=ks, v_scale=vs,
+                              layout=m.ROPE_HALF if layout == "half" else m.ROPE_INTERLEAVED)
+        ref, size = U.rotate_plain(q, np.arange(at - 3, at), f, 64, layout, 1.0)
+        # BF16's half step; sine and cosine (half a step of FP32), three roundings, and 2^-64 turns a position
+        tol = 2.0 ** -8 * ref.abs() + (2.0 ** -22 + at * 2.0 ** -61) * size
+        assert ((got.double().cpu() - ref).abs() <= tol).all()
