@@ -516,7 +516,8 @@ int mnw_kv_append(const void* q, long long q_stride, const void* k, long long k_
  * second product as BF16 (BF16 caches), TF32 (INT8 caches, up to 32 query rows
  * a kv head: new tokens of a sequence * Hq / Hkv) or FP16 (INT8, more rows:
  * products with values below 2^-38 of the row's largest are lost; INT4: below
- * 2^-30).  Row tiles
+ * 2^-30, and with more than 32 rows value rows of magnitudes outside 2^-80 ..
+ * 2^80 lose more).  Row tiles
  * times key tiles of the full block table have to stay below 2^31
  * (MNW_E_UNSUPPORTED).  ws: device, 256-byte aligned,
  * >= mnw_attn_paged_workspace_size() bytes, any contents; calls that overlap
@@ -540,7 +541,7 @@ int mnw_kv_values(const void* cache, const void* scale, int fmt, int n_pages, in
  * x: device bf16 [T, H]; y (the shared projection's output) and out: device
  * bf16 [T, N]; rows *_stride elements apart (multiples of 8), so that slices of
  * a wider tensor can be passed; out may be y itself (with its stride), and else
- * must not overlap it.  a: device bf16 [n_adapters, R, H]; b: device bf16
+ * must not overlap it, nor x.  a: device bf16 [n_adapters, R, H]; b: device bf16
  * [n_adapters, N, R]; adapter: device int32 [T], -1 for a token without one
  * (out = y).  scale: device f32 [n_adapters], NULL for 1.  ranks: device int32
  * [n_adapters], NULL for R: of adapter i the first ranks[i] rows of A and

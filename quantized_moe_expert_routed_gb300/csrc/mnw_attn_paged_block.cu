@@ -916,6 +916,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // p = 2^(s fac - unit + kLift4), so that p times the value's scale is the FP16 product as it is.  The unit of
           // before serves as long as no product passes 2^14, which is looked for in the products; then, and for a row's
           // first keys, the unit is set and the products are computed (again).
+          const uint64_t one2 = ones(a);
           bool set = t == begin || __any_sync(0xffffffffu, st[0].unit == -INFINITY || st[1].unit == -INFINITY);
           uint32_t pw[32];
           uint64_t l2[2];
@@ -928,8 +929,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint64_t kf = *reinterpret_cast<const uint64_t*>(ks + 8 * i), lf = *reinterpret_cast<const uint64_t*>(vs + kTK + 8 * i);
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                  const uint64_t y = f32x2_fma(f32x2_mul(f32x2_pack(sv[4 * i + 2 * x], sv[4 * i + 2 * x + 1]), kf), fac2[x], lf);
-                  top[x] = fmaxf(fmaxf(top[x], lo32(y)), hi32(y));
+                  const uint64_t y = f32x2_mul(f32x2_pack(sv[4 * i + 2 * x], sv[4 * i + 2 * x + 1]), kf);
+                  top[x] = fmaxf(fmaxf(top[x], __fadd_rn(__fmul_rn(lo32(y), fac[x]), lo32(lf))),
+                                 __fadd_rn(__fmul_rn(hi32(y), fac[x]), hi32(lf)));
                 }
               }
 #pragma unroll
@@ -956,7 +958,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint64_t kf = *reinterpret_cast<const uint64_t*>(ks + 8 * i), vf = *reinterpret_cast<const uint64_t*>(vs + 8 * i);
 #pragma unroll
               for (int x = 0; x < 2; ++x) {
-                const uint64_t e2 = f32x2_fma(f32x2_mul(f32x2_pack(sv[4 * i + 2 * x], sv[4 * i + 2 * x + 1]), kf), fac2[x], neg2[x]);
+                // the score is rounded before the unit goes off, as it was for the unit: of huge ones a fused product would
+                // leave its rounding
+                const uint64_t s2 = f32x2_mul(f32x2_mul(f32x2_pack(sv[4 * i + 2 * x], sv[4 * i + 2 * x + 1]), kf), fac2[x]);
+                const uint64_t e2 = f32x2_fma(s2, one2, neg2[x]);
                 const uint64_t p2 = f32x2_pack(__float_as_uint(ex2(lo32(e2))), __float_as_uint(ex2(hi32(e2))));
                 l2[x] = f32x2_add(l2[x], p2);
                 const uint64_t w2 = f32x2_mul(p2, vf);

@@ -37,7 +37,7 @@ namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32, kTK = kInt4Keys;
 constexpr int kWK = kTK / kWarps;  // keys of a warp
-constexpr float kLow = -1e30f;   // a maximum of nothing: finite, so that -inf minus it is -inf
+constexpr float kLow = -3e38f;   // a maximum of nothing: finite, so that -inf minus it is -inf
 constexpr float kLift = 6.f;     // log2 of the unit's own product as FP16
 constexpr float kMostP = 256.f, kMostW = 16384.f;  // probabilities and products that a row's maximum and unit allow
 
@@ -263,6 +263,7 @@ __global__ void __launch_bounds__(kThreads, int4_runs_per_sm(8 * NT)) paged_int4
     if constexpr (!kQRegs) __syncthreads();
   };
 
+  const uint64_t one2 = ones(a);
   // byte offsets of what a lane reads: keys' and values' rows and records
   const int k_row = key_of(g8) * C::kRowBytes + t4 * (D / 8), k_rec = key_of(g8) * int4row::kRecord;
   const int v_key0 = key_of(2 * t4), v_key1 = key_of(2 * t4 + 1);
@@ -378,7 +379,10 @@ __global__ void __launch_bounds__(kThreads, int4_runs_per_sm(8 * NT)) paged_int4
           for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const uint64_t e2 = f32x2_fma(two(sc[mt][nt][2 * h], sc[mt][nt][2 * h + 1]), fac[mt][nt][h], neg[nt]);
+              // the score is rounded before the maximum goes off, as it was for the maximum: of huge ones a fused product
+              // would leave its rounding
+              const uint64_t s2 = f32x2_mul(two(sc[mt][nt][2 * h], sc[mt][nt][2 * h + 1]), fac[mt][nt][h]);
+              const uint64_t e2 = f32x2_fma(s2, one2, neg[nt]);
               const uint64_t p2 = two(ex2(lo32(e2)), ex2(hi32(e2)));
               now[nt] = f32x2_add(now[nt], p2);
               const uint64_t w2 = f32x2_mul(p2, two(vs[mt][h] * lo32(lift[nt]), vs[mt][h] * hi32(lift[nt])));

@@ -68,6 +68,13 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// Two FP32 ones that the compiler does not know for such (Hq > 0): a packed sum written as x * 1 + y cannot be joined with
+// the product that x is, which a packed addition was.
+__device__ __forceinline__ uint64_t ones(const Args& a) {
+  const uint32_t one = 0x3F800000u | static_cast<uint32_t>(a.Hq >> 31);
+  return f32x2_pack(one, one);
+}
+
 // 16-, 8- and 4-byte asynchronous copies; bytes 0: zeros.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");

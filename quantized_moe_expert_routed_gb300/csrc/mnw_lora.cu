@@ -884,7 +884,8 @@ int mnw_lora_add(const void* x, long long x_stride, const void* a, const void* b
       !aligned(y, 16) || !aligned(out, 16) || !aligned(ws, 256) || !aligned(adapter, 4) || !aligned(ranks, 4) ||
       !aligned(scale, 4) || x_stride % 8 || y_stride % 8 || out_stride % 8 || x_stride < H || y_stride < N || out_stride < N)
     return MNW_E_INVALID_ARG;
-  if (y == out && y_stride != out_stride && T > 1) return MNW_E_INVALID_ARG;  // rows of one over others of the other
+  // rows of one over others of the other, or over x, which is still read
+  if ((y == out && y_stride != out_stride && T > 1) || x == out) return MNW_E_INVALID_ARG;
   if (ws_bytes < need) return MNW_E_WORKSPACE_TOO_SMALL;
   lora::Args p{};
   p.x = static_cast<const __nv_bfloat16*>(x);

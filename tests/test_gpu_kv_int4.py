@@ -99,6 +99,50 @@ def test_append_of_special_rows(d):
     assert np.isnan(s[28:31]).all() and (s[8:20] == 0).all()
 
 
+@pytest.mark.parametrize("layout,d,rot", [("half", 128, 128), ("half", 64, 48), ("interleaved", 128, 32)])
+def test_append_many_tokens_as_few(layout, d, rot):
+    """One call over ragged sequences with several tokens a CTA, and a call per sequence with one: the same bits."""
+    m = M()
+    counts, Hq, Hkv, page = [701, 1, 0, 898, 3], 6, 2, 20
+    lens = [900, 1, 33, 898, 77]
+    cache = I4.Cache(lens, page, Hkv, d, seed=9)
+    T = sum(counts)
+    q, k, v = _randn((T, Hq, d), 1), _randn((T, Hkv, d), 2), _randn((T, Hkv, d), 3)
+    f, _ = m.mnw_rope_frequencies(rot, 1e4, device="cuda")
+    kw = dict(inv_freq=f, layout=m.ROPE_HALF if layout == "half" else m.ROPE_INTERLEAVED)
+    start = U.starts_of(counts)
+    few = [t.clone() for t in (cache.k, cache.v, cache.ks, cache.vs)]
+    got = m.mnw_kv_append(q, k, v, cache.k, cache.v, cache.table, cache.cache_lens,
+                          q_start=torch.tensor(start, dtype=torch.int32, device="cuda"), **kw, **cache.kw())
+    for b, n in enumerate(counts):
+        if n:
+            at = slice(start[b], start[b + 1])
+            one = m.mnw_kv_append(q[at], k[at], v[at], few[0], few[1], cache.table[b:b + 1], cache.cache_lens[b:b + 1],
+                                  k_scale=few[2], v_scale=few[3], **kw)
+            assert torch.equal(got[at], one)
+    assert all(torch.equal(a, b) for a, b in zip((cache.k, cache.v, cache.ks, cache.vs), few))
+
+
+def test_append_leaves_out_what_does_not_fit():
+    m = M()
+    cache = I4.Cache([40, 6], 16, 2, 128, seed=1)
+    q, k, v = _randn((4, 4, 128), 1), _randn((4, 2, 128), 2), _randn((4, 2, 128), 3)
+    f, _ = m.mnw_rope_frequencies(128, 1e4, device="cuda")
+    for lens, table, code in (([40, 1], cache.table, m.DEVERR_BAD_LENGTH),  # fewer positions than new tokens
+                              ([-3, 6], cache.table, m.DEVERR_BAD_LENGTH),
+                              ([10 ** 6, 6], cache.table, m.DEVERR_BAD_LENGTH | m.DEVERR_BAD_PAGE),
+                              ([40, 6], torch.full_like(cache.table, 1000), m.DEVERR_BAD_PAGE),
+                              ([40, 6], torch.full_like(cache.table, -1), m.DEVERR_BAD_PAGE)):
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        kc, vc, ks, vs = _empty(cache)
+        m.mnw_kv_append(q, k, v, kc, vc, table, torch.tensor(lens, dtype=torch.int32, device="cuda"), inv_freq=f, err=err,
+                        k_scale=ks, v_scale=vs)
+        assert m.mnw_moe_read_error(err) & code == code
+        written = int((ks != 0).any(-1).any(1).sum())
+        assert written <= (3 if code & m.DEVERR_BAD_LENGTH else 0)
+        assert torch.equal((ks != 0).any(-1), (kc != 0).any(-1))
+
+
 # ---- attention ----
 
 
@@ -140,6 +184,21 @@ def test_attention_of_wide_scores_and_spread_values():
         q = _randn((1, Hq, d), 4, 30.0)
         out, lse = M().mnw_attn_paged(q, cache.k, cache.v, cache.table, cache.cache_lens, 1, d ** -0.5, want_lse=True, **cache.kw())
         U.check_attention(out, lse, q, [1], cache, 1, d ** -0.5, lost=LOST)
+
+
+def test_attention_of_huge_scores():
+    """Scores of 10^31 in both directions: the largest key's value alone, and finite statistics."""
+    m = M()
+    cache = I4.Cache([50], 16, 1, 128, seed=5, spread=0.0)
+    for Hq in (4, 40):
+        for sign in (1.0, -1.0):
+            q = torch.full((1, Hq, 128), sign * 2.0 ** 100, dtype=torch.bfloat16, device="cuda")
+            out, lse = m.mnw_attn_paged(q, cache.k, cache.v, cache.table, cache.cache_lens, 1, 1.0, want_lse=True, **cache.kw())
+            s = sign * 2.0 ** 100 * cache.rows[0][0][:, 0].sum(1)
+            best = int(s.argmax())
+            want = cache.rows[0][1][best, 0]
+            assert ((out[0].double().cpu() - want).abs() <= (2.0 ** -8 + 2.0 ** -11) * want.abs()).all()
+            assert ((lse[0].double().cpu() - s[best]).abs() <= 2.0 ** -16 * s[best].abs()).all()
 
 
 def test_attention_of_zero_queries_zero_rows_and_empty_sequences():
@@ -240,6 +299,21 @@ def test_values(d, page, Hkv, joint):
     got = m.mnw_kv_values(int8.v, int8.vs)
     want = (int8.v.float() * int8.vs[..., None]).bfloat16()
     assert torch.equal(torch.nan_to_num(got, nan=-7.5), torch.nan_to_num(want, nan=-7.5))
+
+
+def test_values_of_more_chunks_than_31_bits():
+    m = M()
+    Hkv, page, d = 8, 256, 128
+    n_pages = (1 << 31) // (Hkv * page * (d // 8)) + 3
+    cache = torch.zeros((n_pages, Hkv, page, d // 2), dtype=torch.uint8, device="cuda")
+    rec = torch.zeros((n_pages, Hkv, page, 8), dtype=torch.uint8, device="cuda")
+    small = I4.Cache([3 * page], page, Hkv, d, seed=3, spread=0.0)
+    far = torch.tensor([0, n_pages // 2, n_pages - 1], device="cuda")
+    own = small.table[0, :3].long()
+    cache[far], rec[far] = small.k[own], small.ks[own]
+    got = m.mnw_kv_values(cache, rec)
+    assert torch.equal(got[far], m.mnw_kv_values(small.k[own], small.ks[own]))
+    assert (got[1] == 0).all() and (got[n_pages - 2] == 0).all()
 
 
 # ---- together ----

@@ -25,7 +25,7 @@ def call(lib, **kw):  # noqa: F811
     (dict(o=None), INVALID), (dict(x=P(8)), INVALID), (dict(a=P(8)), INVALID), (dict(b=P(24)), INVALID),
     (dict(i=P(2)), INVALID), (dict(s=P(2)), INVALID), (dict(r=P(2)), INVALID), (dict(y=P(8)), INVALID), (dict(o=P(8)), INVALID),
     (dict(T=1100, ws=None), INVALID), (dict(T=1100, wsb=100), SMALL), (dict(ws=P(128)), INVALID), (dict(xs=248), INVALID), (dict(xs=260), INVALID), (dict(ys=120), INVALID), (dict(ys=132), INVALID),
-    (dict(os=120), INVALID), (dict(os=132), INVALID), (dict(o=BIG, os=256), INVALID),
+    (dict(os=120), INVALID), (dict(os=132), INVALID), (dict(o=BIG, os=256), INVALID), (dict(x=P(1 << 23), o=P(1 << 23)), INVALID),
 ])
 def test_refusals(lib, kw, want):  # noqa: F811
     assert call(lib, **kw) == want
