@@ -7,8 +7,22 @@
 // as two BF16 terms (v to 2^-16), so the output's rounding is the only one that
 // counts.
 //
-// Tokens are grouped by adapter first (in order, so results do not depend on
-// timing), then cut into tiles of one adapter.
+// Bound: x, y and the adapters in use are read once and out is written once, 2 R
+// flops a byte at most, so memory is the floor for many tokens; for few it is
+// the chain adapter -> tokens -> x and A -> v -> out.  Two forms:
+//  - up to 1024 tokens one kernel, a cluster of eight CTAs per tile of 32 or 16
+//    tokens of one adapter, each of which finds its tile by itself;
+//  - above, three: tokens are listed by adapter, v = A x and out = y + s B v on
+//    tcgen05 with 128 tokens a tile.
+// Each token's result depends on its own row alone, so it is the same however
+// tokens are arranged.
+//
+// Measured on one GB300 (device time in a replayed graph; one kernel and three):
+// 64 tokens of 24 adapters, H = 4096, N = 5120, R = 16: 7.7 and 29.4 us; 512
+// tokens in runs of 32, R = 64: 14.0 and 22.9; 1024, R = 64: 27.3 and 27.9, in
+// any order 31.5 and 32.4.  9000 tokens of 4 adapters, R = 64 (262 MB): 68 us,
+// 3.9 TB/s: 4 us listing, 20 the first product, 43 the second.  With warp-level
+// products these two took 28 and 60 us.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -288,7 +302,8 @@ __global__ void __launch_bounds__(kThreads, NR <= 8 ? 2 : 1) lora_shrink_kernel(
 // ---- out = y + s B v on tcgen05: a tile of tokens and some columns, a block of kCols at a time ----
 // y comes by cp.async, whole rows of a block, into shared memory, where the product is added, and leaves from there in
 // rows; v lies there as two operands, its two terms.  While one block is worked on, the next one's y and B are under way.
-// (Rows of 384 bytes as bulk copies, in and out: 59 us for the case below; so: BULK_TIME.)
+// (9000 tokens, N = 5120: 43 us.  With rows of y and out as bulk copies of 384 bytes 59 us, two a token and block being
+// more than the copy unit takes; with 8 warps 51.)
 constexpr int kExpandThreads = 512;
 template <int NR>
 struct ExpandCfg {
