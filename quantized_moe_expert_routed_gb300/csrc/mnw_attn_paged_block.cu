@@ -173,9 +173,11 @@ struct RingPos {
 // The roles' waits are polled_wait()s, short in code: the kernel's has to stay
 // below the instruction cache's size (at 142 KB the INT8 form stalled for
 // thousands of cycles at a time).
+// SLEEP: with bounded_wait()'s suspensions, which leave the waiting warp's issue slots to the others.
+template <bool SLEEP>
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* err) {
   int ok = 1;
-  if ((threadIdx.x & 31) == 0) ok = polled_wait(bar, parity, abort, err) ? 1 : 0;
+  if ((threadIdx.x & 31) == 0) ok = (SLEEP ? bounded_wait(bar, parity, abort, err) : polled_wait(bar, parity, abort, err)) ? 1 : 0;
   ok = __shfl_sync(0xffffffffu, ok, 0);
   __syncwarp();
   return ok != 0;
@@ -256,6 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                        const int whole_pages) {
   using C = BCfg<D, FMT>;
   constexpr bool INT8 = C::INT8, INT4 = C::INT4;
+  constexpr bool kSleep = INT4;  // (heads of 64: 75.3 us polled, 73.4 so)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);  // (an offset: the pointer stays a shared-memory one)
   Bars* bars = reinterpret_cast<Bars*>(smem + C::kOffBars);
@@ -434,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         pending = nullptr;
       };
       for (int t = 0; ok && t < tiles; ++t) {
-        if (!warp_wait(&empty[ring.slot], ring.phase ^ 1, abort, a.err)) { ok = false; break; }
+        if (!warp_wait<kSleep>(&empty[ring.slot], ring.phase ^ 1, abort, a.err)) { ok = false; break; }
         uint64_t* bar = &full[ring.slot];
         const uint32_t at = ring_at + ring.slot * C::kTile;
         const bool rows = !whole || __any_sync(0xffffffffu, static_cast<unsigned>(page) >= static_cast<unsigned>(a.n_pages));
@@ -493,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       auto issue = [&]() -> bool {  // once the buffer's last tile is converted
         const uint32_t b = put.slot, to = raw_at + b * C::kRaw;
-        if (!warp_wait(&raw_empty[b], put.phase ^ 1, abort, a.err)) return false;
+        if (!warp_wait<kSleep>(&raw_empty[b], put.phase ^ 1, abort, a.err)) return false;
         if (!whole || __any_sync(0xffffffffu, static_cast<unsigned>(page) >= static_cast<unsigned>(a.n_pages))) {
           by_rows |= 1u << b;
           copy_rows(key0 / 32, (key0 + kMine) / 32, sbase + to, sbase + to + C::kCodes);  // (with the group's commit)
@@ -550,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (copier && lane == 0) mbar_arrive(&raw_full[b]);
         } else {
-          if (!warp_wait(&raw_full[b], get.phase, abort, a.err)) { ok = false; break; }
+          if (!warp_wait<kSleep>(&raw_full[b], get.phase, abort, a.err)) { ok = false; break; }
           under_way &= ~(1u << b);
         }
         const uint8_t* const raw = smem + raw_at + b * C::kRaw;
@@ -570,9 +573,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           sc_now += kStep;
           if (sc_now >= sc_slots) sc_now -= sc_slots;
         }
-        if (!warp_wait(&empty[ring.slot], ring.phase ^ 1, abort, a.err)) { ok = false; break; }
+        if (!warp_wait<kSleep>(&empty[ring.slot], ring.phase ^ 1, abort, a.err)) { ok = false; break; }
         uint8_t* const op = smem + ring_at + ring.slot * C::kTile;
-#pragma unroll 2
+#pragma unroll (D == 128 ? 4 : 2)
         for (int i = 0; i < kMine / 8; ++i) {
           const int row = row0 + 8 * i;
           uint32_t w[kGC];
@@ -627,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (landing_rows) {
           copy_rows(2 * lw, 2 * lw + 2, sbase + raw_at, sbase + scales_at(sc_issue));
         } else if (lw == 0) {
-          if (!warp_wait(raw_empty, (uses & 1) ^ 1, abort, a.err)) return false;
+          if (!warp_wait<kSleep>(raw_empty, (uses & 1) ^ 1, abort, a.err)) return false;
           if (lane == 0) mbar_arrive_expect_tx(raw_full, C::kRaw + kTK * 4);
           __syncwarp();
           if (lane < pieces) {
@@ -654,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_proxy_async_smem();  // rows came by this proxy, the next codes may come by the other
             __syncwarp();
           } else {
-            if (!(values ? warp_wait(raw_full, raw_phase, abort, a.err)
+            if (!(values ? warp_wait<kSleep>(raw_full, raw_phase, abort, a.err)
                          : warp_wait2(raw_full, raw_phase, &empty[ring.slot], ring.phase ^ 1, abort, a.err))) { ok = false; break; }
             raw_phase ^= 1;
             bulk_out = false;
@@ -729,9 +732,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       int seg = 0, left = 0;  // segment of the next scores, its tiles to go
       for (int t = 0; t < tiles; ++t) {
         if (left == 0) {
-          if (!warp_wait(&bars->seg_full[seg % kMaxSegs], (seg / kMaxSegs) & 1, abort, a.err)) break;
+          if (!warp_wait<kSleep>(&bars->seg_full[seg % kMaxSegs], (seg / kMaxSegs) & 1, abort, a.err)) break;
           left = bars->seg[seg % kMaxSegs].tiles;
-          if (!warp_wait(seg ? &bars->q_full : &bars->q0_full, seg ? (seg - 1) & 1 : 0, abort, a.err)) break;
+          if (!warp_wait<kSleep>(seg ? &bars->q_full : &bars->q0_full, seg ? (seg - 1) & 1 : 0, abort, a.err)) break;
         }
         if (!warp_wait2(&bars->full[0][kr.slot], kr.phase, &bars->s_free[buf.slot], buf.phase ^ 1, abort, a.err)) break;
         tc_fence_after();
@@ -764,10 +767,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       int seg = 0, left = 0, begin = 0;  // segment of the next product, its tiles to go, its first tile
       for (int t = 0; t < tiles; ++t) {
         if (left == 0) {
-          if (!warp_wait(&bars->seg_full[seg % kMaxSegs], (seg / kMaxSegs) & 1, abort, a.err)) break;
+          if (!warp_wait<kSleep>(&bars->seg_full[seg % kMaxSegs], (seg / kMaxSegs) & 1, abort, a.err)) break;
           left = bars->seg[seg % kMaxSegs].tiles;
           // the segment before has been read out of O
-          if (seg > 0 && !warp_wait(&bars->epi, (seg - 1) & 1, abort, a.err)) break;
+          if (seg > 0 && !warp_wait<kSleep>(&bars->epi, (seg - 1) & 1, abort, a.err)) break;
         }
         if (!warp_wait2(&bars->full[1][vr.slot], vr.phase, &bars->p_full[buf.slot], buf.phase, abort, a.err)) break;
         tc_fence_after();
@@ -811,7 +814,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(&bars->seg_full[seg % kMaxSegs]);
         }
         if (seg > 0) {  // (the first segment's: the softmax warps)
-          if (!warp_wait(&bars->q_empty, (seg - 1) & 1, abort, a.err)) break;
+          if (!warp_wait<kSleep>(&bars->q_empty, (seg - 1) & 1, abort, a.err)) break;
           query_rows(seg, qw * 64, 64);
           if (lane == 0) mbar_arrive(&bars->q_full);
         }
@@ -844,7 +847,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t ks_phase = 0, vs_phase = 0;
     RingPos buf;  // tile t's score buffer
     for (int seg = 0; ok && t < tiles; ++seg) {
-      if (!warp_wait(&bars->seg_full[seg % kMaxSegs], (seg / kMaxSegs) & 1, abort, a.err)) break;
+      if (!warp_wait<kSleep>(&bars->seg_full[seg % kMaxSegs], (seg / kMaxSegs) & 1, abort, a.err)) break;
       const Seg& sg = bars->seg[seg % kMaxSegs];
       const int rows = min(kRT, sg.s.n * a.G - sg.rt * kRT);
       const int end = t + sg.tiles;
@@ -861,7 +864,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (INT8) {
           if (!warp_poll2(&bars->ks_full[ks_slot], ks_phase, &bars->vs_full[vs_slot], vs_phase, abort, a.err)) { ok = false; break; }
         }
-        if (!warp_wait(&bars->s_full[buf.slot], buf.phase, abort, a.err)) { ok = false; break; }
+        if (!warp_wait<kSleep>(&bars->s_full[buf.slot], buf.phase, abort, a.err)) { ok = false; break; }
         const uint32_t s_at = at16 + buf.slot * kTK;
         const float *ks = nullptr, *vs = nullptr;
         if constexpr (INT8) {
@@ -909,7 +912,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // O and the rows' sums to another unit; the product before has to be complete
         auto rescale = [&](const float (&alpha)[2]) -> bool {
           if (t == begin || !__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) return true;
-          if (!warp_wait(&bars->s_free[(t - 1) % C::kBufs], ((t - 1) / C::kBufs) & 1, abort, a.err)) return false;
+          if (!warp_wait<kSleep>(&bars->s_free[(t - 1) % C::kBufs], ((t - 1) / C::kBufs) & 1, abort, a.err)) return false;
           tc_fence_after();
 #pragma unroll 1
           for (int i = 0; i < D; i += 64) {
@@ -1114,7 +1117,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             a.lse[row[x]] = (INT4 ? (sum == 0.f ? -INFINITY : all) : rs.m + log2f(sum)) * kLn2;
         }
       }
-      if (!warp_wait(&bars->o_full, seg & 1, abort, a.err)) break;
+      if (!warp_wait<kSleep>(&bars->o_full, seg & 1, abort, a.err)) break;
       tc_fence_after();
 #pragma unroll 1
       for (int i = 0; i < D; i += 64) {
