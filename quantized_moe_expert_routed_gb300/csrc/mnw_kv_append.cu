@@ -150,9 +150,13 @@ __global__ void __launch_bounds__(kThreads, FMT == MNW_KV_INT4 ? 4 : 0) kv_appen
   };
   load_batch(0);
 
-  // a warp per token: its sequence, position, slot and angles
-  if (warp < nt) {
-    const int t = t0 + warp;
+  // a warp per token (INT4, whose angles take longer: two): its sequence, position, slot and angles
+  constexpr int kPer = FMT == MNW_KV_INT4 ? 2 : 1;
+  static_assert(kMaxTokens * kPer <= kThreads / 32);
+  const int tw = warp / kPer;
+  const bool first = lane == 0 && warp % kPer == 0;
+  if (tw < nt) {
+    const int t = t0 + tw;
     int b;
     if (a.bt.q_start) {
       int cnt = 0;  // sequences that end at or before t
@@ -173,19 +177,19 @@ __global__ void __launch_bounds__(kThreads, FMT == MNW_KV_INT4 ? 4 : 0) kv_appen
         page = __ldg(a.bt.block_table + static_cast<size_t>(b) * a.bt.max_pages + pi);
         if (page < 0 || page >= a.n_pages) {
           page = -1;
-          if (lane == 0 && a.err) atomicOr(a.err, MNW_DEVERR_BAD_PAGE);
+          if (first && a.err) atomicOr(a.err, MNW_DEVERR_BAD_PAGE);
         }
       } else {
         bad = true;
-        if (pos >= s.len && lane == 0 && a.err) atomicOr(a.err, MNW_DEVERR_BAD_PAGE);  // past the table: no page
+        if (pos >= s.len && first && a.err) atomicOr(a.err, MNW_DEVERR_BAD_PAGE);  // past the table: no page
       }
     }
-    if (bad && lane == 0 && a.err) atomicOr(a.err, MNW_DEVERR_BAD_LENGTH);
-    if (lane == 0) {
-      page_of[warp] = page;
-      slot_of[warp] = slot;
+    if (bad && first && a.err) atomicOr(a.err, MNW_DEVERR_BAD_LENGTH);
+    if (first) {
+      page_of[tw] = page;
+      slot_of[tw] = slot;
     }
-    for (int i = lane; i < pairs; i += 32) {
+    for (int i = lane + 32 * (warp % kPer); i < pairs; i += 32 * kPer) {
       float sn, co;
       const float f = __ldg(a.inv_freq + i);
       if constexpr (FMT == MNW_KV_INT4) {
@@ -195,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, FMT == MNW_KV_INT4 ? 4 : 0) kv_appen
       } else {
         sincospif(2.f * turn_fraction(static_cast<uint32_t>(pos), f), &sn, &co);
       }
-      reinterpret_cast<float2*>(&cs[warp][(i & 7) >> 1][i >> 3])[i & 1] = make_float2(co * a.mscale, sn * a.mscale);
+      reinterpret_cast<float2*>(&cs[tw][(i & 7) >> 1][i >> 3])[i & 1] = make_float2(co * a.mscale, sn * a.mscale);
     }
   }
   __syncthreads();
