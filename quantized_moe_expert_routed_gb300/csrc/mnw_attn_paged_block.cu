@@ -49,10 +49,10 @@
 // converted, and give scales and operand tiles on as for INT8.  The softmax
 // keeps one reference a row for the probabilities and their products with the
 // values' scales, and computes no maximum as long as that serves.  The same two
-// cases over INT4 take 40.6 and 75.5 us (the second over INT8 106): 4200 clocks
-// a tile with heads of 128, 2700 with 64, not one stage's, as halving the
-// softmax's work or leaving out the conversion takes 5 to 10 % off; instruction
-// fetches are the largest stall.
+// cases over INT4 take 39.4 and 73.5 us (the second over INT8 106): 4200 clocks
+// a tile with heads of 128, 2700 with 64, not one stage's: halving the
+// softmax's exponentials takes 5 to 10 % off, leaving out its check of the
+// products 2 to 5.  With heads of 128 instruction fetches are the largest stall.
 //
 // BF16 caches: P is rounded to BF16 relative to a running maximum that moves
 // only when it grows by more than 2^8.  INT8 caches: scores times the key's

@@ -21,8 +21,8 @@
 // 64 tokens of 24 adapters, H = 4096, N = 5120, R = 16: 7.7 and 29.4 us; 512
 // tokens in runs of 32, R = 64: 14.0 and 22.9; 1024, R = 64: 27.3 and 27.9, in
 // any order 31.5 and 32.4.  9000 tokens of 4 adapters, R = 64 (262 MB): 68 us,
-// 3.9 TB/s: 4 us listing, 20 the first product, 43 the second.  With warp-level
-// products these two took 28 and 60 us.
+// 3.9 TB/s.  Its kernels alone and cold: 7.5 us listing, 22 the first product, 45
+// the second; with warp-level products these two took 28 and 68.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, NR <= 8 ? 2 : 1) lora_shrink_kernel(
 // ---- out = y + s B v on tcgen05: a tile of tokens and some columns, a block of kCols at a time ----
 // y comes by cp.async, whole rows of a block, into shared memory, where the product is added, and leaves from there in
 // rows; v lies there as two operands, its two terms.  While one block is worked on, the next one's y and B are under way.
-// (9000 tokens, N = 5120: 43 us.  With rows of y and out as bulk copies of 384 bytes 59 us, two a token and block being
+// (9000 tokens, N = 5120, alone and cold: 45 us.  With rows of y and out as bulk copies of 384 bytes 59 us, two a token and block being
 // more than the copy unit takes; with 8 warps 51.)
 constexpr int kExpandThreads = 512;
 template <int NR>

@@ -1,5 +1,5 @@
 // mnw_turns.cuh -- sine and cosine of position * frequency, rounded to FP32 as
-// the exact values would be (but for about one in two thousand, which are one
+// the exact values would be (but for about one in ten thousand, which are one
 // step off).
 //
 // The angle is taken in turns and in fixed point (64-bit fraction, see
