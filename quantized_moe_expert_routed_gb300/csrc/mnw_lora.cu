@@ -160,6 +160,15 @@ template <int N>
 __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+// What the first BF16 term leaves of v, nothing of an infinite one; and the ranks that count, of the 4 from e on (an
+// infinite x times the zeros of the others would be NaN).
+__device__ __forceinline__ float rest_of(float v, uint32_t first) {
+  const float r = v - __uint_as_float(first);
+  return fabsf(r) < INFINITY ? r : 0.f;
+}
+__device__ __forceinline__ float4 ranks_of(float4 v, int e, int rank) {
+  return make_float4(e < rank ? v.x : 0.f, e + 1 < rank ? v.y : 0.f, e + 2 < rank ? v.z : 0.f, e + 3 < rank ? v.w : 0.f);
+}
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -407,9 +416,10 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const Ar
           f.w += z.w;
         }
       }
+      f = ranks_of(f, e, rank);
       const uint32_t h0 = pack_bf16x2(f.x, f.y), h1 = pack_bf16x2(f.z, f.w);
-      const uint32_t l0 = pack_bf16x2(f.x - __uint_as_float(h0 << 16), f.y - __uint_as_float(h0 & 0xFFFF0000u));
-      const uint32_t l1 = pack_bf16x2(f.z - __uint_as_float(h1 << 16), f.w - __uint_as_float(h1 & 0xFFFF0000u));
+      const uint32_t l0 = pack_bf16x2(rest_of(f.x, h0 << 16), rest_of(f.y, h0 & 0xFFFF0000u));
+      const uint32_t l1 = pack_bf16x2(rest_of(f.z, h1 << 16), rest_of(f.w, h1 & 0xFFFF0000u));
       uint8_t* to = smem + (e >> 6) * C::kPieceA + r * 128 + ((((e & 63) >> 3) ^ (r & 7)) << 4) + (e & 4) * 2;
       *reinterpret_cast<uint2*>(to) = make_uint2(h0, h1);
       *reinterpret_cast<uint2*>(to + C::kPieces * C::kPieceA) = make_uint2(l0, l1);
@@ -710,9 +720,10 @@ __global__ void __launch_bounds__(kThreads, NR <= 8 ? 2 : 1) lora_few_kernel(con
           s.w += z.w;
         }
       }
+      s = ranks_of(s, e % kRp, rank);
       const uint32_t h0 = pack_bf16x2(s.x, s.y), h1 = pack_bf16x2(s.z, s.w);
-      const uint32_t l0 = pack_bf16x2(s.x - __uint_as_float(h0 << 16), s.y - __uint_as_float(h0 & 0xFFFF0000u));
-      const uint32_t l1 = pack_bf16x2(s.z - __uint_as_float(h1 << 16), s.w - __uint_as_float(h1 & 0xFFFF0000u));
+      const uint32_t l0 = pack_bf16x2(rest_of(s.x, h0 << 16), rest_of(s.y, h0 & 0xFFFF0000u));
+      const uint32_t l1 = pack_bf16x2(rest_of(s.z, h1 << 16), rest_of(s.w, h1 & 0xFFFF0000u));
       uint8_t* to = smem + C::kOffV + (e / kRp * C::kRowV + e % kRp) * 2;
       *reinterpret_cast<uint2*>(to) = make_uint2(h0, h1);
       *reinterpret_cast<uint2*>(to + kTF * C::kRowV * 2) = make_uint2(l0, l1);

@@ -89,6 +89,25 @@ def test_ranks_and_what_lies_past_them(T, R):
     assert torch.equal(got[ids == 0], y[ids == 0])
 
 
+@pytest.mark.parametrize("T,R,r", [(7, 16, 1), (40, 32, 3), (300, 64, 9), (2000, 24, 1), (2000, 128, 70)])
+def test_infinities_stay_what_the_formula_makes_of_them(T, R, r):
+    """An infinite input, and finite ones whose inner sum passes BF16 or FP32: infinite outputs where the formula has
+    those, in their rows alone."""
+    H, N = 264, 136
+    y, x, a, b, ids = inputs(T, H, N, R, 2, 900 + T, "one")
+    ids[1] = 0  # (a tile of its own)
+    a, b = a.abs() + 2.0 ** -6, b.abs() + 2.0 ** -6  # terms of one sign: no infinity meets another
+    ranks = torch.tensor([r, r], dtype=torch.int32, device="cuda")
+    x[1, 5] = float("inf")
+    x[2, 0] = float("-inf")
+    x[3] = 2.0 ** 127       # passes FP32 in the sum
+    got = M().mnw_lora_add(y, x, a, b, ids, None, ranks)
+    assert (got[1] == float("inf")).all() and (got[2] == float("-inf")).all() and (got[3] == float("inf")).all()
+    rest = torch.arange(T, device="cuda")
+    rest = rest[(rest == 0) | (rest > 3)]
+    check(got[rest], y[rest], x[rest], a, b, ids[rest], None, ranks)
+
+
 @pytest.mark.parametrize("T", [1, 5, 130, 1500])
 def test_slices_of_wider_tensors(T):
     H, N, n = 512, 264, 3
