@@ -20,7 +20,7 @@
 // Measured on one GB300 (device time in a replayed graph; one kernel and three):
 // 64 tokens of 24 adapters, H = 4096, N = 5120, R = 16: 7.7 and 29.4 us; 512
 // tokens in runs of 32, R = 64: 14.0 and 22.9; 1024, R = 64: 27.3 and 27.9, in
-// any order 31.5 and 32.4.  9000 tokens of 4 adapters, R = 64 (262 MB): 68 us,
+// any order 31.5 and 32.4.  9000 tokens of 4 adapters, R = 64 (262 MB): 66 us,
 // 3.9 TB/s.  Its kernels alone and cold: 7.5 us listing, 22 the first product, 45
 // the second; with warp-level products these two took 28 and 68.
 #include <cuda_bf16.h>
@@ -311,8 +311,8 @@ __global__ void __launch_bounds__(kThreads, NR <= 8 ? 2 : 1) lora_shrink_kernel(
 // ---- out = y + s B v on tcgen05: a tile of tokens and some columns, a block of kCols at a time ----
 // y comes by cp.async, whole rows of a block, into shared memory, where the product is added, and leaves from there in
 // rows; v lies there as two operands, its two terms.  While one block is worked on, the next one's y and B are under way.
-// (9000 tokens, N = 5120, alone and cold: 45 us.  With rows of y and out as bulk copies of 384 bytes 59 us, two a token and block being
-// more than the copy unit takes; with 8 warps 51.)
+// (9000 tokens, N = 5120, in a graph: 66 us with all before it, 61 with the copies alone.  With rows of y and out as bulk copies of 384 bytes 59 us, two a token and block being
+// more than the copy unit takes, 14 us more; with 8 warps 6 more; in three stages of 128 columns, or two CTAs an SM, 0 to 3 more.)
 constexpr int kExpandThreads = 512;
 template <int NR>
 struct ExpandCfg {
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const Ar
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ Tile tile_sh;
   __shared__ uint64_t d_full[2];
-  __shared__ int tokens[kTT];
+  __shared__ long long y_row[kTT], out_row[kTT];  // first elements of the tokens' rows
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -344,17 +344,22 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const Ar
     return;
   }
   const int blocks_all = (a.N + kCols - 1) / kCols;
-  const int b0 = static_cast<int>(static_cast<long long>(blocks_all) * blockIdx.y / a.spans);
-  const int b1 = static_cast<int>(static_cast<long long>(blocks_all) * (blockIdx.y + 1) / a.spans);
-  if (tid < kTT) tokens[tid] = tid < tl.count ? __ldcg(a.order + tl.first + tid) : 0;
+  // every spans-th block is this CTA's, so that the CTAs of a tile go along its rows together
+  const int blocks = (blocks_all - static_cast<int>(blockIdx.y) + a.spans - 1) / a.spans;
+  auto column = [&](int b) { return (b * a.spans + static_cast<int>(blockIdx.y)) * kCols; };
+  if (tid < kTT) {
+    const int t = tid < tl.count ? __ldcg(a.order + tl.first + tid) : 0;
+    y_row[tid] = t * a.y_stride;
+    out_row[tid] = t * a.out_stride;
+  }
   if (none) {  // y as it is
     pdl_wait();
     __syncthreads();
-    const int c0 = b0 * kCols / 8, c1 = min(b1 * kCols, a.N) / 8, w = c1 - c0;
+    const int chunks = a.N / 8, c0 = static_cast<int>(static_cast<long long>(chunks) * blockIdx.y / a.spans);
+    const int w = static_cast<int>(static_cast<long long>(chunks) * (blockIdx.y + 1) / a.spans) - c0;
     for (long long i = tid; i < static_cast<long long>(tl.count) * w; i += kExpandThreads) {
-      const int r = static_cast<int>(i / w), c = c0 + static_cast<int>(i % w);
-      const long long t = tokens[r];
-      *reinterpret_cast<uint4*>(a.out + t * a.out_stride + c * 8) = __ldcg(reinterpret_cast<const uint4*>(a.y + t * a.y_stride + c * 8));
+      const int r = static_cast<int>(i / w), c = (c0 + static_cast<int>(i % w)) * 8;
+      *reinterpret_cast<uint4*>(a.out + out_row[r] + c) = __ldcg(reinterpret_cast<const uint4*>(a.y + y_row[r] + c));
     }
     return;
   }
@@ -362,27 +367,29 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const Ar
   const uint32_t sbase = smem_u32(smem);
   const int rank = rank_of(a, tl.bin);
   const __nv_bfloat16* const wb = a.b + static_cast<long long>(tl.bin) * a.N * a.R;
-  constexpr int kChunks = kCols / 8;  // of a row of a block
-  const uint32_t y_at = C::kOffY;
-  // y's rows into shared memory (in), or out's from there
+  // y's rows into shared memory (in), or out's from there: a warp a row or two, a chunk of 8 columns a lane
+  constexpr int kChunks = kCols / 8, kAtOnce = 32 / kChunks;
+  const int rc = lane % kChunks, rr = lane / kChunks * (kExpandThreads / 32) + warp;
+  const uint32_t r_at = C::kOffY + rr * C::kRowY + rc * 16;
   auto rows = [&](int b, bool in) {
-    const int left = (a.N - b * kCols) / 8;  // chunks to the end
-    const uint32_t slot = y_at + ((b - b0) & 1) * C::kBytesY;
-    for (int i = tid; i < tl.count * kChunks; i += kExpandThreads) {
-      const int r = i / kChunks, c = i % kChunks;
-      if (c >= left) continue;
-      const long long t = tokens[r], col = static_cast<long long>(b) * kCols + c * 8;
-      const uint32_t at = slot + r * C::kRowY + c * 16;
+    const int col = column(b) + rc * 8;
+    if (lane >= kAtOnce * kChunks || col >= a.N) return;
+    const uint32_t at = r_at + (b & 1) * C::kBytesY;
+    constexpr int kStep = kAtOnce * (kExpandThreads / 32);
+#pragma unroll
+    for (int i = 0; i < kTT / kStep; ++i) {
+      const int r = rr + i * kStep;
+      if (r >= tl.count) break;
       if (in)
-        cp_async16(sbase + at, a.y + t * a.y_stride + col, 16);
+        cp_async16(sbase + at + i * (kStep * C::kRowY), a.y + y_row[r] + col, 16);
       else
-        *reinterpret_cast<uint4*>(a.out + t * a.out_stride + col) = *reinterpret_cast<const uint4*>(smem + at);
+        *reinterpret_cast<uint4*>(a.out + out_row[r] + col) = *reinterpret_cast<const uint4*>(smem + at + i * (kStep * C::kRowY));
     }
   };
   auto load_b = [&](int b) {
-    const uint32_t to = sbase + C::kOffB + ((b - b0) & 1) * C::kBytesB;
+    const uint32_t to = sbase + C::kOffB + (b & 1) * C::kBytesB;
     for (int i = tid; i < kCols * NR; i += kExpandThreads) {
-      const int n = i / NR, c = i % NR, col = b * kCols + n, left = min(16, 2 * (rank - c * 8));  // (a rank need not be a multiple of 8)
+      const int n = i / NR, c = i % NR, col = column(b) + n, left = min(16, 2 * (rank - c * 8));  // (a rank need not be a multiple of 8)
       const bool on = col < a.N && left > 0;
       cp_async16(sw128(to + (c >> 3) * C::kPieceB, n, c & 7), on ? wb + static_cast<long long>(col) * a.R + c * 8 : wb, on ? left : 0);
     }
@@ -392,9 +399,9 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const Ar
     abort_flag = 0;
     fence_barrier_init();
   }
-  load_b(b0);
+  load_b(0);
   __syncthreads();
-  rows(b0, true);
+  rows(0, true);
   cp_commit();
   pdl_wait();
   pdl_launch_dependents();
@@ -429,9 +436,9 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const Ar
   constexpr uint32_t idesc = idesc_f16(kTT, kCols, true);
   const int row = (warp & 3) * 32 + lane;  // of the product, in the end, and kShare columns of it
   constexpr int kShare = kCols * 4 / (kExpandThreads / 32);
-  for (int b = b0; b < b1; ++b) {
-    const int at = (b - b0) & 1;
-    const uint32_t phase = (b - b0) >> 1 & 1;
+  for (int b = 0; b < blocks; ++b) {
+    const int at = b & 1;
+    const uint32_t phase = b >> 1 & 1;
     cp_wait<0>();
     fence_proxy_async_smem();
     tc_fence_before();
@@ -448,7 +455,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const Ar
                  sdesc_sw128(bs + kk / 4 * C::kPieceB + (kk & 3) * 32), idesc, term > 0 || kk > 0);
       mma_commit(&d_full[at]);
     }
-    if (b + 1 < b1) {
+    if (b + 1 < blocks) {
       rows(b + 1, true);
       load_b(b + 1);
     }
@@ -456,7 +463,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const Ar
     bounded_wait(&d_full[at], phase, &abort_flag, a.err);
     __syncwarp();
     tc_fence_after();
-    uint8_t* const mine = smem + y_at + at * C::kBytesY + row * C::kRowY + (warp >> 2) * (kShare * 2);
+    uint8_t* const mine = smem + C::kOffY + at * C::kBytesY + row * C::kRowY + (warp >> 2) * (kShare * 2);
 #pragma unroll
     for (int c = 0; c < kShare; c += 16) {
       uint32_t d[16];
@@ -802,7 +809,7 @@ inline int splits_of(int T, int H) {
   const int tiles = (T + kTT - 1) / kTT;
   return std::max(1, std::min({2 * current_sm_count() / tiles, H / 256, 16}));
 }
-// Shares of N in the second product, for about `tiles` tiles and one CTA an SM: fewest rounds of blocks, where a CTA's
+// Shares of N in the second product, each some of its blocks, for about `tiles` tiles and one CTA an SM: fewest rounds of blocks, where a CTA's
 // beginning and end cost about one more.
 inline int spans_of(int tiles, int blocks) {
   const int sms = current_sm_count();
