@@ -10,6 +10,8 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.machinery
+import importlib.util
 import os
 
 import torch
@@ -101,6 +103,22 @@ def load() -> ctypes.CDLL:
             fn.argtypes = args
         _lib = lib
     return _lib
+
+
+_calls = None
+
+
+def _load_calls():
+    """The native form of the paged cache's and the adapters' calls (csrc/mnw_calls.cpp), bound to the library."""
+    global _calls
+    lib = load()
+    spec = importlib.util.spec_from_loader("mnw_calls", importlib.machinery.ExtensionFileLoader("mnw_calls", _build.CALLS))
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    mod.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in (
+        "mnw_kv_append", "mnw_attn_paged", "mnw_attn_paged_workspace_size", "mnw_kv_values", "mnw_lora_add", "mnw_lora_workspace_size")))
+    _calls = mod
+    return mod
 
 
 class MnwError(RuntimeError):
@@ -286,6 +304,8 @@ def mnw_attn_prefill(q, k, v, blk: int, scale: float, out=None, ws=None, err=Non
 
 
 # ---- the decode step around the layer: norm, paged cache, attention ----
+# The calls on the cache and the adapters' go through _calls where nothing is amiss; the Python below it takes the others:
+# a stream of the caller's, another device than the current one, and arguments that it refuses by name.
 
 
 def _need(t, dtype, what, dim=None):
@@ -453,6 +473,13 @@ def mnw_kv_append(q, k, v, k_cache, v_cache, block_table, cache_lens, inv_freq=N
     int32 [B], the new tokens included; q_start int32 [B + 1] or None (T / B
     tokens each).  inv_freq f32 [rot / 2] (None: no rotation); see
     mnw_rope_frequencies and include/mnw_moe.h."""
+    if stream is None:
+        r = (_calls or _load_calls()).kv_append(q, k, v, k_cache, v_cache, block_table, cache_lens, inv_freq, layout, mscale,
+                                                k_scale, v_scale, q_start, q_out, err)
+        if r.__class__ is int:
+            _check(r, "mnw_kv_append")
+        if r is not NotImplemented:
+            return r
     kc, vc, ks, vs, fmt, n_pages, page, page_stride, Hkv, d = _cache_args(k_cache, v_cache, k_scale, v_scale)
     B, most, tp, lp, sp = _batch_args(block_table, cache_lens, q_start)
     kp, T, hk, _, kst = _token_rows(k, "k", d)
@@ -498,6 +525,13 @@ def mnw_attn_paged(q, k_cache, v_cache, block_table, cache_lens, blk, scale, k_s
     (p // blk + 1) * blk.  Returns out [T, Hq, d] bf16, with want_lse or lse
     (out, lse f32 [T, Hq]).  ws: a uint8 device tensor of at least
     mnw_attn_paged_workspace_size bytes, 256-byte aligned."""
+    if stream is None:
+        r = (_calls or _load_calls()).attn_paged(q, k_cache, v_cache, block_table, cache_lens, blk, scale, k_scale, v_scale,
+                                                 q_start, out, lse, want_lse, ws, err)
+        if r.__class__ is int:
+            _check(r, "mnw_attn_paged")
+        if r is not NotImplemented:
+            return r
     kc, vc, ks, vs, fmt, n_pages, page, page_stride, Hkv, d = _cache_args(k_cache, v_cache, k_scale, v_scale)
     B, most, tp, lp, sp = _batch_args(block_table, cache_lens, q_start)
     qp, T, Hq, _, qst = _token_rows(q, "q", d)
@@ -531,6 +565,12 @@ def mnw_kv_values(cache, scale, out=None, stream=None):
     cache: int8 [n_pages, Hkv, page_size, d] with scales f32, or uint8
     [n_pages, Hkv, page_size, d / 2] with records uint8 [n_pages, Hkv,
     page_size, 8] (arguments as mnw_kv_append's)."""
+    if stream is None:
+        r = (_calls or _load_calls()).kv_values(cache, scale, out)
+        if r.__class__ is int:
+            _check(r, "mnw_kv_values")
+        if r is not NotImplemented:
+            return r
     dtype, shape, st = cache.dtype, cache.shape, cache.stride()
     if not cache.is_cuda or (dtype is not torch.int8 and dtype is not torch.uint8) or len(shape) != 4:
         raise MnwError("cache: expected a CUDA tensor of int8, or uint8 (two 4-bit codes a byte), and 4 dimensions")
@@ -577,6 +617,12 @@ def mnw_lora_add(y, x, a, b, adapter, scale=None, ranks=None, out=None, ws=None,
     f32 [n] or None (1); ranks int32 [n] or None (R): the rows of a and columns
     of b that count.  out may be y (in place).  ws: a uint8 device tensor of at
     least mnw_lora_workspace_size bytes, 256-byte aligned."""
+    if stream is None:
+        r = (_calls or _load_calls()).lora_add(y, x, a, b, adapter, scale, ranks, out, ws, err)
+        if r.__class__ is int:
+            _check(r, "mnw_lora_add")
+        if r is not NotImplemented:
+            return r
     yp, T, N, y_stride = _rows(y, "y")
     xp, Tx, H, x_stride = _rows(x, "x")
     if Tx != T:

@@ -1,21 +1,29 @@
 """Build libmnw_moe.so in-tree with nvcc for sm_103a.
 
 Each translation unit compiles in parallel, then one nvcc link makes the
-shared library next to this file.  No CMake, no torch extension machinery.
+shared library next to this file.  The binding of the decode step's calls
+(csrc/mnw_calls.cpp, a Python module on torch's C++ interface) compiles beside
+them with the host compiler.  No CMake, no torch extension machinery.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import os
+import re
 import shutil
 import subprocess
 import sys
+import sysconfig
+
+import torch
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmnw_moe.so")
+# for one torch and one Python, whose C++ interfaces differ between versions
+CALLS = os.path.join(HERE, "mnw_calls_" + re.sub(r"\W", "_", torch.__version__) + sysconfig.get_config_var("EXT_SUFFIX"))
 SOURCES = ["mnw_api.cu", "mnw_route.cu", "mnw_router.cu", "mnw_quant.cu", "mnw_gemm.cu", "mnw_gemm_rows.cu", "mnw_gemm_rows_a8.cu", "mnw_gemm_warp.cu",
            "mnw_gemm_warp_dep.cu", "mnw_static_ws.cu", "mnw_selftest.cu", "mnw_attention.cu",
            "mnw_norm.cu", "mnw_kv_append.cu", "mnw_attn_paged.cu",
@@ -32,6 +40,22 @@ def _nvcc() -> str:
     return cand
 
 
+def _compile_calls() -> None:
+    root = os.path.dirname(torch.__file__)
+    tmp = CALLS + f".{os.getpid()}.tmp"
+    include = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include"), INCLUDE]
+    lib = os.path.join(root, "lib")
+    cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", *(f for i in include for f in ("-isystem", i)),
+           os.path.join(CSRC, "mnw_calls.cpp"), "-o", tmp, "-L", lib, "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu",
+           "-ltorch_python", f"-Wl,-rpath,{lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"the compiler failed on mnw_calls.cpp:\n{r.stderr}")
+    os.replace(tmp, CALLS)
+
+
 def _deps():
     # sources, the public header and this file (its flags)
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "mnw_moe.h"),
@@ -40,7 +64,8 @@ def _deps():
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps():
+    new = _deps()
+    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= new for f in (LIB, CALLS)):
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
@@ -57,8 +82,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
             sys.stderr.write(r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        calls = ex.submit(_compile_calls)
         objs = list(ex.map(compile_one, SOURCES))
+        calls.result()
     tmp = LIB + f".{os.getpid()}.tmp"
     r = subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
     if r.returncode != 0:
