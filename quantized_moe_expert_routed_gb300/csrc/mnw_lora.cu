@@ -56,14 +56,14 @@ __device__ __forceinline__ int bin_of(const Args& a, int t) {
   const int id = __ldg(a.adapter + t);
   return static_cast<unsigned>(id) < static_cast<unsigned>(a.n) ? id : a.n;
 }
-__device__ __forceinline__ int rank_of(const Args& a, int i) {
-  const int r = a.ranks ? __ldcg(a.ranks + i) : a.R;
+__device__ __forceinline__ int checked_rank(const Args& a, int r) {
   if (static_cast<unsigned>(r) > static_cast<unsigned>(a.R)) {
     if (threadIdx.x == 0 && a.err) atomicOr(a.err, MNW_DEVERR_BAD_ADAPTER);
     return r < 0 ? 0 : a.R;
   }
   return r;
 }
+__device__ __forceinline__ int rank_of(const Args& a, int i) { return checked_rank(a, a.ranks ? __ldcg(a.ranks + i) : a.R); }
 
 // ---- grouping: CTA e lists the tokens of adapter e (e = n: of none) ----
 constexpr int kGroupThreads = 1024, kRun = 16;  // tokens of a thread at a time
@@ -536,7 +536,8 @@ __global__ void __launch_bounds__(kThreads, NR <= 8 ? 2 : 1) lora_few_kernel(con
   __shared__ short counts[kWarps][1026];
   __shared__ int warp_heads[kWarps];
   __shared__ int tokens[kTF];
-  __shared__ int tile_bin, tile_base, tile_count;
+  __shared__ int tile_bin, tile_base, tile_count, tile_rank;
+  __shared__ float tile_scale;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g8 = lane >> 2, t4 = lane & 3;
   const int cta = blockIdx.x % kCluster, q = blockIdx.x / kCluster;
   pdl_launch_dependents();
@@ -553,13 +554,20 @@ __global__ void __launch_bounds__(kThreads, NR <= 8 ? 2 : 1) lora_few_kernel(con
   // A warp numbers its share of the tokens by counts of its own, to which those of the warps before are added.
   const int share = (a.T + kThreads - 1) / kThreads * 32;
   constexpr int kMost = kFewTokens / kThreads;  // tokens of a lane
-  int bin_t[kMost], place_t[kMost];
+  int bin_t[kMost], place_t[kMost], rank_t[kMost];  // with the adapters' ranks and scales, on their way while tokens are numbered
+  float scale_t[kMost];
 #pragma unroll
   for (int i = 0; i < kMost; ++i) {
     const int t = warp * share + i * 32 + lane;
     const bool on = i * 32 < share && t < a.T;
     bin_t[i] = on ? bin_of(a, t) : -1;
     if (on && bin_t[i] == a.n && blockIdx.x == 0 && a.err && __ldg(a.adapter + t) != -1) atomicOr(a.err, MNW_DEVERR_BAD_ADAPTER);
+  }
+#pragma unroll
+  for (int i = 0; i < kMost; ++i) {
+    const bool one = bin_t[i] >= 0 && bin_t[i] < a.n;
+    rank_t[i] = one && a.ranks ? __ldcg(a.ranks + bin_t[i]) : a.R;
+    scale_t[i] = one && a.scale ? __ldcg(a.scale + bin_t[i]) : 1.f;
   }
 #pragma unroll
   for (int i = 0; i < kMost; ++i) {
@@ -591,6 +599,8 @@ __global__ void __launch_bounds__(kThreads, NR <= 8 ? 2 : 1) lora_few_kernel(con
     if (head && heads + __popc(hm & ((1u << lane) - 1u)) == q) {
       tile_bin = bin_t[i];
       tile_base = place_t[i];
+      tile_rank = rank_t[i];
+      tile_scale = scale_t[i];
     }
     heads += __popc(hm);
   }
@@ -607,8 +617,8 @@ __global__ void __launch_bounds__(kThreads, NR <= 8 ? 2 : 1) lora_few_kernel(con
       atomicAdd(&tile_count, 1);
     }
   }
-  const int rank = none ? 0 : rank_of(a, bin);
-  const float scale = none ? 0.f : (a.scale ? __ldg(a.scale + bin) : 1.f);
+  const int rank = none ? 0 : checked_rank(a, tile_rank);
+  const float scale = none ? 0.f : tile_scale;
   __syncthreads();
   const int count = tile_count;
 
