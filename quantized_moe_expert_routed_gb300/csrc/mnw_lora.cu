@@ -18,7 +18,7 @@
 // tokens are arranged.
 //
 // Measured on one GB300 (device time in a replayed graph; one kernel and three):
-// 64 tokens of 24 adapters, H = 4096, N = 5120, R = 16: 7.7 and 29.4 us; 512
+// 64 tokens of 24 adapters, H = 4096, N = 5120, R = 16: 6.0 and 29.4 us; 512
 // tokens in runs of 32, R = 64: 14.0 and 22.9; 1024, R = 64: 27.3 and 27.9, in
 // any order 31.5 and 32.4.  9000 tokens of 4 adapters, R = 64 (262 MB): 66 us,
 // 3.9 TB/s.  Its kernels alone and cold: 7.5 us listing, 22 the first product, 45
@@ -501,9 +501,10 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const Ar
 // share of N in the second.  Operands go from global memory to the instructions' registers, in an order of k that gives a
 // lane 16 neighbouring bytes; what the second product reads is asked for before the exchange.
 constexpr int kFewTokens = 1024, kCluster = 8;
-template <int NR>
+template <int NR, int MT>
 struct FewCfg {
-  static constexpr int kMT = NR <= 4 ? 2 : 1;       // 16-token operand tiles
+  static constexpr int kMT = MT;                    // 16-token operand tiles
+  static constexpr int kDeep = MT == 1 && NR <= 4 ? 2 : 1;  // groups of columns of a warp asked for ahead
   static constexpr int kTF = 16 * kMT;
   static constexpr int kRp = NR * 8, kWarps = kThreads / 32;
   static constexpr int kOffOwn = kWarps * kTF * kRp * 4;       // [kTF][kRp] the CTA's share of v, behind its warps' shares
@@ -528,9 +529,9 @@ __device__ __forceinline__ uint4 first_of(uint4 w, int left) {
   return make_uint4(keep(w.x, 0), keep(w.y, 2), keep(w.z, 4), keep(w.w, 6));
 }
 
-template <int NR>
+template <int NR, int MT>
 __global__ void __launch_bounds__(kThreads, NR <= 8 ? 2 : 1) lora_few_kernel(const Args a) {
-  using C = FewCfg<NR>;
+  using C = FewCfg<NR, MT>;
   constexpr int kMT = C::kMT, kTF = C::kTF, kRp = C::kRp, kWarps = C::kWarps;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ short counts[kWarps][1026];
@@ -629,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, NR <= 8 ? 2 : 1) lora_few_kernel(con
   constexpr int kB = NR == 2 ? 1 : NR / 4;  // chunks of a lane in a row of B
   struct Group {
     uint4 b[4][kB], y[kMT][2];
-  } ahead;  // (two of them: 64 tokens 7.3 -> 8.1 us)
+  } ahead[C::kDeep];
   auto fetch = [&](int g, Group& f) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -660,7 +661,9 @@ __global__ void __launch_bounds__(kThreads, NR <= 8 ? 2 : 1) lora_few_kernel(con
         if (t >= 0 && col < a.N) f.y[mt][x] = *reinterpret_cast<const uint4*>(a.y + t * a.y_stride + col);
       }
   };
-  if (g0 < g1) fetch(g0, ahead);
+#pragma unroll
+  for (int i = 0; i < C::kDeep; ++i)
+    if (g0 + i * kWarps < g1) fetch(g0 + i * kWarps, ahead[i]);
 
   // ---- v: this CTA's share of H ----
   const uint32_t sbase = smem_u32(smem);
@@ -797,7 +800,7 @@ __global__ void __launch_bounds__(kThreads, NR <= 8 ? 2 : 1) lora_few_kernel(con
         ow[mt][x] = none ? u : make_uint4(add(u.x, acc[mt][0][2 * x], acc[mt][0][2 * x + 1]), add(u.y, acc[mt][1][2 * x], acc[mt][1][2 * x + 1]),
                                           add(u.z, acc[mt][2][2 * x], acc[mt][2][2 * x + 1]), add(u.w, acc[mt][3][2 * x], acc[mt][3][2 * x + 1]));
       }
-    if (g + kWarps < g1) fetch(g + kWarps, f);
+    if (g + C::kDeep * kWarps < g1) fetch(g + C::kDeep * kWarps, f);
 #pragma unroll
     for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
@@ -806,7 +809,11 @@ __global__ void __launch_bounds__(kThreads, NR <= 8 ? 2 : 1) lora_few_kernel(con
         if (t >= 0 && col < a.N) *reinterpret_cast<uint4*>(a.out + t * a.out_stride + col) = ow[mt][x];
       }
   };
-  for (int g = g0; g < g1; g += kWarps) finish(g, ahead);
+  for (int g = g0; g < g1; g += C::kDeep * kWarps) {
+#pragma unroll
+    for (int i = 0; i < C::kDeep; ++i)
+      if (g + i * kWarps < g1) finish(g + i * kWarps, ahead[i]);
+  }
   if (!none) cluster_wait();  // a CTA's memory stays until the others have read it
 }
 
@@ -847,10 +854,10 @@ inline Workspace workspace_of(int T, int H, int R, int n) {
   return w;
 }
 
-template <int NR>
+template <int NR, int MT>
 int launch_few(const Args& a, cudaStream_t st) {
-  using C = FewCfg<NR>;
-  auto kern = lora_few_kernel<NR>;
+  using C = FewCfg<NR, MT>;
+  auto kern = lora_few_kernel<NR, MT>;
   static std::atomic<uint64_t> attr{0};
   uint64_t bit;
   if (attrs_needed(attr, &bit)) {
@@ -877,7 +884,14 @@ int launch_few(const Args& a, cudaStream_t st) {
 
 template <int NR>
 int launch(Args& a, uint8_t* ws, cudaStream_t st) {
-  if (a.T <= kFewTokens) return launch_few<NR>(a, st);
+  if (a.T <= kFewTokens) {
+    // Tiles of 16 tokens, whose registers hold two groups of columns ahead, while the GPU takes all of them at a time, and
+    // of 32 above.  H = 4096, N = 5120, R = 16 and 32: 64 tokens of one adapter 5.6 and 6.9 us (tiles of 32: 7.1 and 9.4),
+    // 512 of four 7.8 and 10.2 (10.1 and 13.5), 1024 of one 15.2 and 18.9 (11.1 and 14.8).
+    if constexpr (NR <= 4)
+      if (a.T / 16 > 2 * current_sm_count() / kCluster) return launch_few<NR, 2>(a, st);
+    return launch_few<NR, 1>(a, st);
+  }
   const Workspace w = workspace_of(a.T, a.H, a.R, a.n);
   a.starts = reinterpret_cast<int32_t*>(ws + w.starts);
   a.order = reinterpret_cast<int32_t*>(ws + w.order);
