@@ -96,6 +96,8 @@ __device__ __forceinline__ float rcp(float x) {
   return y;
 }
 
+__device__ __forceinline__ uint64_t twice(float x) { return f32x2_pack(__float_as_uint(x), __float_as_uint(x)); }
+
 // One CTA per `tokens` tokens.  A head row is D/16 pieces of two 16-byte
 // chunks, one thread each: the two that hold both elements of 8 rotation pairs
 // (half layout: chunks p and p + rot/16; elsewhere, and past rot, neighbours),
@@ -305,19 +307,20 @@ __global__ void __launch_bounds__(kThreads, FMT == MNW_KV_INT4 ? 4 : 0) kv_appen
           const float step = unit * static_cast<float>(mul >> (8 * ((e ? c1 : c0) / kGC)) & 0xFFu);
           const float rs = some ? rcp(step) : 0.f;
           // the codes of even and odd elements, a nibble each: rounded to an integer by the sum with 1.5 * 2^23
+          // (packed; whether the product is rounded before that sum or not, the check below holds)
           constexpr float kRound = 12582912.f;
-          float part[2] = {0.f, 0.f}, far = 0.f;
+          uint64_t part = 0ull;
+          float far = 0.f;
 #pragma unroll
-          for (int j = 3; j >= 0; --j)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const float y = __uint_as_float(x ? u[e][j] & 0xFFFF0000u : u[e][j] << 16);
-              const float r = y * rs, n = __fadd_rn(__fadd_rn(r, kRound), -kRound);
-              far = fmaxf(far, fabsf(r - n));
-              part[x] = fmaf(part[x], 16.f, n);
-            }
-          // + 8 in each nibble
-          words[e] = (__float_as_uint(part[0] + (kRound + 34952.f)) & 0xFFFFu) | __float_as_uint(part[1] + (kRound + 34952.f)) << 16;
+          for (int j = 3; j >= 0; --j) {
+            const uint64_t r = f32x2_mul(f32x2_pack(u[e][j] << 16, u[e][j] & 0xFFFF0000u), twice(rs));
+            const uint64_t n = f32x2_add(f32x2_add(r, twice(kRound)), twice(-kRound));
+            const uint64_t off = f32x2_fma(n, twice(-1.f), r);
+            far = fmaxf(fmaxf(far, fabsf(__uint_as_float(static_cast<uint32_t>(off)))), fabsf(__uint_as_float(static_cast<uint32_t>(off >> 32))));
+            part = f32x2_fma(part, twice(16.f), n);
+          }
+          part = f32x2_add(part, twice(kRound + 34952.f));  // + 8 in each nibble
+          words[e] = prmt(static_cast<uint32_t>(part), static_cast<uint32_t>(part >> 32), 0x5410u);
           // y rs is within 2^-19 of y / step: a quotient that lies that close to a half is worked out exactly
           if (far > 0.5f - 0x1p-17f) {
             words[e] = 0;
