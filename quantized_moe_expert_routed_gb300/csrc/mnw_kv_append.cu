@@ -96,7 +96,10 @@ __device__ __forceinline__ float rcp(float x) {
   return y;
 }
 
-__device__ __forceinline__ uint64_t twice(float x) { return f32x2_pack(__float_as_uint(x), __float_as_uint(x)); }
+__device__ __forceinline__ uint64_t two(float x, float y) { return f32x2_pack(__float_as_uint(x), __float_as_uint(y)); }
+__device__ __forceinline__ uint64_t twice(float x) { return two(x, x); }
+__device__ __forceinline__ float lo32(uint64_t x) { return __uint_as_float(static_cast<uint32_t>(x)); }
+__device__ __forceinline__ float hi32(uint64_t x) { return __uint_as_float(static_cast<uint32_t>(x >> 32)); }
 
 // One CTA per `tokens` tokens.  A head row is D/16 pieces of two 16-byte
 // chunks, one thread each: the two that hold both elements of 8 rotation pairs
@@ -108,6 +111,7 @@ template <int D, int FMT, bool HALF>
 __global__ void __launch_bounds__(kThreads, FMT == MNW_KV_INT4 ? 4 : 0) kv_append_kernel(const Args a) {
   constexpr int P = D / 16;  // pieces (threads) of a row
   // sine and cosine, two pairs a word: pairs 8 p + 2 j, 8 p + 2 j + 1 at [j][p], so that a row's lanes read neighbours
+  // (INT4: both cosines, both sines)
   __shared__ float4 cs[kMaxTokens][4][kMaxPairs / 8];
   __shared__ int page_of[kMaxTokens], slot_of[kMaxTokens];  // the token's page (-1: none) and its slot there
   pdl_launch_dependents();
@@ -201,10 +205,20 @@ __global__ void __launch_bounds__(kThreads, FMT == MNW_KV_INT4 ? 4 : 0) kv_appen
       } else {
         sincospif(2.f * turn_fraction(static_cast<uint32_t>(pos), f), &sn, &co);
       }
-      reinterpret_cast<float2*>(&cs[tw][(i & 7) >> 1][i >> 3])[i & 1] = make_float2(co * a.mscale, sn * a.mscale);
+      float* const to = &cs[tw][(i & 7) >> 1][i >> 3].x;
+      if constexpr (FMT == MNW_KV_INT4) {
+        to[i & 1] = co * a.mscale;
+        to[2 + (i & 1)] = sn * a.mscale;
+      } else {
+        reinterpret_cast<float2*>(to)[i & 1] = make_float2(co * a.mscale, sn * a.mscale);
+      }
     }
   }
   __syncthreads();
+
+  // ones that the compiler does not know for such (Hkv > 0): it would join a packed sum with the product in it
+  const uint32_t nought = static_cast<uint32_t>(a.Hkv >> 31);
+  const uint64_t plus = f32x2_pack(0x3F800000u | nought, 0x3F800000u | nought), minus = f32x2_pack(0xBF800000u | nought, 0xBF800000u | nought);
 
 #pragma unroll 1
   for (int base = 0; base < total; base += kBatch * kThreads) {
@@ -220,28 +234,30 @@ __global__ void __launch_bounds__(kThreads, FMT == MNW_KV_INT4 ? 4 : 0) kv_appen
       const int h = is_q ? row : (is_k ? row - q_rows : row - q_rows - a.Hkv);
       uint32_t u[2][4] = {{raw[i][0].x, raw[i][0].y, raw[i][0].z, raw[i][0].w}, {raw[i][1].x, raw[i][1].y, raw[i][1].z, raw[i][1].w}};
       if (in_rot && (is_q || is_k)) {
-        // u cos a - w sin a and u cos a + w sin a (INT4: each operation rounded, see above)
-        auto less = [](float u, float c, float w, float s) {
-          return FMT == MNW_KV_INT4 ? __fsub_rn(__fmul_rn(u, c), __fmul_rn(w, s)) : u * c - w * s;
-        };
-        auto plus = [](float u, float c, float w, float s) {
-          return FMT == MNW_KV_INT4 ? __fadd_rn(__fmul_rn(u, c), __fmul_rn(w, s)) : u * c + w * s;
-        };
         auto lo = [](uint32_t w) { return __uint_as_float(w << 16); };
         auto hi = [](uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); };
 #pragma unroll
         for (int j = 0; j < 4; ++j) {  // pairs 8 p + 2 j, 8 p + 2 j + 1
           const float4 f = cs[tk][j][p];
-          if constexpr (HALF) {
-            const float x0 = lo(u[0][j]), x1 = hi(u[0][j]), w0 = lo(u[1][j]), w1 = hi(u[1][j]);
-            u[0][j] = pack_bf16x2(less(x0, f.x, w0, f.y), less(x1, f.z, w1, f.w));
-            u[1][j] = pack_bf16x2(plus(w0, f.x, x0, f.y), plus(w1, f.z, x1, f.w));
+          uint32_t &a0 = HALF ? u[0][j] : u[j >> 1][2 * (j & 1)], &a1 = HALF ? u[1][j] : u[j >> 1][2 * (j & 1) + 1];
+          // two pairs (x, w): x0 and x1 in a0, w0 and w1 in a1, or (interleaved) a pair each
+          const float x0 = lo(a0), x1 = HALF ? hi(a0) : lo(a1), w0 = HALF ? lo(a1) : hi(a0), w1 = hi(a1);
+          float y0, y1, z0, z1;  // x cos a - w sin a, w cos a + x sin a
+          if constexpr (FMT == MNW_KV_INT4) {  // every operation rounded by itself, see above
+            const uint64_t x = two(x0, x1), w = two(w0, w1), c = two(f.x, f.y), sn = two(f.z, f.w);
+            const uint64_t y = f32x2_fma(f32x2_mul(w, sn), minus, f32x2_mul(x, c)), z = f32x2_fma(f32x2_mul(x, sn), plus, f32x2_mul(w, c));
+            y0 = lo32(y);
+            y1 = hi32(y);
+            z0 = lo32(z);
+            z1 = hi32(z);
           } else {
-            uint32_t &a0 = u[j >> 1][2 * (j & 1)], &a1 = u[j >> 1][2 * (j & 1) + 1];
-            const float x0 = lo(a0), w0 = hi(a0), x1 = lo(a1), w1 = hi(a1);
-            a0 = pack_bf16x2(less(x0, f.x, w0, f.y), plus(w0, f.x, x0, f.y));
-            a1 = pack_bf16x2(less(x1, f.z, w1, f.w), plus(w1, f.z, x1, f.w));
+            y0 = x0 * f.x - w0 * f.y;
+            y1 = x1 * f.z - w1 * f.w;
+            z0 = w0 * f.x + x0 * f.y;
+            z1 = w1 * f.z + x1 * f.w;
           }
+          a0 = HALF ? pack_bf16x2(y0, y1) : pack_bf16x2(y0, z0);
+          a1 = HALF ? pack_bf16x2(z0, z1) : pack_bf16x2(y1, z1);
         }
       }
       const uint4 out0 = make_uint4(u[0][0], u[0][1], u[0][2], u[0][3]), out1 = make_uint4(u[1][0], u[1][1], u[1][2], u[1][3]);
@@ -316,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, FMT == MNW_KV_INT4 ? 4 : 0) kv_appen
             const uint64_t r = f32x2_mul(f32x2_pack(u[e][j] << 16, u[e][j] & 0xFFFF0000u), twice(rs));
             const uint64_t n = f32x2_add(f32x2_add(r, twice(kRound)), twice(-kRound));
             const uint64_t off = f32x2_fma(n, twice(-1.f), r);
-            far = fmaxf(fmaxf(far, fabsf(__uint_as_float(static_cast<uint32_t>(off)))), fabsf(__uint_as_float(static_cast<uint32_t>(off >> 32))));
+            far = fmaxf(fmaxf(far, fabsf(lo32(off))), fabsf(hi32(off)));
             part = f32x2_fma(part, twice(16.f), n);
           }
           part = f32x2_add(part, twice(kRound + 34952.f));  // + 8 in each nibble
