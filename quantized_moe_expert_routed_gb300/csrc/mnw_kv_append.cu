@@ -30,9 +30,9 @@
 // (101 MB) in 16.0 us, 6.3 TB/s, 94 % of the copy rate; 512 tokens into INT8
 // pages in 3.9 us and four tokens in 2.7 us, bound by the chain of loads length
 // -> page -> store.  One 16-byte chunk a thread, with the other element of a
-// pair by shuffles, took 21.0 us for the 8192 (issue slots).  INT4 pages take 23
+// pair by shuffles, took 21.0 us for the 8192 (issue slots).  INT4 pages take 22
 // us for the 8192 tokens (89 MB), bound by the codes' and the angles' arithmetic
-// (issue slots 65 %).  Correctly rounded divisions where now a product and a
+// (issue slots 68 %).  Correctly rounded divisions where now a product and a
 // check do, and all four multipliers in each lane, cost 7 us more.
 #include <cuda_bf16.h>
 
