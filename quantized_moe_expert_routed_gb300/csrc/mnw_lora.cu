@@ -69,6 +69,7 @@ __device__ __forceinline__ int rank_of(const Args& a, int i) { return checked_ra
 constexpr int kGroupThreads = 1024, kRun = 16;  // tokens of a thread at a time
 __global__ void __launch_bounds__(kGroupThreads) lora_group_kernel(const Args a) {
   constexpr int kWarps = kGroupThreads / 32;
+  static_assert(kWarps == 32);
   __shared__ int sums[kRun][kWarps + 1], befores[kWarps], totals[kRun];
   pdl_wait();
   pdl_launch_dependents();
@@ -76,55 +77,61 @@ __global__ void __launch_bounds__(kGroupThreads) lora_group_kernel(const Args a)
   // Adapters of lower numbers come first; with more tokens than the threads take at a time, theirs are counted beforehand.
   const bool once = a.T <= kGroupThreads * kRun;
   int start = 0, done = 0;
-  for (int pass = once ? 1 : 0; pass < 2; ++pass) {
-    for (int t0 = 0; t0 < a.T; t0 += kGroupThreads * kRun) {
-      int id[kRun];
+  if (!once) {
+    int before = 0;
+#pragma unroll 8
+    for (int t = tid; t < a.T; t += kGroupThreads) before += bin_of(a, t) < e ? 1 : 0;
+    before = __reduce_add_sync(0xffffffffu, before);
+    if (lane == 0) befores[warp] = before;
+    __syncthreads();
+    start = __reduce_add_sync(0xffffffffu, befores[lane]);
+  }
+  for (int t0 = 0; t0 < a.T; t0 += kGroupThreads * kRun) {
+    int id[kRun];
 #pragma unroll
-      for (int i = 0; i < kRun; ++i) {
-        const int t = t0 + i * kGroupThreads + tid;
-        id[i] = t < a.T ? __ldg(a.adapter + t) : INT_MAX;
-      }
-      uint32_t bits = 0;  // which of this thread's tokens are the adapter's
-      int before = 0, warp_sum = 0;
-      __syncthreads();  // the sums before are read
+    for (int i = 0; i < kRun; ++i) {
+      const int t = t0 + i * kGroupThreads + tid;
+      id[i] = t < a.T ? __ldg(a.adapter + t) : INT_MAX;
+    }
+    uint32_t bits = 0;  // which of this thread's tokens are the adapter's
+    int before = 0, warp_sum = 0;
+    __syncthreads();  // the sums before are read
 #pragma unroll
-      for (int i = 0; i < kRun; ++i) {
-        const bool on = t0 + i * kGroupThreads + tid < a.T;
-        const int bin = static_cast<unsigned>(id[i]) < static_cast<unsigned>(a.n) ? id[i] : a.n;
-        const bool is = on && bin == e;
-        bits |= (is ? 1u : 0u) << i;
-        before += on && bin < e ? 1 : 0;
-        if (is && e == a.n && pass == 1 && id[i] != -1 && a.err) atomicOr(a.err, MNW_DEVERR_BAD_ADAPTER);
-        const int c = __popc(__ballot_sync(0xffffffffu, is));
-        if (lane == i) warp_sum = c;
-      }
-      before = __reduce_add_sync(0xffffffffu, before);
-      if (lane < kRun) sums[lane][warp] = warp_sum;
-      if (lane == 0) befores[warp] = before;
-      __syncthreads();
-      if (warp < kRun) {  // a warp per row of sums
-        const int m = sums[warp][lane];
-        int incl = m;
+    for (int i = 0; i < kRun; ++i) {
+      if (t0 + i * kGroupThreads >= a.T) break;
+      const bool on = t0 + i * kGroupThreads + tid < a.T;
+      const int bin = static_cast<unsigned>(id[i]) < static_cast<unsigned>(a.n) ? id[i] : a.n;
+      const bool is = on && bin == e;
+      bits |= (is ? 1u : 0u) << i;
+      before += on && bin < e ? 1 : 0;
+      if (is && e == a.n && id[i] != -1 && a.err) atomicOr(a.err, MNW_DEVERR_BAD_ADAPTER);
+      const int c = __popc(__ballot_sync(0xffffffffu, is));
+      if (lane == i) warp_sum = c;
+    }
+    before = __reduce_add_sync(0xffffffffu, before);
+    if (lane < kRun) sums[lane][warp] = warp_sum;
+    if (lane == 0) befores[warp] = before;
+    __syncthreads();
+    if (warp < kRun && t0 + warp * kGroupThreads < a.T) {  // a warp per row of sums
+      const int m = sums[warp][lane];
+      int incl = m;
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const int o = __shfl_up_sync(0xffffffffu, incl, d);
-          if (lane >= d) incl += o;
-        }
-        sums[warp][lane] = incl - m;
-        if (lane == 31) totals[warp] = incl;
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += o;
       }
-      __syncthreads();
-      if (pass == 0 || once)
-        for (int w = 0; w < kWarps; ++w) start += befores[w];
-      if (pass == 1) {
+      sums[warp][lane] = incl - m;
+      if (lane == 31) totals[warp] = incl;
+    }
+    __syncthreads();
+    if (once) start = __reduce_add_sync(0xffffffffu, befores[lane]);
 #pragma unroll
-        for (int i = 0; i < kRun; ++i) {
-          const bool is = bits >> i & 1;
-          const uint32_t m = __ballot_sync(0xffffffffu, is);
-          if (is) a.order[start + done + sums[i][warp] + __popc(m & ((1u << lane) - 1u))] = t0 + i * kGroupThreads + tid;
-          done += totals[i];
-        }
-      }
+    for (int i = 0; i < kRun; ++i) {
+      if (t0 + i * kGroupThreads >= a.T) break;
+      const bool is = bits >> i & 1;
+      const uint32_t m = __ballot_sync(0xffffffffu, is);
+      if (is) a.order[start + done + sums[i][warp] + __popc(m & ((1u << lane) - 1u))] = t0 + i * kGroupThreads + tid;
+      done += totals[i];
     }
   }
   if (tid == 0) {
