@@ -552,7 +552,7 @@ int mnw_kv_values(const void* cache, const void* scale, int fmt, int n_pages, in
  * have adapters in any order; neighbours of one adapter cost least.
  * H, N and R are multiples of 8, R <= 128, n_adapters <= 1024, T <= 2^24,
  * N <= 2^20.  ws: device, 256-byte aligned, >= mnw_lora_workspace_size() bytes
- * (0 up to 1024 tokens: ws may be NULL), any contents; calls that overlap need
+ * (0 for few tokens: ws may then be NULL), any contents; calls that overlap need
  * one each.  T = 0 is a no-op. */
 size_t mnw_lora_workspace_size(int T, int H, int R, int n_adapters);
 int mnw_lora_add(const void* x, long long x_stride, const void* a, const void* b, const float* scale,

@@ -10,19 +10,17 @@
 // Bound: x, y and the adapters in use are read once and out is written once, 2 R
 // flops a byte at most, so memory is the floor for many tokens; for few it is
 // the chain adapter -> tokens -> x and A -> v -> out.  Two forms:
-//  - up to 1024 tokens one kernel, a cluster of eight CTAs per tile of 32 or 16
-//    tokens of one adapter, each of which finds its tile by itself;
+//  - for few tokens (few_tokens() below) one kernel, a cluster of eight CTAs per
+//    tile of 32 or 16 tokens of one adapter, each of which finds its tile by itself;
 //  - above, three: tokens are listed by adapter, v = A x and out = y + s B v on
 //    tcgen05 with 128 tokens a tile.
 // Each token's result depends on its own row alone, so it is the same however
 // tokens are arranged.
 //
 // Measured on one GB300 (device time in a replayed graph; one kernel and three):
-// 64 tokens of 24 adapters, H = 4096, N = 5120, R = 16: 6.0 and 29.4 us; 512
-// tokens in runs of 32, R = 64: 14.0 and 22.9; 1024, R = 64: 27.3 and 27.9, in
-// any order 31.5 and 32.4.  9000 tokens of 4 adapters, R = 64 (262 MB): 66 us,
-// 3.9 TB/s.  Its kernels alone and cold: 7.5 us listing, 22 the first product, 45
-// the second; with warp-level products these two took 28 and 68.
+// 64 tokens of 24 adapters, H = 4096, N = 5120, R = 16: 6.0 us by one.  9000 tokens
+// of 4 adapters, R = 64 (262 MB): 65 us by three, 4.0 TB/s; alone and cold the first
+// product takes 22, the second 45; with warp-level products they took 28 and 68.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -826,6 +824,16 @@ __global__ void __launch_bounds__(kThreads, NR <= 8 ? 2 : 1) lora_few_kernel(con
 
 // ---- host ----
 
+// Clusters that run at a time; the last form has one CTA an SM.
+inline int clusters_at_once(int R) { return (R <= 64 ? 2 : 1) * current_sm_count() / kCluster; }
+// Tokens up to which one kernel takes a batch: as many as its counters hold for up to 32 ranks, and with more, whose tiles
+// are of 16 tokens, while all tiles run at a time.  One kernel and three, H = 4096, N = 5120, 8 adapters unless given:
+// R = 16: 512 tokens 10.3 and 13.6 us, 1024 of one 11.1 and 13.5, of eight 15.7 and 16.8, of 64 24.2 and 37.2;
+// R = 64: 256 tokens 13.1 and 17.5, 512 of one 13.9 and 16.5, of eight 20.7 and 17.3, 768 26.7 and 19.9, 1024 28.5 and 23.9;
+// R = 128: 256 tokens 23.6 and 26.9, 512 37.0 and 27.7, 1024 66.4 and 33.2 (but 512 of 64 adapters 74.5 and 98.5: how many
+// adapters a batch has is known on the device only.)
+inline int few_tokens(int R) { return R <= 32 ? kFewTokens : std::min(kFewTokens, 16 * clusters_at_once(R)); }
+
 inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 inline int padded(int R) { return R <= 16 ? 16 : (R <= 32 ? 32 : (R <= 64 ? 64 : 128)); }
 // Shares of H in the first product: as many as fill the GPU, 256 elements each at least.
@@ -853,7 +861,7 @@ struct Workspace {
 };
 inline Workspace workspace_of(int T, int H, int R, int n) {
   Workspace w{};
-  if (T <= kFewTokens) return w;
+  if (T <= few_tokens(R)) return w;
   w.starts = 0;
   w.order = up256((static_cast<size_t>(n) + 2) * 4);
   w.v = w.order + up256(static_cast<size_t>(T) * 4);
@@ -891,12 +899,12 @@ int launch_few(const Args& a, cudaStream_t st) {
 
 template <int NR>
 int launch(Args& a, uint8_t* ws, cudaStream_t st) {
-  if (a.T <= kFewTokens) {
+  if (a.T <= few_tokens(a.R)) {
     // Tiles of 16 tokens, whose registers hold two groups of columns ahead, while the GPU takes all of them at a time, and
     // of 32 above.  H = 4096, N = 5120, R = 16 and 32: 64 tokens of one adapter 5.6 and 6.9 us (tiles of 32: 7.1 and 9.4),
     // 512 of four 7.8 and 10.2 (10.1 and 13.5), 1024 of one 15.2 and 18.9 (11.1 and 14.8).
     if constexpr (NR <= 4)
-      if (a.T / 16 > 2 * current_sm_count() / kCluster) return launch_few<NR, 2>(a, st);
+      if (a.T > 16 * clusters_at_once(a.R)) return launch_few<NR, 2>(a, st);
     return launch_few<NR, 1>(a, st);
   }
   const Workspace w = workspace_of(a.T, a.H, a.R, a.n);

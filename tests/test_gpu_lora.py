@@ -55,6 +55,10 @@ SHAPES = [
     (64, 4096, 2048, 16, 24, "random"), (127, 256, 128, 32, 2, "one"), (128, 264, 136, 64, 1, "one"), (129, 72, 520, 72, 1, "one"),
     (200, 1024, 1280, 128, 7, "runs"), (256, 512, 256, 8, 64, "random"), (257, 520, 248, 56, 3, "random"), (700, 640, 768, 32, 12, "runs"),
     (1024, 512, 512, 16, 16, "random"), (1025, 512, 512, 64, 16, "runs"), (3000, 256, 264, 16, 1024, "random"), (2500, 1536, 1000, 64, 4, "runs"), (40000, 64, 40, 8, 5, "random"), (600, 128, 2600, 128, 3, "random"),
+    # around the limits of the one kernel and of its tiles' sizes
+    (303, 136, 72, 128, 2, "random"), (304, 136, 72, 72, 1, "one"), (305, 136, 72, 128, 2, "random"), (607, 72, 136, 64, 3, "runs"),
+    (608, 72, 136, 40, 1, "one"), (609, 72, 136, 64, 3, "random"), (608, 72, 136, 16, 1, "one"), (609, 72, 136, 16, 1, "one"),
+    (1023, 72, 136, 32, 1024, "random"), (1024, 72, 136, 128, 1024, "random"),
 ]
 
 
