@@ -121,7 +121,8 @@ struct BCfg {
   static constexpr uint32_t kOffRaw = kOffV + kSlotsV * kTile;            // keys' codes, values' codes
   static constexpr uint32_t kOffKS = kOffRaw + 2 * kRaws * kRaw;          // [kScalesK][kTK] scales of keys
   static constexpr uint32_t kOffVS = kOffKS + (INT8 ? kScalesK * kTK * 4 : 0);  // [kScalesV][2][kTK] of values, and their log2
-  static constexpr uint32_t kOffBars = kOffVS + (INT8 ? kScalesV * 2 * kTK * 4 : 0);
+  static constexpr uint32_t kOffOnes = kOffVS + (INT8 ? kScalesV * 2 * kTK * 4 : 0);  // INT4: keys' scales of a tile that has them
+  static constexpr uint32_t kOffBars = kOffOnes + (INT4 ? kTK * 4 : 0);
 };
 
 // A run's part of one item.
@@ -300,6 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(&bars->tmem_base, kTmemCols);
     tmem_relinquish();
   }
+  if (INT4 && threadIdx.x < kTK) reinterpret_cast<float*>(smem + C::kOffOnes)[threadIdx.x] = 1.f;
   pdl_wait();
   const Run run = find_run<kRT, kTK, kThreads, kMaxSlack>(a, &split);
   Cursor<kRT, kTK> kc{};
@@ -564,8 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < kMine; i += 32) {
             const int key = key0 + i + lane;
             const float s = *reinterpret_cast<const float*>(rec + key * int4row::kRecord);
-            // a key of zeros keeps a scale: a masked score of -inf has to stay one
-            sc[key] = values ? s : (s == 0.f ? 0x1p-126f : s * kHalfUnit);
+            sc[key] = values ? s : s * kHalfUnit;
             if (values) sc[kTK + key] = fmaxf(__log2f(s), kLeastLog2);
           }
           __syncwarp();
@@ -904,7 +905,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        if (__any_sync(0xffffffffu, min(st[0].left, st[1].left) < kTK)) {
+        const bool masked = __any_sync(0xffffffffu, min(st[0].left, st[1].left) < kTK);
+        if (masked) {
+          if constexpr (INT4) {
+            // the keys' scales before the mask, which a scale of NaN (a key that is not finite) must not undo
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const uint64_t kf = *reinterpret_cast<const uint64_t*>(ks + 8 * i);
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                const uint64_t y = f32x2_mul(f32x2_pack(sv[4 * i + 2 * x], sv[4 * i + 2 * x + 1]), kf);
+                sv[4 * i + 2 * x] = static_cast<uint32_t>(y);
+                sv[4 * i + 2 * x + 1] = static_cast<uint32_t>(y >> 32);
+              }
+            }
+          }
 #pragma unroll
           for (int e = 0; e < 64; ++e)
             if (8 * (e >> 2) + 2 * t4 + (e & 1) >= st[(e >> 1) & 1].left) sv[e] = 0xff800000u;  // -inf
@@ -929,6 +944,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // p = 2^(s fac - unit + kLift4), so that p times the value's scale is the FP16 product as it is.  The unit of
           // before serves as long as no product passes 2^14, which is looked for in the products; then, and for a row's
           // first keys, the unit is set and the products are computed (again).
+          ks = reinterpret_cast<const float*>(smem + (masked ? C::kOffOnes : C::kOffKS + ks_slot * (kTK * 4))) + 2 * t4;
           const uint64_t one2 = ones(a);
           bool set = t == begin || __any_sync(0xffffffffu, st[0].unit == -INFINITY || st[1].unit == -INFINITY);
           uint32_t pw[32];
@@ -1158,7 +1174,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int D, int FMT>
 int launch(const Args& a, int runs, cudaStream_t st) {
   constexpr size_t kSmem = BCfg<D, FMT>::kOffBars + sizeof(Bars) + 1024;
-  static_assert(kSmem <= 232448 - 512, "shared memory of a CTA");
+  static_assert(kSmem <= 232448 - 1024, "shared memory of a CTA, beside 1 KB of static variables");
   auto kern = paged_block_kernel<D, FMT>;
   static std::atomic<uint64_t> attr{0};
   uint64_t bit;
