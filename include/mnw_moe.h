@@ -517,7 +517,9 @@ int mnw_kv_append(const void* q, long long q_stride, const void* k, long long k_
  * a kv head: new tokens of a sequence * Hq / Hkv) or FP16 (INT8, more rows:
  * products with values below 2^-38 of the row's largest are lost; INT4: below
  * 2^-30, and with more than 32 rows value rows of magnitudes outside 2^-80 ..
- * 2^80 lose more).  Row tiles
+ * 2^80 lose more).  A cached row that is not finite reaches the query rows that
+ * see it; of BF16 and INT8 caches a value row may also make those NaN that do
+ * not see it and lie in one tile with some that do (0 * NaN).  Row tiles
  * times key tiles of the full block table have to stay below 2^31
  * (MNW_E_UNSUPPORTED).  ws: device, 256-byte aligned,
  * >= mnw_attn_paged_workspace_size() bytes, any contents; calls that overlap

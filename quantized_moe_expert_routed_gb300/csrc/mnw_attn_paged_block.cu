@@ -253,6 +253,13 @@ __device__ __forceinline__ uint32_t half2_bits(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// The larger ones; a NaN gives the other.
+__device__ __forceinline__ uint32_t f16x2_max(uint32_t a, uint32_t b) {
+  uint32_t y;
+  asm("max.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+  return y;
+}
+
 template <int D, int FMT>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const Args a,
@@ -998,7 +1005,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 most = __vmaxu2(most, pw[2 * i + x]);
               }
             }
-            if (set) break;
+            if (set) {
+              // Hidden keys in the tile: to rows that do not see the first of its values that are not finite, 0 * NaN adds
+              // nothing.  (Behind the pass that NaN leads to; what it needs is worked out here, as holding it costs 1 us.)
+              if (__any_sync(0xffffffffu, min(st[0].left, st[1].left) < kTK)) {
+                const float* all = reinterpret_cast<const float*>(smem + C::kOffVS) + vs_slot * 2 * kTK;
+                int bad = kTK;
+#pragma unroll
+                for (int i = kTK - 32; i >= 0; i -= 32)
+                  if (!(fabsf(all[i + lane]) < INFINITY)) bad = i + lane;
+                bad = __reduce_min_sync(0xffffffffu, bad);
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                  if (bad < kTK && bad >= st[x].left) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) pw[2 * i + x] = f16x2_max(pw[2 * i + x], 0u);
+                  }
+              }
+              break;
+            }
             set = __any_sync(0xffffffffu, max(most >> 16, most & 0xFFFFu) > kMostBits) != 0;
             if (!set) break;
           }

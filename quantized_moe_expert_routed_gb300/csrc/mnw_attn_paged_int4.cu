@@ -85,6 +85,13 @@ __device__ __forceinline__ uint64_t two(float lo, float hi) { return f32x2_pack(
 __device__ __forceinline__ float lo32(uint64_t x) { return __uint_as_float(static_cast<uint32_t>(x)); }
 __device__ __forceinline__ float hi32(uint64_t x) { return __uint_as_float(static_cast<uint32_t>(x >> 32)); }
 
+// The largest of magnitudes; NaN where one is.
+__device__ __forceinline__ float most_nan(float most, float a, float b) {
+  float y;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(most), "f"(a), "f"(b));
+  return y;
+}
+
 // Row i of a warp's 16-key operand tiles is key i ^ (i / 2 % 2): the keys that a load's lanes read then lie in rows of
 // both parities, whose 64 bytes are the two halves of the banks.
 __device__ __forceinline__ int key_of(int i) { return i ^ ((i >> 1) & 1); }
@@ -397,11 +404,11 @@ __global__ void __launch_bounds__(kThreads, int4_runs_per_sm(8 * NT)) paged_int4
               now[nt] = f32x2_add(now[nt], p2);
               const uint64_t w2 = f32x2_mul(p2, two(vs[mt][h] * lo32(lift[nt]), vs[mt][h] * hi32(lift[nt])));
               most_p = fmaxf(fmaxf(most_p, lo32(p2)), hi32(p2));
-              most_w = fmaxf(fmaxf(most_w, fabsf(lo32(w2))), fabsf(hi32(w2)));
+              most_w = most_nan(most_w, lo32(w2), hi32(w2));
               pw[mt][nt][h] = half2_of(lo32(w2), hi32(w2));
             }
         }
-        if (!__any_sync(0xffffffffu, most_p > kMostP || most_w > kMostW)) break;
+        if (!__any_sync(0xffffffffu, most_p > kMostP || !(most_w <= kMostW))) break;
         float alpha[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -440,6 +447,17 @@ __global__ void __launch_bounds__(kThreads, int4_runs_per_sm(8 * NT)) paged_int4
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[i][nt][e] *= alpha[nt][e & 1];
+        if (pass == 1) {  // NaN: a hidden value that is not finite, 0 * NaN, adds nothing
+#pragma unroll
+          for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int p = p0 + 16 * mt + 8 * h + key_of(g8);
+                pw[mt][nt][h] &= (p >= lim[nt][0] ? 0u : 0xFFFFu) | (p >= lim[nt][1] ? 0u : 0xFFFF0000u);
+              }
+        }
       }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) sum[nt] = now[nt];
