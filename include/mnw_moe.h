@@ -512,7 +512,9 @@ int mnw_kv_append(const void* q, long long q_stride, const void* k, long long k_
  * hold anything, NaN included; keys and values inside it have to be finite,
  * those that a mask hides from a row too (a probability of zero times infinity
  * is not zero).  Scores, softmax and
- * sums are FP32; results do not depend on timing.  Probabilities enter the
+ * sums are FP32, the values' before they are divided by the probabilities'
+ * (magnitudes times positions below 2^128); results do not depend on timing.
+ * Probabilities enter the
  * second product as BF16 (BF16 caches), TF32 (INT8 caches, up to 32 query rows
  * a kv head: new tokens of a sequence * Hq / Hkv) or FP16 (INT8, more rows:
  * products with values below 2^-38 of the row's largest are lost; INT4: below

@@ -1148,7 +1148,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (INT8 && !INT4 && rs.unit != -INFINITY) f[x] *= ex2(rs.unit - rs.m - 14.f);
         // INT4: parts are normalised, as the sums' unit says nothing of the scores
         const float all = INT4 ? rs.unit - kLift4 + log2f(sum) : 0.f;
-        if (INT4) f[x] *= int4row::kUnit;
         const int r = r16 + 8 * x;
         row[x] = out_row<kRT>(a, sg.s, sg.g, sg.rt, min(r, rows - 1));
         if (r < rows && t4 == 0) {
@@ -1165,6 +1164,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t o[32];
         tmem_ld_frag(at16 + C::kColO + i, o);
         tmem_wait_ld();
+        if constexpr (INT4) {  // the operands' unit, by itself: its product with f may pass FP32
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * int4row::kUnit);
+        }
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           if (r16 + 8 * x < rows) {

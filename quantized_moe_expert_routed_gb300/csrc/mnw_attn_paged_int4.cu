@@ -527,8 +527,8 @@ __global__ void __launch_bounds__(kThreads, int4_runs_per_sm(8 * NT)) paged_int4
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1) all += __shfl_xor_sync(0xffffffffu, all, d);
           const float m = x ? -hi32(neg[nt]) : -lo32(neg[nt]);
-          // sums relative to the maximum again
-          back[x] = ex2(unit[nt][x] - m - kLift) * int4row::kUnit;
+          // sums relative to the maximum again (and of the operands' unit: one after the other, their product may pass FP32)
+          back[x] = ex2(unit[nt][x] - m - kLift);
           if (g8 == 0) ml[warp][8 * nt + 2 * t4 + x] = make_float2(m == kLow ? -INFINITY : m, all);
         }
         float* const mo = meet(warp);
@@ -537,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, int4_runs_per_sm(8 * NT)) paged_int4
 #pragma unroll
           for (int x = 0; x < 2; ++x)
             *reinterpret_cast<float2*>(mo + (2 * t4 + x) * C::kPad + (D / 8) * g8 + 2 * i) =
-                make_float2(o[i][nt][x] * back[x], o[i][nt][2 + x] * back[x]);
+                make_float2(o[i][nt][x] * int4row::kUnit * back[x], o[i][nt][2 + x] * int4row::kUnit * back[x]);
         __syncthreads();
         const int here = min(8, rows - 8 * nt);
         for (int e = tid * 4; e < here * D; e += kThreads * 4) {
