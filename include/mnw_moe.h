@@ -509,19 +509,18 @@ int mnw_kv_append(const void* q, long long q_stride, const void* k, long long k_
  * [T, Hq], nullable): log of the row's sum of e^(scale * q . k).  A row that
  * sees nothing gives zeros and lse = -inf; rows of no sequence are not
  * written, and none at all where q_start descends.  Slots past the length may
- * hold anything, NaN included; keys and values inside it have to be finite,
- * those that a mask hides from a row too (a probability of zero times infinity
- * is not zero).  Scores, softmax and
- * sums are FP32, the values' before they are divided by the probabilities'
- * (magnitudes times positions below 2^128); results do not depend on timing.
- * Probabilities enter the
- * second product as BF16 (BF16 caches), TF32 (INT8 caches, up to 32 query rows
- * a kv head: new tokens of a sequence * Hq / Hkv) or FP16 (INT8, more rows:
- * products with values below 2^-38 of the row's largest are lost; INT4: below
- * 2^-30, and with more than 32 rows value rows of magnitudes outside 2^-80 ..
- * 2^80 lose more).  A cached row that is not finite reaches the query rows that
- * see it; of BF16 and INT8 caches a value row may also make those NaN that do
- * not see it and lie in one tile with some that do (0 * NaN).  Row tiles
+ * hold anything, NaN included.  A cached row of an INT4 cache that is not finite
+ * reaches the rows that see it alone; of BF16 and INT8 caches values have to be
+ * finite, those that a mask hides from a row too (a probability of zero times
+ * infinity is not zero).  Scores, softmax and sums are FP32, the values' before
+ * they are divided by the probabilities' (magnitudes times positions below
+ * 2^128); results do not depend on timing.  Probabilities enter the second
+ * product as BF16 (BF16 caches), TF32 (INT8 caches, up to 32 query rows a kv
+ * head: new tokens of a sequence * Hq / Hkv) or FP16 (INT8, more rows: products
+ * with values below 2^-38 of the row's largest are lost; INT4: below 2^-30).
+ * With more than 32 rows an INT4 cache's value rows of magnitudes outside 2^-80
+ * .. 2^80 lose more, and scores past 10^8 ask for quantised values within 2^-10
+ * .. 2^10.  Row tiles
  * times key tiles of the full block table have to stay below 2^31
  * (MNW_E_UNSUPPORTED).  ws: device, 256-byte aligned,
  * >= mnw_attn_paged_workspace_size() bytes, any contents; calls that overlap

@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, int4_runs_per_sm(8 * NT)) paged_int4
   uint32_t qf[kQRegs ? kKS : 1][kQRegs ? NT : 1][2];
   uint64_t qfac[NT];                    // score factors
   uint64_t neg[NT], sum[NT], lift[NT];  // minus the maximum (log2), sum, 2^(maximum - unit + kLift)
-  float unit[NT][2];                    // log2 of the products' reference
+  float unit[NT][2];                    // log2 of the products' reference, from the maximum
   int lim[NT][2];                       // first key that is not seen
   float o[kNO][NT][4];
   int rows = 0, lim_lo = 0, lim_hi = 0, kt_begin = 0;
@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, int4_runs_per_sm(8 * NT)) paged_int4
       for (int x = 0; x < 2; ++x) {
         const int r = 8 * nt + 2 * t4 + x;
         lim[nt][x] = r < rows ? row_limit(a, cc.s, ri + r) : lim_hi;
-        unit[nt][x] = kLow;
+        unit[nt][x] = 0.f;
       }
       neg[nt] = two(-kLow, -kLow);
       sum[nt] = lift[nt] = 0ull;
@@ -419,27 +419,30 @@ __global__ void __launch_bounds__(kThreads, int4_runs_per_sm(8 * NT)) paged_int4
 #pragma unroll
             for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const float s = sc[mt][nt][2 * h + x] * (x ? hi32(fac[mt][nt][h]) : lo32(fac[mt][nt][h]));
-                top = fmaxf(top, s);
-                topv = fmaxf(topv, s + __log2f(fabsf(vs[mt][h])));
-              }
+              for (int h = 0; h < 2; ++h)
+                top = fmaxf(top, sc[mt][nt][2 * h + x] * (x ? hi32(fac[mt][nt][h]) : lo32(fac[mt][nt][h])));
 #pragma unroll
-            for (int d = 4; d < 32; d <<= 1) {
-              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-              topv = fmaxf(topv, __shfl_xor_sync(0xffffffffu, topv, d));
-            }
+            for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
             const float m = x ? -hi32(neg[nt]) : -lo32(neg[nt]);
             n[x] = fmaxf(m, top);
+            // relative to the maximum: next to a huge score the logarithm of a value's scale would be lost
+#pragma unroll
+            for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                topv = fmaxf(topv, __fsub_rn(__fmul_rn(sc[mt][nt][2 * h + x], x ? hi32(fac[mt][nt][h]) : lo32(fac[mt][nt][h])), n[x]) +
+                                       __log2f(fabsf(vs[mt][h])));
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) topv = fmaxf(topv, __shfl_xor_sync(0xffffffffu, topv, d));
             // held within 2^100 of the maximum so that the lift stays finite
-            const float u = fmaxf(fmaxf(unit[nt][x], topv), n[x] - 100.f);
+            const float now_at = unit[nt][x] + (m - n[x]), u = fmaxf(fmaxf(now_at, topv), -100.f);
             c[x] = ex2(m - n[x]);
-            alpha[nt][x] = ex2(unit[nt][x] - u);
+            alpha[nt][x] = ex2(now_at - u);
             unit[nt][x] = u;
           }
           neg[nt] = two(-n[0], -n[1]);
           sum[nt] = f32x2_mul(sum[nt], two(c[0], c[1]));
-          lift[nt] = two(ex2(n[0] - unit[nt][0] + kLift), ex2(n[1] - unit[nt][1] + kLift));
+          lift[nt] = two(ex2(kLift - unit[nt][0]), ex2(kLift - unit[nt][1]));
         }
 #pragma unroll
         for (int i = 0; i < kNO; ++i)
@@ -528,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, int4_runs_per_sm(8 * NT)) paged_int4
           for (int d = 4; d < 32; d <<= 1) all += __shfl_xor_sync(0xffffffffu, all, d);
           const float m = x ? -hi32(neg[nt]) : -lo32(neg[nt]);
           // sums relative to the maximum again (and of the operands' unit: one after the other, their product may pass FP32)
-          back[x] = ex2(unit[nt][x] - m - kLift);
+          back[x] = ex2(unit[nt][x] - kLift);
           if (g8 == 0) ml[warp][8 * nt + 2 * t4 + x] = make_float2(m == kLow ? -INFINITY : m, all);
         }
         float* const mo = meet(warp);
