@@ -165,12 +165,22 @@ template <int N>
 __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-// What the first BF16 term leaves of v, nothing of an infinite one; and the ranks that count, of the 4 from e on (an
-// infinite x times the zeros of the others would be NaN).
+// v as two BF16 terms: the nearest (no further than BF16's largest, for finite ones that lie past it), and what that leaves,
+// nothing of an infinite one.
+__device__ __forceinline__ float first_of(float v) {
+  constexpr float kMost = 0x1.FEp127f;
+  return fabsf(v) < INFINITY ? fminf(fmaxf(v, -kMost), kMost) : v;
+}
 __device__ __forceinline__ float rest_of(float v, uint32_t first) {
   const float r = v - __uint_as_float(first);
   return fabsf(r) < INFINITY ? r : 0.f;
 }
+__device__ __forceinline__ void terms_of(float4 v, uint2& first, uint2& rest) {
+  first = make_uint2(pack_bf16x2(first_of(v.x), first_of(v.y)), pack_bf16x2(first_of(v.z), first_of(v.w)));
+  rest = make_uint2(pack_bf16x2(rest_of(v.x, first.x << 16), rest_of(v.y, first.x & 0xFFFF0000u)),
+                    pack_bf16x2(rest_of(v.z, first.y << 16), rest_of(v.w, first.y & 0xFFFF0000u)));
+}
+// The ranks that count, of the 4 from e on (an infinite x times the zeros of the others would be NaN).
 __device__ __forceinline__ float4 ranks_of(float4 v, int e, int rank) {
   return make_float4(e < rank ? v.x : 0.f, e + 1 < rank ? v.y : 0.f, e + 2 < rank ? v.z : 0.f, e + 3 < rank ? v.w : 0.f);
 }
@@ -429,12 +439,11 @@ __global__ void __launch_bounds__(kExpandThreads, 1) lora_expand_kernel(const Ar
         }
       }
       f = ranks_of(f, e, rank);
-      const uint32_t h0 = pack_bf16x2(f.x, f.y), h1 = pack_bf16x2(f.z, f.w);
-      const uint32_t l0 = pack_bf16x2(rest_of(f.x, h0 << 16), rest_of(f.y, h0 & 0xFFFF0000u));
-      const uint32_t l1 = pack_bf16x2(rest_of(f.z, h1 << 16), rest_of(f.w, h1 & 0xFFFF0000u));
+      uint2 first, rest;
+      terms_of(f, first, rest);
       uint8_t* to = smem + (e >> 6) * C::kPieceA + r * 128 + ((((e & 63) >> 3) ^ (r & 7)) << 4) + (e & 4) * 2;
-      *reinterpret_cast<uint2*>(to) = make_uint2(h0, h1);
-      *reinterpret_cast<uint2*>(to + C::kPieces * C::kPieceA) = make_uint2(l0, l1);
+      *reinterpret_cast<uint2*>(to) = first;
+      *reinterpret_cast<uint2*>(to + C::kPieces * C::kPieceA) = rest;
     }
   }
   const float scale = a.scale ? __ldcg(a.scale + tl.bin) : 1.f;
@@ -529,7 +538,7 @@ __device__ __forceinline__ float4 ld_cluster(uint32_t addr, int cta) {
   return v;
 }
 // Elements of a chunk of 8 that lie below `left`.
-__device__ __forceinline__ uint4 first_of(uint4 w, int left) {
+__device__ __forceinline__ uint4 elements_below(uint4 w, int left) {
   auto keep = [&](uint32_t x, int e) { return left >= e + 2 ? x : (left == e + 1 ? x & 0xFFFFu : 0u); };
   return make_uint4(keep(w.x, 0), keep(w.y, 2), keep(w.z, 4), keep(w.w, 6));
 }
@@ -746,12 +755,11 @@ __global__ void __launch_bounds__(kThreads, NR <= 8 ? 2 : 1) lora_few_kernel(con
         }
       }
       s = ranks_of(s, e % kRp, rank);
-      const uint32_t h0 = pack_bf16x2(s.x, s.y), h1 = pack_bf16x2(s.z, s.w);
-      const uint32_t l0 = pack_bf16x2(rest_of(s.x, h0 << 16), rest_of(s.y, h0 & 0xFFFF0000u));
-      const uint32_t l1 = pack_bf16x2(rest_of(s.z, h1 << 16), rest_of(s.w, h1 & 0xFFFF0000u));
+      uint2 first, rest;
+      terms_of(s, first, rest);
       uint8_t* to = smem + C::kOffV + (e / kRp * C::kRowV + e % kRp) * 2;
-      *reinterpret_cast<uint2*>(to) = make_uint2(h0, h1);
-      *reinterpret_cast<uint2*>(to + kTF * C::kRowV * 2) = make_uint2(l0, l1);
+      *reinterpret_cast<uint2*>(to) = first;
+      *reinterpret_cast<uint2*>(to + kTF * C::kRowV * 2) = rest;
     }
     cluster_arrive();  // the others' shares are read
     __syncthreads();
@@ -770,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, NR <= 8 ? 2 : 1) lora_few_kernel(con
         const int e = NR == 2 ? 4 * t4 : 32 * c + 8 * t4;  // the lane's elements of v and B
         if (rank & 7) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) f.b[j][c] = first_of(f.b[j][c], rank - e);
+          for (int j = 0; j < 4; ++j) f.b[j][c] = elements_below(f.b[j][c], rank - e);
         }
 #pragma unroll
         for (int mt = 0; mt < kMT; ++mt)
