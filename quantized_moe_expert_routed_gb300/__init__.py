@@ -551,9 +551,10 @@ def mnw_attn_paged(q, k_cache, v_cache, block_table, cache_lens, blk, scale, k_s
         wp, held = _scratch(wn, q, stream, st)
     else:
         wp, wn = _need(ws, torch.uint8, "ws"), ws.numel()
-    rc = load().mnw_attn_paged(qp, qst, B, T, Hq, Hkv, d, kc, vc, ks, vs, fmt, n_pages, page, page_stride, tp, most, lp, sp,
-                               blk, scale, op, lsp, wp, wn, ep, st)
-    if held is not None:
+    try:
+        rc = load().mnw_attn_paged(qp, qst, B, T, Hq, Hkv, d, kc, vc, ks, vs, fmt, n_pages, page, page_stride, tp, most, lp, sp,
+                                   blk, scale, op, lsp, wp, wn, ep, st)
+    finally:
         _give_back(held)
     if rc:
         _check(rc, "mnw_attn_paged")
@@ -647,8 +648,9 @@ def mnw_lora_add(y, x, a, b, adapter, scale=None, ranks=None, out=None, ws=None,
             wp, held = _scratch(wn, y, stream, st)
     else:
         wp, wn = _need(ws, torch.uint8, "ws"), ws.numel()
-    rc = load().mnw_lora_add(xp, x_stride, ap, bp, sp, kp, n, R, ip, T, H, N, yp, y_stride, op, out_stride, wp, wn, ep, st)
-    if held is not None:
+    try:
+        rc = load().mnw_lora_add(xp, x_stride, ap, bp, sp, kp, n, R, ip, T, H, N, yp, y_stride, op, out_stride, wp, wn, ep, st)
+    finally:
         _give_back(held)
     if rc:
         _check(rc, "mnw_lora_add")
