@@ -305,7 +305,7 @@ def mnw_attn_prefill(q, k, v, blk: int, scale: float, out=None, ws=None, err=Non
 
 # ---- the decode step around the layer: norm, paged cache, attention ----
 # The calls on the cache and the adapters' go through _calls where nothing is amiss; the Python below it takes the others:
-# a stream of the caller's, another device than the current one, and arguments that it refuses by name.
+# a stream of the caller's, and arguments that it refuses by name, among them tensors of another device than the current one.
 
 
 def _need(t, dtype, what, dim=None):
@@ -336,22 +336,36 @@ def _new(shape, dtype, device, stream):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _stream_of(t, stream):
+    """The handle to launch on: the given stream's, or the current one's.  The library launches on the current device."""
+    device = t.get_device()
+    if _current_device() != device or (stream is not None and stream.device_index != device):
+        raise MnwError(f"the tensors are on device {device}, which has to be the current device and the stream's")
     if stream is not None:
         return stream.cuda_stream
-    return _raw_stream(t.get_device()) if _raw_stream else torch.cuda.current_stream(t.device).cuda_stream
+    return _raw_stream(device) if _raw_stream else torch.cuda.current_stream(t.device).cuda_stream
+
+
+def _one_device(t, **others):
+    """Every tensor of a call has to be on tensor t's device: an address of another one is none here."""
+    device = t.get_device()
+    for what, o in others.items():
+        if o is not None and o.get_device() != device:
+            raise MnwError(f"{what}: on device {o.get_device()}, where the call's other tensors are on {device}")
 
 
 # A call's scratch memory, straight from torch's caching allocator: allocated on the call's stream and given back behind
 # the launches, so the next user on that stream comes after them (a tensor for it costs 4 us of the host's time more).
 _raw_alloc = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc", None)
 _raw_delete = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_delete", None)
-_current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
 def _scratch(n, t, stream, handle):
-    """(address, what has to be given to _give_back) of n bytes for a call on tensor t's device and the given stream."""
-    if _raw_alloc and _raw_delete and _current_device and _current_device() == t.get_device():
+    """(address, what has to be given to _give_back) of n bytes for a call on the current device and the given stream."""
+    if _raw_alloc and _raw_delete:
         p = _raw_alloc(n, handle)
         return p, p
     ws = _new((n,), torch.uint8, t.device, stream)
@@ -502,6 +516,8 @@ def mnw_kv_append(q, k, v, k_cache, v_cache, block_table, cache_lens, inv_freq=N
         rot = 2 * inv_freq.numel()
         fp = _whole(inv_freq, torch.float32, (rot // 2,), "inv_freq")
     ep = None if err is None else _ptr(err)
+    _one_device(k, v=v, q=q, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, block_table=block_table,
+                cache_lens=cache_lens, q_start=q_start, inv_freq=inv_freq, q_out=q_out, err=err)
     rc = load().mnw_kv_append(qp, qst, kp, kst, vp, vst, B, T, Hq, Hkv, d, fp, rot, layout, mscale, kc, vc, ks, vs, fmt,
                               n_pages, page, page_stride, tp, most, lp, sp, qo, ep, _stream_of(k, stream))
     if rc:
@@ -545,6 +561,8 @@ def mnw_attn_paged(q, k_cache, v_cache, block_table, cache_lens, blk, scale, k_s
         lse = _new((T, Hq), torch.float32, dev, stream)
     ep = None if err is None else _ptr(err)
     lsp = None if lse is None else _whole(lse, torch.float32, (T, Hq), "lse")
+    _one_device(q, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, block_table=block_table,
+                cache_lens=cache_lens, q_start=q_start, out=out, lse=lse, ws=ws, err=err)
     st, held = _stream_of(q, stream), None
     if ws is None:
         wn = _paged_workspace(B, T, Hq, Hkv, d, q.get_device())
@@ -587,8 +605,9 @@ def mnw_kv_values(cache, scale, out=None, stream=None):
     shape = (n_pages, Hkv, page, d)
     if out is None:
         out = _new(shape, torch.bfloat16, cache.device, stream)
-    rc = load().mnw_kv_values(cache.data_ptr(), sp, fmt, n_pages, page, Hkv, d, page_stride, _whole(out, torch.bfloat16, shape, "out"),
-                              _stream_of(cache, stream))
+    op = _whole(out, torch.bfloat16, shape, "out")
+    _one_device(cache, scale=scale, out=out)
+    rc = load().mnw_kv_values(cache.data_ptr(), sp, fmt, n_pages, page, Hkv, d, page_stride, op, _stream_of(cache, stream))
     if rc:
         _check(rc, "mnw_kv_values")
     return out
@@ -641,6 +660,7 @@ def mnw_lora_add(y, x, a, b, adapter, scale=None, ranks=None, out=None, ws=None,
     if (To, No) != (T, N):
         raise MnwError("out has another shape than y")
     ep = None if err is None else _ptr(err)
+    _one_device(y, x=x, a=a, b=b, adapter=adapter, scale=scale, ranks=ranks, out=out, ws=ws, err=err)
     st, held, wp = _stream_of(y, stream), None, None
     if ws is None:
         wn = _lora_workspace(T, H, R, n, y.get_device())

@@ -10,8 +10,9 @@
 // Each function takes the Python function's arguments (all but the stream: the
 // current one's) and returns its result; the status as an int where the C call
 // refuses; or NotImplemented where anything is not as it has to be, or not
-// plain (another device than the current one, a subclass), without having done
-// anything: the Python function then goes on by itself and says what is wrong.
+// plain (a subclass), or where any tensor is on another device than the current
+// one, without having done anything: the Python function then goes on by itself
+// and says what is wrong.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -57,11 +58,16 @@ struct Scratch {
   }
 };
 
-// The plain CUDA tensor behind an argument, or null.
+// The current device, looked up once a call, at its first CUDA tensor.  (One for all threads: it is used with the
+// interpreter's lock held, and no Python code runs between a call's beginning and current_stream().)
+int device_now = -1;
+// The plain CUDA tensor of that device behind an argument, or null.  Every tensor of a call comes through here.
 const at::Tensor* cuda(PyObject* o) {
   if (!THPVariable_CheckExact(o)) return nullptr;
   const at::Tensor& t = THPVariable_Unpack(o);
-  return t.is_cuda() && t.layout() == at::kStrided ? &t : nullptr;
+  if (!t.is_cuda() || t.layout() != at::kStrided) return nullptr;
+  if (device_now < 0) device_now = c10::cuda::current_device();
+  return t.get_device() == device_now ? &t : nullptr;
 }
 // A contiguous one of the given type and shape; *p its address, null for None where that may be.
 bool whole(PyObject* o, at::ScalarType type, std::initializer_list<int64_t> shape, void** p, bool may_be_none = false) {
@@ -201,12 +207,8 @@ struct Batch {
   }
 };
 
-// The stream to launch on, where the tensor's device is the current one.
-bool here(const at::Tensor& t, cudaStream_t* st) {
-  if (t.get_device() != c10::cuda::current_device()) return false;
-  *st = c10::cuda::getCurrentCUDAStream(t.get_device()).stream();
-  return true;
-}
+// The stream to launch on.
+cudaStream_t current_stream() { return c10::cuda::getCurrentCUDAStream(device_now).stream(); }
 at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const at::Tensor& like) {
   return at::empty(shape, at::TensorOptions().dtype(type).device(like.device()));
 }
@@ -221,20 +223,20 @@ const T* as(void* p) {
 
 PyObject* kv_append(PyObject*, PyObject* const* o, Py_ssize_t n) {
   HANDLE_TH_ERRORS
+  device_now = -1;
   // q, k, v, k_cache, v_cache, block_table, cache_lens, inv_freq, layout, mscale, k_scale, v_scale, q_start, q_out, err
   if (n != 15) Py_RETURN_NOTIMPLEMENTED;
   const at::Tensor *kt = cuda(o[1]), *qt = o[0] == Py_None ? nullptr : cuda(o[0]);
   Cache c;
   Batch b;
   Tokens q, k, v;
-  cudaStream_t st;
   uint32_t* err;
   int layout;
   float mscale;
   void *freq = nullptr, *qo = nullptr;
   int64_t rot = 0;
   if (!kt || !c.read(o[3], o[4], o[10], o[11]) || !b.read(o[5], o[6], o[12]) || !k.read(kt, c.d) || !v.read(cuda(o[2]), c.d) ||
-      k.h != c.h || v.h != c.h || v.T != k.T || !integer(o[8], &layout) || !real(o[9], &mscale) || !word(o[14], &err) || !here(*kt, &st))
+      k.h != c.h || v.h != c.h || v.T != k.T || !integer(o[8], &layout) || !real(o[9], &mscale) || !word(o[14], &err))
     Py_RETURN_NOTIMPLEMENTED;
   if (o[0] == Py_None ? o[13] != Py_None : (!q.read(qt, c.d) || q.T != k.T || !whole(o[13], at::kBFloat16, {q.T, q.h, q.d}, &qo, true)))
     Py_RETURN_NOTIMPLEMENTED;
@@ -244,6 +246,7 @@ PyObject* kv_append(PyObject*, PyObject* const* o, Py_ssize_t n) {
     rot = 2 * f->numel();
   }
   at::Tensor made;
+  const cudaStream_t st = current_stream();
   int rc;
   {
     NoGil free;
@@ -262,13 +265,13 @@ PyObject* kv_append(PyObject*, PyObject* const* o, Py_ssize_t n) {
 
 PyObject* attn_paged(PyObject*, PyObject* const* o, Py_ssize_t n) {
   HANDLE_TH_ERRORS
+  device_now = -1;
   // q, k_cache, v_cache, block_table, cache_lens, blk, scale, k_scale, v_scale, q_start, out, lse, want_lse, ws, err
   if (n != 15) Py_RETURN_NOTIMPLEMENTED;
   const at::Tensor* qt = cuda(o[0]);
   Cache c;
   Batch b;
   Tokens q;
-  cudaStream_t st;
   uint32_t* err;
   int blk;
   float scale;
@@ -276,8 +279,9 @@ PyObject* attn_paged(PyObject*, PyObject* const* o, Py_ssize_t n) {
   size_t bytes;
   if (!qt || !c.read(o[1], o[2], o[7], o[8]) || !b.read(o[3], o[4], o[9]) || !q.read(qt, c.d) || !integer(o[5], &blk) || !real(o[6], &scale) ||
       !whole(o[10], at::kBFloat16, {q.T, q.h, q.d}, &out, true) || !whole(o[11], at::kFloat, {q.T, q.h}, &lse, true) ||
-      !workspace(o[13], &ws, &bytes) || !word(o[14], &err) || !here(*qt, &st))
+      !workspace(o[13], &ws, &bytes) || !word(o[14], &err))
     Py_RETURN_NOTIMPLEMENTED;
+  const cudaStream_t st = current_stream();
   const int want = o[11] != Py_None ? 0 : PyObject_IsTrue(o[12]);
   if (want < 0) return nullptr;
   at::Tensor made, made_lse;
@@ -312,16 +316,16 @@ PyObject* attn_paged(PyObject*, PyObject* const* o, Py_ssize_t n) {
 
 PyObject* kv_values(PyObject*, PyObject* const* o, Py_ssize_t n) {
   HANDLE_TH_ERRORS
+  device_now = -1;
   // cache, scale, out
   if (n != 3) Py_RETURN_NOTIMPLEMENTED;
   const at::Tensor* t = cuda(o[0]);
   Pages c;
-  cudaStream_t st;
   void *scale, *out;
-  if (!c.read(t) || c.fmt == MNW_KV_BF16 || !c.scale(o[1], &scale) || !whole(o[2], at::kBFloat16, {c.n, c.h, c.page, c.d}, &out, true) ||
-      !here(*t, &st))
+  if (!c.read(t) || c.fmt == MNW_KV_BF16 || !c.scale(o[1], &scale) || !whole(o[2], at::kBFloat16, {c.n, c.h, c.page, c.d}, &out, true))
     Py_RETURN_NOTIMPLEMENTED;
   at::Tensor made;
+  const cudaStream_t st = current_stream();
   int rc;
   {
     NoGil free;
@@ -338,11 +342,11 @@ PyObject* kv_values(PyObject*, PyObject* const* o, Py_ssize_t n) {
 
 PyObject* lora_add(PyObject*, PyObject* const* o, Py_ssize_t n) {
   HANDLE_TH_ERRORS
+  device_now = -1;
   // y, x, a, b, adapter, scale, ranks, out, ws, err
   if (n != 10) Py_RETURN_NOTIMPLEMENTED;
   const at::Tensor *yt = cuda(o[0]), *at_ = cuda(o[2]), *ot = o[7] == Py_None ? nullptr : cuda(o[7]);
   Rows y, x, out;
-  cudaStream_t st;
   uint32_t* err;
   void *a, *b, *ids, *scale, *ranks, *ws;
   size_t bytes;
@@ -350,10 +354,11 @@ PyObject* lora_add(PyObject*, PyObject* const* o, Py_ssize_t n) {
   const int64_t many = at_->size(0), R = at_->size(1);
   if (!fits({many, R}) || !whole(o[2], at::kBFloat16, {many, R, x.n}, &a) || !whole(o[3], at::kBFloat16, {many, y.n, R}, &b) ||
       !whole(o[4], at::kInt, {y.T}, &ids) || !whole(o[5], at::kFloat, {many}, &scale, true) || !whole(o[6], at::kInt, {many}, &ranks, true) ||
-      !workspace(o[8], &ws, &bytes) || !word(o[9], &err) || !here(*yt, &st))
+      !workspace(o[8], &ws, &bytes) || !word(o[9], &err))
     Py_RETURN_NOTIMPLEMENTED;
   if (o[7] != Py_None && (!out.read(ot) || out.T != y.T || out.n != y.n)) Py_RETURN_NOTIMPLEMENTED;
   at::Tensor made;
+  const cudaStream_t st = current_stream();
   int rc;
   {
     NoGil free;
