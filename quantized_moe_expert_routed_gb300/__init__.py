@@ -568,7 +568,7 @@ def mnw_attn_paged(q, k_cache, v_cache, block_table, cache_lens, blk, scale, k_s
         wn = _paged_workspace(B, T, Hq, Hkv, d, q.get_device())
         wp, held = _scratch(wn, q, stream, st)
     else:
-        wp, wn = _need(ws, torch.uint8, "ws"), ws.numel()
+        wp, wn = _whole(ws, torch.uint8, ws.shape, "ws"), ws.numel()
     try:
         rc = load().mnw_attn_paged(qp, qst, B, T, Hq, Hkv, d, kc, vc, ks, vs, fmt, n_pages, page, page_stride, tp, most, lp, sp,
                                    blk, scale, op, lsp, wp, wn, ep, st)
@@ -667,7 +667,7 @@ def mnw_lora_add(y, x, a, b, adapter, scale=None, ranks=None, out=None, ws=None,
         if wn:
             wp, held = _scratch(wn, y, stream, st)
     else:
-        wp, wn = _need(ws, torch.uint8, "ws"), ws.numel()
+        wp, wn = _whole(ws, torch.uint8, ws.shape, "ws"), ws.numel()
     try:
         rc = load().mnw_lora_add(xp, x_stride, ap, bp, sp, kp, n, R, ip, T, H, N, yp, y_stride, op, out_stride, wp, wn, ep, st)
     finally:

@@ -86,13 +86,13 @@ bool word(PyObject* o, uint32_t** p) {
   if (t) *p = static_cast<uint32_t*>(t->data_ptr());
   return t != nullptr;
 }
-// A workspace given by the caller, or None.
+// A workspace given by the caller, contiguous (its elements are the bytes that may be written), or None.
 bool workspace(PyObject* o, void** p, size_t* bytes) {
   *p = nullptr;
   *bytes = 0;
   if (o == Py_None) return true;
   const at::Tensor* t = cuda(o);
-  if (!t || t->scalar_type() != at::kByte) return false;
+  if (!t || t->scalar_type() != at::kByte || !t->is_contiguous()) return false;
   *p = t->data_ptr();
   *bytes = static_cast<size_t>(t->numel());
   return true;
