@@ -324,6 +324,15 @@ def _whole(t, dtype, shape, what):
     return t.data_ptr()
 
 
+def _word(err):
+    """Address of the device error word, the first four bytes of any CUDA tensor that has them (None where it has none)."""
+    if err is None:
+        return None
+    if not err.is_cuda or 0 < err.numel() * err.element_size() < 4 or err.data_ptr() % 4:
+        raise MnwError("err: expected a CUDA tensor that begins with a 32-bit word")
+    return err.data_ptr()
+
+
 def _new(shape, dtype, device, stream):
     """A device tensor for results written on `stream`: allocated under it, so its memory is reused in its order."""
     if stream is None:
@@ -515,7 +524,7 @@ def mnw_kv_append(q, k, v, k_cache, v_cache, block_table, cache_lens, inv_freq=N
     if inv_freq is not None:
         rot = 2 * inv_freq.numel()
         fp = _whole(inv_freq, torch.float32, (rot // 2,), "inv_freq")
-    ep = None if err is None else _ptr(err)
+    ep = _word(err)
     _one_device(k, v=v, q=q, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, block_table=block_table,
                 cache_lens=cache_lens, q_start=q_start, inv_freq=inv_freq, q_out=q_out, err=err)
     rc = load().mnw_kv_append(qp, qst, kp, kst, vp, vst, B, T, Hq, Hkv, d, fp, rot, layout, mscale, kc, vc, ks, vs, fmt,
@@ -559,7 +568,7 @@ def mnw_attn_paged(q, k_cache, v_cache, block_table, cache_lens, blk, scale, k_s
         op = _whole(out, torch.bfloat16, (T, Hq, d), "out")
     if lse is None and want_lse:
         lse = _new((T, Hq), torch.float32, dev, stream)
-    ep = None if err is None else _ptr(err)
+    ep = _word(err)
     lsp = None if lse is None else _whole(lse, torch.float32, (T, Hq), "lse")
     _one_device(q, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, block_table=block_table,
                 cache_lens=cache_lens, q_start=q_start, out=out, lse=lse, ws=ws, err=err)
@@ -659,7 +668,7 @@ def mnw_lora_add(y, x, a, b, adapter, scale=None, ranks=None, out=None, ws=None,
     op, To, No, out_stride = _rows(out, "out")
     if (To, No) != (T, N):
         raise MnwError("out has another shape than y")
-    ep = None if err is None else _ptr(err)
+    ep = _word(err)
     _one_device(y, x=x, a=a, b=b, adapter=adapter, scale=scale, ranks=ranks, out=out, ws=ws, err=err)
     st, held, wp = _stream_of(y, stream), None, None
     if ws is None:

@@ -682,7 +682,7 @@ int mnw_attn_paged(const void* q, long long q_stride, int B, int T, int Hq, int 
   rc = paged::check_batch(block_table, cache_lens, q_start, B, T, max_pages, page_size);
   if (rc != MNW_OK) return rc;
   if (!q || !out || !ws || !aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(ws, 256) ||
-      q_stride % 8 || q_stride < static_cast<long long>(Hq) * d)
+      !aligned(err, 4) || q_stride % 8 || q_stride < static_cast<long long>(Hq) * d)
     return MNW_E_INVALID_ARG;
   if (static_cast<long long>(T) * Hq > 0x7fffffffll / 8) return MNW_E_UNSUPPORTED;
   if (ws_bytes < mnw_attn_paged_workspace_size(B, T, Hq, Hkv, d)) return MNW_E_WORKSPACE_TOO_SMALL;

@@ -78,13 +78,14 @@ bool whole(PyObject* o, at::ScalarType type, std::initializer_list<int64_t> shap
   *p = t->data_ptr();
   return true;
 }
-// The error word: any CUDA tensor, or None.
+// The error word: the first four bytes of any CUDA tensor that has them, or None.
 bool word(PyObject* o, uint32_t** p) {
   *p = nullptr;
   if (o == Py_None) return true;
   const at::Tensor* t = cuda(o);
-  if (t) *p = static_cast<uint32_t*>(t->data_ptr());
-  return t != nullptr;
+  if (!t || (t->numel() > 0 && t->numel() * t->itemsize() < 4)) return false;
+  *p = static_cast<uint32_t*>(t->data_ptr());
+  return (reinterpret_cast<uintptr_t>(*p) & 3) == 0;
 }
 // A workspace given by the caller, contiguous (its elements are the bytes that may be written), or None.
 bool workspace(PyObject* o, void** p, size_t* bytes) {

@@ -460,7 +460,7 @@ int mnw_kv_append(const void* q, long long q_stride, const void* k, long long k_
   if (layout != MNW_ROPE_HALF && layout != MNW_ROPE_INTERLEAVED) return MNW_E_INVALID_ARG;
   if (rot % 16) return MNW_E_UNSUPPORTED;
   if (!(mscale > 0.f) || !(mscale < 3.0e38f)) return MNW_E_INVALID_ARG;
-  if (!k || !v || !aligned(k, 16) || !aligned(v, 16) || k_stride % 8 || v_stride % 8 ||
+  if (!k || !v || !aligned(k, 16) || !aligned(v, 16) || !aligned(err, 4) || k_stride % 8 || v_stride % 8 ||
       k_stride < static_cast<long long>(Hkv) * d || v_stride < static_cast<long long>(Hkv) * d)
     return MNW_E_INVALID_ARG;
   if (q) {

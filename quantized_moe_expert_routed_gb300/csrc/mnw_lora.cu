@@ -962,7 +962,7 @@ int mnw_lora_add(const void* x, long long x_stride, const void* a, const void* b
   const size_t need = mnw_lora_workspace_size(T, H, R, n_adapters);
   if (!x || !a || !b || !adapter || !y || !out || (need > 0 && !ws) || !aligned(x, 16) || !aligned(a, 16) || !aligned(b, 16) ||
       !aligned(y, 16) || !aligned(out, 16) || !aligned(ws, 256) || !aligned(adapter, 4) || !aligned(ranks, 4) ||
-      !aligned(scale, 4) || x_stride % 8 || y_stride % 8 || out_stride % 8 || x_stride < H || y_stride < N || out_stride < N)
+      !aligned(scale, 4) || !aligned(err, 4) || x_stride % 8 || y_stride % 8 || out_stride % 8 || x_stride < H || y_stride < N || out_stride < N)
     return MNW_E_INVALID_ARG;
   // rows of one over others of the other, or over x, which is still read
   if ((y == out && y_stride != out_stride && T > 1) || x == out) return MNW_E_INVALID_ARG;
