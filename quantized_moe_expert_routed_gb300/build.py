@@ -3,7 +3,9 @@
 Each translation unit compiles in parallel, then one nvcc link makes the
 shared library next to this file.  The binding of the decode step's calls
 (csrc/mnw_calls.cpp, a Python module on torch's C++ interface) compiles beside
-them with the host compiler.  No CMake, no torch extension machinery.
+them with the host compiler; where it cannot, the library is built all the
+same, and those calls go through their Python form.  No CMake, no torch
+extension machinery.
 """
 from __future__ import annotations
 
@@ -15,15 +17,11 @@ import subprocess
 import sys
 import sysconfig
 
-import torch
-
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmnw_moe.so")
-# for one torch and one Python, whose C++ interfaces differ between versions
-CALLS = os.path.join(HERE, "mnw_calls_" + re.sub(r"\W", "_", torch.__version__) + sysconfig.get_config_var("EXT_SUFFIX"))
 SOURCES = ["mnw_api.cu", "mnw_route.cu", "mnw_router.cu", "mnw_quant.cu", "mnw_gemm.cu", "mnw_gemm_rows.cu", "mnw_gemm_rows_a8.cu", "mnw_gemm_warp.cu",
            "mnw_gemm_warp_dep.cu", "mnw_static_ws.cu", "mnw_selftest.cu", "mnw_attention.cu",
            "mnw_norm.cu", "mnw_kv_append.cu", "mnw_attn_paged.cu",
@@ -40,20 +38,42 @@ def _nvcc() -> str:
     return cand
 
 
+def calls_path() -> str:
+    """The binding's file, for one torch and one Python, whose C++ interfaces differ between versions."""
+    import torch
+    return os.path.join(HERE, "mnw_calls_" + re.sub(r"\W", "_", torch.__version__) + sysconfig.get_config_var("EXT_SUFFIX"))
+
+
+def calls_failed() -> str:
+    """Where the reason stands that the binding could not be compiled; a source newer than it is tried again."""
+    return calls_path() + ".failed.txt"
+
+
 def _compile_calls() -> None:
-    root = os.path.dirname(torch.__file__)
-    tmp = CALLS + f".{os.getpid()}.tmp"
-    include = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
-               sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include"), INCLUDE]
-    lib = os.path.join(root, "lib")
-    cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", *(f for i in include for f in ("-isystem", i)),
-           os.path.join(CSRC, "mnw_calls.cpp"), "-o", tmp, "-L", lib, "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu",
-           "-ltorch_python", f"-Wl,-rpath,{lib}"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"the compiler failed on mnw_calls.cpp:\n{r.stderr}")
-    os.replace(tmp, CALLS)
+    calls = calls_path()
+    tmp = calls + f".{os.getpid()}.tmp"
+    try:
+        import torch
+        root = os.path.dirname(torch.__file__)
+        include = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                   sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include"), INCLUDE]
+        lib = os.path.join(root, "lib")
+        cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", *(f for i in include for f in ("-isystem", i)),
+               os.path.join(CSRC, "mnw_calls.cpp"), "-o", tmp, "-L", lib, "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu",
+               "-ltorch_python", f"-Wl,-rpath,{lib}"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        why = None if r.returncode == 0 else f"the compiler failed on mnw_calls.cpp:\n{r.stderr}"
+    except (OSError, RuntimeError) as e:  # no compiler
+        why = f"mnw_calls.cpp was not compiled: {e}"
+    if why is None:
+        os.replace(tmp, calls)
+        return
+    if os.path.exists(calls):  # of older sources
+        os.remove(calls)
+    with open(tmp, "w") as f:
+        f.write(why)
+    os.replace(tmp, calls_failed())
 
 
 def _deps():
@@ -65,8 +85,17 @@ def _deps():
 
 def build(force: bool = False, verbose: bool = False) -> str:
     new = _deps()
-    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= new for f in (LIB, CALLS)):
-        return LIB
+    fresh = lambda f: not force and os.path.exists(f) and os.path.getmtime(f) >= new  # noqa: E731
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        calls = None if fresh(calls_path()) or fresh(calls_failed()) else ex.submit(_compile_calls)
+        if not fresh(LIB):
+            _build_library(ex, verbose)
+        if calls:
+            calls.result()
+    return LIB
+
+
+def _build_library(ex, verbose: bool) -> None:
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
 
@@ -82,16 +111,12 @@ def build(force: bool = False, verbose: bool = False) -> str:
             sys.stderr.write(r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        calls = ex.submit(_compile_calls)
-        objs = list(ex.map(compile_one, SOURCES))
-        calls.result()
+    objs = list(ex.map(compile_one, SOURCES))
     tmp = LIB + f".{os.getpid()}.tmp"
     r = subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"nvcc link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":
