@@ -1,5 +1,6 @@
 """A call whose arguments are refused keeps none of the memory that it took."""
 import ctypes
+import gc
 
 import pytest
 import torch
@@ -8,6 +9,13 @@ import int4_util as U4
 from test_gpu_decode_ops import M, _randn
 
 pytestmark = pytest.mark.gpu
+
+
+def allocated():
+    """Bytes held, without what earlier tests left for the collector (it would go at any time)."""
+    torch.cuda.synchronize()
+    gc.collect()
+    return torch.cuda.memory_allocated()
 
 
 def test_refused_arguments_leave_no_memory_behind():
@@ -23,16 +31,14 @@ def test_refused_arguments_leave_no_memory_behind():
     for call in calls:
         call()
         call(stream=here)
-        memory = torch.cuda.memory_allocated()
+        memory = allocated()
         for bad in (dict(blk=32.0), dict(blk="x"), dict(scale="x"), dict(blk=0)):
             for s in ({}, dict(stream=here)):
                 with pytest.raises((m.MnwError, ctypes.ArgumentError, TypeError)):
                     call(**bad, **s)
-                torch.cuda.synchronize()
-                assert torch.cuda.memory_allocated() == memory, (bad, s)
-    held = torch.cuda.memory_allocated()
+                assert allocated() == memory, (bad, s)
+    held = allocated()
     for s in ({}, dict(stream=here)):
         with pytest.raises(m.MnwError):
             m.mnw_lora_add(y, x, a, b, ids, out=x, **s)  # refused by the library, behind the scratch's allocation
-        torch.cuda.synchronize()
-        assert torch.cuda.memory_allocated() == held
+        assert allocated() == held
