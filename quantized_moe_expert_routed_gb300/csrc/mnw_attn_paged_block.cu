@@ -63,6 +63,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <climits>
 #include <cstring>
 
 #include "mnw_attn_split.cuh"
@@ -121,8 +122,7 @@ struct BCfg {
   static constexpr uint32_t kOffRaw = kOffV + kSlotsV * kTile;            // keys' codes, values' codes
   static constexpr uint32_t kOffKS = kOffRaw + 2 * kRaws * kRaw;          // [kScalesK][kTK] scales of keys
   static constexpr uint32_t kOffVS = kOffKS + (INT8 ? kScalesK * kTK * 4 : 0);  // [kScalesV][2][kTK] of values, and their log2
-  static constexpr uint32_t kOffOnes = kOffVS + (INT8 ? kScalesV * 2 * kTK * 4 : 0);  // INT4: keys' scales of a tile that has them
-  static constexpr uint32_t kOffBars = kOffOnes + (INT4 ? kTK * 4 : 0);
+  static constexpr uint32_t kOffBars = kOffVS + (INT8 ? kScalesV * 2 * kTK * 4 : 0);
 };
 
 // A run's part of one item.
@@ -142,6 +142,7 @@ struct Bars {
   uint64_t seg_full[kMaxSegs];
   uint64_t drain[2];
   float qfac[4][kRT];                   // [segment % 4] INT8: the query rows' powers of two
+  int odd_k[kMaxKScales][2], odd_v[kMaxVScales][2];  // INT4: first of a tile's (of each loader warp's) rows that are not finite
   Seg seg[kMaxSegs];
   uint32_t tmem_base;
   int abort;
@@ -253,13 +254,6 @@ __device__ __forceinline__ uint32_t half2_bits(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// The larger ones; a NaN gives the other.
-__device__ __forceinline__ uint32_t f16x2_max(uint32_t a, uint32_t b) {
-  uint32_t y;
-  asm("max.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
-  return y;
-}
-
 template <int D, int FMT>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_block_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const Args a,
@@ -308,7 +302,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(&bars->tmem_base, kTmemCols);
     tmem_relinquish();
   }
-  if (INT4 && threadIdx.x < kTK) reinterpret_cast<float*>(smem + C::kOffOnes)[threadIdx.x] = 1.f;
   pdl_wait();
   const Run run = find_run<kRT, kTK, kThreads, kMaxSlack>(a, &split);
   Cursor<kRT, kTK> kc{};
@@ -567,15 +560,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const uint8_t* const raw = smem + raw_at + b * C::kRaw;
         const uint8_t* const rec = raw + C::kCodes;
+        // A row that is not finite (a scale of NaN) must not reach the query rows that do not see it, though a masked score is
+        // multiplied by its key's scale and a probability of 0 by its value's.  So it gets a scale that is a number, and the
+        // softmax is told the first such row of a tile.  (Masking the products in the softmax instead: 76.4 us with 64-wide
+        // heads for 73.3; the first row looked for behind a branch here: 43.2 with heads of 128 for 39.7.)
         {  // the scales, for the softmax; the values' at once, as it runs while they still wait for their slot
           float* sc = reinterpret_cast<float*>(smem + (values ? C::kOffVS + sc_now * (2 * kTK * 4) : C::kOffKS + sc_now * (kTK * 4)));
+          int odd = INT_MAX;
 #pragma unroll
           for (int i = 0; i < kMine; i += 32) {
             const int key = key0 + i + lane;
             const float s = *reinterpret_cast<const float*>(rec + key * int4row::kRecord);
-            sc[key] = values ? s : s * kHalfUnit;
-            if (values) sc[kTK + key] = fmaxf(__log2f(s), kLeastLog2);
+            const bool finite = fabsf(s) < INFINITY;
+            odd = finite ? odd : min(odd, key);
+            // (a key of zeros keeps a scale, too: a masked score of -inf has to stay one)
+            const float given = values ? (finite ? s : 0.f) : (finite && s != 0.f ? s * kHalfUnit : 0x1p-126f);
+            sc[key] = given;
+            if (values) sc[kTK + key] = fmaxf(__log2f(given), kLeastLog2);
           }
+          odd = __reduce_min_sync(0xffffffffu, odd);
+          if (lane == 0) (values ? bars->odd_v[sc_now] : bars->odd_k[sc_now])[C::kTurns ? 0 : lw] = odd;
           __syncwarp();
           if (lane == 0) mbar_arrive(values ? &bars->vs_full[sc_now] : &bars->ks_full[sc_now]);
           sc_now += kStep;
@@ -912,21 +916,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        const bool masked = __any_sync(0xffffffffu, min(st[0].left, st[1].left) < kTK);
-        if (masked) {
-          if constexpr (INT4) {
-            // the keys' scales before the mask, which a scale of NaN (a key that is not finite) must not undo
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const uint64_t kf = *reinterpret_cast<const uint64_t*>(ks + 8 * i);
-#pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                const uint64_t y = f32x2_mul(f32x2_pack(sv[4 * i + 2 * x], sv[4 * i + 2 * x + 1]), kf);
-                sv[4 * i + 2 * x] = static_cast<uint32_t>(y);
-                sv[4 * i + 2 * x + 1] = static_cast<uint32_t>(y >> 32);
-              }
-            }
-          }
+        if (__any_sync(0xffffffffu, min(st[0].left, st[1].left) < kTK)) {
 #pragma unroll
           for (int e = 0; e < 64; ++e)
             if (8 * (e >> 2) + 2 * t4 + (e & 1) >= st[(e >> 1) & 1].left) sv[e] = 0xff800000u;  // -inf
@@ -951,7 +941,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           // p = 2^(s fac - unit + kLift4), so that p times the value's scale is the FP16 product as it is.  The unit of
           // before serves as long as no product passes 2^14, which is looked for in the products; then, and for a row's
           // first keys, the unit is set and the products are computed (again).
-          ks = reinterpret_cast<const float*>(smem + (masked ? C::kOffOnes : C::kOffKS + ks_slot * (kTK * 4))) + 2 * t4;
           const uint64_t one2 = ones(a);
           bool set = t == begin || __any_sync(0xffffffffu, st[0].unit == -INFINITY || st[1].unit == -INFINITY);
           uint32_t pw[32];
@@ -1005,29 +994,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 most = __vmaxu2(most, pw[2 * i + x]);
               }
             }
-            if (set) {
-              // Hidden keys in the tile: to rows that do not see the first of its values that are not finite, 0 * NaN adds
-              // nothing.  (Behind the pass that NaN leads to; what it needs is worked out here, as holding it costs 1 us.)
-              if (__any_sync(0xffffffffu, min(st[0].left, st[1].left) < kTK)) {
-                const float* all = reinterpret_cast<const float*>(smem + C::kOffVS) + vs_slot * 2 * kTK;
-                int bad = kTK;
-#pragma unroll
-                for (int i = kTK - 32; i >= 0; i -= 32)
-                  if (!(fabsf(all[i + lane]) < INFINITY)) bad = i + lane;
-                bad = __reduce_min_sync(0xffffffffu, bad);
-#pragma unroll
-                for (int x = 0; x < 2; ++x)
-                  if (bad < kTK && bad >= st[x].left) {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) pw[2 * i + x] = f16x2_max(pw[2 * i + x], 0u);
-                  }
-              }
-              break;
-            }
+            if (set) break;
             set = __any_sync(0xffffffffu, max(most >> 16, most & 0xFFFFu) > kMostBits) != 0;
             if (!set) break;
           }
           if (!ok) break;
+          // rows that see a key or a value that is not finite are NaN: by their sums, by a product
+          const int odd_k = C::kTurns ? bars->odd_k[ks_slot][0] : min(bars->odd_k[ks_slot][0], bars->odd_k[ks_slot][1]);
+          const int odd_v = C::kTurns ? bars->odd_v[vs_slot][0] : min(bars->odd_v[vs_slot][0], bars->odd_v[vs_slot][1]);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (odd_k < st[x].left) st[x].l = __uint_as_float(0x7FC00000u);
+            if (odd_v < st[x].left) pw[x] = 0x7FFF7FFFu;
+          }
           tmem_st_pairs(s_at, *reinterpret_cast<uint32_t(*)[16]>(&pw[0]));
           tmem_st_pairs(s_at + 32, *reinterpret_cast<uint32_t(*)[16]>(&pw[16]));
 #pragma unroll
