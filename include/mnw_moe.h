@@ -461,7 +461,9 @@ int mnw_rmsnorm(const void* x, long long x_stride, const void* residual, const v
  * 4 (e / 2) + 16 (e % 2) of a 32-bit word.  S is the smallest BF16 value with
  * 1785 S >= the row's largest magnitude, m = max(1, ceil(the quarter's largest
  * / (7 S))), code = rne(x / (S m)).  A row below 2^-100 is stored as zeros; one
- * with an infinity or a NaN gets S = NaN, and reads as NaN.
+ * with an infinity or a NaN gets S = NaN, and reads as NaN.  (A finite row
+ * within 1 % of BF16's largest value may read as infinite, and a key row above
+ * 2^126 give infinite scores.)
  * d is 64 or 128, page_size 1 .. 65536.
  * block_table int32 [B, max_pages]: position p of sequence b lies in page
  * block_table[b][p / page_size], slot p % page_size; entries past the length

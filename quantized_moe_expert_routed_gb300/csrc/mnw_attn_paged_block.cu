@@ -49,7 +49,8 @@
 // converted, and give scales and operand tiles on as for INT8.  The softmax
 // keeps one reference a row for the probabilities and their products with the
 // values' scales, and computes no maximum as long as that serves.  The same two
-// cases over INT4 take 39.4 and 73.5 us (the second over INT8 106): 4200 clocks
+// cases over INT4 take 39.6 and 72.6 us (BF16 27.3 and 44.6, INT8 43.0 and 106:
+// the conversion costs more than the bytes that it saves): 4200 clocks
 // a tile with heads of 128, 2700 with 64, not one stage's: halving the
 // softmax's exponentials takes 5 to 10 % off, leaving out its check of the
 // products 2 to 5.  With heads of 128 instruction fetches are the largest stall.

@@ -326,8 +326,9 @@ __global__ void __launch_bounds__(kThreads, NR <= 8 ? 2 : 1) lora_shrink_kernel(
 // ---- out = y + s B v on tcgen05: a tile of tokens and some columns, a block of kCols at a time ----
 // y comes by cp.async, whole rows of a block, into shared memory, where the product is added, and leaves from there in
 // rows; v lies there as two operands, its two terms.  While one block is worked on, the next one's y and B are under way.
-// (9000 tokens, N = 5120, in a graph: 66 us with all before it, 61 with the copies alone.  With rows of y and out as bulk copies of 384 bytes 59 us, two a token and block being
-// more than the copy unit takes, 14 us more; with 8 warps 6 more; in three stages of 128 columns, or two CTAs an SM, 0 to 3 more.)
+// (9000 tokens, N = 5120, in a graph with all before it: 65 us, with the copies alone 61.  This kernel by itself and cold:
+// 45, with rows of y and out as bulk copies of 384 bytes 59, two a token and block being more than the copy unit takes;
+// with 8 warps 6 more; in three stages of 128 columns, or two CTAs an SM, 0 to 3 more.)
 constexpr int kExpandThreads = 512;
 template <int NR>
 struct ExpandCfg {
@@ -832,10 +833,12 @@ __global__ void __launch_bounds__(kThreads, NR <= 8 ? 2 : 1) lora_few_kernel(con
 
 // ---- host ----
 
-// Clusters that run at a time; the last form has one CTA an SM.
+// About the clusters that run at a time, by the SMs; the last form has one CTA an SM.  (A cluster lies in one part of the
+// GPU, whose SMs are not a multiple of 8: on 152 SMs the occupancy query says 36 and 15 where this says 38 and 19.  The
+// rules below were measured with these numbers: at R = 128 256 tokens, more than 15 tiles, are still faster by one kernel.)
 inline int clusters_at_once(int R) { return (R <= 64 ? 2 : 1) * current_sm_count() / kCluster; }
 // Tokens up to which one kernel takes a batch: as many as its counters hold for up to 32 ranks, and with more, whose tiles
-// are of 16 tokens, while all tiles run at a time.  One kernel and three, H = 4096, N = 5120, 8 adapters unless given:
+// are of 16 tokens, about one round of tiles.  One kernel and three, H = 4096, N = 5120, 8 adapters unless given:
 // R = 16: 512 tokens 10.3 and 13.6 us, 1024 of one 11.1 and 13.5, of eight 15.7 and 16.8, of 64 24.2 and 37.2;
 // R = 64: 256 tokens 13.1 and 17.5, 512 of one 13.9 and 16.5, of eight 20.7 and 17.3, 768 26.7 and 19.9, 1024 28.5 and 23.9;
 // R = 128: 256 tokens 23.6 and 26.9, 512 37.0 and 27.7, 1024 66.4 and 33.2 (but 512 of 64 adapters 74.5 and 98.5: how many
@@ -908,8 +911,8 @@ int launch_few(const Args& a, cudaStream_t st) {
 template <int NR>
 int launch(Args& a, uint8_t* ws, cudaStream_t st) {
   if (a.T <= few_tokens(a.R)) {
-    // Tiles of 16 tokens, whose registers hold two groups of columns ahead, while the GPU takes all of them at a time, and
-    // of 32 above.  H = 4096, N = 5120, R = 16 and 32: 64 tokens of one adapter 5.6 and 6.9 us (tiles of 32: 7.1 and 9.4),
+    // Tiles of 16 tokens, whose registers hold two groups of columns ahead, up to about one round of tiles, and of 32
+    // above.  H = 4096, N = 5120, R = 16 and 32: 64 tokens of one adapter 5.6 and 6.9 us (tiles of 32: 7.1 and 9.4),
     // 512 of four 7.8 and 10.2 (10.1 and 13.5), 1024 of one 15.2 and 18.9 (11.1 and 14.8).
     if constexpr (NR <= 4)
       if (a.T > 16 * clusters_at_once(a.R)) return launch_few<NR, 2>(a, st);
