@@ -143,7 +143,7 @@ struct Bars {
   uint64_t seg_full[kMaxSegs];
   uint64_t drain[2];
   float qfac[4][kRT];                   // [segment % 4] INT8: the query rows' powers of two
-  int odd_k[kMaxKScales][2], odd_v[kMaxVScales][2];  // INT4: first of a tile's (of each loader warp's) rows that are not finite
+  int2 odd_k[kMaxKScales], odd_v[kMaxVScales];  // INT4: first of a tile's (of each loader warp's) rows that are not finite
   Seg seg[kMaxSegs];
   uint32_t tmem_base;
   int abort;
@@ -580,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (values) sc[kTK + key] = fmaxf(__log2f(given), kLeastLog2);
           }
           odd = __reduce_min_sync(0xffffffffu, odd);
-          if (lane == 0) (values ? bars->odd_v[sc_now] : bars->odd_k[sc_now])[C::kTurns ? 0 : lw] = odd;
+          if (lane == 0) *(&(values ? bars->odd_v : bars->odd_k)[sc_now].x + (C::kTurns ? 0 : lw)) = odd;
           __syncwarp();
           if (lane == 0) mbar_arrive(values ? &bars->vs_full[sc_now] : &bars->ks_full[sc_now]);
           sc_now += kStep;
@@ -1001,8 +1001,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (!ok) break;
           // rows that see a key or a value that is not finite are NaN: by their sums, by a product
-          const int odd_k = C::kTurns ? bars->odd_k[ks_slot][0] : min(bars->odd_k[ks_slot][0], bars->odd_k[ks_slot][1]);
-          const int odd_v = C::kTurns ? bars->odd_v[vs_slot][0] : min(bars->odd_v[vs_slot][0], bars->odd_v[vs_slot][1]);
+          const int2 of_k = bars->odd_k[ks_slot], of_v = bars->odd_v[vs_slot];
+          const int odd_k = C::kTurns ? of_k.x : min(of_k.x, of_k.y), odd_v = C::kTurns ? of_v.x : min(of_v.x, of_v.y);
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             if (odd_k < st[x].left) st[x].l = __uint_as_float(0x7FC00000u);

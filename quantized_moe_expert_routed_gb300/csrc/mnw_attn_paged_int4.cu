@@ -40,6 +40,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <climits>
+
 #include "mnw_attn_split.cuh"
 #include "mnw_int4_row.cuh"
 
@@ -411,6 +413,18 @@ __global__ void __launch_bounds__(kThreads, int4_runs_per_sm(8 * NT)) paged_int4
             }
         }
         if (!__any_sync(0xffffffffu, most_p > kMostP || !(most_w <= kMostW))) break;
+        // a value that is not finite counts nothing (0 * NaN would, in rows that do not see it) and makes the rows that see it
+        // NaN by what they hold
+        int odd = INT_MAX;
+#pragma unroll
+        for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            if (!(fabsf(vs[mt][h]) < INFINITY)) {
+              odd = min(odd, p0 + 16 * mt + 8 * h + key_of(g8));
+              vs[mt][h] = 0.f;
+            }
+        odd = __reduce_min_sync(0xffffffffu, odd);
         float alpha[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -421,8 +435,10 @@ __global__ void __launch_bounds__(kThreads, int4_runs_per_sm(8 * NT)) paged_int4
 #pragma unroll
             for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
-              for (int h = 0; h < 2; ++h)
-                top = fmaxf(top, sc[mt][nt][2 * h + x] * (x ? hi32(fac[mt][nt][h]) : lo32(fac[mt][nt][h])));
+              for (int h = 0; h < 2; ++h) {
+                sc[mt][nt][2 * h + x] = __fmul_rn(sc[mt][nt][2 * h + x], x ? hi32(fac[mt][nt][h]) : lo32(fac[mt][nt][h]));
+                top = fmaxf(top, sc[mt][nt][2 * h + x]);
+              }
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
             const float m = x ? -hi32(neg[nt]) : -lo32(neg[nt]);
@@ -432,16 +448,17 @@ __global__ void __launch_bounds__(kThreads, int4_runs_per_sm(8 * NT)) paged_int4
             for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
               for (int h = 0; h < 2; ++h)
-                topv = fmaxf(topv, __fsub_rn(__fmul_rn(sc[mt][nt][2 * h + x], x ? hi32(fac[mt][nt][h]) : lo32(fac[mt][nt][h])), n[x]) +
-                                       __log2f(fabsf(vs[mt][h])));
+                topv = fmaxf(topv, sc[mt][nt][2 * h + x] - n[x] + __log2f(fabsf(vs[mt][h])));
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) topv = fmaxf(topv, __shfl_xor_sync(0xffffffffu, topv, d));
             // held within 2^100 of the maximum so that the lift stays finite
             const float now_at = unit[nt][x] + (m - n[x]), u = fmaxf(fmaxf(now_at, topv), -100.f);
             c[x] = ex2(m - n[x]);
-            alpha[nt][x] = ex2(now_at - u);
+            alpha[nt][x] = odd < lim[nt][x] ? __uint_as_float(0x7FC00000u) : ex2(now_at - u);
             unit[nt][x] = u;
           }
+#pragma unroll
+          for (int mt = 0; mt < kMT; ++mt) fac[mt][nt][0] = fac[mt][nt][1] = two(1.f, 1.f);
           neg[nt] = two(-n[0], -n[1]);
           sum[nt] = f32x2_mul(sum[nt], two(c[0], c[1]));
           lift[nt] = two(ex2(kLift - unit[nt][0]), ex2(kLift - unit[nt][1]));
@@ -452,17 +469,6 @@ __global__ void __launch_bounds__(kThreads, int4_runs_per_sm(8 * NT)) paged_int4
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[i][nt][e] *= alpha[nt][e & 1];
-        if (pass == 1) {  // NaN: a hidden value that is not finite, 0 * NaN, adds nothing
-#pragma unroll
-          for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const int p = p0 + 16 * mt + 8 * h + key_of(g8);
-                pw[mt][nt][h] &= (p >= lim[nt][0] ? 0u : 0xFFFFu) | (p >= lim[nt][1] ? 0u : 0xFFFF0000u);
-              }
-        }
       }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) sum[nt] = now[nt];
