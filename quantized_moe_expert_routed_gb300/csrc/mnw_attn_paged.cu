@@ -542,8 +542,8 @@ __global__ void __launch_bounds__(WR* WK * 32) paged_attn_kernel(const Args a) {
 // convert the codes: 32 rows 335 and 537, 34 and 40; 64 rows 54 and 40.
 inline int row_tile(long long rows, bool int8) { return rows <= 16 ? 16 : (int8 && rows <= 32 ? 32 : kBlockRows); }
 // INT4: the row tiles of the transposed kernel, which converts a code once for all of them, and the block kernel above 32.
-// 2 sequences of 100,000 positions, 8 kv heads of 128, in one tile of rows here and in the block kernel: 32 rows 138 and 227
-// us, 48 rows (two tiles) 247 and 227; 16 of up to 4000: 32 rows 36.5 and 37.8, 48 rows 45.9 and 37.7.
+// 2 sequences of 100,000 positions, 8 kv heads of 128, in one tile of rows there and in the block kernel: 32 rows 137 and 216
+// us, 48 rows (two tiles) 247 and 216; 16 of up to 4000: 32 rows 35.1 and 36.8, 48 rows 45.9 and 36.8.
 inline int row_tile_int4(long long rows) { return rows <= 8 ? 8 : (rows <= 16 ? 16 : (rows <= 32 ? 32 : kBlockRows)); }
 // CTAs resident on an SM
 inline int runs_per_sm(int rt, bool int4) { return rt == kBlockRows ? 1 : (int4 ? int4_runs_per_sm(rt) : 2); }

@@ -18,13 +18,13 @@
 //
 // Bound: one pass over the cache, 144 bytes a position and kv head (d = 128).
 // Measured on one GB300: 2 single tokens over 200,000 positions, 32 query and 8
-// key heads of 128 (461 MB): 109 us, 4.2 TB/s; 32 over 2048 to 8192 positions in
+// key heads of 128 (461 MB): 105 us, 4.4 TB/s; 32 over 2048 to 8192 positions in
 // pages of 16, 16 and 4 heads (95 MB): 33 us; one over 777: 8.4 us.  Latency
-// bounds it: 16 keys take about 376 instructions, 160 of them the conversion
+// bounds it: 16 keys take about 360 instructions, 160 of them the conversion
 // (mask, and product with the multiplier, two codes each), and 12 warps an SM of
-// 167 registers each issue 2.1 a clock, half of what it could (52 % of the slots;
-// memory 37 %, tensor pipe 17 %).  With all slots the same instructions would
-// take some 56 us, less than the bytes' 68.  A CTA's warps meeting at every tile,
+// 167 registers each issue 2.0 a clock, half of what it could (50 % of the slots;
+// memory 38 %, tensor pipe 18 %).  With all slots the same instructions would
+// take some 53 us, less than the bytes' 68.  A CTA's warps meeting at every tile,
 // with 16-byte copies by all threads, took 123 us; two CTAs with more registers
 // for a wider group of keys 110 to 115.
 //
