@@ -553,7 +553,8 @@ int mnw_kv_values(const void* cache, const void* scale, int fmt, int n_pages, in
  * columns of B count, and the others are not used, whatever they hold.  An
  * adapter outside [-1, n_adapters) counts as -1, a rank outside [0, R] as the
  * nearer end, and MNW_DEVERR_BAD_ADAPTER is OR-ed into *err (device, nullable).
- * Sums are FP32; A x enters the second product to 2^-16 of itself.  Tokens may
+ * Sums are FP32; A x enters the second product to 2^-16 of itself (as two
+ * terms, so an infinite element of B gives NaN).  Tokens may
  * have adapters in any order; neighbours of one adapter cost least.
  * H, N and R are multiples of 8, R <= 128, n_adapters <= 1024, T <= 2^24,
  * N <= 2^20.  ws: device, 256-byte aligned, >= mnw_lora_workspace_size() bytes

@@ -373,7 +373,7 @@ _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.curre
 def _stream_of(t, stream):
     """The handle to launch on: the given stream's, or the current one's.  The library launches on the current device."""
     device = t.get_device()
-    if _current_device() != device or (stream is not None and stream.device_index != device):
+    if _current_device() != device or (stream is not None and getattr(stream, "device_index", device) != device):
         raise MnwError(f"the tensors are on device {device}, which has to be the current device and the stream's")
     if stream is not None:
         return stream.cuda_stream

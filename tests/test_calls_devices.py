@@ -46,3 +46,13 @@ def test_a_stream_of_another_device(name, monkeypatch):
     with pytest.raises(M.MnwError, match="stream"):
         getattr(M, name)(**tensors, **rest, stream=Stream)
     assert not lib.calls
+
+
+@pytest.mark.parametrize("name", C.CALLS)
+def test_a_stream_that_does_not_say_its_device(name, monkeypatch):
+    class Stream:  # (another library's)
+        cuda_stream = 77
+    tensors, rest = C.arguments(name)
+    lib = C.install(monkeypatch)
+    getattr(M, name)(**tensors, **rest, stream=Stream)
+    assert lib.calls[0][1][-1] == 77
